@@ -15,10 +15,11 @@
 // after one CTA barrier, then the codes.  Longer rows (int8 codes only) use a
 // plain one-CTA-per-row kernel with a warp per group.
 //
-// Two row kernels that sit in front of a product are fused into k_rotq's
+// Three row kernels that sit in front of a product are fused into k_rotq's
 // prologue, so their bf16 output is never written: SwiGLU (the down
-// projection's input) and the modulated layer norm (the input of a DiT
-// block's QKV and gate/up products).  The pages list both among the row
+// projection's input), the modulated layer norm (the input of a DiT block's
+// QKV and gate/up products) and the root-mean-square norm with its residual's
+// addition (the same place in a decoder layer).  The pages list both among the row
 // kernels next to the projections, candidates for fusion, with fp32 norms
 // (TensorFold PR #948, "What comes next").
 
@@ -379,8 +380,43 @@ __device__ __forceinline__ void rotate_tail(int n, float (&v)[8]) {
 }
 
 // Row prologues of k_rotq: the row as given, SwiGLU of a gate and an up row,
-// or the modulated layer norm of the row.
-constexpr int kPrePlain = 0, kPreSwiglu = 1, kPreNorm = 2;
+// the modulated layer norm of the row, or the root-mean-square norm of the row
+// and its residual.
+constexpr int kPrePlain = 0, kPreSwiglu = 1, kPreNorm = 2, kPreRms = 3;
+
+// What the root-mean-square norm writes beside the codes (each NULL: not
+// written): the residual stream h = bf16(x + r) and the normed row in bf16.
+struct RmsOut {
+    uint16_t *H;
+    int64_t ldh;
+    uint16_t *Y;
+    int64_t ldy;
+};
+
+// Loads of rows that the same call may write (H in the place of X or R): not
+// through the read-only path.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+// The tail group's E values of one lane, stored at p as bf16.
+__device__ __forceinline__ void put_tail_bf16(uint16_t *p, int E, const float (&v)[8]) {
+    const uint32_t a = bf16_pair(v[0], v[1]), b = bf16_pair(v[2], v[3]);
+    if (E == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+    else if (E == 2) *reinterpret_cast<uint32_t *>(p) = a;
+    else *p = static_cast<uint16_t>(a);
+}
 
 // The modulated layer norm's fp32 arithmetic on one value, rounded to bf16
 // as an unfused norm kernel would store it: h = (x - mu) rstd (1 + sc) + sh.
@@ -406,7 +442,11 @@ constexpr int kRotqMaxWarps = 17;   // 64 full groups (4 a warp) and a tail warp
 // layer norm h = bf16((x - mu) rstd (1 + scale) + shift), mu and the biased
 // variance var over the row in fp32 (one more CTA barrier: two passes inside
 // each warp, then the warps' moments merged), rstd = rsqrtf(var + eps), the
-// modulation read per column through the read-only cache.
+// modulation read per column through the read-only cache.  PRE = kPreRms: the
+// row is y = h rstd gamma, h = bf16(x + r) of X's row and U's (U may be NULL),
+// rstd = 1 / sqrt(mean(h^2) + eps) from one more barrier, gamma in `scale`; y
+// is not rounded before the transform.  h and bf16(y) are written where `ro`
+// asks for them, and without `out` the row ends there.
 
 // CTAs an SM should hold, by warps a CTA: a thread keeps about 80 registers
 constexpr int rotq_min_blocks(int maxw) {
@@ -416,10 +456,11 @@ template <bool TILED, int PRE, int MAXW>
 __global__ void __launch_bounds__(MAXW * 32, rotq_min_blocks(MAXW))
 k_rotq(const uint16_t *__restrict__ X, int64_t M, int64_t K, int64_t ldx, void *__restrict__ out,
        float *__restrict__ sx, unsigned int *trl, const uint16_t *__restrict__ U, int64_t ldu,
-       const float *__restrict__ shift, const float *__restrict__ scale, float eps) {
+       const float *__restrict__ shift, const float *__restrict__ scale, float eps, RmsOut ro) {
     constexpr bool SWIGLU = PRE == kPreSwiglu;
     __shared__ float red[2][kRotqMaxWarps];
-    __shared__ float red_n[2][PRE == kPreNorm ? kRotqMaxWarps : 1];   // the warps' means and M2
+    // the warps' means and M2, or by row parity their sums of squares
+    __shared__ float red_n[2][PRE == kPreNorm || PRE == kPreRms ? kRotqMaxWarps : 1];
     __shared__ unsigned int win[2][16], winq[2][16];   // a row's window sums of |codes|, codes squared
     __shared__ unsigned int run_sh[2][5][32];           // warp 0's largest run sums over the rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -446,6 +487,16 @@ k_rotq(const uint16_t *__restrict__ X, int64_t M, int64_t K, int64_t ldx, void *
     auto load_row = [&](int64_t m) {
         if (!active) return;
         const uint16_t *src = X + m * ldx + col0;
+        if constexpr (PRE == kPreRms) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[i] = ld_once(src + kRun * i);
+            if (U) {
+                const uint16_t *us = U + m * ldu + col0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rawu[i] = ld_once(us + kRun * i);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[i] = ld_stream(src + kRun * i);
         if constexpr (SWIGLU) {
@@ -491,6 +542,85 @@ k_rotq(const uint16_t *__restrict__ X, int64_t M, int64_t K, int64_t ldx, void *
         float amax = 0.0f;
         const int64_t t0 = Gf * kGroup;
         if (tail_warp) Et = load_tail_global<SWIGLU>(X + m * ldx + t0, SWIGLU ? U + m * ldu + t0 : nullptr, tail, vt);
+        if constexpr (PRE == kPreRms) {
+            if (U) {   // h = bf16(x + r)
+                if (tail_warp) {
+                    float rt[8];
+                    load_tail_global<false>(U + m * ldu + t0, nullptr, tail, rt);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        vt[e] = __uint_as_float(static_cast<uint32_t>(f32_to_bf16_bits(vt[e] + rt[e])) << 16);
+                } else if (active) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w[4] = {rawu[i].x, rawu[i].y, rawu[i].z, rawu[i].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            o[k] = bf16_pair(v[8 * i + 2 * k] + __uint_as_float(w[k] << 16),
+                                             v[8 * i + 2 * k + 1] + __uint_as_float(w[k] & 0xFFFF0000u));
+                            v[8 * i + 2 * k] = __uint_as_float(o[k] << 16);
+                            v[8 * i + 2 * k + 1] = __uint_as_float(o[k] & 0xFFFF0000u);
+                        }
+                        raw[i] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+            if (ro.H) {
+                uint16_t *hrow = ro.H + m * ro.ldh;
+                if (tail_warp) {
+                    put_tail_bf16(hrow + t0 + static_cast<int64_t>(lane) * Et, Et, vt);
+                } else if (active) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(hrow + col0 + kRun * i) = raw[i];
+                }
+            }
+            float s2 = 0.0f;
+            if (tail_warp) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s2 = e < Et ? fmaf(vt[e], vt[e], s2) : s2;
+            } else {
+                unsigned long long acc = f2pack(0.0f, 0.0f);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const unsigned long long d = f2pack(v[e], v[e + 1]);
+                    asm("fma.rn.f32x2 %0, %1, %1, %0;" : "+l"(acc) : "l"(d));
+                }
+                float a0, a1;
+                f2unpack(acc, a0, a1);
+                s2 = a0 + a1;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+            if (lane == 0) red_n[par][warp] = s2;
+            __syncthreads();
+            float sum = 0.0f;
+            for (int w = 0; w < W; ++w) sum += red_n[par][w];
+            const float ms = sum / static_cast<float>(K) + eps;
+            const float rstd = ms > 0.0f ? __frsqrt_rn(ms) : 0.0f;
+            uint16_t *yrow = ro.Y ? ro.Y + m * ro.ldy : nullptr;
+            if (tail_warp) {
+                const int64_t c0 = t0 + static_cast<int64_t>(lane) * Et;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < Et) vt[e] = vt[e] * rstd * __ldg(scale + c0 + e);
+                if (yrow) put_tail_bf16(yrow + c0, Et, vt);
+            } else if (active) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 *g4 = reinterpret_cast<const float4 *>(scale + col0 + kRun * i);
+                    const float4 a = __ldg(g4), b = __ldg(g4 + 1);
+                    const float ga[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * i + e] = v[8 * i + e] * rstd * ga[e];
+                    if (yrow)
+                        *reinterpret_cast<uint4 *>(yrow + col0 + kRun * i) =
+                            make_uint4(bf16_pair(v[8 * i], v[8 * i + 1]), bf16_pair(v[8 * i + 2], v[8 * i + 3]),
+                                       bf16_pair(v[8 * i + 4], v[8 * i + 5]), bf16_pair(v[8 * i + 6], v[8 * i + 7]));
+                }
+            }
+            if (!out) continue;
+        }
         if constexpr (PRE == kPreNorm) {
             // each warp's mean and sum of squared deviations over its own
             // values (two passes inside the warp), merged after one barrier
@@ -737,7 +867,8 @@ __global__ void __launch_bounds__(32) k_zero_trailer(unsigned int *trl) {
 template <bool TILED, int PRE = kPrePlain>
 tq_status launch_rotq(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, void *out, float *sx,
                       unsigned int *trl, cudaStream_t s, const uint16_t *U = nullptr, int64_t ldu = 0,
-                      const float *shift = nullptr, const float *scale = nullptr, float eps = 0.0f) {
+                      const float *shift = nullptr, const float *scale = nullptr, float eps = 0.0f,
+                      RmsOut ro = {}) {
     const int64_t Gf = K / kGroup;
     const int warps = static_cast<int>((Gf + 3) / 4) + (K % kGroup ? 1 : 0);
     if (warps < 1 || warps > kRotqMaxWarps) return TQ_ERR_SHAPE;
@@ -772,10 +903,10 @@ tq_status launch_rotq(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, void
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kern, X, M, K, ldx, out, sx, trl, U, ldu, shift, scale, eps);
+        e = cudaLaunchKernelEx(&cfg, kern, X, M, K, ldx, out, sx, trl, U, ldu, shift, scale, eps, ro);
         return e == cudaSuccess ? TQ_OK : cuda_fail(e);
     } else {
-        kern<<<grid, NT, 0, s>>>(X, M, K, ldx, out, sx, trl, U, ldu, shift, scale, eps);
+        kern<<<grid, NT, 0, s>>>(X, M, K, ldx, out, sx, trl, U, ldu, shift, scale, eps, ro);
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? TQ_OK : cuda_fail(e);
     }
@@ -813,6 +944,17 @@ tq_status launch_modnorm_quant_tiled(const uint16_t *X, int64_t M, int64_t K, in
     if (K > kRingMaxK) return TQ_ERR_SHAPE;
     return launch_rotq<true, kPreNorm>(X, M, K, ldx, At, sx, tiled_act_trailer(At, M, K), s, nullptr, 0, shift,
                                        scale, eps);
+}
+
+tq_status launch_rmsnorm_quant(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const uint16_t *R,
+                               int64_t ldr, const float *gamma, float eps, uint16_t *H, int64_t ldh, uint16_t *Y,
+                               int64_t ldy, void *out, bool tiled, float *sx, cudaStream_t s) {
+    if (M == 0) return TQ_OK;
+    if (K > kRingMaxK) return TQ_ERR_SHAPE;
+    const RmsOut ro = {H, ldh, Y, ldy};
+    return tiled ? launch_rotq<true, kPreRms>(X, M, K, ldx, out, sx, tiled_act_trailer(out, M, K), s, R, ldr,
+                                              nullptr, gamma, eps, ro)
+                 : launch_rotq<false, kPreRms>(X, M, K, ldx, out, sx, nullptr, s, R, ldr, nullptr, gamma, eps, ro);
 }
 
 tq_status launch_rotate_quant_act(const uint16_t *X, int64_t M, int64_t K,

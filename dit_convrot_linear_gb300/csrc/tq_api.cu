@@ -164,6 +164,7 @@ const char *tq_status_str(tq_status s) {
         case TQ_ERR_CUDA: return "TQ_ERR_CUDA: a CUDA call failed";
         case TQ_ERR_DEVICE_TIMEOUT: return "TQ_ERR_DEVICE_TIMEOUT: a bounded device wait expired";
         case TQ_ERR_DEVICE: return "TQ_ERR_DEVICE: no usable sm_103 device is current";
+        case TQ_ERR_INDEX: return "TQ_ERR_INDEX: an index read on the device is out of range";
     }
     return "TQ_ERR_UNKNOWN";
 }
@@ -565,9 +566,172 @@ tq_status tq_device_status(cudaStream_t stream) {
         const unsigned int zero = 0;
         e = cudaMemcpyToSymbol(g_status_word, &zero, sizeof(zero));
         if (e != cudaSuccess) return cuda_fail(e);
-        return TQ_ERR_DEVICE_TIMEOUT;
+        return (v & ~kStatusIndex) ? TQ_ERR_DEVICE_TIMEOUT : TQ_ERR_INDEX;
     }
     return TQ_OK;
+}
+
+// ------------------------------------------------------- an attention layer
+
+static tq_status check_rmsnorm(const void *X, int64_t M, int64_t K, int64_t ldx, const void *R, int64_t ldr,
+                               const float *gamma, float eps, const void *H, int64_t ldh) {
+    if (!std::isfinite(eps) || eps < 0.0f) return TQ_ERR_MODE;
+    tq_status st = check_bf16_rows(X, M, K, ldx);
+    if (st != TQ_OK) return st;
+    if (R && (st = check_bf16_rows(R, M, K, ldr)) != TQ_OK) return st;
+    if (H && (st = check_bf16_rows(H, M, K, ldh)) != TQ_OK) return st;
+    if (!gamma) return TQ_ERR_NULL;
+    if (!aligned(gamma, 16)) return TQ_ERR_ALIGN;
+    if ((H == X && H && ldh != ldx) || (H && H == R && ldh != ldr)) return TQ_ERR_SHAPE;
+    return TQ_OK;
+}
+
+tq_status tq_rmsnorm_quant_act(const void *X, int64_t M, int64_t K, int64_t ldx, const void *R, int64_t ldr,
+                               const float *gamma, float eps, void *H, int64_t ldh, void *Y, int64_t ldy,
+                               int8_t *Xq, float *sx, cudaStream_t stream) {
+    if (M < 0 || !valid_k(K) || K > TQ_MAX_K_TILED) return TQ_ERR_SHAPE;
+    if (M == 0) return TQ_OK;
+    tq_status st = check_rmsnorm(X, M, K, ldx, R, ldr, gamma, eps, H, ldh);
+    if (st != TQ_OK) return st;
+    if (!Y && !Xq) return TQ_ERR_NULL;
+    if (Y && (st = check_bf16_rows(Y, M, K, ldy)) != TQ_OK) return st;
+    if ((Xq == nullptr) != (sx == nullptr)) return TQ_ERR_NULL;
+    if (Xq && (!aligned(Xq, 16) || !aligned(sx, 4))) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_rmsnorm_quant(static_cast<const uint16_t *>(X), M, K, ldx, static_cast<const uint16_t *>(R), ldr,
+                                gamma, eps, static_cast<uint16_t *>(H), ldh, static_cast<uint16_t *>(Y), ldy, Xq,
+                                false, sx, stream);
+}
+
+tq_status tq_rmsnorm_quant_act_tiled(const void *X, int64_t M, int64_t K, int64_t ldx, const void *R, int64_t ldr,
+                                     const float *gamma, float eps, void *H, int64_t ldh, void *At,
+                                     size_t at_bytes, float *sx, cudaStream_t stream) {
+    if (M < 0 || !valid_k(K) || K > TQ_MAX_K_TILED) return TQ_ERR_SHAPE;
+    if (M == 0) return TQ_OK;
+    tq_status st = check_rmsnorm(X, M, K, ldx, R, ldr, gamma, eps, H, ldh);
+    if (st != TQ_OK) return st;
+    if (!At || !sx) return TQ_ERR_NULL;
+    const size_t need = tq_act_tiled_bytes(M, K);
+    if (need == 0) return TQ_ERR_OVERFLOW;
+    if (at_bytes < need) return TQ_ERR_WORKSPACE;
+    if (!aligned(At, 256) || !aligned(sx, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_rmsnorm_quant(static_cast<const uint16_t *>(X), M, K, ldx, static_cast<const uint16_t *>(R), ldr,
+                                gamma, eps, static_cast<uint16_t *>(H), ldh, nullptr, 0, At, true, sx, stream);
+}
+
+tq_status tq_rope(const void *X, int64_t tokens, int64_t heads, int64_t dim, int64_t ldx,
+                  const tq_rope_spec *spec, void *Y, int64_t ldy, cudaStream_t stream) {
+    if (!spec) return TQ_ERR_NULL;
+    if (tokens < 0 || heads < 0 || heads > (1 << 20) || dim < 8 || dim > TQ_ROPE_MAX_DIM || dim % 8)
+        return TQ_ERR_SHAPE;
+    if (spec->naxes < 1 || spec->naxes > TQ_ROPE_MAX_AXES || spec->pairs < 1 || spec->pairs > dim / 2)
+        return TQ_ERR_SHAPE;
+    if (spec->interleaved != 0 && spec->interleaved != 1) return TQ_ERR_MODE;
+    if (tokens == 0 || heads == 0) return TQ_OK;
+    tq_status st = check_bf16_rows(X, tokens, heads * dim, ldx);
+    if (st != TQ_OK) return st;
+    if ((st = check_bf16_rows(Y, tokens, heads * dim, ldy)) != TQ_OK) return st;
+    if (X == Y && ldx != ldy) return TQ_ERR_SHAPE;
+    if (!spec->pos || !spec->inv_freq) return TQ_ERR_NULL;
+    if (spec->ldpos < tokens) return TQ_ERR_SHAPE;
+    if (!mul_ok(spec->naxes, spec->ldpos)) return TQ_ERR_OVERFLOW;
+    if (!aligned(spec->pos, 4) || !aligned(spec->inv_freq, 4)) return TQ_ERR_ALIGN;
+    if (spec->axis)
+        for (int p = 0; p < spec->pairs; ++p)
+            if (spec->axis[p] >= spec->naxes) return TQ_ERR_SHAPE;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_rope(static_cast<const uint16_t *>(X), tokens, static_cast<int>(heads), static_cast<int>(dim), ldx,
+                       *spec, static_cast<uint16_t *>(Y), ldy, dev, stream);
+}
+
+size_t tq_kv4_page_bytes(int heads, int dim, int page_size) {
+    if (heads < 1 || heads > 1024 || (dim != 64 && dim != 128 && dim != 256)) return 0;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return 0;
+    return static_cast<size_t>(heads) * (page_size / 16) * (16 * dim + 128);
+}
+
+// The cache's description; *empty: nothing to do.
+static tq_status check_kv4(const tq_kv4 *kv, bool *empty) {
+    *empty = false;
+    if (!kv) return TQ_ERR_NULL;
+    const size_t page = tq_kv4_page_bytes(kv->heads, kv->dim, kv->page_size);
+    if (page == 0) return TQ_ERR_SHAPE;
+    if (kv->npages < 0 || kv->npages > INT32_MAX || kv->nseq < 0 || kv->nseq > TQ_KV4_MAX_SEQS || kv->tokens < 0 ||
+        kv->tokens > INT32_MAX || kv->table_cols < 0 || kv->ldt < kv->table_cols)
+        return TQ_ERR_SHAPE;
+    if (kv->nseq == 0 || kv->tokens == 0) {
+        *empty = true;
+        return TQ_OK;
+    }
+    if (!kv->pool || !kv->table || !kv->kv_len || !kv->q_start) return TQ_ERR_NULL;
+    if (!mul_ok(kv->npages, static_cast<int64_t>(page)) || !mul_ok(kv->nseq, kv->ldt) ||
+        !mul_ok(kv->nseq * kv->ldt, 4) || !mul_ok(kv->table_cols, kv->page_size))
+        return TQ_ERR_OVERFLOW;
+    if (!aligned(kv->pool, 16) || !aligned(kv->table, 4) || !aligned(kv->kv_len, 4) || !aligned(kv->q_start, 4))
+        return TQ_ERR_ALIGN;
+    return TQ_OK;
+}
+
+tq_status tq_kv4_append(const tq_kv4 *kv, const void *K, int64_t ldk, const void *V, int64_t ldv,
+                        cudaStream_t stream) {
+    bool empty;
+    tq_status st = check_kv4(kv, &empty);
+    if (st != TQ_OK || empty) return st;
+    const int64_t row = static_cast<int64_t>(kv->heads) * kv->dim;
+    if ((st = check_bf16_rows(K, kv->tokens, row, ldk)) != TQ_OK) return st;
+    if ((st = check_bf16_rows(V, kv->tokens, row, ldv)) != TQ_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_kv4_append(*kv, static_cast<const uint16_t *>(K), ldk, static_cast<const uint16_t *>(V), ldv, dev,
+                             stream);
+}
+
+tq_status tq_kv4_read(const tq_kv4 *kv, void *K, int64_t ldk, void *V, int64_t ldv, cudaStream_t stream) {
+    bool empty;
+    tq_status st = check_kv4(kv, &empty);
+    if (st != TQ_OK || empty) return st;
+    const int64_t row = static_cast<int64_t>(kv->heads) * kv->dim;
+    if (!K && !V) return TQ_ERR_NULL;
+    if (K && (st = check_bf16_rows(K, kv->tokens, row, ldk)) != TQ_OK) return st;
+    if (V && (st = check_bf16_rows(V, kv->tokens, row, ldv)) != TQ_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_kv4_read(*kv, static_cast<uint16_t *>(K), ldk, static_cast<uint16_t *>(V), ldv, dev, stream);
+}
+
+size_t tq_kv4_workspace_bytes(void) {
+    DeviceInfo dev;
+    return current_device(&dev) == TQ_OK ? kv4_workspace_bytes(dev) : 0;
+}
+
+tq_status tq_kv4_attention(const tq_kv4 *kv, const void *Q, int64_t heads_q, int64_t ldq, int64_t max_q,
+                           float scale, int causal, int64_t window, void *O, int64_t ldo, float *lse,
+                           void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    bool empty;
+    tq_status st = check_kv4(kv, &empty);
+    if (st != TQ_OK) return st;
+    if ((causal != 0 && causal != 1) || !std::isfinite(scale) || scale <= 0.0f) return TQ_ERR_MODE;
+    if (heads_q < kv->heads || heads_q % kv->heads || heads_q / kv->heads > 64 || max_q < 1 || window < 0)
+        return TQ_ERR_SHAPE;
+    if (empty) return TQ_OK;
+    const int64_t row = heads_q * kv->dim;
+    if ((st = check_bf16_rows(Q, kv->tokens, row, ldq)) != TQ_OK) return st;
+    if ((st = check_bf16_rows(O, kv->tokens, row, ldo)) != TQ_OK) return st;
+    if (Q == O && ldq != ldo) return TQ_ERR_SHAPE;
+    if (!mul_ok(kv->tokens, heads_q, INT32_MAX)) return TQ_ERR_OVERFLOW;
+    if (!aligned(lse, 4)) return TQ_ERR_ALIGN;
+    if (!workspace) return TQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    if (ws_bytes < kv4_workspace_bytes(dev)) return TQ_ERR_WORKSPACE;
+    Kv4Attn a = {static_cast<const uint16_t *>(Q), ldq, static_cast<uint16_t *>(O), ldo, lse,
+                 static_cast<int>(heads_q), max_q, scale, causal, window, workspace};
+    return launch_kv4_attention(*kv, a, dev, stream);
 }
 
 tq_status tq_grouped_bytes(const tq_a16_call *calls, int64_t ncalls, int bits, size_t *bytes) {

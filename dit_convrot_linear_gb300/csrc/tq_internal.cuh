@@ -154,6 +154,40 @@ tq_status launch_swiglu_quant_tiled(const uint16_t *G, int64_t ldg, const uint16
                                     int64_t M, int64_t K, void *At, float *sx, cudaStream_t s);
 tq_status launch_modnorm_quant_tiled(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const float *shift,
                                      const float *scale, float eps, void *At, float *sx, cudaStream_t s);
+// RMS norm of bf16(X + R) (R NULL: of X) into the rotated operand `out` (int8
+// rows, or tiled; NULL: none), with bf16(X + R) to H and the normed row to Y
+// where those are not NULL.
+tq_status launch_rmsnorm_quant(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const uint16_t *R,
+                               int64_t ldr, const float *gamma, float eps, uint16_t *H, int64_t ldh, uint16_t *Y,
+                               int64_t ldy, void *out, bool tiled, float *sx, cudaStream_t s);
+
+// Rotary positions (spec.axis: host bytes [pairs]).
+tq_status launch_rope(const uint16_t *X, int64_t T, int heads, int dim, int64_t ldx, const tq_rope_spec &spec,
+                      uint16_t *Y, int64_t ldy, const DeviceInfo &dev, cudaStream_t s);
+
+// The 4-bit cache: kernels set this bit of the status word when a page, length
+// or row range read on the device is out of range.
+constexpr unsigned int kStatusIndex = 0x10000u;
+tq_status launch_kv4_append(const tq_kv4 &kv, const uint16_t *K, int64_t ldk, const uint16_t *V, int64_t ldv,
+                            const DeviceInfo &dev, cudaStream_t s);
+tq_status launch_kv4_read(const tq_kv4 &kv, uint16_t *K, int64_t ldk, uint16_t *V, int64_t ldv,
+                          const DeviceInfo &dev, cudaStream_t s);
+size_t kv4_workspace_bytes(const DeviceInfo &dev);
+struct Kv4Attn {
+    const uint16_t *Q;
+    int64_t ldq;
+    uint16_t *O;
+    int64_t ldo;
+    float *lse;
+    int heads_q;
+    int64_t max_q;
+    float scale;
+    int causal;
+    int64_t window;
+    void *ws;
+};
+tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceInfo &dev, cudaStream_t s);
+
 tq_status launch_gemm_a8_tiled(const void *At, const float *sx, int64_t M, int64_t K,
                                const uint8_t *Wq, const float *sw, int64_t N, int bits,
                                void *Y, int ytype, int64_t ldy, const DeviceInfo &dev,

@@ -19,7 +19,7 @@ TQ_OK = 0
 STATUS = {0: "TQ_OK", 1: "TQ_ERR_NULL", 2: "TQ_ERR_SHAPE", 3: "TQ_ERR_BITS",
           4: "TQ_ERR_MODE", 5: "TQ_ERR_OVERFLOW", 6: "TQ_ERR_ALIGN",
           7: "TQ_ERR_WORKSPACE", 8: "TQ_ERR_CUDA", 9: "TQ_ERR_DEVICE_TIMEOUT",
-          10: "TQ_ERR_DEVICE"}
+          10: "TQ_ERR_DEVICE", 11: "TQ_ERR_INDEX"}
 MODES = {"W8A16": 0, "W4A16": 1, "W8A8": 2}
 OUT = {"f32": 0, "bf16": 1, "i32": 2}
 
@@ -60,6 +60,14 @@ SIGNATURES = {
     "tq_chain_create": (_C, [_P, _I, _C, _C, _P, _Z, ctypes.POINTER(ctypes.c_void_p)]),
     "tq_quantize_weights_blocked": (_C, [_P, _I, _I, _I, _C, _C, _C, _P, _P, _P]),
     "tq_linear_blocked": (_C, [_P, _I, _I, _I, _P, _P, _C, _I, _C, _C, _P, _C, _I, _P]),
+    "tq_rmsnorm_quant_act": (_C, [_P, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _I, _P, _P, _P]),
+    "tq_rmsnorm_quant_act_tiled": (_C, [_P, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _Z, _P, _P]),
+    "tq_rope": (_C, [_P, _I, _I, _I, _I, _P, _P, _I, _P]),
+    "tq_kv4_page_bytes": (_Z, [_C, _C, _C]),
+    "tq_kv4_append": (_C, [_P, _P, _I, _P, _I, _P]),
+    "tq_kv4_read": (_C, [_P, _P, _I, _P, _I, _P]),
+    "tq_kv4_workspace_bytes": (_Z, []),
+    "tq_kv4_attention": (_C, [_P, _P, _I, _I, _I, ctypes.c_float, _C, _I, _P, _I, _P, _P, _Z, _P]),
 }
 
 
@@ -77,6 +85,19 @@ class A16Call(ctypes.Structure):
 class ChainCall(ctypes.Structure):
     """``tq_chain_call``: one call of a chained plan (U NULL, or the up rows)."""
     _fields_ = [("call", A16Call), ("U", _P), ("ldu", _I)]
+
+
+class RopeSpecC(ctypes.Structure):
+    """``tq_rope_spec``: the rotary positions of a call."""
+    _fields_ = [("pos", _P), ("ldpos", _I), ("inv_freq", _P), ("axis", _P), ("naxes", _C), ("pairs", _C),
+                ("interleaved", _C)]
+
+
+class KV4C(ctypes.Structure):
+    """``tq_kv4``: a 4-bit cache and the batch a call is about."""
+    _fields_ = [("pool", _P), ("npages", _I), ("page_size", _C), ("heads", _C), ("dim", _C), ("table", _P),
+                ("table_cols", _I), ("ldt", _I), ("kv_len", _P), ("q_start", _P), ("nseq", _I), ("tokens", _I)]
+
 
 _lib = None
 
@@ -643,3 +664,214 @@ class ChainPlan(GroupedPlan):
         self.bits = bits
         self.ncalls = len(recs)
 
+
+# ------------------------------------------------------- an attention layer
+
+def _norm_args(X, gamma, R, H):
+    import torch
+    M, K = X.shape
+    _req(X, "X", dtype=torch.bfloat16, rows=M, cols=K)
+    _req(gamma, "gamma", dtype=torch.float32, nbytes=4 * K)
+    if R is not None:
+        _req(R, "R", dtype=torch.bfloat16, rows=M, cols=K)
+    if H is not None:
+        _req(H, "H", dtype=torch.bfloat16, rows=M, cols=K)
+    return M, K
+
+
+def _ld(t) -> int:
+    return 0 if t is None else t.stride(0)
+
+
+def rmsnorm_quant_act(X, gamma, eps=1e-6, R=None, H=None, Y=None, Xq=None, sx=None, stream=None):
+    """The RMS norm of h = bf16(X + R) (bf16 [M, K], any row stride; no R: of
+    X) with weight gamma (fp32 [K]), rotated and quantised per token.  ``H``
+    receives h, ``Y`` the normed rows in bf16, where given.  Returns (Xq, sx)
+    for linear_q8."""
+    import torch
+    M, K = _norm_args(X, gamma, R, H)
+    if Xq is None:
+        Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
+    if sx is None:
+        sx = torch.empty(M, dtype=torch.float32, device=X.device)
+    if Y is not None:
+        _req(Y, "Y", dtype=torch.bfloat16, rows=M, cols=K)
+    _req(Xq, "Xq", dtype=torch.int8, rows=M, cols=K, dense=True)
+    _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
+    _check(lib().tq_rmsnorm_quant_act(_ptr(X), M, K, X.stride(0), _ptr(R), _ld(R), _ptr(gamma), float(eps), _ptr(H),
+                                      _ld(H), _ptr(Y), _ld(Y), _ptr(Xq), _ptr(sx), _stream(stream)),
+           "tq_rmsnorm_quant_act")
+    return Xq, sx
+
+
+def rmsnorm(X, gamma, eps=1e-6, R=None, H=None, Y=None, stream=None):
+    """The RMS norm alone, bf16 [M, K] (the input of the A16 products):
+    ``rmsnorm_quant_act`` without its codes.  Returns Y."""
+    import torch
+    M, K = _norm_args(X, gamma, R, H)
+    if Y is None:
+        Y = torch.empty((M, K), dtype=torch.bfloat16, device=X.device)
+    _req(Y, "Y", dtype=torch.bfloat16, rows=M, cols=K)
+    _check(lib().tq_rmsnorm_quant_act(_ptr(X), M, K, X.stride(0), _ptr(R), _ld(R), _ptr(gamma), float(eps), _ptr(H),
+                                      _ld(H), _ptr(Y), Y.stride(0), 0, 0, _stream(stream)),
+           "tq_rmsnorm_quant_act")
+    return Y
+
+
+def rmsnorm_quant_act_tiled(X, gamma, eps=1e-6, R=None, H=None, At=None, sx=None, stream=None):
+    """``rmsnorm_quant_act`` into the tiled operand.  Returns (At, sx) for
+    linear_tiled / linear_tt."""
+    import torch
+    M, K = _norm_args(X, gamma, R, H)
+    need = act_tiled_bytes(M, K)
+    if At is None:
+        At = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+    if sx is None:
+        sx = torch.empty(M, dtype=torch.float32, device=X.device)
+    _req(At, "At", nbytes=need)
+    _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
+    _check(lib().tq_rmsnorm_quant_act_tiled(_ptr(X), M, K, X.stride(0), _ptr(R), _ld(R), _ptr(gamma), float(eps),
+                                            _ptr(H), _ld(H), _ptr(At), _nbytes(At), _ptr(sx), _stream(stream)),
+           "tq_rmsnorm_quant_act_tiled")
+    return At, sx
+
+
+class RopeSpec:
+    """Which pairs of a head turn, how fast and by which axis: ``inv_freq``
+    (device fp32 [pairs]), ``axis`` (a number per pair; none: axis 0), pairs of
+    neighbours (``interleaved``) or of values p and p + pairs."""
+
+    def __init__(self, inv_freq, axis=None, interleaved: bool = False):
+        import torch
+        pairs = inv_freq.numel()
+        _req(inv_freq, "inv_freq", dtype=torch.float32, nbytes=4 * pairs)
+        if not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous")
+        if axis is not None and len(axis) != pairs:
+            raise ValueError(f"axis names {len(axis)} pairs, inv_freq has {pairs}")
+        self.inv_freq = inv_freq
+        self.axis = None if axis is None else (ctypes.c_uint8 * pairs)(*[int(a) for a in axis])
+        self.pairs, self.interleaved = pairs, bool(interleaved)
+
+
+def _heads(X, what, tokens=None, heads=None, dim=None):
+    """Rows of heads, bf16 [tokens, heads, dim], a token's heads side by side."""
+    import torch
+    _req(X, what, dtype=torch.bfloat16)
+    s = X.shape
+    if len(s) != 3 or (tokens is not None and s[0] != tokens) or (heads is not None and s[1] != heads) or (
+            dim is not None and s[2] != dim):
+        raise ValueError(f"{what} is {tuple(s)}, expected [{tokens or 'tokens'}, {heads or 'heads'}, {dim or 'dim'}]")
+    if X.numel() and (X.stride(2) != 1 or (s[1] > 1 and X.stride(1) != s[2])):
+        raise ValueError(f"{what}: a token's heads must lie side by side, got strides {X.stride()}")
+    # one token has no step to the next: its row's length stands for it
+    return X.stride(0) if s[0] > 1 else s[1] * s[2]
+
+
+def rope(X, pos, spec: RopeSpec, Y=None, stream=None):
+    """Rotary positions on every head of X (bf16 [tokens, heads, dim], any
+    token stride), pos int32 [axes, tokens].  ``Y`` may be X.  Returns Y."""
+    import torch
+    T, H, D = X.shape
+    if Y is None:
+        Y = torch.empty((T, H, D), dtype=torch.bfloat16, device=X.device)
+    ldx, ldy = _heads(X, "X"), _heads(Y, "Y", T, H, D)
+    _req(pos, "pos", dtype=torch.int32, rows=1, cols=T)
+    c = RopeSpecC(_ptr(pos), pos.stride(0) if pos.shape[0] > 1 else T, _ptr(spec.inv_freq),
+                  None if spec.axis is None else ctypes.addressof(spec.axis), pos.shape[0], spec.pairs,
+                  int(spec.interleaved))
+    _check(lib().tq_rope(_ptr(X), T, H, D, ldx, ctypes.addressof(c), _ptr(Y), ldy, _stream(stream)), "tq_rope")
+    return Y
+
+
+def kv4_page_bytes(heads: int, dim: int, page_size: int) -> int:
+    return int(lib().tq_kv4_page_bytes(heads, dim, page_size))
+
+
+def kv4_workspace(device="cuda"):
+    """A zeroed workspace for ``kv4_attention`` (one per stream)."""
+    import torch
+    return torch.zeros(int(lib().tq_kv4_workspace_bytes()), dtype=torch.uint8, device=device)
+
+
+class KV4Cache:
+    """Pages of a 4-bit key/value cache (format: ``tq_kv4`` in include/tq.h)."""
+
+    def __init__(self, npages: int, page_size: int, heads: int, dim: int, pool=None, device="cuda"):
+        import torch
+        self.page_bytes = kv4_page_bytes(heads, dim, page_size)
+        if self.page_bytes == 0:
+            raise ValueError(f"no 4-bit cache of {heads} heads of {dim} in pages of {page_size}")
+        if pool is None:
+            pool = torch.zeros(npages * self.page_bytes, dtype=torch.uint8, device=device)
+        _req(pool, "pool", nbytes=npages * self.page_bytes)
+        if not pool.is_contiguous():
+            raise ValueError("pool must be contiguous")
+        self.npages, self.page_size, self.heads, self.dim, self.pool = npages, page_size, heads, dim, pool
+
+
+class KV4Batch:
+    """The sequences of a call: ``table`` int32 [sequences, pages], ``kv_len``
+    int32 [sequences] (this call's rows among them), ``q_start`` int32
+    [sequences + 1] (rows of sequence b: q_start[b] .. q_start[b + 1] - 1),
+    ``tokens`` rows in all, at most ``max_q`` of one sequence.  The arrays may
+    change on the device between calls; their addresses are kept."""
+
+    def __init__(self, cache: KV4Cache, table, kv_len, q_start, tokens: int, max_q: int = 1):
+        import torch
+        if table.dim() != 2:
+            raise ValueError("table must be [sequences, pages]")
+        n, cols = table.shape
+        _req(table, "table", dtype=torch.int32, rows=n, cols=cols)
+        for t, what, k in ((kv_len, "kv_len", n), (q_start, "q_start", n + 1)):
+            _req(t, what, dtype=torch.int32, nbytes=4 * k)
+            if not t.is_contiguous():
+                raise ValueError(f"{what} must be contiguous")
+        self.cache, self.tokens, self.max_q = cache, tokens, max_q
+        self._keep = (table, kv_len, q_start)
+        self._c = KV4C(_ptr(cache.pool), cache.npages, cache.page_size, cache.heads, cache.dim, _ptr(table), cols,
+                       max(table.stride(0), cols), _ptr(kv_len), _ptr(q_start), n, tokens)
+        self._p = ctypes.addressof(self._c)
+
+
+def kv4_append(batch: KV4Batch, K, V, stream=None):
+    """Quantise the batch's keys and values (bf16 [tokens, heads, dim], any
+    token stride) into their pages."""
+    c = batch.cache
+    ldk, ldv = _heads(K, "K", batch.tokens, c.heads, c.dim), _heads(V, "V", batch.tokens, c.heads, c.dim)
+    _check(lib().tq_kv4_append(batch._p, _ptr(K), ldk, _ptr(V), ldv, _stream(stream)), "tq_kv4_append")
+
+
+def kv4_read(batch: KV4Batch, K=None, V=None, stream=None):
+    """The batch's rows as the values their codes stand for: (K, V), bf16
+    [tokens, heads, dim]."""
+    import torch
+    c = batch.cache
+    shape = (batch.tokens, c.heads, c.dim)
+    K = torch.zeros(shape, dtype=torch.bfloat16, device=c.pool.device) if K is None else K
+    V = torch.zeros(shape, dtype=torch.bfloat16, device=c.pool.device) if V is None else V
+    ldk, ldv = _heads(K, "K", *shape), _heads(V, "V", *shape)
+    _check(lib().tq_kv4_read(batch._p, _ptr(K), ldk, _ptr(V), ldv, _stream(stream)), "tq_kv4_read")
+    return K, V
+
+
+def kv4_attention(batch: KV4Batch, Q, scale: float, workspace, causal: bool = True, window: int = 0, O=None,
+                  lse=None, stream=None):
+    """Attention of the batch's queries (bf16 [tokens, query heads, dim], any
+    token stride) over the cache: softmax(scale * q.k) v over the positions a
+    row may see.  ``workspace`` from ``kv4_workspace()``; ``lse`` (fp32
+    [tokens, query heads]) receives the log of each row's sum.  Returns O."""
+    import torch
+    T, H, D = Q.shape
+    if O is None:
+        O = torch.zeros((T, H, D), dtype=torch.bfloat16, device=Q.device)
+    ldq, ldo = _heads(Q, "Q", batch.tokens, None, batch.cache.dim), _heads(O, "O", T, H, D)
+    if lse is not None:
+        _req(lse, "lse", dtype=torch.float32, nbytes=4 * T * H)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    _req(workspace, "workspace")
+    _check(lib().tq_kv4_attention(batch._p, _ptr(Q), H, ldq, batch.max_q, float(scale), int(bool(causal)), window,
+                                  _ptr(O), ldo, _ptr(lse), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "tq_kv4_attention")
+    return O

@@ -65,7 +65,9 @@ typedef enum {
     TQ_ERR_WORKSPACE = 7,   /* workspace missing or smaller than required */
     TQ_ERR_CUDA = 8,        /* a CUDA call failed (see tq_last_cuda_error) */
     TQ_ERR_DEVICE_TIMEOUT = 9, /* a bounded device-side wait expired */
-    TQ_ERR_DEVICE = 10      /* no usable sm_103 device is current */
+    TQ_ERR_DEVICE = 10,     /* no usable sm_103 device is current */
+    TQ_ERR_INDEX = 11       /* a kernel met an index on the device (a cache page, a length) that
+                               is out of range and left out what it names (tq_device_status) */
 } tq_status;
 
 typedef enum {
@@ -460,7 +462,9 @@ tq_status tq_linear_blocked(const void *X, int64_t M, int64_t K, int64_t ldx, co
  * Synchronises `stream`, then reads and clears the library's device status
  * word on the current device.  Returns TQ_ERR_DEVICE_TIMEOUT if a bounded
  * device-side wait expired in any call since the last check (that call's
- * output is then invalid), TQ_ERR_CUDA on a CUDA error, else TQ_OK.
+ * output is then invalid), TQ_ERR_INDEX if a kernel met a page number, length
+ * or row range on the device that is out of range (it left out what that
+ * names), TQ_ERR_CUDA on a CUDA error, else TQ_OK.
  *
  * The pages' runtimes report a failure as a named error the caller can act
  * on rather than stopping (TensorFold PR #948, review follow-up: errors such
@@ -642,6 +646,194 @@ tq_status tq_chain_bytes(const tq_chain_call *calls, int64_t ncalls, int bits, s
  */
 tq_status tq_chain_create(const tq_chain_call *calls, int64_t ncalls, int bits, tq_out ytype,
                           void *dmem, size_t dbytes, tq_grouped *plan);
+
+/*
+ * ---------------------------------------------------------------------------
+ * An attention layer around the projections: the norm that makes a
+ * projection's operand, rotary positions, and a key/value cache held in 4 bits
+ * with the attention that reads it.
+ */
+
+/*
+ * Root-mean-square norm of a row, with the residual's addition before it, into
+ * a projection's operand:
+ *   h = bf16(x + r);   y = h / sqrt(mean(h^2) + eps) * gamma
+ * (Zhang and Sennrich, "Root Mean Square Layer Normalization", 2019).  h is
+ * rounded to bf16 because the residual stream is stored in bf16, and the norm
+ * is that of the stored values.  The sum of squares, the norm and the rotation
+ * stay in fp32: y is rounded only where it is written.
+ *
+ *   X      bf16 [M, K], rules of tq_rotate_quant_act; K <= TQ_MAX_K_TILED.
+ *   R      bf16 [M, K] rows at R + m * ldr (X's rules), or NULL: h = x.
+ *   gamma  fp32 [K], 16-byte aligned.
+ *   eps    finite and >= 0, else TQ_ERR_MODE.
+ *   H      bf16 [M, K] rows at H + m * ldh (X's rules), or NULL (not written).
+ *          It may be X or R itself (same stride); it must not otherwise
+ *          overlap an input.
+ *   Y      bf16 [M, K] rows at Y + m * ldy (X's rules), or NULL: y rounded to
+ *          bf16, unrotated, the input of the A16 products (tq_linear).  It must
+ *          not overlap X, R or H.
+ *   Xq, sx int8 [M, K] dense (16-byte aligned) and fp32 [M], or both NULL: y
+ *          rotated and quantised per token, the input of tq_linear_q8.
+ * At least one of Y and Xq is given.  A row of zeros gives zeros (with eps = 0
+ * too).  A code may differ by one from the fp64 reference, as for
+ * tq_rotate_quant_act.
+ */
+tq_status tq_rmsnorm_quant_act(const void *X, int64_t M, int64_t K, int64_t ldx, const void *R, int64_t ldr,
+                               const float *gamma, float eps, void *H, int64_t ldh, void *Y, int64_t ldy,
+                               int8_t *Xq, float *sx, cudaStream_t stream);
+
+/*
+ * The same into the tiled operand of tq_linear_tiled and tq_linear_tt (codes
+ * and token scales those of tq_rmsnorm_quant_act).
+ *   At, at_bytes, sx   as tq_rotate_quant_act_tiled.
+ */
+tq_status tq_rmsnorm_quant_act_tiled(const void *X, int64_t M, int64_t K, int64_t ldx, const void *R, int64_t ldr,
+                                     const float *gamma, float eps, void *H, int64_t ldh, void *At,
+                                     size_t at_bytes, float *sx, cudaStream_t stream);
+
+/* Most position axes of a rotary embedding. */
+#define TQ_ROPE_MAX_AXES 4
+/* Largest head width the rotary embedding takes. */
+#define TQ_ROPE_MAX_DIM 256
+
+/* Rotary positions of a call: pair p of every head of token t turns by the
+ * angle pos[axis[p]][t] * inv_freq[p]. */
+typedef struct {
+    const int32_t *pos;      /* device int32 [naxes, tokens], axis a at pos + a * ldpos */
+    int64_t ldpos;           /* >= the tokens of the call */
+    const float *inv_freq;   /* device fp32 [pairs] */
+    const uint8_t *axis;     /* HOST bytes [pairs], each < naxes (copied by the call); NULL: all 0 */
+    int naxes;               /* 1 .. TQ_ROPE_MAX_AXES (one for text; time, height and width for video) */
+    int pairs;               /* 1 .. dim / 2; values past 2 * pairs are left as they are */
+    int interleaved;         /* 1: pair p is values 2p, 2p + 1; 0: values p, p + pairs */
+} tq_rope_spec;
+
+/*
+ * Rotary position embedding (Su et al., "RoFormer", 2021) with one or more
+ * position axes, on the heads of the query and key rows:
+ *   (x0, x1) -> (x0 cos a - x1 sin a, x1 cos a + x0 sin a).
+ * The angle is formed and reduced in fp64, so that a late position turns as
+ * exactly as an early one; sine, cosine and the turn are fp32, rounded to bf16.
+ *
+ *   X      bf16: head i of token t is the dim values at X + t * ldx + i * dim
+ *          (the query and key heads of a fused projection's row in one call);
+ *          ldx >= heads * dim, ldx % 8 == 0, X 16-byte aligned.
+ *   dim    a multiple of 8, 8 .. TQ_ROPE_MAX_DIM.
+ *   Y      as X with ldy; it may be X itself (ldy == ldx), but must not
+ *          otherwise overlap X.
+ */
+tq_status tq_rope(const void *X, int64_t tokens, int64_t heads, int64_t dim, int64_t ldx,
+                  const tq_rope_spec *spec, void *Y, int64_t ldy, cudaStream_t stream);
+
+/*
+ * A key/value cache in 4 bits, in pages.
+ *
+ * Keys and values are rotated per head by the normalised Hadamard matrix H of
+ * the head width (the weights' own method, applied to the cache: the rotation
+ * spreads a channel's outliers before the few levels of 4 bits are laid over
+ * them), then quantised with one fp32 scale per token and head,
+ * s = fp32(amax / 7), code = rint(v / s) in -7 .. 7.  Attention rotates the
+ * queries in the same way, q.k = (Hq).(Hk), and turns its output back.
+ *
+ * The pool holds npages pages.  A page is `heads` records, one a head; a record
+ * holds page_size / 16 blocks of 16 tokens, each of 16 * dim + 128 bytes:
+ *   byte 0            keys: 16 rows of dim / 2 bytes; byte i of a row holds the
+ *                     codes of values 2i (low nibble) and 2i + 1, each plus 8
+ *   byte 8 * dim      values: 8 rows of dim bytes, row p for tokens 2p and
+ *                     2p + 1; the two bytes at 4u hold token 2p's values
+ *                     4u .. 4u + 3, the two at 4u + 2 token 2p + 1's, each a
+ *                     code plus 8, low nibble first
+ *   byte 16 * dim     fp32 scales of the 16 keys, then of the 16 values
+ * so a block's 16 rows are what one step of the tensor cores reads, each lane's
+ * words side by side.  The format is public: pages may be copied, sent and
+ * shared between sequences as they are.
+ */
+typedef struct {
+    void *pool;              /* npages pages of tq_kv4_page_bytes; 16-byte aligned */
+    int64_t npages;
+    int page_size;           /* tokens a page: 16, 32, 64 or 128 */
+    int heads;               /* key/value heads, 1 .. 1024 */
+    int dim;                 /* head width: 64, 128 or 256 */
+    const int32_t *table;    /* device int32 [nseq, table_cols]: sequence b's pages at table + b * ldt */
+    int64_t table_cols;      /* pages a sequence may have */
+    int64_t ldt;             /* >= table_cols */
+    const int32_t *kv_len;   /* device int32 [nseq]: the sequence's tokens, this call's among them */
+    const int32_t *q_start;  /* device int32 [nseq + 1]: sequence b's rows of this call are
+                                q_start[b] .. q_start[b + 1] - 1 */
+    int64_t nseq;            /* 1 .. TQ_KV4_MAX_SEQS */
+    int64_t tokens;          /* rows of this call, over all sequences */
+} tq_kv4;
+/*
+ * Row i of a sequence's n rows is position kv_len - n + i.  A row before
+ * position 0 (an unused slot of a fixed batch: kv_len = 0) is not written, sees
+ * nothing, and reads as zeros.  The device arrays are checked as they are read:
+ * a page number outside the pool (its tokens are left out), a length below 0 or
+ * above table_cols * page_size (taken as the nearest) and a row range outside
+ * 0 .. tokens or running backwards (taken as empty) set TQ_ERR_INDEX.  Rows that
+ * no sequence owns are not written.  A page number past a sequence's length is
+ * not read.
+ */
+
+#define TQ_KV4_MAX_SEQS 65536
+
+/* Bytes of one page (0 for sizes the cache does not take). */
+size_t tq_kv4_page_bytes(int heads, int dim, int page_size);
+
+/*
+ * Quantises the call's keys and values into their pages.
+ *   K, V   bf16: head i of row t is the dim values at K + t * ldk + i * dim;
+ *          ldk, ldv >= heads * dim and multiples of 8; 16-byte aligned.  Keys
+ *          come with their positions in them (tq_rope).
+ * Two rows of one call must not have the same place (two sequences that share
+ * their last page).
+ */
+tq_status tq_kv4_append(const tq_kv4 *kv, const void *K, int64_t ldk, const void *V, int64_t ldv,
+                        cudaStream_t stream);
+
+/*
+ * The call's rows read back from the cache as the values their codes stand for,
+ * code * scale rotated back, rounded to bf16 (q_start = the running sum of
+ * kv_len gives whole sequences).
+ *   K, V   as tq_kv4_append, written; either may be NULL.
+ */
+tq_status tq_kv4_read(const tq_kv4 *kv, void *K, int64_t ldk, void *V, int64_t ldv, cudaStream_t stream);
+
+/* Bytes of the attention's workspace on the current device (0 when no usable
+ * device is current).  It does not depend on the sizes of a call. */
+size_t tq_kv4_workspace_bytes(void);
+
+/*
+ * Attention of the call's queries over the cache:
+ *   o = H^T softmax(scale * (H q) . k') v'
+ * over the positions j that row i of its sequence, at position p, may see:
+ * j < kv_len, j <= p when causal, j > p - window when window > 0.  A row that
+ * sees nothing gives zeros.  Query head i reads key/value head i / (heads_q /
+ * heads).
+ *
+ * Scores, softmax statistics and sums are fp32.  The rotated query is rounded
+ * to fp16 (relative to its row's largest value), and so is each weight times
+ * its value's scale: half the relative error of bf16's last place an eighth
+ * time over, below the 4-bit rounding of what they meet.
+ *
+ *   Q        bf16: head i of row t at Q + t * ldq + i * dim (K's rules).
+ *   heads_q  a multiple of kv->heads, at most 64 times it, else TQ_ERR_SHAPE.
+ *   max_q    rows of the longest sequence in this call (1 for decoding).  It
+ *            decides how rows are grouped: larger or smaller than the truth is
+ *            slower, not wrong.
+ *   scale    finite, > 0, else TQ_ERR_MODE (1 / sqrt(dim) as a rule).
+ *   causal   1 or 0.     window   0 (none) or the tokens a row may look back on.
+ *   O        bf16, layout as Q with ldo.  It may be Q itself (ldo == ldq).
+ *   lse      fp32 [tokens, heads_q] dense or NULL: the natural logarithm of the
+ *            row's sum of exp(score), -inf for a row that sees nothing, with
+ *            which two attentions over parts of a context are joined.
+ *   workspace  tq_kv4_workspace_bytes() bytes, 256-byte aligned, ZEROED before
+ *            its first use; rules of tq_linear_tt_split's (every call leaves it
+ *            zeroed where that matters; one per stream).
+ */
+tq_status tq_kv4_attention(const tq_kv4 *kv, const void *Q, int64_t heads_q, int64_t ldq, int64_t max_q,
+                           float scale, int causal, int64_t window, void *O, int64_t ldo, float *lse,
+                           void *workspace, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
