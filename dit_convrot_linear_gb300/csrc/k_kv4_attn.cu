@@ -1,149 +1,922 @@
-// Attention over the 4-bit cache, one CTA per query row and head.
+// Attention over the 4-bit cache: o = H^T softmax(scale (H q) . k') v', with
+// k' = s_k (u - 8) and v' = s_v (u - 8), u the stored nibbles.
 //
-// o = H^T softmax(scale (H q) . k') v' with k' = s_k (u - 8), v' = s_v (u - 8):
-// one pass over the row's positions in steps of 128, a running maximum and sum
-// in fp32, a thread per position for the scores and per value column for the
-// weighted sum.
+// Decoding is bound by the cache's stream: dim + 8 bytes a token and key/value
+// head, read once for all query heads that share it.  The kernel is one pass:
+//
+//   - The query rows of a sequence and key/value head (its tokens times the
+//     heads that share it) are cut into row tiles of R = 8 NR, the positions a
+//     row tile may see into tiles of 32.  All (sequence, head, row tile, tile)
+//     quadruples, in this order, are cut into equal runs, one a CTA, so ragged
+//     lengths fill the GPU evenly and a single long row is split over all of
+//     it.  The lengths are read on the device; each CTA finds its run by a scan.
+//   - In a CTA a producer warp copies tiles into a ring of stages for each
+//     consumer warp (bulk copies: a block of 16 tokens, keys, values and scales,
+//     lies in one piece); consumer warps take turns at the tiles and keep their
+//     own maximum, sum and output, joined in shared memory at the end of a run's
+//     part in a row tile, and over CTAs through the workspace by the one that
+//     comes last (in run order: the result does not depend on timing).
+//   - Products run on mma.sync m16n8k16: with 8 to 32 query rows against 32
+//     tokens there is no 128-row tile for the tensor cores' own memory, and the
+//     operands come from registers: a nibble masked out of a word is the fp16
+//     subnormal u 2^-24 (odd nibbles, left in place, 16 times that), so a lane's
+//     16-byte load is a whole operand row without conversion.  Tokens are the
+//     rows (M) of S^T = K Q^T and the depth of O^T = V^T P^T, query rows the
+//     columns, so that few rows waste little.  The bias of 8 is taken off the
+//     scores by the accumulator's start value (-8 sum q) and off the output by
+//     one more product with a constant operand (8 sum w).
+//   - The running maximum is raised only when a score passes it by 2^8: the
+//     weights then stay below 2^8 and the output is seldom rescaled.  A weight
+//     times its value's scale is rounded to fp16 relative to the largest scale
+//     met (2^-12 of itself, an order below the cache's own rounding); sums stay
+//     in fp32.
 
-#include <math_constants.h>
+#include <cfloat>
 
+#include "tq_a16.cuh"
 #include "tq_kv4.cuh"
 
 namespace tq {
 namespace {
 
-constexpr int kStep = 128;
+constexpr int kTile = 32;                    // tokens a tile: two blocks
+constexpr unsigned int kStatusKvTimeout = 128u;
+// A copy of the library built for its own tests lets every stage expect bytes
+// that no copy brings (their waits then run out).
+#ifdef TQ_TEST_UNSET_BYTES
+constexpr uint32_t kUnset = TQ_TEST_UNSET_BYTES;
+#else
+constexpr uint32_t kUnset = 0;
+#endif
+constexpr float kNone = -FLT_MAX;            // running maximum before any score
+constexpr float kSlack = 8.0f;               // log2 by which a score may pass it
+constexpr float kLog2e = 1.4426950408889634f;
 
-template <int E>
-__global__ void __launch_bounds__(kStep)
-k_kv4_attn_rows(const __grid_constant__ tq_kv4 kv, const __grid_constant__ Kv4Attn a, unsigned int *status) {
-    constexpr int D = 32 * E;
-    constexpr int C = (D + kStep - 1) / kStep;       // value columns a thread
-    __shared__ float q_sh[D], o_sh[D], w_sh[kStep], red[2][kStep / 32];
-    __shared__ const unsigned char *blk_sh[kStep / kKvBlock];
+template <int D_, int NR_, int NW_, int STAGES_, int CTAS_>
+struct Cfg {
+    static constexpr int D = D_, NR = NR_, NW = NW_, STAGES = STAGES_, CTAS = CTAS_;
+    static constexpr int R = 8 * NR;                         // query rows a row tile
+    static constexpr int NT = (NW + 1) * 32;                 // threads: consumers, then the producer
+    static constexpr int W = D / 32;                         // 32-bit words of a row a lane
+    static constexpr bool QREG = NR * W <= 4;                // queries stay in registers
+    static constexpr int BLK = kv_block_bytes(D);
+    static constexpr int TILE = 2 * BLK;
+    static constexpr int QROW = 2 * D + 64;                  // bytes; rows 64 bytes apart mod 128: no bank conflicts
+    static constexpr int OROW = D + 4;                       // floats
+    static constexpr int OBUF = R * OROW * 4;
+    static constexpr int JOIN0 = 34816 / OBUF;               // warps that join at once
+    static constexpr int JOIN = JOIN0 < 1 ? 1 : JOIN0 < NW ? JOIN0 : NW;
+    // shared memory
+    static constexpr int oQ = NW * STAGES * TILE;
+    static constexpr int oO = oQ + R * QROW;
+    static constexpr int oStat = oO + JOIN * OBUF;           // per row: factor, bias; per warp and row: m, l
+    static constexpr int oBar = (oStat + (2 * R + 2 * NW * R) * 4 + 7) / 8 * 8;
+    static constexpr int oMask = oBar + 2 * NW * STAGES * 8;
+    static constexpr int oScan = (oMask + NW * STAGES * 4 + 7) / 8 * 8;
+    static constexpr int SMEM = oScan + NT * 8 + 32 * 8 + 64;
+};
+
+struct Geo {                                 // what the cutting of a batch depends on
+    int g, causal, rows;                     // query heads a key/value head, mask, rows a row tile
+    int64_t window;
+};
+
+struct Run {                                 // one row tile of one key/value head
+    int b, h, rt;
+    KvSeq q;
+    int nrt;                                 // row tiles of the sequence
+    int lo, hi, t0, cost;                    // positions its rows see, first tile, tiles (at least one)
+};
+
+__device__ __forceinline__ void range_of(const Geo &ge, const KvSeq &q, int rt, int &lo, int &hi, int &t0, int &cost) {
+    const int rows = q.n * ge.g, r0 = rt * ge.rows;
+    const int i0 = r0 / ge.g, i1 = (min(r0 + ge.rows, rows) - 1) / ge.g;
+    const int p1 = q.len - q.n + i1;
+    hi = p1 < 0 ? 0 : ge.causal ? min(p1 + 1, q.len) : q.len;
+    const int64_t from = static_cast<int64_t>(q.len) - q.n + i0 - ge.window + 1;
+    lo = ge.window > 0 && from > 0 ? static_cast<int>(from < hi ? from : hi) : 0;
+    t0 = lo / kTile;
+    cost = max(1, (hi + kTile - 1) / kTile - t0);
+}
+
+__device__ __forceinline__ int row_tiles(const Geo &ge, const KvSeq &q) {
+    return (q.n * ge.g + ge.rows - 1) / ge.rows;
+}
+
+// Tiles of all row tiles of a sequence (one head), by one thread.
+__device__ __forceinline__ int64_t seq_cost(const Geo &ge, const KvSeq &q) {
+    const int nrt = row_tiles(ge, q);
+    int64_t sum = 0;
+    for (int rt = 0; rt < nrt; ++rt) {
+        int lo, hi, t0, c;
+        range_of(ge, q, rt, lo, hi, t0, c);
+        sum += c;
+    }
+    return sum;
+}
+
+// The same by a warp.
+__device__ __forceinline__ int64_t seq_cost_warp(const Geo &ge, const KvSeq &q) {
+    const int nrt = row_tiles(ge, q), lane = threadIdx.x & 31;
+    int64_t sum = 0;
+    for (int rt = lane; rt < nrt; rt += 32) {
+        int lo, hi, t0, c;
+        range_of(ge, q, rt, lo, hi, t0, c);
+        sum += c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// The next row tile in order.
+__device__ __forceinline__ bool advance(const tq_kv4 &kv, const Geo &ge, Run &u) {
+    if (++u.rt >= u.nrt) {
+        u.rt = 0;
+        if (++u.h >= kv.heads) {
+            u.h = 0;
+            bool bad = false;
+            do {
+                if (++u.b >= kv.nseq) return false;
+                u.q = kv_seq(kv, u.b, bad);
+            } while (u.q.n == 0);
+            u.nrt = row_tiles(ge, u.q);
+        }
+    }
+    range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
+    return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values held as mma fragments are.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
+    if constexpr (W == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 4)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(addr + 4 * i));
+    }
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ void join_bar(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
+
+// 2^k as fp32, k clamped to the normal range
+__device__ __forceinline__ float pow2i(int k) {
+    return __uint_as_float(static_cast<uint32_t>(min(max(k, -126), 127) + 127) << 23);
+}
+
+struct AttnParams {
+    tq_kv4 kv;
+    Kv4Attn a;
+    Geo geo;
+    unsigned int *count;     // [grid] arrivals, zero between calls
+    float *part;             // [2 grid][R][D] partial outputs
+    float *stat;             // [2 grid][R][2] their maxima (log2) and sums
+    unsigned int *status;
+    int min_run;             // fewest tiles a run
+    int wide;                // rows of one sequence may fill more than one row tile
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_constant__ AttnParams p) {
+    constexpr int D = C::D, NR = C::NR, NW = C::NW, R = C::R, W = C::W, S = C::STAGES;
+    extern __shared__ __align__(128) unsigned char sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int hq = blockIdx.x % a.heads_q;
-    const int64_t t = blockIdx.x / a.heads_q;
-    const int h = hq / (a.heads_q / kv.heads);
+    const uint32_t smb = smem_addr(sm);
+    float *rowf = reinterpret_cast<float *>(sm + C::oStat);
+    float *rowc = rowf + R;
+    float *wm = rowc + R;                // [NW][R]
+    float *wl = wm + NW * R;             // [NW][R]
+    const uint32_t bar_full = smb + C::oBar, bar_empty = bar_full + NW * S * 8;
+    volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(sm + C::oMask);
+    int64_t *scan = reinterpret_cast<int64_t *>(sm + C::oScan);
+    int64_t *wsum = scan + C::NT;
+    volatile int *flag = reinterpret_cast<volatile int *>(wsum + 32);   // 0: a wait ran out, 1: last to arrive,
+                                                                     // 2: located sequence, 3: tiles issued
+    float *obuf = reinterpret_cast<float *>(sm + C::oO);
+    const tq_kv4 &kv = p.kv;
+    const Geo &ge = p.geo;
+
+    if (tid == 0) {
+        for (int i = 0; i < NW * S; ++i) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_full + 8 * i) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_empty + 8 * i) : "memory");
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        flag[0] = flag[3] = 0;
+    }
+
+    // ---------------------------------------------------- this CTA's run
     bool bad = false;
-
-    // the sequence that owns this row
-    int64_t b = -1;
-    KvSeq q = {0, 0, 0};
-    for (int64_t i = 0; i < kv.nseq; ++i) {
-        const KvSeq c = kv_seq(kv, i, bad);
-        if (t >= c.start && t < static_cast<int64_t>(c.start) + c.n) {
-            b = i;
-            q = c;
-        }
-    }
-    if (bad && tid == 0) atomicOr(status, kStatusIndex);
-    if (b < 0) return;
-    const int64_t pos = q.len - q.n + (t - q.start);
-    const int64_t hi = pos < 0 ? 0 : a.causal && pos + 1 < q.len ? pos + 1 : q.len;
-    const int64_t lo = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-
-    if (warp == 0) {
-        float v[8];
-        load_bf16<E, float>(a.Q + t * a.ldq + static_cast<int64_t>(hq) * D + lane * E, v);
-        warp_fwht<E, float>(v);
-        const float c = sqrtf(1.0f / D);
-#pragma unroll
-        for (int e = 0; e < E; ++e) q_sh[lane * E + e] = c * v[e];
-    }
-    float m = -CUDART_INF_F, l = 0.0f, acc[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = 0.0f;
-    for (int64_t base = lo / kKvBlock * kKvBlock; base < hi; base += kStep) {
+    auto costs = [&](int64_t base) {     // scan[i] = tiles of sequence base + i, all heads
         __syncthreads();
-        if (tid < kStep / kKvBlock) {
-            const int64_t at = base + tid * kKvBlock;
-            const int page = at < hi ? kv_page(kv, b, static_cast<int>(at)) : -1;
-            blk_sh[tid] = page >= 0 ? kv_block(kv, page, h, static_cast<int>(at % kv.page_size)) : nullptr;
-            if (at < hi && page < 0) atomicOr(status, kStatusIndex);
-        }
-        __syncthreads();
-        const int64_t j = base + tid;
-        const unsigned char *blk = blk_sh[tid / kKvBlock];
-        const int r = tid % kKvBlock;
-        const bool see = blk && j >= lo && j < hi;
-        float x = -CUDART_INF_F;
-        if (see) {
-            float sum = 0.0f;
-            for (int i = 0; i < D / 2; ++i) {
-                const int u = blk[r * (D / 2) + i];
-                sum = fmaf(q_sh[2 * i], static_cast<float>((u & 15) - 8), sum);
-                sum = fmaf(q_sh[2 * i + 1], static_cast<float>((u >> 4) - 8), sum);
+        if (p.wide) {
+            for (int i = warp; i < C::NT; i += NW + 1) {
+                int64_t c = 0;
+                if (base + i < kv.nseq) c = seq_cost_warp(ge, kv_seq(kv, base + i, bad)) * kv.heads;
+                if (lane == 0) scan[i] = c;
             }
-            x = sum * reinterpret_cast<const float *>(blk + 16 * D)[r] * a.scale;
+        } else {
+            scan[tid] = base + tid < kv.nseq ? seq_cost(ge, kv_seq(kv, base + tid, bad)) * kv.heads : 0;
         }
-        float mx = x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (lane == 0) red[0][warp] = mx;
         __syncthreads();
-        mx = m;
+    };
+    auto chunk_scan = [&](int64_t &mine, int64_t &total) {   // exclusive prefix of scan[tid], and the chunk's sum
+        const int64_t c = scan[tid];
+        int64_t x = c;
 #pragma unroll
-        for (int w = 0; w < kStep / 32; ++w) mx = fmaxf(mx, red[0][w]);
-        const float base_m = mx > -CUDART_INF_F ? mx : 0.0f;
-        const float w = see ? expf(x - base_m) : 0.0f;
-        const float fix = expf(m - base_m);
-        w_sh[tid] = see ? w * reinterpret_cast<const float *>(blk + 16 * D)[16 + r] : 0.0f;
-        float sum = w;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) red[1][warp] = sum;
-        __syncthreads();
-        l *= fix;
-#pragma unroll
-        for (int k = 0; k < kStep / 32; ++k) l += red[1][k];
-        m = mx;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int d = tid + c * kStep;
-            acc[c] *= fix;
-            if (d >= D) continue;
-            for (int k = 0; k < kStep; ++k) {
-                const unsigned char *vb = blk_sh[k / kKvBlock];
-                if (!vb) continue;
-                const int row = k % kKvBlock;
-                const int u = vb[8 * D + (row >> 1) * D + (d >> 2) * 4 + (row & 1) * 2 + ((d & 3) >> 1)];
-                acc[c] = fmaf(w_sh[k], static_cast<float>(((u >> (4 * (d & 1))) & 15) - 8), acc[c]);
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
         }
+        if (lane == 31) wsum[warp] = x;
+        __syncthreads();
+        int64_t before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < NW + 1; ++w) {
+            if (w < warp) before += wsum[w];
+            all += wsum[w];
+        }
+        mine = before + x - c;
+        total = all;
+        __syncthreads();
+    };
+    int64_t total = 0, mine = 0, chunk = 0;
+    for (int64_t base = 0; base < kv.nseq; base += C::NT) {
+        costs(base);
+        chunk_scan(mine, chunk);
+        total += chunk;
     }
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusIndex);
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    per = per < p.min_run ? p.min_run : per;
+    const int64_t c0 = blockIdx.x * per, c1 = c0 + per < total ? c0 + per : total;
+    if (c0 >= c1) return;
+    int64_t before = 0;
+    for (int64_t base = 0; base < kv.nseq; base += C::NT) {
+        if (kv.nseq > C::NT) {           // one chunk: the scan above is still at hand
+            costs(base);
+            chunk_scan(mine, chunk);
+        }
+        if (c0 < before + chunk) {
+            const int64_t at = c0 - before - mine;
+            if (at >= 0 && at < scan[tid]) {
+                flag[2] = static_cast<int>(base + tid);
+                scan[tid] = -1 - at;     // kept for the broadcast below
+            }
+            __syncthreads();
+            break;
+        }
+        before += chunk;
+    }
+    Run u;
+    u.b = flag[2];
+    int64_t at = -1 - scan[u.b % C::NT];   // tiles of the sequence before this run
+    {
+        bool again = false;
+        u.q = kv_seq(kv, u.b, again);
+        u.nrt = row_tiles(ge, u.q);
+        const int64_t head = seq_cost_warp(ge, u.q);
+        u.h = static_cast<int>(at / head);
+        at -= u.h * head;
+        u.rt = 0;
+        // the row tile: by 32 at a time
+        for (int base = 0; base < u.nrt; base += 32) {
+            int lo, hi, t0, c = 0;
+            if (base + lane < u.nrt) range_of(ge, u.q, base + lane, lo, hi, t0, c);
+            int64_t x = c;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (tid + c * kStep < D) o_sh[tid + c * kStep] = l > 0.0f ? acc[c] / l : 0.0f;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, x > at);
+            if (in) {
+                const int l = __ffs(in) - 1;
+                u.rt = base + l;
+                at -= __shfl_sync(0xffffffffu, x - c, l);
+                break;
+            }
+            at -= __shfl_sync(0xffffffffu, x, 31);
+        }
+        range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
+    }
     __syncthreads();
-    if (warp == 0) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = o_sh[lane * E + e];
-        warp_fwht<E, float>(v);
-        const float c = sqrtf(1.0f / D);
-        uint16_t *o = a.O + t * a.ldo + static_cast<int64_t>(hq) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = f32_to_bf16_bits(c * v[e]);
-        if (a.lse && lane == 0) a.lse[t * a.heads_q + hq] = l > 0.0f ? m + logf(l) : -CUDART_INF_F;
+    const int first = static_cast<int>(at);          // tile of the first row tile that the run starts at
+    const int64_t n_all = c1 - c0;
+
+    // The end of every warp.  After a wait that ran out nobody has seen the
+    // copies land: thread 0 waits for the last use of every stage.
+    auto leave = [&]() {
+        __syncthreads();
+        if (flag[0] && tid == 0) {
+            const long long t0 = clock64();
+            for (int w = 0; w < NW; ++w)
+                for (int st = 0; st < S; ++st) {
+                    const int uses = (flag[3] - w + NW - 1) / NW;        // of this warp's ring
+                    if (uses <= st) continue;
+                    const int last = (uses - 1 - st) / S;                // of this stage
+                    const long long left = kA16DrainLimit - (clock64() - t0);
+                    mbar_wait_bounded(bar_full + 8 * (w * S + st), last & 1, left > 0 ? left : 0);
+                }
+        }
+        __syncthreads();
+    };
+
+    if (warp == NW) {
+        // ------------------------------------------------ producer
+        int64_t done = 0;
+        int from = first;
+        bool failed = false;
+        const int per_page = kv.page_size / kTile;   // tiles a page (0: a page is half a tile)
+        while (done < n_all && !failed) {
+            const int n = static_cast<int>(min(static_cast<int64_t>(u.cost - from), n_all - done));
+            for (int base = 0; base < n && !failed; base += 32) {
+                // pages of 32 tiles at once
+                const int t = u.t0 + from + base + lane;
+                const int pos = t * kTile;
+                const unsigned char *src0 = nullptr, *src1 = nullptr;
+                if (base + lane < n && pos < u.hi) {
+                    const int pg = kv_page(kv, u.b, pos);
+                    if (pg >= 0) src0 = kv_block(kv, pg, u.h, pos % kv.page_size);
+                    if (per_page == 0 && pos + kKvBlock < u.hi) {
+                        const int pg1 = kv_page(kv, u.b, pos + kKvBlock);
+                        if (pg1 >= 0) src1 = kv_block(kv, pg1, u.h, 0);
+                        else bad = true;
+                    }
+                    if (pg < 0) bad = true;
+                }
+                const int m = min(32, n - base);
+                for (int l = 0; l < m; ++l) {
+                    const int64_t k = done + base + l;
+                    const int w = static_cast<int>(k % NW);
+                    const int64_t use = k / NW;
+                    const int st = static_cast<int>(use % S), slot = w * S + st;
+                    if (use >= S &&
+                        !mbar_wait_bounded(bar_empty + 8 * slot, static_cast<uint32_t>((use / S - 1) & 1),
+                                           flag[0] ? 0 : kA16WaitLimit)) {
+                        failed = true;
+                        break;
+                    }
+                    if (lane == 0) flag[3] = static_cast<int>(k + 1);
+                    if (lane == l) {
+                        const uint32_t dst = smb + slot * C::TILE, bar = bar_full + 8 * slot;
+                        uint32_t bytes = kUnset, mk = 0;
+                        if (src0) bytes += per_page ? C::TILE : C::BLK, mk |= per_page ? 3u : 1u;
+                        if (src1) bytes += C::BLK, mk |= 2u;
+                        mask_sh[slot] = mk;
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                                     : "memory");
+                        if (src0)
+                            asm volatile(
+                                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                                ::"r"(dst), "l"(src0), "r"(per_page ? C::TILE : C::BLK), "r"(bar)
+                                : "memory");
+                        if (src1)
+                            asm volatile(
+                                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                                ::"r"(dst + C::BLK), "l"(src1), "r"(C::BLK), "r"(bar)
+                                : "memory");
+                    }
+                }
+                __syncwarp();
+            }
+            if (failed) break;
+            done += n;
+            from = 0;
+            if (done < n_all && !advance(kv, ge, u)) break;
+        }
+        if (bad) atomicOr(p.status, kStatusIndex);
+        if (failed && lane == 0) {
+            flag[0] = 1;
+            atomicOr(p.status, kStatusKvTimeout);
+        }
+        leave();
+        return;
     }
+
+    // ---------------------------------------------------- consumers
+    const int r = lane >> 2, j = lane & 3;
+    int64_t done = 0;                     // tiles of the run before this part
+    int from = first;
+    bool lost = false;
+    while (done < n_all) {
+        const int n = static_cast<int>(min(static_cast<int64_t>(u.cost - from), n_all - done));
+        const int rows = u.q.n * ge.g, r0 = u.rt * R;
+
+        // the row tile's queries: rotated, as fp16 in the order of the words'
+        // nibbles (0, 4), (1, 5), (2, 6), (3, 7), the odd ones over 16
+        for (int i = warp; i < R; i += NW) {
+            constexpr int E = D / 32;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            if (r0 + i < rows) {
+                const int tok = (r0 + i) / ge.g, hq = u.h * ge.g + (r0 + i) % ge.g;
+                load_bf16<E, float>(p.a.Q + static_cast<int64_t>(u.q.start + tok) * p.a.ldq +
+                                        static_cast<int64_t>(hq) * D + lane * E,
+                                    v);
+                warp_fwht<E, float>(v);
+            }
+            const float cn = sqrtf(1.0f / D);
+            float mx = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                v[e] = cn * v[e];
+                mx = fmaxf(mx, fabsf(v[e]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // the row's largest value in [2^13, 2^14)
+            const int k = mx > 0.0f ? min(13 - (static_cast<int>(__float_as_uint(mx) >> 23) - 127), 126) : 0;
+            const float up = pow2i(k);
+            float sum = 0.0f;
+            unsigned char *qrow = sm + C::oQ + i * C::QROW;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int d = lane * E + e, jj = d / (D / 4), w = (d % (D / 4)) / 8, nb = d % 8;
+                const float x = (nb & 1) ? v[e] * up * 0.0625f : v[e] * up;
+                const __half hx = __float2half_rn(x);
+                sum += (nb & 1) ? 16.0f * __half2float(hx) : __half2float(hx);
+                *reinterpret_cast<__half *>(qrow + ((w * 4 + jj) * 8 + (nb & 3) * 2 + (nb >> 2)) * 2) = hx;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) {
+                rowf[i] = p.a.scale * kLog2e * (16777216.0f * pow2i(-k));
+                rowc[i] = -8.0f / 16777216.0f * sum;
+            }
+        }
+        join_bar(NW * 32);
+
+        // per lane: query rows 8 nt + 2 j and 8 nt + 2 j + 1
+        float f[NR][2], cst[NR][2], m[NR][2], l[NR][2];
+        int vlo[NR][2], vhi[NR][2], all_lo = 0, all_hi = 0x7fffffff;
+        uint32_t qf[C::QREG ? NR : 1][C::QREG ? W : 1][4];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int i = nt * 8 + 2 * j + c;
+                f[nt][c] = rowf[i];
+                cst[nt][c] = rowc[i];
+                m[nt][c] = kNone;
+                l[nt][c] = 0.0f;
+                vlo[nt][c] = vhi[nt][c] = 0;
+                if (r0 + i < rows) {
+                    const int pos = u.q.len - u.q.n + (r0 + i) / ge.g;
+                    vhi[nt][c] = pos < 0 ? 0 : ge.causal ? min(pos + 1, u.q.len) : u.q.len;
+                    const int64_t w0 = static_cast<int64_t>(pos) - ge.window + 1;
+                    vlo[nt][c] = ge.window > 0 && w0 > 0 ? static_cast<int>(w0 < vhi[nt][c] ? w0 : vhi[nt][c]) : 0;
+                    all_lo = max(all_lo, vlo[nt][c]);
+                    all_hi = min(all_hi, vhi[nt][c]);
+                }
+            }
+            if constexpr (C::QREG) {
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    uint32_t t4[4];
+                    lds_words<4>(smb + C::oQ + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, t4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) qf[nt][w][e] = t4[e];
+                }
+            }
+        }
+        all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+        all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+
+        float o[NR][D / 16][4], oc[NR][4];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) oc[nt][e] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][t][e] = 0.0f;
+        }
+        float gv = pow2i(127);                // power of two that value scales are multiplied by
+
+        // this warp's tiles of the part
+        const int skip = static_cast<int>((warp - done % NW + NW) % NW);
+        for (int i = skip; i < n; i += NW) {
+            const int64_t use = (done + i) / NW;
+            const int st = static_cast<int>(use % S), slot = warp * S + st;
+            if (!lost && !mbar_wait_bounded(bar_full + 8 * slot, static_cast<uint32_t>((use / S) & 1),
+                                            flag[0] ? 0 : kA16WaitLimit)) {
+                lost = true;
+                flag[0] = 1;
+                if (lane == 0) atomicOr(p.status, kStatusKvTimeout);
+            }
+            if (lost) continue;
+            const int tile_at = (u.t0 + from + i) * kTile;
+            const uint32_t base = smb + slot * C::TILE;
+            const uint32_t have = mask_sh[slot];
+            const bool inside = have == 3u && tile_at >= all_lo && tile_at + kTile <= all_hi;
+
+            // scores: S^T, tokens r and r + 8 of each block
+            float s[2][NR][4], sk[2][2], sv[2][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t blk = base + k * C::BLK;
+                uint32_t x[W], y[W];
+                lds_words<W>(blk + r * (D / 2) + j * (D / 8), x);
+                lds_words<W>(blk + (r + 8) * (D / 2) + j * (D / 8), y);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    sk[k][c] = lds_f32(blk + 16 * D + (r + 8 * c) * 4);
+                    sv[k][c] = lds_f32(blk + 16 * D + 64 + (r + 8 * c) * 4);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt) {
+                    s[k][nt][0] = s[k][nt][2] = cst[nt][0];
+                    s[k][nt][1] = s[k][nt][3] = cst[nt][1];
+                }
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t x8 = x[w] >> 8, y8 = y[w] >> 8;
+                    const uint32_t a0 = x[w] & 0x000F000Fu, a1 = y[w] & 0x000F000Fu;
+                    const uint32_t a2 = x[w] & 0x00F000F0u, a3 = y[w] & 0x00F000F0u;
+                    const uint32_t b0 = x8 & 0x000F000Fu, b1 = y8 & 0x000F000Fu;
+                    const uint32_t b2 = x8 & 0x00F000F0u, b3 = y8 & 0x00F000F0u;
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt) {
+                        uint32_t q4[4];
+                        if constexpr (C::QREG) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) q4[e] = qf[nt][w][e];
+                        } else {
+                            lds_words<4>(smb + C::oQ + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, q4);
+                        }
+                        mma_f16(s[k][nt], a0, a1, a2, a3, q4[0], q4[1]);
+                        mma_f16(s[k][nt], b0, b1, b2, b3, q4[2], q4[3]);
+                    }
+                }
+            }
+
+            // which of them count
+            uint32_t see = 0xffffffffu;       // bit (k, c, nt, row)
+            if (!inside) {
+                see = 0u;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int pos = tile_at + k * 16 + c * 8 + r;
+                        const bool there = (have >> k) & 1u;
+#pragma unroll
+                        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (there && pos >= vlo[nt][e] && pos < vhi[nt][e])
+                                    see |= 1u << (((k * 2 + c) * NR + nt) * 2 + e);
+                        if (!there || pos < u.lo || pos >= u.hi) sv[k][c] = 0.0f;
+                    }
+            }
+            auto seen = [&](int k, int nt, int e) {      // e: fragment value, token half e / 2, row e % 2
+                return inside || ((see >> (((k * 2 + (e >> 1)) * NR + nt) * 2 + (e & 1))) & 1u);
+            };
+
+            // weights relative to the running maximum
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[k][nt][e] *= sk[k][e >> 1];
+                        if (!inside && !seen(k, nt, e)) s[k][nt][e] = -INFINITY;
+                        top = fmaxf(top, fmaf(s[k][nt][e], f[nt][e & 1], -m[nt][e & 1]));
+                    }
+            if (__any_sync(0xffffffffu, top > kSlack)) {
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float t = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+                        const float to = fmaxf(m[nt][c], t * f[nt][c]);
+                        const float fix = ex2(m[nt][c] - to);
+                        m[nt][c] = to;
+                        l[nt][c] *= fix;
+                        oc[nt][c] *= fix;
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) {
+                            o[nt][d][c] *= fix;
+                            o[nt][d][c + 2] *= fix;
+                        }
+                    }
+            }
+            // value scales near the top of fp16's range, the largest met below 2^7
+            float big = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
+            if (__any_sync(0xffffffffu, big * gv > 128.0f)) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+                const float to = pow2i(5 - (static_cast<int>(__float_as_uint(big) >> 23) - 127));
+                const float fix = to / gv;
+                gv = to;
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        oc[nt][e] *= fix;
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) o[nt][d][e] *= fix;
+                    }
+            }
+
+            // output: O^T, value words of token pairs j and j + 4
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t blk = base + k * C::BLK + 8 * D;
+                uint32_t x[W], y[W], b0[NR], b1[NR];
+                lds_words<W>(blk + j * D + r * (D / 8), x);
+                lds_words<W>(blk + (j + 4) * D + r * (D / 8), y);
+                const float g0 = sv[k][0] * gv, g1 = sv[k][1] * gv;
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt) {
+                    float w4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float w = ex2(fmaf(s[k][nt][e], f[nt][e & 1], -m[nt][e & 1]));
+                        l[nt][e & 1] += w;
+                        w4[e] = w * (e < 2 ? g0 : g1);
+                    }
+                    b0[nt] = transpose8(half2_bits(w4[0], w4[1]));
+                    b1[nt] = transpose8(half2_bits(w4[2], w4[3]));
+                    mma_f16(oc[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, b0[nt], b1[nt]);
+                }
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t x8 = x[w] >> 8, y8 = y[w] >> 8;
+                    const uint32_t a0 = x[w] & 0x000F000Fu, a1 = x[w] & 0x00F000F0u;
+                    const uint32_t a2 = y[w] & 0x000F000Fu, a3 = y[w] & 0x00F000F0u;
+                    const uint32_t c0_ = x8 & 0x000F000Fu, c1_ = x8 & 0x00F000F0u;
+                    const uint32_t c2_ = y8 & 0x000F000Fu, c3_ = y8 & 0x00F000F0u;
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt) {
+                        mma_f16(o[nt][2 * w], a0, a1, a2, a3, b0[nt], b1[nt]);
+                        mma_f16(o[nt][2 * w + 1], c0_, c1_, c2_, c3_, b0[nt], b1[nt]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar_empty + 8 * slot) : "memory");
+        }
+
+        // ------------------------------------------------ join the warps
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+                if (r == 0) {
+                    wm[warp * R + nt * 8 + 2 * j + c] = m[nt][c];
+                    wl[warp * R + nt * 8 + 2 * j + c] = l[nt][c];
+                }
+            }
+        join_bar(NW * 32);
+        // the warp's share of each row, relative to the row's largest maximum
+        float fac[NR][2];
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float mx = kNone;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wm[w * R + nt * 8 + 2 * j + c]);
+                fac[nt][c] = ex2(m[nt][c] - mx) * (16777216.0f / gv);
+            }
+        for (int round = 0; round * C::JOIN < NW; ++round) {
+            if (warp / C::JOIN == round) {
+                float *buf = obuf + (warp % C::JOIN) * (C::OBUF / 4);
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            float4 *dst = reinterpret_cast<float4 *>(buf + (nt * 8 + 2 * j + c) * C::OROW + r * (D / 8) + 4 * w);
+                            const float b = oc[nt][c], fc = fac[nt][c];
+                            float4 v = make_float4((o[nt][2 * w][c] - b) * fc, (o[nt][2 * w][c + 2] * 0.0625f - b) * fc,
+                                                   (o[nt][2 * w + 1][c] - b) * fc,
+                                                   (o[nt][2 * w + 1][c + 2] * 0.0625f - b) * fc);
+                            if (round) {
+                                const float4 t = *dst;
+                                v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+                            }
+                            *dst = v;
+                        }
+            }
+            join_bar(NW * 32);
+        }
+        auto row_stat = [&](int i, float &mx, float &sum) {
+            mx = kNone;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wm[w * R + i]);
+            sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) sum += wl[w * R + i] * ex2(wm[w * R + i] - mx);
+        };
+        constexpr int CH = R * D / 4;                    // 16-byte pieces of the row tile
+        const bool whole = from == 0 && n == u.cost;
+        bool write = true;
+        if (!whole) {
+            // this part to the workspace; the CTA that comes last joins all
+            // parts.  A row tile's parts belong to CTAs c_first .. c_last; only
+            // the first of them can hold it as its run's last part, the others
+            // hold it as their run's first.
+            const int64_t start = c0 + done - from;      // the row tile's first tile, over the batch
+            const int cf = static_cast<int>(start / per), cl = static_cast<int>((start + u.cost - 1) / per);
+            auto slot_of = [&](int c) { return static_cast<int64_t>(2) * c + (c == cf ? 1 : 0); };
+            float *part = p.part + slot_of(blockIdx.x) * R * D;
+            float *stat = p.stat + slot_of(blockIdx.x) * R * 2;
+            for (int i = tid; i < CH; i += NW * 32) {
+                const int row = i / (D / 4), col = i % (D / 4) * 4;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int b = 0; b < C::JOIN; ++b) {
+                    const float4 t = *reinterpret_cast<const float4 *>(obuf + b * (C::OBUF / 4) + row * C::OROW + col);
+                    v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+                }
+                __stcg(reinterpret_cast<float4 *>(part + row * D + col), v);
+            }
+            for (int i = tid; i < R; i += NW * 32) {
+                float mx, sum;
+                row_stat(i, mx, sum);
+                __stcg(reinterpret_cast<float2 *>(stat + 2 * i), make_float2(mx, sum));
+            }
+            __threadfence();
+            join_bar(NW * 32);
+            if (tid == 0) {
+                const unsigned int old = atomicAdd(p.count + cf, 1u);
+                flag[1] = old == static_cast<unsigned int>(cl - cf);
+                if (flag[1]) p.count[cf] = 0u;
+                __threadfence();
+            }
+            join_bar(NW * 32);
+            write = flag[1] != 0;
+            if (write) {
+                for (int i = tid; i < R; i += NW * 32) {
+                    float mx = kNone, sum = 0.0f;
+                    for (int c = cf; c <= cl; ++c) mx = fmaxf(mx, __ldcg(p.stat + slot_of(c) * R * 2 + 2 * i));
+                    for (int c = cf; c <= cl; ++c) {
+                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(p.stat + slot_of(c) * R * 2 + 2 * i));
+                        sum += t.y * ex2(t.x - mx);
+                    }
+                    wm[i] = mx;
+                    wl[i] = sum;
+                }
+                join_bar(NW * 32);
+                for (int i = tid; i < CH; i += NW * 32) {
+                    const int row = i / (D / 4), col = i % (D / 4) * 4;
+                    const float mx = wm[row];
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int c = cf; c <= cl; ++c) {
+                        const int64_t sl = slot_of(c);
+                        const float fc = ex2(__ldcg(p.stat + sl * R * 2 + 2 * row) - mx);
+                        const float4 t = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * R * D + row * D + col));
+                        v = make_float4(fmaf(fc, t.x, v.x), fmaf(fc, t.y, v.y), fmaf(fc, t.z, v.z), fmaf(fc, t.w, v.w));
+                    }
+                    *reinterpret_cast<float4 *>(obuf + row * C::OROW + col) = v;
+                }
+            }
+        } else {
+            float mx[1], sum[1];
+            for (int i = tid; i < CH; i += NW * 32) {
+                const int row = i / (D / 4), col = i % (D / 4) * 4;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int b = 0; b < C::JOIN; ++b) {
+                    const float4 t = *reinterpret_cast<const float4 *>(obuf + b * (C::OBUF / 4) + row * C::OROW + col);
+                    v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+                }
+                *reinterpret_cast<float4 *>(obuf + row * C::OROW + col) = v;
+            }
+            if (tid < R) row_stat(tid, mx[0], sum[0]);
+            join_bar(NW * 32);                            // every read of wm, wl before they are written
+            if (tid < R) {
+                wm[tid] = mx[0];
+                wl[tid] = sum[0];
+            }
+        }
+        if (write) {
+            join_bar(NW * 32);
+            for (int i = warp; i < R && r0 + i < rows; i += NW) {
+                constexpr int E = D / 32;
+                const int64_t tok = u.q.start + (r0 + i) / ge.g;
+                const int hq = u.h * ge.g + (r0 + i) % ge.g;
+                const float sum = wl[i], inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = obuf[i * C::OROW + lane * E + e];
+                warp_fwht<E, float>(v);
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e)
+                    w[e] = static_cast<uint32_t>(f32_to_bf16_bits(sum > 0.0f ? v[2 * e] * inv : 0.0f)) |
+                           (static_cast<uint32_t>(f32_to_bf16_bits(sum > 0.0f ? v[2 * e + 1] * inv : 0.0f)) << 16);
+                uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + lane * E;
+                if (flag[0]) continue;                    // the sums are not whole
+                if constexpr (E == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<uint32_t *>(dst) = w[0];
+                if (p.a.lse && lane == 0)
+                    p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (wm[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+            }
+        }
+        join_bar(NW * 32);
+        done += n;
+        from = 0;
+        if (done < n_all && !advance(kv, ge, u)) break;
+    }
+    leave();
+}
+
+constexpr int kMaxCtas = 2;                              // CTAs an SM, over the variants
+constexpr int kMaxPart = 32 * 128;                       // R * D, over the variants
+constexpr int kMaxRows = 32;
+
+template <class C>
+tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
+    static_assert(C::CTAS <= kMaxCtas && C::R * C::D <= kMaxPart && C::R <= kMaxRows, "workspace");
+    const int grid = dev.sms * C::CTAS;
+    unsigned char *ws = static_cast<unsigned char *>(p.a.ws);
+    const size_t most = static_cast<size_t>(dev.sms) * kMaxCtas;
+    p.count = reinterpret_cast<unsigned int *>(ws);
+    p.stat = reinterpret_cast<float *>(ws + (most * 4 + 255) / 256 * 256);
+    p.part = p.stat + most * 2 * kMaxRows * 2;
+    p.geo.rows = C::R;
+    p.min_run = 4;
+    p.wide = p.a.max_q * p.geo.g > C::R;
+    const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (fe != cudaSuccess) return cuda_fail(fe);
+    k_kv4_attn<C><<<grid, C::NT, C::SMEM, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
 
 }  // namespace
 
 size_t kv4_workspace_bytes(const DeviceInfo &dev) {
-    (void)dev;
-    return 256;
+    const size_t most = static_cast<size_t>(dev.sms) * kMaxCtas;
+    return (most * 4 + 255) / 256 * 256 + most * 2 * (kMaxRows * 2 + kMaxPart) * 4;
 }
 
 tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceInfo &dev, cudaStream_t s) {
-    (void)dev;
-    unsigned int *status = status_word();
-    if (!status) return TQ_ERR_DEVICE;
-    auto kern = kv.dim == 64 ? k_kv4_attn_rows<2> : kv.dim == 128 ? k_kv4_attn_rows<4> : k_kv4_attn_rows<8>;
-    kern<<<static_cast<unsigned>(kv.tokens * a.heads_q), kStep, 0, s>>>(kv, a, status);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+    AttnParams p = {};
+    p.kv = kv;
+    p.a = a;
+    p.geo.g = a.heads_q / kv.heads;
+    p.geo.causal = a.causal;
+    p.geo.window = a.window;
+    p.status = status_word();
+    if (!p.status) return TQ_ERR_DEVICE;
+    const int64_t rows = a.max_q * p.geo.g;
+    if (kv.dim == 64) {
+        if (rows <= 8) return launch<Cfg<64, 1, 7, 4, 2>>(p, dev, s);
+        if (rows <= 16) return launch<Cfg<64, 2, 7, 4, 2>>(p, dev, s);
+        return launch<Cfg<64, 4, 11, 4, 1>>(p, dev, s);
+    }
+    if (kv.dim == 128) {
+        if (rows <= 8) return launch<Cfg<128, 1, 7, 2, 2>>(p, dev, s);
+        if (rows <= 16) return launch<Cfg<128, 2, 11, 3, 1>>(p, dev, s);
+        return launch<Cfg<128, 4, 7, 4, 1>>(p, dev, s);
+    }
+    if (rows <= 8) return launch<Cfg<256, 1, 11, 2, 1>>(p, dev, s);
+    return launch<Cfg<256, 2, 7, 2, 1>>(p, dev, s);
 }
 
 }  // namespace tq
