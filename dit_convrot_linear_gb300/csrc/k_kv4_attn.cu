@@ -73,7 +73,8 @@ struct Cfg {
     static constexpr int oBar = (oStat + (2 * R + 2 * NW * R) * 4 + 7) / 8 * 8;
     static constexpr int oMask = oBar + 2 * NW * STAGES * 8;
     static constexpr int oScan = (oMask + NW * STAGES * 4 + 7) / 8 * 8;
-    static constexpr int SMEM = oScan + NT * 8 + 32 * 8 + 64;
+    static constexpr int oFound = oScan + NT * 8 + 32 * 8 + 16;
+    static constexpr int SMEM = oFound + 64;
 };
 
 struct Geo {                                 // what the cutting of a batch depends on
@@ -99,6 +100,14 @@ __device__ __forceinline__ void range_of(const Geo &ge, const KvSeq &q, int rt, 
     cost = max(1, (hi + kTile - 1) / kTile - t0);
 }
 
+// Positions that row i of a sequence sees.
+__device__ __forceinline__ void row_range(const Geo &ge, const KvSeq &q, int i, int &lo, int &hi) {
+    const int pos = q.len - q.n + i;
+    hi = pos < 0 ? 0 : ge.causal ? min(pos + 1, q.len) : q.len;
+    const int64_t from = static_cast<int64_t>(pos) - ge.window + 1;
+    lo = ge.window > 0 && from > 0 ? static_cast<int>(from < hi ? from : hi) : 0;
+}
+
 __device__ __forceinline__ int row_tiles(const Geo &ge, const KvSeq &q) {
     return (q.n * ge.g + ge.rows - 1) / ge.rows;
 }
@@ -107,6 +116,7 @@ __device__ __forceinline__ int row_tiles(const Geo &ge, const KvSeq &q) {
 __device__ __forceinline__ int64_t seq_cost(const Geo &ge, const KvSeq &q) {
     const int nrt = row_tiles(ge, q);
     int64_t sum = 0;
+#pragma unroll 1
     for (int rt = 0; rt < nrt; ++rt) {
         int lo, hi, t0, c;
         range_of(ge, q, rt, lo, hi, t0, c);
@@ -162,35 +172,63 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // Transpose of an 8 x 8 matrix of 16-bit values held as mma fragments are.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
 template <int W>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
+__device__ __forceinline__ void lds_words(const unsigned char *p, uint32_t (&w)[W]) {
     if constexpr (W == 2) {
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x; w[1] = v.y;
     } else {
 #pragma unroll
-        for (int i = 0; i < W; i += 4)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                         : "r"(addr + 4 * i));
+        for (int i = 0; i < W; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
     }
 }
 
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
+// the product as a value of its operands alone, so that the compiler may order it
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ void join_bar(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
 // 2^k as fp32, k clamped to the normal range
 __device__ __forceinline__ float pow2i(int k) {
     return __uint_as_float(static_cast<uint32_t>(min(max(k, -126), 127) + 127) << 23);
 }
+
+// a / b for a, b > 0: in 32 bits where they fit
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+struct Found {                               // where a CTA's run starts
+    int64_t at, head;                        // tiles of the sequence before it; tiles a head
+    int b;
+    KvSeq q;
+};
 
 struct AttnParams {
     tq_kv4 kv;
@@ -219,7 +257,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     int64_t *scan = reinterpret_cast<int64_t *>(sm + C::oScan);
     int64_t *wsum = scan + C::NT;
     volatile int *flag = reinterpret_cast<volatile int *>(wsum + 32);   // 0: a wait ran out, 1: last to arrive,
-                                                                     // 2: located sequence, 3: tiles issued
+                                                                     // 3: tiles issued
+    Found *found = reinterpret_cast<Found *>(sm + C::oFound);
     float *obuf = reinterpret_cast<float *>(sm + C::oO);
     const tq_kv4 &kv = p.kv;
     const Geo &ge = p.geo;
@@ -235,23 +274,27 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     }
 
     // ---------------------------------------------------- this CTA's run
+    pdl_launch_dependents();
+    pdl_wait();                           // lengths, pages, queries and the workspace may come from the launch before
     bool bad = false;
-    auto costs = [&](int64_t base) {     // scan[i] = tiles of sequence base + i, all heads
-        __syncthreads();
-        if (p.wide) {
+    KvSeq mine = {0, 0, 0};               // sequence base + tid of the scan's step, its tiles a head, and
+    int64_t head = 0, mine_at = 0, step_sum = 0;   // those of all heads before it in the step and in the step
+    auto scan_step = [&](int64_t base) {
+        mine = {0, 0, 0};
+        if (base + tid < kv.nseq) mine = kv_seq(kv, base + tid, bad);
+        if (p.wide) {                     // a warp a sequence
             for (int i = warp; i < C::NT; i += NW + 1) {
                 int64_t c = 0;
-                if (base + i < kv.nseq) c = seq_cost_warp(ge, kv_seq(kv, base + i, bad)) * kv.heads;
+                bool again = false;
+                if (base + i < kv.nseq) c = seq_cost_warp(ge, kv_seq(kv, base + i, again));
                 if (lane == 0) scan[i] = c;
             }
+            __syncthreads();
+            head = scan[tid];
         } else {
-            scan[tid] = base + tid < kv.nseq ? seq_cost(ge, kv_seq(kv, base + tid, bad)) * kv.heads : 0;
+            head = seq_cost(ge, mine);
         }
-        __syncthreads();
-    };
-    auto chunk_scan = [&](int64_t &mine, int64_t &total) {   // exclusive prefix of scan[tid], and the chunk's sum
-        const int64_t c = scan[tid];
-        int64_t x = c;
+        int64_t x = head * kv.heads;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -265,50 +308,47 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             if (w < warp) before += wsum[w];
             all += wsum[w];
         }
-        mine = before + x - c;
-        total = all;
-        __syncthreads();
+        mine_at = before + x - head * kv.heads;
+        step_sum = all;
     };
-    int64_t total = 0, mine = 0, chunk = 0;
+    int64_t total = 0;
     for (int64_t base = 0; base < kv.nseq; base += C::NT) {
-        costs(base);
-        chunk_scan(mine, chunk);
-        total += chunk;
+        if (base) __syncthreads();
+        scan_step(base);
+        total += step_sum;
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusIndex);
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    int64_t per = quotient(total + gridDim.x - 1, gridDim.x);
     per = per < p.min_run ? p.min_run : per;
     const int64_t c0 = blockIdx.x * per, c1 = c0 + per < total ? c0 + per : total;
     if (c0 >= c1) return;
-    int64_t before = 0;
+    int64_t passed = 0;
     for (int64_t base = 0; base < kv.nseq; base += C::NT) {
-        if (kv.nseq > C::NT) {           // one chunk: the scan above is still at hand
-            costs(base);
-            chunk_scan(mine, chunk);
-        }
-        if (c0 < before + chunk) {
-            const int64_t at = c0 - before - mine;
-            if (at >= 0 && at < scan[tid]) {
-                flag[2] = static_cast<int>(base + tid);
-                scan[tid] = -1 - at;     // kept for the broadcast below
-            }
+        if (kv.nseq > C::NT) {            // one step: its scan is still at hand
             __syncthreads();
+            scan_step(base);
+        }
+        if (c0 < passed + step_sum) {
+            const int64_t at = c0 - passed - mine_at;
+            if (at >= 0 && at < head * kv.heads) {
+                found->b = static_cast<int>(base + tid);
+                found->q = mine;
+                found->at = at;
+                found->head = head;
+            }
             break;
         }
-        before += chunk;
+        passed += step_sum;
     }
+    __syncthreads();
     Run u;
-    u.b = flag[2];
-    int64_t at = -1 - scan[u.b % C::NT];   // tiles of the sequence before this run
-    {
-        bool again = false;
-        u.q = kv_seq(kv, u.b, again);
-        u.nrt = row_tiles(ge, u.q);
-        const int64_t head = seq_cost_warp(ge, u.q);
-        u.h = static_cast<int>(at / head);
-        at -= u.h * head;
-        u.rt = 0;
-        // the row tile: by 32 at a time
+    u.b = found->b;
+    u.q = found->q;
+    u.nrt = row_tiles(ge, u.q);
+    u.h = static_cast<int>(quotient(found->at, found->head));
+    int64_t at = found->at - u.h * found->head;
+    u.rt = 0;
+    if (u.nrt > 1) {                      // the row tile: by 32 at a time
         for (int base = 0; base < u.nrt; base += 32) {
             int lo, hi, t0, c = 0;
             if (base + lane < u.nrt) range_of(ge, u.q, base + lane, lo, hi, t0, c);
@@ -327,9 +367,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             }
             at -= __shfl_sync(0xffffffffu, x, 31);
         }
-        range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
     }
-    __syncthreads();
+    range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
     const int first = static_cast<int>(at);          // tile of the first row tile that the run starts at
     const int64_t n_all = c1 - c0;
 
@@ -339,22 +378,22 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         __syncthreads();
         if (flag[0] && tid == 0) {
             const long long t0 = clock64();
-            for (int w = 0; w < NW; ++w)
-                for (int st = 0; st < S; ++st) {
-                    const int uses = (flag[3] - w + NW - 1) / NW;        // of this warp's ring
-                    if (uses <= st) continue;
-                    const int last = (uses - 1 - st) / S;                // of this stage
-                    const long long left = kA16DrainLimit - (clock64() - t0);
-                    mbar_wait_bounded(bar_full + 8 * (w * S + st), last & 1, left > 0 ? left : 0);
-                }
+            for (int slot = 0; slot < NW * S && slot < flag[3]; ++slot) {
+                const int last = (flag[3] - 1 - slot) / (NW * S);        // the stage's last use
+                const long long left = kA16DrainLimit - (clock64() - t0);
+                mbar_wait_bounded(bar_full + 8 * slot, last & 1, left > 0 ? left : 0);
+            }
         }
         __syncthreads();
     };
 
     if (warp == NW) {
         // ------------------------------------------------ producer
+        // Tile k of the run goes to stage k % (NW S), whose consumer is warp
+        // k % NW.
         int64_t done = 0;
-        int from = first;
+        int from = first, slot = 0, issued = 0;
+        uint32_t phase = 1;               // a stage's first use finds it empty
         bool failed = false;
         const int per_page = kv.page_size / kTile;   // tiles a page (0: a page is half a tile)
         while (done < n_all && !failed) {
@@ -376,35 +415,27 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 }
                 const int m = min(32, n - base);
                 for (int l = 0; l < m; ++l) {
-                    const int64_t k = done + base + l;
-                    const int w = static_cast<int>(k % NW);
-                    const int64_t use = k / NW;
-                    const int st = static_cast<int>(use % S), slot = w * S + st;
-                    if (use >= S &&
-                        !mbar_wait_bounded(bar_empty + 8 * slot, static_cast<uint32_t>((use / S - 1) & 1),
-                                           flag[0] ? 0 : kA16WaitLimit)) {
+                    if (!mbar_try(bar_empty + 8 * slot, phase) &&
+                        !mbar_wait_bounded(bar_empty + 8 * slot, phase, flag[0] ? 0 : kA16WaitLimit)) {
                         failed = true;
                         break;
                     }
-                    if (lane == 0) flag[3] = static_cast<int>(k + 1);
-                    if (lane == l) {
+                    const uint64_t a0 = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src0), l);
+                    const uint64_t a1 = per_page ? 0 : __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src1), l);
+                    if (elect_one()) {
                         const uint32_t dst = smb + slot * C::TILE, bar = bar_full + 8 * slot;
-                        uint32_t bytes = kUnset, mk = 0;
-                        if (src0) bytes += per_page ? C::TILE : C::BLK, mk |= per_page ? 3u : 1u;
-                        if (src1) bytes += C::BLK, mk |= 2u;
-                        mask_sh[slot] = mk;
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                        const uint32_t n0 = per_page ? C::TILE : C::BLK;
+                        mask_sh[slot] = (a0 ? (per_page ? 3u : 1u) : 0u) | (a1 ? 2u : 0u);
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                                     "r"(kUnset + (a0 ? n0 : 0u) + (a1 ? C::BLK : 0u))
                                      : "memory");
-                        if (src0)
-                            asm volatile(
-                                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                                ::"r"(dst), "l"(src0), "r"(per_page ? C::TILE : C::BLK), "r"(bar)
-                                : "memory");
-                        if (src1)
-                            asm volatile(
-                                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                                ::"r"(dst + C::BLK), "l"(src1), "r"(C::BLK), "r"(bar)
-                                : "memory");
+                        if (a0) bulk_copy(dst, a0, n0, bar);
+                        if (a1) bulk_copy(dst + C::BLK, a1, C::BLK, bar);
+                    }
+                    ++issued;
+                    if (++slot == NW * S) {
+                        slot = 0;
+                        phase ^= 1;
                     }
                 }
                 __syncwarp();
@@ -415,6 +446,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             if (done < n_all && !advance(kv, ge, u)) break;
         }
         if (bad) atomicOr(p.status, kStatusIndex);
+        if (lane == 0) flag[3] = issued;
         if (failed && lane == 0) {
             flag[0] = 1;
             atomicOr(p.status, kStatusKvTimeout);
@@ -428,6 +460,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     int64_t done = 0;                     // tiles of the run before this part
     int from = first;
     bool lost = false;
+    int stage = warp, next = warp;        // this warp's next stage, and its next tile of the part
+    uint32_t stage_phase = 0;
     while (done < n_all) {
         const int n = static_cast<int>(min(static_cast<int64_t>(u.cost - from), n_all - done));
         const int rows = u.q.n * ge.g, r0 = u.rt * R;
@@ -479,7 +513,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 
         // per lane: query rows 8 nt + 2 j and 8 nt + 2 j + 1
         float f[NR][2], cst[NR][2], m[NR][2], l[NR][2];
-        int vlo[NR][2], vhi[NR][2], all_lo = 0, all_hi = 0x7fffffff;
+        int all_lo = 0, all_hi = 0x7fffffff;          // positions that every row sees
         uint32_t qf[C::QREG ? NR : 1][C::QREG ? W : 1][4];
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt) {
@@ -490,21 +524,18 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 cst[nt][c] = rowc[i];
                 m[nt][c] = kNone;
                 l[nt][c] = 0.0f;
-                vlo[nt][c] = vhi[nt][c] = 0;
                 if (r0 + i < rows) {
-                    const int pos = u.q.len - u.q.n + (r0 + i) / ge.g;
-                    vhi[nt][c] = pos < 0 ? 0 : ge.causal ? min(pos + 1, u.q.len) : u.q.len;
-                    const int64_t w0 = static_cast<int64_t>(pos) - ge.window + 1;
-                    vlo[nt][c] = ge.window > 0 && w0 > 0 ? static_cast<int>(w0 < vhi[nt][c] ? w0 : vhi[nt][c]) : 0;
-                    all_lo = max(all_lo, vlo[nt][c]);
-                    all_hi = min(all_hi, vhi[nt][c]);
+                    int lo, hi;
+                    row_range(ge, u.q, (r0 + i) / ge.g, lo, hi);
+                    all_lo = max(all_lo, lo);
+                    all_hi = min(all_hi, hi);
                 }
             }
             if constexpr (C::QREG) {
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     uint32_t t4[4];
-                    lds_words<4>(smb + C::oQ + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, t4);
+                    lds_words<4>(sm + C::oQ + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, t4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) qf[nt][w][e] = t4[e];
                 }
@@ -526,35 +557,38 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         float gv = pow2i(127);                // power of two that value scales are multiplied by
 
         // this warp's tiles of the part
-        const int skip = static_cast<int>((warp - done % NW + NW) % NW);
-        for (int i = skip; i < n; i += NW) {
-            const int64_t use = (done + i) / NW;
-            const int st = static_cast<int>(use % S), slot = warp * S + st;
-            if (!lost && !mbar_wait_bounded(bar_full + 8 * slot, static_cast<uint32_t>((use / S) & 1),
-                                            flag[0] ? 0 : kA16WaitLimit)) {
+        for (; next < n; next += NW) {
+            const int i = next;
+            const int slot = stage;
+            const uint32_t full_phase = stage_phase;
+            stage += NW;
+            if (stage >= NW * S) {
+                stage = warp;
+                stage_phase ^= 1;
+            }
+            if (!lost && !mbar_try(bar_full + 8 * slot, full_phase) &&
+                !mbar_wait_bounded(bar_full + 8 * slot, full_phase, flag[0] ? 0 : kA16WaitLimit)) {
                 lost = true;
                 flag[0] = 1;
                 if (lane == 0) atomicOr(p.status, kStatusKvTimeout);
             }
             if (lost) continue;
             const int tile_at = (u.t0 + from + i) * kTile;
-            const uint32_t base = smb + slot * C::TILE;
+            const unsigned char *base = sm + slot * C::TILE;
             const uint32_t have = mask_sh[slot];
-            const bool inside = have == 3u && tile_at >= all_lo && tile_at + kTile <= all_hi;
 
-            // scores: S^T, tokens r and r + 8 of each block
-            float s[2][NR][4], sk[2][2], sv[2][2];
+            // scores: S^T, tokens r and r + 8 of each block, times the key's scale
+            float s[2][NR][4], sv[2][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint32_t blk = base + k * C::BLK;
+                const unsigned char *blk = base + k * C::BLK;
                 uint32_t x[W], y[W];
                 lds_words<W>(blk + r * (D / 2) + j * (D / 8), x);
                 lds_words<W>(blk + (r + 8) * (D / 2) + j * (D / 8), y);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    sk[k][c] = lds_f32(blk + 16 * D + (r + 8 * c) * 4);
-                    sv[k][c] = lds_f32(blk + 16 * D + 64 + (r + 8 * c) * 4);
-                }
+                const float *sc = reinterpret_cast<const float *>(blk + 16 * D);
+                const float sk[2] = {sc[r], sc[r + 8]};
+                sv[k][0] = sc[16 + r];
+                sv[k][1] = sc[24 + r];
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt) {
                     s[k][nt][0] = s[k][nt][2] = cst[nt][0];
@@ -574,38 +608,45 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 #pragma unroll
                             for (int e = 0; e < 4; ++e) q4[e] = qf[nt][w][e];
                         } else {
-                            lds_words<4>(smb + C::oQ + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, q4);
+                            lds_words<4>(sm + C::oQ + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, q4);
                         }
-                        mma_f16(s[k][nt], a0, a1, a2, a3, q4[0], q4[1]);
-                        mma_f16(s[k][nt], b0, b1, b2, b3, q4[2], q4[3]);
+                        mma(s[k][nt], a0, a1, a2, a3, q4[0], q4[1]);
+                        mma(s[k][nt], b0, b1, b2, b3, q4[2], q4[3]);
                     }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[k][nt][e] *= sk[e >> 1];
             }
 
-            // which of them count
-            uint32_t see = 0xffffffffu;       // bit (k, c, nt, row)
-            if (!inside) {
-                see = 0u;
+            // a tile at the edge of what its rows see, or with a page left out
+            if (!(have == 3u && tile_at >= all_lo && tile_at + kTile <= all_hi)) {
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        int lo = 0, hi = 0;
+                        if (r0 + nt * 8 + 2 * j + e < rows) row_range(ge, u.q, (r0 + nt * 8 + 2 * j + e) / ge.g, lo, hi);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const int pos = tile_at + k * 16 + c * 8 + r;
+                                if (!((have >> k) & 1u) || pos < lo || pos >= hi) s[k][nt][2 * c + e] = -INFINITY;
+                            }
+                    }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const int pos = tile_at + k * 16 + c * 8 + r;
-                        const bool there = (have >> k) & 1u;
-#pragma unroll
-                        for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (there && pos >= vlo[nt][e] && pos < vhi[nt][e])
-                                    see |= 1u << (((k * 2 + c) * NR + nt) * 2 + e);
-                        if (!there || pos < u.lo || pos >= u.hi) sv[k][c] = 0.0f;
+                        if (!((have >> k) & 1u) || pos < u.lo || pos >= u.hi) sv[k][c] = 0.0f;
                     }
             }
-            auto seen = [&](int k, int nt, int e) {      // e: fragment value, token half e / 2, row e % 2
-                return inside || ((see >> (((k * 2 + (e >> 1)) * NR + nt) * 2 + (e & 1))) & 1u);
-            };
 
-            // weights relative to the running maximum
+            // log2 of the weights, relative to the running maximum
+            float ex[2][NR][4];
             float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -613,9 +654,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[k][nt][e] *= sk[k][e >> 1];
-                        if (!inside && !seen(k, nt, e)) s[k][nt][e] = -INFINITY;
-                        top = fmaxf(top, fmaf(s[k][nt][e], f[nt][e & 1], -m[nt][e & 1]));
+                        ex[k][nt][e] = fmaf(s[k][nt][e], f[nt][e & 1], -m[nt][e & 1]);
+                        top = fmaxf(top, ex[k][nt][e]);
                     }
             if (__any_sync(0xffffffffu, top > kSlack)) {
 #pragma unroll
@@ -634,6 +674,11 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                         for (int d = 0; d < D / 16; ++d) {
                             o[nt][d][c] *= fix;
                             o[nt][d][c + 2] *= fix;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            ex[k][nt][c] = fmaf(s[k][nt][c], f[nt][c], -to);
+                            ex[k][nt][c + 2] = fmaf(s[k][nt][c + 2], f[nt][c], -to);
                         }
                     }
             }
@@ -658,7 +703,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             // output: O^T, value words of token pairs j and j + 4
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint32_t blk = base + k * C::BLK + 8 * D;
+                const unsigned char *blk = base + k * C::BLK + 8 * D;
                 uint32_t x[W], y[W], b0[NR], b1[NR];
                 lds_words<W>(blk + j * D + r * (D / 8), x);
                 lds_words<W>(blk + (j + 4) * D + r * (D / 8), y);
@@ -668,13 +713,13 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                     float w4[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float w = ex2(fmaf(s[k][nt][e], f[nt][e & 1], -m[nt][e & 1]));
+                        const float w = ex2(ex[k][nt][e]);
                         l[nt][e & 1] += w;
                         w4[e] = w * (e < 2 ? g0 : g1);
                     }
                     b0[nt] = transpose8(half2_bits(w4[0], w4[1]));
                     b1[nt] = transpose8(half2_bits(w4[2], w4[3]));
-                    mma_f16(oc[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, b0[nt], b1[nt]);
+                    mma(oc[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, b0[nt], b1[nt]);
                 }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
@@ -685,8 +730,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                     const uint32_t c2_ = y8 & 0x000F000Fu, c3_ = y8 & 0x00F000F0u;
 #pragma unroll
                     for (int nt = 0; nt < NR; ++nt) {
-                        mma_f16(o[nt][2 * w], a0, a1, a2, a3, b0[nt], b1[nt]);
-                        mma_f16(o[nt][2 * w + 1], c0_, c1_, c2_, c3_, b0[nt], b1[nt]);
+                        mma(o[nt][2 * w], a0, a1, a2, a3, b0[nt], b1[nt]);
+                        mma(o[nt][2 * w + 1], c0_, c1_, c2_, c3_, b0[nt], b1[nt]);
                     }
                 }
             }
@@ -758,7 +803,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             // the first of them can hold it as its run's last part, the others
             // hold it as their run's first.
             const int64_t start = c0 + done - from;      // the row tile's first tile, over the batch
-            const int cf = static_cast<int>(start / per), cl = static_cast<int>((start + u.cost - 1) / per);
+            const int cf = static_cast<int>(quotient(start, per)), cl = static_cast<int>(quotient(start + u.cost - 1, per));
             auto slot_of = [&](int c) { return static_cast<int64_t>(2) * c + (c == cf ? 1 : 0); };
             float *part = p.part + slot_of(blockIdx.x) * R * D;
             float *stat = p.stat + slot_of(blockIdx.x) * R * 2;
@@ -777,13 +822,16 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 row_stat(i, mx, sum);
                 __stcg(reinterpret_cast<float2 *>(stat + 2 * i), make_float2(mx, sum));
             }
-            __threadfence();
             join_bar(NW * 32);
             if (tid == 0) {
+                __threadfence();                         // the CTA's stores, ordered before it by the barrier
                 const unsigned int old = atomicAdd(p.count + cf, 1u);
-                flag[1] = old == static_cast<unsigned int>(cl - cf);
-                if (flag[1]) p.count[cf] = 0u;
-                __threadfence();
+                const int last = old == static_cast<unsigned int>(cl - cf);
+                flag[1] = last;
+                if (last) {
+                    p.count[cf] = 0u;
+                    __threadfence();
+                }
             }
             join_bar(NW * 32);
             write = flag[1] != 0;
@@ -859,6 +907,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         }
         join_bar(NW * 32);
         done += n;
+        next -= n;
         from = 0;
         if (done < n_all && !advance(kv, ge, u)) break;
     }
@@ -883,8 +932,17 @@ tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
     p.wide = p.a.max_q * p.geo.g > C::R;
     const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (fe != cudaSuccess) return cuda_fail(fe);
-    k_kv4_attn<C><<<grid, C::NT, C::SMEM, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(C::NT);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<C>, p);
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
 
