@@ -10,12 +10,13 @@
 //     quadruples, in this order, are cut into equal runs, one a CTA, so ragged
 //     lengths fill the GPU evenly and a single long row is split over all of
 //     it.  The lengths are read on the device; each CTA finds its run by a scan.
-//   - In a CTA a producer warp copies tiles into a ring of stages for each
-//     consumer warp (bulk copies: a block of 16 tokens, keys, values and scales,
-//     lies in one piece); consumer warps take turns at the tiles and keep their
-//     own maximum, sum and output, joined in shared memory at the end of a run's
-//     part in a row tile, and over CTAs through the workspace by the one that
-//     comes last (in run order: the result does not depend on timing).
+//   - A CTA's warps take turns at its tiles, each with a ring of stages of its
+//     own that it fills by bulk copies (a block of 16 tokens, keys, values and
+//     scales, lies in one piece) as it frees them; no warp waits for another.
+//     Each keeps its own maximum, sum and output, joined in shared memory at the
+//     end of a run's part in a row tile, and over CTAs through the workspace by
+//     the one that comes last (in run order: the result does not depend on
+//     timing).
 //   - Products run on mma.sync m16n8k16: with 8 to 32 query rows against 32
 //     tokens there is no 128-row tile for the tensor cores' own memory, and the
 //     operands come from registers: a nibble masked out of a word is the fp16
@@ -56,7 +57,7 @@ template <int D_, int NR_, int NW_, int STAGES_, int CTAS_>
 struct Cfg {
     static constexpr int D = D_, NR = NR_, NW = NW_, STAGES = STAGES_, CTAS = CTAS_;
     static constexpr int R = 8 * NR;                         // query rows a row tile
-    static constexpr int NT = (NW + 1) * 32;                 // threads: consumers, then the producer
+    static constexpr int NT = NW * 32;                       // threads
     static constexpr int W = D / 32;                         // 32-bit words of a row a lane
     static constexpr bool QREG = NR * W <= 4;                // queries stay in registers
     static constexpr int BLK = kv_block_bytes(D);
@@ -65,14 +66,17 @@ struct Cfg {
     static constexpr int OROW = D + 4;                       // floats
     static constexpr int OBUF = R * OROW * 4;
     static constexpr int JOIN0 = 34816 / OBUF;               // warps that join at once
-    static constexpr int JOIN = JOIN0 < 1 ? 1 : JOIN0 < NW ? JOIN0 : NW;
+    static constexpr int JOIN = JOIN0 < NW ? JOIN0 : NW;
+    static_assert(JOIN >= 2, "the second buffer holds the parts' factors in the last join");
     // shared memory
     static constexpr int oQ = NW * STAGES * TILE;
     static constexpr int oO = oQ + R * QROW;
     static constexpr int oStat = oO + JOIN * OBUF;           // per row: factor, bias; per warp and row: m, l
     static constexpr int oBar = (oStat + (2 * R + 2 * NW * R) * 4 + 7) / 8 * 8;
-    static constexpr int oMask = oBar + 2 * NW * STAGES * 8;
-    static constexpr int oScan = (oMask + NW * STAGES * 4 + 7) / 8 * 8;
+    static constexpr int oMask = oBar + NW * STAGES * 8;
+    static constexpr int oSeq = (oMask + NW * STAGES * 4 + 7) / 8 * 8;
+    static constexpr int oIter = oSeq + NT * static_cast<int>(sizeof(KvSeq));
+    static constexpr int oScan = (oIter + NW * 64 + 7) / 8 * 8;
     static constexpr int oFound = oScan + NT * 8 + 32 * 8 + 16;
     static constexpr int SMEM = oFound + 64;
 };
@@ -82,7 +86,7 @@ struct Geo {                                 // what the cutting of a batch depe
     int64_t window;
 };
 
-struct Run {                                 // one row tile of one key/value head
+struct Run {                                 // one row tile of one key/value head (at most 64 bytes)
     int b, h, rt;
     KvSeq q;
     int nrt;                                 // row tiles of the sequence
@@ -139,8 +143,9 @@ __device__ __forceinline__ int64_t seq_cost_warp(const Geo &ge, const KvSeq &q) 
     return sum;
 }
 
-// The next row tile in order.
-__device__ __forceinline__ bool advance(const tq_kv4 &kv, const Geo &ge, Run &u) {
+// The next row tile in order.  `seqs`: the sequences' descriptions in shared
+// memory, where one step of the scan held them all (else nullptr).
+__device__ __forceinline__ bool advance(const tq_kv4 &kv, const Geo &ge, const KvSeq *seqs, Run &u) {
     if (++u.rt >= u.nrt) {
         u.rt = 0;
         if (++u.h >= kv.heads) {
@@ -148,7 +153,7 @@ __device__ __forceinline__ bool advance(const tq_kv4 &kv, const Geo &ge, Run &u)
             bool bad = false;
             do {
                 if (++u.b >= kv.nseq) return false;
-                u.q = kv_seq(kv, u.b, bad);
+                u.q = seqs ? seqs[u.b] : kv_seq(kv, u.b, bad);
             } while (u.q.n == 0);
             u.nrt = row_tiles(ge, u.q);
         }
@@ -198,8 +203,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-__device__ __forceinline__ void join_bar(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
@@ -252,25 +255,26 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     float *rowc = rowf + R;
     float *wm = rowc + R;                // [NW][R]
     float *wl = wm + NW * R;             // [NW][R]
-    const uint32_t bar_full = smb + C::oBar, bar_empty = bar_full + NW * S * 8;
-    volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(sm + C::oMask);
+    const uint32_t bar0 = smb + C::oBar + warp * S * 8;      // this warp's stages
+    volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(sm + C::oMask) + warp * S;
+    unsigned char *ring = sm + warp * S * C::TILE;
+    const uint32_t ring_at = smb + warp * S * C::TILE;
     int64_t *scan = reinterpret_cast<int64_t *>(sm + C::oScan);
     int64_t *wsum = scan + C::NT;
-    volatile int *flag = reinterpret_cast<volatile int *>(wsum + 32);   // 0: a wait ran out, 1: last to arrive,
-                                                                     // 3: tiles issued
-    Found *found = reinterpret_cast<Found *>(sm + C::oFound);
-    float *obuf = reinterpret_cast<float *>(sm + C::oO);
+    volatile int *flag = reinterpret_cast<volatile int *>(wsum + 32);   // 0: a wait ran out, 1: last to arrive
     const tq_kv4 &kv = p.kv;
     const Geo &ge = p.geo;
+    KvSeq *seqs_sh = reinterpret_cast<KvSeq *>(sm + C::oSeq);
+    const KvSeq *seqs = kv.nseq <= C::NT ? seqs_sh : nullptr;
+    Found *found = reinterpret_cast<Found *>(sm + C::oFound);
+    float *obuf = reinterpret_cast<float *>(sm + C::oO);
 
     if (tid == 0) {
-        for (int i = 0; i < NW * S; ++i) {
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_full + 8 * i) : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar_empty + 8 * i) : "memory");
-        }
+        for (int i = 0; i < NW * S; ++i)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smb + C::oBar + 8 * i) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        flag[0] = flag[3] = 0;
+        flag[0] = 0;
     }
 
     // ---------------------------------------------------- this CTA's run
@@ -282,8 +286,9 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     auto scan_step = [&](int64_t base) {
         mine = {0, 0, 0};
         if (base + tid < kv.nseq) mine = kv_seq(kv, base + tid, bad);
+        seqs_sh[tid] = mine;
         if (p.wide) {                     // a warp a sequence
-            for (int i = warp; i < C::NT; i += NW + 1) {
+            for (int i = warp; i < C::NT; i += NW) {
                 int64_t c = 0;
                 bool again = false;
                 if (base + i < kv.nseq) c = seq_cost_warp(ge, kv_seq(kv, base + i, again));
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         __syncthreads();
         int64_t before = 0, all = 0;
 #pragma unroll
-        for (int w = 0; w < NW + 1; ++w) {
+        for (int w = 0; w < NW; ++w) {
             if (w < warp) before += wsum[w];
             all += wsum[w];
         }
@@ -372,96 +377,74 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     const int first = static_cast<int>(at);          // tile of the first row tile that the run starts at
     const int64_t n_all = c1 - c0;
 
-    // The end of every warp.  After a wait that ran out nobody has seen the
-    // copies land: thread 0 waits for the last use of every stage.
-    auto leave = [&]() {
-        __syncthreads();
-        if (flag[0] && tid == 0) {
-            const long long t0 = clock64();
-            for (int slot = 0; slot < NW * S && slot < flag[3]; ++slot) {
-                const int last = (flag[3] - 1 - slot) / (NW * S);        // the stage's last use
-                const long long left = kA16DrainLimit - (clock64() - t0);
-                mbar_wait_bounded(bar_full + 8 * slot, last & 1, left > 0 ? left : 0);
-            }
-        }
-        __syncthreads();
-    };
-
-    if (warp == NW) {
-        // ------------------------------------------------ producer
-        // Tile k of the run goes to stage k % (NW S), whose consumer is warp
-        // k % NW.
-        int64_t done = 0;
-        int from = first, slot = 0, issued = 0;
-        uint32_t phase = 1;               // a stage's first use finds it empty
-        bool failed = false;
-        const int per_page = kv.page_size / kTile;   // tiles a page (0: a page is half a tile)
-        while (done < n_all && !failed) {
-            const int n = static_cast<int>(min(static_cast<int64_t>(u.cost - from), n_all - done));
-            for (int base = 0; base < n && !failed; base += 32) {
-                // pages of 32 tiles at once
-                const int t = u.t0 + from + base + lane;
-                const int pos = t * kTile;
-                const unsigned char *src0 = nullptr, *src1 = nullptr;
-                if (base + lane < n && pos < u.hi) {
-                    const int pg = kv_page(kv, u.b, pos);
-                    if (pg >= 0) src0 = kv_block(kv, pg, u.h, pos % kv.page_size);
-                    if (per_page == 0 && pos + kKvBlock < u.hi) {
-                        const int pg1 = kv_page(kv, u.b, pos + kKvBlock);
-                        if (pg1 >= 0) src1 = kv_block(kv, pg1, u.h, 0);
+    // ---------------------------------------------------- this warp's copies
+    // Its tiles are warp, warp + NW, .. of the run.  Lane i holds where tile i of
+    // 32 at a time lies (two pieces where a page is half a tile; 0: nowhere),
+    // and the stages are filled in turn.
+    uint64_t src0 = 0, src1 = 0;
+    const bool halves = kv.page_size < kTile;
+    {
+        Run *it = reinterpret_cast<Run *>(sm + C::oIter + warp * 64);
+        if (lane == 0) *it = u;
+        __syncwarp();
+    }
+    int64_t it_start = -first;                       // the iterator's row tile begins at this tile of the run
+    auto find_tiles = [&](int64_t k0) {              // tiles k0, k0 + NW, .. of the run
+        Run *it = reinterpret_cast<Run *>(sm + C::oIter + warp * 64);
+        Run v = *it;
+        const int64_t k = k0 + static_cast<int64_t>(lane) * NW, end = min(k0 + 32 * NW, n_all);
+        src0 = src1 = 0;
+        for (;;) {
+            if (k >= it_start && k < it_start + v.cost && k < n_all) {
+                const int pos = (v.t0 + static_cast<int>(k - it_start)) * kTile;
+                if (pos < v.hi) {
+                    const int pg = kv_page(kv, v.b, pos);
+                    if (pg >= 0) src0 = reinterpret_cast<uint64_t>(kv_block(kv, pg, v.h, pos & (kv.page_size - 1)));
+                    else bad = true;
+                    if (halves && pos + kKvBlock < v.hi) {
+                        const int pg1 = kv_page(kv, v.b, pos + kKvBlock);
+                        if (pg1 >= 0) src1 = reinterpret_cast<uint64_t>(kv_block(kv, pg1, v.h, 0));
                         else bad = true;
                     }
-                    if (pg < 0) bad = true;
                 }
-                const int m = min(32, n - base);
-                for (int l = 0; l < m; ++l) {
-                    if (!mbar_try(bar_empty + 8 * slot, phase) &&
-                        !mbar_wait_bounded(bar_empty + 8 * slot, phase, flag[0] ? 0 : kA16WaitLimit)) {
-                        failed = true;
-                        break;
-                    }
-                    const uint64_t a0 = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src0), l);
-                    const uint64_t a1 = per_page ? 0 : __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src1), l);
-                    if (elect_one()) {
-                        const uint32_t dst = smb + slot * C::TILE, bar = bar_full + 8 * slot;
-                        const uint32_t n0 = per_page ? C::TILE : C::BLK;
-                        mask_sh[slot] = (a0 ? (per_page ? 3u : 1u) : 0u) | (a1 ? 2u : 0u);
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                                     "r"(kUnset + (a0 ? n0 : 0u) + (a1 ? C::BLK : 0u))
-                                     : "memory");
-                        if (a0) bulk_copy(dst, a0, n0, bar);
-                        if (a1) bulk_copy(dst + C::BLK, a1, C::BLK, bar);
-                    }
-                    ++issued;
-                    if (++slot == NW * S) {
-                        slot = 0;
-                        phase ^= 1;
-                    }
-                }
-                __syncwarp();
             }
-            if (failed) break;
-            done += n;
-            from = 0;
-            if (done < n_all && !advance(kv, ge, u)) break;
+            if (it_start + v.cost >= end) break;
+            it_start += v.cost;
+            if (!advance(kv, ge, seqs, v)) break;
         }
-        if (bad) atomicOr(p.status, kStatusIndex);
-        if (lane == 0) flag[3] = issued;
-        if (failed && lane == 0) {
-            flag[0] = 1;
-            atomicOr(p.status, kStatusKvTimeout);
+        __syncwarp();
+        if (lane == 0) *it = v;
+        __syncwarp();
+    };
+    int sent = 0;                                    // tiles copied so far
+    auto send = [&](int64_t k, int stage) {          // tile k of the run, into a free stage
+        if (k >= n_all) return;
+        if ((sent & 31) == 0) find_tiles(k);
+        const uint64_t a0 = __shfl_sync(0xffffffffu, src0, sent & 31);
+        const uint64_t a1 = halves ? __shfl_sync(0xffffffffu, src1, sent & 31) : 0;
+        ++sent;
+        if (elect_one()) {
+            const uint32_t dst = ring_at + stage * C::TILE, bar = bar0 + 8 * stage;
+            const uint32_t n0 = halves ? C::BLK : C::TILE;
+            mask_sh[stage] = (a0 ? (halves ? 1u : 3u) : 0u) | (a1 ? 2u : 0u);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                         "r"(kUnset + (a0 ? n0 : 0u) + (a1 ? C::BLK : 0u))
+                         : "memory");
+            if (a0) bulk_copy(dst, a0, n0, bar);
+            if (a1) bulk_copy(dst + C::BLK, a1, C::BLK, bar);
         }
-        leave();
-        return;
-    }
+        __syncwarp();
+    };
+#pragma unroll 1
+    for (int i = 0; i < S; ++i) send(warp + static_cast<int64_t>(i) * NW, i);
 
-    // ---------------------------------------------------- consumers
+    // ---------------------------------------------------- parts of the run
     const int r = lane >> 2, j = lane & 3;
     int64_t done = 0;                     // tiles of the run before this part
     int from = first;
     bool lost = false;
-    int stage = warp, next = warp;        // this warp's next stage, and its next tile of the part
-    uint32_t stage_phase = 0;
+    int stage = 0, next = warp;           // this warp's next stage, and its next tile of the part
+    uint32_t phase = 0;
     while (done < n_all) {
         const int n = static_cast<int>(min(static_cast<int64_t>(u.cost - from), n_all - done));
         const int rows = u.q.n * ge.g, r0 = u.rt * R;
@@ -509,7 +492,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 rowc[i] = -8.0f / 16777216.0f * sum;
             }
         }
-        join_bar(NW * 32);
+        __syncthreads();
 
         // per lane: query rows 8 nt + 2 j and 8 nt + 2 j + 1
         float f[NR][2], cst[NR][2], m[NR][2], l[NR][2];
@@ -559,23 +542,16 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         // this warp's tiles of the part
         for (; next < n; next += NW) {
             const int i = next;
-            const int slot = stage;
-            const uint32_t full_phase = stage_phase;
-            stage += NW;
-            if (stage >= NW * S) {
-                stage = warp;
-                stage_phase ^= 1;
-            }
-            if (!lost && !mbar_try(bar_full + 8 * slot, full_phase) &&
-                !mbar_wait_bounded(bar_full + 8 * slot, full_phase, flag[0] ? 0 : kA16WaitLimit)) {
+            if (!lost && !mbar_try(bar0 + 8 * stage, phase) &&
+                !mbar_wait_bounded(bar0 + 8 * stage, phase, flag[0] ? 0 : kA16WaitLimit)) {
                 lost = true;
                 flag[0] = 1;
                 if (lane == 0) atomicOr(p.status, kStatusKvTimeout);
             }
             if (lost) continue;
             const int tile_at = (u.t0 + from + i) * kTile;
-            const unsigned char *base = sm + slot * C::TILE;
-            const uint32_t have = mask_sh[slot];
+            const unsigned char *base = ring + stage * C::TILE;
+            const uint32_t have = mask_sh[stage];
 
             // scores: S^T, tokens r and r + 8 of each block, times the key's scale
             float s[2][NR][4], sv[2][2];
@@ -735,8 +711,12 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar_empty + 8 * slot) : "memory");
+            __syncwarp();                 // every lane has read the stage
+            send(done + i + static_cast<int64_t>(S) * NW, stage);
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1;
+            }
         }
 
         // ------------------------------------------------ join the warps
@@ -751,7 +731,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                     wl[warp * R + nt * 8 + 2 * j + c] = l[nt][c];
                 }
             }
-        join_bar(NW * 32);
+        __syncthreads();
         // the warp's share of each row, relative to the row's largest maximum
         float fac[NR][2];
 #pragma unroll
@@ -784,7 +764,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                             *dst = v;
                         }
             }
-            join_bar(NW * 32);
+            __syncthreads();
         }
         auto row_stat = [&](int i, float &mx, float &sum) {
             mx = kNone;
@@ -807,7 +787,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             auto slot_of = [&](int c) { return static_cast<int64_t>(2) * c + (c == cf ? 1 : 0); };
             float *part = p.part + slot_of(blockIdx.x) * R * D;
             float *stat = p.stat + slot_of(blockIdx.x) * R * 2;
-            for (int i = tid; i < CH; i += NW * 32) {
+            for (int i = tid; i < CH; i += C::NT) {
                 const int row = i / (D / 4), col = i % (D / 4) * 4;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -817,12 +797,12 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 }
                 __stcg(reinterpret_cast<float4 *>(part + row * D + col), v);
             }
-            for (int i = tid; i < R; i += NW * 32) {
+            for (int i = tid; i < R; i += C::NT) {
                 float mx, sum;
                 row_stat(i, mx, sum);
                 __stcg(reinterpret_cast<float2 *>(stat + 2 * i), make_float2(mx, sum));
             }
-            join_bar(NW * 32);
+            __syncthreads();
             if (tid == 0) {
                 __threadfence();                         // the CTA's stores, ordered before it by the barrier
                 const unsigned int old = atomicAdd(p.count + cf, 1u);
@@ -833,37 +813,66 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                     __threadfence();
                 }
             }
-            join_bar(NW * 32);
+            __syncthreads();
             write = flag[1] != 0;
             if (write) {
-                for (int i = tid; i < R; i += NW * 32) {
-                    float mx = kNone, sum = 0.0f;
-                    for (int c = cf; c <= cl; ++c) mx = fmaxf(mx, __ldcg(p.stat + slot_of(c) * R * 2 + 2 * i));
-                    for (int c = cf; c <= cl; ++c) {
-                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(p.stat + slot_of(c) * R * 2 + 2 * i));
-                        sum += t.y * ex2(t.x - mx);
-                    }
-                    wm[i] = mx;
-                    wl[i] = sum;
+                // the rows' largest maximum over the parts, then 32 parts at a
+                // time: their factors, and every thread's pieces of the output
+                float *fac = obuf + C::OBUF / 4, *sums = fac + 32 * R, *best = sums + 32 * R;
+                constexpr int PER = C::NT / R;
+                const int row_ = tid % R, sub = tid / R;
+                float mx = kNone;
+                for (int c = cf + sub; c <= cl; c += PER)
+                    mx = fmaxf(mx, __ldcg(p.stat + slot_of(c) * R * 2 + 2 * row_));
+                best[tid] = mx;
+                __syncthreads();
+                if (tid < R) {
+#pragma unroll
+                    for (int k = 1; k < PER; ++k) mx = fmaxf(mx, best[k * R + tid]);
+                    wm[tid] = mx;
+                    wl[tid] = 0.0f;
                 }
-                join_bar(NW * 32);
-                for (int i = tid; i < CH; i += NW * 32) {
-                    const int row = i / (D / 4), col = i % (D / 4) * 4;
-                    const float mx = wm[row];
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = cf; c <= cl; ++c) {
-                        const int64_t sl = slot_of(c);
-                        const float fc = ex2(__ldcg(p.stat + sl * R * 2 + 2 * row) - mx);
-                        const float4 t = __ldcg(reinterpret_cast<const float4 *>(p.part + sl * R * D + row * D + col));
-                        v = make_float4(fmaf(fc, t.x, v.x), fmaf(fc, t.y, v.y), fmaf(fc, t.z, v.z), fmaf(fc, t.w, v.w));
+                constexpr int MINE = (CH + C::NT - 1) / C::NT;
+                float4 v[MINE];
+#pragma unroll
+                for (int k = 0; k < MINE; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c32 = cf; c32 <= cl; c32 += 32) {
+                    const int np = min(32, cl - c32 + 1);
+                    __syncthreads();
+                    for (int k = sub; k < np; k += PER) {
+                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(p.stat + slot_of(c32 + k) * R * 2 + 2 * row_));
+                        const float fc = ex2(t.x - wm[row_]);
+                        fac[k * R + row_] = fc;
+                        sums[k * R + row_] = fc * t.y;
                     }
-                    *reinterpret_cast<float4 *>(obuf + row * C::OROW + col) = v;
+                    __syncthreads();
+                    if (tid < R)
+                        for (int k = 0; k < np; ++k) wl[tid] += sums[k * R + tid];
+#pragma unroll
+                    for (int k = 0; k < MINE; ++k) {
+                        const int i = tid + k * C::NT;
+                        if (CH % C::NT && i >= CH) continue;
+                        const int row = i / (D / 4), col = i % (D / 4) * 4;
+#pragma unroll 8
+                        for (int c = 0; c < np; ++c) {
+                            const float fc = fac[c * R + row];
+                            const float4 t =
+                                __ldcg(reinterpret_cast<const float4 *>(p.part + (slot_of(c32 + c) * R + row) * D + col));
+                            v[k] = make_float4(fmaf(fc, t.x, v[k].x), fmaf(fc, t.y, v[k].y), fmaf(fc, t.z, v[k].z),
+                                               fmaf(fc, t.w, v[k].w));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < MINE; ++k) {
+                    const int i = tid + k * C::NT;
+                    if (CH % C::NT && i >= CH) continue;
+                    *reinterpret_cast<float4 *>(obuf + i / (D / 4) * C::OROW + i % (D / 4) * 4) = v[k];
                 }
             }
         } else {
             float mx[1], sum[1];
-            for (int i = tid; i < CH; i += NW * 32) {
+            for (int i = tid; i < CH; i += C::NT) {
                 const int row = i / (D / 4), col = i % (D / 4) * 4;
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -874,14 +883,14 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 *reinterpret_cast<float4 *>(obuf + row * C::OROW + col) = v;
             }
             if (tid < R) row_stat(tid, mx[0], sum[0]);
-            join_bar(NW * 32);                            // every read of wm, wl before they are written
+            __syncthreads();                            // every read of wm, wl before they are written
             if (tid < R) {
                 wm[tid] = mx[0];
                 wl[tid] = sum[0];
             }
         }
         if (write) {
-            join_bar(NW * 32);
+            __syncthreads();
             for (int i = warp; i < R && r0 + i < rows; i += NW) {
                 constexpr int E = D / 32;
                 const int64_t tok = u.q.start + (r0 + i) / ge.g;
@@ -905,13 +914,22 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                     p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (wm[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
             }
         }
-        join_bar(NW * 32);
+        __syncthreads();
         done += n;
         next -= n;
         from = 0;
-        if (done < n_all && !advance(kv, ge, u)) break;
+        if (done < n_all && !advance(kv, ge, seqs, u)) break;
     }
-    leave();
+    if (bad) atomicOr(p.status, kStatusIndex);
+    if (lost && lane == 0) {
+        // after a wait that ran out nobody has seen the copies land: wait for
+        // the last use of each of this warp's stages
+        const long long t0 = clock64();
+        for (int i = 0; i < S && i < sent; ++i) {
+            const long long left = kA16DrainLimit - (clock64() - t0);
+            mbar_wait_bounded(bar0 + 8 * i, ((sent - 1 - i) / S) & 1, left > 0 ? left : 0);
+        }
+    }
 }
 
 constexpr int kMaxCtas = 2;                              // CTAs an SM, over the variants
@@ -964,17 +982,17 @@ tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceI
     if (!p.status) return TQ_ERR_DEVICE;
     const int64_t rows = a.max_q * p.geo.g;
     if (kv.dim == 64) {
-        if (rows <= 8) return launch<Cfg<64, 1, 7, 4, 2>>(p, dev, s);
-        if (rows <= 16) return launch<Cfg<64, 2, 7, 4, 2>>(p, dev, s);
-        return launch<Cfg<64, 4, 11, 4, 1>>(p, dev, s);
+        if (rows <= 8) return launch<Cfg<64, 1, 8, 4, 2>>(p, dev, s);
+        if (rows <= 16) return launch<Cfg<64, 2, 8, 4, 2>>(p, dev, s);
+        return launch<Cfg<64, 4, 8, 4, 1>>(p, dev, s);
     }
     if (kv.dim == 128) {
-        if (rows <= 8) return launch<Cfg<128, 1, 7, 2, 2>>(p, dev, s);
-        if (rows <= 16) return launch<Cfg<128, 2, 11, 3, 1>>(p, dev, s);
-        return launch<Cfg<128, 4, 7, 4, 1>>(p, dev, s);
+        if (rows <= 8) return launch<Cfg<128, 1, 8, 2, 2>>(p, dev, s);
+        if (rows <= 16) return launch<Cfg<128, 2, 12, 3, 1>>(p, dev, s);
+        return launch<Cfg<128, 4, 8, 4, 1>>(p, dev, s);
     }
-    if (rows <= 8) return launch<Cfg<256, 1, 11, 2, 1>>(p, dev, s);
-    return launch<Cfg<256, 2, 7, 2, 1>>(p, dev, s);
+    if (rows <= 8) return launch<Cfg<256, 1, 8, 2, 1>>(p, dev, s);
+    return launch<Cfg<256, 2, 8, 2, 1>>(p, dev, s);
 }
 
 }  // namespace tq
