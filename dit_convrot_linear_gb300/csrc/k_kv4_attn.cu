@@ -41,6 +41,7 @@ namespace tq {
 namespace {
 
 constexpr int kTile = 32;                    // tokens a tile: two blocks
+constexpr int kMinRun = 48;                  // fewest tiles a part, where row tiles are cut on their own
 constexpr unsigned int kStatusKvTimeout = 128u;
 // A copy of the library built for its own tests lets every stage expect bytes
 // that no copy brings (their waits then run out).
@@ -65,20 +66,22 @@ struct Cfg {
     static constexpr int QROW = 2 * D + 64;                  // bytes; rows 64 bytes apart mod 128: no bank conflicts
     static constexpr int OROW = D + 4;                       // floats
     static constexpr int OBUF = R * OROW * 4;
-    static constexpr int JOIN0 = 34816 / OBUF;               // warps that join at once
-    static constexpr int JOIN = JOIN0 < NW ? JOIN0 : NW;
-    static_assert(JOIN >= 2, "the second buffer holds the parts' factors in the last join");
+    static constexpr int JOIN0 = 34816 / OBUF;               // output buffers: as many warps join at once
+    static constexpr int JOIN = JOIN0 < 2 ? 2 : JOIN0 < NW ? JOIN0 : NW;
     // shared memory
     static constexpr int oQ = NW * STAGES * TILE;
     static constexpr int oO = oQ + R * QROW;
-    static constexpr int oStat = oO + JOIN * OBUF;           // per row: factor, bias; per warp and row: m, l
-    static constexpr int oBar = (oStat + (2 * R + 2 * NW * R) * 4 + 7) / 8 * 8;
+    static constexpr int oStat = oO + JOIN * OBUF;           // the float arrays named in the kernel
+    static constexpr int oBar = oStat + (2 * R + 4 * NW * R) * 4;
     static constexpr int oMask = oBar + NW * STAGES * 8;
     static constexpr int oSeq = (oMask + NW * STAGES * 4 + 7) / 8 * 8;
     static constexpr int oIter = oSeq + NT * static_cast<int>(sizeof(KvSeq));
-    static constexpr int oScan = (oIter + NW * 64 + 7) / 8 * 8;
-    static constexpr int oFound = oScan + NT * 8 + 32 * 8 + 16;
-    static constexpr int SMEM = oFound + 64;
+    static constexpr int oFound = oIter + NW * 64;
+    static constexpr int oPart = oFound + 64;
+    static constexpr int oFlag = oPart + 2 * 64;
+    static constexpr int SMEM = oFlag + 16;
+    static constexpr int oScan = oO;                         // before any output
+    static_assert(NT * 8 + NW * 8 <= JOIN * OBUF && SMEM <= 228 * 1024 / CTAS - 1024, "shared memory");
 };
 
 struct Geo {                                 // what the cutting of a batch depends on
@@ -174,6 +177,12 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     return w;
 }
 
+__device__ __forceinline__ uint32_t bf16_bits2(float lo, float hi) {          // bf16
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
 // Transpose of an 8 x 8 matrix of 16-bit values held as mma fragments are.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -233,6 +242,12 @@ struct Found {                               // where a CTA's run starts
     KvSeq q;
 };
 
+struct Part {                                // a part of a row tile whose others are elsewhere
+    Run u;
+    int cf, cl;                              // CTAs that hold its parts
+};
+static_assert(sizeof(Run) <= 64 && sizeof(Part) <= 64 && sizeof(Found) <= 64, "shared memory");
+
 struct AttnParams {
     tq_kv4 kv;
     Kv4Attn a;
@@ -242,31 +257,34 @@ struct AttnParams {
     float *stat;             // [2 grid][R][2] their maxima (log2) and sums
     unsigned int *status;
     int min_run;             // fewest tiles a run
+    int aligned;             // few row tiles: cut each on its own
     int wide;                // rows of one sequence may fill more than one row tile
 };
 
 template <class C>
 __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_constant__ AttnParams p) {
     constexpr int D = C::D, NR = C::NR, NW = C::NW, R = C::R, W = C::W, S = C::STAGES;
+    constexpr bool OWN = C::JOIN == NW;      // an output buffer a warp
     extern __shared__ __align__(128) unsigned char sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t smb = smem_addr(sm);
     float *rowf = reinterpret_cast<float *>(sm + C::oStat);
     float *rowc = rowf + R;
-    float *wm = rowc + R;                // [NW][R]
-    float *wl = wm + NW * R;             // [NW][R]
+    float2 *wstat = reinterpret_cast<float2 *>(rowc + R);    // [NW][R] each warp's maximum and sum
+    float2 *red = wstat + NW * R;        // [NW][R] a row's maximum and sum over the sources, by warps
     const uint32_t bar0 = smb + C::oBar + warp * S * 8;      // this warp's stages
     volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(sm + C::oMask) + warp * S;
     unsigned char *ring = sm + warp * S * C::TILE;
     const uint32_t ring_at = smb + warp * S * C::TILE;
     int64_t *scan = reinterpret_cast<int64_t *>(sm + C::oScan);
     int64_t *wsum = scan + C::NT;
-    volatile int *flag = reinterpret_cast<volatile int *>(wsum + 32);   // 0: a wait ran out, 1: last to arrive
+    volatile int *flag = reinterpret_cast<volatile int *>(sm + C::oFlag);   // 0: a wait ran out, 1, 2: last to arrive
     const tq_kv4 &kv = p.kv;
     const Geo &ge = p.geo;
     KvSeq *seqs_sh = reinterpret_cast<KvSeq *>(sm + C::oSeq);
     const KvSeq *seqs = kv.nseq <= C::NT ? seqs_sh : nullptr;
     Found *found = reinterpret_cast<Found *>(sm + C::oFound);
+    Part *parts = reinterpret_cast<Part *>(sm + C::oPart);
     float *obuf = reinterpret_cast<float *>(sm + C::oO);
 
     if (tid == 0) {
@@ -283,6 +301,23 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     bool bad = false;
     KvSeq mine = {0, 0, 0};               // sequence base + tid of the scan's step, its tiles a head, and
     int64_t head = 0, mine_at = 0, step_sum = 0;   // those of all heads before it in the step and in the step
+    auto block_scan = [&](int64_t v, int64_t &before, int64_t &all) {      // exclusive prefix, and the sum
+        int64_t x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) wsum[warp] = x;
+        __syncthreads();
+        before = x - v;
+        all = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += wsum[w];
+            all += wsum[w];
+        }
+    };
     auto scan_step = [&](int64_t base) {
         mine = {0, 0, 0};
         if (base + tid < kv.nseq) mine = kv_seq(kv, base + tid, bad);
@@ -299,22 +334,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         } else {
             head = seq_cost(ge, mine);
         }
-        int64_t x = head * kv.heads;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) wsum[warp] = x;
-        __syncthreads();
-        int64_t before = 0, all = 0;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if (w < warp) before += wsum[w];
-            all += wsum[w];
-        }
-        mine_at = before + x - head * kv.heads;
-        step_sum = all;
+        block_scan(head * kv.heads, mine_at, step_sum);
     };
     int64_t total = 0;
     for (int64_t base = 0; base < kv.nseq; base += C::NT) {
@@ -325,58 +345,104 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusIndex);
     int64_t per = quotient(total + gridDim.x - 1, gridDim.x);
     per = per < p.min_run ? p.min_run : per;
-    const int64_t c0 = blockIdx.x * per, c1 = c0 + per < total ? c0 + per : total;
-    if (c0 >= c1) return;
-    int64_t passed = 0;
-    for (int64_t base = 0; base < kv.nseq; base += C::NT) {
-        if (kv.nseq > C::NT) {            // one step: its scan is still at hand
-            __syncthreads();
-            scan_step(base);
-        }
-        if (c0 < passed + step_sum) {
-            const int64_t at = c0 - passed - mine_at;
-            if (at >= 0 && at < head * kv.heads) {
-                found->b = static_cast<int>(base + tid);
-                found->q = mine;
-                found->at = at;
-                found->head = head;
-            }
-            break;
-        }
-        passed += step_sum;
-    }
-    __syncthreads();
+    const int cta = static_cast<int>(blockIdx.x);
     Run u;
-    u.b = found->b;
-    u.q = found->q;
-    u.nrt = row_tiles(ge, u.q);
-    u.h = static_cast<int>(quotient(found->at, found->head));
-    int64_t at = found->at - u.h * found->head;
-    u.rt = 0;
-    if (u.nrt > 1) {                      // the row tile: by 32 at a time
-        for (int base = 0; base < u.nrt; base += 32) {
-            int lo, hi, t0, c = 0;
-            if (base + lane < u.nrt) range_of(ge, u.q, base + lane, lo, hi, t0, c);
-            int64_t x = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
+    int64_t c0 = 0, n_all, at;            // the run's first tile over the batch, its tiles; its first tile in its row tile
+    bool aligned = false;                 // each row tile is cut on its own, into parts of about `per` tiles
+    int acf = 0, acl = 0;                 // the CTAs that hold its parts then
+    auto parts_of = [&](int64_t cost) { return cost < per ? 1 : static_cast<int>(quotient(cost, per)); };
+    if (p.aligned) {
+        int np = 0;                       // parts of a head of this thread's sequence
+        const int nrt = row_tiles(ge, mine);
+        for (int rt = 0; rt < nrt; ++rt) {
+            int lo, hi, t0, c;
+            range_of(ge, mine, rt, lo, hi, t0, c);
+            np += parts_of(c);
+        }
+        int64_t np_at, np_sum;
+        __syncthreads();
+        block_scan(static_cast<int64_t>(np) * kv.heads, np_at, np_sum);
+        aligned = np_sum <= gridDim.x;
+        if (aligned) {
+            if (cta >= np_sum) return;
+            const int64_t k = cta - np_at;
+            if (k >= 0 && k < static_cast<int64_t>(np) * kv.heads) {
+                found->b = tid;
+                found->q = mine;
+                found->at = k;
+                found->head = np;
             }
-            const unsigned in = __ballot_sync(0xffffffffu, x > at);
-            if (in) {
-                const int l = __ffs(in) - 1;
-                u.rt = base + l;
-                at -= __shfl_sync(0xffffffffu, x - c, l);
+            __syncthreads();
+            u.b = found->b;
+            u.q = found->q;
+            u.nrt = row_tiles(ge, u.q);
+            u.h = static_cast<int>(found->at) / static_cast<int>(found->head);
+            int k2 = static_cast<int>(found->at) % static_cast<int>(found->head), n2 = 1;
+            for (u.rt = 0; u.rt < u.nrt; ++u.rt) {
+                range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
+                n2 = parts_of(u.cost);
+                if (k2 < n2) break;
+                k2 -= n2;
+            }
+            acf = cta - k2;
+            acl = acf + n2 - 1;
+            at = static_cast<int64_t>(u.cost) * k2 / n2;
+            n_all = static_cast<int64_t>(u.cost) * (k2 + 1) / n2 - at;
+        }
+    }
+    if (!aligned) {
+        c0 = cta * per;
+        const int64_t c1 = c0 + per < total ? c0 + per : total;
+        if (c0 >= c1) return;
+        n_all = c1 - c0;
+        int64_t passed = 0;
+        for (int64_t base = 0; base < kv.nseq; base += C::NT) {
+            if (kv.nseq > C::NT) {        // one step: its scan is still at hand
+                __syncthreads();
+                scan_step(base);
+            }
+            if (c0 < passed + step_sum) {
+                const int64_t k = c0 - passed - mine_at;
+                if (k >= 0 && k < head * kv.heads) {
+                    found->b = static_cast<int>(base + tid);
+                    found->q = mine;
+                    found->at = k;
+                    found->head = head;
+                }
                 break;
             }
-            at -= __shfl_sync(0xffffffffu, x, 31);
+            passed += step_sum;
         }
+        __syncthreads();
+        u.b = found->b;
+        u.q = found->q;
+        u.nrt = row_tiles(ge, u.q);
+        u.h = static_cast<int>(quotient(found->at, found->head));
+        at = found->at - u.h * found->head;
+        u.rt = 0;
+        if (u.nrt > 1) {                  // the row tile: by 32 at a time
+            for (int base = 0; base < u.nrt; base += 32) {
+                int lo, hi, t0, c = 0;
+                if (base + lane < u.nrt) range_of(ge, u.q, base + lane, lo, hi, t0, c);
+                int64_t x = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                const unsigned in = __ballot_sync(0xffffffffu, x > at);
+                if (in) {
+                    const int l = __ffs(in) - 1;
+                    u.rt = base + l;
+                    at -= __shfl_sync(0xffffffffu, x - c, l);
+                    break;
+                }
+                at -= __shfl_sync(0xffffffffu, x, 31);
+            }
+        }
+        range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
     }
-    range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
     const int first = static_cast<int>(at);          // tile of the first row tile that the run starts at
-    const int64_t n_all = c1 - c0;
-
     // ---------------------------------------------------- this warp's copies
     // Its tiles are warp, warp + NW, .. of the run.  Lane i holds where tile i of
     // 32 at a time lies (two pieces where a page is half a tile; 0: nowhere),
@@ -445,7 +511,41 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     bool lost = false;
     int stage = 0, next = warp;           // this warp's next stage, and its next tile of the part
     uint32_t phase = 0;
-    while (done < n_all) {
+    // Row tiles in turn.  Parts whose others are elsewhere go to the workspace;
+    // at the end of the run their arrivals are counted (once, for all of them),
+    // and the CTA that comes last joins them.  A row tile's parts belong to CTAs
+    // cf .. cl; only the first of them can hold it as its run's last part (slot
+    // 2 cf + 1), the others hold it as their run's first (slot 2 c).  Joining the
+    // warps and joining the parts are one piece of code: what few CTAs run has to
+    // be fetched from far away.
+    int nparts = 0, joined = -1;          // parts left elsewhere; parts looked at for the last join
+    int cf = 0, cl = 0;
+    for (;;) {
+      const bool last = done >= n_all;    // joining parts, not warps
+      bool whole = true;
+      if (last) {
+        if (joined < 0) {
+            if (nparts == 0) break;
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();          // the CTA's stores, ordered before it by the barrier
+                for (int i = 0; i < nparts; ++i) {
+                    const unsigned int old = atomicAdd(p.count + parts[i].cf, 1u);
+                    flag[1 + i] = old == static_cast<unsigned int>(parts[i].cl - parts[i].cf);
+                    if (flag[1 + i]) p.count[parts[i].cf] = 0u;
+                }
+                __threadfence();
+            }
+            __syncthreads();
+            joined = 0;
+        }
+        while (joined < nparts && !flag[1 + joined]) ++joined;
+        if (joined == nparts) break;
+        u = parts[joined].u;
+        cf = parts[joined].cf;
+        cl = parts[joined].cl;
+        ++joined;
+      } else {
         const int n = static_cast<int>(min(static_cast<int64_t>(u.cost - from), n_all - done));
         const int rows = u.q.n * ge.g, r0 = u.rt * R;
 
@@ -726,25 +826,28 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
-                if (r == 0) {
-                    wm[warp * R + nt * 8 + 2 * j + c] = m[nt][c];
-                    wl[warp * R + nt * 8 + 2 * j + c] = l[nt][c];
-                }
+                if (r == 0) wstat[warp * R + nt * 8 + 2 * j + c] = make_float2(m[nt][c], l[nt][c]);
             }
-        __syncthreads();
-        // the warp's share of each row, relative to the row's largest maximum
-        float fac[NR][2];
+        // Each warp's output into a buffer of its own, relative to its own
+        // maximum; where there are fewer buffers than warps, in rounds, relative
+        // to the rows' largest.
+        float up[NR][2];
+        if constexpr (!OWN) __syncthreads();
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float mx = kNone;
+                up[nt][c] = 16777216.0f / gv;
+                if constexpr (!OWN) {
+                    float mx = kNone;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wm[w * R + nt * 8 + 2 * j + c]);
-                fac[nt][c] = ex2(m[nt][c] - mx) * (16777216.0f / gv);
+                    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wstat[w * R + nt * 8 + 2 * j + c].x);
+                    up[nt][c] *= ex2(m[nt][c] - mx);
+                }
             }
+#pragma unroll 1
         for (int round = 0; round * C::JOIN < NW; ++round) {
-            if (warp / C::JOIN == round) {
+            if (OWN || warp / C::JOIN == round) {
                 float *buf = obuf + (warp % C::JOIN) * (C::OBUF / 4);
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt)
@@ -753,11 +856,11 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 #pragma unroll
                         for (int w = 0; w < W; ++w) {
                             float4 *dst = reinterpret_cast<float4 *>(buf + (nt * 8 + 2 * j + c) * C::OROW + r * (D / 8) + 4 * w);
-                            const float b = oc[nt][c], fc = fac[nt][c];
+                            const float b = oc[nt][c], fc = up[nt][c];
                             float4 v = make_float4((o[nt][2 * w][c] - b) * fc, (o[nt][2 * w][c + 2] * 0.0625f - b) * fc,
                                                    (o[nt][2 * w + 1][c] - b) * fc,
                                                    (o[nt][2 * w + 1][c + 2] * 0.0625f - b) * fc);
-                            if (round) {
+                            if (!OWN && round) {
                                 const float4 t = *dst;
                                 v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
                             }
@@ -766,159 +869,136 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             }
             __syncthreads();
         }
-        auto row_stat = [&](int i, float &mx, float &sum) {
-            mx = kNone;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wm[w * R + i]);
-            sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) sum += wl[w * R + i] * ex2(wm[w * R + i] - mx);
-        };
-        constexpr int CH = R * D / 4;                    // 16-byte pieces of the row tile
-        const bool whole = from == 0 && n == u.cost;
-        bool write = true;
+
+        whole = from == 0 && n == u.cost;
         if (!whole) {
-            // this part to the workspace; the CTA that comes last joins all
-            // parts.  A row tile's parts belong to CTAs c_first .. c_last; only
-            // the first of them can hold it as its run's last part, the others
-            // hold it as their run's first.
             const int64_t start = c0 + done - from;      // the row tile's first tile, over the batch
-            const int cf = static_cast<int>(quotient(start, per)), cl = static_cast<int>(quotient(start + u.cost - 1, per));
-            auto slot_of = [&](int c) { return static_cast<int64_t>(2) * c + (c == cf ? 1 : 0); };
-            float *part = p.part + slot_of(blockIdx.x) * R * D;
-            float *stat = p.stat + slot_of(blockIdx.x) * R * 2;
-            for (int i = tid; i < CH; i += C::NT) {
-                const int row = i / (D / 4), col = i % (D / 4) * 4;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int b = 0; b < C::JOIN; ++b) {
-                    const float4 t = *reinterpret_cast<const float4 *>(obuf + b * (C::OBUF / 4) + row * C::OROW + col);
-                    v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
-                }
-                __stcg(reinterpret_cast<float4 *>(part + row * D + col), v);
-            }
-            for (int i = tid; i < R; i += C::NT) {
-                float mx, sum;
-                row_stat(i, mx, sum);
-                __stcg(reinterpret_cast<float2 *>(stat + 2 * i), make_float2(mx, sum));
-            }
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();                         // the CTA's stores, ordered before it by the barrier
-                const unsigned int old = atomicAdd(p.count + cf, 1u);
-                const int last = old == static_cast<unsigned int>(cl - cf);
-                flag[1] = last;
-                if (last) {
-                    p.count[cf] = 0u;
-                    __threadfence();
-                }
-            }
-            __syncthreads();
-            write = flag[1] != 0;
-            if (write) {
-                // the rows' largest maximum over the parts, then 32 parts at a
-                // time: their factors, and every thread's pieces of the output
-                float *fac = obuf + C::OBUF / 4, *sums = fac + 32 * R, *best = sums + 32 * R;
-                constexpr int PER = C::NT / R;
-                const int row_ = tid % R, sub = tid / R;
-                float mx = kNone;
-                for (int c = cf + sub; c <= cl; c += PER)
-                    mx = fmaxf(mx, __ldcg(p.stat + slot_of(c) * R * 2 + 2 * row_));
-                best[tid] = mx;
-                __syncthreads();
-                if (tid < R) {
-#pragma unroll
-                    for (int k = 1; k < PER; ++k) mx = fmaxf(mx, best[k * R + tid]);
-                    wm[tid] = mx;
-                    wl[tid] = 0.0f;
-                }
-                constexpr int MINE = (CH + C::NT - 1) / C::NT;
-                float4 v[MINE];
-#pragma unroll
-                for (int k = 0; k < MINE; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int c32 = cf; c32 <= cl; c32 += 32) {
-                    const int np = min(32, cl - c32 + 1);
-                    __syncthreads();
-                    for (int k = sub; k < np; k += PER) {
-                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(p.stat + slot_of(c32 + k) * R * 2 + 2 * row_));
-                        const float fc = ex2(t.x - wm[row_]);
-                        fac[k * R + row_] = fc;
-                        sums[k * R + row_] = fc * t.y;
-                    }
-                    __syncthreads();
-                    if (tid < R)
-                        for (int k = 0; k < np; ++k) wl[tid] += sums[k * R + tid];
-#pragma unroll
-                    for (int k = 0; k < MINE; ++k) {
-                        const int i = tid + k * C::NT;
-                        if (CH % C::NT && i >= CH) continue;
-                        const int row = i / (D / 4), col = i % (D / 4) * 4;
-#pragma unroll 8
-                        for (int c = 0; c < np; ++c) {
-                            const float fc = fac[c * R + row];
-                            const float4 t =
-                                __ldcg(reinterpret_cast<const float4 *>(p.part + (slot_of(c32 + c) * R + row) * D + col));
-                            v[k] = make_float4(fmaf(fc, t.x, v[k].x), fmaf(fc, t.y, v[k].y), fmaf(fc, t.z, v[k].z),
-                                               fmaf(fc, t.w, v[k].w));
-                        }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < MINE; ++k) {
-                    const int i = tid + k * C::NT;
-                    if (CH % C::NT && i >= CH) continue;
-                    *reinterpret_cast<float4 *>(obuf + i / (D / 4) * C::OROW + i % (D / 4) * 4) = v[k];
-                }
-            }
-        } else {
-            float mx[1], sum[1];
-            for (int i = tid; i < CH; i += C::NT) {
-                const int row = i / (D / 4), col = i % (D / 4) * 4;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int b = 0; b < C::JOIN; ++b) {
-                    const float4 t = *reinterpret_cast<const float4 *>(obuf + b * (C::OBUF / 4) + row * C::OROW + col);
-                    v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
-                }
-                *reinterpret_cast<float4 *>(obuf + row * C::OROW + col) = v;
-            }
-            if (tid < R) row_stat(tid, mx[0], sum[0]);
-            __syncthreads();                            // every read of wm, wl before they are written
-            if (tid < R) {
-                wm[tid] = mx[0];
-                wl[tid] = sum[0];
-            }
+            cf = aligned ? acf : static_cast<int>(quotient(start, per));
+            cl = aligned ? acl : static_cast<int>(quotient(start + u.cost - 1, per));
+            if (tid == 0) parts[nparts] = {u, cf, cl};
+            ++nparts;
         }
-        if (write) {
-            __syncthreads();
-            for (int i = warp; i < R && r0 + i < rows; i += NW) {
-                constexpr int E = D / 32;
-                const int64_t tok = u.q.start + (r0 + i) / ge.g;
-                const int hq = u.h * ge.g + (r0 + i) % ge.g;
-                const float sum = wl[i], inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = obuf[i * C::OROW + lane * E + e];
-                warp_fwht<E, float>(v);
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e)
-                    w[e] = static_cast<uint32_t>(f32_to_bf16_bits(sum > 0.0f ? v[2 * e] * inv : 0.0f)) |
-                           (static_cast<uint32_t>(f32_to_bf16_bits(sum > 0.0f ? v[2 * e + 1] * inv : 0.0f)) << 16);
-                uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + lane * E;
-                if (flag[0]) continue;                    // the sums are not whole
-                if constexpr (E == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-                else *reinterpret_cast<uint32_t *>(dst) = w[0];
-                if (p.a.lse && lane == 0)
-                    p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (wm[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-            }
-        }
-        __syncthreads();
         done += n;
         next -= n;
         from = 0;
-        if (done < n_all && !advance(kv, ge, seqs, u)) break;
+      }
+
+      constexpr int CH = R * D / 4, PER = C::NT / R;     // 16-byte pieces of the row tile; threads a row
+      const bool keep = last || whole;
+      const int np = last ? cl - cf + 1 : NW;            // sources
+      const float2 *st = last ? reinterpret_cast<const float2 *>(p.stat) + static_cast<int64_t>(2) * cf * R : wstat;
+      const int sstep = last ? 2 * R : R, sfirst = last ? R : 0;
+      // A part's piece is a trip to far memory: each thread brings as many as the
+      // rings hold (they are empty by now) into places of its own there, the
+      // first of them while the statistics come.
+      constexpr int DEPTH = NW * S * C::TILE / (C::NT * 16);
+      static_assert(DEPTH >= C::JOIN, "one step joins the warps");
+      auto bring = [&](int i, int k0, int n) {
+        const float *src = p.part + static_cast<int64_t>(2) * cf * (R * D) + i * 4;
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+            const int kk = k0 + k;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smb + (k * C::NT + tid) * 16),
+                         "l"(src + (kk ? 2 * kk : 1) * (R * D))
+                         : "memory");
+        }
+      };
+      if (last && tid < CH) bring(tid, 0, min(np, DEPTH));
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (static_cast<int>(blockIdx.x) == cf ? 1 : 0);
+      {
+        // each row's maximum over the sources, and the sum relative to it
+        const int row = tid % R;
+        float mx = kNone, sum = 0.0f;
+#pragma unroll 2
+        for (int k = tid / R; k < np; k += PER) {
+            const float2 t = st[k * sstep + (k ? 0 : sfirst) + row];
+            const float to = fmaxf(mx, t.x);
+            sum = fmaf(sum, ex2(mx - to), t.y * ex2(t.x - to));
+            mx = to;
+        }
+#pragma unroll
+        for (int x = R; x < 32; x <<= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, mx, x), s2 = __shfl_xor_sync(0xffffffffu, sum, x);
+            const float to = fmaxf(mx, m2);
+            sum = fmaf(sum, ex2(mx - to), s2 * ex2(m2 - to));
+            mx = to;
+        }
+        if (lane < R) red[warp * R + row] = make_float2(mx, sum);
+      }
+      __syncthreads();
+      auto row_stat = [&](int row, float &mx, float &sum) {
+        mx = kNone;
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) mx = fmaxf(mx, red[w * R + row].x);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) sum = fmaf(red[w * R + row].y, ex2(red[w * R + row].x - mx), sum);
+      };
+      {
+        const int no = last ? np : C::JOIN;
+        const bool scaled = last || OWN;                 // else the buffers share the largest maximum
+        float *dst = keep ? obuf : p.part + slot * (R * D);
+        const int drow = keep ? C::OROW : D;
+#pragma unroll 1
+        for (int i = tid; i < CH; i += C::NT) {
+            const int row = i / (D / 4), col = i % (D / 4) * 4;
+            float mx, sum;
+            row_stat(row, mx, sum);
+            const float *sp = reinterpret_cast<const float *>(st + row);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int k0 = 0; k0 < no; k0 += DEPTH) {
+                const int n = min(no - k0, DEPTH);
+                const float4 *src = reinterpret_cast<const float4 *>(obuf + row * C::OROW + col);
+                int step = C::OBUF / 16;
+                if (last) {
+                    if (k0 || i != tid) bring(i, k0, n);
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    src = reinterpret_cast<const float4 *>(sm) + tid;
+                    step = C::NT;
+                }
+#pragma unroll 4
+                for (int k = 0; k < n; ++k) {
+                    const int kk = k0 + k;
+                    const float fc = scaled ? ex2(sp[2 * (kk * sstep + (kk ? 0 : sfirst))] - mx) : 1.0f;
+                    const float4 t = src[k * step];
+                    v = make_float4(fmaf(fc, t.x, v.x), fmaf(fc, t.y, v.y), fmaf(fc, t.z, v.z), fmaf(fc, t.w, v.w));
+                }
+            }
+            *reinterpret_cast<float4 *>(dst + row * drow + col) = v;
+            if (!keep && col == 0) reinterpret_cast<float2 *>(p.stat)[slot * R + row] = make_float2(mx, sum);
+        }
+      }
+      __syncthreads();
+      if (keep) {
+        const int rows = u.q.n * ge.g, r0 = u.rt * R;
+#pragma unroll 1
+        for (int i = warp; i < R && r0 + i < rows; i += NW) {
+            constexpr int E = D / 32;
+            const int64_t tok = u.q.start + (r0 + i) / ge.g;
+            const int hq = u.h * ge.g + (r0 + i) % ge.g;
+            float mx, sum;
+            row_stat(i, mx, sum);
+            const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = obuf[i * C::OROW + lane * E + e];
+            warp_fwht<E, float>(v);
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+                w[e] = sum > 0.0f ? bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+            if (flag[0]) continue;                       // the sums are not whole
+            uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + lane * E;
+            if constexpr (E == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t *>(dst) = w[0];
+            if (p.a.lse && lane == 0)
+                p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        }
+      }
+      __syncthreads();
+      if (!last && done < n_all && !advance(kv, ge, seqs, u)) break;
     }
     if (bad) atomicOr(p.status, kStatusIndex);
     if (lost && lane == 0) {
@@ -932,22 +1012,27 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     }
 }
 
-constexpr int kMaxCtas = 2;                              // CTAs an SM, over the variants
-constexpr int kMaxPart = 32 * 128;                       // R * D, over the variants
-constexpr int kMaxRows = 32;
+constexpr int kMaxSlots = 8;                             // parts an SM (two a CTA), over the variants
+constexpr int kMaxPart = 2 * 4 * 8 * 256;                // slots an SM times R times D, over the variants
+size_t count_bytes(const DeviceInfo &dev) { return (static_cast<size_t>(dev.sms) * kMaxSlots / 2 * 4 + 255) / 256 * 256; }
 
 template <class C>
 tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
-    static_assert(C::CTAS <= kMaxCtas && C::R * C::D <= kMaxPart && C::R <= kMaxRows, "workspace");
+    static_assert(2 * C::CTAS <= kMaxSlots && 2 * C::CTAS * C::R * C::D <= kMaxPart && C::CTAS * C::R <= 64, "workspace");
     const int grid = dev.sms * C::CTAS;
     unsigned char *ws = static_cast<unsigned char *>(p.a.ws);
-    const size_t most = static_cast<size_t>(dev.sms) * kMaxCtas;
     p.count = reinterpret_cast<unsigned int *>(ws);
-    p.stat = reinterpret_cast<float *>(ws + (most * 4 + 255) / 256 * 256);
-    p.part = p.stat + most * 2 * kMaxRows * 2;
+    p.stat = reinterpret_cast<float *>(ws + count_bytes(dev));
+    p.part = p.stat + static_cast<size_t>(dev.sms) * 2 * 64 * 2;
     p.geo.rows = C::R;
-    p.min_run = 4;
     p.wide = p.a.max_q * p.geo.g > C::R;
+    // Row tiles, if max_q is right: where there are several CTAs for each, each
+    // is cut into parts of its own (at least kMinRun tiles, so a short context
+    // is not cut at all: joining parts costs 4 us, a tile 0.1); else all tiles
+    // into equal runs, of at least one a warp.
+    const int64_t tiles = p.kv.nseq * p.kv.heads * ((p.a.max_q * p.geo.g + C::R - 1) / C::R);
+    p.aligned = p.kv.nseq <= C::NT && tiles * 4 <= grid;
+    p.min_run = p.aligned ? kMinRun : C::NW;
     const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (fe != cudaSuccess) return cuda_fail(fe);
     cudaLaunchConfig_t cfg = {};
@@ -967,8 +1052,7 @@ tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
 }  // namespace
 
 size_t kv4_workspace_bytes(const DeviceInfo &dev) {
-    const size_t most = static_cast<size_t>(dev.sms) * kMaxCtas;
-    return (most * 4 + 255) / 256 * 256 + most * 2 * (kMaxRows * 2 + kMaxPart) * 4;
+    return count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * 64 * 2 + kMaxPart) * 4;
 }
 
 tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceInfo &dev, cudaStream_t s) {
@@ -983,7 +1067,7 @@ tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceI
     const int64_t rows = a.max_q * p.geo.g;
     if (kv.dim == 64) {
         if (rows <= 8) return launch<Cfg<64, 1, 8, 4, 2>>(p, dev, s);
-        if (rows <= 16) return launch<Cfg<64, 2, 8, 4, 2>>(p, dev, s);
+        if (rows <= 16) return launch<Cfg<64, 2, 8, 3, 2>>(p, dev, s);
         return launch<Cfg<64, 4, 8, 4, 1>>(p, dev, s);
     }
     if (kv.dim == 128) {
