@@ -41,6 +41,7 @@ namespace tq {
 namespace {
 
 constexpr int kTile = 32;                    // tokens a tile: two blocks
+constexpr int kOver = 16;                    // tiles that starting and ending a row tile stand for
 constexpr int kMinRun = 48;                  // fewest tiles a part, where row tiles are cut on their own
 constexpr unsigned int kStatusKvTimeout = 128u;
 // A copy of the library built for its own tests lets every stage expect bytes
@@ -72,13 +73,14 @@ struct Cfg {
     static constexpr int oQ = NW * STAGES * TILE;
     static constexpr int oO = oQ + R * QROW;
     static constexpr int oStat = oO + JOIN * OBUF;           // the float arrays named in the kernel
-    static constexpr int oBar = oStat + (2 * R + 4 * NW * R) * 4;
+    static constexpr int oBar = oStat + (2 * R + 2 * NW * R) * 4;
     static constexpr int oMask = oBar + NW * STAGES * 8;
     static constexpr int oSeq = (oMask + NW * STAGES * 4 + 7) / 8 * 8;
     static constexpr int oIter = oSeq + NT * static_cast<int>(sizeof(KvSeq));
     static constexpr int oFound = oIter + NW * 64;
     static constexpr int oPart = oFound + 64;
-    static constexpr int oFlag = oPart + 2 * 64;
+    static constexpr int oNext = oPart + 2 * 64;
+    static constexpr int oFlag = oNext + 64;
     static constexpr int SMEM = oFlag + 16;
     static constexpr int oScan = oO;                         // before any output
     static_assert(NT * 8 + NW * 8 <= JOIN * OBUF && SMEM <= 228 * 1024 / CTAS - 1024, "shared memory");
@@ -93,7 +95,7 @@ struct Run {                                 // one row tile of one key/value he
     int b, h, rt;
     KvSeq q;
     int nrt;                                 // row tiles of the sequence
-    int lo, hi, t0, cost;                    // positions its rows see, first tile, tiles (at least one)
+    int lo, hi, t0, cost;                    // positions its rows see, first tile, tiles (0: they see nothing)
 };
 
 __device__ __forceinline__ void range_of(const Geo &ge, const KvSeq &q, int rt, int &lo, int &hi, int &t0, int &cost) {
@@ -104,7 +106,7 @@ __device__ __forceinline__ void range_of(const Geo &ge, const KvSeq &q, int rt, 
     const int64_t from = static_cast<int64_t>(q.len) - q.n + i0 - ge.window + 1;
     lo = ge.window > 0 && from > 0 ? static_cast<int>(from < hi ? from : hi) : 0;
     t0 = lo / kTile;
-    cost = max(1, (hi + kTile - 1) / kTile - t0);
+    cost = (hi + kTile - 1) / kTile - t0;
 }
 
 // Positions that row i of a sequence sees.
@@ -119,7 +121,11 @@ __device__ __forceinline__ int row_tiles(const Geo &ge, const KvSeq &q) {
     return (q.n * ge.g + ge.rows - 1) / ge.rows;
 }
 
-// Tiles of all row tiles of a sequence (one head), by one thread.
+// A row tile's weight in the cutting: its tiles, and as many as starting and
+// ending a row tile takes as long as.
+__device__ __forceinline__ int weight(int tiles) { return tiles ? tiles + kOver : 0; }
+
+// Weight of all row tiles of a sequence (one head), by one thread.
 __device__ __forceinline__ int64_t seq_cost(const Geo &ge, const KvSeq &q) {
     const int nrt = row_tiles(ge, q);
     int64_t sum = 0;
@@ -127,7 +133,7 @@ __device__ __forceinline__ int64_t seq_cost(const Geo &ge, const KvSeq &q) {
     for (int rt = 0; rt < nrt; ++rt) {
         int lo, hi, t0, c;
         range_of(ge, q, rt, lo, hi, t0, c);
-        sum += c;
+        sum += weight(c);
     }
     return sum;
 }
@@ -139,7 +145,7 @@ __device__ __forceinline__ int64_t seq_cost_warp(const Geo &ge, const KvSeq &q) 
     for (int rt = lane; rt < nrt; rt += 32) {
         int lo, hi, t0, c;
         range_of(ge, q, rt, lo, hi, t0, c);
-        sum += c;
+        sum += weight(c);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -149,20 +155,45 @@ __device__ __forceinline__ int64_t seq_cost_warp(const Geo &ge, const KvSeq &q) 
 // The next row tile in order.  `seqs`: the sequences' descriptions in shared
 // memory, where one step of the scan held them all (else nullptr).
 __device__ __forceinline__ bool advance(const tq_kv4 &kv, const Geo &ge, const KvSeq *seqs, Run &u) {
-    if (++u.rt >= u.nrt) {
-        u.rt = 0;
-        if (++u.h >= kv.heads) {
-            u.h = 0;
-            bool bad = false;
-            do {
-                if (++u.b >= kv.nseq) return false;
-                u.q = seqs ? seqs[u.b] : kv_seq(kv, u.b, bad);
-            } while (u.q.n == 0);
-            u.nrt = row_tiles(ge, u.q);
+    do {                                     // row tiles that see nothing are left out
+        if (++u.rt >= u.nrt) {
+            u.rt = 0;
+            if (++u.h >= kv.heads) {
+                u.h = 0;
+                bool bad = false;
+                do {
+                    if (++u.b >= kv.nseq) return false;
+                    u.q = seqs ? seqs[u.b] : kv_seq(kv, u.b, bad);
+                } while (u.q.n == 0 || u.q.len == 0);
+                u.nrt = row_tiles(ge, u.q);
+            }
+        }
+        range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
+    } while (u.cost == 0);
+    return true;
+}
+
+// Zeros for the row tiles that see nothing (rows before position 0), a
+// sequence a CTA.
+template <int D>
+__device__ __noinline__ void zero_rows(const tq_kv4 &kv, const Kv4Attn &a, const Geo &ge) {
+    for (int64_t b = blockIdx.x; b < kv.nseq; b += gridDim.x) {
+        bool bad = false;
+        const KvSeq q = kv_seq(kv, b, bad);
+        const int none = q.n - q.len;        // rows before position 0
+        if (none <= 0) continue;
+        const int rows = q.n * ge.g, cut = q.len == 0 ? rows : none * ge.g / ge.rows * ge.rows;
+        const int64_t pieces = static_cast<int64_t>(cut) * kv.heads * (D / 8);
+        for (int64_t i = threadIdx.x; i < pieces; i += blockDim.x) {
+            const int c = static_cast<int>(i % (D / 8));
+            const int64_t k = i / (D / 8);
+            const int row = static_cast<int>(k % cut), h = static_cast<int>(k / cut);
+            const int64_t tok = q.start + row / ge.g;
+            const int hq = h * ge.g + row % ge.g;
+            *reinterpret_cast<uint4 *>(a.O + tok * a.ldo + static_cast<int64_t>(hq) * D + c * 8) = make_uint4(0, 0, 0, 0);
+            if (a.lse && c == 0) a.lse[tok * a.heads_q + hq] = -INFINITY;
         }
     }
-    range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
-    return true;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -271,7 +302,6 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     float *rowf = reinterpret_cast<float *>(sm + C::oStat);
     float *rowc = rowf + R;
     float2 *wstat = reinterpret_cast<float2 *>(rowc + R);    // [NW][R] each warp's maximum and sum
-    float2 *red = wstat + NW * R;        // [NW][R] a row's maximum and sum over the sources, by warps
     const uint32_t bar0 = smb + C::oBar + warp * S * 8;      // this warp's stages
     volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(sm + C::oMask) + warp * S;
     unsigned char *ring = sm + warp * S * C::TILE;
@@ -343,14 +373,16 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         total += step_sum;
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusIndex);
+    auto leave_idle = [&]() { zero_rows<D>(kv, p.a, ge); };
     int64_t per = quotient(total + gridDim.x - 1, gridDim.x);
     per = per < p.min_run ? p.min_run : per;
     const int cta = static_cast<int>(blockIdx.x);
     Run u;
-    int64_t c0 = 0, n_all, at;            // the run's first tile over the batch, its tiles; its first tile in its row tile
+    int64_t uw = 0, n_all = 0;            // weight before the run's first row tile over the batch; the run's tiles
+    int first = 0;                        // the run's first tile in its row tile
     bool aligned = false;                 // each row tile is cut on its own, into parts of about `per` tiles
     int acf = 0, acl = 0;                 // the CTAs that hold its parts then
-    auto parts_of = [&](int64_t cost) { return cost < per ? 1 : static_cast<int>(quotient(cost, per)); };
+    auto parts_of = [&](int64_t cost) { return cost < per ? cost > 0 : static_cast<int>(quotient(cost, per)); };
     if (p.aligned) {
         int np = 0;                       // parts of a head of this thread's sequence
         const int nrt = row_tiles(ge, mine);
@@ -364,7 +396,10 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         block_scan(static_cast<int64_t>(np) * kv.heads, np_at, np_sum);
         aligned = np_sum <= gridDim.x;
         if (aligned) {
-            if (cta >= np_sum) return;
+            if (cta >= np_sum) {
+                leave_idle();
+                return;
+            }
             const int64_t k = cta - np_at;
             if (k >= 0 && k < static_cast<int64_t>(np) * kv.heads) {
                 found->b = tid;
@@ -386,15 +421,16 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             }
             acf = cta - k2;
             acl = acf + n2 - 1;
-            at = static_cast<int64_t>(u.cost) * k2 / n2;
-            n_all = static_cast<int64_t>(u.cost) * (k2 + 1) / n2 - at;
+            first = static_cast<int>(static_cast<int64_t>(u.cost) * k2 / n2);
+            n_all = static_cast<int64_t>(u.cost) * (k2 + 1) / n2 - first;
         }
     }
     if (!aligned) {
-        c0 = cta * per;
-        const int64_t c1 = c0 + per < total ? c0 + per : total;
-        if (c0 >= c1) return;
-        n_all = c1 - c0;
+        const int64_t c0 = cta * per, c1 = c0 + per < total ? c0 + per : total;
+        if (c0 >= c1) {
+            leave_idle();
+            return;
+        }
         int64_t passed = 0;
         for (int64_t base = 0; base < kv.nseq; base += C::NT) {
             if (kv.nseq > C::NT) {        // one step: its scan is still at hand
@@ -418,12 +454,13 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         u.q = found->q;
         u.nrt = row_tiles(ge, u.q);
         u.h = static_cast<int>(quotient(found->at, found->head));
-        at = found->at - u.h * found->head;
+        int64_t at = found->at - u.h * found->head;
         u.rt = 0;
         if (u.nrt > 1) {                  // the row tile: by 32 at a time
             for (int base = 0; base < u.nrt; base += 32) {
                 int lo, hi, t0, c = 0;
                 if (base + lane < u.nrt) range_of(ge, u.q, base + lane, lo, hi, t0, c);
+                c = weight(c);
                 int64_t x = c;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -441,8 +478,23 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             }
         }
         range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
+        // the weight of starting comes first: a run that ends within it leaves
+        // the row tile to the next
+        first = at > kOver ? static_cast<int>(at) - kOver : 0;
+        uw = c0 - at;
+        Run v = u;
+        int64_t w = uw;
+        for (int f = first;; f = 0) {
+            const int64_t end = c1 - w - kOver;
+            n_all += end > f ? (end < v.cost ? end : v.cost) - f : 0;
+            w += kOver + v.cost;
+            if (w >= c1 || !advance(kv, ge, seqs, v)) break;
+        }
+        if (n_all == 0) {
+            leave_idle();
+            return;
+        }
     }
-    const int first = static_cast<int>(at);          // tile of the first row tile that the run starts at
     // ---------------------------------------------------- this warp's copies
     // Its tiles are warp, warp + NW, .. of the run.  Lane i holds where tile i of
     // 32 at a time lies (two pieces where a page is half a tile; 0: nowhere),
@@ -520,6 +572,24 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     // be fetched from far away.
     int nparts = 0, joined = -1;          // parts left elsewhere; parts looked at for the last join
     int cf = 0, cl = 0;
+    // The raw queries of the next row tile come while the tiles of this one are
+    // read: a row a warp, and further ones by turns.
+    constexpr int E = D / 32, RW = (R + NW - 1) / NW;
+    uint32_t raw[RW][E / 2];
+    auto load_queries = [&](const Run &v) {
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            const int row = v.rt * R + warp + k * NW;
+            const bool is = warp + k * NW < R && row < v.q.n * ge.g;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                p.a.Q + static_cast<int64_t>(v.q.start + (is ? row / ge.g : 0)) * p.a.ldq +
+                static_cast<int64_t>(v.h * ge.g + (is ? row % ge.g : 0)) * D + lane * E);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) raw[k][e] = is ? src[e] : 0u;
+        }
+    };
+    load_queries(u);
+    Run *next_sh = reinterpret_cast<Run *>(sm + C::oNext);
     for (;;) {
       const bool last = done >= n_all;    // joining parts, not warps
       bool whole = true;
@@ -551,18 +621,15 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 
         // the row tile's queries: rotated, as fp16 in the order of the words'
         // nibbles (0, 4), (1, 5), (2, 6), (3, 7), the odd ones over 16
-        for (int i = warp; i < R; i += NW) {
-            constexpr int E = D / 32;
+#pragma unroll
+        for (int k0 = 0; k0 < RW; ++k0) {
+            const int i = warp + k0 * NW;
+            if (R % NW && i >= R) break;
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-            if (r0 + i < rows) {
-                const int tok = (r0 + i) / ge.g, hq = u.h * ge.g + (r0 + i) % ge.g;
-                load_bf16<E, float>(p.a.Q + static_cast<int64_t>(u.q.start + tok) * p.a.ldq +
-                                        static_cast<int64_t>(hq) * D + lane * E,
-                                    v);
-                warp_fwht<E, float>(v);
-            }
+            for (int e = 0; e < E; ++e)
+                v[e] = __uint_as_float(e & 1 ? raw[k0][e / 2] & 0xFFFF0000u : raw[k0][e / 2] << 16);
+            warp_fwht<E, float>(v);
             const float cn = sqrtf(1.0f / D);
             float mx = 0.0f;
 #pragma unroll
@@ -591,6 +658,12 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 rowf[i] = p.a.scale * kLog2e * (16777216.0f * pow2i(-k));
                 rowc[i] = -8.0f / 16777216.0f * sum;
             }
+        }
+        if (done + n < n_all) {
+            Run v = u;
+            advance(kv, ge, seqs, v);
+            load_queries(v);
+            if (tid == 0) *next_sh = v;
         }
         __syncthreads();
 
@@ -872,9 +945,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 
         whole = from == 0 && n == u.cost;
         if (!whole) {
-            const int64_t start = c0 + done - from;      // the row tile's first tile, over the batch
-            cf = aligned ? acf : static_cast<int>(quotient(start, per));
-            cl = aligned ? acl : static_cast<int>(quotient(start + u.cost - 1, per));
+            cf = aligned ? acf : static_cast<int>(quotient(uw + kOver, per));
+            cl = aligned ? acl : static_cast<int>(quotient(uw + kOver + u.cost - 1, per));
             if (tid == 0) parts[nparts] = {u, cf, cl};
             ++nparts;
         }
@@ -883,123 +955,111 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         from = 0;
       }
 
-      constexpr int CH = R * D / 4, PER = C::NT / R;     // 16-byte pieces of the row tile; threads a row
+      // A warp joins a row over its sources: the warps' buffers, or the parts (a
+      // piece of a part is a trip to far memory: each lane brings as many as the
+      // rings hold, empty by now, into places of its own there).
+      constexpr int DEPTH = NW * S * C::TILE / (C::NT * 4 * E);
+      static_assert(DEPTH >= NW, "one step joins the warps");
       const bool keep = last || whole;
-      const int np = last ? cl - cf + 1 : NW;            // sources
+      const bool scaled = last || OWN;                   // else the buffers share the largest maximum
+      const int np = last ? cl - cf + 1 : NW, no = scaled ? np : C::JOIN;
       const float2 *st = last ? reinterpret_cast<const float2 *>(p.stat) + static_cast<int64_t>(2) * cf * R : wstat;
       const int sstep = last ? 2 * R : R, sfirst = last ? R : 0;
-      // A part's piece is a trip to far memory: each thread brings as many as the
-      // rings hold (they are empty by now) into places of its own there, the
-      // first of them while the statistics come.
-      constexpr int DEPTH = NW * S * C::TILE / (C::NT * 16);
-      static_assert(DEPTH >= C::JOIN, "one step joins the warps");
-      auto bring = [&](int i, int k0, int n) {
-        const float *src = p.part + static_cast<int64_t>(2) * cf * (R * D) + i * 4;
-#pragma unroll 1
-        for (int k = 0; k < n; ++k) {
-            const int kk = k0 + k;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smb + (k * C::NT + tid) * 16),
-                         "l"(src + (kk ? 2 * kk : 1) * (R * D))
-                         : "memory");
-        }
-      };
-      if (last && tid < CH) bring(tid, 0, min(np, DEPTH));
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (static_cast<int>(blockIdx.x) == cf ? 1 : 0);
-      {
-        // each row's maximum over the sources, and the sum relative to it
-        const int row = tid % R;
-        float mx = kNone, sum = 0.0f;
-#pragma unroll 2
-        for (int k = tid / R; k < np; k += PER) {
-            const float2 t = st[k * sstep + (k ? 0 : sfirst) + row];
-            const float to = fmaxf(mx, t.x);
-            sum = fmaf(sum, ex2(mx - to), t.y * ex2(t.x - to));
-            mx = to;
-        }
-#pragma unroll
-        for (int x = R; x < 32; x <<= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, mx, x), s2 = __shfl_xor_sync(0xffffffffu, sum, x);
-            const float to = fmaxf(mx, m2);
-            sum = fmaf(sum, ex2(mx - to), s2 * ex2(m2 - to));
-            mx = to;
-        }
-        if (lane < R) red[warp * R + row] = make_float2(mx, sum);
-      }
-      __syncthreads();
-      auto row_stat = [&](int row, float &mx, float &sum) {
-        mx = kNone;
-        sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) mx = fmaxf(mx, red[w * R + row].x);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) sum = fmaf(red[w * R + row].y, ex2(red[w * R + row].x - mx), sum);
-      };
-      {
-        const int no = last ? np : C::JOIN;
-        const bool scaled = last || OWN;                 // else the buffers share the largest maximum
-        float *dst = keep ? obuf : p.part + slot * (R * D);
-        const int drow = keep ? C::OROW : D;
+      const int rows = u.q.n * ge.g, r0 = u.rt * R;
 #pragma unroll 1
-        for (int i = tid; i < CH; i += C::NT) {
-            const int row = i / (D / 4), col = i % (D / 4) * 4;
-            float mx, sum;
-            row_stat(row, mx, sum);
-            const float *sp = reinterpret_cast<const float *>(st + row);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = warp; i < R && r0 + i < rows; i += NW) {
+        auto bring = [&](int k0, int n) {
+            const float *src = p.part + static_cast<int64_t>(2) * cf * (R * D) + i * D + lane * E;
 #pragma unroll 1
-            for (int k0 = 0; k0 < no; k0 += DEPTH) {
-                const int n = min(no - k0, DEPTH);
-                const float4 *src = reinterpret_cast<const float4 *>(obuf + row * C::OROW + col);
-                int step = C::OBUF / 16;
-                if (last) {
-                    if (k0 || i != tid) bring(i, k0, n);
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    src = reinterpret_cast<const float4 *>(sm) + tid;
-                    step = C::NT;
-                }
-#pragma unroll 4
-                for (int k = 0; k < n; ++k) {
-                    const int kk = k0 + k;
-                    const float fc = scaled ? ex2(sp[2 * (kk * sstep + (kk ? 0 : sfirst))] - mx) : 1.0f;
-                    const float4 t = src[k * step];
-                    v = make_float4(fmaf(fc, t.x, v.x), fmaf(fc, t.y, v.y), fmaf(fc, t.z, v.z), fmaf(fc, t.w, v.w));
+            for (int k = 0; k < n; ++k) {
+                const int kk = k0 + k;
+                const float *from_ = src + static_cast<int64_t>(kk ? 2 * kk : 1) * (R * D);
+                const uint32_t to = smb + (k * C::NT + tid) * (4 * E);
+                if constexpr (E == 2) {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from_) : "memory");
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; e += 4)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 4 * e), "l"(from_ + e)
+                                     : "memory");
                 }
             }
-            *reinterpret_cast<float4 *>(dst + row * drow + col) = v;
-            if (!keep && col == 0) reinterpret_cast<float2 *>(p.stat)[slot * R + row] = make_float2(mx, sum);
-        }
-      }
-      __syncthreads();
-      if (keep) {
-        const int rows = u.q.n * ge.g, r0 = u.rt * R;
+        };
+        if (last) bring(0, min(no, DEPTH));
+        float mx = kNone;
 #pragma unroll 1
-        for (int i = warp; i < R && r0 + i < rows; i += NW) {
-            constexpr int E = D / 32;
-            const int64_t tok = u.q.start + (r0 + i) / ge.g;
-            const int hq = u.h * ge.g + (r0 + i) % ge.g;
-            float mx, sum;
-            row_stat(i, mx, sum);
-            const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
-            float v[8];
+        for (int k = lane; k < np; k += 32) mx = fmaxf(mx, st[k * sstep + (k ? 0 : sfirst) + i].x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = obuf[i * C::OROW + lane * E + e];
-            warp_fwht<E, float>(v);
-            uint32_t w[4];
+        for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        float sum = 0.0f, v[8];
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-                w[e] = sum > 0.0f ? bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
-            if (flag[0]) continue;                       // the sums are not whole
-            uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + lane * E;
-            if constexpr (E == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t *>(dst) = w[0];
-            if (p.a.lse && lane == 0)
-                p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll 1
+        for (int k0 = 0, in = 0; k0 < np; k0 += 32) {    // `in`: sources brought before this step's
+            float fac = 0.0f;
+            if (k0 + lane < np) {
+                const float2 t2 = st[(k0 + lane) * sstep + (k0 + lane ? 0 : sfirst) + i];
+                fac = ex2(t2.x - mx);
+                sum = fmaf(fac, t2.y, sum);
+            }
+            if (!scaled) fac = 1.0f;
+            const int n = min(32, no - k0);
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const float *src;
+                if (last) {
+                    const int at_ = (k0 + k) - in;
+                    if (at_ == DEPTH) {
+                        in += DEPTH;
+                        bring(in, min(no - in, DEPTH));
+                    }
+                    if (at_ == 0 || at_ == DEPTH) asm volatile("cp.async.wait_all;" ::: "memory");
+                    src = reinterpret_cast<const float *>(sm + ((k0 + k - in) * C::NT + tid) * (4 * E));
+                } else {
+                    src = obuf + k * (C::OBUF / 4) + i * C::OROW + lane * E;
+                }
+                const float f = __shfl_sync(0xffffffffu, fac, k);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = fmaf(f, src[e], v[e]);
+            }
         }
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        if (!keep) {                                     // to the workspace
+            float *dst = p.part + (slot * R + i) * D + lane * E;
+            if constexpr (E == 2) {
+                *reinterpret_cast<float2 *>(dst) = make_float2(v[0], v[1]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; e += 4)
+                    *reinterpret_cast<float4 *>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            }
+            if (lane == 0) reinterpret_cast<float2 *>(p.stat)[slot * R + i] = make_float2(mx, sum);
+            continue;
+        }
+        const int64_t tok = u.q.start + (r0 + i) / ge.g;
+        const int hq = u.h * ge.g + (r0 + i) % ge.g;
+        const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
+        warp_fwht<E, float>(v);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) w[e] = sum > 0.0f ? bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+        if (flag[0]) continue;                           // the sums are not whole
+        uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + lane * E;
+        if constexpr (E == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(dst) = w[0];
+        if (p.a.lse && lane == 0)
+            p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
       __syncthreads();
-      if (!last && done < n_all && !advance(kv, ge, seqs, u)) break;
+      if (!last && done < n_all) {
+        uw += u.cost + kOver;
+        u = *next_sh;
+      }
     }
+    zero_rows<D>(kv, p.a, ge);
     if (bad) atomicOr(p.status, kStatusIndex);
     if (lost && lane == 0) {
         // after a wait that ran out nobody has seen the copies land: wait for
@@ -1032,7 +1092,7 @@ tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
     // into equal runs, of at least one a warp.
     const int64_t tiles = p.kv.nseq * p.kv.heads * ((p.a.max_q * p.geo.g + C::R - 1) / C::R);
     p.aligned = p.kv.nseq <= C::NT && tiles * 4 <= grid;
-    p.min_run = p.aligned ? kMinRun : C::NW;
+    p.min_run = p.aligned ? kMinRun : kOver;
     const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (fe != cudaSuccess) return cuda_fail(fe);
     cudaLaunchConfig_t cfg = {};
