@@ -74,13 +74,12 @@ struct Cfg {
     static constexpr int oO = oQ + R * QROW;
     static constexpr int oStat = oO + JOIN * OBUF;           // the float arrays named in the kernel
     static constexpr int oBar = oStat + (2 * R + 2 * NW * R) * 4;
-    static constexpr int oMask = oBar + NW * STAGES * 8;
-    static constexpr int oSeq = (oMask + NW * STAGES * 4 + 7) / 8 * 8;
+    static constexpr int oSeq = oBar + NW * STAGES * 8;
     static constexpr int oIter = oSeq + NT * static_cast<int>(sizeof(KvSeq));
     static constexpr int oFound = oIter + NW * 64;
     static constexpr int oPart = oFound + 64;
     static constexpr int oNext = oPart + 2 * 64;
-    static constexpr int oFlag = oNext + 64;
+    static constexpr int oFlag = oNext + 2 * 64;
     static constexpr int SMEM = oFlag + 16;
     static constexpr int oScan = oO;                         // before any output
     static_assert(NT * 8 + NW * 8 <= JOIN * OBUF && SMEM <= 228 * 1024 / CTAS - 1024, "shared memory");
@@ -214,6 +213,17 @@ __device__ __forceinline__ uint32_t bf16_bits2(float lo, float hi) {          //
     return w;
 }
 
+// A word's nibbles 0 .. 7 as fp16 pairs, in units of 2^-24 (a 16-bit pattern
+// below 2^10 is that many times 2^-24): the pairs (0, 4) and (2, 6), and each
+// with 16 times its neighbours (1, 5) and (3, 7) added.  Four instructions:
+// taking the neighbours out would be a fifth, and is left to whoever uses them.
+__device__ __forceinline__ void nibbles(uint32_t x, uint32_t &n04, uint32_t &n04_15, uint32_t &n26, uint32_t &n26_37) {
+    n04_15 = x & 0x00FF00FFu;
+    asm("prmt.b32 %0, %1, 0, 0x4341;" : "=r"(n26_37) : "r"(x));
+    n04 = x & 0x000F000Fu;
+    n26 = n26_37 & 0x000F000Fu;
+}
+
 // Transpose of an 8 x 8 matrix of 16-bit values held as mma fragments are.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -277,7 +287,7 @@ struct Part {                                // a part of a row tile whose other
     Run u;
     int cf, cl;                              // CTAs that hold its parts
 };
-static_assert(sizeof(Run) <= 64 && sizeof(Part) <= 64 && sizeof(Found) <= 64, "shared memory");
+static_assert(2 * sizeof(Run) <= 128 && sizeof(Part) <= 64 && sizeof(Found) <= 64, "shared memory");
 
 struct AttnParams {
     tq_kv4 kv;
@@ -303,8 +313,6 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     float *rowc = rowf + R;
     float2 *wstat = reinterpret_cast<float2 *>(rowc + R);    // [NW][R] each warp's maximum and sum
     const uint32_t bar0 = smb + C::oBar + warp * S * 8;      // this warp's stages
-    volatile uint32_t *mask_sh = reinterpret_cast<volatile uint32_t *>(sm + C::oMask) + warp * S;
-    unsigned char *ring = sm + warp * S * C::TILE;
     const uint32_t ring_at = smb + warp * S * C::TILE;
     int64_t *scan = reinterpret_cast<int64_t *>(sm + C::oScan);
     int64_t *wsum = scan + C::NT;
@@ -378,7 +386,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     per = per < p.min_run ? p.min_run : per;
     const int cta = static_cast<int>(blockIdx.x);
     Run u;
-    int64_t uw = 0, n_all = 0;            // weight before the run's first row tile over the batch; the run's tiles
+    int64_t uw = 0;                       // weight before the run's first row tile over the batch
+    int n_all = 0;                        // the run's tiles
     int first = 0;                        // the run's first tile in its row tile
     bool aligned = false;                 // each row tile is cut on its own, into parts of about `per` tiles
     int acf = 0, acl = 0;                 // the CTAs that hold its parts then
@@ -422,7 +431,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             acf = cta - k2;
             acl = acf + n2 - 1;
             first = static_cast<int>(static_cast<int64_t>(u.cost) * k2 / n2);
-            n_all = static_cast<int64_t>(u.cost) * (k2 + 1) / n2 - first;
+            n_all = static_cast<int>(static_cast<int64_t>(u.cost) * (k2 + 1) / n2) - first;
         }
     }
     if (!aligned) {
@@ -486,7 +495,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         int64_t w = uw;
         for (int f = first;; f = 0) {
             const int64_t end = c1 - w - kOver;
-            n_all += end > f ? (end < v.cost ? end : v.cost) - f : 0;
+            n_all += end > f ? (end < v.cost ? static_cast<int>(end) : v.cost) - f : 0;
             w += kOver + v.cost;
             if (w >= c1 || !advance(kv, ge, seqs, v)) break;
         }
@@ -497,33 +506,31 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     }
     // ---------------------------------------------------- this warp's copies
     // Its tiles are warp, warp + NW, .. of the run.  Lane i holds where tile i of
-    // 32 at a time lies (two pieces where a page is half a tile; 0: nowhere),
-    // and the stages are filled in turn.
-    uint64_t src0 = 0, src1 = 0;
+    // 32 at a time lies (the number of its block in the pool plus one, two of them
+    // where a page is half a tile; 0: nowhere), and the stages are filled in turn.
+    uint32_t src0 = 0, src1 = 0;
     const bool halves = kv.page_size < kTile;
     {
         Run *it = reinterpret_cast<Run *>(sm + C::oIter + warp * 64);
         if (lane == 0) *it = u;
         __syncwarp();
     }
-    int64_t it_start = -first;                       // the iterator's row tile begins at this tile of the run
-    auto find_tiles = [&](int64_t k0) {              // tiles k0, k0 + NW, .. of the run
+    int n_send = n_all, it_start = -first;           // the iterator's row tile begins at this tile of the run
+    auto find_tiles = [&](int k0) {                  // tiles k0, k0 + NW, .. of the run
         Run *it = reinterpret_cast<Run *>(sm + C::oIter + warp * 64);
         Run v = *it;
-        const int64_t k = k0 + static_cast<int64_t>(lane) * NW, end = min(k0 + 32 * NW, n_all);
+        const int k = k0 + lane * NW, end = min(k0 + 32 * NW, n_all);
         src0 = src1 = 0;
         for (;;) {
             if (k >= it_start && k < it_start + v.cost && k < n_all) {
-                const int pos = (v.t0 + static_cast<int>(k - it_start)) * kTile;
+                const int pos = (v.t0 + k - it_start) * kTile;
                 if (pos < v.hi) {
-                    const int pg = kv_page(kv, v.b, pos);
-                    if (pg >= 0) src0 = reinterpret_cast<uint64_t>(kv_block(kv, pg, v.h, pos & (kv.page_size - 1)));
-                    else bad = true;
+                    src0 = kv_block_number(kv, v.b, v.h, pos) + 1;
                     if (halves && pos + kKvBlock < v.hi) {
-                        const int pg1 = kv_page(kv, v.b, pos + kKvBlock);
-                        if (pg1 >= 0) src1 = reinterpret_cast<uint64_t>(kv_block(kv, pg1, v.h, 0));
-                        else bad = true;
+                        src1 = kv_block_number(kv, v.b, v.h, pos + kKvBlock) + 1;
+                        bad |= src1 == 0;
                     }
+                    bad |= src0 == 0;
                 }
             }
             if (it_start + v.cost >= end) break;
@@ -535,34 +542,37 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         __syncwarp();
     };
     int sent = 0;                                    // tiles copied so far
-    auto send = [&](int64_t k, int stage) {          // tile k of the run, into a free stage
-        if (k >= n_all) return;
-        if ((sent & 31) == 0) find_tiles(k);
-        const uint64_t a0 = __shfl_sync(0xffffffffu, src0, sent & 31);
-        const uint64_t a1 = halves ? __shfl_sync(0xffffffffu, src1, sent & 31) : 0;
-        ++sent;
-        if (elect_one()) {
-            const uint32_t dst = ring_at + stage * C::TILE, bar = bar0 + 8 * stage;
-            const uint32_t n0 = halves ? C::BLK : C::TILE;
-            mask_sh[stage] = (a0 ? (halves ? 1u : 3u) : 0u) | (a1 ? 2u : 0u);
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                         "r"(kUnset + (a0 ? n0 : 0u) + (a1 ? C::BLK : 0u))
-                         : "memory");
-            if (a0) bulk_copy(dst, a0, n0, bar);
-            if (a1) bulk_copy(dst + C::BLK, a1, C::BLK, bar);
+    uint32_t there = 0;                              // per stage, next one lowest: which of its blocks are there
+    auto send = [&](int k, uint32_t at, uint32_t bar) {      // tile k of the run, into the stage at `at`
+        uint32_t a0 = 0, a1 = 0;
+        if (k < n_send) {
+            if ((sent & 31) == 0) find_tiles(k);
+            a0 = __shfl_sync(0xffffffffu, src0, sent & 31);
+            if (halves) a1 = __shfl_sync(0xffffffffu, src1, sent & 31);
+            ++sent;
+            if (elect_one()) {
+                const uint32_t n0 = halves ? C::BLK : C::TILE;
+                const uint64_t pool = reinterpret_cast<uint64_t>(kv.pool) - C::BLK;
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                             "r"(kUnset + (a0 ? n0 : 0u) + (a1 ? C::BLK : 0u))
+                             : "memory");
+                if (a0) bulk_copy(at, pool + static_cast<uint64_t>(a0) * C::BLK, n0, bar);
+                if (a1) bulk_copy(at + C::BLK, pool + static_cast<uint64_t>(a1) * C::BLK, C::BLK, bar);
+            }
+            __syncwarp();
         }
-        __syncwarp();
+        there = (there >> 2) | (((a0 ? (halves ? 1u : 3u) : 0u) | (a1 ? 2u : 0u)) << (2 * (S - 1)));
     };
 #pragma unroll 1
-    for (int i = 0; i < S; ++i) send(warp + static_cast<int64_t>(i) * NW, i);
+    for (int i = 0; i < S; ++i) send(warp + i * NW, ring_at + i * C::TILE, bar0 + 8 * i);
 
     // ---------------------------------------------------- parts of the run
     const int r = lane >> 2, j = lane & 3;
-    int64_t done = 0;                     // tiles of the run before this part
+    int done = 0;                         // tiles of the run before this part
     int from = first;
     bool lost = false;
-    int stage = 0, next = warp;           // this warp's next stage, and its next tile of the part
-    uint32_t phase = 0;
+    uint32_t at = ring_at, bar = bar0, phase = 0;    // this warp's next stage
+    int next = warp;                      // and its next tile of the part
     // Row tiles in turn.  Parts whose others are elsewhere go to the workspace;
     // at the end of the run their arrivals are counted (once, for all of them),
     // and the CTA that comes last joins them.  A row tile's parts belong to CTAs
@@ -589,7 +599,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         }
     };
     load_queries(u);
-    Run *next_sh = reinterpret_cast<Run *>(sm + C::oNext);
+    Run *next_sh = reinterpret_cast<Run *>(sm + C::oNext), *cur_sh = next_sh + 1;
     for (;;) {
       const bool last = done >= n_all;    // joining parts, not warps
       bool whole = true;
@@ -616,11 +626,11 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         cl = parts[joined].cl;
         ++joined;
       } else {
-        const int n = static_cast<int>(min(static_cast<int64_t>(u.cost - from), n_all - done));
+        const int n = min(u.cost - from, n_all - done);
         const int rows = u.q.n * ge.g, r0 = u.rt * R;
 
         // the row tile's queries: rotated, as fp16 in the order of the words'
-        // nibbles (0, 4), (1, 5), (2, 6), (3, 7), the odd ones over 16
+        // nibbles (0, 4), (1, 5), (2, 6), (3, 7)
 #pragma unroll
         for (int k0 = 0; k0 < RW; ++k0) {
             const int i = warp + k0 * NW;
@@ -642,15 +652,19 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             // the row's largest value in [2^13, 2^14)
             const int k = mx > 0.0f ? min(13 - (static_cast<int>(__float_as_uint(mx) >> 23) - 127), 126) : 0;
             const float up = pow2i(k);
+            // an odd value's operand meets its nibble with 16 times it: over 16;
+            // an even one's meets it alone once more, so that much is taken off
             float sum = 0.0f;
             unsigned char *qrow = sm + C::oQ + i * C::QROW;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
+            for (int e = 0; e < E; e += 2) {
                 const int d = lane * E + e, jj = d / (D / 4), w = (d % (D / 4)) / 8, nb = d % 8;
-                const float x = (nb & 1) ? v[e] * up * 0.0625f : v[e] * up;
-                const __half hx = __float2half_rn(x);
-                sum += (nb & 1) ? 16.0f * __half2float(hx) : __half2float(hx);
-                *reinterpret_cast<__half *>(qrow + ((w * 4 + jj) * 8 + (nb & 3) * 2 + (nb >> 2)) * 2) = hx;
+                const __half odd = __float2half_rn(v[e + 1] * up * 0.0625f);
+                const __half even = __float2half_rn(v[e] * up - __half2float(odd));
+                sum += __half2float(even) + 17.0f * __half2float(odd);
+                __half *dst = reinterpret_cast<__half *>(qrow + ((w * 4 + jj) * 8 + (nb & 3) * 2 + (nb >> 2)) * 2);
+                dst[0] = even;
+                dst[2] = odd;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -665,6 +679,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             load_queries(v);
             if (tid == 0) *next_sh = v;
         }
+        if (tid == 0) *cur_sh = u;
         __syncthreads();
 
         // per lane: query rows 8 nt + 2 j and 8 nt + 2 j + 1
@@ -713,18 +728,21 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         float gv = pow2i(127);                // power of two that value scales are multiplied by
 
         // this warp's tiles of the part
+        const int tile0 = u.t0 + from;
+#pragma unroll 1
         for (; next < n; next += NW) {
-            const int i = next;
-            if (!lost && !mbar_try(bar0 + 8 * stage, phase) &&
-                !mbar_wait_bounded(bar0 + 8 * stage, phase, flag[0] ? 0 : kA16WaitLimit)) {
-                lost = true;
-                flag[0] = 1;
-                if (lane == 0) atomicOr(p.status, kStatusKvTimeout);
+            if (!mbar_try(bar, phase)) {
+                if (lost || !mbar_wait_bounded(bar, phase, flag[0] ? 0 : kA16WaitLimit)) {
+                    lost = true;
+                    n_send = 0;           // nothing more is sent into stages that did not fill
+                    flag[0] = 1;
+                    if (lane == 0) atomicOr(p.status, kStatusKvTimeout);
+                    continue;
+                }
             }
-            if (lost) continue;
-            const int tile_at = (u.t0 + from + i) * kTile;
-            const unsigned char *base = ring + stage * C::TILE;
-            const uint32_t have = mask_sh[stage];
+            const int tile_at = (tile0 + next) * kTile;
+            const unsigned char *base = sm + (at - smb);
+            const uint32_t have = there & 3u;
 
             // scores: S^T, tokens r and r + 8 of each block, times the key's scale
             float s[2][NR][4], sv[2][2];
@@ -745,11 +763,9 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    const uint32_t x8 = x[w] >> 8, y8 = y[w] >> 8;
-                    const uint32_t a0 = x[w] & 0x000F000Fu, a1 = y[w] & 0x000F000Fu;
-                    const uint32_t a2 = x[w] & 0x00F000F0u, a3 = y[w] & 0x00F000F0u;
-                    const uint32_t b0 = x8 & 0x000F000Fu, b1 = y8 & 0x000F000Fu;
-                    const uint32_t b2 = x8 & 0x00F000F0u, b3 = y8 & 0x00F000F0u;
+                    uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+                    nibbles(x[w], a0, a2, b0, b2);
+                    nibbles(y[w], a1, a3, b1, b3);
 #pragma unroll
                     for (int nt = 0; nt < NR; ++nt) {
                         uint32_t q4[4];
@@ -775,8 +791,9 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        const int row = cur_sh->rt * R + nt * 8 + 2 * j + e;
                         int lo = 0, hi = 0;
-                        if (r0 + nt * 8 + 2 * j + e < rows) row_range(ge, u.q, (r0 + nt * 8 + 2 * j + e) / ge.g, lo, hi);
+                        if (row < cur_sh->q.n * ge.g) row_range(ge, cur_sh->q, row / ge.g, lo, hi);
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -790,7 +807,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const int pos = tile_at + k * 16 + c * 8 + r;
-                        if (!((have >> k) & 1u) || pos < u.lo || pos >= u.hi) sv[k][c] = 0.0f;
+                        if (!((have >> k) & 1u) || pos < cur_sh->lo || pos >= cur_sh->hi) sv[k][c] = 0.0f;
                     }
             }
 
@@ -872,11 +889,9 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    const uint32_t x8 = x[w] >> 8, y8 = y[w] >> 8;
-                    const uint32_t a0 = x[w] & 0x000F000Fu, a1 = x[w] & 0x00F000F0u;
-                    const uint32_t a2 = y[w] & 0x000F000Fu, a3 = y[w] & 0x00F000F0u;
-                    const uint32_t c0_ = x8 & 0x000F000Fu, c1_ = x8 & 0x00F000F0u;
-                    const uint32_t c2_ = y8 & 0x000F000Fu, c3_ = y8 & 0x00F000F0u;
+                    uint32_t a0, a1, a2, a3, c0_, c1_, c2_, c3_;
+                    nibbles(x[w], a0, a1, c0_, c1_);
+                    nibbles(y[w], a2, a3, c2_, c3_);
 #pragma unroll
                     for (int nt = 0; nt < NR; ++nt) {
                         mma(o[nt][2 * w], a0, a1, a2, a3, b0[nt], b1[nt]);
@@ -885,12 +900,16 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 }
             }
             __syncwarp();                 // every lane has read the stage
-            send(done + i + static_cast<int64_t>(S) * NW, stage);
-            if (++stage == S) {
-                stage = 0;
+            send(done + next + S * NW, at, bar);
+            at += C::TILE;
+            bar += 8;
+            if (at == ring_at + S * C::TILE) {
+                at = ring_at;
+                bar = bar0;
                 phase ^= 1;
             }
         }
+        u = *cur_sh;
 
         // ------------------------------------------------ join the warps
 #pragma unroll
@@ -930,9 +949,10 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                         for (int w = 0; w < W; ++w) {
                             float4 *dst = reinterpret_cast<float4 *>(buf + (nt * 8 + 2 * j + c) * C::OROW + r * (D / 8) + 4 * w);
                             const float b = oc[nt][c], fc = up[nt][c];
-                            float4 v = make_float4((o[nt][2 * w][c] - b) * fc, (o[nt][2 * w][c + 2] * 0.0625f - b) * fc,
+                            float4 v = make_float4((o[nt][2 * w][c] - b) * fc,
+                                                   ((o[nt][2 * w][c + 2] - o[nt][2 * w][c]) * 0.0625f - b) * fc,
                                                    (o[nt][2 * w + 1][c] - b) * fc,
-                                                   (o[nt][2 * w + 1][c + 2] * 0.0625f - b) * fc);
+                                                   ((o[nt][2 * w + 1][c + 2] - o[nt][2 * w + 1][c]) * 0.0625f - b) * fc);
                             if (!OWN && round) {
                                 const float4 t = *dst;
                                 v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);

@@ -669,7 +669,7 @@ static tq_status check_kv4(const tq_kv4 *kv, bool *empty) {
     }
     if (!kv->pool || !kv->table || !kv->kv_len || !kv->q_start) return TQ_ERR_NULL;
     if (!mul_ok(kv->npages, static_cast<int64_t>(page)) || !mul_ok(kv->nseq, kv->ldt) ||
-        !mul_ok(kv->nseq * kv->ldt, 4) || !mul_ok(kv->table_cols, kv->page_size))
+        !mul_ok(kv->npages * kv->heads, kv->page_size / 16, INT64_C(0xfffffffe)) || !mul_ok(kv->nseq * kv->ldt, 4) || !mul_ok(kv->table_cols, kv->page_size))
         return TQ_ERR_OVERFLOW;
     if (!aligned(kv->pool, 16) || !aligned(kv->table, 4) || !aligned(kv->kv_len, 4) || !aligned(kv->q_start, 4))
         return TQ_ERR_ALIGN;

@@ -48,6 +48,15 @@ __device__ __forceinline__ int kv_page(const tq_kv4 &kv, int64_t b, int pos) {
     return page >= 0 && page < kv.npages ? page : -1;
 }
 
+// The number in the pool of the block that holds head h of a sequence's token
+// at `pos`, or 2^32 - 1 (the host refuses pools of as many blocks).
+__device__ __forceinline__ uint32_t kv_block_number(const tq_kv4 &kv, int64_t b, int h, int pos) {
+    const int page = kv_page(kv, b, pos);
+    const int per = kv.page_size / kKvBlock;
+    return page < 0 ? 0xffffffffu
+                    : (static_cast<uint32_t>(page) * kv.heads + h) * per + (pos & (kv.page_size - 1)) / kKvBlock;
+}
+
 // The block that holds head h of a page's token `slot`.
 __device__ __forceinline__ unsigned char *kv_block(const tq_kv4 &kv, int page, int h, int slot) {
     const int64_t rec = kv_record_bytes(kv.dim, kv.page_size);
