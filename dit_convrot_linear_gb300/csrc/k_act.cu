@@ -23,6 +23,7 @@
 // kernels next to the projections, candidates for fusion, with fp32 norms
 // (TensorFold PR #948, "What comes next").
 
+#include <atomic>
 #include <cfloat>
 #include <type_traits>
 
@@ -884,10 +885,15 @@ tq_status launch_rotq(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, void
                 : warps <= 16 ? k_rotq<TILED, PRE, 16>
                               : k_rotq<TILED, PRE, kRotqMaxWarps>;
     // persistent: as many CTAs as are resident at once
-    int per_sm = 0;
-    const cudaError_t oe = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, 0);
-    if (oe != cudaSuccess) return cuda_fail(oe);
-    per_sm = per_sm < 1 ? 1 : per_sm;
+    // (asked once per row length; the answer depends on the kernel alone)
+    static std::atomic<int> asked[kRotqMaxWarps + 1];
+    int per_sm = asked[warps].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        const cudaError_t oe = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, 0);
+        if (oe != cudaSuccess) return cuda_fail(oe);
+        per_sm = per_sm < 1 ? 1 : per_sm;
+        asked[warps].store(per_sm, std::memory_order_relaxed);
+    }
     const int64_t want = static_cast<int64_t>(dev.sms) * per_sm;
     const unsigned grid = static_cast<unsigned>(M < want ? M : want);
     if constexpr (TILED) {

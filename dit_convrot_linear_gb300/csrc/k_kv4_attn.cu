@@ -504,6 +504,24 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             return;
         }
     }
+    // The raw queries of the next row tile come while the tiles of this one are
+    // read: a row a warp, and further ones by turns.
+    constexpr int E = D / 32, RW = (R + NW - 1) / NW;
+    uint32_t raw[RW][E / 2];
+    auto load_queries = [&](const Run &v) {
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            const int row = v.rt * R + warp + k * NW;
+            const bool is = warp + k * NW < R && row < v.q.n * ge.g;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                p.a.Q + static_cast<int64_t>(v.q.start + (is ? row / ge.g : 0)) * p.a.ldq +
+                static_cast<int64_t>(v.h * ge.g + (is ? row % ge.g : 0)) * D + lane * E);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) raw[k][e] = is ? src[e] : 0u;
+        }
+    };
+    load_queries(u);
+
     // ---------------------------------------------------- this warp's copies
     // Its tiles are warp, warp + NW, .. of the run.  Lane i holds where tile i of
     // 32 at a time lies (the number of its block in the pool plus one, two of them
@@ -582,23 +600,6 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     // be fetched from far away.
     int nparts = 0, joined = -1;          // parts left elsewhere; parts looked at for the last join
     int cf = 0, cl = 0;
-    // The raw queries of the next row tile come while the tiles of this one are
-    // read: a row a warp, and further ones by turns.
-    constexpr int E = D / 32, RW = (R + NW - 1) / NW;
-    uint32_t raw[RW][E / 2];
-    auto load_queries = [&](const Run &v) {
-#pragma unroll
-        for (int k = 0; k < RW; ++k) {
-            const int row = v.rt * R + warp + k * NW;
-            const bool is = warp + k * NW < R && row < v.q.n * ge.g;
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                p.a.Q + static_cast<int64_t>(v.q.start + (is ? row / ge.g : 0)) * p.a.ldq +
-                static_cast<int64_t>(v.h * ge.g + (is ? row % ge.g : 0)) * D + lane * E);
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) raw[k][e] = is ? src[e] : 0u;
-        }
-    };
-    load_queries(u);
     Run *next_sh = reinterpret_cast<Run *>(sm + C::oNext), *cur_sh = next_sh + 1;
     for (;;) {
       const bool last = done >= n_all;    // joining parts, not warps

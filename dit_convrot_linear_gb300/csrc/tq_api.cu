@@ -625,7 +625,7 @@ tq_status tq_rmsnorm_quant_act_tiled(const void *X, int64_t M, int64_t K, int64_
 tq_status tq_rope(const void *X, int64_t tokens, int64_t heads, int64_t dim, int64_t ldx,
                   const tq_rope_spec *spec, void *Y, int64_t ldy, cudaStream_t stream) {
     if (!spec) return TQ_ERR_NULL;
-    if (tokens < 0 || heads < 0 || heads > (1 << 20) || dim < 8 || dim > TQ_ROPE_MAX_DIM || dim % 8)
+    if (tokens < 0 || heads < 0 || heads > 4096 || dim < 8 || dim > TQ_ROPE_MAX_DIM || dim % 8)
         return TQ_ERR_SHAPE;
     if (spec->naxes < 1 || spec->naxes > TQ_ROPE_MAX_AXES || spec->pairs < 1 || spec->pairs > dim / 2)
         return TQ_ERR_SHAPE;

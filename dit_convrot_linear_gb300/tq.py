@@ -666,21 +666,51 @@ class ChainPlan(GroupedPlan):
 
 
 # ------------------------------------------------------- an attention layer
+# These calls are short: at a few tokens the checks of the host weigh as much as
+# the kernel, so a tensor's properties are read once.
 
-def _norm_args(X, gamma, R, H):
+def _rows(t, what, dtype, M: int, K: int) -> int:
+    """The row stride of a row-major CUDA matrix of at least M x K."""
+    s = t.shape
+    if t.is_cuda and t.dtype is dtype and len(s) == 2 and s[0] >= M and s[1] >= K:
+        ld, one = t.stride()
+        if one == 1 or not t.numel():
+            return ld
+    _req(t, what, dtype=dtype, rows=M, cols=K)
+    return t.stride(0)
+
+
+def _flat(t, what, dtype, n: int):
+    """A contiguous CUDA tensor of at least n values."""
+    if not (t.is_cuda and t.dtype is dtype and t.numel() >= n and t.is_contiguous()):
+        _req(t, what, dtype=dtype, nbytes=n * t.element_size())
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _raw_stream(t, stream) -> int:
+    """The stream of a call on t's device (the current one where none is given)."""
     import torch
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if stream is None else stream.cuda_stream
+
+
+def _norm(X, gamma, eps, R, H, Y, Xq, sx, stream):
+    import torch
+    bf16 = torch.bfloat16
     M, K = X.shape
-    _req(X, "X", dtype=torch.bfloat16, rows=M, cols=K)
-    _req(gamma, "gamma", dtype=torch.float32, nbytes=4 * K)
-    if R is not None:
-        _req(R, "R", dtype=torch.bfloat16, rows=M, cols=K)
-    if H is not None:
-        _req(H, "H", dtype=torch.bfloat16, rows=M, cols=K)
-    return M, K
-
-
-def _ld(t) -> int:
-    return 0 if t is None else t.stride(0)
+    ldx = _rows(X, "X", bf16, M, K)
+    _flat(gamma, "gamma", torch.float32, K)
+    ldr = 0 if R is None else _rows(R, "R", bf16, M, K)
+    ldh = 0 if H is None else _rows(H, "H", bf16, M, K)
+    ldy = 0 if Y is None else _rows(Y, "Y", bf16, M, K)
+    if Xq is not None:
+        if _rows(Xq, "Xq", torch.int8, M, K) != K and M > 1:
+            raise ValueError(f"Xq must be dense (row stride {K})")
+        _flat(sx, "sx", torch.float32, M)
+    _check((_lib or load()).tq_rmsnorm_quant_act(
+        X.data_ptr(), M, K, ldx, 0 if R is None else R.data_ptr(), ldr, gamma.data_ptr(), eps,
+        0 if H is None else H.data_ptr(), ldh, 0 if Y is None else Y.data_ptr(), ldy,
+        0 if Xq is None else Xq.data_ptr(), 0 if Xq is None else sx.data_ptr(), _raw_stream(X, stream)),
+        "tq_rmsnorm_quant_act")
 
 
 def rmsnorm_quant_act(X, gamma, eps=1e-6, R=None, H=None, Y=None, Xq=None, sx=None, stream=None):
@@ -689,18 +719,11 @@ def rmsnorm_quant_act(X, gamma, eps=1e-6, R=None, H=None, Y=None, Xq=None, sx=No
     receives h, ``Y`` the normed rows in bf16, where given.  Returns (Xq, sx)
     for linear_q8."""
     import torch
-    M, K = _norm_args(X, gamma, R, H)
     if Xq is None:
-        Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
+        Xq = torch.empty(X.shape, dtype=torch.int8, device=X.device)
     if sx is None:
-        sx = torch.empty(M, dtype=torch.float32, device=X.device)
-    if Y is not None:
-        _req(Y, "Y", dtype=torch.bfloat16, rows=M, cols=K)
-    _req(Xq, "Xq", dtype=torch.int8, rows=M, cols=K, dense=True)
-    _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
-    _check(lib().tq_rmsnorm_quant_act(_ptr(X), M, K, X.stride(0), _ptr(R), _ld(R), _ptr(gamma), float(eps), _ptr(H),
-                                      _ld(H), _ptr(Y), _ld(Y), _ptr(Xq), _ptr(sx), _stream(stream)),
-           "tq_rmsnorm_quant_act")
+        sx = torch.empty(X.shape[0], dtype=torch.float32, device=X.device)
+    _norm(X, gamma, eps, R, H, Y, Xq, sx, stream)
     return Xq, sx
 
 
@@ -708,13 +731,9 @@ def rmsnorm(X, gamma, eps=1e-6, R=None, H=None, Y=None, stream=None):
     """The RMS norm alone, bf16 [M, K] (the input of the A16 products):
     ``rmsnorm_quant_act`` without its codes.  Returns Y."""
     import torch
-    M, K = _norm_args(X, gamma, R, H)
     if Y is None:
-        Y = torch.empty((M, K), dtype=torch.bfloat16, device=X.device)
-    _req(Y, "Y", dtype=torch.bfloat16, rows=M, cols=K)
-    _check(lib().tq_rmsnorm_quant_act(_ptr(X), M, K, X.stride(0), _ptr(R), _ld(R), _ptr(gamma), float(eps), _ptr(H),
-                                      _ld(H), _ptr(Y), Y.stride(0), 0, 0, _stream(stream)),
-           "tq_rmsnorm_quant_act")
+        Y = torch.empty(X.shape, dtype=torch.bfloat16, device=X.device)
+    _norm(X, gamma, eps, R, H, Y, None, None, stream)
     return Y
 
 
@@ -722,17 +741,23 @@ def rmsnorm_quant_act_tiled(X, gamma, eps=1e-6, R=None, H=None, At=None, sx=None
     """``rmsnorm_quant_act`` into the tiled operand.  Returns (At, sx) for
     linear_tiled / linear_tt."""
     import torch
-    M, K = _norm_args(X, gamma, R, H)
+    bf16 = torch.bfloat16
+    M, K = X.shape
+    ldx = _rows(X, "X", bf16, M, K)
+    _flat(gamma, "gamma", torch.float32, K)
+    ldr = 0 if R is None else _rows(R, "R", bf16, M, K)
+    ldh = 0 if H is None else _rows(H, "H", bf16, M, K)
     need = act_tiled_bytes(M, K)
     if At is None:
         At = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
     if sx is None:
         sx = torch.empty(M, dtype=torch.float32, device=X.device)
     _req(At, "At", nbytes=need)
-    _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
-    _check(lib().tq_rmsnorm_quant_act_tiled(_ptr(X), M, K, X.stride(0), _ptr(R), _ld(R), _ptr(gamma), float(eps),
-                                            _ptr(H), _ld(H), _ptr(At), _nbytes(At), _ptr(sx), _stream(stream)),
-           "tq_rmsnorm_quant_act_tiled")
+    _flat(sx, "sx", torch.float32, M)
+    _check((_lib or load()).tq_rmsnorm_quant_act_tiled(
+        X.data_ptr(), M, K, ldx, 0 if R is None else R.data_ptr(), ldr, gamma.data_ptr(), eps,
+        0 if H is None else H.data_ptr(), ldh, At.data_ptr(), _nbytes(At), sx.data_ptr(), _raw_stream(X, stream)),
+        "tq_rmsnorm_quant_act_tiled")
     return At, sx
 
 
@@ -752,20 +777,26 @@ class RopeSpec:
         self.inv_freq = inv_freq
         self.axis = None if axis is None else (ctypes.c_uint8 * pairs)(*[int(a) for a in axis])
         self.pairs, self.interleaved = pairs, bool(interleaved)
+        self._c = RopeSpecC(None, 0, _ptr(inv_freq), None if axis is None else ctypes.addressof(self.axis), 1, pairs,
+                            int(self.interleaved))
+        self._p = ctypes.addressof(self._c)
 
 
-def _heads(X, what, tokens=None, heads=None, dim=None):
-    """Rows of heads, bf16 [tokens, heads, dim], a token's heads side by side."""
+def _heads(X, what, tokens=None, heads=None, dim=None) -> int:
+    """The token stride of rows of heads, bf16 [tokens, heads, dim], a token's
+    heads side by side."""
     import torch
-    _req(X, what, dtype=torch.bfloat16)
     s = X.shape
+    if not X.is_cuda or X.dtype is not torch.bfloat16:
+        _req(X, what, dtype=torch.bfloat16)
     if len(s) != 3 or (tokens is not None and s[0] != tokens) or (heads is not None and s[1] != heads) or (
             dim is not None and s[2] != dim):
         raise ValueError(f"{what} is {tuple(s)}, expected [{tokens or 'tokens'}, {heads or 'heads'}, {dim or 'dim'}]")
-    if X.numel() and (X.stride(2) != 1 or (s[1] > 1 and X.stride(1) != s[2])):
+    ld, head, one = X.stride()
+    if (one != 1 or (head != s[2] and s[1] > 1)) and X.numel():
         raise ValueError(f"{what}: a token's heads must lie side by side, got strides {X.stride()}")
     # one token has no step to the next: its row's length stands for it
-    return X.stride(0) if s[0] > 1 else s[1] * s[2]
+    return ld if s[0] > 1 else s[1] * s[2]
 
 
 def rope(X, pos, spec: RopeSpec, Y=None, stream=None):
@@ -775,12 +806,15 @@ def rope(X, pos, spec: RopeSpec, Y=None, stream=None):
     T, H, D = X.shape
     if Y is None:
         Y = torch.empty((T, H, D), dtype=torch.bfloat16, device=X.device)
-    ldx, ldy = _heads(X, "X"), _heads(Y, "Y", T, H, D)
-    _req(pos, "pos", dtype=torch.int32, rows=1, cols=T)
-    c = RopeSpecC(_ptr(pos), pos.stride(0) if pos.shape[0] > 1 else T, _ptr(spec.inv_freq),
-                  None if spec.axis is None else ctypes.addressof(spec.axis), pos.shape[0], spec.pairs,
-                  int(spec.interleaved))
-    _check(lib().tq_rope(_ptr(X), T, H, D, ldx, ctypes.addressof(c), _ptr(Y), ldy, _stream(stream)), "tq_rope")
+    ldx = _heads(X, "X")
+    ldy = ldx if Y is X else _heads(Y, "Y", T, H, D)
+    ldpos = _rows(pos, "pos", torch.int32, 1, T)
+    c = spec._c
+    c.pos = pos.data_ptr()
+    c.naxes = pos.shape[0]
+    c.ldpos = ldpos if c.naxes > 1 else T
+    _check((_lib or load()).tq_rope(X.data_ptr(), T, H, D, ldx, spec._p, Y.data_ptr(), ldy, _raw_stream(X, stream)),
+           "tq_rope")
     return Y
 
 
@@ -839,7 +873,8 @@ def kv4_append(batch: KV4Batch, K, V, stream=None):
     token stride) into their pages."""
     c = batch.cache
     ldk, ldv = _heads(K, "K", batch.tokens, c.heads, c.dim), _heads(V, "V", batch.tokens, c.heads, c.dim)
-    _check(lib().tq_kv4_append(batch._p, _ptr(K), ldk, _ptr(V), ldv, _stream(stream)), "tq_kv4_append")
+    _check((_lib or load()).tq_kv4_append(batch._p, K.data_ptr(), ldk, V.data_ptr(), ldv, _raw_stream(K, stream)),
+           "tq_kv4_append")
 
 
 def kv4_read(batch: KV4Batch, K=None, V=None, stream=None):
@@ -851,7 +886,8 @@ def kv4_read(batch: KV4Batch, K=None, V=None, stream=None):
     K = torch.zeros(shape, dtype=torch.bfloat16, device=c.pool.device) if K is None else K
     V = torch.zeros(shape, dtype=torch.bfloat16, device=c.pool.device) if V is None else V
     ldk, ldv = _heads(K, "K", *shape), _heads(V, "V", *shape)
-    _check(lib().tq_kv4_read(batch._p, _ptr(K), ldk, _ptr(V), ldv, _stream(stream)), "tq_kv4_read")
+    _check((_lib or load()).tq_kv4_read(batch._p, K.data_ptr(), ldk, V.data_ptr(), ldv, _raw_stream(K, stream)),
+           "tq_kv4_read")
     return K, V
 
 
@@ -867,11 +903,10 @@ def kv4_attention(batch: KV4Batch, Q, scale: float, workspace, causal: bool = Tr
         O = torch.zeros((T, H, D), dtype=torch.bfloat16, device=Q.device)
     ldq, ldo = _heads(Q, "Q", batch.tokens, None, batch.cache.dim), _heads(O, "O", T, H, D)
     if lse is not None:
-        _req(lse, "lse", dtype=torch.float32, nbytes=4 * T * H)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
-    _req(workspace, "workspace")
-    _check(lib().tq_kv4_attention(batch._p, _ptr(Q), H, ldq, batch.max_q, float(scale), int(bool(causal)), window,
-                                  _ptr(O), ldo, _ptr(lse), _ptr(workspace), _nbytes(workspace), _stream(stream)),
-           "tq_kv4_attention")
+        _flat(lse, "lse", torch.float32, T * H)
+    _flat(workspace, "workspace", torch.uint8, 1)
+    _check((_lib or load()).tq_kv4_attention(
+        batch._p, Q.data_ptr(), H, ldq, batch.max_q, scale, 1 if causal else 0, window, O.data_ptr(), ldo,
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(Q, stream)),
+        "tq_kv4_attention")
     return O

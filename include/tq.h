@@ -719,6 +719,7 @@ typedef struct {
  *   X      bf16: head i of token t is the dim values at X + t * ldx + i * dim
  *          (the query and key heads of a fused projection's row in one call);
  *          ldx >= heads * dim, ldx % 8 == 0, X 16-byte aligned.
+ *   heads  0 .. 4096.
  *   dim    a multiple of 8, 8 .. TQ_ROPE_MAX_DIM.
  *   Y      as X with ldy; it may be X itself (ldy == ldx), but must not
  *          otherwise overlap X.
