@@ -40,30 +40,6 @@ __device__ __forceinline__ void begin(const tq_kv4 &kv, int *starts, bool &bad) 
     __syncthreads();
 }
 
-// The transform of a row held by eight lanes, V neighbouring values each, scaled by sqrt(1 / dim).
-template <int V>
-__device__ __forceinline__ void turn_row(float (&v)[V]) {
-#pragma unroll
-    for (int h = 1; h < V; h <<= 1)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (!(i & h)) {
-                const float a = v[i], b = v[i + h];
-                v[i] = a + b;
-                v[i + h] = a - b;
-            }
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) {
-        const float sg = (lane & m) ? -1.0f : 1.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = fmaf(sg, v[i], __shfl_xor_sync(0xffffffffu, v[i], m));
-    }
-    const float c = sqrtf(1.0f / (kLanes * V));
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= c;
-}
-
 // A lane's work: row t of head h, keys or values.  Items run over four tokens,
 // then heads and sides, then the next tokens.
 struct Item {

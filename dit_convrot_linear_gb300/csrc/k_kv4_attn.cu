@@ -85,41 +85,6 @@ struct Cfg {
     static_assert(NT * 8 + NW * 8 <= JOIN * OBUF && SMEM <= 228 * 1024 / CTAS - 1024, "shared memory");
 };
 
-struct Geo {                                 // what the cutting of a batch depends on
-    int g, causal, rows;                     // query heads a key/value head, mask, rows a row tile
-    int64_t window;
-};
-
-struct Run {                                 // one row tile of one key/value head (at most 64 bytes)
-    int b, h, rt;
-    KvSeq q;
-    int nrt;                                 // row tiles of the sequence
-    int lo, hi, t0, cost;                    // positions its rows see, first tile, tiles (0: they see nothing)
-};
-
-__device__ __forceinline__ void range_of(const Geo &ge, const KvSeq &q, int rt, int &lo, int &hi, int &t0, int &cost) {
-    const int rows = q.n * ge.g, r0 = rt * ge.rows;
-    const int i0 = r0 / ge.g, i1 = (min(r0 + ge.rows, rows) - 1) / ge.g;
-    const int p1 = q.len - q.n + i1;
-    hi = p1 < 0 ? 0 : ge.causal ? min(p1 + 1, q.len) : q.len;
-    const int64_t from = static_cast<int64_t>(q.len) - q.n + i0 - ge.window + 1;
-    lo = ge.window > 0 && from > 0 ? static_cast<int>(from < hi ? from : hi) : 0;
-    t0 = lo / kTile;
-    cost = (hi + kTile - 1) / kTile - t0;
-}
-
-// Positions that row i of a sequence sees.
-__device__ __forceinline__ void row_range(const Geo &ge, const KvSeq &q, int i, int &lo, int &hi) {
-    const int pos = q.len - q.n + i;
-    hi = pos < 0 ? 0 : ge.causal ? min(pos + 1, q.len) : q.len;
-    const int64_t from = static_cast<int64_t>(pos) - ge.window + 1;
-    lo = ge.window > 0 && from > 0 ? static_cast<int>(from < hi ? from : hi) : 0;
-}
-
-__device__ __forceinline__ int row_tiles(const Geo &ge, const KvSeq &q) {
-    return (q.n * ge.g + ge.rows - 1) / ge.rows;
-}
-
 // A row tile's weight in the cutting: its tiles, and as many as starting and
 // ending a row tile takes as long as.
 __device__ __forceinline__ int weight(int tiles) { return tiles ? tiles + kOver : 0; }
@@ -131,7 +96,7 @@ __device__ __forceinline__ int64_t seq_cost(const Geo &ge, const KvSeq &q) {
 #pragma unroll 1
     for (int rt = 0; rt < nrt; ++rt) {
         int lo, hi, t0, c;
-        range_of(ge, q, rt, lo, hi, t0, c);
+        range_of<kTile>(ge, q, rt, lo, hi, t0, c);
         sum += weight(c);
     }
     return sum;
@@ -143,7 +108,7 @@ __device__ __forceinline__ int64_t seq_cost_warp(const Geo &ge, const KvSeq &q) 
     int64_t sum = 0;
     for (int rt = lane; rt < nrt; rt += 32) {
         int lo, hi, t0, c;
-        range_of(ge, q, rt, lo, hi, t0, c);
+        range_of<kTile>(ge, q, rt, lo, hi, t0, c);
         sum += weight(c);
     }
 #pragma unroll
@@ -167,50 +132,9 @@ __device__ __forceinline__ bool advance(const tq_kv4 &kv, const Geo &ge, const K
                 u.nrt = row_tiles(ge, u.q);
             }
         }
-        range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
+        range_of<kTile>(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
     } while (u.cost == 0);
     return true;
-}
-
-// Zeros for the row tiles that see nothing (rows before position 0), a
-// sequence a CTA.
-template <int D>
-__device__ __noinline__ void zero_rows(const tq_kv4 &kv, const Kv4Attn &a, const Geo &ge) {
-    for (int64_t b = blockIdx.x; b < kv.nseq; b += gridDim.x) {
-        bool bad = false;
-        const KvSeq q = kv_seq(kv, b, bad);
-        const int none = q.n - q.len;        // rows before position 0
-        if (none <= 0) continue;
-        const int rows = q.n * ge.g, cut = q.len == 0 ? rows : none * ge.g / ge.rows * ge.rows;
-        const int64_t pieces = static_cast<int64_t>(cut) * kv.heads * (D / 8);
-        for (int64_t i = threadIdx.x; i < pieces; i += blockDim.x) {
-            const int c = static_cast<int>(i % (D / 8));
-            const int64_t k = i / (D / 8);
-            const int row = static_cast<int>(k % cut), h = static_cast<int>(k / cut);
-            const int64_t tok = q.start + row / ge.g;
-            const int hq = h * ge.g + row % ge.g;
-            *reinterpret_cast<uint4 *>(a.O + tok * a.ldo + static_cast<int64_t>(hq) * D + c * 8) = make_uint4(0, 0, 0, 0);
-            if (a.lse && c == 0) a.lse[tok * a.heads_q + hq] = -INFINITY;
-        }
-    }
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    uint32_t w;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-    return w;
-}
-
-__device__ __forceinline__ uint32_t bf16_bits2(float lo, float hi) {          // bf16
-    uint32_t w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-    return w;
 }
 
 // A word's nibbles 0 .. 7 as fp16 pairs, in units of 2^-24 (a 16-bit pattern
@@ -252,29 +176,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t one;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
-    return one != 0;
-}
-
-__device__ __forceinline__ void bulk_copy(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
-// 2^k as fp32, k clamped to the normal range
-__device__ __forceinline__ float pow2i(int k) {
-    return __uint_as_float(static_cast<uint32_t>(min(max(k, -126), 127) + 127) << 23);
-}
-
-// a / b for a, b > 0: in 32 bits where they fit
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
 }
 
 struct Found {                               // where a CTA's run starts
@@ -397,7 +298,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         const int nrt = row_tiles(ge, mine);
         for (int rt = 0; rt < nrt; ++rt) {
             int lo, hi, t0, c;
-            range_of(ge, mine, rt, lo, hi, t0, c);
+            range_of<kTile>(ge, mine, rt, lo, hi, t0, c);
             np += parts_of(c);
         }
         int64_t np_at, np_sum;
@@ -423,7 +324,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             u.h = static_cast<int>(found->at) / static_cast<int>(found->head);
             int k2 = static_cast<int>(found->at) % static_cast<int>(found->head), n2 = 1;
             for (u.rt = 0; u.rt < u.nrt; ++u.rt) {
-                range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
+                range_of<kTile>(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
                 n2 = parts_of(u.cost);
                 if (k2 < n2) break;
                 k2 -= n2;
@@ -468,7 +369,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         if (u.nrt > 1) {                  // the row tile: by 32 at a time
             for (int base = 0; base < u.nrt; base += 32) {
                 int lo, hi, t0, c = 0;
-                if (base + lane < u.nrt) range_of(ge, u.q, base + lane, lo, hi, t0, c);
+                if (base + lane < u.nrt) range_of<kTile>(ge, u.q, base + lane, lo, hi, t0, c);
                 c = weight(c);
                 int64_t x = c;
 #pragma unroll
@@ -486,7 +387,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 at -= __shfl_sync(0xffffffffu, x, 31);
             }
         }
-        range_of(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
+        range_of<kTile>(ge, u.q, u.rt, u.lo, u.hi, u.t0, u.cost);
         // the weight of starting comes first: a run that ends within it leaves
         // the row tile to the next
         first = at > kOver ? static_cast<int>(at) - kOver : 0;
@@ -900,7 +801,9 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                     }
                 }
             }
-            __syncwarp();                 // every lane has read the stage
+            // every lane's reads of the stage before the next copy into it
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
             send(done + next + S * NW, at, bar);
             at += C::TILE;
             bar += 8;
@@ -1133,7 +1036,9 @@ tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
 }  // namespace
 
 size_t kv4_workspace_bytes(const DeviceInfo &dev) {
-    return count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * 64 * 2 + kMaxPart) * 4;
+    const size_t runs = count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * 64 * 2 + kMaxPart) * 4;
+    const size_t tc = kv4_tc_workspace_bytes(dev);
+    return (runs + 255) / 256 * 256 + tc;
 }
 
 tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceInfo &dev, cudaStream_t s) {
@@ -1146,6 +1051,10 @@ tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceI
     p.status = status_word();
     if (!p.status) return TQ_ERR_DEVICE;
     const int64_t rows = a.max_q * p.geo.g;
+    if (kv4_tc_takes(kv, a, rows)) {
+        const size_t runs = count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * 64 * 2 + kMaxPart) * 4;
+        return launch_kv4_attention_tc(kv, a, static_cast<unsigned char *>(a.ws) + (runs + 255) / 256 * 256, dev, s);
+    }
     if (kv.dim == 64) {
         if (rows <= 8) return launch<Cfg<64, 1, 8, 4, 2>>(p, dev, s);
         if (rows <= 16) return launch<Cfg<64, 2, 8, 3, 2>>(p, dev, s);

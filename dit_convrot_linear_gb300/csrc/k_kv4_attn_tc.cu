@@ -1,0 +1,1000 @@
+// Attention over the 4-bit cache for many query rows a key/value head (a
+// prompt's chunk, drafted tokens), on tcgen05: o = H^T softmax(scale (H q) . k') v'.
+//
+// With tens to thousands of rows the products bound the kernel, and mma.sync
+// reaches about a quarter of the tensor cores' rate here (9.1 cycles an
+// m16n8k16 measured, 520 TFLOP/s).  A CTA takes row tiles of one or two times
+// 128 query rows (a sequence's tokens times the heads that share a key/value
+// head) against tiles of 128 positions:
+//
+//   - a loader warp copies blocks of 16 tokens into a ring;
+//   - four warps widen them to fp16 operands in shared memory: a nibble masked
+//     out of a word is the fp16 subnormal u 2^-24, one fused multiply-add with
+//     (s, -8 s) makes it s (u - 8), s the token's scale over a power of two of
+//     the tile's largest.  Keys are the K-major rows of S = Q K^T; values, whose
+//     words hold two tokens, are the K-major rows of O = P V as they come;
+//   - one thread issues the products: S into TMEM (128 columns a row tile), P
+//     (fp16, over S's columns) times V into O, also in TMEM.  With two row tiles
+//     one's softmax runs during the other's products; with one, S has two places;
+//   - a thread a row does the softmax: its 128 scores come from TMEM, no value
+//     crosses lanes.  It speculates that the running maximum holds (it is raised
+//     only when passed by 2^8) and repeats the tile where it does not; O is then
+//     rescaled in place, which the tensor cores' order of work makes safe.
+//
+// Row tiles that are fewer than the SMs are cut along the positions; a second
+// kernel joins their parts, a warp a row, in order (the result does not depend
+// on timing).  Sums and statistics are fp32; q, k', p and v' are rounded to fp16
+// relative to their row's, tile's or maximum's scale.
+
+#include <cfloat>
+
+#include "tq_a16.cuh"
+#include "tq_kv4.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kTileT = 128;                  // positions a tile
+constexpr int kHalf = 64;                    // positions copied and widened at a time
+constexpr int kBlocks = kHalf / kKvBlock;    // blocks of them
+constexpr int kRing = 3;                     // halves in the ring
+constexpr unsigned int kStatusKvTcTimeout = 256u;
+constexpr float kNoneT = -FLT_MAX;
+constexpr float kSlackT = 8.0f;
+constexpr float kLog2eT = 1.4426950408889634f;
+constexpr int kMinPart = 4;                  // fewest tiles a part
+constexpr int kMaxSeqsT = 256;               // sequences the cutting holds in shared memory
+constexpr int kNoE = -1024;                  // exponent of a half whose values are all zero
+constexpr int kCols = 512;                   // TMEM columns
+constexpr int kMaxSmsT = 160;                // more SMs than this stay unused
+constexpr int kMaxItems = 2 * kMaxSmsT;      // parts of a call whose row tiles are cut
+
+template <int D_, int NQ_>
+struct TCfg {
+    static constexpr int D = D_, NQ = NQ_;
+    static constexpr int RU = 128 * NQ;                      // query rows a row tile
+    static constexpr int WSM = 4 * NQ;                       // softmax warps
+    static constexpr int W_DQ = WSM, W_LD = WSM + 4, W_MMA = WSM + 5;
+    static constexpr int NT = (WSM + 6) * 32;
+    static constexpr int BLK = kv_block_bytes(D);
+    static constexpr int RAW = kBlocks * BLK;
+    static constexpr int KT = kTileT * D * 2;                // bytes of a key tile, of a value tile, of a query tile
+    static constexpr int oK = 0, oV = 2 * KT, oQ = 4 * KT, oRaw = oQ + NQ * KT;
+    static constexpr int oBar = oRaw + kRing * RAW;
+    static constexpr int USED = oBar + 32 * 8;
+    static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;       // one CTA an SM: it takes all of TMEM
+};
+
+struct Item {                                // a part of a row tile
+    int idx, np, t0, n, lo, hi;              // its number; parts of its row tile; tiles; positions of the row tile
+    int b, h, rt;
+    KvSeq q;
+};
+
+struct Split {                               // a row tile in parts, for the join (32 bytes)
+    int np, start, rows, h, rt, pad[3];
+};
+
+struct TcParams {
+    tq_kv4 kv;
+    Kv4Attn a;
+    Geo geo;
+    unsigned int *status;
+    int *head;                               // items of this call (0: no row tile is in parts)
+    Split *table;                            // [2 grid]
+    float2 *stat;                            // [2 grid][RU]
+    float *part;                             // [2 grid][RU][D]
+    int split;                               // row tiles may be cut
+};
+
+__device__ __forceinline__ uint32_t sa(const void *p) { return smem_addr(p); }
+
+// A bounded wait by a whole warp, with one answer for all its lanes.  On expiry
+// the CTA's flag is raised, and every wait ends at once from then on; the roles
+// run through their loops without work, so that no barrier is left waiting.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *status) {
+    bool ok = mbar_try(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const long long t0 = clock64();
+        while (!ok) {
+            ok = mbar_try(bar, parity);
+            if (ok || *abort) break;
+            if (clock64() - t0 > kA16WaitLimit) {
+                *abort = 1;
+                atomicOr(status, kStatusKvTcTimeout);
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    return ok;
+}
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// K-major operand of 8x8 core matrices, 64 columns a panel (rows * 128 bytes)
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+    return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46);
+}
+
+#define TQ_R32(v)                                                                                                 \
+    "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), \
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),           \
+        "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]),           \
+        "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+
+__device__ __forceinline__ void t_ld32(uint32_t at, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void t_st32(uint32_t at, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+        TQ_R32(v));
+}
+
+__device__ __forceinline__ void t_ld8(uint32_t at, uint32_t *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(at));
+}
+
+__device__ __forceinline__ void t_st8(uint32_t at, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
+}
+
+__device__ __forceinline__ void t_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void t_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// d += a b with the fp16 pair (exact but for one rounding)
+__device__ __forceinline__ uint32_t hfma2_(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t hmul2_(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+constexpr uint32_t kMinus8 = 0x80088008u;    // -8 2^-24 twice
+constexpr uint32_t kSixteenth = 0x2C002C00u; // 1/16 twice
+
+template <class C>
+__global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant__ TcParams p) {
+    constexpr int D = C::D, NQ = C::NQ, RU = C::RU, PAN = kTileT * 128;      // PAN: bytes of a 64-column panel of 128 rows
+    extern __shared__ __align__(1024) unsigned char sm[];
+    __shared__ uint32_t tmem_sh;
+    __shared__ volatile int abort_sh;
+    __shared__ int n_items_sh, split_sh;
+    __shared__ int64_t per_sh;
+    __shared__ int item_sh[kMaxSeqsT], before_sh[kMaxSeqsT];
+    __shared__ KvSeq seq_sh[kMaxSeqsT];
+    __shared__ float max_sh[2][4][2];
+    __shared__ __align__(16) __half sv_sh[kHalf];
+    struct Info {                            // of a half: blocks that are there; 2^(e + 10) of the keys, exponent of the values
+        int at;
+        uint32_t there;
+        float kx;
+        int ev;
+    };
+    __shared__ Info raw_info[kRing], kv_info[4][2];
+    int64_t *cost_sh = reinterpret_cast<int64_t *>(sm);      // before any operand
+    int *unit_sh = reinterpret_cast<int *>(sm + kMaxSeqsT * 8);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const tq_kv4 &kv = p.kv;
+    const Geo &ge = p.geo;
+    const uint32_t smb = sa(sm);
+    const uint32_t bar = smb + C::oBar;
+    const uint32_t raw_full = bar, raw_empty = bar + 24, k_full = bar + 48, k_empty = bar + 64, v_full = bar + 80,
+                   v_empty = bar + 96, s_full = bar + 112, p_full = bar + 128, q_full = bar + 144, pv_done = bar + 160,
+                   all_done = bar + 176;
+
+    if (tid == 0) {
+        auto init = [&](uint32_t b, int n) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n) : "memory");
+        };
+        for (int i = 0; i < kRing; ++i) {
+            init(raw_full + 8 * i, 1);
+            init(raw_empty + 8 * i, 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            init(k_full + 8 * i, 8);             // four warps, two halves
+            init(k_empty + 8 * i, 1);
+            init(v_full + 8 * i, 8);
+            init(v_empty + 8 * i, 1);
+            init(s_full + 8 * i, 1);
+            init(p_full + 8 * i, 4);
+            init(q_full + 8 * i, 4);
+            init(pv_done + 8 * i, 1);
+        }
+        init(all_done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        abort_sh = 0;
+    }
+    if (warp == C::W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&tmem_sh)), "r"(kCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // ---------------------------------------------------- cutting
+    // Row tiles and their tiles of each sequence (a warp a sequence), all of
+    // them, then the parts: none where there are row tiles enough.
+    const int nseq = static_cast<int>(kv.nseq);
+    bool bad = false;
+    for (int i = tid; i < nseq; i += C::NT) seq_sh[i] = kv_seq(kv, i, bad);
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusIndex);
+    __syncthreads();
+    for (int i = warp; i < nseq; i += C::NT / 32) {
+        const KvSeq q = seq_sh[i];
+        const int nrt = row_tiles(ge, q);
+        int64_t sum = 0;
+        int units = 0;
+        for (int rt = lane; rt < nrt; rt += 32) {
+            int lo, hi, t0, c;
+            range_of<kTileT>(ge, q, rt, lo, hi, t0, c);
+            sum += c;
+            units += c > 0;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        units = __reduce_add_sync(0xffffffffu, units);
+        if (lane == 0) {
+            cost_sh[i] = sum;
+            unit_sh[i] = units;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int64_t sum = 0, units = 0;
+        for (int i = lane; i < nseq; i += 32) {
+            sum += cost_sh[i];
+            units += unit_sh[i];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            units += __shfl_xor_sync(0xffffffffu, units, o);
+        }
+        if (lane == 0) {
+            const int64_t per = quotient(sum * kv.heads + gridDim.x, gridDim.x);
+            per_sh = per < kMinPart ? kMinPart : per;
+            split_sh = p.split && units * kv.heads <= gridDim.x;
+        }
+    }
+    __syncthreads();
+    const int64_t per = per_sh;
+    const bool split = split_sh != 0;
+    auto parts_of = [&](int cost) { return cost == 0 ? 0 : !split || cost < per ? 1 : static_cast<int>(quotient(cost, per)); };
+    for (int i = warp; i < nseq; i += C::NT / 32) {
+        const KvSeq q = seq_sh[i];
+        const int nrt = row_tiles(ge, q);
+        int n = 0;
+        for (int rt = lane; rt < nrt; rt += 32) {
+            int lo, hi, t0, c;
+            range_of<kTileT>(ge, q, rt, lo, hi, t0, c);
+            n += parts_of(c);
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) item_sh[i] = n;           // of one head
+    }
+    __syncthreads();
+    if (warp == 0) {                             // running sums
+        int run = 0;
+        for (int base = 0; base < nseq; base += 32) {
+            const int v = base + lane < nseq ? item_sh[base + lane] * kv.heads : 0;
+            int x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (base + lane < nseq) before_sh[base + lane] = run + x - v;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) {
+            n_items_sh = run;
+            if (blockIdx.x == 0 && p.split) *p.head = split ? run : 0;
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_sh;
+    const int n_items = n_items_sh;
+
+    // Item `idx`, by a whole warp.
+    auto item = [&](int idx) {
+        Item it;
+        int lo = 0, hi = nseq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before_sh[mid] <= idx) lo = mid;
+            else hi = mid;
+        }
+        it.idx = idx;
+        it.b = lo;
+        it.q = seq_sh[lo];
+        int k = idx - before_sh[lo];
+        it.h = k / item_sh[lo];
+        k -= it.h * item_sh[lo];
+        const int nrt = row_tiles(ge, it.q);
+        it.rt = 0;
+        int part = 0, t0 = 0, c = 0;
+        it.np = 1;
+        for (int base = 0; base < nrt; base += 32) {
+            int l1 = 0, h1 = 0, n = 0;
+            if (base + lane < nrt) {
+                range_of<kTileT>(ge, it.q, base + lane, l1, h1, t0, c);
+                n = parts_of(c);
+            }
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, x > k);
+            if (in) {
+                const int l = __ffs(in) - 1;
+                it.rt = base + l;
+                part = k - __shfl_sync(0xffffffffu, x - n, l);
+                it.np = __shfl_sync(0xffffffffu, n, l);
+                break;
+            }
+            k -= __shfl_sync(0xffffffffu, x, 31);
+        }
+        range_of<kTileT>(ge, it.q, it.rt, it.lo, it.hi, t0, c);
+        const int f = static_cast<int>(static_cast<int64_t>(c) * part / it.np);
+        it.n = static_cast<int>(static_cast<int64_t>(c) * (part + 1) / it.np) - f;
+        it.t0 = t0 + f;
+        if (it.np > 1 && part == 0 && warp == 0 && lane == 0)
+            p.table[idx] = {it.np, it.q.start, it.q.n * ge.g, it.h, it.rt, {0, 0, 0}};
+        if (split && it.np == 1 && warp == 0 && lane == 0) p.table[idx].np = 1;
+        else if (split && part > 0 && warp == 0 && lane == 0) p.table[idx].np = 0;
+        return it;
+    };
+
+    if (warp == C::W_LD) {
+        // ------------------------------------------------ loader
+        int k = 0, sent = 0;                     // halves
+        for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
+            const Item it = item(idx);
+            for (int t = 0; t < 2 * it.n; ++t, ++k) {
+                const int s = k % kRing;
+                const int at = it.t0 * kTileT + t * kHalf;
+                // a copy a page's piece of the half: lane 0 .. 3 a block each, the
+                // first of a page's for all of them
+                const int each = min(kBlocks, kv.page_size / kKvBlock);
+                uint32_t num = 0;
+                const int pos = at + (lane / each * each) * kKvBlock;
+                if (lane < kBlocks && pos < it.hi) {
+                    num = kv_block_number(kv, it.b, it.h, pos) + 1;
+                    if (num == 0) bad = true;
+                }
+                const uint32_t there = __ballot_sync(0xffffffffu, num != 0) & ((1u << kBlocks) - 1);
+                if (!tc_wait(raw_empty + 8 * s, ((k / kRing) & 1) ^ 1, &abort_sh, p.status)) continue;
+                if (lane == 0) {
+                    raw_info[s].at = at;
+                    raw_info[s].there = there;
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(raw_full + 8 * s),
+                                 "r"(static_cast<uint32_t>(__popc(there)) * C::BLK)
+                                 : "memory");
+                    ++sent;
+                }
+                __syncwarp();
+                if (num && lane % each == 0)
+                    bulk_copy(smb + C::oRaw + s * C::RAW + lane * C::BLK,
+                              reinterpret_cast<uint64_t>(kv.pool) + static_cast<uint64_t>(num - 1) * C::BLK,
+                              each * C::BLK, raw_full + 8 * s);
+                __syncwarp();
+            }
+        }
+        if (bad) atomicOr(p.status, kStatusIndex);
+        if (lane == 0)                           // never leave with copies landing
+            for (int i = sent > kRing ? sent - kRing : 0; i < sent; ++i)
+                mbar_wait_bounded(raw_full + 8 * (i % kRing), (i / kRing) & 1, kA16DrainLimit);
+        __syncwarp();
+    } else if (warp >= C::W_DQ && warp < C::W_DQ + 4) {
+        // ------------------------------------------------ widening
+        const int t = tid - C::W_DQ * 32, dw = warp - C::W_DQ;
+        const int tok = t & (kHalf - 1), part = t / kHalf;       // this thread's token, and which half of its key row
+        int k = 0;                                               // halves
+        for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
+            const Item it = item(idx);
+            for (int i = 0; i < 2 * it.n; ++i, ++k) {
+                const int rs = k % kRing, s = (k >> 1) & 1, half = k & 1;
+                const uint32_t par = ((k >> 2) & 1) ^ 1;
+                const bool ok = tc_wait(raw_full + 8 * rs, (k / kRing) & 1, &abort_sh, p.status);
+                const unsigned char *raw = sm + C::oRaw + rs * C::RAW;
+                const int at = raw_info[rs].at;
+                const uint32_t there = raw_info[rs].there;
+                // the token's scales, and the half's largest
+                const unsigned char *blk = raw + (tok / kKvBlock) * C::BLK;
+                const int pos = at + tok, row = tok % kKvBlock;
+                const bool is = ok && ((there >> (tok / kKvBlock)) & 1u) && pos >= it.lo && pos < it.hi;
+                const float *sc = reinterpret_cast<const float *>(blk + 16 * D);
+                const float sk = is ? sc[row] : 0.0f, sv = is ? sc[16 + row] : 0.0f;
+                float mk = sk, mv = sv;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+                    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+                }
+                if (lane == 0) {
+                    max_sh[half][dw][0] = mk;
+                    max_sh[half][dw][1] = mv;
+                }
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                mk = fmaxf(max_sh[half][0][0], max_sh[half][1][0]);
+                mv = fmaxf(max_sh[half][0][1], max_sh[half][1][1]);
+                const int ek = mk > 0.0f ? static_cast<int>(__float_as_uint(mk) >> 23) - 127 : 0;
+                const int ev = mv > 0.0f ? static_cast<int>(__float_as_uint(mv) >> 23) - 127 : kNoE;
+                // scales over the power of two of the largest, times 2^14
+                const float fk = sk * pow2i(-ek) * 16384.0f, fv = sv * pow2i(-ev) * 16384.0f;
+                if (part == 0) sv_sh[tok] = __float2half_rn(fv);
+                // keys: 8 nibbles to 16 bytes in the order (0, 4), (1, 5), (2, 6), (3, 7)
+                if (tc_wait(k_empty + 8 * s, par, &abort_sh, p.status) && ok) {
+                    if (t == 0) kv_info[(k >> 1) & 3][half] = {at, there, pow2i(ek + 10), ev};
+                    const __half2 h2 = __half2half2(__float2half_rn(fk));
+                    const uint32_t s1 = *reinterpret_cast<const uint32_t *>(&h2);
+                    const uint32_t s16 = hmul2_(s1, kSixteenth), b = hmul2_(s1, kMinus8);
+                    const int r = half * kHalf + tok;
+                    unsigned char *dst = sm + C::oK + s * C::KT + ((r >> 3) << 10) + (r & 7) * 16;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(blk + row * (D / 2));
+#pragma unroll
+                    for (int c0 = 0; c0 < D / 64; ++c0) {
+                        const int c = part * (D / 64) + c0;
+                        const uint4 x4 = src[c];
+                        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t y = x[e] >> 8;
+                            const uint4 o = make_uint4(hfma2_(x[e] & 0x000F000Fu, s1, b), hfma2_(x[e] & 0x00F000F0u, s16, b),
+                                                       hfma2_(y & 0x000F000Fu, s1, b), hfma2_(y & 0x00F000F0u, s16, b));
+                            const int ch = c * 4 + e;            // 8 columns
+                            *reinterpret_cast<uint4 *>(dst + (ch >> 3) * PAN + (ch & 7) * 128) = o;
+                        }
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) arrive(k_full + 8 * s);
+                }
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                // values: a thread a column, eight tokens at a time: its nibble of
+                // four words, each two tokens
+                if (tc_wait(v_empty + 8 * s, par, &abort_sh, p.status) && ok) {
+                    const int sh = (lane & 2) * 4;               // nibbles 2 and 3 are 8 bits up
+                    const uint32_t mask = lane & 1 ? 0x00F000F0u : 0x000F000Fu;
+#pragma unroll
+                    for (int o2 = 0; o2 < 2; ++o2) {
+                        const int o = dw + 4 * o2;
+                        const uint4 sc4 = *reinterpret_cast<const uint4 *>(sv_sh + 8 * o);
+                        const uint32_t s1[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
+                        uint32_t sx[4], b[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            b[q] = hmul2_(s1[q], kMinus8);
+                            sx[q] = lane & 1 ? hmul2_(s1[q], kSixteenth) : s1[q];
+                        }
+                        const unsigned char *vb = raw + (o >> 1) * C::BLK + 8 * D + (o & 1) * 4 * D;
+                        unsigned char *dst = sm + C::oV + s * C::KT + half * (D * 128) + o * 128;
+#pragma unroll
+                        for (int d0 = 0; d0 < D; d0 += 32) {
+                            const int d = d0 + lane;
+                            uint32_t r[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t w = *reinterpret_cast<const uint32_t *>(vb + q * D + (d >> 2) * 4);
+                                r[q] = hfma2_((w >> sh) & mask, sx[q], b[q]);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + ((d >> 3) << 10) + (d & 7) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+                        }
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        arrive(v_full + 8 * s);
+                        arrive(raw_empty + 8 * rs);
+                    }
+                }
+            }
+        }
+    } else if (warp == C::W_MMA) {
+        // ------------------------------------------------ products
+        constexpr uint32_t kIdS = (1u << 4) | (static_cast<uint32_t>(kTileT >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+        constexpr uint32_t kIdO = (1u << 4) | (static_cast<uint32_t>(D >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+        int k = 0, ni = 0;
+        bool issued = false;
+        auto score = [&](int q, int slot, int s) {       // S[slot] = Q[q] K[s]^T
+            fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * PAN + (kk & 3) * 256;
+                    const uint64_t ad = operand(smb + C::oQ + q * C::KT + off), bd = operand(smb + C::oK + s * C::KT + off);
+                    asm volatile(
+                        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem + slot * 128),
+                        "l"(ad), "l"(bd), "r"(kIdS), "r"(kk > 0 ? 1u : 0u));
+                }
+                commit(s_full + 8 * slot);
+            }
+            __syncwarp();
+        };
+        auto weigh = [&](int q, int slot, int s, bool first) {   // O[q] += P[slot] V[s]
+            fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kTileT / 16; ++kk) {
+                    const uint64_t bd = operand(smb + C::oV + s * C::KT + (kk >> 2) * (D * 128) + (kk & 3) * 256);
+                    asm volatile(
+                        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem + 256 + q * 128),
+                        "r"(tmem + slot * 128 + kk * 8), "l"(bd), "r"(kIdO), "r"(first && kk == 0 ? 0u : 1u));
+                }
+                commit(pv_done + 8 * q);
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t b) {
+            if (elect_one()) commit(b);
+            __syncwarp();
+        };
+        bool ok = true;
+        auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && tc_wait(b, parity, &abort_sh, p.status); };
+        for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x, ++ni) {
+            const Item it = item(idx);
+            for (int q = 0; q < NQ; ++q) wait(q_full + 8 * q, ni & 1);
+            wait(k_full + 8 * (k & 1), (k >> 1) & 1);
+            if (ok) {
+                issued = true;
+                if constexpr (NQ == 2) {
+                    score(0, 0, k & 1);
+                    score(1, 1, k & 1);
+                } else {
+                    score(0, k & 1, k & 1);
+                }
+                release(k_empty + 8 * (k & 1));
+            }
+            for (int i = 0; i < it.n; ++i, ++k) {
+                const int s = k & 1, s2 = s ^ 1;
+                const bool more = i + 1 < it.n;
+                if constexpr (NQ == 1) {
+                    if (more) {                          // the next scores during this softmax
+                        wait(k_full + 8 * s2, ((k + 1) >> 1) & 1);
+                        if (ok) {
+                            score(0, s2, s2);
+                            release(k_empty + 8 * s2);
+                        }
+                    }
+                    wait(v_full + 8 * s, (k >> 1) & 1);
+                    wait(p_full + 8 * s, (k >> 1) & 1);
+                    if (ok) {
+                        weigh(0, s, s, i == 0);
+                        release(v_empty + 8 * s);
+                    }
+                } else {
+                    wait(v_full + 8 * s, (k >> 1) & 1);
+                    wait(p_full, k & 1);
+                    if (ok) weigh(0, 0, s, i == 0);
+                    if (more) {
+                        wait(k_full + 8 * s2, ((k + 1) >> 1) & 1);
+                        if (ok) score(0, 0, s2);
+                    }
+                    wait(p_full + 8, k & 1);
+                    if (ok) {
+                        weigh(1, 1, s, i == 0);
+                        release(v_empty + 8 * s);
+                        if (more) {
+                            score(1, 1, s2);
+                            release(k_empty + 8 * s2);
+                        }
+                    }
+                }
+            }
+        }
+        if (issued) {                                    // every product ends before TMEM is freed
+            release(all_done);
+            if (lane == 0) mbar_wait_bounded(all_done, 0, kA16DrainLimit);
+            __syncwarp();
+        }
+    } else if (warp < C::WSM) {
+        // ------------------------------------------------ softmax: a thread a row
+        const int q = warp >> 2, wq = warp & 3, row = q * 128 + wq * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+        const uint32_t o_at = tmem + lanes + 256 + q * 128;
+        int k = 0;
+        bool ok = true;
+        float f = 0.0f;                                  // the row's factor
+        for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
+            const Item it = item(idx);
+            const int rows = it.q.n * ge.g, r0 = it.rt * RU;
+            // queries: eight lanes a row, rotated, as fp16 with the row's largest
+            // value in [2^13, 2^14), eight columns in the keys' order
+            const int mine = min(32, max(0, rows - (r0 + q * 128 + wq * 32)));     // rows of this warp
+#pragma unroll 1
+            for (int g4 = 0; g4 < 32; g4 += 4) {
+                constexpr int N = D / 8;
+                const int rr = g4 + lane / 8, l8 = lane & 7;
+                const int i = r0 + q * 128 + wq * 32 + rr;
+                float v[N];
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[e] = 0.0f;
+                if (g4 < mine) {                         // (a warp's empty rows are zeros)
+                    if (rr < mine) {
+                        const uint16_t *src = p.a.Q + static_cast<int64_t>(it.q.start + i / ge.g) * p.a.ldq +
+                                              static_cast<int64_t>(it.h * ge.g + i % ge.g) * D + l8 * N;
+#pragma unroll
+                        for (int e = 0; e < N; e += 8) {
+                            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + e));
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                v[e + 2 * c] = __uint_as_float(w[c] << 16);
+                                v[e + 2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u);
+                            }
+                        }
+                    }
+                    turn_row<N>(v);
+                }
+                float mx = 0.0f;
+#pragma unroll
+                for (int e = 0; e < N; ++e) mx = fmaxf(mx, fabsf(v[e]));
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const int ke = mx > 0.0f ? min(13 - (static_cast<int>(__float_as_uint(mx) >> 23) - 127), 126) : 0;
+                const float up = pow2i(ke);
+                const int r = wq * 32 + rr;
+                const float rf = __shfl_sync(0xffffffffu, p.a.scale * kLog2eT * pow2i(-ke), (lane & 3) * 8);
+                if ((lane & ~3) == g4) f = rf;           // lane's row is lane
+                unsigned char *dst = sm + C::oQ + q * C::KT + ((r >> 3) << 10) + (r & 7) * 16;
+#pragma unroll
+                for (int e = 0; e < N; e += 8) {
+                    const uint4 o = make_uint4(half2_bits(v[e] * up, v[e + 4] * up), half2_bits(v[e + 1] * up, v[e + 5] * up),
+                                               half2_bits(v[e + 2] * up, v[e + 6] * up), half2_bits(v[e + 3] * up, v[e + 7] * up));
+                    const int ch = (l8 * N + e) / 8;
+                    *reinterpret_cast<uint4 *>(dst + (ch >> 3) * PAN + (ch & 7) * 128) = o;
+                }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) arrive(q_full + 8 * q);
+            int rlo = 0, rhi = 0;
+            const bool is = r0 + row < rows;
+            if (is) row_range(ge, it.q, (r0 + row) / ge.g, rlo, rhi);
+            const int wlo = __reduce_max_sync(0xffffffffu, is ? rlo : 0), whi = __reduce_min_sync(0xffffffffu, is ? rhi : 0x7fffffff);
+            float m = kNoneT, l = 0.0f;
+            int E = 0;
+            for (int i = 0; i < it.n; ++i, ++k) {
+                const int slot = NQ == 2 ? q : k & 1;
+                const uint32_t par = NQ == 2 ? k & 1 : (k >> 1) & 1;
+                ok = ok && tc_wait(s_full + 8 * slot, par, &abort_sh, p.status);
+                if (!ok) continue;
+                fence_after();
+                if (mine > 0) {
+                    const uint32_t s_at = tmem + lanes + slot * 128;
+                    const Info i0 = kv_info[k & 3][0], i1 = kv_info[k & 3][1];
+                    const uint32_t there = i0.there | (i1.there << kBlocks);
+                    const float F0 = f * i0.kx, F1 = f * i1.kx;
+                    const bool edge = !(there == (1u << 2 * kBlocks) - 1 && i0.at >= wlo && i0.at + kTileT <= whi);
+                    // E: an exponent that no value's scale passes (4 times the
+                    // first ones', so that it is seldom raised)
+                    const int evm = max(i0.ev, i1.ev), E0 = E;
+                    const bool newE = i == 0 || evm > E;
+                    if (newE) E = evm == kNoE ? -126 : evm + 2;
+                    const int e0 = i0.ev == kNoE ? E : i0.ev, e1 = i1.ev == kNoE ? E : i1.ev;
+                    const float d0 = static_cast<float>(e0 - E), d1 = static_cast<float>(e1 - E);
+                    uint32_t pk[64];
+                    float sum[2];
+                    auto masked = [&](int c, uint32_t (&v)[32]) {        // what the row does not see
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int pos = i0.at + 32 * c + e;
+                            if (pos < rlo || pos >= rhi || !((there >> ((32 * c + e) / kKvBlock)) & 1u))
+                                v[e] = 0xFF800000u;
+                        }
+                    };
+                    auto weights = [&]() {       // of all 128; the largest exponent above the running maximum
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float F = h ? F1 : F0, dh = h ? d1 : d0, dm = dh - m;
+                            float s0 = 0.0f, s1 = 0.0f, th = -INFINITY;
+#pragma unroll
+                            for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                                uint32_t v[32];
+                                t_ld32(s_at + 32 * c, v);
+                                if (edge) masked(c, v);
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float x0 = fmaf(__uint_as_float(v[e]), F, dm), x1 = fmaf(__uint_as_float(v[e + 1]), F, dm);
+                                    th = fmaxf(th, fmaxf(x0, x1));
+                                    const float w0 = ex2(x0), w1 = ex2(x1);
+                                    s0 += w0;
+                                    s1 += w1;
+                                    pk[16 * c + e / 2] = half2_bits(w0, w1);
+                                }
+                            }
+                            sum[h] = s0 + s1;
+                            top = fmaxf(top, th - dh);
+                        }
+                        return top;
+                    };
+                    float top = INFINITY;
+                    if (i > 0) top = weights();
+                    if (__any_sync(0xffffffffu, newE || top > kSlackT)) {
+                        float t = -INFINITY;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t v[32];
+                            t_ld32(s_at + 32 * c, v);
+                            if (edge) masked(c, v);
+                            float tc = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) tc = fmaxf(tc, __uint_as_float(v[e]));
+                            t = fmaxf(t, tc * (c < 2 ? F0 : F1));
+                        }
+                        const float to = fmaxf(m, t), fix = ex2(m - to);
+                        m = to;
+                        l *= fix;
+                        if (i > 0) {
+                            if constexpr (NQ == 1) ok = tc_wait(pv_done, (k - 1) & 1, &abort_sh, p.status);
+                            fence_after();
+                            const float of = fix * pow2i(E0 - E);
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t v[32];
+                                t_ld32(o_at + 32 * c, v);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * of);
+                                t_st32(o_at + 32 * c, v);
+                            }
+                            t_wait_st();
+                        }
+                        weights();
+                    }
+                    l = fmaf(sum[0], pow2i(E - e0), fmaf(sum[1], pow2i(E - e1), l));
+                    t_st32(s_at, pk);
+                    t_st32(s_at + 32, pk + 32);
+                    t_wait_st();
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(p_full + 8 * slot);
+            }
+            // the output: O is whole once the last product has ended
+            ok = ok && tc_wait(pv_done + 8 * q, (k - 1) & 1, &abort_sh, p.status);
+            fence_after();
+            if (mine > 0 && ok) {
+                if (it.np > 1) {
+                    const float up = pow2i(E + 10);
+                    if (is) p.stat[static_cast<int64_t>(it.idx) * RU + row] = make_float2(m, l);
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        t_ld32(o_at + 32 * c, v);
+                        float *dst = p.part + (static_cast<int64_t>(it.idx) * RU + row) * D + 32 * c;
+                        if (is)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4 *>(dst + e) =
+                                    make_float4(__uint_as_float(v[e]) * up, __uint_as_float(v[e + 1]) * up,
+                                                __uint_as_float(v[e + 2]) * up, __uint_as_float(v[e + 3]) * up);
+                    }
+                } else {
+                    // turn back: the butterfly over the 32-column pieces, eight
+                    // columns of each at a time, then inside each piece
+                    constexpr int P = D / 32;
+#pragma unroll 1
+                    for (int c = 0; c < 32; c += 8) {
+                        uint32_t v[P][8];
+#pragma unroll
+                        for (int b = 0; b < P; ++b) t_ld8(o_at + 32 * b + c, v[b]);
+                        t_wait_ld();
+#pragma unroll
+                        for (int h = 1; h < P; h <<= 1)
+#pragma unroll
+                            for (int b = 0; b < P; ++b)
+                                if (!(b & h))
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) {
+                                        const float x = __uint_as_float(v[b][e]), y = __uint_as_float(v[b + h][e]);
+                                        v[b][e] = __float_as_uint(x + y);
+                                        v[b + h][e] = __float_as_uint(x - y);
+                                    }
+#pragma unroll
+                        for (int b = 0; b < P; ++b) t_st8(o_at + 32 * b + c, v[b]);
+                        t_wait_st();
+                    }
+                    const float inv = l > 0.0f ? sqrtf(1.0f / D) / l * pow2i(E + 10) : 0.0f;
+                    const int64_t tok = it.q.start + (is ? (r0 + row) / ge.g : 0);
+                    const int hq = it.h * ge.g + (r0 + row) % ge.g;
+                    uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D;
+#pragma unroll 1
+                    for (int c = 0; c < P; ++c) {
+                        uint32_t v[32];
+                        t_ld32(o_at + 32 * c, v);
+#pragma unroll
+                        for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(e & h)) {
+                                    const float x = __uint_as_float(v[e]), y = __uint_as_float(v[e + h]);
+                                    v[e] = __float_as_uint(x + y);
+                                    v[e + h] = __float_as_uint(x - y);
+                                }
+                        if (!is) continue;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = l > 0.0f ? bf16_bits2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv) : 0u;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<uint4 *>(dst + 32 * c + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                    }
+                    if (is && p.a.lse)
+                        p.a.lse[tok * p.a.heads_q + hq] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                }
+            }
+            fence_before();
+        }
+    }
+    zero_rows<D>(kv, p.a, ge);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == C::W_MMA)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+}
+
+// Joins the parts of row tiles that were cut: a warp a row.
+template <int D>
+__global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ TcParams p) {
+    constexpr int E = D / 32;
+    __shared__ int list[kMaxItems / 2], n_sh;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int items = min(*p.head, kMaxItems);
+    if (items == 0) return;
+    if (warp == 0) {                             // the row tiles that were cut, in order
+        int n = 0;
+        for (int base = 0; base < items; base += 32) {
+            const bool cut = base + lane < items && p.table[base + lane].np > 1;
+            const unsigned in = __ballot_sync(0xffffffffu, cut);
+            if (cut) list[n + __popc(in & ((1u << lane) - 1))] = base + lane;
+            n += __popc(in);
+        }
+        if (lane == 0) n_sh = n;
+    }
+    __syncthreads();
+    const int ru = p.geo.rows, g = p.geo.g, work = n_sh * ru;
+    for (int w = blockIdx.x * (kThreads / 32) + warp; w < work; w += gridDim.x * (kThreads / 32)) {
+        const int idx = list[w / ru], i = w % ru;
+        const Split sp = p.table[idx];
+        if (sp.rt * ru + i >= sp.rows) continue;
+        const float2 *st = p.stat + static_cast<int64_t>(idx) * ru + i;
+        const float *src = p.part + (static_cast<int64_t>(idx) * ru + i) * D + lane * E;
+        const int64_t so = ru, po = static_cast<int64_t>(ru) * D;
+        float mx = kNoneT;
+        for (int k = lane; k < sp.np; k += 32) mx = fmaxf(mx, st[k * so].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float sum = 0.0f, v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < sp.np; ++k) {
+            const float2 t = st[k * so];
+            const float f = ex2(t.x - mx);
+            sum = fmaf(f, t.y, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = fmaf(f, src[k * po + e], v[e]);
+        }
+        warp_fwht<E, float>(v);
+        const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
+        const int row = sp.rt * ru + i;
+        const int64_t tok = sp.start + row / g;
+        const int hq = sp.h * g + row % g;
+        uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + lane * E;
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) o[e] = sum > 0.0f ? bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+        if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(o[0], o[1]);
+        else *reinterpret_cast<uint32_t *>(dst) = o[0];
+        if (p.a.lse && lane == 0)
+            p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    }
+}
+
+constexpr int kMaxRU = 256, kMaxD = 128;
+
+template <class C>
+tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
+    const int grid = dev.sms < kMaxSmsT ? dev.sms : kMaxSmsT;
+    const size_t slots = kMaxItems;
+    unsigned char *at = static_cast<unsigned char *>(ws);
+    p.head = reinterpret_cast<int *>(at);
+    p.table = reinterpret_cast<Split *>(at + 256);
+    p.stat = reinterpret_cast<float2 *>(at + 256 + slots * sizeof(Split));
+    p.part = reinterpret_cast<float *>(at + 256 + slots * (sizeof(Split) + kMaxRU * sizeof(float2)));
+    p.geo.rows = C::RU;
+    const int64_t units = p.kv.nseq * p.kv.heads * ((p.a.max_q * p.geo.g + C::RU - 1) / C::RU);
+    p.split = units <= grid;
+    const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn_tc<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (fe != cudaSuccess) return cuda_fail(fe);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(C::NT);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn_tc<C>, p);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (!p.split) return TQ_OK;
+    cfg.gridDim = dim3(grid * 4);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, k_kv4_join<C::D>, p);
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+size_t kv4_tc_workspace_bytes(const DeviceInfo &dev) {
+    (void)dev;
+    const size_t slots = kMaxItems;
+    return 256 + slots * (sizeof(Split) + kMaxRU * (sizeof(float2) + kMaxD * sizeof(float)));
+}
+
+bool kv4_tc_takes(const tq_kv4 &kv, const Kv4Attn &a, int64_t rows) {
+    (void)a;
+    return kv.dim <= kMaxD && kv.nseq <= kMaxSeqsT && rows > 16;
+}
+
+tq_status launch_kv4_attention_tc(const tq_kv4 &kv, const Kv4Attn &a, void *ws, const DeviceInfo &dev, cudaStream_t s) {
+    TcParams p = {};
+    p.kv = kv;
+    p.a = a;
+    p.geo.g = a.heads_q / kv.heads;
+    p.geo.causal = a.causal;
+    p.geo.window = a.window;
+    p.status = status_word();
+    if (!p.status) return TQ_ERR_DEVICE;
+    const bool two = a.max_q * p.geo.g > 128;
+    if (kv.dim == 64) return two ? launch<TCfg<64, 2>>(p, ws, dev, s) : launch<TCfg<64, 1>>(p, ws, dev, s);
+    return two ? launch<TCfg<128, 2>>(p, ws, dev, s) : launch<TCfg<128, 1>>(p, ws, dev, s);
+}
+
+}  // namespace tq

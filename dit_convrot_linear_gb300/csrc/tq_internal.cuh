@@ -187,6 +187,12 @@ struct Kv4Attn {
     void *ws;
 };
 tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceInfo &dev, cudaStream_t s);
+// Its form for many query rows a key/value head, on tcgen05 (`rows`: of the
+// longest sequence and one head); ws: its part of the workspace.
+bool kv4_tc_takes(const tq_kv4 &kv, const Kv4Attn &a, int64_t rows);
+size_t kv4_tc_workspace_bytes(const DeviceInfo &dev);
+tq_status launch_kv4_attention_tc(const tq_kv4 &kv, const Kv4Attn &a, void *ws, const DeviceInfo &dev,
+                                  cudaStream_t s);
 
 tq_status launch_gemm_a8_tiled(const void *At, const float *sx, int64_t M, int64_t K,
                                const uint8_t *Wq, const float *sw, int64_t N, int bits,

@@ -64,4 +64,130 @@ __device__ __forceinline__ unsigned char *kv_block(const tq_kv4 &kv, int page, i
            (slot / kKvBlock) * kv_block_bytes(kv.dim);
 }
 
+struct Geo {                                 // what the cutting of a batch depends on
+    int g, causal, rows;                     // query heads a key/value head, mask, rows a row tile
+    int64_t window;
+};
+
+struct Run {                                 // one row tile of one key/value head (at most 64 bytes)
+    int b, h, rt;
+    KvSeq q;
+    int nrt;                                 // row tiles of the sequence
+    int lo, hi, t0, cost;                    // positions its rows see, first tile, tiles (0: they see nothing)
+};
+
+// A row tile's positions and tiles of TILE positions.
+template <int TILE>
+__device__ __forceinline__ void range_of(const Geo &ge, const KvSeq &q, int rt, int &lo, int &hi, int &t0, int &cost) {
+    const int rows = q.n * ge.g, r0 = rt * ge.rows;
+    const int i0 = r0 / ge.g, i1 = (min(r0 + ge.rows, rows) - 1) / ge.g;
+    const int p1 = q.len - q.n + i1;
+    hi = p1 < 0 ? 0 : ge.causal ? min(p1 + 1, q.len) : q.len;
+    const int64_t from = static_cast<int64_t>(q.len) - q.n + i0 - ge.window + 1;
+    lo = ge.window > 0 && from > 0 ? static_cast<int>(from < hi ? from : hi) : 0;
+    t0 = lo / TILE;
+    cost = (hi + TILE - 1) / TILE - t0;
+}
+
+// Positions that row i of a sequence sees.
+__device__ __forceinline__ void row_range(const Geo &ge, const KvSeq &q, int i, int &lo, int &hi) {
+    const int pos = q.len - q.n + i;
+    hi = pos < 0 ? 0 : ge.causal ? min(pos + 1, q.len) : q.len;
+    const int64_t from = static_cast<int64_t>(pos) - ge.window + 1;
+    lo = ge.window > 0 && from > 0 ? static_cast<int>(from < hi ? from : hi) : 0;
+}
+
+__device__ __forceinline__ int row_tiles(const Geo &ge, const KvSeq &q) {
+    return (q.n * ge.g + ge.rows - 1) / ge.rows;
+}
+
+// The transform of a row held by eight neighbouring lanes, V neighbouring values
+// each, scaled by sqrt(1 / (8 V)).
+template <int V>
+__device__ __forceinline__ void turn_row(float (&v)[V]) {
+#pragma unroll
+    for (int h = 1; h < V; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (!(i & h)) {
+                const float a = v[i], b = v[i + h];
+                v[i] = a + b;
+                v[i + h] = a - b;
+            }
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) {
+        const float sg = (lane & m) ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = fmaf(sg, v[i], __shfl_xor_sync(0xffffffffu, v[i], m));
+    }
+    const float c = sqrtf(1.0f / (8 * V));
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] *= c;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+__device__ __forceinline__ uint32_t bf16_bits2(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// 2^k as fp32, k clamped to the normal range
+__device__ __forceinline__ float pow2i(int k) {
+    return __uint_as_float(static_cast<uint32_t>(min(max(k, -126), 127) + 127) << 23);
+}
+
+// a / b for a, b > 0: in 32 bits where they fit
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
+// Zeros for the row tiles that see nothing (rows before position 0), a
+// sequence a CTA.
+template <int D>
+__device__ __noinline__ static void zero_rows(const tq_kv4 &kv, const Kv4Attn &a, const Geo &ge) {
+    for (int64_t b = blockIdx.x; b < kv.nseq; b += gridDim.x) {
+        bool bad = false;
+        const KvSeq q = kv_seq(kv, b, bad);
+        const int none = q.n - q.len;        // rows before position 0
+        if (none <= 0) continue;
+        const int rows = q.n * ge.g, cut = q.len == 0 ? rows : none * ge.g / ge.rows * ge.rows;
+        const int64_t pieces = static_cast<int64_t>(cut) * kv.heads * (D / 8);
+        for (int64_t i = threadIdx.x; i < pieces; i += blockDim.x) {
+            const int c = static_cast<int>(i % (D / 8));
+            const int64_t k = i / (D / 8);
+            const int row = static_cast<int>(k % cut), h = static_cast<int>(k / cut);
+            const int64_t tok = q.start + row / ge.g;
+            const int hq = h * ge.g + row % ge.g;
+            *reinterpret_cast<uint4 *>(a.O + tok * a.ldo + static_cast<int64_t>(hq) * D + c * 8) = make_uint4(0, 0, 0, 0);
+            if (a.lse && c == 0) a.lse[tok * a.heads_q + hq] = -INFINITY;
+        }
+    }
+}
+
 }  // namespace tq
