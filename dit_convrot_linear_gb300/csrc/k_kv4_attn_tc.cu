@@ -8,10 +8,10 @@
 // head) against tiles of 128 positions:
 //
 //   - a loader warp copies blocks of 16 tokens into a ring;
-//   - four warps widen them to fp16 operands in shared memory: a nibble masked
-//     out of a word is the fp16 subnormal u 2^-24, one fused multiply-add with
-//     (s, -8 s) makes it s (u - 8), s the token's scale over a power of two of
-//     the tile's largest.  Keys are the K-major rows of S = Q K^T; values, whose
+//   - four warps widen them to fp16 operands in shared memory, 32 positions of a
+//     tile each, without a word between them: a nibble masked out of a word is
+//     the fp16 subnormal u 2^-24, one fused multiply-add with (s, -8 s) makes it
+//     s (u - 8), s the token's scale over a power of two of the largest of the 32.  Keys are the K-major rows of S = Q K^T; values, whose
 //     words hold two tokens, are the K-major rows of O = P V as they come;
 //   - one thread issues the products: S into TMEM (128 columns a row tile), P
 //     (fp16, over S's columns) times V into O, also in TMEM.  With two row tiles
@@ -47,7 +47,9 @@ constexpr int kMaxSeqsT = 256;               // sequences the cutting holds in s
 constexpr int kNoE = -1024;                  // exponent of a half whose values are all zero
 constexpr int kCols = 512;                   // TMEM columns
 constexpr int kMaxSmsT = 160;                // more SMs than this stay unused
-constexpr int kMaxItems = 2 * kMaxSmsT;      // parts of a call whose row tiles are cut
+constexpr int kMaxItems = 640;               // parts of a call whose row tiles are cut (of one 128-row tile; half as many of two)
+constexpr int kMaxParts = 64;                // of one row tile
+constexpr float kPartTiles = 4.0f;           // tiles that a part's start and end stand for
 
 template <int D_, int NQ_>
 struct TCfg {
@@ -64,6 +66,9 @@ struct TCfg {
     static constexpr int USED = oBar + 32 * 8;
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;       // one CTA an SM: it takes all of TMEM
 };
+
+template <class C>
+constexpr int kMaxItemsOf() { return kMaxItems * 128 / C::RU; }
 
 struct Item {                                // a part of a row tile
     int idx, np, t0, n, lo, hi;              // its number; parts of its row tile; tiles; positions of the row tile
@@ -181,6 +186,16 @@ __device__ __forceinline__ uint32_t hmul2_(uint32_t a, uint32_t b) {
     return d;
 }
 
+__device__ __forceinline__ unsigned long long pair2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void split2(unsigned long long r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+
 constexpr uint32_t kMinus8 = 0x80088008u;    // -8 2^-24 twice
 constexpr uint32_t kSixteenth = 0x2C002C00u; // 1/16 twice
 
@@ -194,15 +209,13 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
     __shared__ int64_t per_sh;
     __shared__ int item_sh[kMaxSeqsT], before_sh[kMaxSeqsT];
     __shared__ KvSeq seq_sh[kMaxSeqsT];
-    __shared__ float max_sh[2][4][2];
-    __shared__ __align__(16) __half sv_sh[kHalf];
-    struct Info {                            // of a half: blocks that are there; 2^(e + 10) of the keys, exponent of the values
-        int at;
+    struct Info {                            // of 32 positions: blocks that are there; 2^(e + 10) of the keys, exponent of the values
         uint32_t there;
         float kx;
         int ev;
     };
-    __shared__ Info raw_info[kRing], kv_info[4][2];
+    __shared__ uint32_t raw_there[kRing];
+    __shared__ Info kv_info[4][4];
     int64_t *cost_sh = reinterpret_cast<int64_t *>(sm);      // before any operand
     int *unit_sh = reinterpret_cast<int *>(sm + kMaxSeqsT * 8);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -220,12 +233,12 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         };
         for (int i = 0; i < kRing; ++i) {
             init(raw_full + 8 * i, 1);
-            init(raw_empty + 8 * i, 4);
+            init(raw_empty + 8 * i, 2);
         }
         for (int i = 0; i < 2; ++i) {
-            init(k_full + 8 * i, 8);             // four warps, two halves
+            init(k_full + 8 * i, 4);
             init(k_empty + 8 * i, 1);
-            init(v_full + 8 * i, 8);
+            init(v_full + 8 * i, 4);
             init(v_empty + 8 * i, 1);
             init(s_full + 8 * i, 1);
             init(p_full + 8 * i, 4);
@@ -282,16 +295,42 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
             units += __shfl_xor_sync(0xffffffffu, units, o);
         }
+        // Into how many parts: what makes the rounds over the SMs, each as long
+        // as a part of a row tile of mean length and its start and end, shortest.
+        units *= kv.heads;
+        float best = FLT_MAX;
+        int parts = 1;
+        const float mean = units ? static_cast<float>(sum * kv.heads) / static_cast<float>(units) : 0.0f;
+        if (p.split && units > 0 && units <= kMaxItemsOf<C>() / 2)
+            for (int n = 1 + lane; n <= kMaxParts; n += 32) {
+                const int64_t rounds = (units * n + gridDim.x - 1) / gridDim.x;
+                const float t = static_cast<float>(rounds) * (mean / static_cast<float>(n) + kPartTiles);
+                if (units * n * 5 / 4 + 8 <= kMaxItemsOf<C>() && mean >= n * kMinPart && t < best) {
+                    best = t;
+                    parts = n;
+                }
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float b2 = __shfl_xor_sync(0xffffffffu, best, o);
+            const int n2 = __shfl_xor_sync(0xffffffffu, parts, o);
+            if (b2 < best || (b2 == best && n2 < parts)) {
+                best = b2;
+                parts = n2;
+            }
+        }
         if (lane == 0) {
-            const int64_t per = quotient(sum * kv.heads + gridDim.x, gridDim.x);
-            per_sh = per < kMinPart ? kMinPart : per;
-            split_sh = p.split && units * kv.heads <= gridDim.x;
+            per_sh = parts > 1 ? static_cast<int64_t>(mean / static_cast<float>(parts)) : 0;
+            split_sh = parts > 1;
         }
     }
     __syncthreads();
     const int64_t per = per_sh;
-    const bool split = split_sh != 0;
-    auto parts_of = [&](int cost) { return cost == 0 ? 0 : !split || cost < per ? 1 : static_cast<int>(quotient(cost, per)); };
+    bool split = split_sh != 0;
+    auto parts_of = [&](int cost) {
+        return cost == 0 ? 0 : !split || cost < 2 * per ? 1 : static_cast<int>(quotient(cost + per / 2, per));
+    };
+    for (int again = 0; again < 2; ++again) {    // a second time without parts where they are too many
     for (int i = warp; i < nseq; i += C::NT / 32) {
         const KvSeq q = seq_sh[i];
         const int nrt = row_tiles(ge, q);
@@ -318,11 +357,13 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
             if (base + lane < nseq) before_sh[base + lane] = run + x - v;
             run += __shfl_sync(0xffffffffu, x, 31);
         }
-        if (lane == 0) {
-            n_items_sh = run;
-            if (blockIdx.x == 0 && p.split) *p.head = split ? run : 0;
-        }
+        if (lane == 0) n_items_sh = run;
     }
+    __syncthreads();
+    if (!split || n_items_sh <= kMaxItemsOf<C>()) break;
+    split = false;
+    }
+    if (tid == 0 && blockIdx.x == 0 && p.split) *p.head = split ? n_items_sh : 0;
     fence_before();
     __syncthreads();
     fence_after();
@@ -401,8 +442,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 const uint32_t there = __ballot_sync(0xffffffffu, num != 0) & ((1u << kBlocks) - 1);
                 if (!tc_wait(raw_empty + 8 * s, ((k / kRing) & 1) ^ 1, &abort_sh, p.status)) continue;
                 if (lane == 0) {
-                    raw_info[s].at = at;
-                    raw_info[s].there = there;
+                    raw_there[s] = there;
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(raw_full + 8 * s),
                                  "r"(static_cast<uint32_t>(__popc(there)) * C::BLK)
                                  : "memory");
@@ -423,54 +463,39 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         __syncwarp();
     } else if (warp >= C::W_DQ && warp < C::W_DQ + 4) {
         // ------------------------------------------------ widening
-        const int t = tid - C::W_DQ * 32, dw = warp - C::W_DQ;
-        const int tok = t & (kHalf - 1), part = t / kHalf;       // this thread's token, and which half of its key row
-        int k = 0;                                               // halves
+        const int dw = warp - C::W_DQ;                           // positions 32 dw .. of each tile
+        int k = 0;
         for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
             const Item it = item(idx);
-            for (int i = 0; i < 2 * it.n; ++i, ++k) {
-                const int rs = k % kRing, s = (k >> 1) & 1, half = k & 1;
-                const uint32_t par = ((k >> 2) & 1) ^ 1;
-                const bool ok = tc_wait(raw_full + 8 * rs, (k / kRing) & 1, &abort_sh, p.status);
-                const unsigned char *raw = sm + C::oRaw + rs * C::RAW;
-                const int at = raw_info[rs].at;
-                const uint32_t there = raw_info[rs].there;
-                // the token's scales, and the half's largest
-                const unsigned char *blk = raw + (tok / kKvBlock) * C::BLK;
-                const int pos = at + tok, row = tok % kKvBlock;
-                const bool is = ok && ((there >> (tok / kKvBlock)) & 1u) && pos >= it.lo && pos < it.hi;
+            for (int i = 0; i < it.n; ++i, ++k) {
+                const int kh = 2 * k + (dw >> 1), rs = kh % kRing, s = k & 1;
+                const uint32_t par = ((k >> 1) & 1) ^ 1;
+                const bool ok = tc_wait(raw_full + 8 * rs, (kh / kRing) & 1, &abort_sh, p.status);
+                const unsigned char *raw = sm + C::oRaw + rs * C::RAW + (dw & 1) * 2 * C::BLK;
+                const uint32_t there = (raw_there[rs] >> (2 * (dw & 1))) & 3u;
+                // a lane a token: its scales, and the largest
+                const unsigned char *blk = raw + (lane / kKvBlock) * C::BLK;
+                const int pos = (it.t0 + i) * kTileT + 32 * dw + lane, row = lane % kKvBlock;
+                const bool is = ok && ((there >> (lane / kKvBlock)) & 1u) && pos >= it.lo && pos < it.hi;
                 const float *sc = reinterpret_cast<const float *>(blk + 16 * D);
                 const float sk = is ? sc[row] : 0.0f, sv = is ? sc[16 + row] : 0.0f;
-                float mk = sk, mv = sv;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-                    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-                }
-                if (lane == 0) {
-                    max_sh[half][dw][0] = mk;
-                    max_sh[half][dw][1] = mv;
-                }
-                asm volatile("bar.sync 2, 128;" ::: "memory");
-                mk = fmaxf(max_sh[half][0][0], max_sh[half][1][0]);
-                mv = fmaxf(max_sh[half][0][1], max_sh[half][1][1]);
-                const int ek = mk > 0.0f ? static_cast<int>(__float_as_uint(mk) >> 23) - 127 : 0;
-                const int ev = mv > 0.0f ? static_cast<int>(__float_as_uint(mv) >> 23) - 127 : kNoE;
+                const uint32_t mk = __reduce_max_sync(0xffffffffu, __float_as_uint(sk)) >> 23;   // scales are not negative
+                const uint32_t mv = __reduce_max_sync(0xffffffffu, __float_as_uint(sv)) >> 23;
+                const int ek = mk ? static_cast<int>(mk) - 127 : 0, ev = mv ? static_cast<int>(mv) - 127 : kNoE;
                 // scales over the power of two of the largest, times 2^14
-                const float fk = sk * pow2i(-ek) * 16384.0f, fv = sv * pow2i(-ev) * 16384.0f;
-                if (part == 0) sv_sh[tok] = __float2half_rn(fv);
+                const __half hk = __float2half_rn(sk * pow2i(-ek) * 16384.0f), hv = __float2half_rn(sv * pow2i(-ev) * 16384.0f);
                 // keys: 8 nibbles to 16 bytes in the order (0, 4), (1, 5), (2, 6), (3, 7)
-                if (tc_wait(k_empty + 8 * s, par, &abort_sh, p.status) && ok) {
-                    if (t == 0) kv_info[(k >> 1) & 3][half] = {at, there, pow2i(ek + 10), ev};
-                    const __half2 h2 = __half2half2(__float2half_rn(fk));
+                const bool kok = tc_wait(k_empty + 8 * s, par, &abort_sh, p.status) && ok;
+                if (kok) {
+                    if (lane == 0) kv_info[k & 3][dw] = {there, pow2i(ek + 10), ev};
+                    const __half2 h2 = __half2half2(hk);
                     const uint32_t s1 = *reinterpret_cast<const uint32_t *>(&h2);
                     const uint32_t s16 = hmul2_(s1, kSixteenth), b = hmul2_(s1, kMinus8);
-                    const int r = half * kHalf + tok;
+                    const int r = 32 * dw + lane;
                     unsigned char *dst = sm + C::oK + s * C::KT + ((r >> 3) << 10) + (r & 7) * 16;
                     const uint4 *src = reinterpret_cast<const uint4 *>(blk + row * (D / 2));
 #pragma unroll
-                    for (int c0 = 0; c0 < D / 64; ++c0) {
-                        const int c = part * (D / 64) + c0;
+                    for (int c = 0; c < D / 32; ++c) {
                         const uint4 x4 = src[c];
                         const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
@@ -486,25 +511,24 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     __syncwarp();
                     if (lane == 0) arrive(k_full + 8 * s);
                 }
-                asm volatile("bar.sync 2, 128;" ::: "memory");
-                // values: a thread a column, eight tokens at a time: its nibble of
+                // values: a lane a column, eight tokens at a time: its nibble of
                 // four words, each two tokens
                 if (tc_wait(v_empty + 8 * s, par, &abort_sh, p.status) && ok) {
                     const int sh = (lane & 2) * 4;               // nibbles 2 and 3 are 8 bits up
                     const uint32_t mask = lane & 1 ? 0x00F000F0u : 0x000F000Fu;
+                    const uint32_t own = __half_as_ushort(hv);
+                    const uint32_t two = own | (__shfl_down_sync(0xffffffffu, own, 1) << 16);    // of even lanes
 #pragma unroll
-                    for (int o2 = 0; o2 < 2; ++o2) {
-                        const int o = dw + 4 * o2;
-                        const uint4 sc4 = *reinterpret_cast<const uint4 *>(sv_sh + 8 * o);
-                        const uint32_t s1[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
+                    for (int o = 0; o < 4; ++o) {
                         uint32_t sx[4], b[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            b[q] = hmul2_(s1[q], kMinus8);
-                            sx[q] = lane & 1 ? hmul2_(s1[q], kSixteenth) : s1[q];
+                            const uint32_t s1 = __shfl_sync(0xffffffffu, two, 8 * o + 2 * q);
+                            b[q] = hmul2_(s1, kMinus8);
+                            sx[q] = lane & 1 ? hmul2_(s1, kSixteenth) : s1;
                         }
                         const unsigned char *vb = raw + (o >> 1) * C::BLK + 8 * D + (o & 1) * 4 * D;
-                        unsigned char *dst = sm + C::oV + s * C::KT + half * (D * 128) + o * 128;
+                        unsigned char *dst = sm + C::oV + s * C::KT + (dw >> 1) * (D * 128) + (4 * (dw & 1) + o) * 128;
 #pragma unroll
                         for (int d0 = 0; d0 < D; d0 += 32) {
                             const int d = d0 + lane;
@@ -700,50 +724,63 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 fence_after();
                 if (mine > 0) {
                     const uint32_t s_at = tmem + lanes + slot * 128;
-                    const Info i0 = kv_info[k & 3][0], i1 = kv_info[k & 3][1];
-                    const uint32_t there = i0.there | (i1.there << kBlocks);
-                    const float F0 = f * i0.kx, F1 = f * i1.kx;
-                    const bool edge = !(there == (1u << 2 * kBlocks) - 1 && i0.at >= wlo && i0.at + kTileT <= whi);
+                    const int at = (it.t0 + i) * kTileT;
+                    uint32_t there = 0;
+                    float F[4];
+                    int ev[4], evm = kNoE;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const Info in = kv_info[k & 3][c];
+                        there |= in.there << (2 * c);
+                        F[c] = f * in.kx;
+                        ev[c] = in.ev;
+                        evm = max(evm, in.ev);
+                    }
+                    const bool edge = !(there == 0xFFu && at >= wlo && at + kTileT <= whi);
                     // E: an exponent that no value's scale passes (4 times the
                     // first ones', so that it is seldom raised)
-                    const int evm = max(i0.ev, i1.ev), E0 = E;
+                    const int E0 = E;
                     const bool newE = i == 0 || evm > E;
                     if (newE) E = evm == kNoE ? -126 : evm + 2;
-                    const int e0 = i0.ev == kNoE ? E : i0.ev, e1 = i1.ev == kNoE ? E : i1.ev;
-                    const float d0 = static_cast<float>(e0 - E), d1 = static_cast<float>(e1 - E);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) ev[c] = ev[c] == kNoE ? 0 : max(ev[c] - E, -100);    // <= 0
                     uint32_t pk[64];
-                    float sum[2];
+                    float add = 0.0f;
                     auto masked = [&](int c, uint32_t (&v)[32]) {        // what the row does not see
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const int pos = i0.at + 32 * c + e;
+                            const int pos = at + 32 * c + e;
                             if (pos < rlo || pos >= rhi || !((there >> ((32 * c + e) / kKvBlock)) & 1u))
                                 v[e] = 0xFF800000u;
                         }
                     };
                     auto weights = [&]() {       // of all 128; the largest exponent above the running maximum
                         float top = -INFINITY;
+                        add = 0.0f;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float F = h ? F1 : F0, dh = h ? d1 : d0, dm = dh - m;
-                            float s0 = 0.0f, s1 = 0.0f, th = -INFINITY;
+                        for (int c = 0; c < 4; ++c) {
+                            const float dc = static_cast<float>(ev[c]);
+                            const unsigned long long f2 = pair2(F[c], F[c]), m2 = pair2(dc - m, dc - m);
+                            unsigned long long s2 = pair2(0.0f, 0.0f);
+                            float th = -INFINITY;
+                            uint32_t v[32];
+                            t_ld32(s_at + 32 * c, v);
+                            if (edge) masked(c, v);
 #pragma unroll
-                            for (int c = 2 * h; c < 2 * h + 2; ++c) {
-                                uint32_t v[32];
-                                t_ld32(s_at + 32 * c, v);
-                                if (edge) masked(c, v);
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    const float x0 = fmaf(__uint_as_float(v[e]), F, dm), x1 = fmaf(__uint_as_float(v[e + 1]), F, dm);
-                                    th = fmaxf(th, fmaxf(x0, x1));
-                                    const float w0 = ex2(x0), w1 = ex2(x1);
-                                    s0 += w0;
-                                    s1 += w1;
-                                    pk[16 * c + e / 2] = half2_bits(w0, w1);
-                                }
+                            for (int e = 0; e < 32; e += 2) {
+                                unsigned long long x2;
+                                asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x2) : "l"(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]))), "l"(f2), "l"(m2));
+                                float x0, x1;
+                                split2(x2, x0, x1);
+                                th = fmaxf(th, fmaxf(x0, x1));
+                                const float w0 = ex2(x0), w1 = ex2(x1);
+                                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s2) : "l"(pair2(w0, w1)));
+                                pk[16 * c + e / 2] = half2_bits(w0, w1);
                             }
-                            sum[h] = s0 + s1;
-                            top = fmaxf(top, th - dh);
+                            float s0, s1;
+                            split2(s2, s0, s1);
+                            add = fmaf(s0 + s1, pow2i(-ev[c]), add);
+                            top = fmaxf(top, th - dc);
                         }
                         return top;
                     };
@@ -759,7 +796,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                             float tc = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) tc = fmaxf(tc, __uint_as_float(v[e]));
-                            t = fmaxf(t, tc * (c < 2 ? F0 : F1));
+                            t = fmaxf(t, tc * f * kv_info[k & 3][c].kx);
                         }
                         const float to = fmaxf(m, t), fix = ex2(m - to);
                         m = to;
@@ -780,7 +817,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                         }
                         weights();
                     }
-                    l = fmaf(sum[0], pow2i(E - e0), fmaf(sum[1], pow2i(E - e1), l));
+                    l += add;
                     t_st32(s_at, pk);
                     t_st32(s_at + 32, pk + 32);
                     t_wait_st();
@@ -934,7 +971,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ T
     }
 }
 
-constexpr int kMaxRU = 256, kMaxD = 128;
+constexpr int kMaxD = 128;
 
 template <class C>
 tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
@@ -944,10 +981,10 @@ tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
     p.head = reinterpret_cast<int *>(at);
     p.table = reinterpret_cast<Split *>(at + 256);
     p.stat = reinterpret_cast<float2 *>(at + 256 + slots * sizeof(Split));
-    p.part = reinterpret_cast<float *>(at + 256 + slots * (sizeof(Split) + kMaxRU * sizeof(float2)));
+    p.part = reinterpret_cast<float *>(at + 256 + slots * (sizeof(Split) + 128 * sizeof(float2)));
     p.geo.rows = C::RU;
     const int64_t units = p.kv.nseq * p.kv.heads * ((p.a.max_q * p.geo.g + C::RU - 1) / C::RU);
-    p.split = units <= grid;
+    p.split = units <= kMaxItemsOf<C>() / 2;
     const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn_tc<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (fe != cudaSuccess) return cuda_fail(fe);
     cudaLaunchConfig_t cfg = {};
@@ -975,7 +1012,7 @@ tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
 size_t kv4_tc_workspace_bytes(const DeviceInfo &dev) {
     (void)dev;
     const size_t slots = kMaxItems;
-    return 256 + slots * (sizeof(Split) + kMaxRU * (sizeof(float2) + kMaxD * sizeof(float)));
+    return 256 + slots * (sizeof(Split) + 128 * (sizeof(float2) + kMaxD * sizeof(float)));
 }
 
 bool kv4_tc_takes(const tq_kv4 &kv, const Kv4Attn &a, int64_t rows) {
