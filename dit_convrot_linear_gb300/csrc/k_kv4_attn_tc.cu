@@ -8,18 +8,21 @@
 // head) against tiles of 128 positions:
 //
 //   - a loader warp copies blocks of 16 tokens into a ring;
-//   - four warps widen them to fp16 operands in shared memory, 32 positions of a
-//     tile each, without a word between them: a nibble masked out of a word is
-//     the fp16 subnormal u 2^-24, one fused multiply-add with (s, -8 s) makes it
-//     s (u - 8), s the token's scale over a power of two of the largest of the 32.  Keys are the K-major rows of S = Q K^T; values, whose
+//   - eight warps widen them to fp16 operands in shared memory, a block of a tile
+//     each, without a word between them: a nibble masked out of a word is the
+//     fp16 subnormal u 2^-24, one fused multiply-add with (s, -8 s) makes it
+//     s (u - 8), s the token's scale over a power of two of the block's largest.  Keys are the K-major rows of S = Q K^T; values, whose
 //     words hold two tokens, are the K-major rows of O = P V as they come;
 //   - one thread issues the products: S into TMEM (128 columns a row tile), P
 //     (fp16, over S's columns) times V into O, also in TMEM.  With two row tiles
 //     one's softmax runs during the other's products; with one, S has two places;
-//   - a thread a row does the softmax: its 128 scores come from TMEM, no value
-//     crosses lanes.  It speculates that the running maximum holds (it is raised
-//     only when passed by 2^8) and repeats the tile where it does not; O is then
-//     rescaled in place, which the tensor cores' order of work makes safe.
+//   - a thread a row does the softmax: its 128 scores come from TMEM, twice (the
+//     maximum, then the weights, which go back over them), no value crosses
+//     lanes.  The running maximum is raised only when passed by 2^8; O is then
+//     rescaled in place, which the tensor cores' order of work makes safe.  (One
+//     pass that takes the maximum for granted and repeats itself where it was
+//     not is as much work, but three times the code, which four kinds of warps
+//     then fetch again and again.)
 //
 // Row tiles that are fewer than the SMs are cut along the positions; a second
 // kernel joins their parts, a warp a row, in order (the result does not depend
@@ -56,8 +59,8 @@ struct TCfg {
     static constexpr int D = D_, NQ = NQ_;
     static constexpr int RU = 128 * NQ;                      // query rows a row tile
     static constexpr int WSM = 4 * NQ;                       // softmax warps
-    static constexpr int W_DQ = WSM, W_LD = WSM + 4, W_MMA = WSM + 5;
-    static constexpr int NT = (WSM + 6) * 32;
+    static constexpr int W_DQ = WSM, W_LD = WSM + 8, W_MMA = WSM + 9;
+    static constexpr int NT = (WSM + 10) * 32;
     static constexpr int BLK = kv_block_bytes(D);
     static constexpr int RAW = kBlocks * BLK;
     static constexpr int KT = kTileT * D * 2;                // bytes of a key tile, of a value tile, of a query tile
@@ -148,7 +151,6 @@ __device__ __forceinline__ void t_ld32(uint32_t at, uint32_t (&v)[32]) {
           "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(at));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void t_st32(uint32_t at, const uint32_t *v) {
@@ -157,6 +159,14 @@ __device__ __forceinline__ void t_st32(uint32_t at, const uint32_t *v) {
         "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
         "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
         TQ_R32(v));
+}
+
+__device__ __forceinline__ void t_ld16(uint32_t at, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(at));
 }
 
 __device__ __forceinline__ void t_ld8(uint32_t at, uint32_t *v) {
@@ -170,7 +180,32 @@ __device__ __forceinline__ void t_st8(uint32_t at, const uint32_t *v) {
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
 }
 
-__device__ __forceinline__ void t_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loaded registers are operands of the wait, so that no use of them moves
+// before it.
+__device__ __forceinline__ void t_wait_ld(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                   "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                   "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void t_wait_ld(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void t_wait_ld(uint32_t (&v)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void t_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // d += a b with the fp16 pair (exact but for one rounding)
@@ -209,13 +244,13 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
     __shared__ int64_t per_sh;
     __shared__ int item_sh[kMaxSeqsT], before_sh[kMaxSeqsT];
     __shared__ KvSeq seq_sh[kMaxSeqsT];
-    struct Info {                            // of 32 positions: blocks that are there; 2^(e + 10) of the keys, exponent of the values
-        uint32_t there;
-        float kx;
+    struct __align__(16) Info {              // of a block: 2^(e + 10) of the keys, exponent of the values (read as a
+        float kx;                            // pair: first, at 16 bytes); whether it is there
         int ev;
+        int there, pad;
     };
     __shared__ uint32_t raw_there[kRing];
-    __shared__ Info kv_info[4][4];
+    __shared__ Info kv_info[4][8];
     int64_t *cost_sh = reinterpret_cast<int64_t *>(sm);      // before any operand
     int *unit_sh = reinterpret_cast<int *>(sm + kMaxSeqsT * 8);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -233,12 +268,12 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         };
         for (int i = 0; i < kRing; ++i) {
             init(raw_full + 8 * i, 1);
-            init(raw_empty + 8 * i, 2);
+            init(raw_empty + 8 * i, 4);
         }
         for (int i = 0; i < 2; ++i) {
-            init(k_full + 8 * i, 4);
+            init(k_full + 8 * i, 8);
             init(k_empty + 8 * i, 1);
-            init(v_full + 8 * i, 4);
+            init(v_full + 8 * i, 8);
             init(v_empty + 8 * i, 1);
             init(s_full + 8 * i, 1);
             init(p_full + 8 * i, 4);
@@ -461,22 +496,22 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
             for (int i = sent > kRing ? sent - kRing : 0; i < sent; ++i)
                 mbar_wait_bounded(raw_full + 8 * (i % kRing), (i / kRing) & 1, kA16DrainLimit);
         __syncwarp();
-    } else if (warp >= C::W_DQ && warp < C::W_DQ + 4) {
+    } else if (warp >= C::W_DQ && warp < C::W_DQ + 8) {
         // ------------------------------------------------ widening
-        const int dw = warp - C::W_DQ;                           // positions 32 dw .. of each tile
+        const int dw = warp - C::W_DQ;                           // block dw of each tile
+        const int row = lane % kKvBlock, part = lane / kKvBlock; // two lanes a token
         int k = 0;
         for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
             const Item it = item(idx);
             for (int i = 0; i < it.n; ++i, ++k) {
-                const int kh = 2 * k + (dw >> 1), rs = kh % kRing, s = k & 1;
+                const int kh = 2 * k + dw / kBlocks, rs = kh % kRing, s = k & 1;
                 const uint32_t par = ((k >> 1) & 1) ^ 1;
                 const bool ok = tc_wait(raw_full + 8 * rs, (kh / kRing) & 1, &abort_sh, p.status);
-                const unsigned char *raw = sm + C::oRaw + rs * C::RAW + (dw & 1) * 2 * C::BLK;
-                const uint32_t there = (raw_there[rs] >> (2 * (dw & 1))) & 3u;
-                // a lane a token: its scales, and the largest
-                const unsigned char *blk = raw + (lane / kKvBlock) * C::BLK;
-                const int pos = (it.t0 + i) * kTileT + 32 * dw + lane, row = lane % kKvBlock;
-                const bool is = ok && ((there >> (lane / kKvBlock)) & 1u) && pos >= it.lo && pos < it.hi;
+                const unsigned char *blk = sm + C::oRaw + rs * C::RAW + (dw % kBlocks) * C::BLK;
+                const bool there = (raw_there[rs] >> (dw % kBlocks)) & 1u;
+                // the token's scales, and the block's largest
+                const int pos = (it.t0 + i) * kTileT + kKvBlock * dw + row;
+                const bool is = ok && there && pos >= it.lo && pos < it.hi;
                 const float *sc = reinterpret_cast<const float *>(blk + 16 * D);
                 const float sk = is ? sc[row] : 0.0f, sv = is ? sc[16 + row] : 0.0f;
                 const uint32_t mk = __reduce_max_sync(0xffffffffu, __float_as_uint(sk)) >> 23;   // scales are not negative
@@ -487,15 +522,16 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 // keys: 8 nibbles to 16 bytes in the order (0, 4), (1, 5), (2, 6), (3, 7)
                 const bool kok = tc_wait(k_empty + 8 * s, par, &abort_sh, p.status) && ok;
                 if (kok) {
-                    if (lane == 0) kv_info[k & 3][dw] = {there, pow2i(ek + 10), ev};
+                    if (lane == 0) kv_info[k & 3][dw] = {pow2i(ek + 10), ev, there, 0};
                     const __half2 h2 = __half2half2(hk);
                     const uint32_t s1 = *reinterpret_cast<const uint32_t *>(&h2);
                     const uint32_t s16 = hmul2_(s1, kSixteenth), b = hmul2_(s1, kMinus8);
-                    const int r = 32 * dw + lane;
+                    const int r = kKvBlock * dw + row;
                     unsigned char *dst = sm + C::oK + s * C::KT + ((r >> 3) << 10) + (r & 7) * 16;
                     const uint4 *src = reinterpret_cast<const uint4 *>(blk + row * (D / 2));
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
+                    for (int c0 = 0; c0 < D / 64; ++c0) {
+                        const int c = part * (D / 64) + c0;
                         const uint4 x4 = src[c];
                         const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
@@ -519,7 +555,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     const uint32_t own = __half_as_ushort(hv);
                     const uint32_t two = own | (__shfl_down_sync(0xffffffffu, own, 1) << 16);    // of even lanes
 #pragma unroll
-                    for (int o = 0; o < 4; ++o) {
+                    for (int o = 0; o < 2; ++o) {
                         uint32_t sx[4], b[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -527,8 +563,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                             b[q] = hmul2_(s1, kMinus8);
                             sx[q] = lane & 1 ? hmul2_(s1, kSixteenth) : s1;
                         }
-                        const unsigned char *vb = raw + (o >> 1) * C::BLK + 8 * D + (o & 1) * 4 * D;
-                        unsigned char *dst = sm + C::oV + s * C::KT + (dw >> 1) * (D * 128) + (4 * (dw & 1) + o) * 128;
+                        const unsigned char *vb = blk + 8 * D + o * 4 * D;
+                        unsigned char *dst = sm + C::oV + s * C::KT + (dw >> 2) * (D * 128) + (2 * (dw & 3) + o) * 128;
 #pragma unroll
                         for (int d0 = 0; d0 < D; d0 += 32) {
                             const int d = d0 + lane;
@@ -725,79 +761,46 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 if (mine > 0) {
                     const uint32_t s_at = tmem + lanes + slot * 128;
                     const int at = (it.t0 + i) * kTileT;
-                    uint32_t there = 0;
-                    float F[4];
-                    int ev[4], evm = kNoE;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const Info in = kv_info[k & 3][c];
-                        there |= in.there << (2 * c);
-                        F[c] = f * in.kx;
-                        ev[c] = in.ev;
-                        evm = max(evm, in.ev);
-                    }
-                    const bool edge = !(there == 0xFFu && at >= wlo && at + kTileT <= whi);
-                    // E: an exponent that no value's scale passes (4 times the
-                    // first ones', so that it is seldom raised)
-                    const int E0 = E;
-                    const bool newE = i == 0 || evm > E;
-                    if (newE) E = evm == kNoE ? -126 : evm + 2;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) ev[c] = ev[c] == kNoE ? 0 : max(ev[c] - E, -100);    // <= 0
-                    uint32_t pk[64];
-                    float add = 0.0f;
-                    auto masked = [&](int c, uint32_t (&v)[32]) {        // what the row does not see
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int pos = at + 32 * c + e;
-                            if (pos < rlo || pos >= rhi || !((there >> ((32 * c + e) / kKvBlock)) & 1u))
-                                v[e] = 0xFF800000u;
-                        }
-                    };
-                    auto weights = [&]() {       // of all 128; the largest exponent above the running maximum
-                        float top = -INFINITY;
-                        add = 0.0f;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float dc = static_cast<float>(ev[c]);
-                            const unsigned long long f2 = pair2(F[c], F[c]), m2 = pair2(dc - m, dc - m);
-                            unsigned long long s2 = pair2(0.0f, 0.0f);
-                            float th = -INFINITY;
-                            uint32_t v[32];
-                            t_ld32(s_at + 32 * c, v);
-                            if (edge) masked(c, v);
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                unsigned long long x2;
-                                asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x2) : "l"(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]))), "l"(f2), "l"(m2));
-                                float x0, x1;
-                                split2(x2, x0, x1);
-                                th = fmaxf(th, fmaxf(x0, x1));
-                                const float w0 = ex2(x0), w1 = ex2(x1);
-                                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s2) : "l"(pair2(w0, w1)));
-                                pk[16 * c + e / 2] = half2_bits(w0, w1);
-                            }
-                            float s0, s1;
-                            split2(s2, s0, s1);
-                            add = fmaf(s0 + s1, pow2i(-ev[c]), add);
-                            top = fmaxf(top, th - dc);
-                        }
-                        return top;
-                    };
-                    float top = INFINITY;
-                    if (i > 0) top = weights();
-                    if (__any_sync(0xffffffffu, newE || top > kSlackT)) {
-                        float t = -INFINITY;
+                    const Info *in = kv_info[k & 3];
+                    const uint32_t there = __ballot_sync(0xffffffffu, lane < 8 && in[lane & 7].there);
+                    const int evm = __reduce_max_sync(0xffffffffu, in[lane & 7].ev);
+                    if (!(there == 0xFFu && at >= wlo && at + kTileT <= whi)) {      // what the row does not see
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t v[32];
                             t_ld32(s_at + 32 * c, v);
-                            if (edge) masked(c, v);
-                            float tc = -INFINITY;
+                            t_wait_ld(v);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) tc = fmaxf(tc, __uint_as_float(v[e]));
-                            t = fmaxf(t, tc * f * kv_info[k & 3][c].kx);
+                            for (int e = 0; e < 32; ++e) {
+                                const int pos = at + 32 * c + e;
+                                if (pos < rlo || pos >= rhi || !((there >> (2 * c + e / kKvBlock)) & 1u)) v[e] = 0xFF800000u;
+                            }
+                            t_st32(s_at + 32 * c, v);
                         }
+                        t_wait_st();
+                    }
+                    // the largest score, in units of log2
+                    float t = -INFINITY;
+                    {
+                        uint32_t v[2][16];
+                        t_ld16(s_at, v[0]);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            t_wait_ld(v[c & 1]);
+                            if (c < 7) t_ld16(s_at + 16 * (c + 1), v[(c + 1) & 1]);
+                            float t0 = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) t0 = fmaxf(t0, __uint_as_float(v[c & 1][e]));
+                            t = fmaxf(t, t0 * in[c].kx);
+                        }
+                        t *= f;
+                    }
+                    // E: an exponent that no value's scale passes (4 times the
+                    // first ones', so that it is seldom raised)
+                    const bool newE = i == 0 || evm > E;
+                    if (__any_sync(0xffffffffu, newE || t - m > kSlackT)) {
+                        const int E0 = E;
+                        if (newE) E = evm == kNoE ? -126 : evm + 2;
                         const float to = fmaxf(m, t), fix = ex2(m - to);
                         m = to;
                         l *= fix;
@@ -809,17 +812,46 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                             for (int c = 0; c < D / 32; ++c) {
                                 uint32_t v[32];
                                 t_ld32(o_at + 32 * c, v);
+                                t_wait_ld(v);
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * of);
                                 t_st32(o_at + 32 * c, v);
                             }
                             t_wait_st();
                         }
-                        weights();
                     }
-                    l += add;
-                    t_st32(s_at, pk);
-                    t_st32(s_at + 32, pk + 32);
+                    // the weights, over the scores already read
+                    {
+                        uint32_t v[2][16];
+                        t_ld16(s_at, v[0]);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            t_wait_ld(v[c & 1]);
+                            if (c < 7) t_ld16(s_at + 16 * (c + 1), v[(c + 1) & 1]);
+                            const float2 ke = *reinterpret_cast<const float2 *>(&in[c].kx);
+                            const int ei = __float_as_int(ke.y), ed = ei == kNoE ? 0 : max(ei - E, -100);    // <= 0
+                            const float F = f * ke.x, dm = static_cast<float>(ed) - m;
+                            const unsigned long long f2 = pair2(F, F), m2 = pair2(dm, dm);
+                            unsigned long long s2 = pair2(0.0f, 0.0f);
+                            uint32_t pk[8];
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                unsigned long long x2;
+                                asm("fma.rn.f32x2 %0, %1, %2, %3;"
+                                    : "=l"(x2)
+                                    : "l"(pair2(__uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1]))), "l"(f2), "l"(m2));
+                                float x0, x1;
+                                split2(x2, x0, x1);
+                                const float w0 = ex2(x0), w1 = ex2(x1);
+                                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s2) : "l"(pair2(w0, w1)));
+                                pk[e / 2] = half2_bits(w0, w1);
+                            }
+                            float s0, s1;
+                            split2(s2, s0, s1);
+                            l = fmaf(s0 + s1, pow2i(-ed), l);
+                            t_st8(s_at + 8 * c, pk);
+                        }
+                    }
                     t_wait_st();
                 }
                 fence_before();
@@ -837,6 +869,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
                         t_ld32(o_at + 32 * c, v);
+                        t_wait_ld(v);
                         float *dst = p.part + (static_cast<int64_t>(it.idx) * RU + row) * D + 32 * c;
                         if (is)
 #pragma unroll
@@ -854,7 +887,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                         uint32_t v[P][8];
 #pragma unroll
                         for (int b = 0; b < P; ++b) t_ld8(o_at + 32 * b + c, v[b]);
-                        t_wait_ld();
+#pragma unroll
+                        for (int b = 0; b < P; ++b) t_wait_ld(v[b]);
 #pragma unroll
                         for (int h = 1; h < P; h <<= 1)
 #pragma unroll
@@ -878,6 +912,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     for (int c = 0; c < P; ++c) {
                         uint32_t v[32];
                         t_ld32(o_at + 32 * c, v);
+                        t_wait_ld(v);
 #pragma unroll
                         for (int h = 1; h < 32; h <<= 1)
 #pragma unroll
