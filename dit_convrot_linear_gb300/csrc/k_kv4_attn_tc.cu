@@ -16,9 +16,9 @@
 //   - one thread issues the products: S into TMEM (128 columns a row tile), P
 //     (fp16, over S's columns) times V into O, also in TMEM.  With two row tiles
 //     one's softmax runs during the other's products; with one, S has two places;
-//   - a thread a row does the softmax: its 128 scores come from TMEM, twice (the
-//     maximum, then the weights, which go back over them), no value crosses
-//     lanes.  The running maximum is raised only when passed by 2^8; O is then
+//   - two threads a row do the softmax, 64 positions each: the scores come from
+//     TMEM, twice (the maximum, which the two exchange, then the weights, which go
+//     back over them).  The running maximum is raised only when passed by 2^8; O is then
 //     rescaled in place, which the tensor cores' order of work makes safe.  (One
 //     pass that takes the maximum for granted and repeats itself where it was
 //     not is as much work, but three times the code, which four kinds of warps
@@ -45,20 +45,18 @@ constexpr unsigned int kStatusKvTcTimeout = 256u;
 constexpr float kNoneT = -FLT_MAX;
 constexpr float kSlackT = 8.0f;
 constexpr float kLog2eT = 1.4426950408889634f;
-constexpr int kMinPart = 4;                  // fewest tiles a part
 constexpr int kMaxSeqsT = 256;               // sequences the cutting holds in shared memory
 constexpr int kNoE = -1024;                  // exponent of a half whose values are all zero
 constexpr int kCols = 512;                   // TMEM columns
 constexpr int kMaxSmsT = 160;                // more SMs than this stay unused
-constexpr int kMaxItems = 640;               // parts of a call whose row tiles are cut (of one 128-row tile; half as many of two)
-constexpr int kMaxParts = 64;                // of one row tile
-constexpr float kPartTiles = 4.0f;           // tiles that a part's start and end stand for
+constexpr int kStart = 4;                    // tiles that a part's start and end stand for
+constexpr int kMinPart = 4;                  // fewest tiles a part
 
 template <int D_, int NQ_>
 struct TCfg {
     static constexpr int D = D_, NQ = NQ_;
     static constexpr int RU = 128 * NQ;                      // query rows a row tile
-    static constexpr int WSM = 4 * NQ;                       // softmax warps
+    static constexpr int WSM = 8 * NQ;                       // softmax warps: two for the same 32 rows, half the columns each
     static constexpr int W_DQ = WSM, W_LD = WSM + 8, W_MMA = WSM + 9;
     static constexpr int NT = (WSM + 10) * 32;
     static constexpr int BLK = kv_block_bytes(D);
@@ -70,17 +68,20 @@ struct TCfg {
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;       // one CTA an SM: it takes all of TMEM
 };
 
-template <class C>
-constexpr int kMaxItemsOf() { return kMaxItems * 128 / C::RU; }
-
-struct Item {                                // a part of a row tile
-    int idx, np, t0, n, lo, hi;              // its number; parts of its row tile; tiles; positions of the row tile
+struct Item {                                // a CTA's part of a row tile
+    int n, at, lo, hi;                       // tiles, its first position; positions of the row tile
+    int slot;                                // where its sums go (-1: it is the whole row tile)
     int b, h, rt;
+    bool last;                               // it ends its row tile
+    int64_t next;                            // where the CTA goes on
     KvSeq q;
 };
 
-struct Split {                               // a row tile in parts, for the join (32 bytes)
-    int np, start, rows, h, rt, pad[3];
+// What the join knows of a CTA: whether its first part goes on with the row tile
+// of the CTA before (1) and ends it (2); whether its last one begins a row tile
+// that the next CTA goes on with (4), and which.
+struct Cut {
+    int flags, start, rows, h, rt, pad[3];
 };
 
 struct TcParams {
@@ -88,11 +89,10 @@ struct TcParams {
     Kv4Attn a;
     Geo geo;
     unsigned int *status;
-    int *head;                               // items of this call (0: no row tile is in parts)
-    Split *table;                            // [2 grid]
+    int ctas;                                // of the attention kernel
+    Cut *table;                              // [grid]
     float2 *stat;                            // [2 grid][RU]
     float *part;                             // [2 grid][RU][D]
-    int split;                               // row tiles may be cut
 };
 
 __device__ __forceinline__ uint32_t sa(const void *p) { return smem_addr(p); }
@@ -240,9 +240,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_sh;
-    __shared__ int n_items_sh, split_sh;
-    __shared__ int64_t per_sh;
-    __shared__ int item_sh[kMaxSeqsT], before_sh[kMaxSeqsT];
+    __shared__ int64_t run_sh[2], before_sh[kMaxSeqsT + 1];      // before: of all heads of the sequences before
     __shared__ KvSeq seq_sh[kMaxSeqsT];
     struct __align__(16) Info {              // of a block: 2^(e + 10) of the keys, exponent of the values (read as a
         float kx;                            // pair: first, at 16 bytes); whether it is there
@@ -250,9 +248,11 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         int there, pad;
     };
     __shared__ uint32_t raw_there[kRing];
+    __shared__ float rowf_sh[RU];                            // a row's factor
+    // what a row's two threads exchange: their maxima (in 16 bits, rounded up:
+    // any bound serves that both take), and their sums
+    __shared__ union { uint16_t max[2][2][RU]; float sum[2][RU]; } pair_sh;
     __shared__ Info kv_info[4][8];
-    int64_t *cost_sh = reinterpret_cast<int64_t *>(sm);      // before any operand
-    int *unit_sh = reinterpret_cast<int *>(sm + kMaxSeqsT * 8);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const tq_kv4 &kv = p.kv;
     const Geo &ge = p.geo;
@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
             init(v_full + 8 * i, 8);
             init(v_empty + 8 * i, 1);
             init(s_full + 8 * i, 1);
-            init(p_full + 8 * i, 4);
-            init(q_full + 8 * i, 4);
+            init(p_full + 8 * i, 8);
+            init(q_full + 8 * i, 8);
             init(pv_done + 8 * i, 1);
         }
         init(all_done, 1);
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
     pdl_wait();
 
     // ---------------------------------------------------- cutting
-    // Row tiles and their tiles of each sequence (a warp a sequence), all of
-    // them, then the parts: none where there are row tiles enough.
+    // The row tiles stand in a line, each as long as its tiles and kStart; a CTA
+    // takes an equal piece of it.  First the lengths (a warp a sequence).
     const int nseq = static_cast<int>(kv.nseq);
     bool bad = false;
     for (int i = tid; i < nseq; i += C::NT) seq_sh[i] = kv_seq(kv, i, bad);
@@ -303,168 +303,123 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         const KvSeq q = seq_sh[i];
         const int nrt = row_tiles(ge, q);
         int64_t sum = 0;
-        int units = 0;
         for (int rt = lane; rt < nrt; rt += 32) {
             int lo, hi, t0, c;
             range_of<kTileT>(ge, q, rt, lo, hi, t0, c);
-            sum += c;
-            units += c > 0;
+            if (c > 0) sum += c + kStart;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        units = __reduce_add_sync(0xffffffffu, units);
-        if (lane == 0) {
-            cost_sh[i] = sum;
-            unit_sh[i] = units;
-        }
+        if (lane == 0) before_sh[i + 1] = sum * kv.heads;
     }
-    __syncthreads();
-    if (warp == 0) {
-        int64_t sum = 0, units = 0;
-        for (int i = lane; i < nseq; i += 32) {
-            sum += cost_sh[i];
-            units += unit_sh[i];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            units += __shfl_xor_sync(0xffffffffu, units, o);
-        }
-        // Into how many parts: what makes the rounds over the SMs, each as long
-        // as a part of a row tile of mean length and its start and end, shortest.
-        units *= kv.heads;
-        float best = FLT_MAX;
-        int parts = 1;
-        const float mean = units ? static_cast<float>(sum * kv.heads) / static_cast<float>(units) : 0.0f;
-        if (p.split && units > 0 && units <= kMaxItemsOf<C>() / 2)
-            for (int n = 1 + lane; n <= kMaxParts; n += 32) {
-                const int64_t rounds = (units * n + gridDim.x - 1) / gridDim.x;
-                const float t = static_cast<float>(rounds) * (mean / static_cast<float>(n) + kPartTiles);
-                if (units * n * 5 / 4 + 8 <= kMaxItemsOf<C>() && mean >= n * kMinPart && t < best) {
-                    best = t;
-                    parts = n;
-                }
-            }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float b2 = __shfl_xor_sync(0xffffffffu, best, o);
-            const int n2 = __shfl_xor_sync(0xffffffffu, parts, o);
-            if (b2 < best || (b2 == best && n2 < parts)) {
-                best = b2;
-                parts = n2;
-            }
-        }
-        if (lane == 0) {
-            per_sh = parts > 1 ? static_cast<int64_t>(mean / static_cast<float>(parts)) : 0;
-            split_sh = parts > 1;
-        }
-    }
-    __syncthreads();
-    const int64_t per = per_sh;
-    bool split = split_sh != 0;
-    auto parts_of = [&](int cost) {
-        return cost == 0 ? 0 : !split || cost < 2 * per ? 1 : static_cast<int>(quotient(cost + per / 2, per));
-    };
-    for (int again = 0; again < 2; ++again) {    // a second time without parts where they are too many
-    for (int i = warp; i < nseq; i += C::NT / 32) {
-        const KvSeq q = seq_sh[i];
-        const int nrt = row_tiles(ge, q);
-        int n = 0;
-        for (int rt = lane; rt < nrt; rt += 32) {
-            int lo, hi, t0, c;
-            range_of<kTileT>(ge, q, rt, lo, hi, t0, c);
-            n += parts_of(c);
-        }
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) item_sh[i] = n;           // of one head
-    }
+    if (tid == 0) before_sh[0] = 0;
     __syncthreads();
     if (warp == 0) {                             // running sums
-        int run = 0;
+        int64_t run = 0;
         for (int base = 0; base < nseq; base += 32) {
-            const int v = base + lane < nseq ? item_sh[base + lane] * kv.heads : 0;
-            int x = v;
+            int64_t x = base + lane < nseq ? before_sh[base + lane + 1] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            if (base + lane < nseq) before_sh[base + lane] = run + x - v;
+            if (base + lane < nseq) before_sh[base + lane + 1] = run + x;
             run += __shfl_sync(0xffffffffu, x, 31);
         }
-        if (lane == 0) n_items_sh = run;
     }
-    __syncthreads();
-    if (!split || n_items_sh <= kMaxItemsOf<C>()) break;
-    split = false;
-    }
-    if (tid == 0 && blockIdx.x == 0 && p.split) *p.head = split ? n_items_sh : 0;
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_sh;
-    const int n_items = n_items_sh;
 
-    // Item `idx`, by a whole warp.
-    auto item = [&](int idx) {
-        Item it;
+    // The row tile at `x` of the line, by a whole warp; where it begins, and its
+    // tiles and the first of them.
+    auto find = [&](int64_t x, Item &it, int64_t &begin, int &t0, int &tiles) {
         int lo = 0, hi = nseq;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (before_sh[mid] <= idx) lo = mid;
+            if (before_sh[mid] <= x) lo = mid;
             else hi = mid;
         }
-        it.idx = idx;
         it.b = lo;
         it.q = seq_sh[lo];
-        int k = idx - before_sh[lo];
-        it.h = k / item_sh[lo];
-        k -= it.h * item_sh[lo];
+        const int64_t each = quotient(before_sh[lo + 1] - before_sh[lo], kv.heads);
+        int64_t k = x - before_sh[lo];
+        it.h = static_cast<int>(quotient(k, each));
+        k -= it.h * each;
         const int nrt = row_tiles(ge, it.q);
         it.rt = 0;
-        int part = 0, t0 = 0, c = 0;
-        it.np = 1;
         for (int base = 0; base < nrt; base += 32) {
-            int l1 = 0, h1 = 0, n = 0;
-            if (base + lane < nrt) {
-                range_of<kTileT>(ge, it.q, base + lane, l1, h1, t0, c);
-                n = parts_of(c);
-            }
-            int x = n;
+            int l1 = 0, h1 = 0, c = 0;
+            if (base + lane < nrt) range_of<kTileT>(ge, it.q, base + lane, l1, h1, t0, c);
+            const int n = c > 0 ? c + kStart : 0;
+            int s = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
+                const int y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
             }
-            const unsigned in = __ballot_sync(0xffffffffu, x > k);
+            const unsigned in = __ballot_sync(0xffffffffu, s > k);
             if (in) {
                 const int l = __ffs(in) - 1;
                 it.rt = base + l;
-                part = k - __shfl_sync(0xffffffffu, x - n, l);
-                it.np = __shfl_sync(0xffffffffu, n, l);
+                k -= __shfl_sync(0xffffffffu, s - n, l);
                 break;
             }
-            k -= __shfl_sync(0xffffffffu, x, 31);
+            k -= __shfl_sync(0xffffffffu, s, 31);
         }
-        range_of<kTileT>(ge, it.q, it.rt, it.lo, it.hi, t0, c);
-        const int f = static_cast<int>(static_cast<int64_t>(c) * part / it.np);
-        it.n = static_cast<int>(static_cast<int64_t>(c) * (part + 1) / it.np) - f;
-        it.t0 = t0 + f;
-        if (it.np > 1 && part == 0 && warp == 0 && lane == 0)
-            p.table[idx] = {it.np, it.q.start, it.q.n * ge.g, it.h, it.rt, {0, 0, 0}};
-        if (split && it.np == 1 && warp == 0 && lane == 0) p.table[idx].np = 1;
-        else if (split && part > 0 && warp == 0 && lane == 0) p.table[idx].np = 0;
+        begin = x - k;
+        range_of<kTileT>(ge, it.q, it.rt, it.lo, it.hi, t0, tiles);
+    };
+    // This CTA's piece: from the warps 0 and 1, its two ends.  An end with fewer
+    // than kMinPart tiles of its row tile on one side moves to that side.
+    if (warp < 2) {
+        const int64_t total = before_sh[nseq];
+        const int64_t runs = min(static_cast<int64_t>(gridDim.x), max(quotient(total, kStart + kMinPart), int64_t{1}));
+        int64_t x = total;
+        if (blockIdx.x + warp < runs) {
+            x = quotient(total * (blockIdx.x + warp), runs);
+            if (x < total) {
+                Item it;
+                int64_t begin;
+                int t0, tiles;
+                find(x, it, begin, t0, tiles);
+                const int64_t in = x - begin - kStart;
+                if (in < kMinPart) x = begin;
+                else if (tiles - in < kMinPart) x = begin + kStart + tiles;
+            }
+        }
+        if (lane == 0) run_sh[warp] = x;
+    }
+    __syncthreads();
+    const int64_t run0 = run_sh[0], run1 = run_sh[1];
+
+    // The part of a row tile that begins at `x`.
+    auto item = [&](int64_t x) {
+        Item it;
+        int64_t begin;
+        int t0, tiles;
+        find(x, it, begin, t0, tiles);
+        const int from = x == begin ? 0 : static_cast<int>(x - begin - kStart);
+        const int64_t end = begin + kStart + tiles;
+        const int to = run1 >= end ? tiles : static_cast<int>(run1 - begin - kStart);
+        it.n = to - from;
+        it.at = (t0 + from) * kTileT;
+        it.slot = from > 0 ? 2 * static_cast<int>(blockIdx.x) : to < tiles ? 2 * static_cast<int>(blockIdx.x) + 1 : -1;
+        it.last = to == tiles;
+        it.next = min(run1, end);
         return it;
     };
 
     if (warp == C::W_LD) {
         // ------------------------------------------------ loader
         int k = 0, sent = 0;                     // halves
-        for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
-            const Item it = item(idx);
+        for (int64_t x = run0; x < run1;) {
+            const Item it = item(x);
+            x = it.next;
             for (int t = 0; t < 2 * it.n; ++t, ++k) {
                 const int s = k % kRing;
-                const int at = it.t0 * kTileT + t * kHalf;
+                const int at = it.at + t * kHalf;
                 // a copy a page's piece of the half: lane 0 .. 3 a block each, the
                 // first of a page's for all of them
                 const int each = min(kBlocks, kv.page_size / kKvBlock);
@@ -501,8 +456,9 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         const int dw = warp - C::W_DQ;                           // block dw of each tile
         const int row = lane % kKvBlock, part = lane / kKvBlock; // two lanes a token
         int k = 0;
-        for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
-            const Item it = item(idx);
+        for (int64_t x = run0; x < run1;) {
+            const Item it = item(x);
+            x = it.next;
             for (int i = 0; i < it.n; ++i, ++k) {
                 const int kh = 2 * k + dw / kBlocks, rs = kh % kRing, s = k & 1;
                 const uint32_t par = ((k >> 1) & 1) ^ 1;
@@ -510,7 +466,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 const unsigned char *blk = sm + C::oRaw + rs * C::RAW + (dw % kBlocks) * C::BLK;
                 const bool there = (raw_there[rs] >> (dw % kBlocks)) & 1u;
                 // the token's scales, and the block's largest
-                const int pos = (it.t0 + i) * kTileT + kKvBlock * dw + row;
+                const int pos = it.at + i * kTileT + kKvBlock * dw + row;
                 const bool is = ok && there && pos >= it.lo && pos < it.hi;
                 const float *sc = reinterpret_cast<const float *>(blk + 16 * D);
                 const float sk = is ? sc[row] : 0.0f, sv = is ? sc[16 + row] : 0.0f;
@@ -531,7 +487,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     const uint4 *src = reinterpret_cast<const uint4 *>(blk + row * (D / 2));
 #pragma unroll
                     for (int c0 = 0; c0 < D / 64; ++c0) {
-                        const int c = part * (D / 64) + c0;
+                        // (from a chunk by the row, so that eight rows read different banks)
+                        const int c = ((row >> (D == 128 ? 1 : 2)) + part * (D / 64) + c0) & (D / 32 - 1);
                         const uint4 x4 = src[c];
                         const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
@@ -617,7 +574,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     asm volatile(
                         "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
                         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem + 256 + q * 128),
-                        "r"(tmem + slot * 128 + kk * 8), "l"(bd), "r"(kIdO), "r"(first && kk == 0 ? 0u : 1u));
+                        "r"(tmem + slot * 128 + (kk >> 2) * 64 + (kk & 3) * 8), "l"(bd), "r"(kIdO),
+                        "r"(first && kk == 0 ? 0u : 1u));
                 }
                 commit(pv_done + 8 * q);
             }
@@ -629,8 +587,9 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         };
         bool ok = true;
         auto wait = [&](uint32_t b, uint32_t parity) { ok = ok && tc_wait(b, parity, &abort_sh, p.status); };
-        for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x, ++ni) {
-            const Item it = item(idx);
+        for (int64_t x = run0; x < run1; ++ni) {
+            const Item it = item(x);
+            x = it.next;
             for (int q = 0; q < NQ; ++q) wait(q_full + 8 * q, ni & 1);
             wait(k_full + 8 * (k & 1), (k >> 1) & 1);
             if (ok) {
@@ -686,21 +645,26 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
             __syncwarp();
         }
     } else if (warp < C::WSM) {
-        // ------------------------------------------------ softmax: a thread a row
-        const int q = warp >> 2, wq = warp & 3, row = q * 128 + wq * 32 + lane;
+        // ------------------------------------------------ softmax: two threads a row
+        const int q = warp >> 3, wq = warp & 3, hc = (warp >> 2) & 1, row = q * 128 + wq * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t o_at = tmem + lanes + 256 + q * 128;
+        Cut cut = {};                                    // (warp 0 keeps it)
+        // the two warps of the same rows (both come by whatever has run out)
+        auto pair_bar = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + q * 4 + wq) : "memory"); };
         int k = 0;
         bool ok = true;
-        float f = 0.0f;                                  // the row's factor
-        for (int idx = blockIdx.x; idx < n_items; idx += gridDim.x) {
-            const Item it = item(idx);
+        for (int64_t x = run0; x < run1;) {
+            const Item it = item(x);
+            x = it.next;
             const int rows = it.q.n * ge.g, r0 = it.rt * RU;
+            if (it.slot == 2 * static_cast<int>(blockIdx.x)) cut.flags = it.last ? 3 : 1;
+            else if (it.slot >= 0) cut = {cut.flags | 4, it.q.start, rows, it.h, it.rt, {0, 0, 0}};
             // queries: eight lanes a row, rotated, as fp16 with the row's largest
             // value in [2^13, 2^14), eight columns in the keys' order
             const int mine = min(32, max(0, rows - (r0 + q * 128 + wq * 32)));     // rows of this warp
 #pragma unroll 1
-            for (int g4 = 0; g4 < 32; g4 += 4) {
+            for (int g4 = 16 * hc; g4 < 16 * hc + 16; g4 += 4) {
                 constexpr int N = D / 8;
                 const int rr = g4 + lane / 8, l8 = lane & 7;
                 const int i = r0 + q * 128 + wq * 32 + rr;
@@ -732,8 +696,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 const int ke = mx > 0.0f ? min(13 - (static_cast<int>(__float_as_uint(mx) >> 23) - 127), 126) : 0;
                 const float up = pow2i(ke);
                 const int r = wq * 32 + rr;
-                const float rf = __shfl_sync(0xffffffffu, p.a.scale * kLog2eT * pow2i(-ke), (lane & 3) * 8);
-                if ((lane & ~3) == g4) f = rf;           // lane's row is lane
+                if (l8 == 0) rowf_sh[q * 128 + r] = p.a.scale * kLog2eT * pow2i(-ke);
                 unsigned char *dst = sm + C::oQ + q * C::KT + ((r >> 3) << 10) + (r & 7) * 16;
 #pragma unroll
                 for (int e = 0; e < N; e += 8) {
@@ -746,6 +709,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
             fence_async();
             __syncwarp();
             if (lane == 0) arrive(q_full + 8 * q);
+            pair_bar();                                  // the rows' factors, of both warps
+            const float f = rowf_sh[row];
             int rlo = 0, rhi = 0;
             const bool is = r0 + row < rows;
             if (is) row_range(ge, it.q, (r0 + row) / ge.g, rlo, rhi);
@@ -756,38 +721,39 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 const int slot = NQ == 2 ? q : k & 1;
                 const uint32_t par = NQ == 2 ? k & 1 : (k >> 1) & 1;
                 ok = ok && tc_wait(s_full + 8 * slot, par, &abort_sh, p.status);
-                if (!ok) continue;
                 fence_after();
                 if (mine > 0) {
-                    const uint32_t s_at = tmem + lanes + slot * 128;
-                    const int at = (it.t0 + i) * kTileT;
+                    const uint32_t s_at = tmem + lanes + slot * 128 + 64 * hc;       // this warp's columns
+                    const int at = it.at + i * kTileT + 64 * hc;
                     const Info *in = kv_info[k & 3];
-                    const uint32_t there = __ballot_sync(0xffffffffu, lane < 8 && in[lane & 7].there);
+                    const uint32_t there = __ballot_sync(0xffffffffu, lane < 8 && in[lane & 7].there) >> (4 * hc);
                     const int evm = __reduce_max_sync(0xffffffffu, in[lane & 7].ev);
-                    if (!(there == 0xFFu && at >= wlo && at + kTileT <= whi)) {      // what the row does not see
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t v[32];
-                            t_ld32(s_at + 32 * c, v);
-                            t_wait_ld(v);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int pos = at + 32 * c + e;
-                                if (pos < rlo || pos >= rhi || !((there >> (2 * c + e / kKvBlock)) & 1u)) v[e] = 0xFF800000u;
-                            }
-                            t_st32(s_at + 32 * c, v);
-                        }
-                        t_wait_st();
-                    }
-                    // the largest score, in units of log2
+                    in += 4 * hc;
                     float t = -INFINITY;
-                    {
+                    if (ok) {
+                        if (!((there & 15u) == 15u && at >= wlo && at + 64 <= whi)) {    // what the row does not see
+#pragma unroll 1
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t v[32];
+                                t_ld32(s_at + 32 * c, v);
+                                t_wait_ld(v);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const int pos = at + 32 * c + e;
+                                    if (pos < rlo || pos >= rhi || !((there >> (2 * c + e / kKvBlock)) & 1u))
+                                        v[e] = 0xFF800000u;
+                                }
+                                t_st32(s_at + 32 * c, v);
+                            }
+                            t_wait_st();
+                        }
+                        // the largest score, in units of log2
                         uint32_t v[2][16];
                         t_ld16(s_at, v[0]);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
+                        for (int c = 0; c < 4; ++c) {
                             t_wait_ld(v[c & 1]);
-                            if (c < 7) t_ld16(s_at + 16 * (c + 1), v[(c + 1) & 1]);
+                            if (c < 3) t_ld16(s_at + 16 * (c + 1), v[(c + 1) & 1]);
                             float t0 = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) t0 = fmaxf(t0, __uint_as_float(v[c & 1][e]));
@@ -795,10 +761,14 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                         }
                         t *= f;
                     }
+                    const uint16_t up16 = __bfloat16_as_ushort(__float2bfloat16_ru(t));
+                    pair_sh.max[k & 1][hc][row] = up16;
+                    pair_bar();
+                    t = fmaxf(bf16_bits_to_f32(up16), bf16_bits_to_f32(pair_sh.max[k & 1][hc ^ 1][row]));
                     // E: an exponent that no value's scale passes (4 times the
                     // first ones', so that it is seldom raised)
                     const bool newE = i == 0 || evm > E;
-                    if (__any_sync(0xffffffffu, newE || t - m > kSlackT)) {
+                    if (ok && __any_sync(0xffffffffu, newE || t - m > kSlackT)) {
                         const int E0 = E;
                         if (newE) E = evm == kNoE ? -126 : evm + 2;
                         const float to = fmaxf(m, t), fix = ex2(m - to);
@@ -808,26 +778,27 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                             if constexpr (NQ == 1) ok = tc_wait(pv_done, (k - 1) & 1, &abort_sh, p.status);
                             fence_after();
                             const float of = fix * pow2i(E0 - E);
+                            if (ok)
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t v[32];
-                                t_ld32(o_at + 32 * c, v);
-                                t_wait_ld(v);
+                                for (int c = hc; c < D / 32; c += 2) {       // every other piece of O
+                                    uint32_t v[32];
+                                    t_ld32(o_at + 32 * c, v);
+                                    t_wait_ld(v);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * of);
-                                t_st32(o_at + 32 * c, v);
-                            }
+                                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * of);
+                                    t_st32(o_at + 32 * c, v);
+                                }
                             t_wait_st();
                         }
                     }
                     // the weights, over the scores already read
-                    {
+                    if (ok) {
                         uint32_t v[2][16];
                         t_ld16(s_at, v[0]);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
+                        for (int c = 0; c < 4; ++c) {
                             t_wait_ld(v[c & 1]);
-                            if (c < 7) t_ld16(s_at + 16 * (c + 1), v[(c + 1) & 1]);
+                            if (c < 3) t_ld16(s_at + 16 * (c + 1), v[(c + 1) & 1]);
                             const float2 ke = *reinterpret_cast<const float2 *>(&in[c].kx);
                             const int ei = __float_as_int(ke.y), ed = ei == kNoE ? 0 : max(ei - E, -100);    // <= 0
                             const float F = f * ke.x, dm = static_cast<float>(ed) - m;
@@ -856,87 +827,99 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) arrive(p_full + 8 * slot);
+                if (lane == 0 && ok) arrive(p_full + 8 * slot);
             }
             // the output: O is whole once the last product has ended
             ok = ok && tc_wait(pv_done + 8 * q, (k - 1) & 1, &abort_sh, p.status);
             fence_after();
-            if (mine > 0 && ok) {
-                if (it.np > 1) {
+            if (mine > 0) {
+                pair_bar();                              // the last maxima have been read
+                pair_sh.sum[hc][row] = l;
+                pair_bar();
+                l += pair_sh.sum[hc ^ 1][row];
+                if (it.slot >= 0) {
                     const float up = pow2i(E + 10);
-                    if (is) p.stat[static_cast<int64_t>(it.idx) * RU + row] = make_float2(m, l);
+                    if (is && hc == 0) p.stat[static_cast<int64_t>(it.slot) * RU + row] = make_float2(m, l);
+                    if (ok)
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t v[32];
-                        t_ld32(o_at + 32 * c, v);
-                        t_wait_ld(v);
-                        float *dst = p.part + (static_cast<int64_t>(it.idx) * RU + row) * D + 32 * c;
-                        if (is)
+                        for (int c = hc; c < D / 32; c += 2) {
+                            uint32_t v[32];
+                            t_ld32(o_at + 32 * c, v);
+                            t_wait_ld(v);
+                            float *dst = p.part + (static_cast<int64_t>(it.slot) * RU + row) * D + 32 * c;
+                            if (is)
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4 *>(dst + e) =
-                                    make_float4(__uint_as_float(v[e]) * up, __uint_as_float(v[e + 1]) * up,
-                                                __uint_as_float(v[e + 2]) * up, __uint_as_float(v[e + 3]) * up);
-                    }
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<float4 *>(dst + e) =
+                                        make_float4(__uint_as_float(v[e]) * up, __uint_as_float(v[e + 1]) * up,
+                                                    __uint_as_float(v[e + 2]) * up, __uint_as_float(v[e + 3]) * up);
+                        }
                 } else {
                     // turn back: the butterfly over the 32-column pieces, eight
                     // columns of each at a time, then inside each piece
                     constexpr int P = D / 32;
+                    if (ok)
 #pragma unroll 1
-                    for (int c = 0; c < 32; c += 8) {
-                        uint32_t v[P][8];
+                        for (int c = 16 * hc; c < 16 * hc + 16; c += 8) {
+                            uint32_t v[P][8];
 #pragma unroll
-                        for (int b = 0; b < P; ++b) t_ld8(o_at + 32 * b + c, v[b]);
+                            for (int b = 0; b < P; ++b) t_ld8(o_at + 32 * b + c, v[b]);
 #pragma unroll
-                        for (int b = 0; b < P; ++b) t_wait_ld(v[b]);
+                            for (int b = 0; b < P; ++b) t_wait_ld(v[b]);
 #pragma unroll
-                        for (int h = 1; h < P; h <<= 1)
+                            for (int h = 1; h < P; h <<= 1)
 #pragma unroll
-                            for (int b = 0; b < P; ++b)
-                                if (!(b & h))
+                                for (int b = 0; b < P; ++b)
+                                    if (!(b & h))
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e) {
-                                        const float x = __uint_as_float(v[b][e]), y = __uint_as_float(v[b + h][e]);
-                                        v[b][e] = __float_as_uint(x + y);
-                                        v[b + h][e] = __float_as_uint(x - y);
-                                    }
+                                        for (int e = 0; e < 8; ++e) {
+                                            const float x = __uint_as_float(v[b][e]), y = __uint_as_float(v[b + h][e]);
+                                            v[b][e] = __float_as_uint(x + y);
+                                            v[b + h][e] = __float_as_uint(x - y);
+                                        }
 #pragma unroll
-                        for (int b = 0; b < P; ++b) t_st8(o_at + 32 * b + c, v[b]);
-                        t_wait_st();
-                    }
+                            for (int b = 0; b < P; ++b) t_st8(o_at + 32 * b + c, v[b]);
+                            t_wait_st();
+                        }
+                    fence_before();
+                    pair_bar();
+                    fence_after();
                     const float inv = l > 0.0f ? sqrtf(1.0f / D) / l * pow2i(E + 10) : 0.0f;
                     const int64_t tok = it.q.start + (is ? (r0 + row) / ge.g : 0);
                     const int hq = it.h * ge.g + (r0 + row) % ge.g;
                     uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D;
+                    if (ok)
 #pragma unroll 1
-                    for (int c = 0; c < P; ++c) {
-                        uint32_t v[32];
-                        t_ld32(o_at + 32 * c, v);
-                        t_wait_ld(v);
+                        for (int c = hc; c < P; c += 2) {
+                            uint32_t v[32];
+                            t_ld32(o_at + 32 * c, v);
+                            t_wait_ld(v);
 #pragma unroll
-                        for (int h = 1; h < 32; h <<= 1)
+                            for (int h = 1; h < 32; h <<= 1)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(e & h)) {
-                                    const float x = __uint_as_float(v[e]), y = __uint_as_float(v[e + h]);
-                                    v[e] = __float_as_uint(x + y);
-                                    v[e + h] = __float_as_uint(x - y);
-                                }
-                        if (!is) continue;
-                        uint32_t w[16];
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(e & h)) {
+                                        const float x = __uint_as_float(v[e]), y = __uint_as_float(v[e + h]);
+                                        v[e] = __float_as_uint(x + y);
+                                        v[e + h] = __float_as_uint(x - y);
+                                    }
+                            uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            w[e] = l > 0.0f ? bf16_bits2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv) : 0u;
+                            for (int e = 0; e < 16; ++e)
+                                w[e] = l > 0.0f ? bf16_bits2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv) : 0u;
+                            if (is)
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<uint4 *>(dst + 32 * c + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
-                    }
-                    if (is && p.a.lse)
+                                for (int e = 0; e < 16; e += 4)
+                                    *reinterpret_cast<uint4 *>(dst + 32 * c + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                        }
+                    if (is && hc == 0 && ok && p.a.lse)
                         p.a.lse[tok * p.a.heads_q + hq] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 }
             }
             fence_before();
+            pair_bar();                                  // both have read O, and pair_sh
         }
+        if (warp == 0 && lane == 0) p.table[blockIdx.x] = cut;
     }
     zero_rows<D>(kv, p.a, ge);
     fence_before();
@@ -950,18 +933,18 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
 template <int D>
 __global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ TcParams p) {
     constexpr int E = D / 32;
-    __shared__ int list[kMaxItems / 2], n_sh;
+    __shared__ int list[kMaxSmsT], flags[kMaxSmsT], n_sh;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int items = min(*p.head, kMaxItems);
-    if (items == 0) return;
+    for (int i = threadIdx.x; i < p.ctas; i += kThreads) flags[i] = p.table[i].flags;
+    __syncthreads();
     if (warp == 0) {                             // the row tiles that were cut, in order
         int n = 0;
-        for (int base = 0; base < items; base += 32) {
-            const bool cut = base + lane < items && p.table[base + lane].np > 1;
-            const unsigned in = __ballot_sync(0xffffffffu, cut);
-            if (cut) list[n + __popc(in & ((1u << lane) - 1))] = base + lane;
+        for (int base = 0; base < p.ctas; base += 32) {
+            const bool begins = base + lane < p.ctas && (flags[base + lane] & 4);
+            const unsigned in = __ballot_sync(0xffffffffu, begins);
+            if (begins) list[n + __popc(in & ((1u << lane) - 1))] = base + lane;
             n += __popc(in);
         }
         if (lane == 0) n_sh = n;
@@ -969,26 +952,29 @@ __global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ T
     __syncthreads();
     const int ru = p.geo.rows, g = p.geo.g, work = n_sh * ru;
     for (int w = blockIdx.x * (kThreads / 32) + warp; w < work; w += gridDim.x * (kThreads / 32)) {
-        const int idx = list[w / ru], i = w % ru;
-        const Split sp = p.table[idx];
+        const int cta = list[w / ru], i = w % ru;
+        const Cut sp = p.table[cta];
         if (sp.rt * ru + i >= sp.rows) continue;
-        const float2 *st = p.stat + static_cast<int64_t>(idx) * ru + i;
-        const float *src = p.part + (static_cast<int64_t>(idx) * ru + i) * D + lane * E;
+        int np = 1;                              // parts: the last of this CTA, the first of the next ones
+        while (cta + np < p.ctas && flags[cta + np++] == 1) {}
+        auto slot = [&](int k) { return static_cast<int64_t>(k ? 2 * (cta + k) : 2 * cta + 1); };
+        const float2 *st = p.stat + i;
+        const float *src = p.part + static_cast<int64_t>(i) * D + lane * E;
         const int64_t so = ru, po = static_cast<int64_t>(ru) * D;
         float mx = kNoneT;
-        for (int k = lane; k < sp.np; k += 32) mx = fmaxf(mx, st[k * so].x);
+        for (int k = lane; k < np; k += 32) mx = fmaxf(mx, st[slot(k) * so].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         float sum = 0.0f, v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.0f;
 #pragma unroll 4
-        for (int k = 0; k < sp.np; ++k) {
-            const float2 t = st[k * so];
+        for (int k = 0; k < np; ++k) {
+            const float2 t = st[slot(k) * so];
             const float f = ex2(t.x - mx);
             sum = fmaf(f, t.y, sum);
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = fmaf(f, src[k * po + e], v[e]);
+            for (int e = 0; e < E; ++e) v[e] = fmaf(f, src[slot(k) * po + e], v[e]);
         }
         warp_fwht<E, float>(v);
         const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
@@ -1011,15 +997,12 @@ constexpr int kMaxD = 128;
 template <class C>
 tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
     const int grid = dev.sms < kMaxSmsT ? dev.sms : kMaxSmsT;
-    const size_t slots = kMaxItems;
     unsigned char *at = static_cast<unsigned char *>(ws);
-    p.head = reinterpret_cast<int *>(at);
-    p.table = reinterpret_cast<Split *>(at + 256);
-    p.stat = reinterpret_cast<float2 *>(at + 256 + slots * sizeof(Split));
-    p.part = reinterpret_cast<float *>(at + 256 + slots * (sizeof(Split) + 128 * sizeof(float2)));
+    p.table = reinterpret_cast<Cut *>(at);
+    p.stat = reinterpret_cast<float2 *>(at + kMaxSmsT * sizeof(Cut));
+    p.part = reinterpret_cast<float *>(at + kMaxSmsT * (sizeof(Cut) + 2 * C::RU * sizeof(float2)));
     p.geo.rows = C::RU;
-    const int64_t units = p.kv.nseq * p.kv.heads * ((p.a.max_q * p.geo.g + C::RU - 1) / C::RU);
-    p.split = units <= kMaxItemsOf<C>() / 2;
+    p.ctas = grid;
     const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn_tc<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (fe != cudaSuccess) return cuda_fail(fe);
     cudaLaunchConfig_t cfg = {};
@@ -1034,7 +1017,6 @@ tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn_tc<C>, p);
     if (e != cudaSuccess) return cuda_fail(e);
-    if (!p.split) return TQ_OK;
     cfg.gridDim = dim3(grid * 4);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 0;
@@ -1046,8 +1028,7 @@ tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
 
 size_t kv4_tc_workspace_bytes(const DeviceInfo &dev) {
     (void)dev;
-    const size_t slots = kMaxItems;
-    return 256 + slots * (sizeof(Split) + 128 * (sizeof(float2) + kMaxD * sizeof(float)));
+    return kMaxSmsT * (sizeof(Cut) + 2 * 256 * (sizeof(float2) + kMaxD * sizeof(float)));
 }
 
 bool kv4_tc_takes(const tq_kv4 &kv, const Kv4Attn &a, int64_t rows) {
