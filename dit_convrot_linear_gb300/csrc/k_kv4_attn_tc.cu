@@ -52,6 +52,13 @@ constexpr int kMaxSmsT = 160;                // more SMs than this stay unused
 constexpr int kStart = 4;                    // tiles that a part's start and end stand for
 constexpr int kMinPart = 4;                  // fewest tiles a part
 
+// A build for the library's own tests expects bytes that no copy brings.
+#ifdef TQ_TEST_UNSET_BYTES
+constexpr uint32_t kUnset = TQ_TEST_UNSET_BYTES;
+#else
+constexpr uint32_t kUnset = 0;
+#endif
+
 template <int D_, int NQ_>
 struct TCfg {
     static constexpr int D = D_, NQ = NQ_;
@@ -99,7 +106,9 @@ __device__ __forceinline__ uint32_t sa(const void *p) { return smem_addr(p); }
 
 // A bounded wait by a whole warp, with one answer for all its lanes.  On expiry
 // the CTA's flag is raised, and every wait ends at once from then on; the roles
-// run through their loops without work, so that no barrier is left waiting.
+// run through their loops without work, so that no barrier is left waiting.  A
+// role that has given up waits and arrives no more: a barrier that stands still
+// has always completed one of the two parities, and an arrival too many faults.
 __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *status) {
     bool ok = mbar_try(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) {
@@ -229,6 +238,12 @@ __device__ __forceinline__ unsigned long long pair2(float a, float b) {
 
 __device__ __forceinline__ void split2(unsigned long long r, float &a, float &b) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 constexpr uint32_t kMinus8 = 0x80088008u;    // -8 2^-24 twice
@@ -414,6 +429,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
     if (warp == C::W_LD) {
         // ------------------------------------------------ loader
         int k = 0, sent = 0;                     // halves
+        bool ok = true;
         for (int64_t x = run0; x < run1;) {
             const Item it = item(x);
             x = it.next;
@@ -430,11 +446,12 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     if (num == 0) bad = true;
                 }
                 const uint32_t there = __ballot_sync(0xffffffffu, num != 0) & ((1u << kBlocks) - 1);
-                if (!tc_wait(raw_empty + 8 * s, ((k / kRing) & 1) ^ 1, &abort_sh, p.status)) continue;
+                ok = ok && tc_wait(raw_empty + 8 * s, ((k / kRing) & 1) ^ 1, &abort_sh, p.status);
+                if (!ok) continue;
                 if (lane == 0) {
                     raw_there[s] = there;
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(raw_full + 8 * s),
-                                 "r"(static_cast<uint32_t>(__popc(there)) * C::BLK)
+                                 "r"(static_cast<uint32_t>(__popc(there)) * C::BLK + kUnset)
                                  : "memory");
                     ++sent;
                 }
@@ -456,18 +473,20 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         const int dw = warp - C::W_DQ;                           // block dw of each tile
         const int row = lane % kKvBlock, part = lane / kKvBlock; // two lanes a token
         int k = 0;
+        bool ok = true;
         for (int64_t x = run0; x < run1;) {
             const Item it = item(x);
             x = it.next;
             for (int i = 0; i < it.n; ++i, ++k) {
                 const int kh = 2 * k + dw / kBlocks, rs = kh % kRing, s = k & 1;
                 const uint32_t par = ((k >> 1) & 1) ^ 1;
-                const bool ok = tc_wait(raw_full + 8 * rs, (kh / kRing) & 1, &abort_sh, p.status);
+                ok = ok && tc_wait(raw_full + 8 * rs, (kh / kRing) & 1, &abort_sh, p.status);
+                if (!ok) continue;
                 const unsigned char *blk = sm + C::oRaw + rs * C::RAW + (dw % kBlocks) * C::BLK;
                 const bool there = (raw_there[rs] >> (dw % kBlocks)) & 1u;
                 // the token's scales, and the block's largest
                 const int pos = it.at + i * kTileT + kKvBlock * dw + row;
-                const bool is = ok && there && pos >= it.lo && pos < it.hi;
+                const bool is = there && pos >= it.lo && pos < it.hi;
                 const float *sc = reinterpret_cast<const float *>(blk + 16 * D);
                 const float sk = is ? sc[row] : 0.0f, sv = is ? sc[16 + row] : 0.0f;
                 const uint32_t mk = __reduce_max_sync(0xffffffffu, __float_as_uint(sk)) >> 23;   // scales are not negative
@@ -476,8 +495,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 // scales over the power of two of the largest, times 2^14
                 const __half hk = __float2half_rn(sk * pow2i(-ek) * 16384.0f), hv = __float2half_rn(sv * pow2i(-ev) * 16384.0f);
                 // keys: 8 nibbles to 16 bytes in the order (0, 4), (1, 5), (2, 6), (3, 7)
-                const bool kok = tc_wait(k_empty + 8 * s, par, &abort_sh, p.status) && ok;
-                if (kok) {
+                ok = tc_wait(k_empty + 8 * s, par, &abort_sh, p.status);
+                if (ok) {
                     if (lane == 0) kv_info[k & 3][dw] = {pow2i(ek + 10), ev, there, 0};
                     const __half2 h2 = __half2half2(hk);
                     const uint32_t s1 = *reinterpret_cast<const uint32_t *>(&h2);
@@ -506,7 +525,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 }
                 // values: a lane a column, eight tokens at a time: its nibble of
                 // four words, each two tokens
-                if (tc_wait(v_empty + 8 * s, par, &abort_sh, p.status) && ok) {
+                ok = ok && tc_wait(v_empty + 8 * s, par, &abort_sh, p.status);
+                if (ok) {
                     const int sh = (lane & 2) * 4;               // nibbles 2 and 3 are 8 bits up
                     const uint32_t mask = lane & 1 ? 0x00F000F0u : 0x000F000Fu;
                     const uint32_t own = __half_as_ushort(hv);
@@ -696,7 +716,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 const int ke = mx > 0.0f ? min(13 - (static_cast<int>(__float_as_uint(mx) >> 23) - 127), 126) : 0;
                 const float up = pow2i(ke);
                 const int r = wq * 32 + rr;
-                if (l8 == 0) rowf_sh[q * 128 + r] = p.a.scale * kLog2eT * pow2i(-ke);
+                if (l8 == 0) rowf_sh[q * 128 + r] = fmaxf(p.a.scale * kLog2eT * pow2i(-ke), FLT_MIN);
                 unsigned char *dst = sm + C::oQ + q * C::KT + ((r >> 3) << 10) + (r & 7) * 16;
 #pragma unroll
                 for (int e = 0; e < N; e += 8) {
@@ -756,7 +776,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                             if (c < 3) t_ld16(s_at + 16 * (c + 1), v[(c + 1) & 1]);
                             float t0 = -INFINITY;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) t0 = fmaxf(t0, __uint_as_float(v[c & 1][e]));
+                            for (int e = 0; e < 16; e += 2) t0 = max3(t0, __uint_as_float(v[c & 1][e]), __uint_as_float(v[c & 1][e + 1]));
                             t = fmaxf(t, t0 * in[c].kx);
                         }
                         t *= f;
@@ -801,7 +821,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                             if (c < 3) t_ld16(s_at + 16 * (c + 1), v[(c + 1) & 1]);
                             const float2 ke = *reinterpret_cast<const float2 *>(&in[c].kx);
                             const int ei = __float_as_int(ke.y), ed = ei == kNoE ? 0 : max(ei - E, -100);    // <= 0
-                            const float F = f * ke.x, dm = static_cast<float>(ed) - m;
+                            const float F = fmaxf(f * ke.x, FLT_MIN), dm = static_cast<float>(ed) - m;
                             const unsigned long long f2 = pair2(F, F), m2 = pair2(dm, dm);
                             unsigned long long s2 = pair2(0.0f, 0.0f);
                             uint32_t pk[8];

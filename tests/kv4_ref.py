@@ -76,7 +76,7 @@ def sequence(pool, table_row, length, page):
     return k * sk[..., None], v * sv[..., None], sk, sv
 
 
-def attend(q, kc, vc, length, new, scale, causal, window):
+def attend(q, kc, vc, length, new, scale, causal, window, widened=False):
     """o, lse, bound on |o - kernel's| before the bf16 rounding, and on lse's:
     q [new, hq, dim] fp64, kc / vc [heads, length, dim] of the rotated basis.
 
@@ -85,7 +85,14 @@ def attend(q, kc, vc, length, new, scale, causal, window):
     a score moves by at most eps = 2^-10 scale sum |q'||k'|, a weight by a
     factor e^(+-2 eps) after its normalisation; a weight times a value scale is
     rounded to fp16, 2^-11 of it (2^-10 with the sums').  Turned back, a row's
-    error is at most the mean of its rotated ones times sqrt(dim)."""
+    error is at most the mean of its rotated ones times sqrt(dim).
+
+    widened (more than 16 query rows a key/value head): keys and values are
+    rounded too, a token's scale over its block's and its product with the code,
+    2^-11 each, so three roundings where one was: 2^-9 covers them.  A weight
+    over its value's scale below the row's largest by 2^14 loses bits, 2^-25 of
+    that largest one's (2^-22 with the scale's margin of 4 and code's of 8), and
+    a scale 2^28 below its block's largest 2^-39 of that one's."""
     n, hq, dim = q.shape
     heads = kc.shape[0]
     g = hq // heads
@@ -110,9 +117,11 @@ def attend(q, kc, vc, length, new, scale, causal, window):
             w /= tot
             o[i, h] = (w @ v) @ H
             lse[i, h] = m + np.log(tot)
-            eps = 2.0 ** -10 * scale * (np.abs(k) @ np.abs(qr)).max()
+            eps = 2.0 ** (-9 if widened else -10) * scale * (np.abs(k) @ np.abs(qr)).max()
             el[i, h] = eps + 2.0 ** -20 * (1 + abs(lse[i, h]))
-            eo[i, h] = (np.expm1(2 * eps) + 2.0 ** -10) * (w @ np.abs(v)).sum() / np.sqrt(dim)
+            eo[i, h] = (np.expm1(2 * eps) + 2.0 ** (-9 if widened else -10)) * (w @ np.abs(v)).sum() / np.sqrt(dim)
+            if widened:
+                eo[i, h] += (hi - lo) * 2.0 ** -22 * w.max() * np.abs(v).max() * np.sqrt(dim)
     return o, lse, eo, el
 
 

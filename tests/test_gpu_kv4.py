@@ -200,7 +200,7 @@ def test_append_bad_page_and_lengths_are_left_out(tq):
 
 # ------------------------------------------------------------------ attention
 
-def check(tq, w, heads_q, causal=True, window=0, seed=0, scale=None, Q=None, max_q=None, stream=None):
+def check(tq, w, heads_q, causal=True, window=0, seed=0, scale=None, Q=None, max_q=None, widened=False, l2=True):
     import torch
     dim = w.dim
     scale = dim ** -0.5 if scale is None else scale
@@ -222,7 +222,7 @@ def check(tq, w, heads_q, causal=True, window=0, seed=0, scale=None, Q=None, max
             continue
         kc, vc, _, _ = w.cached(b) if length else (np.zeros((w.heads, 0, dim)),) * 2 + (None, None)
         at = w.starts[b]
-        o, l, eo, el = ref.attend(f64(Q[at:at + new]), kc, vc, length, new, scale, causal, window)
+        o, l, eo, el = ref.attend(f64(Q[at:at + new]), kc, vc, length, new, scale, causal, window, widened)
         d = np.abs(got[at:at + new] - o)
         assert np.all(d <= 2.0 ** -8 * np.abs(o) * (1 + 2.0 ** -8) + eo[..., None] * (1 + 2.0 ** -8)), \
             f"sequence {b}: {np.nanmax(d)}"
@@ -232,7 +232,7 @@ def check(tq, w, heads_q, causal=True, window=0, seed=0, scale=None, Q=None, max
         assert np.all(np.abs(gb[fin] - l[fin]) <= el[fin])
         num += float((d ** 2).sum())
         den += float((o ** 2).sum())
-    assert num <= (2.0 ** -8) ** 2 * den or den == 0.0
+    assert not l2 or num <= (2.0 ** -8) ** 2 * den or den == 0.0
     return O, lse
 
 
