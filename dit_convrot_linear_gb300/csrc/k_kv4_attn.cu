@@ -17,11 +17,13 @@
 //     end of a run's part in a row tile, and over CTAs through the workspace by
 //     the one that comes last (in run order: the result does not depend on
 //     timing).
-//   - Products run on mma.sync m16n8k16: with 8 to 32 query rows against 32
+//   - Products run on mma.sync m16n8k16: with 8 or 16 query rows against 32
 //     tokens there is no 128-row tile for the tensor cores' own memory, and the
 //     operands come from registers: a nibble masked out of a word is the fp16
-//     subnormal u 2^-24 (odd nibbles, left in place, 16 times that), so a lane's
-//     16-byte load is a whole operand row without conversion.  Tokens are the
+//     subnormal u 2^-24, so a lane's 16-byte load is a whole operand row without
+//     conversion; an odd nibble is used with its even neighbour left below it (u
+//     + 16 u'), which the query's even element, less a sixteenth of the odd one,
+//     or the output's subtraction at the end, takes out.  Tokens are the
 //     rows (M) of S^T = K Q^T and the depth of O^T = V^T P^T, query rows the
 //     columns, so that few rows waste little.  The bias of 8 is taken off the
 //     scores by the accumulator's start value (-8 sum q) and off the output by
@@ -67,7 +69,7 @@ struct Cfg {
     static constexpr int QROW = 2 * D + 64;                  // bytes; rows 64 bytes apart mod 128: no bank conflicts
     static constexpr int OROW = D + 4;                       // floats
     static constexpr int OBUF = R * OROW * 4;
-    static constexpr int JOIN0 = 34816 / OBUF;               // output buffers: as many warps join at once
+    static constexpr int JOIN0 = (CTAS == 1 ? 67584 : 34816) / OBUF;     // output buffers: as many warps join at once
     static constexpr int JOIN = JOIN0 < 2 ? 2 : JOIN0 < NW ? JOIN0 : NW;
     // shared memory
     static constexpr int oQ = NW * STAGES * TILE;
@@ -261,15 +263,15 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         mine = {0, 0, 0};
         if (base + tid < kv.nseq) mine = kv_seq(kv, base + tid, bad);
         seqs_sh[tid] = mine;
-        if (p.wide) {                     // a warp a sequence
-            for (int i = warp; i < C::NT; i += NW) {
-                int64_t c = 0;
-                bool again = false;
-                if (base + i < kv.nseq) c = seq_cost_warp(ge, kv_seq(kv, base + i, again));
+        if (p.wide) {                     // many row tiles: a warp a sequence
+            const int here = static_cast<int>(kv.nseq - base < C::NT ? kv.nseq - base : C::NT);
+            __syncthreads();
+            for (int i = warp; i < here; i += NW) {
+                const int64_t c = seq_cost_warp(ge, seqs_sh[i]);
                 if (lane == 0) scan[i] = c;
             }
             __syncthreads();
-            head = scan[tid];
+            head = tid < here ? scan[tid] : 0;
         } else {
             head = seq_cost(ge, mine);
         }
@@ -997,19 +999,20 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 }
 
 constexpr int kMaxSlots = 8;                             // parts an SM (two a CTA), over the variants
-constexpr int kMaxPart = 2 * 4 * 8 * 256;                // slots an SM times R times D, over the variants
+constexpr int kMaxPart = 2 * 16 * 256;                   // slots an SM times R times D, over the variants
+constexpr int kMaxStat = 4 * 16;                         // slots an SM times R
 size_t count_bytes(const DeviceInfo &dev) { return (static_cast<size_t>(dev.sms) * kMaxSlots / 2 * 4 + 255) / 256 * 256; }
 
 template <class C>
 tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
-    static_assert(2 * C::CTAS <= kMaxSlots && 2 * C::CTAS * C::R * C::D <= kMaxPart && C::CTAS * C::R <= 64, "workspace");
+    static_assert(2 * C::CTAS <= kMaxSlots && 2 * C::CTAS * C::R * C::D <= kMaxPart && 2 * C::CTAS * C::R <= kMaxStat, "workspace");
     const int grid = dev.sms * C::CTAS;
     unsigned char *ws = static_cast<unsigned char *>(p.a.ws);
     p.count = reinterpret_cast<unsigned int *>(ws);
     p.stat = reinterpret_cast<float *>(ws + count_bytes(dev));
-    p.part = p.stat + static_cast<size_t>(dev.sms) * 2 * 64 * 2;
+    p.part = p.stat + static_cast<size_t>(dev.sms) * kMaxStat * 2;
     p.geo.rows = C::R;
-    p.wide = p.a.max_q * p.geo.g > C::R;
+    p.wide = p.a.max_q * p.geo.g > 4 * C::R;
     // Row tiles, if max_q is right: where there are several CTAs for each, each
     // is cut into parts of its own (at least kMinRun tiles, so a short context
     // is not cut at all: joining parts costs 4 us, a tile 0.1); else all tiles
@@ -1036,7 +1039,7 @@ tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
 }  // namespace
 
 size_t kv4_workspace_bytes(const DeviceInfo &dev) {
-    const size_t runs = count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * 64 * 2 + kMaxPart) * 4;
+    const size_t runs = count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * kMaxStat + kMaxPart) * 4;
     const size_t tc = kv4_tc_workspace_bytes(dev);
     return (runs + 255) / 256 * 256 + tc;
 }
@@ -1052,18 +1055,21 @@ tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceI
     if (!p.status) return TQ_ERR_DEVICE;
     const int64_t rows = a.max_q * p.geo.g;
     if (kv4_tc_takes(kv, a, rows)) {
-        const size_t runs = count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * 64 * 2 + kMaxPart) * 4;
+        const size_t runs = count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * kMaxStat + kMaxPart) * 4;
         return launch_kv4_attention_tc(kv, a, static_cast<unsigned char *>(a.ws) + (runs + 255) / 256 * 256, dev, s);
     }
+    // Up to 8 rows at a time, or 16 (rows beyond them are further row tiles).  A
+    // CTA with its eight warps' output buffers is faster than one of twelve warps
+    // that share four: 24 sequences of 4 rows' window of 4096, 57 us against 67;
+    // four contexts of 131072, 166 against 159.  32 rows at once took 107 us where
+    // two times 16 took 63: its accumulators leave a warp no room to overlap.
     if (kv.dim == 64) {
         if (rows <= 8) return launch<Cfg<64, 1, 8, 4, 2>>(p, dev, s);
-        if (rows <= 16) return launch<Cfg<64, 2, 8, 3, 2>>(p, dev, s);
-        return launch<Cfg<64, 4, 8, 4, 1>>(p, dev, s);
+        return launch<Cfg<64, 2, 8, 3, 2>>(p, dev, s);
     }
     if (kv.dim == 128) {
         if (rows <= 8) return launch<Cfg<128, 1, 8, 2, 2>>(p, dev, s);
-        if (rows <= 16) return launch<Cfg<128, 2, 12, 3, 1>>(p, dev, s);
-        return launch<Cfg<128, 4, 8, 4, 1>>(p, dev, s);
+        return launch<Cfg<128, 2, 8, 4, 1>>(p, dev, s);
     }
     if (rows <= 8) return launch<Cfg<256, 1, 8, 2, 1>>(p, dev, s);
     return launch<Cfg<256, 2, 8, 2, 1>>(p, dev, s);

@@ -1053,7 +1053,7 @@ size_t kv4_tc_workspace_bytes(const DeviceInfo &dev) {
 
 bool kv4_tc_takes(const tq_kv4 &kv, const Kv4Attn &a, int64_t rows) {
     (void)a;
-    return kv.dim <= kMaxD && kv.nseq <= kMaxSeqsT && rows > 16;
+    return kv.dim <= kMaxD && kv.nseq <= kMaxSeqsT && rows > 32;
 }
 
 tq_status launch_kv4_attention_tc(const tq_kv4 &kv, const Kv4Attn &a, void *ws, const DeviceInfo &dev, cudaStream_t s) {

@@ -87,7 +87,7 @@ def attend(q, kc, vc, length, new, scale, causal, window, widened=False):
     rounded to fp16, 2^-11 of it (2^-10 with the sums').  Turned back, a row's
     error is at most the mean of its rotated ones times sqrt(dim).
 
-    widened (more than 16 query rows a key/value head): keys and values are
+    widened (more than 32 query rows a key/value head): keys and values are
     rounded too, a token's scale over its block's and its product with the code,
     2^-11 each, so three roundings where one was: 2^-9 covers them.  A weight
     over its value's scale below the row's largest by 2^14 loses bits, 2^-25 of

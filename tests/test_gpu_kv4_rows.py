@@ -1,4 +1,4 @@
-"""Attention over the 4-bit cache for more than 16 query rows a key/value head
+"""Attention over the 4-bit cache for tens of query rows a key/value head
 (prompts, chunks of them, drafted tokens), against the 64-bit model on the GPU's
 own cache bytes.  Bars, set before the first run: kv4_ref.attend's bound for
 widened keys and values plus half a bf16 step, element by element, and relative
@@ -162,13 +162,13 @@ def test_expired_wait_is_reported(tq):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = tq.SIGNATURES[name]
     w = World(tq, [(700, 9), (20, 9)], 1, 128, 16, seed=23)
-    Q = rows(w.tokens, 2, 128, 13, outliers=False)
-    O = torch.zeros((w.tokens, 2, 128), dtype=torch.bfloat16, device="cuda")
+    Q = rows(w.tokens, 4, 128, 13, outliers=False)
+    O = torch.zeros((w.tokens, 4, 128), dtype=torch.bfloat16, device="cuda")
     ws = tq.kv4_workspace()
     s = torch.cuda.current_stream().cuda_stream
-    assert L.tq_kv4_attention(w.batch._p, Q.data_ptr(), 2, 256, 9, 0.1, 1, 0, O.data_ptr(), 256, None, ws.data_ptr(),
+    assert L.tq_kv4_attention(w.batch._p, Q.data_ptr(), 4, 512, 9, 0.1, 1, 0, O.data_ptr(), 512, None, ws.data_ptr(),
                               ws.numel(), s) == 0
     assert L.tq_device_status(s) == TIMEOUT and L.tq_device_status(s) == 0
     got = tq.kv4_attention(w.batch, Q, 0.1, ws)
     assert torch.equal(got, tq.kv4_attention(w.batch, Q, 0.1, tq.kv4_workspace()))
-    check(tq, w, 2, widened=True)
+    check(tq, w, 4, widened=True)
