@@ -881,32 +881,35 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         from = 0;
       }
 
-      // A warp joins a row over its sources: the warps' buffers, or the parts (a
+      // L lanes join a row over its sources: the warps' buffers, or the parts (a
       // piece of a part is a trip to far memory: each lane brings as many as the
       // rings hold, empty by now, into places of its own there).
-      constexpr int DEPTH = NW * S * C::TILE / (C::NT * 4 * E);
-      static_assert(DEPTH >= NW, "one step joins the warps");
+      constexpr int L = C::NT / R < 32 ? C::NT / R : 32, V = D / L;      // lanes a row, values a lane
+      constexpr int DEPTH = NW * S * C::TILE / (C::NT * 4 * V);
+      static_assert(DEPTH >= NW && L >= 16, "one step joins the warps");
       const bool keep = last || whole;
       const bool scaled = last || OWN;                   // else the buffers share the largest maximum
       const int np = last ? cl - cf + 1 : NW, no = scaled ? np : C::JOIN;
       const float2 *st = last ? reinterpret_cast<const float2 *>(p.stat) + static_cast<int64_t>(2) * cf * R : wstat;
       const int sstep = last ? 2 * R : R, sfirst = last ? R : 0;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (static_cast<int>(blockIdx.x) == cf ? 1 : 0);
-      const int rows = u.q.n * ge.g, r0 = u.rt * R;
+      const int rows = u.q.n * ge.g, r0 = u.rt * R, sub = lane % L;
 #pragma unroll 1
-      for (int i = warp; i < R && r0 + i < rows; i += NW) {
+      for (int base = warp * (32 / L); base < R && r0 + base < rows; base += C::NT / L) {
+        const int i = base + lane / L;
+        const bool is = r0 + i < rows;                   // (a last row without a partner: its lanes go along)
         auto bring = [&](int k0, int n) {
-            const float *src = p.part + static_cast<int64_t>(2) * cf * (R * D) + i * D + lane * E;
+            const float *src = p.part + static_cast<int64_t>(2) * cf * (R * D) + i * D + sub * V;
 #pragma unroll 1
             for (int k = 0; k < n; ++k) {
                 const int kk = k0 + k;
                 const float *from_ = src + static_cast<int64_t>(kk ? 2 * kk : 1) * (R * D);
-                const uint32_t to = smb + (k * C::NT + tid) * (4 * E);
-                if constexpr (E == 2) {
+                const uint32_t to = smb + (k * C::NT + tid) * (4 * V);
+                if constexpr (V == 2) {
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from_) : "memory");
                 } else {
 #pragma unroll
-                    for (int e = 0; e < E; e += 4)
+                    for (int e = 0; e < V; e += 4)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 4 * e), "l"(from_ + e)
                                      : "memory");
                 }
@@ -915,22 +918,22 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         if (last) bring(0, min(no, DEPTH));
         float mx = kNone;
 #pragma unroll 1
-        for (int k = lane; k < np; k += 32) mx = fmaxf(mx, st[k * sstep + (k ? 0 : sfirst) + i].x);
+        for (int k = sub; k < np; k += L) mx = fmaxf(mx, st[k * sstep + (k ? 0 : sfirst) + i].x);
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        float sum = 0.0f, v[8];
+        for (int x = 1; x < L; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        float sum = 0.0f, v[V];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        for (int e = 0; e < V; ++e) v[e] = 0.0f;
 #pragma unroll 1
-        for (int k0 = 0, in = 0; k0 < np; k0 += 32) {    // `in`: sources brought before this step's
+        for (int k0 = 0, in = 0; k0 < np; k0 += L) {     // `in`: sources brought before this step's
             float fac = 0.0f;
-            if (k0 + lane < np) {
-                const float2 t2 = st[(k0 + lane) * sstep + (k0 + lane ? 0 : sfirst) + i];
+            if (k0 + sub < np) {
+                const float2 t2 = st[(k0 + sub) * sstep + (k0 + sub ? 0 : sfirst) + i];
                 fac = ex2(t2.x - mx);
                 sum = fmaf(fac, t2.y, sum);
             }
             if (!scaled) fac = 1.0f;
-            const int n = min(32, no - k0);
+            const int n = min(L, no - k0);
 #pragma unroll 4
             for (int k = 0; k < n; ++k) {
                 const float *src;
@@ -941,42 +944,60 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                         bring(in, min(no - in, DEPTH));
                     }
                     if (at_ == 0 || at_ == DEPTH) asm volatile("cp.async.wait_all;" ::: "memory");
-                    src = reinterpret_cast<const float *>(sm + ((k0 + k - in) * C::NT + tid) * (4 * E));
+                    src = reinterpret_cast<const float *>(sm + ((k0 + k - in) * C::NT + tid) * (4 * V));
                 } else {
-                    src = obuf + k * (C::OBUF / 4) + i * C::OROW + lane * E;
+                    src = obuf + k * (C::OBUF / 4) + i * C::OROW + sub * V;
                 }
-                const float f = __shfl_sync(0xffffffffu, fac, k);
+                const float f = __shfl_sync(0xffffffffu, fac, k, L);
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = fmaf(f, src[e], v[e]);
+                for (int e = 0; e < V; ++e) v[e] = fmaf(f, src[e], v[e]);
             }
         }
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        for (int x = 1; x < L; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         if (!keep) {                                     // to the workspace
-            float *dst = p.part + (slot * R + i) * D + lane * E;
-            if constexpr (E == 2) {
+            float *dst = p.part + (slot * R + i) * D + sub * V;
+            if constexpr (V == 2) {
                 *reinterpret_cast<float2 *>(dst) = make_float2(v[0], v[1]);
             } else {
 #pragma unroll
-                for (int e = 0; e < E; e += 4)
+                for (int e = 0; e < V; e += 4)
                     *reinterpret_cast<float4 *>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             }
-            if (lane == 0) reinterpret_cast<float2 *>(p.stat)[slot * R + i] = make_float2(mx, sum);
+            if (sub == 0) reinterpret_cast<float2 *>(p.stat)[slot * R + i] = make_float2(mx, sum);
             continue;
         }
+        const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
+#pragma unroll
+        for (int h = 1; h < V; h <<= 1)                  // turned back
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (!(e & h)) {
+                    const float a = v[e], b = v[e + h];
+                    v[e] = a + b;
+                    v[e + h] = a - b;
+                }
+#pragma unroll
+        for (int x = 1; x < L; x <<= 1)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float b = __shfl_xor_sync(0xffffffffu, v[e], x);
+                v[e] = sub & x ? b - v[e] : v[e] + b;
+            }
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) w[e] = sum > 0.0f ? bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+        if (flag[0] || !is) continue;                    // the sums are not whole
         const int64_t tok = u.q.start + (r0 + i) / ge.g;
         const int hq = u.h * ge.g + (r0 + i) % ge.g;
-        const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
-        warp_fwht<E, float>(v);
-        uint32_t w[4];
+        uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + sub * V;
+        if constexpr (V == 2) *reinterpret_cast<uint32_t *>(dst) = w[0];
+        else if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        else
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) w[e] = sum > 0.0f ? bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
-        if (flag[0]) continue;                           // the sums are not whole
-        uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + lane * E;
-        if constexpr (E == 8) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t *>(dst) = w[0];
-        if (p.a.lse && lane == 0)
+            for (int e = 0; e < V / 2; e += 4)
+                *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+        if (p.a.lse && sub == 0)
             p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
       __syncthreads();
