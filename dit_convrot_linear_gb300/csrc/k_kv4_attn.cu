@@ -43,7 +43,8 @@ namespace tq {
 namespace {
 
 constexpr int kTile = 32;                    // tokens a tile: two blocks
-constexpr int kOver = 16;                    // tiles that starting and ending a row tile stand for
+constexpr int kOver = 40;                    // tiles that starting and ending a row tile stand for
+constexpr int kLeast = 16;                   // the shortest run
 constexpr int kMinRun = 48;                  // fewest tiles a part, where row tiles are cut on their own
 constexpr unsigned int kStatusKvTimeout = 128u;
 // A copy of the library built for its own tests lets every stage expect bytes
@@ -1040,7 +1041,7 @@ tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
     // into equal runs, of at least one a warp.
     const int64_t tiles = p.kv.nseq * p.kv.heads * ((p.a.max_q * p.geo.g + C::R - 1) / C::R);
     p.aligned = p.kv.nseq <= C::NT && tiles * 4 <= grid;
-    p.min_run = p.aligned ? kMinRun : kOver;
+    p.min_run = p.aligned ? kMinRun : kLeast;
     const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (fe != cudaSuccess) return cuda_fail(fe);
     cudaLaunchConfig_t cfg = {};
