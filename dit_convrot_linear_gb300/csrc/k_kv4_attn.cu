@@ -43,7 +43,6 @@ namespace tq {
 namespace {
 
 constexpr int kTile = 32;                    // tokens a tile: two blocks
-constexpr int kOver = 40;                    // tiles that starting and ending a row tile stand for
 constexpr int kLeast = 16;                   // the shortest run
 constexpr int kMinRun = 48;                  // fewest tiles a part, where row tiles are cut on their own
 constexpr unsigned int kStatusKvTimeout = 128u;
@@ -58,9 +57,12 @@ constexpr float kNone = -FLT_MAX;            // running maximum before any score
 constexpr float kSlack = 8.0f;               // log2 by which a score may pass it
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D_, int NR_, int NW_, int STAGES_, int CTAS_>
+template <int D_, int NR_, int NW_, int GW_, int STAGES_, int CTAS_>
 struct Cfg {
-    static constexpr int D = D_, NR = NR_, NW = NW_, STAGES = STAGES_, CTAS = CTAS_;
+    static constexpr int D = D_, NR = NR_, NW = NW_, GW = GW_, STAGES = STAGES_, CTAS = CTAS_;
+    static constexpr int G = NW / GW;                        // groups of GW warps, each with runs of its own
+    static constexpr int GT = GW * 32;
+    static constexpr int OVER = 40 / G;                      // tiles that starting and ending a row tile stand for
     static constexpr int R = 8 * NR;                         // query rows a row tile
     static constexpr int NT = NW * 32;                       // threads
     static constexpr int W = D / 32;                         // 32-bit words of a row a lane
@@ -74,25 +76,28 @@ struct Cfg {
     static constexpr int JOIN = JOIN0 < 2 ? 2 : JOIN0 < NW ? JOIN0 : NW;
     // shared memory
     static constexpr int oQ = NW * STAGES * TILE;
-    static constexpr int oO = oQ + R * QROW;
+    static constexpr int oO = oQ + (QREG ? 0 : G * R * QROW);    // (queries that go to registers lie under the output)
     static constexpr int oStat = oO + JOIN * OBUF;           // the float arrays named in the kernel
-    static constexpr int oBar = oStat + (2 * R + 2 * NW * R) * 4;
+    static constexpr int oBar = oStat + (2 * R * G + 2 * NW * R) * 4;
+    static constexpr int QGROUP = QREG ? GW * OBUF : R * QROW;
     static constexpr int oSeq = oBar + NW * STAGES * 8;
     static constexpr int oIter = oSeq + NT * static_cast<int>(sizeof(KvSeq));
     static constexpr int oFound = oIter + NW * 64;
-    static constexpr int oPart = oFound + 64;
-    static constexpr int oNext = oPart + 2 * 64;
-    static constexpr int oFlag = oNext + 2 * 64;
-    static constexpr int SMEM = oFlag + 16;
+    static constexpr int oPart = oFound + G * 64;
+    static constexpr int oNext = oPart + G * 2 * 64;
+    static constexpr int oFlag = oNext + G * 2 * 64;
+    static constexpr int SMEM = oFlag + 4 * (1 + 2 * G);
     static constexpr int oScan = oO;                         // before any output
-    static_assert(NT * 8 + NW * 8 <= JOIN * OBUF && SMEM <= 228 * 1024 / CTAS - 1024, "shared memory");
+    static_assert(NW % GW == 0 && (G == 1 || JOIN == NW) && NT * 8 + NW * 8 <= JOIN * OBUF && R * QROW <= OBUF * JOIN / G && SMEM <= 228 * 1024 / CTAS - 1024, "shared memory");
 };
 
 // A row tile's weight in the cutting: its tiles, and as many as starting and
 // ending a row tile takes as long as.
-__device__ __forceinline__ int weight(int tiles) { return tiles ? tiles + kOver : 0; }
+template <int OVER>
+__device__ __forceinline__ int weight(int tiles) { return tiles ? tiles + OVER : 0; }
 
 // Weight of all row tiles of a sequence (one head), by one thread.
+template <int OVER>
 __device__ __forceinline__ int64_t seq_cost(const Geo &ge, const KvSeq &q) {
     const int nrt = row_tiles(ge, q);
     int64_t sum = 0;
@@ -100,19 +105,20 @@ __device__ __forceinline__ int64_t seq_cost(const Geo &ge, const KvSeq &q) {
     for (int rt = 0; rt < nrt; ++rt) {
         int lo, hi, t0, c;
         range_of<kTile>(ge, q, rt, lo, hi, t0, c);
-        sum += weight(c);
+        sum += weight<OVER>(c);
     }
     return sum;
 }
 
 // The same by a warp.
+template <int OVER>
 __device__ __forceinline__ int64_t seq_cost_warp(const Geo &ge, const KvSeq &q) {
     const int nrt = row_tiles(ge, q), lane = threadIdx.x & 31;
     int64_t sum = 0;
     for (int rt = lane; rt < nrt; rt += 32) {
         int lo, hi, t0, c;
         range_of<kTile>(ge, q, rt, lo, hi, t0, c);
-        sum += weight(c);
+        sum += weight<OVER>(c);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -209,25 +215,34 @@ struct AttnParams {
 template <class C>
 __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_constant__ AttnParams p) {
     constexpr int D = C::D, NR = C::NR, NW = C::NW, R = C::R, W = C::W, S = C::STAGES;
+    constexpr int GW = C::GW, G = C::G, GT = C::GT, kOver = C::OVER;
     constexpr bool OWN = C::JOIN == NW;      // an output buffer a warp
     extern __shared__ __align__(128) unsigned char sm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t smb = smem_addr(sm);
-    float *rowf = reinterpret_cast<float *>(sm + C::oStat);
+    const int group = warp / GW, gw = warp % GW, gtid = tid % GT;
+    auto group_sync = [&]() {
+        if constexpr (G == 1) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(GT) : "memory");
+    };
+    float *rowf = reinterpret_cast<float *>(sm + C::oStat) + group * 2 * R;
     float *rowc = rowf + R;
-    float2 *wstat = reinterpret_cast<float2 *>(rowc + R);    // [NW][R] each warp's maximum and sum
+    // each warp's maximum and sum [GW][R]
+    float2 *wstat = reinterpret_cast<float2 *>(sm + C::oStat + G * 2 * R * 4) + group * GW * R;
     const uint32_t bar0 = smb + C::oBar + warp * S * 8;      // this warp's stages
     const uint32_t ring_at = smb + warp * S * C::TILE;
     int64_t *scan = reinterpret_cast<int64_t *>(sm + C::oScan);
     int64_t *wsum = scan + C::NT;
-    volatile int *flag = reinterpret_cast<volatile int *>(sm + C::oFlag);   // 0: a wait ran out, 1, 2: last to arrive
+    volatile int *flag = reinterpret_cast<volatile int *>(sm + C::oFlag);   // 0: a wait ran out; two a group: last to arrive
+    volatile int *came_last = flag + 1 + 2 * group;
     const tq_kv4 &kv = p.kv;
     const Geo &ge = p.geo;
     KvSeq *seqs_sh = reinterpret_cast<KvSeq *>(sm + C::oSeq);
     const KvSeq *seqs = kv.nseq <= C::NT ? seqs_sh : nullptr;
-    Found *found = reinterpret_cast<Found *>(sm + C::oFound);
-    Part *parts = reinterpret_cast<Part *>(sm + C::oPart);
-    float *obuf = reinterpret_cast<float *>(sm + C::oO);
+    Found *found = reinterpret_cast<Found *>(sm + C::oFound + group * 64);
+    Part *parts = reinterpret_cast<Part *>(sm + C::oPart + group * 128);
+    float *obuf = reinterpret_cast<float *>(sm + C::oO) + group * (OWN ? GW : 0) * (C::OBUF / 4);
+    unsigned char *qsm = sm + C::oQ + group * C::QGROUP;
 
     if (tid == 0) {
         for (int i = 0; i < NW * S; ++i)
@@ -268,13 +283,13 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             const int here = static_cast<int>(kv.nseq - base < C::NT ? kv.nseq - base : C::NT);
             __syncthreads();
             for (int i = warp; i < here; i += NW) {
-                const int64_t c = seq_cost_warp(ge, seqs_sh[i]);
+                const int64_t c = seq_cost_warp<kOver>(ge, seqs_sh[i]);
                 if (lane == 0) scan[i] = c;
             }
             __syncthreads();
             head = tid < here ? scan[tid] : 0;
         } else {
-            head = seq_cost(ge, mine);
+            head = seq_cost<kOver>(ge, mine);
         }
         block_scan(head * kv.heads, mine_at, step_sum);
     };
@@ -286,9 +301,10 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     }
     if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusIndex);
     auto leave_idle = [&]() { zero_rows<D>(kv, p.a, ge); };
-    int64_t per = quotient(total + gridDim.x - 1, gridDim.x);
+    const int64_t runs = static_cast<int64_t>(gridDim.x) * G;
+    int64_t per = quotient(total + runs - 1, runs);
     per = per < p.min_run ? p.min_run : per;
-    const int cta = static_cast<int>(blockIdx.x);
+    const int run = static_cast<int>(blockIdx.x) * G + group;
     Run u;
     int64_t uw = 0;                       // weight before the run's first row tile over the batch
     int n_all = 0;                        // the run's tiles
@@ -296,7 +312,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     bool aligned = false;                 // each row tile is cut on its own, into parts of about `per` tiles
     int acf = 0, acl = 0;                 // the CTAs that hold its parts then
     auto parts_of = [&](int64_t cost) { return cost < per ? cost > 0 : static_cast<int>(quotient(cost, per)); };
-    if (p.aligned) {
+    if (G == 1 && p.aligned) {
         int np = 0;                       // parts of a head of this thread's sequence
         const int nrt = row_tiles(ge, mine);
         for (int rt = 0; rt < nrt; ++rt) {
@@ -307,13 +323,13 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         int64_t np_at, np_sum;
         __syncthreads();
         block_scan(static_cast<int64_t>(np) * kv.heads, np_at, np_sum);
-        aligned = np_sum <= gridDim.x;
+        aligned = np_sum <= runs;
         if (aligned) {
-            if (cta >= np_sum) {
+            if (run >= np_sum) {
                 leave_idle();
                 return;
             }
-            const int64_t k = cta - np_at;
+            const int64_t k = run - np_at;
             if (k >= 0 && k < static_cast<int64_t>(np) * kv.heads) {
                 found->b = tid;
                 found->q = mine;
@@ -332,37 +348,39 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 if (k2 < n2) break;
                 k2 -= n2;
             }
-            acf = cta - k2;
+            acf = run - k2;
             acl = acf + n2 - 1;
             first = static_cast<int>(static_cast<int64_t>(u.cost) * k2 / n2);
             n_all = static_cast<int>(static_cast<int64_t>(u.cost) * (k2 + 1) / n2) - first;
         }
     }
     if (!aligned) {
-        const int64_t c0 = cta * per, c1 = c0 + per < total ? c0 + per : total;
-        if (c0 >= c1) {
-            leave_idle();
-            return;
-        }
+        const int64_t first0 = static_cast<int64_t>(blockIdx.x) * G * per;     // of the CTA's runs
         int64_t passed = 0;
         for (int64_t base = 0; base < kv.nseq; base += C::NT) {
             if (kv.nseq > C::NT) {        // one step: its scan is still at hand
                 __syncthreads();
                 scan_step(base);
             }
-            if (c0 < passed + step_sum) {
-                const int64_t k = c0 - passed - mine_at;
+            for (int g = 0; g < G; ++g) {
+                const int64_t k = first0 + g * per - passed - mine_at;
                 if (k >= 0 && k < head * kv.heads) {
-                    found->b = static_cast<int>(base + tid);
-                    found->q = mine;
-                    found->at = k;
-                    found->head = head;
+                    Found *f = reinterpret_cast<Found *>(sm + C::oFound + g * 64);
+                    f->b = static_cast<int>(base + tid);
+                    f->q = mine;
+                    f->at = k;
+                    f->head = head;
                 }
-                break;
             }
             passed += step_sum;
+            if (first0 + (G - 1) * per < passed) break;
         }
         __syncthreads();
+        const int64_t c0 = run * per, c1 = c0 + per < total ? c0 + per : total;
+        if (c0 >= c1) {
+            leave_idle();
+            return;
+        }
         u.b = found->b;
         u.q = found->q;
         u.nrt = row_tiles(ge, u.q);
@@ -373,7 +391,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             for (int base = 0; base < u.nrt; base += 32) {
                 int lo, hi, t0, c = 0;
                 if (base + lane < u.nrt) range_of<kTile>(ge, u.q, base + lane, lo, hi, t0, c);
-                c = weight(c);
+                c = weight<kOver>(c);
                 int64_t x = c;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -410,13 +428,14 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     }
     // The raw queries of the next row tile come while the tiles of this one are
     // read: a row a warp, and further ones by turns.
-    constexpr int E = D / 32, RW = (R + NW - 1) / NW;
+    constexpr int E = D / 32, RW = (R + GW - 1) / GW;
+    constexpr bool AHEAD = RW <= 2;                  // (more rows would cost the registers)
     uint32_t raw[RW][E / 2];
     auto load_queries = [&](const Run &v) {
 #pragma unroll
         for (int k = 0; k < RW; ++k) {
-            const int row = v.rt * R + warp + k * NW;
-            const bool is = warp + k * NW < R && row < v.q.n * ge.g;
+            const int row = v.rt * R + gw + k * GW;
+            const bool is = gw + k * GW < R && row < v.q.n * ge.g;
             const uint32_t *src = reinterpret_cast<const uint32_t *>(
                 p.a.Q + static_cast<int64_t>(v.q.start + (is ? row / ge.g : 0)) * p.a.ldq +
                 static_cast<int64_t>(v.h * ge.g + (is ? row % ge.g : 0)) * D + lane * E);
@@ -424,10 +443,10 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             for (int e = 0; e < E / 2; ++e) raw[k][e] = is ? src[e] : 0u;
         }
     };
-    load_queries(u);
+    if constexpr (AHEAD) load_queries(u);
 
     // ---------------------------------------------------- this warp's copies
-    // Its tiles are warp, warp + NW, .. of the run.  Lane i holds where tile i of
+    // Its tiles are gw, gw + GW, .. of the run.  Lane i holds where tile i of
     // 32 at a time lies (the number of its block in the pool plus one, two of them
     // where a page is half a tile; 0: nowhere), and the stages are filled in turn.
     uint32_t src0 = 0, src1 = 0;
@@ -438,10 +457,10 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         __syncwarp();
     }
     int n_send = n_all, it_start = -first;           // the iterator's row tile begins at this tile of the run
-    auto find_tiles = [&](int k0) {                  // tiles k0, k0 + NW, .. of the run
+    auto find_tiles = [&](int k0) {                  // tiles k0, k0 + GW, .. of the run
         Run *it = reinterpret_cast<Run *>(sm + C::oIter + warp * 64);
         Run v = *it;
-        const int k = k0 + lane * NW, end = min(k0 + 32 * NW, n_all);
+        const int k = k0 + lane * GW, end = min(k0 + 32 * GW, n_all);
         src0 = src1 = 0;
         for (;;) {
             if (k >= it_start && k < it_start + v.cost && k < n_all) {
@@ -486,7 +505,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         there = (there >> 2) | (((a0 ? (halves ? 1u : 3u) : 0u) | (a1 ? 2u : 0u)) << (2 * (S - 1)));
     };
 #pragma unroll 1
-    for (int i = 0; i < S; ++i) send(warp + i * NW, ring_at + i * C::TILE, bar0 + 8 * i);
+    for (int i = 0; i < S; ++i) send(gw + i * GW, ring_at + i * C::TILE, bar0 + 8 * i);
 
     // ---------------------------------------------------- parts of the run
     const int r = lane >> 2, j = lane & 3;
@@ -494,7 +513,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     int from = first;
     bool lost = false;
     uint32_t at = ring_at, bar = bar0, phase = 0;    // this warp's next stage
-    int next = warp;                      // and its next tile of the part
+    int next = gw;                        // and its next tile of the part
     // Row tiles in turn.  Parts whose others are elsewhere go to the workspace;
     // at the end of the run their arrivals are counted (once, for all of them),
     // and the CTA that comes last joins them.  A row tile's parts belong to CTAs
@@ -504,27 +523,27 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     // be fetched from far away.
     int nparts = 0, joined = -1;          // parts left elsewhere; parts looked at for the last join
     int cf = 0, cl = 0;
-    Run *next_sh = reinterpret_cast<Run *>(sm + C::oNext), *cur_sh = next_sh + 1;
+    Run *next_sh = reinterpret_cast<Run *>(sm + C::oNext + group * 128), *cur_sh = next_sh + 1;
     for (;;) {
       const bool last = done >= n_all;    // joining parts, not warps
       bool whole = true;
       if (last) {
         if (joined < 0) {
             if (nparts == 0) break;
-            __syncthreads();
-            if (tid == 0) {
+            group_sync();
+            if (gtid == 0) {
                 __threadfence();          // the CTA's stores, ordered before it by the barrier
                 for (int i = 0; i < nparts; ++i) {
                     const unsigned int old = atomicAdd(p.count + parts[i].cf, 1u);
-                    flag[1 + i] = old == static_cast<unsigned int>(parts[i].cl - parts[i].cf);
-                    if (flag[1 + i]) p.count[parts[i].cf] = 0u;
+                    came_last[i] = old == static_cast<unsigned int>(parts[i].cl - parts[i].cf);
+                    if (came_last[i]) p.count[parts[i].cf] = 0u;
                 }
                 __threadfence();
             }
-            __syncthreads();
+            group_sync();
             joined = 0;
         }
-        while (joined < nparts && !flag[1 + joined]) ++joined;
+        while (joined < nparts && !came_last[joined]) ++joined;
         if (joined == nparts) break;
         u = parts[joined].u;
         cf = parts[joined].cf;
@@ -534,12 +553,13 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         const int n = min(u.cost - from, n_all - done);
         const int rows = u.q.n * ge.g, r0 = u.rt * R;
 
+        if constexpr (!AHEAD) load_queries(u);
         // the row tile's queries: rotated, as fp16 in the order of the words'
         // nibbles (0, 4), (1, 5), (2, 6), (3, 7)
 #pragma unroll
         for (int k0 = 0; k0 < RW; ++k0) {
-            const int i = warp + k0 * NW;
-            if (R % NW && i >= R) break;
+            const int i = gw + k0 * GW;
+            if (R % GW && i >= R) break;
             float v[8];
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -560,7 +580,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             // an odd value's operand meets its nibble with 16 times it: over 16;
             // an even one's meets it alone once more, so that much is taken off
             float sum = 0.0f;
-            unsigned char *qrow = sm + C::oQ + i * C::QROW;
+            unsigned char *qrow = qsm + i * C::QROW;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const int d = lane * E + e, jj = d / (D / 4), w = (d % (D / 4)) / 8, nb = d % 8;
@@ -581,11 +601,11 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         if (done + n < n_all) {
             Run v = u;
             advance(kv, ge, seqs, v);
-            load_queries(v);
-            if (tid == 0) *next_sh = v;
+            if constexpr (AHEAD) load_queries(v);
+            if (gtid == 0) *next_sh = v;
         }
-        if (tid == 0) *cur_sh = u;
-        __syncthreads();
+        if (gtid == 0) *cur_sh = u;
+        group_sync();
 
         // per lane: query rows 8 nt + 2 j and 8 nt + 2 j + 1
         float f[NR][2], cst[NR][2], m[NR][2], l[NR][2];
@@ -611,12 +631,13 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     uint32_t t4[4];
-                    lds_words<4>(sm + C::oQ + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, t4);
+                    lds_words<4>(qsm + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, t4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) qf[nt][w][e] = t4[e];
                 }
             }
         }
+        if constexpr (C::QREG) group_sync();             // before any output lands there
         all_lo = __reduce_max_sync(0xffffffffu, all_lo);
         all_hi = __reduce_min_sync(0xffffffffu, all_hi);
 
@@ -635,7 +656,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         // this warp's tiles of the part
         const int tile0 = u.t0 + from;
 #pragma unroll 1
-        for (; next < n; next += NW) {
+        for (; next < n; next += GW) {
             if (!mbar_try(bar, phase)) {
                 if (lost || !mbar_wait_bounded(bar, phase, flag[0] ? 0 : kA16WaitLimit)) {
                     lost = true;
@@ -678,7 +699,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
 #pragma unroll
                             for (int e = 0; e < 4; ++e) q4[e] = qf[nt][w][e];
                         } else {
-                            lds_words<4>(sm + C::oQ + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, q4);
+                            lds_words<4>(qsm + (nt * 8 + r) * C::QROW + (w * 4 + j) * 16, q4);
                         }
                         mma(s[k][nt], a0, a1, a2, a3, q4[0], q4[1]);
                         mma(s[k][nt], b0, b1, b2, b3, q4[2], q4[3]);
@@ -807,7 +828,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             // every lane's reads of the stage before the next copy into it
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            send(done + next + S * NW, at, bar);
+            send(done + next + S * GW, at, bar);
             at += C::TILE;
             bar += 8;
             if (at == ring_at + S * C::TILE) {
@@ -825,13 +846,13 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
-                if (r == 0) wstat[warp * R + nt * 8 + 2 * j + c] = make_float2(m[nt][c], l[nt][c]);
+                if (r == 0) wstat[gw * R + nt * 8 + 2 * j + c] = make_float2(m[nt][c], l[nt][c]);
             }
         // Each warp's output into a buffer of its own, relative to its own
         // maximum; where there are fewer buffers than warps, in rounds, relative
         // to the rows' largest.
         float up[NR][2];
-        if constexpr (!OWN) __syncthreads();
+        if constexpr (!OWN) group_sync();
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
@@ -840,14 +861,14 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                 if constexpr (!OWN) {
                     float mx = kNone;
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wstat[w * R + nt * 8 + 2 * j + c].x);
+                    for (int w = 0; w < GW; ++w) mx = fmaxf(mx, wstat[w * R + nt * 8 + 2 * j + c].x);
                     up[nt][c] *= ex2(m[nt][c] - mx);
                 }
             }
 #pragma unroll 1
-        for (int round = 0; round * C::JOIN < NW; ++round) {
+        for (int round = 0; OWN ? round < 1 : round * C::JOIN < NW; ++round) {
             if (OWN || warp / C::JOIN == round) {
-                float *buf = obuf + (warp % C::JOIN) * (C::OBUF / 4);
+                float *buf = obuf + (OWN ? gw : warp % C::JOIN) * (C::OBUF / 4);
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
@@ -867,14 +888,14 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                             *dst = v;
                         }
             }
-            __syncthreads();
+            group_sync();
         }
 
         whole = from == 0 && n == u.cost;
         if (!whole) {
             cf = aligned ? acf : static_cast<int>(quotient(uw + kOver, per));
             cl = aligned ? acl : static_cast<int>(quotient(uw + kOver + u.cost - 1, per));
-            if (tid == 0) parts[nparts] = {u, cf, cl};
+            if (gtid == 0) parts[nparts] = {u, cf, cl};
             ++nparts;
         }
         done += n;
@@ -885,18 +906,20 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
       // L lanes join a row over its sources: the warps' buffers, or the parts (a
       // piece of a part is a trip to far memory: each lane brings as many as the
       // rings hold, empty by now, into places of its own there).
-      constexpr int L = C::NT / R < 32 ? C::NT / R : 32, V = D / L;      // lanes a row, values a lane
-      constexpr int DEPTH = NW * S * C::TILE / (C::NT * 4 * V);
-      static_assert(DEPTH >= NW && L >= 16, "one step joins the warps");
+      constexpr int L0 = GT / R < D / 4 ? GT / R : D / 4;
+      constexpr int L = L0 >= 32 ? 32 : L0 >= 16 ? 16 : 8, V = D / L;   // lanes a row, values a lane
+      constexpr int DEPTH = GW * S * C::TILE / (GT * 4 * V);
+      static_assert(DEPTH >= 1 && L >= GW, "one step joins the warps");
+      const uint32_t gring = smb + group * GW * S * C::TILE;
       const bool keep = last || whole;
       const bool scaled = last || OWN;                   // else the buffers share the largest maximum
-      const int np = last ? cl - cf + 1 : NW, no = scaled ? np : C::JOIN;
-      const float2 *st = last ? reinterpret_cast<const float2 *>(p.stat) + static_cast<int64_t>(2) * cf * R : wstat;
-      const int sstep = last ? 2 * R : R, sfirst = last ? R : 0;
-      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (static_cast<int>(blockIdx.x) == cf ? 1 : 0);
+      const int np = last ? cl - cf + 1 : GW, no = scaled ? np : C::JOIN;
+      const float2 *st = reinterpret_cast<const float2 *>(p.stat) + static_cast<int64_t>(2) * cf * R;
+      constexpr int sstep = 2 * R, sfirst = R;
+      const int64_t slot = 2 * static_cast<int64_t>(run) + (run == cf ? 1 : 0);
       const int rows = u.q.n * ge.g, r0 = u.rt * R, sub = lane % L;
 #pragma unroll 1
-      for (int base = warp * (32 / L); base < R && r0 + base < rows; base += C::NT / L) {
+      for (int base = gw * (32 / L); base < R && r0 + base < rows; base += GT / L) {
         const int i = base + lane / L;
         const bool is = r0 + i < rows;                   // (a last row without a partner: its lanes go along)
         auto bring = [&](int k0, int n) {
@@ -905,21 +928,19 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             for (int k = 0; k < n; ++k) {
                 const int kk = k0 + k;
                 const float *from_ = src + static_cast<int64_t>(kk ? 2 * kk : 1) * (R * D);
-                const uint32_t to = smb + (k * C::NT + tid) * (4 * V);
-                if constexpr (V == 2) {
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from_) : "memory");
-                } else {
+                const uint32_t to = gring + (k * GT + gtid) * (4 * V);
 #pragma unroll
-                    for (int e = 0; e < V; e += 4)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 4 * e), "l"(from_ + e)
-                                     : "memory");
-                }
+                for (int e = 0; e < V; e += 4)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 4 * e), "l"(from_ + e) : "memory");
             }
         };
         if (last) bring(0, min(no, DEPTH));
+        // (another join on this SM may have left a line with this one's statistics
+        // in L1 before they were written: past it)
+        auto stat = [&](int k) { return last ? __ldcg(st + k * sstep + (k ? 0 : sfirst) + i) : wstat[k * R + i]; };
         float mx = kNone;
 #pragma unroll 1
-        for (int k = sub; k < np; k += L) mx = fmaxf(mx, st[k * sstep + (k ? 0 : sfirst) + i].x);
+        for (int k = sub; k < np; k += L) mx = fmaxf(mx, stat(k).x);
 #pragma unroll
         for (int x = 1; x < L; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
         float sum = 0.0f, v[V];
@@ -929,7 +950,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         for (int k0 = 0, in = 0; k0 < np; k0 += L) {     // `in`: sources brought before this step's
             float fac = 0.0f;
             if (k0 + sub < np) {
-                const float2 t2 = st[(k0 + sub) * sstep + (k0 + sub ? 0 : sfirst) + i];
+                const float2 t2 = stat(k0 + sub);
                 fac = ex2(t2.x - mx);
                 sum = fmaf(fac, t2.y, sum);
             }
@@ -945,7 +966,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                         bring(in, min(no - in, DEPTH));
                     }
                     if (at_ == 0 || at_ == DEPTH) asm volatile("cp.async.wait_all;" ::: "memory");
-                    src = reinterpret_cast<const float *>(sm + ((k0 + k - in) * C::NT + tid) * (4 * V));
+                    src = reinterpret_cast<const float *>(sm + (gring - smb) + ((k0 + k - in) * GT + gtid) * (4 * V));
                 } else {
                     src = obuf + k * (C::OBUF / 4) + i * C::OROW + sub * V;
                 }
@@ -958,13 +979,9 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         for (int x = 1; x < L; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         if (!keep) {                                     // to the workspace
             float *dst = p.part + (slot * R + i) * D + sub * V;
-            if constexpr (V == 2) {
-                *reinterpret_cast<float2 *>(dst) = make_float2(v[0], v[1]);
-            } else {
 #pragma unroll
-                for (int e = 0; e < V; e += 4)
-                    *reinterpret_cast<float4 *>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-            }
+            for (int e = 0; e < V; e += 4)
+                *reinterpret_cast<float4 *>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             if (sub == 0) reinterpret_cast<float2 *>(p.stat)[slot * R + i] = make_float2(mx, sum);
             continue;
         }
@@ -992,8 +1009,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         const int64_t tok = u.q.start + (r0 + i) / ge.g;
         const int hq = u.h * ge.g + (r0 + i) % ge.g;
         uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + sub * V;
-        if constexpr (V == 2) *reinterpret_cast<uint32_t *>(dst) = w[0];
-        else if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
         else
 #pragma unroll
             for (int e = 0; e < V / 2; e += 4)
@@ -1001,7 +1017,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
         if (p.a.lse && sub == 0)
             p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
-      __syncthreads();
+      group_sync();
       if (!last && done < n_all) {
         uw += u.cost + kOver;
         u = *next_sh;
@@ -1020,14 +1036,14 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     }
 }
 
-constexpr int kMaxSlots = 8;                             // parts an SM (two a CTA), over the variants
-constexpr int kMaxPart = 2 * 16 * 256;                   // slots an SM times R times D, over the variants
-constexpr int kMaxStat = 4 * 16;                         // slots an SM times R
+constexpr int kMaxSlots = 8;                             // parts an SM (two a run), over the variants
+constexpr int kMaxPart = 8 * 8 * 128;                    // slots an SM times R times D, over the variants
+constexpr int kMaxStat = 8 * 16;                         // slots an SM times R
 size_t count_bytes(const DeviceInfo &dev) { return (static_cast<size_t>(dev.sms) * kMaxSlots / 2 * 4 + 255) / 256 * 256; }
 
 template <class C>
 tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
-    static_assert(2 * C::CTAS <= kMaxSlots && 2 * C::CTAS * C::R * C::D <= kMaxPart && 2 * C::CTAS * C::R <= kMaxStat, "workspace");
+    static_assert(2 * C::CTAS * C::G <= kMaxSlots && 2 * C::CTAS * C::G * C::R * C::D <= kMaxPart && 2 * C::CTAS * C::G * C::R <= kMaxStat, "workspace");
     const int grid = dev.sms * C::CTAS;
     unsigned char *ws = static_cast<unsigned char *>(p.a.ws);
     p.count = reinterpret_cast<unsigned int *>(ws);
@@ -1040,7 +1056,7 @@ tq_status launch(AttnParams &p, const DeviceInfo &dev, cudaStream_t s) {
     // is not cut at all: joining parts costs 4 us, a tile 0.1); else all tiles
     // into equal runs, of at least one a warp.
     const int64_t tiles = p.kv.nseq * p.kv.heads * ((p.a.max_q * p.geo.g + C::R - 1) / C::R);
-    p.aligned = p.kv.nseq <= C::NT && tiles * 4 <= grid;
+    p.aligned = C::G == 1 && p.kv.nseq <= C::NT && tiles * 4 <= grid;
     p.min_run = p.aligned ? kMinRun : kLeast;
     const cudaError_t fe = cudaFuncSetAttribute(k_kv4_attn<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (fe != cudaSuccess) return cuda_fail(fe);
@@ -1080,21 +1096,28 @@ tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceI
         const size_t runs = count_bytes(dev) + static_cast<size_t>(dev.sms) * (2 * kMaxStat + kMaxPart) * 4;
         return launch_kv4_attention_tc(kv, a, static_cast<unsigned char *>(a.ws) + (runs + 255) / 256 * 256, dev, s);
     }
-    // Up to 8 rows at a time, or 16 (rows beyond them are further row tiles).  A
-    // CTA with its eight warps' output buffers is faster than one of twelve warps
-    // that share four: 24 sequences of 4 rows' window of 4096, 57 us against 67;
-    // four contexts of 131072, 166 against 159.  32 rows at once took 107 us where
-    // two times 16 took 63: its accumulators leave a warp no room to overlap.
+    // Up to 8 rows at a time, or 16 (rows beyond them are further row tiles).  32
+    // at once took 107 us where two times 16 took 63 (24 sequences of up to 5
+    // drafted tokens, window 4096): its accumulators leave a warp no room to
+    // overlap.  Where there are more than a quarter as many row tiles as SMs, two
+    // groups of four warps a CTA with runs of their own, so that one starts or
+    // ends a row tile while the other streams: those drafts 50 us against 56, 64
+    // sequences of up to 4096 47 against 52, 256 of up to 700 59 against 78.
+    // With fewer, all eight warps on one part: 4 contexts of 131072 97 us against
+    // 104, one of 777 10.5 against 12.5.  (Groups of two: 48, 57, 60, 113, 19.)
+    const bool wide = rows > 8;
+    const int64_t tiles = kv.nseq * kv.heads * ((rows + (wide ? 15 : 7)) / (wide ? 16 : 8));
+    const bool many = 4 * tiles > dev.sms;
     if (kv.dim == 64) {
-        if (rows <= 8) return launch<Cfg<64, 1, 8, 4, 2>>(p, dev, s);
-        return launch<Cfg<64, 2, 8, 3, 2>>(p, dev, s);
+        if (wide) return many ? launch<Cfg<64, 2, 8, 4, 3, 2>>(p, dev, s) : launch<Cfg<64, 2, 8, 8, 3, 2>>(p, dev, s);
+        return many ? launch<Cfg<64, 1, 8, 4, 4, 2>>(p, dev, s) : launch<Cfg<64, 1, 8, 8, 4, 2>>(p, dev, s);
     }
     if (kv.dim == 128) {
-        if (rows <= 8) return launch<Cfg<128, 1, 8, 2, 2>>(p, dev, s);
-        return launch<Cfg<128, 2, 8, 4, 1>>(p, dev, s);
+        if (wide) return many ? launch<Cfg<128, 2, 8, 4, 3, 1>>(p, dev, s) : launch<Cfg<128, 2, 8, 8, 4, 1>>(p, dev, s);
+        return many ? launch<Cfg<128, 1, 8, 4, 2, 2>>(p, dev, s) : launch<Cfg<128, 1, 8, 8, 2, 2>>(p, dev, s);
     }
-    if (rows <= 8) return launch<Cfg<256, 1, 8, 2, 1>>(p, dev, s);
-    return launch<Cfg<256, 2, 8, 2, 1>>(p, dev, s);
+    if (wide) return launch<Cfg<256, 2, 8, 8, 2, 1>>(p, dev, s);     // (no room for a buffer a warp)
+    return many ? launch<Cfg<256, 1, 8, 4, 2, 1>>(p, dev, s) : launch<Cfg<256, 1, 8, 8, 2, 1>>(p, dev, s);
 }
 
 }  // namespace tq

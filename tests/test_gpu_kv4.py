@@ -258,6 +258,16 @@ def test_several_rows_masks(tq, causal, window, dim, heads_q):
     check(tq, World(tq, seqs, 2, dim, 32, seed=window % 97 + dim), heads_q, causal, window)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("heads,heads_q,new", [(4, 16, 1), (4, 48, 1), (4, 16, 3), (3, 3, 1)])
+def test_many_row_tiles(tq, dim, heads, heads_q, new):
+    """Row tiles for every SM, a few much longer than the rest."""
+    rng = np.random.default_rng(dim + heads_q)
+    seqs = [(int(n), int(rng.integers(1, new + 1))) for n in rng.integers(0, 90, 24)]
+    seqs[3], seqs[17] = (3000, new), (700, new)
+    check(tq, World(tq, seqs, heads, dim, 32, seed=dim), heads_q)
+
+
 @pytest.mark.parametrize("max_q", [1, 2, 8, 1000])
 def test_max_q_is_a_hint(tq, max_q):
     """The same result, within the bars, whatever the hint says."""
