@@ -113,8 +113,12 @@ def rows(tokens, heads, dim, seed, outliers=True):
 # ------------------------------------------------------------ append and read
 
 @pytest.mark.parametrize("dim,page,heads", [(64, 16, 2), (128, 16, 8), (128, 64, 1), (256, 32, 3), (128, 128, 2)])
-def test_append_and_read(tq, dim, page, heads):
+@pytest.mark.parametrize("many", [0, 1])
+def test_append_and_read(tq, dim, page, heads, many):
+    """Rows on their own, and by blocks (where they are many)."""
     seqs = [(1, 1), (37, 5), (16, 16), (129, 129), (200, 1), (0, 2), (33, 0)]
+    if many:
+        seqs += [(1500, 1400), (2001, 2001), (7, 9), (4000 // heads, 3990 // heads), (1000, 1000), (77, 60)]
     w = World(tq, seqs, heads, dim, page, seed=dim + page)
     kv = rows(w.tokens, 2 * heads, dim, 5)
     kv[3] = 0                                               # a row of zeros
@@ -196,6 +200,31 @@ def test_append_bad_page_and_lengths_are_left_out(tq):
     b = tq.KV4Batch(w.cache, w.tab, w.lens, st, w.tokens, 20)
     tq.kv4_append(b, kv[:, :1], kv[:, 1:])
     assert tq.device_status() == INDEX and tq.device_status() == 0
+
+
+def test_long_append_bad_page_and_more_rows_than_tokens(tq):
+    """The same for calls of many rows: a page outside the pool, and a sequence
+    with more rows than tokens (its first ones are before position 0)."""
+    import torch
+    w = World(tq, [(2500, 2500), (40, 700), (333, 333)], heads=4, dim=128, page=32, seed=40)
+    kv = rows(w.tokens, 8, 128, 41)
+    before = w.bytes().copy()
+    w.tab[0, 7] = -3                             # rows 224 .. 255 of sequence 0
+    tq.kv4_append(w.batch, kv[:, :4], kv[:, 4:])
+    assert tq.device_status() == INDEX and tq.device_status() == 0
+    after = w.bytes()
+    lost = w.table[0, 7]
+    assert np.array_equal(before[lost], after[lost])
+    fill = torch.ones(w.tokens, 4, 128, dtype=torch.bfloat16, device="cuda")
+    K, V = tq.kv4_read(w.batch, K=fill.clone(), V=fill.clone())
+    assert tq.device_status() == INDEX
+    for out, x in ((K, kv[:, :4]), (V, kv[:, 4:])):
+        assert not out[224:256].any() and out[:224].any(dim=2).all() and out[256:2500].any(dim=2).all()
+        assert not out[2500:3160].any() and out[3160:].any(dim=2).all()
+        # 4-bit rounding leaves about 0.1 of a normal row
+        keep = np.r_[0:224, 256:2500, 3160:w.tokens]
+        d = f64(out)[keep] - f64(x)[keep]
+        assert (d ** 2).sum() <= 0.2 ** 2 * (f64(x)[keep] ** 2).sum()
 
 
 # ------------------------------------------------------------------ attention
