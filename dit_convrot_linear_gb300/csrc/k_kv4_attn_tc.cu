@@ -41,6 +41,10 @@ constexpr int kTileT = 128;                  // positions a tile
 constexpr int kHalf = 64;                    // positions copied and widened at a time
 constexpr int kBlocks = kHalf / kKvBlock;    // blocks of them
 constexpr int kRing = 3;                     // halves in the ring
+// Barriers of their arrival: two a stage, in turn, so that each serves the warps
+// of one half alone (a wait tells only two neighbouring phases apart, and the
+// warps that take every second use of a stage would miss one between).
+constexpr int kFull = 2 * kRing;
 constexpr unsigned int kStatusKvTcTimeout = 256u;
 constexpr float kNoneT = -FLT_MAX;
 constexpr float kSlackT = 8.0f;
@@ -265,26 +269,25 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
     __shared__ uint32_t raw_there[kRing];
     __shared__ float rowf_sh[RU];                            // a row's factor
     // what a row's two threads exchange: their maxima (in 16 bits, rounded up:
-    // any bound serves that both take), and their sums
-    __shared__ union { uint16_t max[2][2][RU]; float sum[2][RU]; } pair_sh;
+    // any bound serves that both take), and their sums.  A row's own place serves
+    // both: its two warps alone keep step.
+    __shared__ union { uint16_t max[2][2]; float sum[2]; } pair_sh[RU];
     __shared__ Info kv_info[4][8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const tq_kv4 &kv = p.kv;
     const Geo &ge = p.geo;
     const uint32_t smb = sa(sm);
     const uint32_t bar = smb + C::oBar;
-    const uint32_t raw_full = bar, raw_empty = bar + 24, k_full = bar + 48, k_empty = bar + 64, v_full = bar + 80,
-                   v_empty = bar + 96, s_full = bar + 112, p_full = bar + 128, q_full = bar + 144, pv_done = bar + 160,
-                   all_done = bar + 176;
+    const uint32_t raw_full = bar, raw_empty = bar + 48, k_full = bar + 72, k_empty = bar + 88, v_full = bar + 104,
+                   v_empty = bar + 120, s_full = bar + 136, p_full = bar + 152, q_full = bar + 168, pv_done = bar + 184,
+                   all_done = bar + 200;
 
     if (tid == 0) {
         auto init = [&](uint32_t b, int n) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n) : "memory");
         };
-        for (int i = 0; i < kRing; ++i) {
-            init(raw_full + 8 * i, 1);
-            init(raw_empty + 8 * i, 4);
-        }
+        for (int i = 0; i < kFull; ++i) init(raw_full + 8 * i, 1);
+        for (int i = 0; i < kRing; ++i) init(raw_empty + 8 * i, 4);
         for (int i = 0; i < 2; ++i) {
             init(k_full + 8 * i, 8);
             init(k_empty + 8 * i, 1);
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 if (!ok) continue;
                 if (lane == 0) {
                     raw_there[s] = there;
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(raw_full + 8 * s),
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(raw_full + 8 * (k % kFull)),
                                  "r"(static_cast<uint32_t>(__popc(there)) * C::BLK + kUnset)
                                  : "memory");
                     ++sent;
@@ -459,14 +462,14 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 if (num && lane % each == 0)
                     bulk_copy(smb + C::oRaw + s * C::RAW + lane * C::BLK,
                               reinterpret_cast<uint64_t>(kv.pool) + static_cast<uint64_t>(num - 1) * C::BLK,
-                              each * C::BLK, raw_full + 8 * s);
+                              each * C::BLK, raw_full + 8 * (k % kFull));
                 __syncwarp();
             }
         }
         if (bad) atomicOr(p.status, kStatusIndex);
         if (lane == 0)                           // never leave with copies landing
             for (int i = sent > kRing ? sent - kRing : 0; i < sent; ++i)
-                mbar_wait_bounded(raw_full + 8 * (i % kRing), (i / kRing) & 1, kA16DrainLimit);
+                mbar_wait_bounded(raw_full + 8 * (i % kFull), (i / kFull) & 1, kA16DrainLimit);
         __syncwarp();
     } else if (warp >= C::W_DQ && warp < C::W_DQ + 8) {
         // ------------------------------------------------ widening
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
             for (int i = 0; i < it.n; ++i, ++k) {
                 const int kh = 2 * k + dw / kBlocks, rs = kh % kRing, s = k & 1;
                 const uint32_t par = ((k >> 1) & 1) ^ 1;
-                ok = ok && tc_wait(raw_full + 8 * rs, (kh / kRing) & 1, &abort_sh, p.status);
+                ok = ok && tc_wait(raw_full + 8 * (kh % kFull), (kh / kFull) & 1, &abort_sh, p.status);
                 if (!ok) continue;
                 const unsigned char *blk = sm + C::oRaw + rs * C::RAW + (dw % kBlocks) * C::BLK;
                 const bool there = (raw_there[rs] >> (dw % kBlocks)) & 1u;
@@ -674,6 +677,11 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
         auto pair_bar = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + q * 4 + wq) : "memory"); };
         int k = 0;
         bool ok = true;
+        // Product k - 1 with the values has ended.  With two row tiles, tile k's
+        // scores tell; with one they come ahead of it, and it is waited for before
+        // tile k's weights are handed over: a wait tells only two neighbouring
+        // phases apart, so none may be left out, nor come when the next has ended.
+        auto product_before = [&]() { ok = ok && (k == 0 || tc_wait(pv_done + 8 * q, (k - 1) & 1, &abort_sh, p.status)); };
         for (int64_t x = run0; x < run1;) {
             const Item it = item(x);
             x = it.next;
@@ -782,9 +790,9 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                         t *= f;
                     }
                     const uint16_t up16 = __bfloat16_as_ushort(__float2bfloat16_ru(t));
-                    pair_sh.max[k & 1][hc][row] = up16;
+                    pair_sh[row].max[k & 1][hc] = up16;
                     pair_bar();
-                    t = fmaxf(bf16_bits_to_f32(up16), bf16_bits_to_f32(pair_sh.max[k & 1][hc ^ 1][row]));
+                    t = fmaxf(bf16_bits_to_f32(up16), bf16_bits_to_f32(pair_sh[row].max[k & 1][hc ^ 1]));
                     // E: an exponent that no value's scale passes (4 times the
                     // first ones', so that it is seldom raised)
                     const bool newE = i == 0 || evm > E;
@@ -795,7 +803,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                         m = to;
                         l *= fix;
                         if (i > 0) {
-                            if constexpr (NQ == 1) ok = tc_wait(pv_done, (k - 1) & 1, &abort_sh, p.status);
+                            if constexpr (NQ == 1) product_before();
                             fence_after();
                             const float of = fix * pow2i(E0 - E);
                             if (ok)
@@ -845,18 +853,19 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     }
                     t_wait_st();
                 }
+                if constexpr (NQ == 1) product_before();
                 fence_before();
                 __syncwarp();
                 if (lane == 0 && ok) arrive(p_full + 8 * slot);
             }
             // the output: O is whole once the last product has ended
-            ok = ok && tc_wait(pv_done + 8 * q, (k - 1) & 1, &abort_sh, p.status);
+            product_before();
             fence_after();
             if (mine > 0) {
                 pair_bar();                              // the last maxima have been read
-                pair_sh.sum[hc][row] = l;
+                pair_sh[row].sum[hc] = l;
                 pair_bar();
-                l += pair_sh.sum[hc ^ 1][row];
+                l += pair_sh[row].sum[hc ^ 1];
                 if (it.slot >= 0) {
                     const float up = pow2i(E + 10);
                     if (is && hc == 0) p.stat[static_cast<int64_t>(it.slot) * RU + row] = make_float2(m, l);
