@@ -321,6 +321,44 @@ def test_one_long_sequence_and_many_sequences(tq):
     check(tq, World(tq, seqs, 1, 64, 16, seed=14), 2)
 
 
+@pytest.mark.parametrize("heads_q,new", [(8, 1), (16, 5)])
+def test_sums_over_very_long_contexts(tq, heads_q, new):
+    """Four sequences of 131072 tokens on the same pages, near-equal weights:
+    outputs a hundredth of the values, of sums that must not carry the codes' bias
+    of 8 along.  Relative L2 at most 0.0025: bf16's half step leaves 0.0017 at
+    most (2^-9 / sqrt(3) of a value just above a power of two), weights rounded
+    to fp16 2^-11 / sqrt(3)."""
+    import torch
+    heads, dim, page, n = 8, 128, 128, 131072
+    rng = np.random.default_rng(50)
+    np_ = n // page
+    kc, vc = (np.clip(np.rint(rng.normal(size=(np_, heads, page // 16, 16, dim)) * 2.6), -7, 7).astype(np.int64)
+              for _ in range(2))
+    sk, sv = (rng.uniform(a, 2 * a, (np_, heads, page // 16, 16)).astype(np.float32) for a in (0.05, 0.25))
+    pool = torch.from_numpy(ref.pack(kc, vc, sk, sv).reshape(-1)).cuda()
+    cache = tq.KV4Cache(np_, page, heads, dim, pool=pool)
+    tab = torch.arange(np_, dtype=torch.int32, device="cuda").expand(4, np_).contiguous()
+    batch = tq.KV4Batch(cache, tab, dev32([n] * 4), dev32(np.arange(5) * new), 4 * new, new)
+    Q = rows(4 * new, heads_q, dim, 51, outliers=False)
+    O = f64(tq.kv4_attention(batch, Q, dim ** -0.5, tq.kv4_workspace()))
+    assert tq.device_status() == 0
+    H, q = ref.hadamard(dim), f64(Q)
+    num = den = 0.0
+    for h in range(heads):
+        k = (kc[:, h] * sk[:, h, ..., None].astype(np.float64)).reshape(n, dim)
+        v = (vc[:, h] * sv[:, h, ..., None].astype(np.float64)).reshape(n, dim)
+        g = heads_q // heads
+        for b in (0, 3):
+            for i in range(new):
+                x = (q[b * new + i, h * g:(h + 1) * g] @ H) @ k.T * dim ** -0.5
+                x[:, n - new + i + 1:] = -np.inf
+                w = np.exp(x - x.max(1, keepdims=True))
+                o = (w / w.sum(1, keepdims=True)) @ v @ H
+                num += ((O[b * new + i, h * g:(h + 1) * g] - o) ** 2).sum()
+                den += (o ** 2).sum()
+    assert num <= 0.0025 ** 2 * den, (num / den) ** 0.5
+
+
 def test_value_scales_of_all_sizes(tq):
     """Values whose scales span 2^-20 .. 2^20 within a sequence, and all tiny."""
     check(tq, World(tq, [(300, 1), (90, 2)], 1, 128, 16, seed=15, vspread=20.0), 4)
