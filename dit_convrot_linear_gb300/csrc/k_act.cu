@@ -448,6 +448,9 @@ constexpr int kRotqMaxWarps = 17;   // 64 full groups (4 a warp) and a tail warp
 // rstd = 1 / sqrt(mean(h^2) + eps) from one more barrier, gamma in `scale`; y
 // is not rounded before the transform.  h and bf16(y) are written where `ro`
 // asks for them, and without `out` the row ends there.
+// (4032 rows of 4096 with the residual written, tiled: 49 us, 20 for the bytes; 45 % of
+// the issue slots, and each row waits for its sum.  61 rows to bf16 3.2 us,
+// one row and its product's operand 8.3.)
 
 // CTAs an SM should hold, by warps a CTA: a thread keeps about 80 registers
 constexpr int rotq_min_blocks(int maxw) {

@@ -7,10 +7,11 @@
 //   - The query rows of a sequence and key/value head (its tokens times the
 //     heads that share it) are cut into row tiles of R = 8 NR, the positions a
 //     row tile may see into tiles of 32.  All (sequence, head, row tile, tile)
-//     quadruples, in this order, are cut into equal runs, one a CTA, so ragged
-//     lengths fill the GPU evenly and a single long row is split over all of
-//     it.  The lengths are read on the device; each CTA finds its run by a scan.
-//   - A CTA's warps take turns at its tiles, each with a ring of stages of its
+//     quadruples, in this order, are cut into equal runs, one a group of warps
+//     (a CTA's eight, or two groups of four), so ragged lengths fill the GPU
+//     evenly and a single long row is split over all of it.  The lengths are read
+//     on the device; each CTA finds its runs by a scan.
+//   - A group's warps take turns at its tiles, each with a ring of stages of its
 //     own that it fills by bulk copies (a block of 16 tokens, keys, values and
 //     scales, lies in one piece) as it frees them; no warp waits for another.
 //     Each keeps its own maximum, sum and output, joined in shared memory at the
@@ -33,6 +34,15 @@
 //     times its value's scale is rounded to fp16 relative to the largest scale
 //     met (2^-12 of itself, an order below the cache's own rounding); sums stay
 //     in fp32.
+//
+// Measured (8 key/value heads of 128, 32 query heads), against the time of the
+// bytes at the card's copy rate: four contexts of 131072 98 us, 84 (86 %); 64
+// sequences of up to 4096 47, 25; 24 of up to 5 drafted tokens, window 4096, 51,
+// 15; one of 777 tokens (14 heads of 64 on 2) 10.7, of which a launch that does
+// nothing is 2 to 3.  The long ones are bound by the stream.  The others by what
+// happens once a run: about 6 us until the first tile is at hand (lengths, then
+// pages, then blocks, each a trip to memory that waits for the one before), 3 to
+// 4 us where a row tile ends and the next begins, 3 to 5 us to join parts.
 
 #include <cfloat>
 

@@ -814,8 +814,10 @@ size_t tq_kv4_workspace_bytes(void);
  *
  * Scores, softmax statistics and sums are fp32.  The rotated query is rounded
  * to fp16 (relative to its row's largest value), and so is each weight times
- * its value's scale: half the relative error of bf16's last place an eighth
- * time over, below the 4-bit rounding of what they meet.
+ * its value's scale; with more than 32 query rows a key/value head, keys and
+ * values too (relative to their block of 16 tokens).  Each such rounding is
+ * within 2^-11 of the value, an eighth of bf16's and far below the 4-bit
+ * rounding of the keys and values themselves.
  *
  *   Q        bf16: head i of row t at Q + t * ldq + i * dim (K's rules).
  *   heads_q  a multiple of kv->heads, at most 64 times it, else TQ_ERR_SHAPE.
