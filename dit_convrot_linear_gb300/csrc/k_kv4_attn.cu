@@ -96,7 +96,7 @@ struct Cfg {
     static constexpr int oFound = oIter + NW * 64;
     static constexpr int oPart = oFound + G * 64;
     static constexpr int oNext = oPart + G * 2 * 64;
-    static constexpr int oFlag = oNext + G * 2 * 64;
+    static constexpr int oFlag = oNext + G * 3 * 64;
     static constexpr int SMEM = oFlag + 4 * (1 + 2 * G);
     static constexpr int oScan = oO;                         // before any output
     static_assert(NW % GW == 0 && (G == 1 || JOIN == NW) && NT * 8 + NW * 8 <= JOIN * OBUF && R * QROW <= OBUF * JOIN / G && SMEM <= 228 * 1024 / CTAS - 1024, "shared memory");
@@ -208,7 +208,7 @@ struct Part {                                // a part of a row tile whose other
     Run u;
     int cf, cl;                              // CTAs that hold its parts
 };
-static_assert(2 * sizeof(Run) <= 128 && sizeof(Part) <= 64 && sizeof(Found) <= 64, "shared memory");
+static_assert(3 * sizeof(Run) <= 192 && sizeof(Part) <= 64 && sizeof(Found) <= 64, "shared memory");
 
 struct AttnParams {
     tq_kv4 kv;
@@ -534,7 +534,9 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
     // be fetched from far away.
     int nparts = 0, joined = -1;          // parts left elsewhere; parts looked at for the last join
     int cf = 0, cl = 0;
-    Run *next_sh = reinterpret_cast<Run *>(sm + C::oNext + group * 128), *cur_sh = next_sh + 1;
+    // the next row tile, in two places in turn (a slow warp may still read the last)
+    Run *next_sh = reinterpret_cast<Run *>(sm + C::oNext + group * 192), *cur_sh = next_sh + 2;
+    int turn = 0;
     for (;;) {
       const bool last = done >= n_all;    // joining parts, not warps
       bool whole = true;
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             Run v = u;
             advance(kv, ge, seqs, v);
             if constexpr (AHEAD) load_queries(v);
-            if (gtid == 0) *next_sh = v;
+            if (gtid == 0) next_sh[turn] = v;
         }
         if (gtid == 0) *cur_sh = u;
         group_sync();
@@ -1049,7 +1051,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
       group_sync();
       if (!last && done < n_all) {
         uw += u.cost + kOver;
-        u = *next_sh;
+        u = next_sh[turn];
+        turn ^= 1;
       }
     }
     zero_rows<D>(kv, p.a, ge);
