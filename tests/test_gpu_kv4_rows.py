@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 
 import kv4_ref as ref
-from test_gpu_kv4 import INDEX, TIMEOUT, World, check, f64, rows
+from test_gpu_kv4 import INDEX, TIMEOUT, World, check, dev32, f64, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -132,6 +132,32 @@ def test_few_and_many_rows_share_a_workspace(tq):
         assert torch.equal(tq.kv4_attention(a.batch, qa, 0.09, ws), oa)
         assert torch.equal(tq.kv4_attention(b.batch, qb, 0.09, ws), ob)
     assert tq.device_status() == 0
+
+
+@pytest.mark.parametrize("seqs,heads,heads_q,dim", [
+    ([(300, 300)], 8, 8, 128), ([(4096, 1024)], 4, 16, 128), ([(900, 33), (2000, 70), (64, 40)], 2, 4, 64),
+    ([(3000, 5), (70, 3), (1500, 1)] * 6, 2, 8, 128), ([(2000, 1), (90, 1)] * 16, 4, 16, 256)])
+def test_results_do_not_depend_on_timing(tq, seqs, heads, heads_q, dim):
+    """The same call from cold caches, from an idle device and back to back, its
+    results the same bits: no warp reads what another has yet to write."""
+    import torch
+    w = World(tq, seqs, heads, dim, 16, seed=60, fill=False, noise=False)
+    full = np.array([n for n, _ in seqs])
+    kv = rows(int(full.sum()), 2 * heads, dim, 61)
+    tq.kv4_append(tq.KV4Batch(w.cache, w.tab, w.lens, dev32(np.concatenate([[0], full.cumsum()])), int(full.sum()),
+                              int(full.max())), kv[:, :heads], kv[:, heads:])
+    Q = rows(w.tokens, heads_q, dim, 62, outliers=False)
+    ws, flush = tq.kv4_workspace(), torch.empty(400 << 20, dtype=torch.uint8, device="cuda")
+    outs = []
+    for i in range(18):
+        if i % 3 == 0:
+            flush.fill_(i)
+        if i % 3 == 1:
+            torch.cuda.synchronize()
+        lse = torch.empty(w.tokens, heads_q, device="cuda")
+        outs.append((tq.kv4_attention(w.batch, Q, dim ** -0.5, ws, lse=lse), lse))
+    assert tq.device_status() == 0
+    assert all(torch.equal(o, outs[0][0]) and torch.equal(x, outs[0][1]) for o, x in outs)
 
 
 def test_bad_page_is_left_out(tq):
