@@ -31,8 +31,8 @@
 // relative to their row's, block's or maximum's scale.
 //
 // Measured (8 key/value heads of 128, 32 query heads): 1024 rows over 16384
-// tokens 305 us, 139 for their operations at a large library product's rate (mma.sync
-// took 1056); four times 4096 rows after 4096 992 us, 503.  A pair of row tiles
+// tokens 300 us, 139 for their operations at a large library product's rate (mma.sync
+// took 1056); the last 4096 rows of as many 972 us, 503.  A pair of row tiles
 // takes about 4800 cycles a tile of positions where its products alone would take
 // 2050: a row tile's softmax (2900) and its products (1700, slowed by the widening
 // warps' stores: both operands of S come from shared memory, all of its bandwidth)
@@ -1056,7 +1056,7 @@ tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn_tc<C>, p);
     if (e != cudaSuccess) return cuda_fail(e);
-    cfg.gridDim = dim3(grid * 4);
+    cfg.gridDim = dim3(grid * 8);                // (1024 rows over 16384: 300 us, with half as many 305)
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, k_kv4_join<C::D>, p);
