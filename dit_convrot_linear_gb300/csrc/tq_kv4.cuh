@@ -19,9 +19,10 @@ struct KvSeq {
     int len, n, start;
 };
 
+// Tokens a sequence can have: positions and the ends of their tiles fit 32 bits.
 __device__ __forceinline__ int64_t kv_capacity(const tq_kv4 &kv) {
     const int64_t c = kv.table_cols * kv.page_size;
-    return c < 0x7fffffff ? c : 0x7fffffff;
+    return c < 0x7fffff00 ? c : 0x7fffff00;
 }
 
 // Sequence b, its arrays checked: a length outside 0 .. capacity is taken as

@@ -770,10 +770,10 @@ typedef struct {
  * position 0 (an unused slot of a fixed batch: kv_len = 0) is not written, sees
  * nothing, and reads as zeros.  The device arrays are checked as they are read:
  * a page number outside the pool (its tokens are left out), a length below 0 or
- * above table_cols * page_size (taken as the nearest) and a row range outside
- * 0 .. tokens or running backwards (taken as empty) set TQ_ERR_INDEX.  Rows that
- * no sequence owns are not written.  A page number past a sequence's length is
- * not read.
+ * above table_cols * page_size or 2^31 - 256 (taken as the nearest) and a row
+ * range outside 0 .. tokens or running backwards (taken as empty) set
+ * TQ_ERR_INDEX.  Rows that no sequence owns are not written.  A page number past
+ * a sequence's length is not read.
  */
 
 #define TQ_KV4_MAX_SEQS 65536
