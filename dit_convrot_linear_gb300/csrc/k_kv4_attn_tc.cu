@@ -278,10 +278,15 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
     };
     __shared__ uint32_t raw_there[kRing];
     __shared__ float rowf_sh[RU];                            // a row's factor
-    // what a row's two threads exchange: their maxima (in 16 bits, rounded up:
-    // any bound serves that both take), and their sums.  A row's own place serves
-    // both: its two warps alone keep step.
-    __shared__ union { uint16_t max[2][2]; float sum[2]; } pair_sh[RU];
+    // What a row's two threads exchange: their maxima, and their sums.  A row's own
+    // place serves both: its two warps alone keep step.  The maxima stay in fp32:
+    // a bound above them by log2 units (16 bits of a score of thousands are off by
+    // tens) would leave the weights below fp16's range.  With two row tiles one
+    // place a half serves every tile: tile k + 1's scores come only after both
+    // warps have handed over tile k's weights, and so have read its maxima; with
+    // one they come ahead, so there are two places in turn.
+    constexpr int PLACES = NQ == 2 ? 1 : 2;
+    __shared__ union { float max[PLACES][2]; float sum[2]; } pair_sh[RU];
     __shared__ Info kv_info[4][8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const tq_kv4 &kv = p.kv;
@@ -799,10 +804,9 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                         }
                         t *= f;
                     }
-                    const uint16_t up16 = __bfloat16_as_ushort(__float2bfloat16_ru(t));
-                    pair_sh[row].max[k & 1][hc] = up16;
+                    pair_sh[row].max[k % PLACES][hc] = t;
                     pair_bar();
-                    t = fmaxf(bf16_bits_to_f32(up16), bf16_bits_to_f32(pair_sh[row].max[k & 1][hc ^ 1]));
+                    t = fmaxf(t, pair_sh[row].max[k % PLACES][hc ^ 1]);
                     // E: an exponent that no value's scale passes (4 times the
                     // first ones', so that it is seldom raised)
                     const bool newE = i == 0 || evm > E;

@@ -1,0 +1,63 @@
+"""The 4-bit cache and attention over it where a call can go wrong quietly:
+scores with a large common part.  Against the 64-bit model on the GPU's own cache bytes."""
+import numpy as np
+import pytest
+
+import kv4_ref as ref
+from test_gpu_kv4 import World, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def laid(tq, seqs, dim, codes_k, scales_k, codes_v, scales_v, heads=1, page=16):
+    """A World whose sequences hold the given codes [heads, length, dim] and
+    scales [heads, length] (one set for all)."""
+    import torch
+    w = World(tq, seqs, heads, dim, page, seed=1, fill=False, noise=False)
+    pool = np.zeros((w.npages, heads, page // 16, ref.block_bytes(dim)), dtype=np.uint8)
+    for b, (n, _) in enumerate(seqs):
+        w._store(pool, b, codes_k[:, :n], scales_k[:, :n], 0)
+        w._store(pool, b, codes_v[:, :n], scales_v[:, :n], 1)
+    w.pool.copy_(torch.from_numpy(pool.reshape(-1)))
+    return w
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,heads_q", [(1, 4), (5, 4), (20, 4), (50, 4), (300, 2)])
+def test_scores_with_a_large_common_part(tq, dim, new, heads_q):
+    """Scores of thousands that differ by a few: every key has 4 s in the one
+    value that a constant query meets, s = 1, 1 + 2^-10 or 1 + 2^-9, all exact in
+    fp16.  So a score's roundings are fp32's, below 2^-12 in the exponent (2^-24
+    of 19000 and its factors), and those of a query's factor to fp16 are common to
+    a row (2^-11 of the log sum).  Bars: weights and values rounded to fp16, a common factor of 2^-11 on
+    differences of at most 32, 2^-6 a weight's for the others than the first;
+    relative L2 2^-7 over the call, an element 2^-6 of its weighted values."""
+    rng = np.random.default_rng(dim + new)
+    n = 400
+    ck = rng.integers(-7, 8, (1, n, dim))
+    ck[..., 0] = 4
+    sk = 1.0 + rng.integers(0, 3, (1, n)) / 1024.0
+    cv, sv, _ = ref.quantise(rng.normal(size=(1, n, dim)), dim)
+    w = laid(tq, [(n, new), (n - 130, new if new < 200 else 1)], dim, ck, sk, cv, sv)
+    import torch
+    size = np.array([45, -45, 94, -94, 188, -188, 400, -400]) * (1.0 if dim == 64 else 0.5)
+    q = np.zeros((w.tokens, heads_q, dim))
+    q += rng.choice(size, (w.tokens, heads_q))[..., None]
+    Q = torch.from_numpy(q).cuda().bfloat16()
+    O = torch.full_like(Q, float("nan"))
+    lse = torch.empty(w.tokens, heads_q, device="cuda")
+    tq.kv4_attention(w.batch, Q, 1.0, tq.kv4_workspace(), O=O, lse=lse)
+    assert tq.device_status() == 0
+    got, gl = f64(O), f64(lse)
+    num = den = 0.0
+    for b, (length, m) in enumerate(w.seqs):
+        kc, vc, _, _ = w.cached(b)
+        at = w.starts[b]
+        qb = f64(Q[at:at + m])
+        o, l, _, _ = ref.attend(qb, kc, vc, length, m, 1.0, True, 0)
+        d = np.abs(got[at:at + m] - o)
+        assert np.all(d <= 2.0 ** -8 * np.abs(o) + 2.0 ** -6 * np.abs(vc).sum(-1).max() / np.sqrt(dim))
+        assert np.all(np.abs(gl[at:at + m] - l) <= 2.0 ** -10 * np.abs(l))
+        num += float((d ** 2).sum())
+        den += float((o ** 2).sum())
+    assert num <= (2.0 ** -7) ** 2 * den, (num / den) ** 0.5
