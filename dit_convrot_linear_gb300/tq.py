@@ -861,10 +861,14 @@ class KV4Batch:
             _req(t, what, dtype=torch.int32, nbytes=4 * k)
             if not t.is_contiguous():
                 raise ValueError(f"{what} must be contiguous")
+        # one sequence has no step to the next: its row's length stands for it
+        ldt = table.stride(0) if n > 1 else max(table.stride(0), cols)
+        if ldt < cols:
+            raise ValueError(f"table: rows of {cols} pages {ldt} apart overlap (an expanded tensor needs .contiguous())")
         self.cache, self.tokens, self.max_q = cache, tokens, max_q
         self._keep = (table, kv_len, q_start)
         self._c = KV4C(_ptr(cache.pool), cache.npages, cache.page_size, cache.heads, cache.dim, _ptr(table), cols,
-                       max(table.stride(0), cols), _ptr(kv_len), _ptr(q_start), n, tokens)
+                       ldt, _ptr(kv_len), _ptr(q_start), n, tokens)
         self._p = ctypes.addressof(self._c)
 
 

@@ -1,10 +1,11 @@
 """The 4-bit cache and attention over it where a call can go wrong quietly:
-scores with a large common part.  Against the 64-bit model on the GPU's own cache bytes."""
+scores with a large common part, padded page tables.  Against the 64-bit model
+on the GPU's own cache bytes."""
 import numpy as np
 import pytest
 
 import kv4_ref as ref
-from test_gpu_kv4 import World, f64
+from test_gpu_kv4 import World, dev32, f64, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,19 @@ def test_scores_with_a_large_common_part(tq, dim, new, heads_q):
         num += float((d ** 2).sum())
         den += float((o ** 2).sum())
     assert num <= (2.0 ** -7) ** 2 * den, (num / den) ** 0.5
+
+
+def test_page_table_with_wide_rows(tq):
+    """A table that is part of a wider one gives the dense table's results; an
+    expanded one is refused before anything runs."""
+    import torch
+    w = World(tq, [(100, 2), (33, 1), (70, 5)], 2, 64, 16, seed=60)
+    Q = rows(w.tokens, 4, 64, 61, outliers=False)
+    wide = torch.full((3, w.cols + 5), -1, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + w.cols] = w.tab
+    b = tq.KV4Batch(w.cache, wide[:, 2:2 + w.cols], w.lens, dev32(w.starts), w.tokens, 5)
+    w.batch.max_q = 5
+    assert torch.equal(tq.kv4_attention(b, Q, 0.1, tq.kv4_workspace()), tq.kv4_attention(w.batch, Q, 0.1, tq.kv4_workspace()))
+    assert tq.device_status() == 0
+    with pytest.raises(ValueError):
+        tq.KV4Batch(w.cache, w.tab[:1].expand(3, w.cols), w.lens, dev32(w.starts), w.tokens, 5)
