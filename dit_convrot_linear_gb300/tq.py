@@ -779,7 +779,6 @@ class RopeSpec:
         self.pairs, self.interleaved = pairs, bool(interleaved)
         self._c = RopeSpecC(None, 0, _ptr(inv_freq), None if axis is None else ctypes.addressof(self.axis), 1, pairs,
                             int(self.interleaved))
-        self._p = ctypes.addressof(self._c)
 
 
 def _heads(X, what, tokens=None, heads=None, dim=None) -> int:
@@ -809,12 +808,13 @@ def rope(X, pos, spec: RopeSpec, Y=None, stream=None):
     ldx = _heads(X, "X")
     ldy = ldx if Y is X else _heads(Y, "Y", T, H, D)
     ldpos = _rows(pos, "pos", torch.int32, 1, T)
-    c = spec._c
+    # a copy of the call's own: calls of several threads may share the spec
+    c = RopeSpecC.from_buffer_copy(spec._c)
     c.pos = pos.data_ptr()
-    c.naxes = pos.shape[0]
-    c.ldpos = ldpos if c.naxes > 1 else T
-    _check((_lib or load()).tq_rope(X.data_ptr(), T, H, D, ldx, spec._p, Y.data_ptr(), ldy, _raw_stream(X, stream)),
-           "tq_rope")
+    c.naxes = naxes = pos.shape[0]
+    c.ldpos = ldpos if naxes > 1 else T
+    _check((_lib or load()).tq_rope(X.data_ptr(), T, H, D, ldx, ctypes.addressof(c), Y.data_ptr(), ldy,
+                                    _raw_stream(X, stream)), "tq_rope")
     return Y
 
 

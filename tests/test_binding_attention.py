@@ -68,3 +68,41 @@ def test_page_table_whose_rows_overlap_is_refused(binding, strides):
 def test_page_table_row_step(binding, shape, strides, ldt):
     """The step between rows as it is; one row has none, its length stands for it."""
     assert batch(binding, shape, strides)._c.ldt == ldt
+
+
+def test_two_threads_share_a_rope_spec(binding, monkeypatch):
+    """A model's spec serves calls from several threads: each call's positions
+    are its own, whatever another call does between its set-up and its launch."""
+    import threading
+
+    import torch
+    spec = binding.RopeSpec(Stub(torch.float32, (64,), at=0x500), axis=[0, 1] * 32)
+    before = bytes(spec._c)
+    both, seen, wrong = threading.Barrier(2, timeout=20), {}, []
+
+    def tq_rope(x, tokens, heads, dim, ldx, c, y, ldy, stream):
+        both.wait()                          # both calls are set up
+        s = binding.RopeSpecC.from_address(c)
+        seen[x] = (s.pos, s.naxes, s.ldpos, s.inv_freq, s.pairs, bytes((binding.ctypes.c_uint8 * 64).from_address(s.axis)))
+        both.wait()
+        return 0
+
+    monkeypatch.setattr(binding, "_lib", types.SimpleNamespace(tq_rope=tq_rope))
+    stream = types.SimpleNamespace(cuda_stream=0)
+
+    def call(x, pos, axes, tokens):
+        try:
+            X = Stub(torch.bfloat16, (tokens, 2, 128), at=x)
+            binding.rope(X, Stub(torch.int32, (axes, tokens), at=pos), spec, Y=X, stream=stream)
+        except Exception as e:               # noqa: BLE001  (for the main thread to show)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=call, args=a) for a in ((0x1000, 0x2000, 2, 5), (0x3000, 0x4000, 4, 9))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    axis = bytes([0, 1] * 32)
+    assert seen == {0x1000: (0x2000, 2, 5, 0x500, 64, axis), 0x3000: (0x4000, 4, 9, 0x500, 64, axis)}
+    assert bytes(spec._c) == before          # a call leaves the spec as it is
