@@ -164,8 +164,9 @@ k_kv4_append(const __grid_constant__ tq_kv4 kv, const uint16_t *__restrict__ K, 
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     for (int64_t base = 0; base < kv.nseq; base += kSeqs) {
         if (base) __syncthreads();
-        const int64_t all = static_cast<int64_t>(line_up(kv, base, ln, bad)) * 2 * kv.heads;
-        if (blockIdx.x) bad = false;          // one CTA's word is enough
+        bool off = false;                     // every CTA sees these: one's word is enough
+        const int64_t all = static_cast<int64_t>(line_up(kv, base, ln, off)) * 2 * kv.heads;
+        if (blockIdx.x == 0) bad |= off;
         for (int64_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < all; w += step) {
             const Item it = item_of(kv, base, ln, w);
             uint4 u[2][CH];
@@ -313,8 +314,9 @@ k_kv4_read(const __grid_constant__ tq_kv4 kv, uint16_t *__restrict__ K, int64_t 
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
     for (int64_t base = 0; base < kv.nseq; base += kSeqs) {
         if (base) __syncthreads();
-        const int64_t all = static_cast<int64_t>(line_up(kv, base, ln, bad)) * 2 * kv.heads;
-        if (blockIdx.x) bad = false;
+        bool off = false;
+        const int64_t all = static_cast<int64_t>(line_up(kv, base, ln, off)) * 2 * kv.heads;
+        if (blockIdx.x == 0) bad |= off;
         for (int64_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < all; w += step) {
             const Item it = item_of(kv, base, ln, w);
             uint16_t *out = it.value ? V : K;

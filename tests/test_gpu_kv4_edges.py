@@ -1,11 +1,11 @@
 """The 4-bit cache and attention over it where a call can go wrong quietly:
-scores with a large common part, padded page tables.  Against the 64-bit model
-on the GPU's own cache bytes."""
+scores with a large common part, padded page tables, bad pages among many
+sequences.  Against the 64-bit model on the GPU's own cache bytes."""
 import numpy as np
 import pytest
 
 import kv4_ref as ref
-from test_gpu_kv4 import World, dev32, f64, rows
+from test_gpu_kv4 import INDEX, World, dev32, f64, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +78,20 @@ def test_page_table_with_wide_rows(tq):
     assert tq.device_status() == 0
     with pytest.raises(ValueError):
         tq.KV4Batch(w.cache, w.tab[:1].expand(3, w.cols), w.lens, dev32(w.starts), w.tokens, 5)
+
+
+@pytest.mark.parametrize("bad", [7, 300, 511, 580])
+def test_bad_page_among_many_sequences(tq, bad):
+    """A page outside the pool is reported whichever of 600 sequences has it and
+    whichever part of the GPU meets it, when written and when read."""
+    w = World(tq, [(16, 2)] * 600, 8, 64, 16, seed=70, fill=False, noise=False)
+    kv = rows(w.tokens, 16, 64, 71)
+    tq.kv4_append(w.batch, kv[:, :8], kv[:, 8:])
+    assert tq.device_status() == 0
+    w.tab[bad, 0] = w.npages
+    tq.kv4_append(w.batch, kv[:, :8], kv[:, 8:])
+    assert tq.device_status() == INDEX and tq.device_status() == 0
+    K, V = tq.kv4_read(w.batch)
+    assert tq.device_status() == INDEX and tq.device_status() == 0
+    gone = slice(2 * bad, 2 * bad + 2)
+    assert not K[gone].any() and not V[gone].any() and int((K != 0).any(2).all(1).sum()) == w.tokens - 2
