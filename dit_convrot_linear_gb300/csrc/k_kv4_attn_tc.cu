@@ -9,9 +9,12 @@
 //
 //   - a loader warp copies blocks of 16 tokens into a ring;
 //   - eight warps widen them to fp16 operands in shared memory, a block of a tile
-//     each, without a word between them: a nibble masked out of a word is the
-//     fp16 subnormal u 2^-24, one fused multiply-add with (s, -8 s) makes it
-//     s (u - 8), s the token's scale over a power of two of the block's largest.
+//     each, without a word between them: a nibble put under 1024's exponent is
+//     1024 + u (or 1024 + 16 u), from which u - 8 comes exactly, times s, the
+//     token's scale over a power of two of the block's largest.  (A nibble taken
+//     as the subnormal u 2^-24 saves that step, but its product with s is among
+//     fp16's subnormals from a scale 2^-4 of the block's largest on: 0.8 % off at
+//     2^-8.  As it is, the product keeps its 11 bits down to 2^-25.)
 //     Keys are the K-major rows of S = Q K^T; values, whose words hold two tokens,
 //     are the K-major rows of O = P V as they come;
 //   - one thread issues the products: S into TMEM (128 columns a row tile), P
@@ -231,7 +234,7 @@ __device__ __forceinline__ void t_wait_ld(uint32_t (&v)[8]) {
 }
 __device__ __forceinline__ void t_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// d += a b with the fp16 pair (exact but for one rounding)
+// a b + c of fp16 pairs (exact but for one rounding), and a b
 __device__ __forceinline__ uint32_t hfma2_(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -260,8 +263,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-constexpr uint32_t kMinus8 = 0x80088008u;    // -8 2^-24 twice
-constexpr uint32_t kSixteenth = 0x2C002C00u; // 1/16 twice
+// u - 8, u = 0 .. 15 in bits 0 .. 3 (FAR: bits 4 .. 7) of both halves of x, the
+// others zero: 1024 + u less 1032, or (1024 + 16 u) / 16 less 72
+constexpr uint32_t k1024 = 0x64006400u, kOne = 0x3C003C00u, kMinus1032 = 0xE408E408u;
+constexpr uint32_t kSixteenth = 0x2C002C00u, kMinus72 = 0xD480D480u;
+template <bool FAR>
+__device__ __forceinline__ uint32_t code_of(uint32_t x) {
+    return FAR ? hfma2_(x | k1024, kSixteenth, kMinus72) : hfma2_(x | k1024, kOne, kMinus1032);
+}
+
+constexpr float kWide = 2048.0f;             // widened keys and values are this many times what they stand for
 
 template <class C>
 __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant__ TcParams p) {
@@ -271,7 +282,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
     __shared__ volatile int abort_sh;
     __shared__ int64_t run_sh[2], before_sh[kMaxSeqsT + 1];      // before: of all heads of the sequences before
     __shared__ KvSeq seq_sh[kMaxSeqsT];
-    struct __align__(16) Info {              // of a block: 2^(e + 10) of the keys, exponent of the values (read as a
+    struct __align__(16) Info {              // of a block: 2^e / kWide of the keys, exponent of the values (read as a
         float kx;                            // pair: first, at 16 bytes); whether it is there
         int ev;
         int there, pad;
@@ -510,15 +521,14 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 const uint32_t mk = __reduce_max_sync(0xffffffffu, __float_as_uint(sk)) >> 23;   // scales are not negative
                 const uint32_t mv = __reduce_max_sync(0xffffffffu, __float_as_uint(sv)) >> 23;
                 const int ek = mk ? static_cast<int>(mk) - 127 : 0, ev = mv ? static_cast<int>(mv) - 127 : kNoE;
-                // scales over the power of two of the largest, times 2^14
-                const __half hk = __float2half_rn(sk * pow2i(-ek) * 16384.0f), hv = __float2half_rn(sv * pow2i(-ev) * 16384.0f);
+                // scales over the power of two of the largest: 7 times one stays below 2^15
+                const __half hk = __float2half_rn(sk * pow2i(-ek) * kWide), hv = __float2half_rn(sv * pow2i(-ev) * kWide);
                 // keys: 8 nibbles to 16 bytes in the order (0, 4), (1, 5), (2, 6), (3, 7)
                 ok = tc_wait(k_empty + 8 * s, par, &abort_sh, p.status);
                 if (ok) {
-                    if (lane == 0) kv_info[k & 3][dw] = {pow2i(ek + 10), ev, there, 0};
+                    if (lane == 0) kv_info[k & 3][dw] = {pow2i(ek) * (1.0f / kWide), ev, there, 0};
                     const __half2 h2 = __half2half2(hk);
                     const uint32_t s1 = *reinterpret_cast<const uint32_t *>(&h2);
-                    const uint32_t s16 = hmul2_(s1, kSixteenth), b = hmul2_(s1, kMinus8);
                     const int r = kKvBlock * dw + row;
                     unsigned char *dst = sm + C::oK + s * C::KT + ((r >> 3) << 10) + (r & 7) * 16;
                     const uint4 *src = reinterpret_cast<const uint4 *>(blk + row * (D / 2));
@@ -531,8 +541,9 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t y = x[e] >> 8;
-                            const uint4 o = make_uint4(hfma2_(x[e] & 0x000F000Fu, s1, b), hfma2_(x[e] & 0x00F000F0u, s16, b),
-                                                       hfma2_(y & 0x000F000Fu, s1, b), hfma2_(y & 0x00F000F0u, s16, b));
+                            const uint4 o = make_uint4(
+                                hmul2_(code_of<false>(x[e] & 0x000F000Fu), s1), hmul2_(code_of<true>(x[e] & 0x00F000F0u), s1),
+                                hmul2_(code_of<false>(y & 0x000F000Fu), s1), hmul2_(code_of<true>(y & 0x00F000F0u), s1));
                             const int ch = c * 4 + e;            // 8 columns
                             *reinterpret_cast<uint4 *>(dst + (ch >> 3) * PAN + (ch & 7) * 128) = o;
                         }
@@ -545,19 +556,14 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 // four words, each two tokens
                 ok = ok && tc_wait(v_empty + 8 * s, par, &abort_sh, p.status);
                 if (ok) {
-                    const int sh = (lane & 2) * 4;               // nibbles 2 and 3 are 8 bits up
-                    const uint32_t mask = lane & 1 ? 0x00F000F0u : 0x000F000Fu;
+                    const int sh = (lane & 3) * 4;
                     const uint32_t own = __half_as_ushort(hv);
                     const uint32_t two = own | (__shfl_down_sync(0xffffffffu, own, 1) << 16);    // of even lanes
 #pragma unroll
                     for (int o = 0; o < 2; ++o) {
-                        uint32_t sx[4], b[4];
+                        uint32_t s1[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t s1 = __shfl_sync(0xffffffffu, two, 8 * o + 2 * q);
-                            b[q] = hmul2_(s1, kMinus8);
-                            sx[q] = lane & 1 ? hmul2_(s1, kSixteenth) : s1;
-                        }
+                        for (int q = 0; q < 4; ++q) s1[q] = __shfl_sync(0xffffffffu, two, 8 * o + 2 * q);
                         const unsigned char *vb = blk + 8 * D + o * 4 * D;
                         unsigned char *dst = sm + C::oV + s * C::KT + (dw >> 2) * (D * 128) + (2 * (dw & 3) + o) * 128;
 #pragma unroll
@@ -567,7 +573,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 const uint32_t w = *reinterpret_cast<const uint32_t *>(vb + q * D + (d >> 2) * 4);
-                                r[q] = hfma2_((w >> sh) & mask, sx[q], b[q]);
+                                r[q] = hmul2_(code_of<false>((w >> sh) & 0x000F000Fu), s1[q]);
                             }
                             *reinterpret_cast<uint4 *>(dst + ((d >> 3) << 10) + (d & 7) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
                         }
@@ -881,7 +887,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 pair_bar();
                 l += pair_sh[row].sum[hc ^ 1];
                 if (it.slot >= 0) {
-                    const float up = pow2i(E + 10);
+                    const float up = pow2i(E) * (1.0f / kWide);
                     if (is && hc == 0) p.stat[static_cast<int64_t>(it.slot) * RU + row] = make_float2(m, l);
                     if (ok)
 #pragma unroll 1
@@ -927,7 +933,7 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     fence_before();
                     pair_bar();
                     fence_after();
-                    const float inv = l > 0.0f ? sqrtf(1.0f / D) / l * pow2i(E + 10) : 0.0f;
+                    const float inv = l > 0.0f ? sqrtf(1.0f / D) / l * pow2i(E) * (1.0f / kWide) : 0.0f;
                     const int64_t tok = it.q.start + (is ? (r0 + row) / ge.g : 0);
                     const int hq = it.h * ge.g + (r0 + row) % ge.g;
                     uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D;

@@ -814,10 +814,16 @@ size_t tq_kv4_workspace_bytes(void);
  *
  * Scores, softmax statistics and sums are fp32.  The rotated query is rounded
  * to fp16 (relative to its row's largest value), and so is each weight times
- * its value's scale; with more than 32 query rows a key/value head, keys and
- * values too (relative to their block of 16 tokens).  Each such rounding is
- * within 2^-11 of the value, an eighth of bf16's and far below the 4-bit
- * rounding of the keys and values themselves.
+ * its value's scale; with more than 32 query rows a key/value head, a token's
+ * scales and their products with its codes too (relative to their block of 16
+ * tokens).  Each such rounding is within 2^-11 of the value (with up to 32 query
+ * rows a query value's of it and a sixteenth of the one beside it), an eighth of
+ * bf16's and far below the 4-bit rounding of the keys and values themselves.
+ * What is very small beside others is rounded relative to them: a scale below
+ * 2^-25 of its block's largest to 2^-36 of that; a query value below 2^-22 of its
+ * row's largest to 2^-34 of that; a weight times its scale below 2^-12 of the
+ * largest such product or scale among the query rows that are worked on together
+ * to 2^-23 of that.
  *
  *   Q        bf16: head i of row t at Q + t * ldq + i * dim (K's rules).
  *   heads_q  a multiple of kv->heads, at most 64 times it, else TQ_ERR_SHAPE.

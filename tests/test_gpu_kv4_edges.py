@@ -1,6 +1,7 @@
 """The 4-bit cache and attention over it where a call can go wrong quietly:
 scores with a large common part, padded page tables, bad pages among many
-sequences.  Against the 64-bit model on the GPU's own cache bytes."""
+sequences, token scales far below their block's largest.  Against the
+64-bit model on the GPU's own cache bytes."""
 import numpy as np
 import pytest
 
@@ -95,3 +96,40 @@ def test_bad_page_among_many_sequences(tq, bad):
     assert tq.device_status() == INDEX and tq.device_status() == 0
     gone = slice(2 * bad, 2 * bad + 2)
     assert not K[gone].any() and not V[gone].any() and int((K != 0).any(2).all(1).sum()) == w.tokens - 2
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,heads_q", [(6, 4), (80, 1), (150, 2)])
+def test_scales_far_below_their_blocks_largest(tq, dim, new, heads_q):
+    """Rows that see themselves alone, their scales 2^0 .. 2^-16 of their block's
+    largest: the output is the value, the log sum the score.  Every rounding is
+    within 2^-11 of what it rounds, however small that is beside its block: a
+    key's scale, its product with the code and the query 3 x 2^-11 of the score, a
+    value's two and the weight's 3 x 2^-11 and half a bf16 step (2^-8)."""
+    import torch
+    rng = np.random.default_rng(dim + new)
+    n = new
+    # one code a token and the query's rotated values all alike, so that a code's
+    # error is the score's
+    ck = np.broadcast_to(rng.integers(1, 8, (1, n, 1)) * rng.choice([-1, 1], (1, n, 1)), (1, n, dim)).copy()
+    cv = rng.integers(-7, 8, (1, n, dim))
+    sk, sv = (2.0 ** -rng.integers(0, 17, (1, n)) * rng.uniform(1, 2, (1, n)) for _ in range(2))
+    sk[:, ::16], sv[:, ::16] = 1.0, 1.5
+    sk, sv = sk.astype(np.float32).astype(np.float64), sv.astype(np.float32).astype(np.float64)
+    w = laid(tq, [(n, new)], dim, ck, sk, cv, sv)
+    q = np.zeros((w.tokens, heads_q, dim))
+    q[..., 0] = 8.0
+    Q = torch.from_numpy(q).cuda().bfloat16()
+    O = torch.full_like(Q, float("nan"))
+    lse = torch.empty(w.tokens, heads_q, device="cuda")
+    tq.kv4_attention(w.batch, Q, 1.0, tq.kv4_workspace(), window=1, O=O, lse=lse)
+    assert tq.device_status() == 0
+    kc, vc, _, _ = w.cached(0)
+    score = (kc[0] @ (f64(Q[0, 0]) @ ref.hadamard(dim)))[:, None]
+    assert np.all(np.abs(f64(lse) - score) <= 3 * 2.0 ** -11 * np.abs(score) * 1.01 + 2.0 ** -20)
+    want = (vc[0] @ ref.hadamard(dim))[:, None]
+    bar = 2.0 ** -8 * np.abs(want) + 3 * 2.0 ** -11 * 1.01 * np.abs(vc[0]).sum(-1)[:, None, None] / np.sqrt(dim)
+    assert np.all(np.abs(f64(O) - want) <= bar)
+    # a call's rows as a whole: roundings of either sign, half of the worst at most
+    num, den = ((f64(O) - want) ** 2).sum((1, 2)), (want ** 2).sum((1, 2)) * heads_q
+    assert np.all(num <= (2.0 ** -8) ** 2 * den), np.sqrt(num / den).max()
