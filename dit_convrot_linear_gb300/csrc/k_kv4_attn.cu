@@ -788,21 +788,38 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
                     }
             }
             // value scales near the top of fp16's range, the largest met below 2^7
-            float big = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
-            if (__any_sync(0xffffffffu, big * gv > 128.0f)) {
+            float big = max_nan(max_nan(sv[0][0], sv[0][1]), max_nan(sv[1][0], sv[1][1]));
+            if (__any_sync(0xffffffffu, !(big * gv <= 128.0f))) {
+                // a value whose scale is not finite goes into the scores of the rows
+                // that see it: 0 times it would be NaN in the others' outputs
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (!(sv[k][c] <= FLT_MAX)) {
+                            sv[k][c] = 0.0f;
+#pragma unroll
+                            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                                for (int e = 2 * c; e < 2 * c + 2; ++e)
+                                    if (s[k][nt][e] != -INFINITY) ex[k][nt][e] = __uint_as_float(0x7FFFFFFFu);
+                        }
+                big = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-                const float to = pow2i(5 - (static_cast<int>(__float_as_uint(big) >> 23) - 127));
-                const float fix = to / gv;
-                gv = to;
+                if (big * gv > 128.0f) {                 // (of the whole warp)
+                    const float to = pow2i(5 - (static_cast<int>(__float_as_uint(big) >> 23) - 127));
+                    const float fix = to / gv;
+                    gv = to;
 #pragma unroll
-                for (int nt = 0; nt < NR; ++nt)
+                    for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        oc[nt][e] *= fix;
+                        for (int e = 0; e < 4; ++e) {
+                            oc[nt][e] *= fix;
 #pragma unroll
-                        for (int d = 0; d < D / 16; ++d) o[nt][d][e] *= fix;
-                    }
+                            for (int d = 0; d < D / 16; ++d) o[nt][d][e] *= fix;
+                        }
+                }
             }
 
             // output: O^T, value words of token pairs j and j + 4

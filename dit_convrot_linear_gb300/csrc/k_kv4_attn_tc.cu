@@ -517,12 +517,16 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                 const int pos = it.at + i * kTileT + kKvBlock * dw + row;
                 const bool is = there && pos >= it.lo && pos < it.hi;
                 const float *sc = reinterpret_cast<const float *>(blk + 16 * D);
-                const float sk = is ? sc[row] : 0.0f, sv = is ? sc[16 + row] : 0.0f;
+                // (a key or value whose scale is not finite is NaN in its scores, which
+                // reach the rows that see it: 0 times the value would be NaN in others)
+                const bool fine = !is || (sc[row] <= FLT_MAX && sc[16 + row] <= FLT_MAX);
+                const float sk = is && fine ? sc[row] : 0.0f, sv = is && fine ? sc[16 + row] : 0.0f;
                 const uint32_t mk = __reduce_max_sync(0xffffffffu, __float_as_uint(sk)) >> 23;   // scales are not negative
                 const uint32_t mv = __reduce_max_sync(0xffffffffu, __float_as_uint(sv)) >> 23;
                 const int ek = mk ? static_cast<int>(mk) - 127 : 0, ev = mv ? static_cast<int>(mv) - 127 : kNoE;
                 // scales over the power of two of the largest: 7 times one stays below 2^15
-                const __half hk = __float2half_rn(sk * pow2i(-ek) * kWide), hv = __float2half_rn(sv * pow2i(-ev) * kWide);
+                const __half hk = fine ? __float2half_rn(sk * pow2i(-ek) * kWide) : __ushort_as_half(0x7FFF);
+                const __half hv = __float2half_rn(sv * pow2i(-ev) * kWide);
                 // keys: 8 nibbles to 16 bytes in the order (0, 4), (1, 5), (2, 6), (3, 7)
                 ok = tc_wait(k_empty + 8 * s, par, &abort_sh, p.status);
                 if (ok) {

@@ -127,6 +127,13 @@ __device__ __forceinline__ void turn_row(float (&v)[V]) {
     for (int i = 0; i < V; ++i) v[i] *= c;
 }
 
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

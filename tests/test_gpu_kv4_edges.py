@@ -1,7 +1,7 @@
 """The 4-bit cache and attention over it where a call can go wrong quietly:
 scores with a large common part, padded page tables, bad pages among many
-sequences, token scales far below their block's largest.  Against the
-64-bit model on the GPU's own cache bytes."""
+sequences, token scales far below their block's largest or not finite.
+Against the 64-bit model on the GPU's own cache bytes."""
 import numpy as np
 import pytest
 
@@ -133,3 +133,39 @@ def test_scales_far_below_their_blocks_largest(tq, dim, new, heads_q):
     # a call's rows as a whole: roundings of either sign, half of the worst at most
     num, den = ((f64(O) - want) ** 2).sum((1, 2)), (want ** 2).sum((1, 2)) * heads_q
     assert np.all(num <= (2.0 ** -8) ** 2 * den), np.sqrt(num / den).max()
+
+
+def with_scale(w, b, pos, k, v):
+    """The cache's bytes with other scales at a position of a sequence."""
+    blocks = w.bytes().copy()
+    at = 16 * w.dim + 4 * (pos % 16)
+    blk = blocks[w.table[b, pos // w.page], :, pos % w.page // 16]
+    for x, o in ((k, 0), (v, 64)):
+        if x is not None:
+            blk[:, at + o:at + o + 4] = np.array([x], np.float32).view(np.uint8)
+    return blocks.reshape(-1)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,heads_q", [(3, 2), (12, 2), (40, 4)])
+@pytest.mark.parametrize("side", ["k", "v"])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_a_scale_that_is_not_finite_where_some_rows_see_it(tq, dim, new, heads_q, side, what):
+    """The rows that do not see such a token give the bits that they give where its
+    scales are zero, though it lies in a tile that others of them see."""
+    import torch
+    n = 200
+    w = World(tq, [(n, new), (50, new)], 1, dim, 16, seed=80)
+    Q = rows(2 * new, heads_q, dim, 82, outliers=False)
+    at = n - new // 2 - 1                                    # seen by the last new // 2 + 1 rows
+    zero, odd = with_scale(w, 0, at, 0.0, 0.0), with_scale(w, 0, at, *((what, None) if side == "k" else (None, what)))
+    outs = []
+    for pool in (zero, odd):
+        w.pool.copy_(torch.from_numpy(pool))
+        lse = torch.zeros(2 * new, heads_q, device="cuda")
+        outs.append((tq.kv4_attention(w.batch, Q, dim ** -0.5, tq.kv4_workspace(), lse=lse), lse))
+    assert tq.device_status() == 0
+    for a, b in zip(*outs):
+        blind = torch.ones(2 * new, dtype=torch.bool, device="cuda")
+        blind[new - new // 2 - 1:new] = False
+        assert a.isfinite().all() and torch.equal(a[blind], b[blind])
