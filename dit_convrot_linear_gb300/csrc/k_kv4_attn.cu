@@ -1033,7 +1033,8 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             if (sub == 0) reinterpret_cast<float2 *>(p.stat)[slot * R + i] = make_float2(mx, sum);
             continue;
         }
-        const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
+        const bool none = sum <= 0.0f;                   // (a NaN sum is not: it goes on to the output)
+        const float inv = none ? 0.0f : sqrtf(1.0f / D) / sum;
 #pragma unroll
         for (int h = 1; h < V; h <<= 1)                  // turned back
 #pragma unroll
@@ -1052,7 +1053,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             }
         uint32_t w[V / 2];
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) w[e] = sum > 0.0f ? bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+        for (int e = 0; e < V / 2; ++e) w[e] = none ? 0u : bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv);
         if (flag[0] || !is) continue;                    // the sums are not whole
         const int64_t tok = u.q.start + (r0 + i) / ge.g;
         const int hq = u.h * ge.g + (r0 + i) % ge.g;
@@ -1063,7 +1064,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) k_kv4_attn(const __grid_consta
             for (int e = 0; e < V / 2; e += 4)
                 *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
         if (p.a.lse && sub == 0)
-            p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+            p.a.lse[tok * p.a.heads_q + hq] = none ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
       }
       group_sync();
       if (!last && done < n_all) {

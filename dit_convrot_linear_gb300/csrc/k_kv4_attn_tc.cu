@@ -937,7 +937,8 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                     fence_before();
                     pair_bar();
                     fence_after();
-                    const float inv = l > 0.0f ? sqrtf(1.0f / D) / l * pow2i(E) * (1.0f / kWide) : 0.0f;
+                    const bool none = l <= 0.0f;             // (a NaN sum is not: it goes on to the output)
+                    const float inv = none ? 0.0f : sqrtf(1.0f / D) / l * pow2i(E) * (1.0f / kWide);
                     const int64_t tok = it.q.start + (is ? (r0 + row) / ge.g : 0);
                     const int hq = it.h * ge.g + (r0 + row) % ge.g;
                     uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D;
@@ -959,14 +960,14 @@ __global__ void __launch_bounds__(C::NT, 1) k_kv4_attn_tc(const __grid_constant_
                             uint32_t w[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                w[e] = l > 0.0f ? bf16_bits2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv) : 0u;
+                                w[e] = none ? 0u : bf16_bits2(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
                             if (is)
 #pragma unroll
                                 for (int e = 0; e < 16; e += 4)
                                     *reinterpret_cast<uint4 *>(dst + 32 * c + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
                         }
                     if (is && hc == 0 && ok && p.a.lse)
-                        p.a.lse[tok * p.a.heads_q + hq] = l > 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        p.a.lse[tok * p.a.heads_q + hq] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
                 }
             }
             fence_before();
@@ -1030,18 +1031,19 @@ __global__ void __launch_bounds__(kThreads) k_kv4_join(const __grid_constant__ T
             for (int e = 0; e < E; ++e) v[e] = fmaf(f, src[slot(k) * po + e], v[e]);
         }
         warp_fwht<E, float>(v);
-        const float inv = sum > 0.0f ? sqrtf(1.0f / D) / sum : 0.0f;
+        const bool none = sum <= 0.0f;
+        const float inv = none ? 0.0f : sqrtf(1.0f / D) / sum;
         const int row = sp.rt * ru + i;
         const int64_t tok = sp.start + row / g;
         const int hq = sp.h * g + row % g;
         uint16_t *dst = p.a.O + tok * p.a.ldo + static_cast<int64_t>(hq) * D + lane * E;
         uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) o[e] = sum > 0.0f ? bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+        for (int e = 0; e < E / 2; ++e) o[e] = none ? 0u : bf16_bits2(v[2 * e] * inv, v[2 * e + 1] * inv);
         if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(o[0], o[1]);
         else *reinterpret_cast<uint32_t *>(dst) = o[0];
         if (p.a.lse && lane == 0)
-            p.a.lse[tok * p.a.heads_q + hq] = sum > 0.0f ? (mx + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+            p.a.lse[tok * p.a.heads_q + hq] = none ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
     }
 }
 

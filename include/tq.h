@@ -825,6 +825,10 @@ size_t tq_kv4_workspace_bytes(void);
  * largest such product or scale among the query rows that are worked on together
  * to 2^-23 of that.
  *
+ * A query that is not finite, a key whose scale in the cache is NaN and a value
+ * whose scale is not finite make the rows that see them NaN, and their log sums;
+ * no other row changes.
+ *
  *   Q        bf16: head i of row t at Q + t * ldq + i * dim (K's rules).
  *   heads_q  a multiple of kv->heads, at most 64 times it, else TQ_ERR_SHAPE.
  *   max_q    rows of the longest sequence in this call (1 for decoding).  It

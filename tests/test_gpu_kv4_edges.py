@@ -169,3 +169,34 @@ def test_a_scale_that_is_not_finite_where_some_rows_see_it(tq, dim, new, heads_q
         blind = torch.ones(2 * new, dtype=torch.bool, device="cuda")
         blind[new - new // 2 - 1:new] = False
         assert a.isfinite().all() and torch.equal(a[blind], b[blind])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,heads_q,n", [(3, 2, 200), (12, 2, 200), (40, 4, 200), (1, 4, 9000), (40, 4, 9000)])
+@pytest.mark.parametrize("side", ["q", "k", "v"])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_what_is_not_finite_shows_in_the_rows_that_see_it(tq, dim, new, heads_q, n, side, what):
+    """NaN in the outputs and log sums of a query that is not finite, and of the
+    rows that see a token whose key's scale is NaN or whose value's is not finite
+    (whole row tiles and such as are cut into parts); every other row as it is without."""
+    import torch
+    w = World(tq, [(n, new), (50, new)], 1, dim, 64, seed=80)
+    Q = rows(2 * new, heads_q, dim, 82, outliers=False)
+    at = n - new // 2 - 1                                    # seen by the last new // 2 + 1 rows
+    hit = torch.zeros(2 * new, heads_q, dtype=torch.bool, device="cuda")
+    if side == "q":
+        zero = odd = w.bytes().reshape(-1).copy()
+        hit[0, 1] = True
+    else:
+        zero, odd = with_scale(w, 0, at, 0.0, 0.0), with_scale(w, 0, at, *((np.nan, None) if side == "k" else (None, what)))
+        hit[new - new // 2 - 1:new] = True
+    outs = []
+    for pool, x in ((zero, 0.25), (odd, what)):
+        w.pool.copy_(torch.from_numpy(pool))
+        if side == "q":
+            Q[0, 1, 7] = x
+        lse = torch.zeros(2 * new, heads_q, device="cuda")
+        outs.append((tq.kv4_attention(w.batch, Q, dim ** -0.5, tq.kv4_workspace(), lse=lse), lse))
+    assert tq.device_status() == 0
+    for a, b in zip(*outs):
+        assert a.isfinite().all() and b[hit].isnan().all() and torch.equal(a[~hit], b[~hit])
