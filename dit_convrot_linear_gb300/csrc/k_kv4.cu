@@ -109,6 +109,12 @@ __device__ __forceinline__ Item item_of(const tq_kv4 &kv, int64_t base, const Li
     return it;
 }
 
+// A row's scale from its largest rotated magnitude: NaN for a row that is not
+// finite, so that it shows wherever the row is read.
+__device__ __forceinline__ float scale_of(float amax) {
+    return amax <= FLT_MAX ? __fdiv_rn(amax, 7.0f) : __uint_as_float(0x7FFFFFFFu);
+}
+
 // W words at p, aligned to them (up to 16 bytes)
 template <int W>
 __device__ __forceinline__ void store_words(unsigned char *p, const uint32_t *w) {
@@ -217,11 +223,11 @@ k_kv4_append(const __grid_constant__ tq_kv4 kv, const uint16_t *__restrict__ K, 
                     for (int e = 0; e < 4; ++e) {
                         float a, b;
                         split(v[r][i][e >> 1][e & 1], a, b);
-                        amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+                        amax = max_nan(amax, max_nan(fabsf(a), fabsf(b)));
                     }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                s[r] = __fdiv_rn(amax * cn, 7.0f);
+                amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                s[r] = scale_of(amax * cn);
                 // rint(v / s) as rint of the product with 1 / s, which is within
                 // some units of 2^-24 of the quotient (nearer a tie than the
                 // transform's own rounding); the sum with 1.5 2^23 + 8 rounds, and
@@ -502,10 +508,10 @@ k_kv4_append_rows(const __grid_constant__ tq_kv4 kv, const uint16_t *__restrict_
         turn_row<N>(v);
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        for (int i = 0; i < N; ++i) amax = max_nan(amax, fabsf(v[i]));
 #pragma unroll
-        for (int m = 1; m < kLanes; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-        const float s = __fdiv_rn(amax, 7.0f);
+        for (int m = 1; m < kLanes; m <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        const float s = scale_of(amax);
         // rint(v / s) as rint of the product with 1 / s, which is within three
         // units of 2^-24 of the quotient (nearer a tie than the transform's own
         // rounding); the sum with 1.5 2^23 + 8 rounds, and leaves the code plus 8

@@ -787,7 +787,9 @@ size_t tq_kv4_page_bytes(int heads, int dim, int page_size);
  *          ldk, ldv >= heads * dim and multiples of 8; 16-byte aligned.  Keys
  *          come with their positions in them (tq_rope).
  * Two rows of one call must not have the same place (two sequences that share
- * their last page).
+ * their last page).  A head's row that is not finite, or passes fp32's
+ * range when rotated, is stored with the scale NaN: it reads as NaN, and the
+ * attention of the rows that see it is NaN.
  */
 tq_status tq_kv4_append(const tq_kv4 *kv, const void *K, int64_t ldk, const void *V, int64_t ldv,
                         cudaStream_t stream);

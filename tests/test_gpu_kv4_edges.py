@@ -200,3 +200,29 @@ def test_what_is_not_finite_shows_in_the_rows_that_see_it(tq, dim, new, heads_q,
     assert tq.device_status() == 0
     for a, b in zip(*outs):
         assert a.isfinite().all() and b[hit].isnan().all() and torch.equal(a[~hit], b[~hit])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("count", [40, 5000])
+def test_rows_that_are_not_finite_are_stored_as_such(tq, dim, count):
+    """NaN or infinities in a head's row (written by rows and by blocks): its
+    scale is NaN, it reads as NaN, every other row is as it is without."""
+    w = World(tq, [(count, count), (33, 0)], 2, dim, 16, seed=83, fill=False, noise=False)
+    kv = rows(w.tokens, 4, dim, 84)
+    hit = {(3, 0): [np.nan], (20, 1): [np.inf], (21, 2): [-np.inf, np.inf], (count - 1, 3): [np.nan, np.inf]}
+    for t, c in hit:
+        kv[t, c] = 0
+    tq.kv4_append(w.batch, kv[:, :2], kv[:, 2:])
+    before = tq.kv4_read(w.batch)
+    for (t, c), x in hit.items():
+        for i, v in enumerate(x):
+            kv[t, c, 7 + 20 * i] = v
+    tq.kv4_append(w.batch, kv[:, :2], kv[:, 2:])
+    after = tq.kv4_read(w.batch)
+    assert tq.device_status() == 0
+    for t, c in hit:
+        assert after[c // 2][t, c % 2].isnan().all()
+        after[c // 2][t, c % 2] = 0
+        blk = w.bytes()[w.table[0, t // 16], c % 2, 0]
+        assert np.isnan(blk[16 * dim:].copy().view(np.float32)[t % 16 + 16 * (c // 2)])
+    assert all((a == b).all() for a, b in zip(after, before))
