@@ -601,7 +601,7 @@ k_rotq(const uint16_t *__restrict__ X, int64_t M, int64_t K, int64_t ldx, void *
             float sum = 0.0f;
             for (int w = 0; w < W; ++w) sum += red_n[par][w];
             const float ms = sum / static_cast<float>(K) + eps;
-            const float rstd = ms > 0.0f ? __frsqrt_rn(ms) : 0.0f;
+            const float rstd = ms <= 0.0f ? 0.0f : __frsqrt_rn(ms);      // (NaN goes on to the row)
             uint16_t *yrow = ro.Y ? ro.Y + m * ro.ldy : nullptr;
             if (tail_warp) {
                 const int64_t c0 = t0 + static_cast<int64_t>(lane) * Et;

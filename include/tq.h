@@ -676,7 +676,8 @@ tq_status tq_chain_create(const tq_chain_call *calls, int64_t ncalls, int bits, 
  *   Xq, sx int8 [M, K] dense (16-byte aligned) and fp32 [M], or both NULL: y
  *          rotated and quantised per token, the input of tq_linear_q8.
  * At least one of Y and Xq is given.  A row of zeros gives zeros (with eps = 0
- * too).  A code may differ by one from the fp64 reference, as for
+ * too).  A NaN in a row, or infinities that meet, make the whole row of Y NaN.
+ * A code may differ by one from the fp64 reference, as for
  * tq_rotate_quant_act.
  */
 tq_status tq_rmsnorm_quant_act(const void *X, int64_t M, int64_t K, int64_t ldx, const void *R, int64_t ldr,

@@ -141,3 +141,25 @@ def test_norm_feeds_the_products(tq):
     want = (vb @ to_np(codes).astype(np.float64).T) * to_np(sw)
     assert rel_l2(to_np(a16), want) <= 100 * REL_L2_Y       # bf16 ties of x' may round the other way
     assert tq.device_status() == 0
+
+
+@pytest.mark.parametrize("K", [64, 896, 4096 + 128])
+def test_rows_that_are_not_finite(tq, K):
+    """A NaN anywhere in a row, or infinities that meet in the residual's
+    addition, make all of the row NaN in bf16; the other rows are as without."""
+    import torch
+    M = 7
+    x, gamma = inputs(M, K, K)
+    r = inputs(M, K, K + 1)[0]
+    want = tq.rmsnorm(x, gamma, R=r)
+    x[1, K - 1] = float("nan")
+    x[3, 0] = float("inf")
+    r[3, 0] = -float("inf")
+    r[5, K // 2] = float("nan")
+    got = tq.rmsnorm(x, gamma, R=r)
+    odd = [1, 3, 5]
+    assert got[odd].isnan().all()
+    keep = [0, 2, 4, 6]
+    assert torch.equal(got[keep], want[keep]) and got[keep].isfinite().all()
+    assert tq.rmsnorm(x, gamma)[1].isnan().all()
+    assert tq.device_status() == 0
