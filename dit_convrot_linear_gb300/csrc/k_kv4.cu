@@ -8,8 +8,8 @@
 // butterflies between registers, a pair of values an instruction.  A lane holds
 // the same 2 x dim / 4 values before and after: two tokens that share the cache's
 // value words.  About 20 instructions a row (eight lanes a row, with three stages
-// of shuffles, spend 85): 8 K tokens of 8 heads 14.9 us to append and 12.7 to
-// read, 6.3 for their bytes; 32 K 42.7 and 38.5, against 25.  What bounds them
+// of shuffles, spend 85): 4132 tokens of 8 heads 7.9 us to append and 6.6 to read,
+// 3.2 for their bytes; 32720 tokens 43.7 and 38.6, against 25.  What bounds them
 // now is the loads in flight: 110 registers let two CTAs an SM.
 
 #include <cfloat>

@@ -40,9 +40,11 @@
 // sequences of up to 4096 47, 25; 24 of up to 5 drafted tokens, window 4096, 51,
 // 15; one of 777 tokens (14 heads of 64 on 2) 10.7, of which a launch that does
 // nothing is 2 to 3.  The long ones are bound by the stream.  The others by what
-// happens once a run: about 6 us until the first tile is at hand (lengths, then
-// pages, then blocks, each a trip to memory that waits for the one before), 3 to
-// 4 us where a row tile ends and the next begins, 3 to 5 us to join parts.
+// happens once a run: about 6 us until the first tile is at hand (lengths, pages
+// and blocks are fetched one after the other here; only the blocks have to wait
+// for the pages), 3 to 4 us where a row tile ends and the next begins, 3 to 5 us
+// to join parts.  Heads 64 wide: those 64 sequences 36, 13.5, one of 777 10.8;
+// 256 wide: 72, 49, and 14.3.
 
 #include <cfloat>
 
@@ -55,7 +57,11 @@ namespace {
 constexpr int kTile = 32;                    // tokens a tile: two blocks
 constexpr int kFold = 4;                     // tiles of a warp between two subtractions of the bias
 constexpr int kLeast = 16;                   // the shortest run
-constexpr int kMinRun = 48;                  // fewest tiles a part, where row tiles are cut on their own
+// Fewest tiles a part, where row tiles are cut on their own: one sequence of 40000
+// on 2 heads, widths 64 / 128 / 256, 20.5 / 23.9 / 25.1 us; with 24 21.9 / 24.0 /
+// 25.7, with 96 22.8 / 29.6 / 31.2 (9000 tokens: 16.6 / 19.8 / 23.2; 15.0 / 17.3 /
+// 18.5; 23.9 / 30.2 / 36.8).
+constexpr int kMinRun = 48;
 constexpr unsigned int kStatusKvTimeout = 128u;
 // A copy of the library built for its own tests lets every stage expect bytes
 // that no copy brings (their waits then run out).
@@ -73,7 +79,10 @@ struct Cfg {
     static constexpr int D = D_, NR = NR_, NW = NW_, GW = GW_, STAGES = STAGES_, CTAS = CTAS_;
     static constexpr int G = NW / GW;                        // groups of GW warps, each with runs of its own
     static constexpr int GT = GW * 32;
-    static constexpr int OVER = 40 / G;                      // tiles that starting and ending a row tile stand for
+    // Tiles that starting and ending a row tile stand for.  Half as many: 64
+    // sequences up to 4096, widths 64 / 128 / 256, 38.5 / 49.9 / 78.0 us where these
+    // take 36.1 / 47.2 / 72.5; twice as many: 35.4 / 47.2 / 76.4.
+    static constexpr int OVER = 40 / G;
     static constexpr int R = 8 * NR;                         // query rows a row tile
     static constexpr int NT = NW * 32;                       // threads
     static constexpr int W = D / 32;                         // 32-bit words of a row a lane
@@ -1155,6 +1164,10 @@ tq_status launch_kv4_attention(const tq_kv4 &kv, const Kv4Attn &a, const DeviceI
     // sequences of up to 4096 47 against 52, 256 of up to 700 59 against 78.
     // With fewer, all eight warps on one part: 4 contexts of 131072 97 us against
     // 104, one of 777 10.5 against 12.5.  (Groups of two: 48, 57, 60, 113, 19.)
+    // Heads 64 wide, groups of four against eight warps: 64 sequences up to 4096
+    // 36 and 41, 256 up to 700 47 and 64, the drafts 38 and 41; 4 of 65536 48 and
+    // 40, one of 777 12.7 and 10.9.  256 wide: 72 and 84, 100 and 134; one of 777
+    // 16.8 and 14.3, but 4 of 65536 97 and 100.
     const bool wide = rows > 8;
     const int64_t tiles = kv.nseq * kv.heads * ((rows + (wide ? 15 : 7)) / (wide ? 16 : 8));
     const bool many = 4 * tiles > dev.sms;

@@ -34,13 +34,13 @@
 // relative to their row's, block's or maximum's scale.
 //
 // Measured (8 key/value heads of 128, 32 query heads): 1024 rows over 16384
-// tokens 300 us, 139 for their operations at a large library product's rate (mma.sync
-// took 1056); the last 4096 rows of as many 972 us, 503.  A pair of row tiles
-// takes about 4800 cycles a tile of positions where its products alone would take
-// 2050: a row tile's softmax (2900) and its products (1700, slowed by the widening
-// warps' stores: both operands of S come from shared memory, all of its bandwidth)
-// follow one another, and TMEM has no room for a second set of scores beside two
-// outputs.
+// tokens 307 us, 139 for their operations at a large library product's rate (mma.sync
+// took 1056); the last 4096 rows of as many 1004 us, 503; four prompts of 4096 830,
+// 288.  Heads of 64: 268 us, 70.  A pair of row tiles takes about 4900 cycles a tile
+// of positions where its products alone would take 2050: a row tile's softmax (2900)
+// and its products (1700, slowed by the widening warps' stores: both operands of S
+// come from shared memory, all of its bandwidth) follow one another, and TMEM has no
+// room for a second set of scores beside two outputs.
 
 #include <cfloat>
 
@@ -66,7 +66,10 @@ constexpr int kMaxSeqsT = 256;               // sequences the cutting holds in s
 constexpr int kNoE = -1024;                  // exponent of a half whose values are all zero
 constexpr int kCols = 512;                   // TMEM columns
 constexpr int kMaxSmsT = 160;                // more SMs than this stay unused
-constexpr int kStart = 4;                    // tiles that a part's start and end stand for
+// Tiles that a part's start and end stand for: 64 rows over 16384, widths 64 / 128,
+// 40.7 / 51.4 us, eight prompts of 2000 435 / 554; with 2 39.4 / 50.6 and 450 / 577,
+// with 8 49.1 / 60.0 and 447 / 551.
+constexpr int kStart = 4;
 constexpr int kMinPart = 4;                  // fewest tiles a part
 
 // A build for the library's own tests expects bytes that no copy brings.
@@ -1072,7 +1075,7 @@ tq_status launch(TcParams &p, void *ws, const DeviceInfo &dev, cudaStream_t s) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn_tc<C>, p);
     if (e != cudaSuccess) return cuda_fail(e);
-    cfg.gridDim = dim3(grid * 8);                // (1024 rows over 16384: 300 us, with half as many 305)
+    cfg.gridDim = dim3(grid * 8);                // (1024 rows over 16384: half as many took 5 us longer)
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, k_kv4_join<C::D>, p);
@@ -1086,6 +1089,15 @@ size_t kv4_tc_workspace_bytes(const DeviceInfo &dev) {
     return kMaxSmsT * (sizeof(Cut) + 2 * 256 * (sizeof(float2) + kMaxD * sizeof(float)));
 }
 
+// From 33 query rows a key/value head on: 64 tokens of four query heads a key/value
+// head over 16384 41 us against 58 on mma.sync (heads 64 wide), 1024 268 against
+// 629, or 307 against 1056 (128 wide).  Where many sequences have few rows each this
+// is not so: 24 sequences of up to 9 drafted tokens (36 query rows), window 4096, 106
+// us against 66 (128 wide), 91 against 46 (64), of up to 16 tokens 91 against 59.  Heads 256 wide (a row tile's output and two
+// places of scores would fill TMEM) and more than 256 sequences (the cutting's arrays
+// in shared memory) have no form here and run on mma.sync: 1024 rows over 16384, 256
+// wide, 1760 us, 279 for their operations; 300 sequences of 16 tokens up to 700 484,
+// where 256 take 316 here.
 bool kv4_tc_takes(const tq_kv4 &kv, const Kv4Attn &a, int64_t rows) {
     (void)a;
     return kv.dim <= kMaxD && kv.nseq <= kMaxSeqsT && rows > 32;

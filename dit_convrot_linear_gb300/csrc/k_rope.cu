@@ -6,8 +6,8 @@
 // angle in fp64), then turns all their heads, eight pairs a thread as two
 // 16-byte pieces half a head apart, or four neighbouring pairs as one.  8190
 // tokens of 48 heads of 128 on three axes: 41 us, 73 % of the copy rate (30 us for
-// the bytes; a few tokens a CTA leave its loads and the angles' arithmetic one
-// after the other); 32 tokens of 40 heads 2.7 us, a launch's own time.
+// the bytes; a CTA's rows are loaded after its angles, and those take fp64, for
+// which this GPU has few lanes); 32 tokens of 40 heads 2.7 us, a launch's own time.
 
 #include <string.h>
 
