@@ -1,0 +1,516 @@
+// A layer's experts around their products: the router's choice of k experts a
+// token with its weights, the sort of the choices by expert, rows gathered by that
+// order, and the weighted sum back into token order, with the gradients of the
+// choice's weights and of the sum.
+//
+// All but the sort are bound by memory at many tokens and by a launch at few.
+
+#include "tq_internal.cuh"
+
+namespace tq {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+// ------------------------------------------------------------ the router
+
+// Order of logits as unsigned numbers: 0 for -inf (never chosen), all bits set for
+// NaN (chosen first: the row's weights come out as NaN, not as a quiet choice).  The
+// two zeros are equal.
+__device__ __forceinline__ uint32_t logit_key(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    if (x != x) return 0xFFFFFFFFu;
+    if (b == 0xFF800000u) return 0u;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float key_logit(uint32_t key) {
+    if (key == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+template <typename L>
+__device__ __forceinline__ float load_logit(const L *p) {
+    if constexpr (sizeof(L) == 4)
+        return __ldg(p);
+    else
+        return bf16_bits_to_f32(__ldg(p));
+}
+
+// A warp a token; lane l holds experts l, l + 32, ...  Each choice is two warp
+// reductions: the largest key, then the lowest expert that has it.
+template <typename L, int NI>
+__global__ void __launch_bounds__(256) k_expert_topk(const L *__restrict__ X, int64_t T, int E, int64_t ld, int k,
+                                                     int renorm, int32_t *__restrict__ ids,
+                                                     float *__restrict__ weights) {
+    const int lane = threadIdx.x & 31;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += step) {
+        uint32_t key[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = lane + 32 * i;
+            key[i] = e < E ? logit_key(load_logit(X + t * ld + e)) : 0u;
+        }
+        float total = 0.0f;                      // over all experts, or over the chosen ones
+        float top = 0.0f, mine = 0.0f;
+        int id = -1;
+        uint32_t left[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) left[i] = key[i];
+        for (int j = 0; j < k; ++j) {
+            uint32_t best = 0u;
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (left[i] > best) {
+                    best = left[i];
+                    at = lane + 32 * i;
+                }
+            const uint32_t win = __reduce_max_sync(kAll, best);
+            if (win == 0u) break;                // nothing left that may be chosen
+            const int e = static_cast<int>(__reduce_min_sync(kAll, best == win ? static_cast<uint32_t>(at) : 0xFFFFu));
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (lane + 32 * i == e) left[i] = 0u;
+            const float v = key_logit(win);
+            if (j == 0) {
+                top = v;
+                if (!renorm) {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        if (key[i] != 0u) s += expf(key_logit(key[i]) - top);
+                    total = warp_sum(s);
+                }
+            }
+            const float w = expf(v - top);
+            if (renorm) total += w;
+            if (lane == j) {
+                id = e;
+                mine = w;
+            }
+        }
+        if (lane < k) {
+            ids[t * k + lane] = id;
+            weights[t * k + lane] = id >= 0 ? mine / total : 0.0f;
+        }
+    }
+}
+
+// dlogits of the weights' gradients dw.  With the chosen ones' own softmax w:
+//   w_i (dw_i - sum_j w_j dw_j) at the chosen, 0 elsewhere;
+// with the softmax p over all experts: p_e (dw at e - sum_j p_j dw_j).
+template <typename L, int NI>
+__global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ X, int64_t T, int E, int64_t ld,
+                                                          const int32_t *__restrict__ ids,
+                                                          const float *__restrict__ dw, int k, int renorm,
+                                                          L *__restrict__ dX, int64_t ldd, unsigned int *status) {
+    const int lane = threadIdx.x & 31;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += step) {
+        int id = -1;
+        float d = 0.0f, v = 0.0f;
+        if (lane < k) {
+            id = ids[t * k + lane];
+            if (id < -1 || id >= E) {
+                atomicOr(status, kStatusIndex);
+                id = -1;
+            }
+            if (id >= 0) {
+                d = dw[t * k + lane];
+                v = load_logit(X + t * ld + id);
+            }
+        }
+        float x[NI], g[NI];
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = lane + 32 * i;
+            x[i] = !renorm && e < E ? load_logit(X + t * ld + e) : -INFINITY;
+            g[i] = 0.0f;
+            top = x[i] > top || x[i] != x[i] ? x[i] : top;
+        }
+        if (renorm && id >= 0) top = v;
+        bool nan = top != top;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        if (__any_sync(kAll, nan)) top = __uint_as_float(0x7FC00000u);
+        if (top == -INFINITY) top = 0.0f;
+        float w = id >= 0 ? expf(v - top) : 0.0f;
+        float total = w;
+        if (!renorm) {
+            total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) total += x[i] = lane + 32 * i < E ? expf(x[i] - top) : 0.0f;
+        }
+        total = warp_sum(total);
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        w *= inv;
+        const float mean = warp_sum(w * d);
+        const float part = renorm ? w * (d - mean) : d;
+        for (int j = 0; j < k; ++j) {
+            const int e = __shfl_sync(kAll, id, j);
+            const float c = __shfl_sync(kAll, part, j);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (lane + 32 * i == e) g[i] += c;
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = lane + 32 * i;
+            if (e >= E) continue;
+            const float r = renorm ? g[i] : x[i] * inv * (g[i] - mean);
+            if constexpr (sizeof(L) == 4)
+                dX[t * ldd + e] = r;
+            else
+                dX[t * ldd + e] = f32_to_bf16_bits(r);
+        }
+    }
+}
+
+// ------------------------------------------------------------ the sort
+
+// A counting sort by one CTA: each warp counts the experts of its own piece of the
+// choices, the counts are summed over warps and experts, and each warp places its
+// piece in order.  Warps' pieces are in order, so equal experts stay in order.
+constexpr int kSortWarps = 32;
+
+__global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *__restrict__ ids, int64_t n, int k,
+                                                                 int E, int32_t *__restrict__ offsets,
+                                                                 int32_t *__restrict__ token,
+                                                                 int32_t *__restrict__ place, unsigned int *status) {
+    extern __shared__ int cnt[];                 // [warps][E], then [E + 1]
+    int *base = cnt + kSortWarps * E;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kSortWarps * E; i += blockDim.x) cnt[i] = 0;
+    __syncthreads();
+    const int64_t per = ((n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int64_t f0 = warp * per, f1 = f0 + per < n ? f0 + per : n;
+    int *mine = cnt + warp * E;
+    for (int64_t f = f0; f < f1; f += 32) {
+        int e = -1;
+        if (f + lane < f1) {
+            e = ids[f + lane];
+            if (e < -1 || e >= E) {
+                atomicOr(status, kStatusIndex);
+                e = -1;
+            }
+        }
+        const uint32_t same = __match_any_sync(kAll, e);
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int sum = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = cnt[w * E + e];
+            cnt[w * E + e] = sum;
+            sum += c;
+        }
+        base[e] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int sum = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane, c = e < E ? base[e] : 0;
+            int s = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(kAll, s, o);
+                if (lane >= o) s += v;
+            }
+            if (e < E) base[e] = sum + s - c;
+            sum += __shfl_sync(kAll, s, 31);
+        }
+        if (lane == 0) base[E] = sum;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = base[e];
+    for (int64_t f = f0; f < f1; f += 32) {
+        int e = -1;
+        if (f + lane < f1) e = ids[f + lane];
+        if (e >= E) e = -1;
+        const uint32_t same = __match_any_sync(kAll, e);
+        int at = -1;
+        if (e >= 0) {
+            at = base[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
+            token[at] = static_cast<int32_t>((f + lane) / k);
+        }
+        if (f + lane < f1) place[f + lane] = at;
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    }
+    for (int64_t i = base[E] + threadIdx.x; i < n; i += blockDim.x) token[i] = -1;
+}
+
+// ------------------------------------------------------------ rows there and back
+
+// 16 bytes of a row as fp32 values
+template <typename V>
+struct Piece;
+template <>
+struct Piece<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void widen(const uint4 &u, float (&v)[4]) {
+        v[0] = __uint_as_float(u.x);
+        v[1] = __uint_as_float(u.y);
+        v[2] = __uint_as_float(u.z);
+        v[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 narrow(const float (&v)[4]) {
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+};
+template <>
+struct Piece<uint16_t> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void widen(const uint4 &u, float (&v)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 narrow(const float (&v)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = f32_to_bf16_bits(v[2 * i]) | (static_cast<uint32_t>(f32_to_bf16_bits(v[2 * i + 1])) << 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// A thread a 16-byte piece of a row.
+__global__ void __launch_bounds__(256) k_expert_gather(const uint4 *__restrict__ X, int64_t rows_x, int pieces,
+                                                       int64_t ldx, const int32_t *__restrict__ rows, int64_t M,
+                                                       uint4 *__restrict__ Y, int64_t ldy, unsigned int *status) {
+    const int64_t n = M * pieces, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+        const int64_t m = i / pieces;
+        const int c = static_cast<int>(i - m * pieces);
+        const int32_t r = __ldg(rows + m);
+        if (r >= 0 && r < rows_x)
+            Y[m * ldy + c] = __ldg(X + r * ldx + c);
+        else if (r != -1 && c == 0)
+            atomicOr(status, kStatusIndex);
+    }
+}
+
+// A thread a 16-byte piece of a token's row: the sum over its choices in their
+// order, in fp32.
+template <typename V>
+__global__ void __launch_bounds__(256) k_expert_combine(const uint4 *__restrict__ Y, int64_t rows, int pieces,
+                                                        int64_t ldy, const int32_t *__restrict__ place,
+                                                        const float *__restrict__ weights, int64_t T, int k,
+                                                        uint4 *__restrict__ O, int64_t ldo, unsigned int *status) {
+    using P = Piece<V>;
+    const int64_t n = T * pieces, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+        const int64_t t = i / pieces;
+        const int c = static_cast<int>(i - t * pieces);
+        float sum[P::N] = {};
+        for (int j = 0; j < k; ++j) {
+            const int32_t at = __ldg(place + t * k + j);
+            if (at < 0 || at >= rows) {
+                if (at != -1 && c == 0) atomicOr(status, kStatusIndex);
+                continue;
+            }
+            const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
+            float v[P::N];
+            P::widen(__ldg(Y + at * ldy + c), v);
+#pragma unroll
+            for (int q = 0; q < P::N; ++q) sum[q] = fmaf(w, v[q], sum[q]);
+        }
+        O[t * ldo + c] = P::narrow(sum);
+    }
+}
+
+// A CTA a token: dY of each of its rows, w * dO, and dw = dO . Y.
+constexpr int kGradThreads = 256;
+template <typename V>
+__global__ void __launch_bounds__(kGradThreads) k_expert_combine_grad(
+    const uint4 *__restrict__ dO, int64_t ldo, const uint4 *__restrict__ Y, int64_t rows, int pieces, int64_t ldy,
+    const int32_t *__restrict__ place, const float *__restrict__ weights, int64_t T, int k, uint4 *__restrict__ dY,
+    int64_t lddy, float *__restrict__ dw, unsigned int *status) {
+    using P = Piece<V>;
+    __shared__ float part[kGradThreads / 32];
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        for (int j = 0; j < k; ++j) {
+            const int32_t at = __ldg(place + t * k + j);
+            const bool in = at >= 0 && at < rows;
+            if (!in && at != -1 && threadIdx.x == 0) atomicOr(status, kStatusIndex);
+            float dot = 0.0f;
+            if (in) {
+                const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
+                for (int c = threadIdx.x; c < pieces; c += kGradThreads) {
+                    float d[P::N], v[P::N];
+                    P::widen(__ldg(dO + t * ldo + c), d);
+                    if (dw) {
+                        P::widen(__ldg(Y + at * ldy + c), v);
+#pragma unroll
+                        for (int q = 0; q < P::N; ++q) dot = fmaf(d[q], v[q], dot);
+                    }
+#pragma unroll
+                    for (int q = 0; q < P::N; ++q) d[q] *= w;
+                    dY[at * lddy + c] = P::narrow(d);
+                }
+            }
+            if (dw) {
+                dot = warp_sum(dot);
+                if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    float s = 0.0f;
+                    for (int i = 0; i < kGradThreads / 32; ++i) s += part[i];
+                    dw[t * k + j] = s;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+unsigned grid_of(int64_t ctas, const DeviceInfo &dev, int each) {
+    const int64_t most = static_cast<int64_t>(dev.sms) * each;
+    return static_cast<unsigned>(ctas < most ? ctas : most);
+}
+
+tq_status launched() {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+
+// F<NI> for the 32-expert pieces of E
+template <template <int> class F, typename... A>
+void by_experts(int64_t E, A... a) {
+    if (E <= 32) F<1>::run(a...);
+    else if (E <= 64) F<2>::run(a...);
+    else if (E <= 128) F<4>::run(a...);
+    else if (E <= 256) F<8>::run(a...);
+    else if (E <= 512) F<16>::run(a...);
+    else F<32>::run(a...);
+}
+
+}  // namespace
+
+namespace {
+template <int NI>
+struct Topk {
+    static void run(const void *x, int type, int64_t T, int E, int64_t ld, int k, int renorm, int32_t *ids, float *w,
+                    unsigned grid, cudaStream_t s) {
+        if (type == 0)
+            k_expert_topk<float, NI><<<grid, 256, 0, s>>>(static_cast<const float *>(x), T, E, ld, k, renorm, ids, w);
+        else
+            k_expert_topk<uint16_t, NI><<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(x), T, E, ld, k, renorm,
+                                                             ids, w);
+    }
+};
+template <int NI>
+struct TopkGrad {
+    static void run(const void *x, int type, int64_t T, int E, int64_t ld, const int32_t *ids, const float *dw, int k,
+                    int renorm, void *dx, int64_t ldd, unsigned int *status, unsigned grid, cudaStream_t s) {
+        if (type == 0)
+            k_expert_topk_grad<float, NI><<<grid, 256, 0, s>>>(static_cast<const float *>(x), T, E, ld, ids, dw, k,
+                                                               renorm, static_cast<float *>(dx), ldd, status);
+        else
+            k_expert_topk_grad<uint16_t, NI><<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(x), T, E, ld, ids, dw,
+                                                                  k, renorm, static_cast<uint16_t *>(dx), ldd, status);
+    }
+};
+}  // namespace
+
+tq_status launch_expert_topk(const void *logits, int type, int64_t T, int64_t E, int64_t ld, int k, int renorm,
+                             int32_t *ids, float *weights, const DeviceInfo &dev, cudaStream_t s) {
+    by_experts<Topk>(E, logits, type, T, static_cast<int>(E), ld, k, renorm, ids, weights,
+                     grid_of((T + 7) / 8, dev, 8), s);
+    return launched();
+}
+
+tq_status launch_expert_topk_grad(const void *logits, int type, int64_t T, int64_t E, int64_t ld, const int32_t *ids,
+                                  const float *dw, int k, int renorm, void *dlogits, int64_t ldd,
+                                  const DeviceInfo &dev, cudaStream_t s) {
+    unsigned int *status = status_word();
+    if (!status) return TQ_ERR_DEVICE;
+    by_experts<TopkGrad>(E, logits, type, T, static_cast<int>(E), ld, ids, dw, k, renorm, dlogits, ldd, status,
+                         grid_of((T + 7) / 8, dev, 8), s);
+    return launched();
+}
+
+tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, int32_t *offsets, int32_t *token,
+                             int32_t *place, const DeviceInfo &dev, cudaStream_t s) {
+    unsigned int *status = status_word();
+    if (!status || dev.id < 0 || dev.id >= 64) return TQ_ERR_DEVICE;
+    const int bytes = static_cast<int>((kSortWarps * E + E + 1) * 4);
+    static bool configured[64] = {false};
+    if (!configured[dev.id]) {
+        const cudaError_t e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (kSortWarps * TQ_MAX_EXPERTS + TQ_MAX_EXPERTS + 1) * 4);
+        if (e != cudaSuccess) return cuda_fail(e);
+        configured[dev.id] = true;
+    }
+    k_expert_sort<<<1, 32 * kSortWarps, bytes, s>>>(ids, T * k, k, static_cast<int>(E), offsets, token, place, status);
+    return launched();
+}
+
+tq_status launch_expert_gather(const void *X, int type, int64_t rows_x, int64_t W, int64_t ldx, const int32_t *rows,
+                               int64_t M, void *Y, int64_t ldy, const DeviceInfo &dev, cudaStream_t s) {
+    unsigned int *status = status_word();
+    if (!status) return TQ_ERR_DEVICE;
+    const int each = type == 0 ? 4 : 8;          // values of 16 bytes
+    const int64_t n = M * (W / each);
+    k_expert_gather<<<grid_of((n + 255) / 256, dev, 8), 256, 0, s>>>(
+        static_cast<const uint4 *>(X), rows_x, static_cast<int>(W / each), ldx / each, rows, M,
+        static_cast<uint4 *>(Y), ldy / each, status);
+    return launched();
+}
+
+tq_status launch_expert_combine(const void *Y, int type, int64_t rows, int64_t W, int64_t ldy, const int32_t *place,
+                                const float *weights, int64_t T, int k, void *O, int64_t ldo, const DeviceInfo &dev,
+                                cudaStream_t s) {
+    unsigned int *status = status_word();
+    if (!status) return TQ_ERR_DEVICE;
+    const int each = type == 0 ? 4 : 8, pieces = static_cast<int>(W / each);
+    const unsigned grid = grid_of((T * pieces + 255) / 256, dev, 8);
+    auto y = static_cast<const uint4 *>(Y);
+    auto o = static_cast<uint4 *>(O);
+    if (type == 0)
+        k_expert_combine<float><<<grid, 256, 0, s>>>(y, rows, pieces, ldy / each, place, weights, T, k, o, ldo / each,
+                                                     status);
+    else
+        k_expert_combine<uint16_t><<<grid, 256, 0, s>>>(y, rows, pieces, ldy / each, place, weights, T, k, o,
+                                                        ldo / each, status);
+    return launched();
+}
+
+tq_status launch_expert_combine_grad(const void *dO, int64_t ldo, const void *Y, int type, int64_t rows, int64_t W,
+                                     int64_t ldy, const int32_t *place, const float *weights, int64_t T, int k,
+                                     void *dY, int64_t lddy, float *dw, const DeviceInfo &dev, cudaStream_t s) {
+    unsigned int *status = status_word();
+    if (!status) return TQ_ERR_DEVICE;
+    const int each = type == 0 ? 4 : 8, pieces = static_cast<int>(W / each);
+    const unsigned grid = grid_of(T, dev, 8);
+    auto d = static_cast<const uint4 *>(dO);
+    auto y = static_cast<const uint4 *>(Y);
+    auto o = static_cast<uint4 *>(dY);
+    if (type == 0)
+        k_expert_combine_grad<float><<<grid, kGradThreads, 0, s>>>(d, ldo / each, y, rows, pieces, ldy / each, place,
+                                                                   weights, T, k, o, lddy / each, dw, status);
+    else
+        k_expert_combine_grad<uint16_t><<<grid, kGradThreads, 0, s>>>(d, ldo / each, y, rows, pieces, ldy / each,
+                                                                      place, weights, T, k, o, lddy / each, dw,
+                                                                      status);
+    return launched();
+}
+
+}  // namespace tq

@@ -734,6 +734,223 @@ tq_status tq_kv4_attention(const tq_kv4 *kv, const void *Q, int64_t heads_q, int
     return launch_kv4_attention(*kv, a, dev, stream);
 }
 
+// ------------------------------------------------------- 8-bit floating point, experts
+
+static bool valid_k_f8(int64_t K) { return K > 0 && K <= TQ_MAX_K && K % 16 == 0; }
+
+tq_status tq_quantize_weights_f8(const void *W, int64_t N, int64_t K, int64_t ldw, uint8_t *codes, float *scales,
+                                 cudaStream_t stream) {
+    if (N < 0 || !valid_k_f8(K)) return TQ_ERR_SHAPE;
+    if (N == 0) return TQ_OK;
+    tq_status st = check_bf16_rows(W, N, K, ldw);
+    if (st != TQ_OK) return st;
+    if (!codes || !scales) return TQ_ERR_NULL;
+    if (!aligned(codes, 16) || !aligned(scales, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_quantize_weights_f8(static_cast<const uint16_t *>(W), N, K, ldw, codes, scales, stream);
+}
+
+// The codes and scales of M rows of K.
+static tq_status check_f8_rows(const uint8_t *Xq, const float *sx, int64_t M, int64_t K) {
+    if (!Xq || !sx) return TQ_ERR_NULL;
+    if (M > INT32_MAX || !mul_ok(M, K)) return TQ_ERR_OVERFLOW;
+    if (!aligned(Xq, 16) || !aligned(sx, 4)) return TQ_ERR_ALIGN;
+    return TQ_OK;
+}
+
+tq_status tq_quant_act_f8(const void *X, int64_t rows_x, int64_t K, int64_t ldx, const int32_t *rows, int64_t M,
+                          uint8_t *Xq, float *sx, cudaStream_t stream) {
+    if (M < 0 || rows_x < 0 || !valid_k_f8(K) || (!rows && M != rows_x)) return TQ_ERR_SHAPE;
+    if (M == 0) return TQ_OK;
+    tq_status st = check_f8_rows(Xq, sx, M, K);
+    if (st != TQ_OK) return st;
+    if ((rows_x > 0 || X) && (st = check_bf16_rows(X, rows_x, K, ldx)) != TQ_OK) return st;
+    if (!aligned(rows, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_quant_act_f8(static_cast<const uint16_t *>(X), rows_x, K, ldx, nullptr, 0, rows, M, Xq, sx, dev,
+                               stream);
+}
+
+tq_status tq_swiglu_quant_act_f8(const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t M, int64_t K,
+                                 uint8_t *Xq, float *sx, cudaStream_t stream) {
+    if (M < 0 || !valid_k_f8(K)) return TQ_ERR_SHAPE;
+    if (M == 0) return TQ_OK;
+    tq_status st = check_f8_rows(Xq, sx, M, K);
+    if (st != TQ_OK) return st;
+    if ((st = check_bf16_rows(G, M, K, ldg)) != TQ_OK) return st;
+    if ((st = check_bf16_rows(U, M, K, ldu)) != TQ_OK) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_quant_act_f8(static_cast<const uint16_t *>(G), M, K, ldg, static_cast<const uint16_t *>(U), ldu,
+                               nullptr, M, Xq, sx, dev, stream);
+}
+
+size_t tq_f8_workspace_bytes(void) {
+    DeviceInfo dev;
+    return current_device(&dev) == TQ_OK ? f8_workspace_bytes(dev) : 0;
+}
+
+static tq_status linear_f8(const uint8_t *Xq, const float *sx, int64_t M, int64_t K, const int32_t *offsets,
+                           int64_t experts, const uint8_t *Wq, const float *sw, int64_t N, void *Y, tq_out ytype,
+                           int64_t ldy, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (M < 0 || N < 0 || !valid_k_f8(K)) return TQ_ERR_SHAPE;
+    if (ytype != TQ_OUT_F32 && ytype != TQ_OUT_BF16) return TQ_ERR_MODE;
+    if (M == 0 || N == 0) return TQ_OK;
+    tq_status st = check_f8_rows(Xq, sx, M, K);
+    if (st != TQ_OK) return st;
+    if (!Wq || !sw) return TQ_ERR_NULL;
+    if (!mul_ok(experts, N, INT32_MAX - 1024) || !mul_ok(experts * N, K)) return TQ_ERR_OVERFLOW;
+    if (!aligned(Wq, 16) || !aligned(sw, 4) || !aligned(offsets, 4)) return TQ_ERR_ALIGN;
+    if ((st = check_output(Y, M, N, ldy, out_size(ytype))) != TQ_OK) return st;
+    if (!workspace) return TQ_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    if (ws_bytes < f8_workspace_bytes(dev)) return TQ_ERR_WORKSPACE;
+    return launch_linear_f8({Xq, sx, M, K, offsets, experts, Wq, sw, N, Y, ldy, ytype == TQ_OUT_BF16 ? 1 : 0,
+                             workspace},
+                            dev, stream);
+}
+
+tq_status tq_linear_f8(const uint8_t *Xq, const float *sx, int64_t M, int64_t K, const uint8_t *Wq, const float *sw,
+                       int64_t N, void *Y, tq_out ytype, int64_t ldy, void *workspace, size_t ws_bytes,
+                       cudaStream_t stream) {
+    return linear_f8(Xq, sx, M, K, nullptr, 1, Wq, sw, N, Y, ytype, ldy, workspace, ws_bytes, stream);
+}
+
+tq_status tq_linear_f8_experts(const uint8_t *Xq, const float *sx, int64_t M, int64_t K, const int32_t *offsets,
+                               int64_t experts, const uint8_t *Wq, const float *sw, int64_t N, void *Y, tq_out ytype,
+                               int64_t ldy, void *workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (experts < 1 || experts > TQ_MAX_EXPERTS) return TQ_ERR_SHAPE;
+    if (!offsets) return TQ_ERR_NULL;
+    return linear_f8(Xq, sx, M, K, offsets, experts, Wq, sw, N, Y, ytype, ldy, workspace, ws_bytes, stream);
+}
+
+// The router's sizes and choices.
+static tq_status check_choices(int64_t tokens, int top, int64_t experts, tq_out type) {
+    if (type != TQ_OUT_F32 && type != TQ_OUT_BF16) return TQ_ERR_MODE;
+    if (tokens < 0 || experts < 1 || experts > TQ_MAX_EXPERTS || top < 1 || top > TQ_MAX_EXPERT_TOP || top > experts)
+        return TQ_ERR_SHAPE;
+    if (!mul_ok(tokens, top, INT32_MAX)) return TQ_ERR_OVERFLOW;
+    return TQ_OK;
+}
+
+tq_status tq_expert_topk(const void *logits, tq_out type, int64_t tokens, int64_t experts, int64_t ld, int top,
+                         int renorm, int32_t *ids, float *weights, cudaStream_t stream) {
+    tq_status st = check_choices(tokens, top, experts, type);
+    if (st != TQ_OK) return st;
+    if (renorm != 0 && renorm != 1) return TQ_ERR_MODE;
+    if (tokens == 0) return TQ_OK;
+    if ((st = check_output(logits, tokens, experts, ld, out_size(type))) != TQ_OK) return st;
+    if (!ids || !weights) return TQ_ERR_NULL;
+    if (!aligned(ids, 4) || !aligned(weights, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_expert_topk(logits, type == TQ_OUT_BF16 ? 1 : 0, tokens, experts, ld, top, renorm, ids, weights,
+                              dev, stream);
+}
+
+tq_status tq_expert_topk_grad(const void *logits, tq_out type, int64_t tokens, int64_t experts, int64_t ld,
+                              const int32_t *ids, const float *dweights, int top, int renorm, void *dlogits,
+                              int64_t ldd, cudaStream_t stream) {
+    tq_status st = check_choices(tokens, top, experts, type);
+    if (st != TQ_OK) return st;
+    if (renorm != 0 && renorm != 1) return TQ_ERR_MODE;
+    if (tokens == 0) return TQ_OK;
+    if ((st = check_output(logits, tokens, experts, ld, out_size(type))) != TQ_OK) return st;
+    if ((st = check_output(dlogits, tokens, experts, ldd, out_size(type))) != TQ_OK) return st;
+    if (!ids || !dweights) return TQ_ERR_NULL;
+    if (!aligned(ids, 4) || !aligned(dweights, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_expert_topk_grad(logits, type == TQ_OUT_BF16 ? 1 : 0, tokens, experts, ld, ids, dweights, top,
+                                   renorm, dlogits, ldd, dev, stream);
+}
+
+tq_status tq_expert_sort(const int32_t *ids, int64_t tokens, int top, int64_t experts, int32_t *offsets,
+                         int32_t *token, int32_t *place, cudaStream_t stream) {
+    // a token may name an expert twice here, so top is not held to the experts' number
+    if (tokens < 0 || experts < 1 || experts > TQ_MAX_EXPERTS || top < 1 || top > TQ_MAX_EXPERT_TOP)
+        return TQ_ERR_SHAPE;
+    if (!mul_ok(tokens, top, INT32_MAX)) return TQ_ERR_OVERFLOW;
+    if (!offsets || (tokens > 0 && (!ids || !token || !place))) return TQ_ERR_NULL;
+    if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(token, 4) || !aligned(place, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    const tq_status st = current_device(&dev);
+    if (st != TQ_OK) return st;
+    return launch_expert_sort(ids, tokens, top, experts, offsets, token, place, dev, stream);
+}
+
+// Rows of fp32 or bf16 in pieces of 16 bytes.
+static tq_status check_pieces(const void *p, int64_t rows, int64_t width, int64_t ld, int esize) {
+    if (!p) return TQ_ERR_NULL;
+    if (ld < width) return TQ_ERR_SHAPE;
+    if (rows > INT32_MAX || !mul_ok(rows, ld) || !mul_ok(rows * ld, esize)) return TQ_ERR_OVERFLOW;
+    if (!aligned(p, 16) || (ld * esize) % 16) return TQ_ERR_ALIGN;
+    return TQ_OK;
+}
+
+static bool valid_width(int64_t width, int esize) {
+    return width > 0 && width <= INT32_MAX && (width * esize) % 16 == 0;
+}
+
+tq_status tq_expert_gather(const void *X, tq_out type, int64_t rows_x, int64_t width, int64_t ldx,
+                           const int32_t *rows, int64_t M, void *Y, int64_t ldy, cudaStream_t stream) {
+    if (type != TQ_OUT_F32 && type != TQ_OUT_BF16) return TQ_ERR_MODE;
+    const int es = out_size(type);
+    if (rows_x < 0 || M < 0 || !valid_width(width, es)) return TQ_ERR_SHAPE;
+    if (M == 0) return TQ_OK;
+    tq_status st = check_pieces(Y, M, width, ldy, es);
+    if (st != TQ_OK) return st;
+    if ((rows_x > 0 || X) && (st = check_pieces(X, rows_x, width, ldx, es)) != TQ_OK) return st;
+    if (!rows) return TQ_ERR_NULL;
+    if (!aligned(rows, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_expert_gather(X, type == TQ_OUT_BF16 ? 1 : 0, rows_x, width, ldx, rows, M, Y, ldy, dev, stream);
+}
+
+tq_status tq_expert_combine(const void *Y, tq_out type, int64_t rows, int64_t width, int64_t ldy,
+                            const int32_t *place, const float *weights, int64_t tokens, int top, void *O, int64_t ldo,
+                            cudaStream_t stream) {
+    if (type != TQ_OUT_F32 && type != TQ_OUT_BF16) return TQ_ERR_MODE;
+    const int es = out_size(type);
+    if (rows < 0 || tokens < 0 || top < 1 || top > TQ_MAX_EXPERT_TOP || !valid_width(width, es)) return TQ_ERR_SHAPE;
+    if (tokens == 0) return TQ_OK;
+    if (!mul_ok(tokens, top, INT32_MAX)) return TQ_ERR_OVERFLOW;
+    tq_status st = check_pieces(O, tokens, width, ldo, es);
+    if (st != TQ_OK) return st;
+    if ((rows > 0 || Y) && (st = check_pieces(Y, rows, width, ldy, es)) != TQ_OK) return st;
+    if (!place) return TQ_ERR_NULL;
+    if (!aligned(place, 4) || !aligned(weights, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_expert_combine(Y, type == TQ_OUT_BF16 ? 1 : 0, rows, width, ldy, place, weights, tokens, top, O,
+                                 ldo, dev, stream);
+}
+
+tq_status tq_expert_combine_grad(const void *dO, int64_t ldo, const void *Y, tq_out type, int64_t rows, int64_t width,
+                                 int64_t ldy, const int32_t *place, const float *weights, int64_t tokens, int top,
+                                 void *dY, int64_t lddy, float *dweights, cudaStream_t stream) {
+    if (type != TQ_OUT_F32 && type != TQ_OUT_BF16) return TQ_ERR_MODE;
+    const int es = out_size(type);
+    if (rows < 0 || tokens < 0 || top < 1 || top > TQ_MAX_EXPERT_TOP || !valid_width(width, es)) return TQ_ERR_SHAPE;
+    if (tokens == 0) return TQ_OK;
+    if (!mul_ok(tokens, top, INT32_MAX)) return TQ_ERR_OVERFLOW;
+    tq_status st = check_pieces(dO, tokens, width, ldo, es);
+    if (st != TQ_OK) return st;
+    if ((rows > 0 || dY) && (st = check_pieces(dY, rows, width, lddy, es)) != TQ_OK) return st;
+    if ((Y || (dweights && rows > 0)) && (st = check_pieces(Y, rows, width, ldy, es)) != TQ_OK) return st;
+    if (!place) return TQ_ERR_NULL;
+    if (!aligned(place, 4) || !aligned(weights, 4) || !aligned(dweights, 4)) return TQ_ERR_ALIGN;
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != TQ_OK) return st;
+    return launch_expert_combine_grad(dO, ldo, Y, type == TQ_OUT_BF16 ? 1 : 0, rows, width, ldy, place, weights,
+                                      tokens, top, dY, lddy, dweights, dev, stream);
+}
+
 tq_status tq_grouped_bytes(const tq_a16_call *calls, int64_t ncalls, int bits, size_t *bytes) {
     if (!bytes) return TQ_ERR_NULL;
     const tq_status st = check_grouped(calls, ncalls, bits, TQ_OUT_F32);

@@ -194,6 +194,48 @@ size_t kv4_tc_workspace_bytes(const DeviceInfo &dev);
 tq_status launch_kv4_attention_tc(const tq_kv4 &kv, const Kv4Attn &a, void *ws, const DeviceInfo &dev,
                                   cudaStream_t s);
 
+// The 8-bit floating-point product (e4m3 codes, a scale for each block of 128).
+tq_status launch_quantize_weights_f8(const uint16_t *W, int64_t N, int64_t K, int64_t ldw, uint8_t *codes,
+                                     float *scales, cudaStream_t s);
+// U not NULL: of silu(X) * U; rows not NULL: row m of the result is row rows[m] of X
+tq_status launch_quant_act_f8(const uint16_t *X, int64_t rows_x, int64_t K, int64_t ldx, const uint16_t *U,
+                              int64_t ldu, const int32_t *rows, int64_t M, uint8_t *Xq, float *sx,
+                              const DeviceInfo &dev, cudaStream_t s);
+struct F8Product {
+    const uint8_t *Xq;
+    const float *sx;           // [blocks of K][M]
+    int64_t M, K;
+    const int32_t *offsets;    // rows of each expert, or null (one matrix)
+    int64_t experts;
+    const uint8_t *Wq;
+    const float *sw;
+    int64_t N;
+    void *Y;
+    int64_t ldy;
+    int ytype;                 // 0 fp32, 1 bf16
+    void *ws;
+};
+size_t f8_workspace_bytes(const DeviceInfo &dev);
+tq_status launch_linear_f8(const F8Product &p, const DeviceInfo &dev, cudaStream_t s);
+
+// A layer's experts: the router's choice, the sort by expert, rows there and back.
+// type: 0 fp32, 1 bf16.
+tq_status launch_expert_topk(const void *logits, int type, int64_t T, int64_t E, int64_t ld, int k, int renorm,
+                             int32_t *ids, float *weights, const DeviceInfo &dev, cudaStream_t s);
+tq_status launch_expert_topk_grad(const void *logits, int type, int64_t T, int64_t E, int64_t ld, const int32_t *ids,
+                                  const float *dw, int k, int renorm, void *dlogits, int64_t ldd,
+                                  const DeviceInfo &dev, cudaStream_t s);
+tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, int32_t *offsets, int32_t *token,
+                             int32_t *place, const DeviceInfo &dev, cudaStream_t s);
+tq_status launch_expert_gather(const void *X, int type, int64_t rows_x, int64_t W, int64_t ldx, const int32_t *rows,
+                               int64_t M, void *Y, int64_t ldy, const DeviceInfo &dev, cudaStream_t s);
+tq_status launch_expert_combine(const void *Y, int type, int64_t rows, int64_t W, int64_t ldy, const int32_t *place,
+                                const float *weights, int64_t T, int k, void *O, int64_t ldo, const DeviceInfo &dev,
+                                cudaStream_t s);
+tq_status launch_expert_combine_grad(const void *dO, int64_t ldo, const void *Y, int type, int64_t rows, int64_t W,
+                                     int64_t ldy, const int32_t *place, const float *weights, int64_t T, int k,
+                                     void *dY, int64_t lddy, float *dw, const DeviceInfo &dev, cudaStream_t s);
+
 tq_status launch_gemm_a8_tiled(const void *At, const float *sx, int64_t M, int64_t K,
                                const uint8_t *Wq, const float *sw, int64_t N, int bits,
                                void *Y, int ytype, int64_t ldy, const DeviceInfo &dev,

@@ -851,6 +851,186 @@ tq_status tq_kv4_attention(const tq_kv4 *kv, const void *Q, int64_t heads_q, int
                            float scale, int causal, int64_t window, void *O, int64_t ldo, float *lse,
                            void *workspace, size_t ws_bytes, cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Products in 8-bit floating point, and a feed-forward layer of experts on them.
+ *
+ * The pages have no counterpart (TensorPencil's FP8 column has no rotation and no
+ * block scales).  The large-M product of this library runs on int8 codes that the
+ * tensor cores of sm_103a take only widened to fp16; e4m3 codes they take as they
+ * are, at twice the rate.
+ *
+ * Codes are e4m3 (sign, 4 bits of exponent, 3 of mantissa; largest value 448, no
+ * infinities), one byte each.  Scales are fp32:
+ *   activations  one for each block of 128 columns of a row, [ceil(K / 128)][M]
+ *                (the scales of a block of all rows side by side);
+ *   weights      one for each block of 128 rows and 128 columns,
+ *                [ceil(N / 128)][ceil(K / 128)] row-major.
+ * The last block of a row or column is as wide as what is left.  The products take
+ * any scale, so published weights in this form are used as they are.  The
+ * library's own quantisers take the smallest power of two s = 2^j, j >= -126, for
+ * which |x| / s <= 448 holds in the block: x / s is then exact and a code is one
+ * rounding (to nearest, ties to even) of it.  A block of zeros has s = 0.  A block
+ * with an infinity or a NaN has the scale NaN and codes 0: the outputs it meets are
+ * NaN, and no others.  There is no rotation: a floating-point code's relative
+ * precision does not depend on its block's largest value.
+ *
+ * K is a multiple of 16, 16 .. TQ_MAX_K.
+ */
+#define TQ_F8_BLOCK 128
+
+/*
+ * Weights.
+ *   W       as tq_quantize_weights.
+ *   codes   e4m3 [N, K] dense, 16-byte aligned.
+ *   scales  fp32 [ceil(N / 128), ceil(K / 128)].
+ */
+tq_status tq_quantize_weights_f8(const void *W, int64_t N, int64_t K, int64_t ldw, uint8_t *codes, float *scales,
+                                 cudaStream_t stream);
+
+/*
+ * Activations; with `rows`, gathered rows (the rows of tokens sorted by expert:
+ * tq_expert_sort's token).
+ *   X      bf16 [rows_x, K] rows at X + i * ldx; ldx >= K, ldx % 8 == 0, X 16-byte
+ *          aligned.
+ *   rows   device int32 [M]: row m of the result is X's row rows[m]; -1: row m of
+ *          Xq and its scales are left as they were.  Any other value outside 0 ..
+ *          rows_x - 1 is left out in the same way and sets TQ_ERR_INDEX.  NULL: row
+ *          m is X's row m (then M == rows_x, else TQ_ERR_SHAPE).
+ *   Xq     e4m3 [M, K] dense, 16-byte aligned.
+ *   sx     fp32 [ceil(K / 128), M].
+ */
+tq_status tq_quant_act_f8(const void *X, int64_t rows_x, int64_t K, int64_t ldx, const int32_t *rows, int64_t M,
+                          uint8_t *Xq, float *sx, cudaStream_t stream);
+
+/*
+ * The same of h = silu(G) * U, silu(g) = g / (1 + e^-g), formed in fp32 and
+ * quantised without a rounding in between (the operand of a gated feed-forward's
+ * down projection).
+ *   G, U   bf16 [M, K] rows at G + m * ldg and U + m * ldu (X's rules).
+ */
+tq_status tq_swiglu_quant_act_f8(const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t M, int64_t K,
+                                 uint8_t *Xq, float *sx, cudaStream_t stream);
+
+/* Bytes of the products' workspace on the current device (0 when no usable device
+ * is current).  It does not depend on the sizes of a call. */
+size_t tq_f8_workspace_bytes(void);
+
+/*
+ * The product
+ *   Y[m][n] = sum_b sx[b][m] * sw[n / 128][b] * sum_{k in block b} xq[m][k] * wq[n][k].
+ * A block's sum is formed by the tensor cores in fp32, the sum over blocks by fp32
+ * fused multiply-adds in the order of b (in parts where K is split, the parts
+ * added in order; the split depends on the sizes alone).  sx * sw is formed in fp32
+ * first and has to be finite.
+ *
+ *   Xq, sx   as written by tq_quant_act_f8.
+ *   Wq, sw   e4m3 [N, K] dense and its scales; Wq 16-byte aligned.
+ *   ytype    TQ_OUT_F32 or TQ_OUT_BF16.
+ *   Y        [M, N], rows at Y + m * ldy; ldy >= N; aligned to its element size.
+ *   workspace  tq_f8_workspace_bytes() bytes, 256-byte aligned, ZEROED before its
+ *            first use; rules of tq_linear_tt_split's (every call leaves it zeroed
+ *            where that matters; one per stream).
+ */
+tq_status tq_linear_f8(const uint8_t *Xq, const float *sx, int64_t M, int64_t K, const uint8_t *Wq, const float *sw,
+                       int64_t N, void *Y, tq_out ytype, int64_t ldy, void *workspace, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/* Most experts of a layer. */
+#define TQ_MAX_EXPERTS 1024
+/* Most experts a token chooses. */
+#define TQ_MAX_EXPERT_TOP 32
+
+/*
+ * The same product with a weight matrix for each expert: rows offsets[e] ..
+ * offsets[e + 1] - 1 of Xq are multiplied by expert e's.
+ *   offsets  device int32 [experts + 1], not decreasing, within 0 .. M (an expert
+ *            without rows costs nothing).  A range that runs backwards, leaves 0 ..
+ *            M or starts before an earlier offset is taken as empty and sets
+ *            TQ_ERR_INDEX.
+ *   experts  1 .. TQ_MAX_EXPERTS.
+ *   M        rows of Xq and Y, and of sx ([ceil(K / 128), M]).  Rows of Y that no
+ *            expert has are left as they were.
+ *   Wq, sw   e4m3 [experts, N, K] dense, scales [experts, ceil(N / 128),
+ *            ceil(K / 128)].
+ */
+tq_status tq_linear_f8_experts(const uint8_t *Xq, const float *sx, int64_t M, int64_t K, const int32_t *offsets,
+                               int64_t experts, const uint8_t *Wq, const float *sw, int64_t N, void *Y, tq_out ytype,
+                               int64_t ldy, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The router: each token's `top` experts by their logits, largest first, the lower
+ * index first among equals, and their weights: the softmax over all experts, or
+ * (renorm = 1) over the chosen ones.  Statistics are fp32.
+ *   logits   fp32 or bf16 (type TQ_OUT_F32 or TQ_OUT_BF16) [tokens, experts], rows
+ *            at logits + t * ld; ld >= experts; aligned to its element size.  -inf
+ *            takes an expert out of a token's reach.  A NaN counts as the largest;
+ *            a row with a NaN or +inf has weights NaN.
+ *   top      1 .. min(experts, TQ_MAX_EXPERT_TOP).
+ *   ids      int32 [tokens, top]: -1 where fewer experts are within reach.
+ *   weights  fp32 [tokens, top]: 0 there.
+ */
+tq_status tq_expert_topk(const void *logits, tq_out type, int64_t tokens, int64_t experts, int64_t ld, int top,
+                         int renorm, int32_t *ids, float *weights, cudaStream_t stream);
+
+/*
+ * Its gradient: dlogits from the gradients of the weights, for choices ids.
+ *   ids       as written by tq_expert_topk; a choice -1 counts for nothing (any other
+ *             id outside 0 .. experts - 1 does too, and sets TQ_ERR_INDEX).
+ *   dweights  fp32 [tokens, top].
+ *   dlogits   of the logits' type, rows at dlogits + t * ldd; it must not overlap
+ *             an input.
+ */
+tq_status tq_expert_topk_grad(const void *logits, tq_out type, int64_t tokens, int64_t experts, int64_t ld,
+                              const int32_t *ids, const float *dweights, int top, int renorm, void *dlogits,
+                              int64_t ldd, cudaStream_t stream);
+
+/*
+ * The choices sorted by expert, those of one expert in the order of their tokens.
+ *   ids      int32 [tokens, top]; -1: no expert (any other value outside 0 ..
+ *            experts - 1 is taken as -1 and sets TQ_ERR_INDEX).
+ *   offsets  int32 [experts + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1.
+ *   token    int32 [tokens * top]: the token of each sorted row, -1 behind the last
+ *            expert's.
+ *   place    int32 [tokens, top]: the sorted row of each choice, -1 for none.
+ */
+tq_status tq_expert_sort(const int32_t *ids, int64_t tokens, int top, int64_t experts, int32_t *offsets,
+                         int32_t *token, int32_t *place, cudaStream_t stream);
+
+/*
+ * Rows gathered: Y's row m is X's row rows[m] (-1: left as it was; other values out
+ * of range too, and they set TQ_ERR_INDEX).  The gradient of the sum below with
+ * weights NULL, whose own gradient it is.
+ *   X, Y   fp32 or bf16 (type) [rows_x, width] and [M, width]; width, ldx and ldy
+ *          multiples of 16 bytes, 16-byte aligned; Y must not overlap X.
+ */
+tq_status tq_expert_gather(const void *X, tq_out type, int64_t rows_x, int64_t width, int64_t ldx,
+                           const int32_t *rows, int64_t M, void *Y, int64_t ldy, cudaStream_t stream);
+
+/*
+ * Rows back in token order: O[t] = sum_j weights[t][j] * Y[place[t][j]], in fp32 in
+ * the order of j.  A place -1 adds nothing (others out of range too, and they set
+ * TQ_ERR_INDEX); a token without any gives zeros.
+ *   Y        fp32 or bf16 (type) [rows, width], tq_expert_gather's rules.
+ *   place    int32 [tokens, top];  weights fp32 [tokens, top] or NULL (all 1).
+ *   O        [tokens, width] of the same type and rules; it must not overlap Y.
+ */
+tq_status tq_expert_combine(const void *Y, tq_out type, int64_t rows, int64_t width, int64_t ldy,
+                            const int32_t *place, const float *weights, int64_t tokens, int top, void *O, int64_t ldo,
+                            cudaStream_t stream);
+
+/*
+ * Its gradients: dY[place[t][j]] = weights[t][j] * dO[t] and dweights[t][j] =
+ * dO[t] . Y[place[t][j]] (0 where there is no place).
+ *   dO        [tokens, width], Y [rows, width] of `type`, tq_expert_gather's rules.
+ *   dY        [rows, width]; rows that no choice leads to are left as they were.
+ *             No two choices may lead to the same row.  It must not overlap dO or Y.
+ *   dweights  fp32 [tokens, top], or NULL (then Y may be NULL).
+ */
+tq_status tq_expert_combine_grad(const void *dO, int64_t ldo, const void *Y, tq_out type, int64_t rows, int64_t width,
+                                 int64_t ldy, const int32_t *place, const float *weights, int64_t tokens, int top,
+                                 void *dY, int64_t lddy, float *dweights, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
