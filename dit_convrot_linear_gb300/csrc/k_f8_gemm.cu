@@ -3,19 +3,24 @@
 // of one matrix, or of one matrix an expert over rows sorted by expert, on tcgen05
 // (kind::f8f6f4: e4m3 operands as they are, at twice the rate of fp16).
 //
-// A pair of CTAs (tcgen05 cta_group::2) computes 256 output columns (weight rows,
-// 128 a CTA: one scale block) of up to NT tokens.  The weights are the MMA's M side
-// and the tokens its N side, so that the tile follows the number of tokens in steps
-// of 16: an expert's few rows cost no empty rows of a 128-row tile.  A step of K is
-// one scale block, four MMAs of 32; the accumulator of each step lies in TMEM of its
-// own and the drain warps add it, times its scales, to the sums in their registers:
-//   acc += (sx[b][token] * sw[block][b]) * part.
+// A pair of CTAs (tcgen05 cta_group::2) computes 256 output columns (weight rows) of
+// up to NT tokens.  A step of K is one scale block, four MMAs of 32; the accumulator
+// of each step lies in TMEM of its own, and the drain warps add it, times its scales,
+// to the sums in their registers.  Two forms:
+//   many tokens  (NT = 256) the tokens are the MMA's M side, so that a TMEM lane is
+//                a token and a step's scales are one number a thread,
+//                acc += (sx[b][token] * sw[block][b]) * part;
+//   few tokens   (NT = 64) the weights are the M side and the tokens the N side, in
+//                steps of 16: an expert's few rows cost no empty rows of a 128-row
+//                tile.  The scales differ from column to column and come from shared
+//                memory; that takes 4 bytes a lane and value, 1024 cycles a step at 256
+//                tokens, and is hidden behind the weights' stream at 64.
 // Per CTA:
-//   drain warps  (a TMEM lane quarter each; with NT = 256 two a quarter, half the
-//                tokens each) multiply and add, and write Y;
+//   drain warps  (a TMEM lane quarter each; with eight of them two a quarter, half
+//                the columns each) multiply and add, and write Y;
 //   MMA warp     allocates TMEM for the pair; in the even CTA one thread issues;
 //   copy warp    tensor copies of both operands into the ring (128-byte swizzle);
-//   scale warp   the tokens' scales of each step into a ring of their own.
+//   scale warp   (few tokens) each step's scales, sx * sw, into a ring of their own.
 //
 // The work is a list of tiles (expert, 256 columns, up to NT tokens).  Whole rounds
 // of tiles go to the pairs one by one; the K steps of a last round that would leave
@@ -30,40 +35,39 @@
 namespace tq {
 namespace {
 
-constexpr int kRowsW = 128;               // weight rows a CTA
+constexpr int kHalf = 128;                // rows a CTA brings to the M side: half a pair's
+constexpr int kTileN = 256;               // weight rows (columns of Y) of a tile
 constexpr int kStepK = 128;               // K of a step: one scale block
-constexpr int kWBytes = kRowsW * kStepK;  // a stage's weights
-constexpr int kBoxRows = 32;              // token rows of one tensor copy
+constexpr int kABytes = kHalf * kStepK;   // a stage's M side
 constexpr long long kF8WaitLimit = 4000000000ll;   // clock cycles, about 2 s
 constexpr unsigned int kStatusF8Timeout = 64u;
 
-// NT tokens a tile.  256: as many as an MMA takes.  64: for few tokens, where the
-// weights' stream is all there is: ten stages of weights in flight.
 template <int NT_>
 struct F8Plan {
     static constexpr int NT = NT_;
-    static constexpr bool WIDE = NT == 256;
-    static constexpr int DRAIN = WIDE ? 8 : 4;                 // drain warps
+    static constexpr bool WIDE = NT == 256;                    // tokens on the M side
+    static constexpr int NCOLS = WIDE ? kTileN : NT;           // columns of an accumulator: the N side
+    static constexpr int COLS = WIDE ? 128 : 64;               // columns a drain warp
+    static constexpr int DRAIN = 4 * NCOLS / COLS;             // drain warps
     static constexpr int THREADS = (DRAIN + 4) * 32;
-    static constexpr int COLS = NT / (DRAIN / 4);              // tokens a drain warp
+    static constexpr int B_BOX = WIDE ? 128 : 32;              // rows of one tensor copy of the N side
+    static constexpr int B_BYTES = NCOLS / 2 * kStepK;
+    static constexpr int STAGE = kABytes + B_BYTES;
     static constexpr int STAGES = WIDE ? 6 : 10;
-    static constexpr int X_BYTES = NT / 2 * kStepK;
-    static constexpr int STAGE = kWBytes + X_BYTES;
     static constexpr int ACCS = WIDE ? 2 : 4;                  // accumulators in TMEM
-    static constexpr int TMEM = NT * ACCS;
-    static constexpr int SCALES = WIDE ? 6 : 12;               // slots of the scale ring
-    static constexpr int OUT_ROWS = 16;                        // tokens a warp turns at once
-    static constexpr int OUT_PITCH = 80;                       // bytes: 32 bf16 columns and padding
+    static constexpr int TMEM = NCOLS * ACCS;
+    static constexpr int SCALES = WIDE ? 0 : 12;               // slots of the scale ring
     static constexpr int OFF_SCALES = STAGES * STAGE;
+    static constexpr int OUT_BYTES = WIDE ? DRAIN * 32 * 64 : 0;   // 64 bytes of 32 rows a warp
     static constexpr int OFF_OUT = OFF_SCALES + SCALES * NT * 4;
-    static constexpr int OFF_BARS = OFF_OUT + DRAIN * OUT_ROWS * OUT_PITCH;
+    static constexpr int OFF_BARS = OFF_OUT + OUT_BYTES;
     static constexpr int NBARS = 2 * STAGES + 2 * ACCS + 2 * SCALES + 1;
     static constexpr int OFF_LIST = OFF_BARS + (NBARS * 8 + 15) / 16 * 16;
-    // the list of experts: rows before, tiles before (E + 1 numbers each)
+    // the list of experts: first row, rows, tiles before
     static constexpr int smem(int64_t experts) { return OFF_LIST + static_cast<int>(experts + 1) * 12 + 16; }
     static constexpr int SLOT = DRAIN * 32 * (COLS / 2) * 8;   // bytes of a CTA's partial tile
 };
-static_assert(F8Plan<256>::smem(TQ_MAX_EXPERTS) <= 227 * 1024 && F8Plan<64>::smem(TQ_MAX_EXPERTS) <= 227 * 1024,
+static_assert(F8Plan<256>::smem(TQ_MAX_EXPERTS) <= 226 * 1024 && F8Plan<64>::smem(TQ_MAX_EXPERTS) <= 226 * 1024,
               "shared memory");
 
 constexpr int kF8MaxDrain = 8;
@@ -77,7 +81,7 @@ struct F8Params {
     int N, ksteps, nblocks, ntiles;      // nblocks: scale blocks of N; ntiles: 256-column tiles
     void *Y;
     int64_t ldy;
-    int ytype, vec;                      // vec: rows of Y are 16-byte aligned
+    int ytype, vec;                      // vec: rows of Y allow 16-byte stores (few tokens: 4-byte ones)
     unsigned int *status;
     unsigned int *counters;              // [pairs][2 CTAs][kF8MaxDrain]
     unsigned char *slots;                // [pairs][2][2 CTAs][SLOT]
@@ -88,7 +92,6 @@ struct F8Params {
 // split tile the pairs that have its first and last step.
 struct F8Seg {
     int e, ntile, m0, cols, k0, k1;      // cols: tokens of the tile (at most NT)
-    int mma_n;                           // cols rounded up to 16
     bool whole;
     int first, last;
 };
@@ -136,7 +139,6 @@ struct F8Iter {
         s.ntile = at / parts;
         s.m0 = l.row0[lo] + part * each;
         s.cols = min(each, rows - part * each);
-        s.mma_n = (max(s.cols, 1) + 15) / 16 * 16;
     }
     __device__ bool next(F8Seg &s) {
         const long long t = pair + static_cast<long long>(i) * pairs;
@@ -163,10 +165,22 @@ struct F8Iter {
     }
 };
 
+// What these barriers hand over is shared memory filled by tensor copies, this CTA's
+// own stores and TMEM: an acquire at CTA scope is enough.
+__device__ __forceinline__ bool f8_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ bool f8_wait(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *status) {
-    if (mbar_try(bar, parity)) return true;
+    if (f8_try(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try(bar, parity)) {
+    while (!f8_try(bar, parity)) {
         if (*abort) return false;
         if (clock64() - t0 > kF8WaitLimit) {
             *abort = 1;
@@ -183,8 +197,11 @@ __device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
     return remote;
 }
 
+// What it hands over is TMEM that has been read (tcgen05.wait::ld came before), no
+// memory: a release at cluster scope would wait for everything this thread has in
+// flight (2000 cycles a step).
 __device__ __forceinline__ void arrive_cluster(uint32_t remote) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
 // K-major operand of 128-byte rows in the 128-byte swizzle: groups of eight rows
@@ -193,15 +210,16 @@ __device__ __forceinline__ uint64_t f8_desc(uint32_t addr) {
     return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// sixteen lanes' 32 columns: for each eight of them the fragment of a 16 x 8 tile
-// (lane t: rows t / 4 and t / 4 + 8, columns 2 (t % 4) and the next)
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr));
+// Waits for what tmem_ld32 has asked for; the operands tie the values' uses to the
+// wait without holding back other loads.
+__device__ __forceinline__ void tmem_wait32(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                   "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                   "+r"(v[29]));
+    asm volatile("" : "+r"(v[30]), "+r"(v[31]));
 }
 
 __device__ __forceinline__ uint64_t pair64(uint32_t lo, uint32_t hi) {
@@ -217,11 +235,6 @@ __device__ __forceinline__ float2 floats(uint64_t v) {
     asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
     return make_float2(__uint_as_float(lo), __uint_as_float(hi));
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -231,9 +244,15 @@ __device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
 
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 template <class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P::THREADS, 1)
-k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const F8Params p) {
+k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Params p) {
     constexpr int NT = P::NT, DRAIN = P::DRAIN, STAGES = P::STAGES, ACCS = P::ACCS, SCALES = P::SCALES;
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + P::OFF_BARS);
@@ -262,7 +281,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
             init(acc_empty0 + 8 * a, 2 * DRAIN);    // used in the even CTA: both CTAs' drain warps
         }
         for (int s = 0; s < SCALES; ++s) {
-            init(sc_full0 + 8 * s, 32);
+            init(sc_full0 + 8 * s, 1);
             init(sc_empty0 + 8 * s, DRAIN);
         }
         init(done, 1);
@@ -329,7 +348,12 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
     const F8List list{row0, rows, tiles, p.experts, total_sh};
 
     if (warp >= DRAIN) {
-        if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // columns of a tile's accumulator: tokens, or weight rows, rounded up to 16
+        auto mma_n = [&](const F8Seg &sg) {
+            const int n = P::WIDE ? min(kTileN, p.N - sg.ntile * kTileN) : sg.cols;
+            return (n + 15) / 16 * 16;
+        };
         if (warp == DRAIN) {
             // -------------------------------------------- MMA issue (even CTA, one thread)
             if (rank == 0 && lane == 0) {
@@ -338,20 +362,20 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
                 F8Seg sg;
                 while (!abort_sh && iter.next(sg)) {
                     // D fp32, A and B e4m3, K-major, M = 256
-                    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(sg.mma_n >> 3) << 17) | (16u << 24);
+                    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(mma_n(sg) >> 3) << 17) | (16u << 24);
                     for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
                         const int s = it % STAGES, a = it % ACCS;
                         if (!f8_wait(acc_empty0 + 8 * a, ((it / ACCS) & 1) ^ 1, &abort_sh, p.status)) break;
                         if (!f8_wait(full0 + 8 * s, (it / STAGES) & 1, &abort_sh, p.status)) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint32_t w = smem_u32(smem + s * P::STAGE);
-                        const uint64_t wd = f8_desc(w), xd = f8_desc(w + kWBytes);
+                        const uint32_t at = smem_u32(smem + s * P::STAGE);
+                        const uint64_t ad = f8_desc(at), bd = f8_desc(at + kABytes);
 #pragma unroll
                         for (int kk = 0; kk < kStepK / 32; ++kk)
                             asm volatile(
                                 "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
                                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-                                ::"r"(tmem + static_cast<uint32_t>(NT * a)), "l"(wd + 2 * kk), "l"(xd + 2 * kk),
+                                ::"r"(tmem + static_cast<uint32_t>(P::NCOLS * a)), "l"(ad + 2 * kk), "l"(bd + 2 * kk),
                                   "r"(idesc), "r"(kk > 0 ? 1u : 0u));
                         auto commit = [](uint32_t bar) {
                             asm volatile(
@@ -378,14 +402,17 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
                 F8Iter<NT> iter(list, p, pair, pairs);
                 F8Seg sg;
                 while (!abort_sh && iter.next(sg)) {
-                    const int n0 = sg.ntile * 2 * kRowsW;
-                    const int boxes = (sg.mma_n / 2 + kBoxRows - 1) / kBoxRows;
-                    // weight rows past N are not loaded (what they multiply is not stored)
-                    const bool mine = n0 + static_cast<int>(rank) * kRowsW < p.N;
+                    // rows of the M side that are past the tile's are not loaded (what comes of
+                    // them is not stored); the N side is copied in whole boxes
+                    const int n0 = sg.ntile * kTileN, half = mma_n(sg) / 2;
+                    const int wrow = sg.e * p.N + n0;
+                    const int rows_a = P::WIDE ? sg.cols : p.N - n0;
+                    const int boxes = (half + P::B_BOX - 1) / P::B_BOX;
+                    const bool mine = static_cast<int>(rank) * kHalf < rows_a;
                     const uint32_t bytes =
-                        2 * boxes * kBoxRows * kStepK + (n0 + kRowsW < p.N ? 2 * kWBytes : kWBytes);
-                    const int wrow = sg.e * p.N + n0 + static_cast<int>(rank) * kRowsW;
-                    const int xrow = sg.m0 + static_cast<int>(rank) * (sg.mma_n / 2);
+                        2 * boxes * P::B_BOX * kStepK + (kHalf < rows_a ? 2 * kABytes : kABytes);
+                    const int arow = (P::WIDE ? sg.m0 : wrow) + static_cast<int>(rank) * kHalf;
+                    const int brow = (P::WIDE ? wrow : sg.m0) + static_cast<int>(rank) * half;
                     for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
                         const int s = it % STAGES;
                         if (!f8_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, &abort_sh, p.status)) break;
@@ -393,7 +420,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
                             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                                          ::"r"(full0 + 8 * s), "r"(bytes) : "memory");
                         const uint32_t bar = in_even_cta(full0 + 8 * s);
-                        const uint32_t w = smem_u32(smem + s * P::STAGE);
+                        const uint32_t at = smem_u32(smem + s * P::STAGE);
                         auto copy = [&](uint32_t dst, const CUtensorMap *map, int row) {
                             asm volatile(
                                 "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx"
@@ -401,9 +428,9 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
                                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(ks * kStepK), "r"(row), "r"(bar)
                                 : "memory");
                         };
-                        if (mine) copy(w, &tmW, wrow);
+                        if (mine) copy(at, &tmA, arow);
                         for (int b = 0; b < boxes; ++b)
-                            copy(w + kWBytes + b * kBoxRows * kStepK, &tmX, xrow + b * kBoxRows);
+                            copy(at + kABytes + b * P::B_BOX * kStepK, &tmB, brow + b * P::B_BOX);
                     }
                 }
                 // after a wait ran out: the copies in flight land before the pair leaves
@@ -415,112 +442,166 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
                         }
                     }
             }
-        } else if (warp == DRAIN + 2) {
+        } else if (!P::WIDE && warp == DRAIN + 2) {
             // -------------------------------------------- the tokens' scales
-            // column c of a tile at ((c / 16) * 4 + (c % 8) / 2) * 4 + (c / 8 % 2) * 2 + c % 2: the four
-            // that a lane of a fragment needs of sixteen columns lie together
+            // sx * sw of a step for each token, loaded AHEAD steps before it is stored
+            constexpr int AHEAD = 4, EACH = NT / 32, RING = P::SCALES > 0 ? P::SCALES : 1;
             uint32_t it = 0;
             F8Iter<NT> iter(list, p, pair, pairs);
             F8Seg sg;
-            while (!abort_sh && iter.next(sg)) {
-                for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
-                    const int s = it % SCALES;
-                    if (!f8_wait(sc_empty0 + 8 * s, ((it / SCALES) & 1) ^ 1, &abort_sh, p.status)) break;
-                    const uint32_t to = smem_u32(smem + P::OFF_SCALES) + s * NT * 4;
-                    const float *from = p.sx + static_cast<int64_t>(ks) * p.M + sg.m0;
+            while (__all_sync(0xffffffffu, !abort_sh) && iter.next(sg)) {
+                const int n0 = sg.ntile * kTileN + static_cast<int>(rank) * kHalf;
+                const float *sw = p.sw + (static_cast<int64_t>(sg.e) * p.nblocks + n0 / 128) * p.ksteps;
+                const float *sx = p.sx + sg.m0 + lane;
+                float x[AHEAD][EACH], w[AHEAD];
+                auto load = [&](int ks, float (&xs)[EACH], float &ws) {
+                    const bool in = ks < sg.k1;
+                    ws = in && n0 < p.N ? __ldg(sw + ks) : 0.0f;
 #pragma unroll
-                    for (int i = 0; i < NT / 32; ++i) {
-                        const int c = lane + 32 * i;
-                        const int at = ((c >> 4) * 4 + ((c & 7) >> 1)) * 4 + ((c >> 3) & 1) * 2 + (c & 1);
-                        if (c < sg.cols)
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + at * 4), "l"(from + c)
-                                         : "memory");
+                    for (int i = 0; i < EACH; ++i)
+                        xs[i] = in && lane + 32 * i < sg.cols ? __ldg(sx + ks * p.M + 32 * i) : 0.0f;
+                };
+#pragma unroll
+                for (int d = 0; d < AHEAD; ++d) load(sg.k0 + d, x[d], w[d]);
+                bool ok = true;
+                for (int ks = sg.k0; ok && ks < sg.k1; ks += AHEAD)
+#pragma unroll
+                    for (int d = 0; d < AHEAD; ++d) {
+                        if (!ok || ks + d >= sg.k1) break;
+                        const int s = it % RING;
+                        ok = __all_sync(0xffffffffu, f8_wait(sc_empty0 + 8 * s, ((it / RING) & 1) ^ 1, &abort_sh,
+                                                             p.status));
+                        if (!ok) break;
+                        float *to = reinterpret_cast<float *>(smem + P::OFF_SCALES) + s * NT + lane;
+#pragma unroll
+                        for (int i = 0; i < EACH; ++i) to[32 * i] = x[d][i] * w[d];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_local(sc_full0 + 8 * s);
+                        load(ks + d + AHEAD, x[d], w[d]);
+                        ++it;
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sc_full0 + 8 * s)
-                                 : "memory");
-                }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     } else {
-        if constexpr (P::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if constexpr (P::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ------------------------------------------------ drain
-        constexpr int GROUPS = P::COLS / 32;             // 32 tokens at a time
+        constexpr int GROUPS = P::COLS / 32;             // 32 columns at a time
+        constexpr int RING = P::SCALES > 0 ? P::SCALES : 1;
         const int q = warp & 3, c0 = (warp >> 2) * P::COLS;
         const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
         const uint32_t acc_empty_even = in_even_cta(acc_empty0);
-        const float *ring = reinterpret_cast<const float *>(smem + P::OFF_SCALES);
+        const float *ring = reinterpret_cast<const float *>(smem + P::OFF_SCALES) + c0;
+        // an accumulator has been read
+        auto hand_back = [&](int a) {
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_cluster(acc_empty_even + 8 * a);
+        };
         uint32_t it = 0;
         F8Iter<NT> iter(list, p, pair, pairs);
         F8Seg sg;
         // the warp acts as one: a lane that saw an abort takes the others along
         while (__all_sync(0xffffffffu, !abort_sh) && iter.next(sg)) {
-            const int n0 = sg.ntile * 2 * kRowsW + static_cast<int>(rank) * kRowsW;
-            const float *sw = p.sw + (static_cast<int64_t>(sg.e) * p.nblocks + n0 / kRowsW) * p.ksteps;
-            const bool some = n0 < p.N;                  // this CTA has columns of the tile
-            const int groups = min(GROUPS, (sg.cols - c0 + 31) / 32);     // those with tokens (none: <= 0)
+            const int row = static_cast<int>(rank) * kHalf + q * 32;     // of this warp, on the M side
+            const int n0 = sg.ntile * kTileN;
+            const int rows_left = (P::WIDE ? sg.cols : p.N - n0) - row;
+            const int cols_left = (P::WIDE ? p.N - n0 : sg.cols) - c0;
+            const bool some = rows_left > 0 && cols_left > 0;            // this warp has some of the tile
+            const int groups = some ? min(GROUPS, (cols_left + 31) / 32) : 0;
+            const int64_t token = static_cast<int64_t>(sg.m0) + row + lane;
             uint64_t acc[GROUPS][16];
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[g][i] = 0ull;
-            float next = some ? __ldg(sw + sg.k0) : 0.0f;
-            int ks = sg.k0;
-            for (; ks < sg.k1; ++ks, ++it) {
-                const int s = it % SCALES, a = it % ACCS;
-                const uint64_t w2 = pair64(next, next);
-                if (some && ks + 1 < sg.k1) next = __ldg(sw + ks + 1);
-                if (!__all_sync(0xffffffffu, f8_wait(sc_full0 + 8 * s, (it / SCALES) & 1, &abort_sh, p.status) &&
-                                                 f8_wait(acc_full0 + 8 * a, (it / ACCS) & 1, &abort_sh, p.status)))
-                    break;
+            // many tokens: this thread's scales, AHEAD steps early (places past the tile's
+            // rows or N read their last one, and what comes of them is not stored)
+            constexpr int AHEAD = 4;
+            float x[AHEAD], w[AHEAD];
+            const float *sx = p.sx + sg.k0 * p.M + min(token, static_cast<int64_t>(sg.m0) + sg.cols - 1);
+            const float *sw = p.sw + (static_cast<int64_t>(sg.e) * p.nblocks + min((n0 + c0) / 128, p.nblocks - 1)) * p.ksteps;
+            auto load = [&](int ks, float &xs, float &ws) {
+                if (ks >= sg.k1) return;
+                xs = __ldg(sx);
+                ws = __ldg(sw + ks);
+                sx += p.M;
+            };
+            if constexpr (P::WIDE)
+#pragma unroll
+                for (int d = 0; d < AHEAD; ++d) load(sg.k0 + d, x[d], w[d]);
+            bool ok = true;
+            auto step = [&](int ks, float &xs, float &ws) {
+                const int a = it % ACCS, s = it % RING;
+                const float f1 = xs * ws;
+                if constexpr (P::WIDE) {
+                    load(ks + AHEAD, xs, ws);
+                    ok = f8_wait(acc_full0 + 8 * a, (it / ACCS) & 1, &abort_sh, p.status);
+                } else {
+                    ok = f8_wait(sc_full0 + 8 * s, (it / RING) & 1, &abort_sh, p.status) &&
+                         f8_wait(acc_full0 + 8 * a, (it / ACCS) & 1, &abort_sh, p.status);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                ++it;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t at = tmem + lanes + static_cast<uint32_t>(P::NCOLS * a + c0);
+                auto add = [&](int g, uint64_t (&sum)[16], bool last) {
+                    uint32_t v[32];
+                    tmem_ld32(at + 32 * g, v);
+                    if constexpr (P::WIDE) {
+                        tmem_wait32(v);
+                        if (last) hand_back(a);
+                        const uint64_t f = pair64(f1, f1);
 #pragma unroll
-                for (int g = 0; g < GROUPS; ++g) {
-                    if (g >= groups) break;
-                    uint32_t v[2][16];
-                    const uint32_t at = tmem + lanes + static_cast<uint32_t>(NT * a + c0 + 32 * g);
-                    tmem_ld_16x32(at, v[0]);
-                    tmem_ld_16x32(at + (16u << 16), v[1]);
-                    uint64_t f[4];
+                        for (int i = 0; i < 16; ++i) fma2(sum[i], pair64(v[2 * i], v[2 * i + 1]), f);
+                    } else {
+                        float4 f[8];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float4 x = *reinterpret_cast<const float4 *>(
-                            ring + s * NT + (((c0 + 32 * g) >> 4) + j) * 16 + (lane & 3) * 4);
-                        f[2 * j] = mul2(pair64(x.x, x.y), w2);
-                        f[2 * j + 1] = mul2(pair64(x.z, x.w), w2);
-                    }
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                        for (int i = 0; i < 8; ++i)
+                            f[i] = *reinterpret_cast<const float4 *>(ring + s * NT + 32 * g + 4 * i);
+                        tmem_wait32(v);
+                        if (last) hand_back(a);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            fma2(acc[g][h * 8 + i * 2], pair64(v[h][4 * i], v[h][4 * i + 1]), f[i]);
-                            fma2(acc[g][h * 8 + i * 2 + 1], pair64(v[h][4 * i + 2], v[h][4 * i + 3]), f[i]);
+                        for (int i = 0; i < 8; ++i) {
+                            fma2(sum[2 * i], pair64(v[4 * i], v[4 * i + 1]), pair64(f[i].x, f[i].y));
+                            fma2(sum[2 * i + 1], pair64(v[4 * i + 2], v[4 * i + 3]), pair64(f[i].z, f[i].w));
                         }
+                    }
+                };
+                if (groups == GROUPS) {
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) add(g, acc[g], g == GROUPS - 1);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < GROUPS - 1; ++g)
+                        if (g < groups) add(g, acc[g], g == groups - 1);
+                    if (groups == 0) hand_back(a);
                 }
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    arrive_cluster(acc_empty_even + 8 * a);
-                    mbar_arrive_local(sc_empty0 + 8 * s);
+                if constexpr (!P::WIDE) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_local(sc_empty0 + 8 * s);
                 }
-            }
-            if (ks < sg.k1) break;                       // a wait ran out
-            if (!some || groups <= 0) continue;          // nothing of the tile is this warp's
+            };
+            for (int ks = sg.k0; ok && ks < sg.k1; ks += AHEAD)
+#pragma unroll
+                for (int d = 0; d < AHEAD; ++d)
+                    if (ok && ks + d < sg.k1) step(ks + d, x[d], w[d]);
+            if (!ok) break;                              // a wait ran out
+            if (!some) continue;
             if (!sg.whole) {
                 // store the part; the warp that comes last adds all parts in order
-                auto slot = [&](int w) {
-                    return reinterpret_cast<uint64_t *>(
-                               p.slots + (static_cast<int64_t>(w) * 4 + (w == sg.first ? 2 : 0) + rank) * P::SLOT) +
+                auto slot = [&](int pr) {
+                    return reinterpret_cast<unsigned long long *>(
+                               p.slots + (static_cast<int64_t>(pr) * 4 + (pr == sg.first ? 2 : 0) + rank) * P::SLOT) +
                            static_cast<int64_t>(warp) * GROUPS * 16 * 32 + lane;
                 };
-                uint64_t *to = slot(pair);
+                unsigned long long *to = slot(pair);
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g)
                     if (g < groups)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) __stcg(reinterpret_cast<unsigned long long *>(to + (g * 16 + i) * 32), acc[g][i]);
+                        for (int i = 0; i < 16; ++i) __stcg(to + (g * 16 + i) * 32, acc[g][i]);
                 __threadfence();
                 __syncwarp();
                 unsigned int *counter = p.counters + (sg.first * 2 + static_cast<int>(rank)) * kF8MaxDrain + warp;
@@ -532,76 +613,128 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUt
                 if (lane == 0) *counter = 0u;
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g)
-                    if (g < groups) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[g][i] = 0ull;
-                        for (int w = sg.first; w <= sg.last; ++w) {
-                            const uint64_t *from = slot(w) + g * 16 * 32;
+                    for (int i = 0; i < 16; ++i) acc[g][i] = 0ull;
+                for (int pr = sg.first; pr <= sg.last; ++pr) {
+                    const unsigned long long *from = slot(pr);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                acc[g][i] = add2(acc[g][i], __ldcg(reinterpret_cast<const unsigned long long *>(from + i * 32)));
+                    for (int g = 0; g < GROUPS; ++g)
+                        if (g < groups)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[g][i] = add2(acc[g][i], __ldcg(from + (g * 16 + i) * 32));
+                }
+            }
+            if constexpr (P::WIDE) {
+                // ---- Y: a lane has a token's columns; 64 bytes of each of the warp's 32 rows at a
+                // time go through shared memory, so that four lanes store a row's 64 bytes.  A
+                // row's chunk c lies at c ^ (row / 2 % 4): no two of eight rows in one bank.
+                unsigned char *turn = smem + P::OFF_OUT + warp * 32 * 64;
+                const int esize = p.ytype == 0 ? 4 : 2, piece = 16 / esize;
+                unsigned char *y = static_cast<unsigned char *>(p.Y) +
+                                   ((static_cast<int64_t>(sg.m0) + row + (lane >> 2)) * p.ldy + n0 + c0 + (lane & 3) * piece) * esize;
+                auto turn_out = [&](const uint4 (&u)[4], int col) {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4 *>(turn + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = u[j];
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int at = r * 8 + (lane >> 2), left = cols_left - col - (lane & 3) * piece;
+                        if (at >= rows_left || left <= 0) continue;
+                        const uint4 o = *reinterpret_cast<const uint4 *>(turn + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4));
+                        unsigned char *to = y + (static_cast<int64_t>(r) * 8 * p.ldy + col) * esize;
+                        if (p.vec && left >= piece) {
+                            *reinterpret_cast<uint4 *>(to) = o;
+                        } else {
+                            const uint32_t h[4] = {o.x, o.y, o.z, o.w};
+                            if (esize == 4) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    if (j < left) reinterpret_cast<uint32_t *>(to)[j] = h[j];
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (j < left)
+                                        reinterpret_cast<uint16_t *>(to)[j] = static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1)));
+                            }
                         }
                     }
-            }
-            // ---- Y: a lane's fragments are two tokens (columns of the tile) by one weight row
-            const int nb = n0 + q * 32;                  // this warp's 32 columns of Y
-            if (p.ytype == 0) {
-                float *Y = static_cast<float *>(p.Y);
+                };
 #pragma unroll
-                for (int g = 0; g < GROUPS; ++g)
-                    if (g < groups)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int c = c0 + 32 * g + ((i >> 1) & 3) * 8 + (lane & 3) * 2;
-                            const int n = nb + (i >> 3) * 16 + (i & 1) * 8 + (lane >> 2);
-                            const float2 v = floats(acc[g][i]);
-                            if (n < p.N) {
-                                float *y = Y + (static_cast<int64_t>(sg.m0) + c) * p.ldy + n;
-                                if (c < sg.cols) *y = v.x;
-                                if (c + 1 < sg.cols) y[p.ldy] = v.y;
-                            }
-                        }
-            } else {
-                // sixteen tokens at a time through shared memory, turned on the way in
-                uint16_t *Y = static_cast<uint16_t *>(p.Y);
-                unsigned char *turn = smem + P::OFF_OUT + warp * P::OUT_ROWS * P::OUT_PITCH;
-                const uint32_t put = smem_u32(turn) + (lane & 7) * P::OUT_PITCH + (lane >> 3) * 16;
-#pragma unroll
-                for (int g = 0; g < GROUPS; ++g)
-                    if (g < groups)
+                for (int g = 0; g < GROUPS; ++g) {
+                    if (g >= groups) break;
+                    uint4 u[4];
+                    if (p.ytype == 0) {
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
-                            __syncwarp();
 #pragma unroll
-                            for (int ii = 0; ii < 2; ++ii) {
-                                uint32_t b[4];           // weight rows 0-7, 8-15, 16-23, 24-31
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const float2 v = floats(acc[g][(j >> 1) * 8 + (hh * 2 + ii) * 2 + (j & 1)]);
-                                    b[j] = f32_to_bf16_bits(v.x) | (static_cast<uint32_t>(f32_to_bf16_bits(v.y)) << 16);
-                                }
-                                asm volatile(
-                                    "stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
-                                    ::"r"(put + ii * 8 * P::OUT_PITCH), "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
-                                    : "memory");
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 a = floats(acc[g][hh * 8 + 2 * j]), b = floats(acc[g][hh * 8 + 2 * j + 1]);
+                                u[j] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                                                  __float_as_uint(b.y));
                             }
-                            __syncwarp();
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const int row = r * 8 + (lane >> 2), c = c0 + 32 * g + hh * 16 + row;
-                                const int n = nb + (lane & 3) * 8;
-                                if (c >= sg.cols || n >= p.N) continue;
-                                const uint4 v = *reinterpret_cast<const uint4 *>(turn + row * P::OUT_PITCH + (lane & 3) * 16);
-                                uint16_t *y = Y + (static_cast<int64_t>(sg.m0) + c) * p.ldy + n;
-                                if (p.vec && n + 8 <= p.N) {
-                                    *reinterpret_cast<uint4 *>(y) = v;
-                                } else {
-                                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                                    for (int j = 0; j < 8 && n + j < p.N; ++j)
-                                        y[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-                                }
-                            }
+                            turn_out(u, 32 * g + 16 * hh);
                         }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 a = floats(acc[g][4 * j + i]);
+                                h[i] = bf16_pair(a.x, a.y);
+                            }
+                            u[j] = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                        turn_out(u, 32 * g);
+                    }
+                }
+            } else {
+                // ---- Y: this lane's column n of tokens c0, c0 + 1, ...
+                const int n = n0 + row + lane;
+                const int64_t first = (static_cast<int64_t>(sg.m0) + c0) * p.ldy;
+                if (p.ytype == 1 && p.vec) {
+                    // two lanes exchange a value: the even one takes both columns of one token, the
+                    // odd one of the next, and a store is 4 bytes
+                    const int odd = lane & 1, ne = n - odd;
+                    uint16_t *y = static_cast<uint16_t *>(p.Y) + first + odd * p.ldy + ne;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g)
+                        if (g < groups)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int c = 32 * g + 2 * i;
+                                const float2 v = floats(acc[g][i]);
+                                const float got = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1);
+                                const uint32_t both = bf16_pair(odd ? got : v.x, odd ? v.y : got);
+                                if (c + odd < cols_left) {
+                                    uint16_t *to = y + c * p.ldy;
+                                    if (ne + 1 < p.N)
+                                        *reinterpret_cast<uint32_t *>(to) = both;
+                                    else if (ne < p.N)
+                                        *to = static_cast<uint16_t>(both);
+                                }
+                            }
+                } else {
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g)
+                        if (g < groups)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 v = floats(acc[g][i]);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int c = 32 * g + 2 * i + j;
+                                    const float u = j ? v.y : v.x;
+                                    if (n >= p.N || c >= cols_left) continue;
+                                    if (p.ytype == 0)
+                                        static_cast<float *>(p.Y)[first + c * p.ldy + n] = u;
+                                    else
+                                        static_cast<uint16_t *>(p.Y)[first + c * p.ldy + n] = f32_to_bf16_bits(u);
+                                }
+                            }
+                }
             }
         }
     }
@@ -632,7 +765,7 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
         cudaError_t e = cudaFuncGetAttributes(&at, kern);
         if (e != cudaSuccess) return cuda_fail(e);
         // the warps' own register counts have to be covered by the launch's
-        if (P::WIDE && at.numRegs * P::THREADS < 216 * 256 + 72 * 128) return TQ_ERR_DEVICE;
+        if (P::WIDE && at.numRegs * P::THREADS < 224 * 256 + 56 * 128) return TQ_ERR_DEVICE;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::smem(TQ_MAX_EXPERTS));
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dev.id] = true;
@@ -645,12 +778,13 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     p.sw = f.sw;
     p.N = static_cast<int>(f.N);
     p.ksteps = static_cast<int>((f.K + kStepK - 1) / kStepK);
-    p.nblocks = static_cast<int>((f.N + kRowsW - 1) / kRowsW);
-    p.ntiles = static_cast<int>((f.N + 2 * kRowsW - 1) / (2 * kRowsW));
+    p.nblocks = static_cast<int>((f.N + 127) / 128);
+    p.ntiles = static_cast<int>((f.N + kTileN - 1) / kTileN);
     p.Y = f.Y;
     p.ldy = f.ldy;
     p.ytype = f.ytype;
-    p.vec = (reinterpret_cast<uintptr_t>(f.Y) & 15) == 0 && f.ldy % 8 == 0 ? 1 : 0;
+    const int piece = P::WIDE ? 16 : 4;
+    p.vec = reinterpret_cast<uintptr_t>(f.Y) % piece == 0 && f.ldy * (f.ytype == 0 ? 4 : 2) % piece == 0 ? 1 : 0;
     p.status = status_word();
     if (!p.status) return TQ_ERR_DEVICE;
     const int most = dev.sms / 2;
@@ -658,15 +792,15 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     p.slots = static_cast<unsigned char *>(f.ws) + kF8CounterBytes(most);
     p.min_steps = 2;
     CUtensorMap tmW, tmX;
-    if (!make_map_u8(&tmW, f.Wq, p.experts * f.N, f.K, kStepK, kRowsW, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_u8(&tmX, f.Xq, f.M, f.K, kStepK, kBoxRows, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!make_map_u8(&tmW, f.Wq, p.experts * f.N, f.K, kStepK, P::WIDE ? P::B_BOX : kHalf, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_u8(&tmX, f.Xq, f.M, f.K, kStepK, P::WIDE ? kHalf : P::B_BOX, CU_TENSOR_MAP_SWIZZLE_128B))
         return TQ_ERR_DEVICE;
     // token tiles there may be: one more an expert than whole ones
     const int64_t token_tiles = f.M / NT + (f.M < p.experts ? f.M : p.experts);
     if (token_tiles * p.ntiles > (1ll << 30)) return TQ_ERR_OVERFLOW;
     const int64_t steps = token_tiles * p.ntiles * p.ksteps;
     const int64_t pairs = steps / p.min_steps < 1 ? 1 : (steps / p.min_steps < most ? steps / p.min_steps : most);
-    kern<<<static_cast<unsigned>(2 * pairs), P::THREADS, P::smem(p.experts), s>>>(tmW, tmX, p);
+    kern<<<static_cast<unsigned>(2 * pairs), P::THREADS, P::smem(p.experts), s>>>(P::WIDE ? tmX : tmW, P::WIDE ? tmW : tmX, p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
