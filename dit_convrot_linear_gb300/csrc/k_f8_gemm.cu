@@ -20,7 +20,7 @@
 //                the columns each) multiply and add, and write Y;
 //   MMA warp     allocates TMEM for the pair; in the even CTA one thread issues;
 //   copy warp    tensor copies of both operands into the ring (128-byte swizzle);
-//   scale warp   (few tokens) each step's scales, sx * sw, into a ring of their own.
+//   scale warp   each step's scales, sx * sw, into shared memory.
 //
 // The work is a list of tiles (expert, 256 columns, up to NT tokens).  Whole rounds
 // of tiles go to the pairs one by one; the K steps of a last round that would leave
@@ -56,12 +56,12 @@ struct F8Plan {
     static constexpr int STAGES = WIDE ? 6 : 10;
     static constexpr int ACCS = WIDE ? 2 : 4;                  // accumulators in TMEM
     static constexpr int TMEM = NCOLS * ACCS;
-    static constexpr int SCALES = WIDE ? 0 : 12;               // slots of the scale ring
+    static constexpr int SCALES = WIDE ? 256 : NT;             // scales of a step: a slot for each accumulator
     static constexpr int OFF_SCALES = STAGES * STAGE;
     static constexpr int OUT_BYTES = WIDE ? DRAIN * 32 * 64 : 0;   // 64 bytes of 32 rows a warp
-    static constexpr int OFF_OUT = OFF_SCALES + SCALES * NT * 4;
+    static constexpr int OFF_OUT = OFF_SCALES + ACCS * SCALES * 4;
     static constexpr int OFF_BARS = OFF_OUT + OUT_BYTES;
-    static constexpr int NBARS = 2 * STAGES + 2 * ACCS + 2 * SCALES + 1;
+    static constexpr int NBARS = 2 * STAGES + 3 * ACCS + 1;
     static constexpr int OFF_LIST = OFF_BARS + (NBARS * 8 + 15) / 16 * 16;
     // the list of experts: first row, rows, tiles before
     static constexpr int smem(int64_t experts) { return OFF_LIST + static_cast<int>(experts + 1) * 12 + 16; }
@@ -96,69 +96,64 @@ struct F8Seg {
     int first, last;
 };
 
-struct F8List {
-    const int *row0, *rows, *tiles;      // in shared memory: an expert's first row, rows, tiles before it
-    int experts, total;                  // total: token tiles of all experts
+// The list of work, in shared memory: of each expert its first row, its rows and the
+// token tiles before it (one more entry), and how the tiles are cut.
+struct F8Cut {
+    int tiles;       // tiles in all
+    int whole;       // of them computed whole
+    int units;       // K steps of the others,
+    int use;         // shared by this many pairs
 };
 
-template <int NT>
+// The pieces of work of a pair, in order.  (What does not change lies in shared
+// memory: the drain warps have few registers to spare.)
 struct F8Iter {
-    const F8List &l;
-    int pair, pairs, ksteps, ntiles, whole_tiles, i, use, first_pair;
-    long long units, u0, u;
-    __device__ F8Iter(const F8List &list, const F8Params &p, int pair_, int pairs_)
-        : l(list), pair(pair_), pairs(pairs_), ksteps(p.ksteps), ntiles(p.ntiles), i(0) {
-        const int tiles = l.total * ntiles;
-        const int rest = tiles % pairs;
-        // the last round is split where it would leave a good part of the pairs idle
-        const bool split = rest > 0 && rest * 100 < pairs * 85;
-        whole_tiles = split ? tiles - rest : tiles;
-        units = split ? static_cast<long long>(rest) * ksteps : 0;
-        use = pairs;                     // pairs that share the split steps
-        if (units < static_cast<long long>(pairs) * p.min_steps)
-            use = max(1, static_cast<int>(units / p.min_steps));
-        u0 = pair < use ? units * pair / use : 0;
-        u = pair < use ? units * (pair + 1) / use : 0;
-    }
-    __device__ int owner(long long x) const {      // the pair whose steps include x
-        int q = static_cast<int>(x * use / units);
-        while (q + 1 < use && units * (q + 1) / use <= x) ++q;
-        while (q > 0 && units * q / use > x) --q;
+    int i, u0;
+    __device__ F8Iter(const F8Cut &c, int pair) : i(0), u0(pair < c.use ? c.units * pair / c.use : 0) {}
+    // the pair whose steps include x
+    static __device__ int owner(const F8Cut &c, int x) {
+        int q = x * c.use / c.units;
+        while (q + 1 < c.use && c.units * (q + 1) / c.use <= x) ++q;
+        while (q > 0 && c.units * q / c.use > x) --q;
         return q;
     }
-    __device__ void place(int tile, F8Seg &s) const {
-        int lo = 0, hi = l.experts;      // tiles[lo] <= tile / ntiles < tiles[hi]
+    static __device__ void place(const int *list, const F8Params &p, int tile, F8Seg &s) {
+        const int *row0 = list, *rows = list + p.experts + 1, *tiles = rows + p.experts + 1;
+        int lo = 0, hi = p.experts;      // tiles[lo] * ntiles <= tile < tiles[hi] * ntiles
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (static_cast<long long>(l.tiles[mid]) * ntiles <= tile) lo = mid; else hi = mid;
+            if (tiles[mid] * p.ntiles <= tile) lo = mid; else hi = mid;
         }
-        const int at = tile - l.tiles[lo] * ntiles, parts = l.tiles[lo + 1] - l.tiles[lo];
-        const int rows = l.rows[lo], each = ((rows + parts - 1) / parts + 15) / 16 * 16;
+        const int at = tile - tiles[lo] * p.ntiles, parts = tiles[lo + 1] - tiles[lo];
+        const int n = rows[lo], each = ((n + parts - 1) / parts + 15) / 16 * 16;
         const int part = at % parts;
         s.e = lo;
         s.ntile = at / parts;
-        s.m0 = l.row0[lo] + part * each;
-        s.cols = min(each, rows - part * each);
+        s.m0 = row0[lo] + part * each;
+        s.cols = min(each, n - part * each);
     }
-    __device__ bool next(F8Seg &s) {
-        const long long t = pair + static_cast<long long>(i) * pairs;
-        if (t < whole_tiles) {
+    __device__ bool next(const F8Cut &c, const int *list, const F8Params &p, F8Seg &s) {
+        const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, ksteps = p.ksteps;
+        const int t = pair + i * pairs;
+        if (t < c.whole) {
             ++i;
-            place(static_cast<int>(t), s);
+            place(list, p, t, s);
             s.k0 = 0;
             s.k1 = ksteps;
             s.whole = true;
             return true;
         }
-        if (u0 >= u) return false;
-        const long long tl = u0 / ksteps, ts = tl * ksteps;
-        place(whole_tiles + static_cast<int>(tl), s);
-        s.k0 = static_cast<int>(u0 - ts);
-        s.k1 = static_cast<int>((u < ts + ksteps ? u : ts + ksteps) - ts);
+        const int u1 = pair < c.use ? c.units * (pair + 1) / c.use : 0;
+        if (u0 >= u1) return false;
+        const int tl = u0 / ksteps, ts = tl * ksteps;
+        place(list, p, c.whole + tl, s);
+        s.k0 = u0 - ts;
+        s.k1 = min(u1, ts + ksteps) - ts;
         s.whole = s.k0 == 0 && s.k1 == ksteps;
+        s.first = s.last = pair;
         if (!s.whole) {
-            s.first = owner(ts);
-            s.last = owner(ts + ksteps - 1);
+            s.first = owner(c, ts);
+            s.last = owner(c, ts + ksteps - 1);
         }
         u0 = ts + s.k1;
         return true;
@@ -253,20 +248,19 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 template <class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P::THREADS, 1)
 k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Params p) {
-    constexpr int NT = P::NT, DRAIN = P::DRAIN, STAGES = P::STAGES, ACCS = P::ACCS, SCALES = P::SCALES;
+    constexpr int NT = P::NT, DRAIN = P::DRAIN, STAGES = P::STAGES, ACCS = P::ACCS;
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + P::OFF_BARS);
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_sh;
-    __shared__ int total_sh;
+    __shared__ F8Cut cut;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
     const uint32_t acc_full0 = empty0 + 8 * STAGES, acc_empty0 = acc_full0 + 8 * ACCS;
-    const uint32_t sc_full0 = acc_empty0 + 8 * ACCS, sc_empty0 = sc_full0 + 8 * SCALES;
-    const uint32_t done = sc_empty0 + 8 * SCALES;
+    const uint32_t sc_empty0 = acc_empty0 + 8 * ACCS, done = sc_empty0 + 8 * ACCS;
 
     if (threadIdx.x == 0) {
         auto init = [](uint32_t bar, uint32_t n) {
@@ -277,26 +271,25 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             init(empty0 + 8 * s, 1);
         }
         for (int a = 0; a < ACCS; ++a) {
-            init(acc_full0 + 8 * a, 1);
+            init(acc_full0 + 8 * a, 2);             // the step's MMAs, and its scales
             init(acc_empty0 + 8 * a, 2 * DRAIN);    // used in the even CTA: both CTAs' drain warps
-        }
-        for (int s = 0; s < SCALES; ++s) {
-            init(sc_full0 + 8 * s, 1);
-            init(sc_empty0 + 8 * s, DRAIN);
+            init(sc_empty0 + 8 * a, DRAIN);         // the slot of the accumulator's scales has been read
         }
         init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         abort_sh = 0;
     }
     // the list of experts: a range that is out of order is empty
-    int *row0 = reinterpret_cast<int *>(smem + P::OFF_LIST), *rows = row0 + p.experts + 1, *tiles = rows + p.experts + 1;
+    const int *list = reinterpret_cast<const int *>(smem + P::OFF_LIST);
     if (warp == 0) {
+        int *row0 = reinterpret_cast<int *>(smem + P::OFF_LIST), *rows = row0 + p.experts + 1, *tiles = rows + p.experts + 1;
+        int total = static_cast<int>((p.M + NT - 1) / NT);       // token tiles
         if (p.offsets == nullptr) {
             if (lane == 0) {
                 row0[0] = 0;
                 rows[0] = static_cast<int>(p.M);
                 tiles[0] = 0;
-                tiles[1] = total_sh = static_cast<int>((p.M + NT - 1) / NT);
+                tiles[1] = total;
             }
         } else {
             int sum = 0, most = INT32_MIN;
@@ -331,7 +324,17 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 most = __shfl_sync(0xffffffffu, top, 31);
             }
             if (bad) atomicOr(p.status, kStatusIndex);
-            if (lane == 0) tiles[p.experts] = total_sh = sum;
+            if (lane == 0) tiles[p.experts] = sum;
+            total = sum;
+        }
+        if (lane == 0) {
+            // the last round of tiles is split where it would leave a good part of the pairs idle
+            const int n = total * p.ntiles, pairs = gridDim.x >> 1, rest = n % pairs;
+            const bool split = rest > 0 && rest * 100 < pairs * 85;
+            cut.tiles = n;
+            cut.whole = split ? n - rest : n;
+            cut.units = split ? rest * p.ksteps : 0;
+            cut.use = max(1, min(pairs, cut.units / p.min_steps));
         }
     }
     if (warp == DRAIN) {
@@ -344,8 +347,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     cluster_sync_all();   // barriers of both CTAs initialised, TMEM allocated
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_base_sh;
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const F8List list{row0, rows, tiles, p.experts, total_sh};
+    const int pair = blockIdx.x >> 1;
 
     if (warp >= DRAIN) {
         if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -358,9 +360,9 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             // -------------------------------------------- MMA issue (even CTA, one thread)
             if (rank == 0 && lane == 0) {
                 uint32_t it = 0;
-                F8Iter<NT> iter(list, p, pair, pairs);
+                F8Iter iter(cut, pair);
                 F8Seg sg;
-                while (!abort_sh && iter.next(sg)) {
+                while (!abort_sh && iter.next(cut, list, p, sg)) {
                     // D fp32, A and B e4m3, K-major, M = 256
                     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(mma_n(sg) >> 3) << 17) | (16u << 24);
                     for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
@@ -399,9 +401,9 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             // -------------------------------------------- tensor copies
             if (lane == 0) {
                 uint32_t it = 0;
-                F8Iter<NT> iter(list, p, pair, pairs);
+                F8Iter iter(cut, pair);
                 F8Seg sg;
-                while (!abort_sh && iter.next(sg)) {
+                while (!abort_sh && iter.next(cut, list, p, sg)) {
                     // rows of the M side that are past the tile's are not loaded (what comes of
                     // them is not stored); the N side is copied in whole boxes
                     const int n0 = sg.ntile * kTileN, half = mma_n(sg) / 2;
@@ -442,24 +444,36 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                     }
             }
-        } else if (!P::WIDE && warp == DRAIN + 2) {
-            // -------------------------------------------- the tokens' scales
-            // sx * sw of a step for each token, loaded AHEAD steps before it is stored
-            constexpr int AHEAD = 4, EACH = NT / 32, RING = P::SCALES > 0 ? P::SCALES : 1;
+        } else if (warp == DRAIN + 2) {
+            // -------------------------------------------- scales
+            // Each step's sx * sw into the accumulator's slot, loaded AHEAD steps before.  Many
+            // tokens: 128 of this CTA's tokens with the first scale block of columns, then with
+            // the second.  Few: each token with this CTA's block.  (Places past the tile's rows or
+            // N take their last one's; what comes of them is not stored.)
+            constexpr int AHEAD = 4, EACH = P::WIDE ? 4 : NT / 32, BLOCKS = P::WIDE ? 2 : 1;
             uint32_t it = 0;
-            F8Iter<NT> iter(list, p, pair, pairs);
+            F8Iter iter(cut, pair);
             F8Seg sg;
-            while (__all_sync(0xffffffffu, !abort_sh) && iter.next(sg)) {
-                const int n0 = sg.ntile * kTileN + static_cast<int>(rank) * kHalf;
-                const float *sw = p.sw + (static_cast<int64_t>(sg.e) * p.nblocks + n0 / 128) * p.ksteps;
-                const float *sx = p.sx + sg.m0 + lane;
-                float x[AHEAD][EACH], w[AHEAD];
-                auto load = [&](int ks, float (&xs)[EACH], float &ws) {
-                    const bool in = ks < sg.k1;
-                    ws = in && n0 < p.N ? __ldg(sw + ks) : 0.0f;
+            while (__all_sync(0xffffffffu, !abort_sh) && iter.next(cut, list, p, sg)) {
+                const int n0 = sg.ntile * kTileN + (P::WIDE ? 0 : static_cast<int>(rank) * kHalf);
+                const int t0 = P::WIDE ? static_cast<int>(rank) * kHalf : 0;
+                const float *sx[EACH], *sw[BLOCKS];
 #pragma unroll
-                    for (int i = 0; i < EACH; ++i)
-                        xs[i] = in && lane + 32 * i < sg.cols ? __ldg(sx + ks * p.M + 32 * i) : 0.0f;
+                for (int i = 0; i < EACH; ++i)
+                    sx[i] = p.sx + sg.k0 * p.M + sg.m0 + min(t0 + lane + 32 * i, sg.cols - 1);
+#pragma unroll
+                for (int j = 0; j < BLOCKS; ++j)
+                    sw[j] = p.sw + (static_cast<int64_t>(sg.e) * p.nblocks + min(n0 / 128 + j, p.nblocks - 1)) * p.ksteps;
+                float x[AHEAD][EACH], w[AHEAD][BLOCKS];
+                auto load = [&](int ks, float (&xs)[EACH], float (&ws)[BLOCKS]) {
+                    if (ks >= sg.k1) return;
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i) {
+                        xs[i] = __ldg(sx[i]);
+                        sx[i] += p.M;
+                    }
+#pragma unroll
+                    for (int j = 0; j < BLOCKS; ++j) ws[j] = __ldg(sw[j] + ks);
                 };
 #pragma unroll
                 for (int d = 0; d < AHEAD; ++d) load(sg.k0 + d, x[d], w[d]);
@@ -468,15 +482,17 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
                     for (int d = 0; d < AHEAD; ++d) {
                         if (!ok || ks + d >= sg.k1) break;
-                        const int s = it % RING;
-                        ok = __all_sync(0xffffffffu, f8_wait(sc_empty0 + 8 * s, ((it / RING) & 1) ^ 1, &abort_sh,
+                        const int a = it % ACCS;
+                        ok = __all_sync(0xffffffffu, f8_wait(sc_empty0 + 8 * a, ((it / ACCS) & 1) ^ 1, &abort_sh,
                                                              p.status));
                         if (!ok) break;
-                        float *to = reinterpret_cast<float *>(smem + P::OFF_SCALES) + s * NT + lane;
+                        float *to = reinterpret_cast<float *>(smem + P::OFF_SCALES) + a * P::SCALES + lane;
 #pragma unroll
-                        for (int i = 0; i < EACH; ++i) to[32 * i] = x[d][i] * w[d];
+                        for (int j = 0; j < BLOCKS; ++j)
+#pragma unroll
+                            for (int i = 0; i < EACH; ++i) to[32 * (j * EACH + i)] = x[d][i] * w[d][j];
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_local(sc_full0 + 8 * s);
+                        if (lane == 0) mbar_arrive_local(acc_full0 + 8 * a);
                         load(ks + d + AHEAD, x[d], w[d]);
                         ++it;
                     }
@@ -487,11 +503,11 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if constexpr (P::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ------------------------------------------------ drain
         constexpr int GROUPS = P::COLS / 32;             // 32 columns at a time
-        constexpr int RING = P::SCALES > 0 ? P::SCALES : 1;
         const int q = warp & 3, c0 = (warp >> 2) * P::COLS;
         const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
         const uint32_t acc_empty_even = in_even_cta(acc_empty0);
-        const float *ring = reinterpret_cast<const float *>(smem + P::OFF_SCALES) + c0;
+        const float *scales = reinterpret_cast<const float *>(smem + P::OFF_SCALES) +
+                              (P::WIDE ? c0 / 128 * 128 + q * 32 + lane : c0);
         // an accumulator has been read
         auto hand_back = [&](int a) {
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -499,94 +515,66 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (lane == 0) arrive_cluster(acc_empty_even + 8 * a);
         };
         uint32_t it = 0;
-        F8Iter<NT> iter(list, p, pair, pairs);
+        F8Iter iter(cut, pair);
         F8Seg sg;
         // the warp acts as one: a lane that saw an abort takes the others along
-        while (__all_sync(0xffffffffu, !abort_sh) && iter.next(sg)) {
+        while (__all_sync(0xffffffffu, !abort_sh) && iter.next(cut, list, p, sg)) {
             const int row = static_cast<int>(rank) * kHalf + q * 32;     // of this warp, on the M side
             const int n0 = sg.ntile * kTileN;
             const int rows_left = (P::WIDE ? sg.cols : p.N - n0) - row;
             const int cols_left = (P::WIDE ? p.N - n0 : sg.cols) - c0;
             const bool some = rows_left > 0 && cols_left > 0;            // this warp has some of the tile
             const int groups = some ? min(GROUPS, (cols_left + 31) / 32) : 0;
-            const int64_t token = static_cast<int64_t>(sg.m0) + row + lane;
             uint64_t acc[GROUPS][16];
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[g][i] = 0ull;
-            // many tokens: this thread's scales, AHEAD steps early (places past the tile's
-            // rows or N read their last one, and what comes of them is not stored)
-            constexpr int AHEAD = 4;
-            float x[AHEAD], w[AHEAD];
-            const float *sx = p.sx + sg.k0 * p.M + min(token, static_cast<int64_t>(sg.m0) + sg.cols - 1);
-            const float *sw = p.sw + (static_cast<int64_t>(sg.e) * p.nblocks + min((n0 + c0) / 128, p.nblocks - 1)) * p.ksteps;
-            auto load = [&](int ks, float &xs, float &ws) {
-                if (ks >= sg.k1) return;
-                xs = __ldg(sx);
-                ws = __ldg(sw + ks);
-                sx += p.M;
-            };
-            if constexpr (P::WIDE)
-#pragma unroll
-                for (int d = 0; d < AHEAD; ++d) load(sg.k0 + d, x[d], w[d]);
             bool ok = true;
-            auto step = [&](int ks, float &xs, float &ws) {
-                const int a = it % ACCS, s = it % RING;
-                const float f1 = xs * ws;
-                if constexpr (P::WIDE) {
-                    load(ks + AHEAD, xs, ws);
-                    ok = f8_wait(acc_full0 + 8 * a, (it / ACCS) & 1, &abort_sh, p.status);
-                } else {
-                    ok = f8_wait(sc_full0 + 8 * s, (it / RING) & 1, &abort_sh, p.status) &&
-                         f8_wait(acc_full0 + 8 * a, (it / ACCS) & 1, &abort_sh, p.status);
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                ++it;
+            int left = sg.k1 - sg.k0;
+#pragma unroll 1
+            for (; left > 0; --left, ++it) {
+                const int a = it % ACCS;
+                ok = __all_sync(0xffffffffu, f8_wait(acc_full0 + 8 * a, (it / ACCS) & 1, &abort_sh, p.status));
+                if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t at = tmem + lanes + static_cast<uint32_t>(P::NCOLS * a + c0);
-                auto add = [&](int g, uint64_t (&sum)[16], bool last) {
-                    uint32_t v[32];
-                    tmem_ld32(at + 32 * g, v);
-                    if constexpr (P::WIDE) {
+                if constexpr (P::WIDE) {
+                    // (columns past N too: what comes of them is not stored)
+                    const float f1 = scales[a * P::SCALES];
+                    const uint64_t f = pair64(f1, f1);
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        uint32_t v[32];
+                        tmem_ld32(at + 32 * g, v);
                         tmem_wait32(v);
-                        if (last) hand_back(a);
-                        const uint64_t f = pair64(f1, f1);
+                        if (g == GROUPS - 1) hand_back(a);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) fma2(sum[i], pair64(v[2 * i], v[2 * i + 1]), f);
-                    } else {
-                        float4 f[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            f[i] = *reinterpret_cast<const float4 *>(ring + s * NT + 32 * g + 4 * i);
-                        tmem_wait32(v);
-                        if (last) hand_back(a);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            fma2(sum[2 * i], pair64(v[4 * i], v[4 * i + 1]), pair64(f[i].x, f[i].y));
-                            fma2(sum[2 * i + 1], pair64(v[4 * i + 2], v[4 * i + 3]), pair64(f[i].z, f[i].w));
-                        }
+                        for (int i = 0; i < 16; ++i) fma2(acc[g][i], pair64(v[2 * i], v[2 * i + 1]), f);
                     }
-                };
-                if (groups == GROUPS) {
-#pragma unroll
-                    for (int g = 0; g < GROUPS; ++g) add(g, acc[g], g == GROUPS - 1);
                 } else {
 #pragma unroll
-                    for (int g = 0; g < GROUPS - 1; ++g)
-                        if (g < groups) add(g, acc[g], g == groups - 1);
+                    for (int g = 0; g < GROUPS; ++g)
+                        if (g < groups) {
+                            uint32_t v[32];
+                            tmem_ld32(at + 32 * g, v);
+                            float4 f[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                f[i] = *reinterpret_cast<const float4 *>(scales + a * P::SCALES + 32 * g + 4 * i);
+                            tmem_wait32(v);
+                            if (g == groups - 1) hand_back(a);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                fma2(acc[g][2 * i], pair64(v[4 * i], v[4 * i + 1]), pair64(f[i].x, f[i].y));
+                                fma2(acc[g][2 * i + 1], pair64(v[4 * i + 2], v[4 * i + 3]), pair64(f[i].z, f[i].w));
+                            }
+                        }
                     if (groups == 0) hand_back(a);
                 }
-                if constexpr (!P::WIDE) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_local(sc_empty0 + 8 * s);
-                }
-            };
-            for (int ks = sg.k0; ok && ks < sg.k1; ks += AHEAD)
-#pragma unroll
-                for (int d = 0; d < AHEAD; ++d)
-                    if (ok && ks + d < sg.k1) step(ks + d, x[d], w[d]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_local(sc_empty0 + 8 * a);
+            }
             if (!ok) break;                              // a wait ran out
             if (!some) continue;
             if (!sg.whole) {
