@@ -275,7 +275,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             init(acc_empty0 + 8 * a, 2 * DRAIN);    // used in the even CTA: both CTAs' drain warps
             init(sc_empty0 + 8 * a, DRAIN);         // the slot of the accumulator's scales has been read
         }
-        init(done, 1);
+        init(done, 2);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         abort_sh = 0;
     }
@@ -350,15 +350,18 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const int pair = blockIdx.x >> 1;
 
     if (warp >= DRAIN) {
-        if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
         // columns of a tile's accumulator: tokens, or weight rows, rounded up to 16
         auto mma_n = [&](const F8Seg &sg) {
             const int n = P::WIDE ? min(kTileN, p.N - sg.ntile * kTileN) : sg.cols;
             return (n + 15) / 16 * 16;
         };
-        if (warp == DRAIN) {
-            // -------------------------------------------- MMA issue (even CTA, one thread)
+        if (warp == DRAIN || warp == DRAIN + 3) {
+            // -------------------------------------------- MMA issue (even CTA, a thread of two warps)
+            // The two take the steps in turn: one's waits, commits and issues take 800 cycles a
+            // step, a step's MMAs 512.
             if (rank == 0 && lane == 0) {
+                const uint32_t turn = warp == DRAIN ? 0 : 1;
                 uint32_t it = 0;
                 F8Iter iter(cut, pair);
                 F8Seg sg;
@@ -366,6 +369,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     // D fp32, A and B e4m3, K-major, M = 256
                     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(mma_n(sg) >> 3) << 17) | (16u << 24);
                     for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
+                        if ((it & 1) != turn) continue;
                         const int s = it % STAGES, a = it % ACCS;
                         if (!f8_wait(acc_empty0 + 8 * a, ((it / ACCS) & 1) ^ 1, &abort_sh, p.status)) break;
                         if (!f8_wait(full0 + 8 * s, (it / STAGES) & 1, &abort_sh, p.status)) break;
@@ -389,7 +393,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     }
                 }
                 // let every issued MMA finish before the pair's TMEM is released
-                if (it > 0) {
+                {
                     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                                  ::"r"(done) : "memory");
                     const long long t0 = clock64();
@@ -500,7 +504,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
         __syncwarp();
     } else {
-        if constexpr (P::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        if constexpr (P::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ------------------------------------------------ drain
         constexpr int GROUPS = P::COLS / 32;             // 32 columns at a time
         const int q = warp & 3, c0 = (warp >> 2) * P::COLS;
@@ -753,7 +757,7 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
         cudaError_t e = cudaFuncGetAttributes(&at, kern);
         if (e != cudaSuccess) return cuda_fail(e);
         // the warps' own register counts have to be covered by the launch's
-        if (P::WIDE && at.numRegs * P::THREADS < 224 * 256 + 56 * 128) return TQ_ERR_DEVICE;
+        if (P::WIDE && at.numRegs * P::THREADS < 184 * 256 + 136 * 128) return TQ_ERR_DEVICE;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::smem(TQ_MAX_EXPERTS));
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dev.id] = true;
