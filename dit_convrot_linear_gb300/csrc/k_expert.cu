@@ -43,8 +43,20 @@ __device__ __forceinline__ float load_logit(const L *p) {
         return bf16_bits_to_f32(__ldg(p));
 }
 
-// A warp a token; lane l holds experts l, l + 32, ...  Each choice is two warp
-// reductions: the largest key, then the lowest expert that has it.
+// Puts the larger of two (key, expert) first; among equals the lower expert.
+__device__ __forceinline__ void order(uint32_t &ka, int &ea, uint32_t &kb, int &eb) {
+    const bool swap = kb > ka || (kb == ka && eb < ea);
+    const uint32_t k = swap ? kb : ka;
+    const int e = swap ? eb : ea;
+    kb = swap ? ka : kb;
+    eb = swap ? ea : eb;
+    ka = k;
+    ea = e;
+}
+
+// A warp a token; lane l holds experts l, l + 32, ..., sorted (a bitonic network).
+// Each choice is two warp reductions over the lanes' first ones: the largest key,
+// then the lowest expert that has it.
 template <typename L, int NI>
 __global__ void __launch_bounds__(256) k_expert_topk(const L *__restrict__ X, int64_t T, int E, int64_t ld, int k,
                                                      int renorm, int32_t *__restrict__ ids,
@@ -53,53 +65,76 @@ __global__ void __launch_bounds__(256) k_expert_topk(const L *__restrict__ X, in
     const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += step) {
         uint32_t key[NI];
+        int ex[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            key[i] = e < E ? logit_key(load_logit(X + t * ld + e)) : 0u;
+            ex[i] = lane + 32 * i;
+            key[i] = ex[i] < E ? logit_key(load_logit(X + t * ld + ex[i])) : 0u;
         }
-        float total = 0.0f;                      // over all experts, or over the chosen ones
-        float top = 0.0f, mine = 0.0f;
-        int id = -1;
-        uint32_t left[NI];
+        // the softmax over all experts is relative to the largest logit
+        uint32_t top = 0u;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) left[i] = key[i];
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = 0u;
-            int at = 0;
+        for (int i = 0; i < NI; ++i) top = max(top, key[i]);
+        top = __reduce_max_sync(kAll, top);
+        float all = 0.0f;
+        if (!renorm) {
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-                if (left[i] > best) {
-                    best = left[i];
-                    at = lane + 32 * i;
-                }
+                if (key[i] != 0u) all += expf(key_logit(key[i]) - key_logit(top));
+            all = warp_sum(all);
+        }
+        if constexpr (NI <= 8) {
+#pragma unroll
+            for (int size = 2; size <= NI; size <<= 1)
+#pragma unroll
+                for (int gap = size >> 1; gap > 0; gap >>= 1)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        if ((i & gap) == 0) {
+                            if ((i & size) == 0 || size == NI)
+                                order(key[i], ex[i], key[i | gap], ex[i | gap]);
+                            else
+                                order(key[i | gap], ex[i | gap], key[i], ex[i]);
+                        }
+        }
+        uint32_t chosen = 0u;                    // key of this lane's choice
+        int id = -1;
+        for (int j = 0; j < k; ++j) {
+            uint32_t best = key[0];
+            int at = ex[0];
+            if constexpr (NI > 8) {
+#pragma unroll
+                for (int i = 1; i < NI; ++i)
+                    if (key[i] > best) {
+                        best = key[i];
+                        at = ex[i];
+                    }
+            }
             const uint32_t win = __reduce_max_sync(kAll, best);
             if (win == 0u) break;                // nothing left that may be chosen
             const int e = static_cast<int>(__reduce_min_sync(kAll, best == win ? static_cast<uint32_t>(at) : 0xFFFFu));
+            if constexpr (NI > 8) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (lane + 32 * i == e) left[i] = 0u;
-            const float v = key_logit(win);
-            if (j == 0) {
-                top = v;
-                if (!renorm) {
-                    float s = 0.0f;
+                for (int i = 0; i < NI; ++i)
+                    if (ex[i] == e) key[i] = 0u;
+            } else if (at == e) {
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if (key[i] != 0u) s += expf(key_logit(key[i]) - top);
-                    total = warp_sum(s);
+                for (int i = 0; i + 1 < NI; ++i) {
+                    key[i] = key[i + 1];
+                    ex[i] = ex[i + 1];
                 }
+                key[NI - 1] = 0u;
             }
-            const float w = expf(v - top);
-            if (renorm) total += w;
             if (lane == j) {
                 id = e;
-                mine = w;
+                chosen = win;
             }
         }
+        const float w = id >= 0 ? expf(key_logit(chosen) - key_logit(top)) : 0.0f;
+        if (renorm) all = warp_sum(w);
         if (lane < k) {
             ids[t * k + lane] = id;
-            weights[t * k + lane] = id >= 0 ? mine / total : 0.0f;
+            weights[t * k + lane] = id >= 0 ? w / all : 0.0f;
         }
     }
 }
@@ -177,80 +212,140 @@ __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ 
 
 // ------------------------------------------------------------ the sort
 
-// A counting sort by one CTA: each warp counts the experts of its own piece of the
-// choices, the counts are summed over warps and experts, and each warp places its
-// piece in order.  Warps' pieces are in order, so equal experts stay in order.
-constexpr int kSortWarps = 32;
+// A counting sort by one cluster.  Each warp counts the experts of its own piece of the
+// choices; the counts are summed over warps, CTAs (through distributed shared memory)
+// and experts; then each warp places its piece.  Pieces are in order, and so are the
+// choices within one, so equal experts stay in order.  Bound by the chain of the steps
+// (a vote among lanes, an update of a shared counter) of a warp: 131072 choices of 256
+// experts 9.5 us with eight CTAs, 311 with one; at 128 choices one CTA takes 3.0 us,
+// eight take 5.7.
+constexpr int kSortWarps = 32, kSortCtas = 8, kSortAhead = 8;
+constexpr int64_t kSortOneCta = 8192;            // choices that one CTA sorts alone
+
+__device__ __forceinline__ int remote_int(uint32_t addr, int cta) {
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(cta));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *__restrict__ ids, int64_t n, int k,
                                                                  int E, int32_t *__restrict__ offsets,
                                                                  int32_t *__restrict__ token,
                                                                  int32_t *__restrict__ place, unsigned int *status) {
-    extern __shared__ int cnt[];                 // [warps][E], then [E + 1]
-    int *base = cnt + kSortWarps * E;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    extern __shared__ int cnt[];                 // [warps][E] counts, then [E] this CTA's, then [E] bases
+    int *sum_cta = cnt + kSortWarps * E, *base = sum_cta + E;
+    __shared__ int part[kSortWarps + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ctas = gridDim.x, cta = blockIdx.x;
     for (int i = threadIdx.x; i < kSortWarps * E; i += blockDim.x) cnt[i] = 0;
-    __syncthreads();
-    const int64_t per = ((n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const int64_t f0 = warp * per, f1 = f0 + per < n ? f0 + per : n;
+    const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
+    const int64_t per = ((n + warps - 1) / warps + 31) / 32 * 32;
+    const int64_t f0 = (static_cast<int64_t>(cta) * kSortWarps + warp) * per, f1 = f0 + per < n ? f0 + per : n;
     int *mine = cnt + warp * E;
-    for (int64_t f = f0; f < f1; f += 32) {
-        int e = -1;
-        if (f + lane < f1) {
-            e = ids[f + lane];
-            if (e < -1 || e >= E) {
-                atomicOr(status, kStatusIndex);
-                e = -1;
+    // f(position, expert or -1, the number given) for the piece's choices in order
+    auto walk = [&](auto &&f) {
+        for (int64_t at = f0; at < f1; at += 32 * kSortAhead) {
+            int e[kSortAhead];
+#pragma unroll
+            for (int i = 0; i < kSortAhead; ++i) {
+                const int64_t g = at + 32 * i + lane;
+                e[i] = g < f1 ? __ldg(ids + g) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kSortAhead; ++i) {
+                if (at + 32 * i >= f1) break;
+                const int v = static_cast<unsigned>(e[i]) < static_cast<unsigned>(E) ? e[i] : -1;
+                f(at + 32 * i + lane, v, e[i]);
             }
         }
-        const uint32_t same = __match_any_sync(kAll, e);
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
-    }
+    };
+    __syncthreads();
+    walk([&](int64_t, int e, int given) {
+        if (given != e) atomicOr(status, kStatusIndex);
+        if (e >= 0) atomicAdd(mine + e, 1);
+    });
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int sum = 0;
+#pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = cnt[w * E + e];
             cnt[w * E + e] = sum;
             sum += c;
         }
-        base[e] = sum;
+        sum_cta[e] = sum;
     }
+    if (ctas > 1) cluster_barrier(); else __syncthreads();
+    // a thread an expert (E <= 1024): choices of it in all CTAs, and in those before this one
+    const int e = threadIdx.x;
+    int all = 0, before = 0;
+    if (e < E) {
+        if (ctas > 1) {
+            const uint32_t addr = static_cast<uint32_t>(__cvta_generic_to_shared(sum_cta + e));
+#pragma unroll
+            for (int c = 0; c < kSortCtas; ++c) {
+                const int v = remote_int(addr, c);
+                all += v;
+                before += c < cta ? v : 0;
+            }
+        } else {
+            all = sum_cta[e];
+        }
+    }
+    int s = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, s, o);
+        if (lane >= o) s += v;
+    }
+    if (lane == 31) part[warp] = s;
     __syncthreads();
     if (warp == 0) {
-        int sum = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane, c = e < E ? base[e] : 0;
-            int s = c;
+        int v = part[lane];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(kAll, s, o);
-                if (lane >= o) s += v;
-            }
-            if (e < E) base[e] = sum + s - c;
-            sum += __shfl_sync(kAll, s, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kAll, v, o);
+            if (lane >= o) v += u;
         }
-        if (lane == 0) base[E] = sum;
+        part[lane] = v;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += blockDim.x) offsets[e] = base[e];
-    for (int64_t f = f0; f < f1; f += 32) {
-        int e = -1;
-        if (f + lane < f1) e = ids[f + lane];
-        if (e >= E) e = -1;
-        const uint32_t same = __match_any_sync(kAll, e);
+    const int start = s - all + (warp > 0 ? part[warp - 1] : 0), total = part[kSortWarps - 1];
+    if (e < E) {
+        base[e] = start + before;
+        if (cta == 0) offsets[e] = start;
+    }
+    if (cta == 0 && threadIdx.x == 0) offsets[E] = total;
+    __syncthreads();
+    const int bits = 32 - __clz(E);
+    walk([&](int64_t f, int e, int) {
+        // the lanes with the same expert: a vote for each bit of its number
+        uint32_t same = __ballot_sync(kAll, e >= 0);
+        for (int b = 0; b < bits; ++b) {
+            const bool one = (e >> b) & 1;
+            const uint32_t v = __ballot_sync(kAll, one);
+            same &= one ? v : ~v;
+        }
         int at = -1;
         if (e >= 0) {
             at = base[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
-            token[at] = static_cast<int32_t>((f + lane) / k);
+            token[at] = static_cast<int32_t>(f / k);
         }
-        if (f + lane < f1) place[f + lane] = at;
+        if (f < f1) place[f] = at;
         __syncwarp();
         if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
         __syncwarp();
-    }
-    for (int64_t i = base[E] + threadIdx.x; i < n; i += blockDim.x) token[i] = -1;
+    });
+    for (int64_t i = total + static_cast<int64_t>(cta) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<int64_t>(ctas) * blockDim.x)
+        token[i] = -1;
+    if (ctas > 1) cluster_barrier();             // nobody leaves while its counts may still be read
 }
 
 // ------------------------------------------------------------ rows there and back
@@ -307,6 +402,8 @@ __global__ void __launch_bounds__(256) k_expert_gather(const uint4 *__restrict__
     }
 }
 
+constexpr int kCombineRows = 8;
+
 // A thread a 16-byte piece of a token's row: the sum over its choices in their
 // order, in fp32.
 template <typename V>
@@ -320,17 +417,26 @@ __global__ void __launch_bounds__(256) k_expert_combine(const uint4 *__restrict_
         const int64_t t = i / pieces;
         const int c = static_cast<int>(i - t * pieces);
         float sum[P::N] = {};
-        for (int j = 0; j < k; ++j) {
-            const int32_t at = __ldg(place + t * k + j);
-            if (at < 0 || at >= rows) {
-                if (at != -1 && c == 0) atomicOr(status, kStatusIndex);
-                continue;
-            }
-            const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
-            float v[P::N];
-            P::widen(__ldg(Y + at * ldy + c), v);
+        for (int j0 = 0; j0 < k; j0 += kCombineRows) {       // as many rows on their way at once
+            uint4 row[kCombineRows];
+            float w[kCombineRows];
+            bool in[kCombineRows];
 #pragma unroll
-            for (int q = 0; q < P::N; ++q) sum[q] = fmaf(w, v[q], sum[q]);
+            for (int j = 0; j < kCombineRows; ++j) {
+                const int32_t at = j0 + j < k ? __ldg(place + t * k + j0 + j) : -1;
+                in[j] = at >= 0 && at < rows;
+                if (!in[j] && at != -1 && c == 0) atomicOr(status, kStatusIndex);
+                w[j] = weights && j0 + j < k ? __ldg(weights + t * k + j0 + j) : 1.0f;
+                if (in[j]) row[j] = ldg_stream(Y + at * ldy + c);
+            }
+#pragma unroll
+            for (int j = 0; j < kCombineRows; ++j) {
+                if (!in[j]) continue;
+                float v[P::N];
+                P::widen(row[j], v);
+#pragma unroll
+                for (int q = 0; q < P::N; ++q) sum[q] = fmaf(w[j], v[q], sum[q]);
+            }
         }
         O[t * ldo + c] = P::narrow(sum);
     }
@@ -451,16 +557,28 @@ tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, in
                              int32_t *place, const DeviceInfo &dev, cudaStream_t s) {
     unsigned int *status = status_word();
     if (!status || dev.id < 0 || dev.id >= 64) return TQ_ERR_DEVICE;
-    const int bytes = static_cast<int>((kSortWarps * E + E + 1) * 4);
+    const int bytes = static_cast<int>((kSortWarps * E + 2 * E) * 4);
     static bool configured[64] = {false};
     if (!configured[dev.id]) {
         const cudaError_t e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (kSortWarps * TQ_MAX_EXPERTS + TQ_MAX_EXPERTS + 1) * 4);
+                                                   (kSortWarps + 2) * TQ_MAX_EXPERTS * 4);
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dev.id] = true;
     }
-    k_expert_sort<<<1, 32 * kSortWarps, bytes, s>>>(ids, T * k, k, static_cast<int>(E), offsets, token, place, status);
-    return launched();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    const unsigned ctas = T * k <= kSortOneCta ? 1u : static_cast<unsigned>(kSortCtas);
+    attr[0].val.clusterDim = {ctas, 1u, 1u};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(32 * kSortWarps);
+    cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_expert_sort, ids, T * k, k, static_cast<int>(E), offsets, token,
+                                             place, status);
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
 
 tq_status launch_expert_gather(const void *X, int type, int64_t rows_x, int64_t W, int64_t ldx, const int32_t *rows,
