@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ 
 // (a vote among lanes, an update of a shared counter) of a warp: 131072 choices of 256
 // experts 9.5 us with eight CTAs, 311 with one; at 128 choices one CTA takes 3.0 us,
 // eight take 5.7.
-constexpr int kSortWarps = 32, kSortCtas = 8, kSortAhead = 8;
-constexpr int64_t kSortOneCta = 8192;            // choices that one CTA sorts alone
+constexpr int kSortWarps = 32, kSortCtas = 16, kSortAhead = 8;
+constexpr int64_t kSortOneCta = 2048;            // choices that one CTA sorts alone
 
 __device__ __forceinline__ int remote_int(uint32_t addr, int cta) {
     uint32_t at;
@@ -402,7 +402,8 @@ __global__ void __launch_bounds__(256) k_expert_gather(const uint4 *__restrict__
     }
 }
 
-constexpr int kCombineRows = 8;
+constexpr int kCombineRows = 8;         // of the sum
+constexpr int kGradRows = 4;
 
 // A thread a 16-byte piece of a token's row: the sum over its choices in their
 // order, in fp32.
@@ -442,7 +443,8 @@ __global__ void __launch_bounds__(256) k_expert_combine(const uint4 *__restrict_
     }
 }
 
-// A CTA a token: dY of each of its rows, w * dO, and dw = dO . Y.
+// A CTA a token: dY of each of its rows, w * dO, and dw = dO . Y, as many rows on
+// their way at once as in the sum.
 constexpr int kGradThreads = 256;
 template <typename V>
 __global__ void __launch_bounds__(kGradThreads) k_expert_combine_grad(
@@ -450,36 +452,55 @@ __global__ void __launch_bounds__(kGradThreads) k_expert_combine_grad(
     const int32_t *__restrict__ place, const float *__restrict__ weights, int64_t T, int k, uint4 *__restrict__ dY,
     int64_t lddy, float *__restrict__ dw, unsigned int *status) {
     using P = Piece<V>;
-    __shared__ float part[kGradThreads / 32];
+    __shared__ float part[kGradRows][kGradThreads / 32];
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-        for (int j = 0; j < k; ++j) {
-            const int32_t at = __ldg(place + t * k + j);
-            const bool in = at >= 0 && at < rows;
-            if (!in && at != -1 && threadIdx.x == 0) atomicOr(status, kStatusIndex);
-            float dot = 0.0f;
-            if (in) {
-                const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
-                for (int c = threadIdx.x; c < pieces; c += kGradThreads) {
-                    float d[P::N], v[P::N];
-                    P::widen(__ldg(dO + t * ldo + c), d);
-                    if (dw) {
-                        P::widen(__ldg(Y + at * ldy + c), v);
+        for (int j0 = 0; j0 < k; j0 += kGradRows) {
+            int32_t at[kGradRows];
+            float w[kGradRows], dot[kGradRows];
 #pragma unroll
-                        for (int q = 0; q < P::N; ++q) dot = fmaf(d[q], v[q], dot);
+            for (int j = 0; j < kGradRows; ++j) {
+                at[j] = j0 + j < k ? __ldg(place + t * k + j0 + j) : -1;
+                w[j] = weights && j0 + j < k ? __ldg(weights + t * k + j0 + j) : 1.0f;
+                dot[j] = 0.0f;
+                if (at[j] < -1 || at[j] >= rows) {
+                    if (threadIdx.x == 0) atomicOr(status, kStatusIndex);
+                    at[j] = -1;
+                }
+            }
+            for (int c = threadIdx.x; c < pieces; c += kGradThreads) {
+                uint4 row[kGradRows];
+                if (dw)
+#pragma unroll
+                    for (int j = 0; j < kGradRows; ++j)
+                        if (at[j] >= 0) row[j] = ldg_stream(Y + at[j] * ldy + c);
+                float d[P::N];
+                P::widen(__ldg(dO + t * ldo + c), d);
+#pragma unroll
+                for (int j = 0; j < kGradRows; ++j) {
+                    if (at[j] < 0) continue;
+                    float v[P::N];
+                    if (dw) {
+                        P::widen(row[j], v);
+#pragma unroll
+                        for (int q = 0; q < P::N; ++q) dot[j] = fmaf(d[q], v[q], dot[j]);
                     }
 #pragma unroll
-                    for (int q = 0; q < P::N; ++q) d[q] *= w;
-                    dY[at * lddy + c] = P::narrow(d);
+                    for (int q = 0; q < P::N; ++q) v[q] = d[q] * w[j];
+                    dY[at[j] * lddy + c] = P::narrow(v);
                 }
             }
             if (dw) {
-                dot = warp_sum(dot);
-                if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+#pragma unroll
+                for (int j = 0; j < kGradRows; ++j) {
+                    dot[j] = warp_sum(dot[j]);
+                    if ((threadIdx.x & 31) == 0) part[j][threadIdx.x >> 5] = dot[j];
+                }
                 __syncthreads();
-                if (threadIdx.x == 0) {
+                if (threadIdx.x < kGradRows && j0 + threadIdx.x < k) {
                     float s = 0.0f;
-                    for (int i = 0; i < kGradThreads / 32; ++i) s += part[i];
-                    dw[t * k + j] = s;
+#pragma unroll
+                    for (int i = 0; i < kGradThreads / 32; ++i) s += part[threadIdx.x][i];
+                    dw[t * k + j0 + threadIdx.x] = s;
                 }
                 __syncthreads();
             }
@@ -539,7 +560,7 @@ struct TopkGrad {
 tq_status launch_expert_topk(const void *logits, int type, int64_t T, int64_t E, int64_t ld, int k, int renorm,
                              int32_t *ids, float *weights, const DeviceInfo &dev, cudaStream_t s) {
     by_experts<Topk>(E, logits, type, T, static_cast<int>(E), ld, k, renorm, ids, weights,
-                     grid_of((T + 7) / 8, dev, 8), s);
+                     grid_of((T + 7) / 8, dev, 64), s);
     return launched();
 }
 
@@ -549,7 +570,7 @@ tq_status launch_expert_topk_grad(const void *logits, int type, int64_t T, int64
     unsigned int *status = status_word();
     if (!status) return TQ_ERR_DEVICE;
     by_experts<TopkGrad>(E, logits, type, T, static_cast<int>(E), ld, ids, dw, k, renorm, dlogits, ldd, status,
-                         grid_of((T + 7) / 8, dev, 8), s);
+                         grid_of((T + 7) / 8, dev, 64), s);
     return launched();
 }
 
@@ -560,8 +581,10 @@ tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, in
     const int bytes = static_cast<int>((kSortWarps * E + 2 * E) * 4);
     static bool configured[64] = {false};
     if (!configured[dev.id]) {
-        const cudaError_t e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (kSortWarps + 2) * TQ_MAX_EXPERTS * 4);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dev.id] = true;
     }

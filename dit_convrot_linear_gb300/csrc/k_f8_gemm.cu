@@ -49,19 +49,25 @@ struct F8Plan {
     static constexpr int NCOLS = WIDE ? kTileN : NT;           // columns of an accumulator: the N side
     static constexpr int COLS = WIDE ? 128 : 64;               // columns a drain warp
     static constexpr int DRAIN = 4 * NCOLS / COLS;             // drain warps
-    static constexpr int THREADS = (DRAIN + 4) * 32;
-    static constexpr int B_BOX = WIDE ? 128 : 32;              // rows of one tensor copy of the N side
+    // many tokens: a step's columns are two accumulators of 128, each with its own MMAs, so
+    // that one is filled while the other is drained
+    static constexpr int HALVES = WIDE ? 2 : 1;
+    static constexpr int ISSUERS = 2 * HALVES;                 // MMA warps: the steps in turn, a half each
+    static constexpr int OTHERS = WIDE ? 8 : 4;                // warps that do not drain
+    static constexpr int THREADS = (DRAIN + OTHERS) * 32;
+    static constexpr int B_BOX = WIDE ? 64 : 32;               // rows of one tensor copy of the N side
     static constexpr int B_BYTES = NCOLS / 2 * kStepK;
     static constexpr int STAGE = kABytes + B_BYTES;
     static constexpr int STAGES = WIDE ? 6 : 10;
-    static constexpr int ACCS = WIDE ? 2 : 4;                  // accumulators in TMEM
-    static constexpr int TMEM = NCOLS * ACCS;
-    static constexpr int SCALES = WIDE ? 256 : NT;             // scales of a step: a slot for each accumulator
+    static constexpr int TURNS = WIDE ? 2 : 4;                 // steps with accumulators in TMEM
+    static constexpr int ACCS = TURNS * HALVES, ACC_COLS = NCOLS / HALVES;
+    static constexpr int TMEM = ACC_COLS * ACCS;
+    static constexpr int SCALES = WIDE ? 256 : NT;             // scales of a step: a slot for each turn
     static constexpr int OFF_SCALES = STAGES * STAGE;
     static constexpr int OUT_BYTES = WIDE ? DRAIN * 32 * 64 : 0;   // 64 bytes of 32 rows a warp
-    static constexpr int OFF_OUT = OFF_SCALES + ACCS * SCALES * 4;
+    static constexpr int OFF_OUT = OFF_SCALES + TURNS * SCALES * 4;
     static constexpr int OFF_BARS = OFF_OUT + OUT_BYTES;
-    static constexpr int NBARS = 2 * STAGES + 3 * ACCS + 1;
+    static constexpr int NBARS = 2 * STAGES + 2 * ACCS + TURNS + 1;
     static constexpr int OFF_LIST = OFF_BARS + (NBARS * 8 + 15) / 16 * 16;
     // the list of experts: first row, rows, tiles before
     static constexpr int smem(int64_t experts) { return OFF_LIST + static_cast<int>(experts + 1) * 12 + 16; }
@@ -217,28 +223,6 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&v)[32]) {
     asm volatile("" : "+r"(v[30]), "+r"(v[31]));
 }
 
-__device__ __forceinline__ uint64_t pair64(uint32_t lo, uint32_t hi) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    return d;
-}
-__device__ __forceinline__ uint64_t pair64(float lo, float hi) {
-    return pair64(__float_as_uint(lo), __float_as_uint(hi));
-}
-__device__ __forceinline__ float2 floats(uint64_t v) {
-    uint32_t lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ void fma2(uint64_t &c, uint64_t a, uint64_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
-}
-
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -248,7 +232,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 template <class P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P::THREADS, 1)
 k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Params p) {
-    constexpr int NT = P::NT, DRAIN = P::DRAIN, STAGES = P::STAGES, ACCS = P::ACCS;
+    constexpr int NT = P::NT, DRAIN = P::DRAIN, STAGES = P::STAGES, ACCS = P::ACCS, TURNS = P::TURNS, HALVES = P::HALVES;
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + P::OFF_BARS);
     __shared__ uint32_t tmem_base_sh;
@@ -260,7 +244,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
     const uint32_t acc_full0 = empty0 + 8 * STAGES, acc_empty0 = acc_full0 + 8 * ACCS;
-    const uint32_t sc_empty0 = acc_empty0 + 8 * ACCS, done = sc_empty0 + 8 * ACCS;
+    const uint32_t sc_empty0 = acc_empty0 + 8 * ACCS, done = sc_empty0 + 8 * TURNS;
 
     if (threadIdx.x == 0) {
         auto init = [](uint32_t bar, uint32_t n) {
@@ -268,14 +252,14 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         };
         for (int s = 0; s < STAGES; ++s) {
             init(full0 + 8 * s, 1);                 // used in the even CTA: its expected bytes cover both
-            init(empty0 + 8 * s, 1);
+            init(empty0 + 8 * s, HALVES);
         }
         for (int a = 0; a < ACCS; ++a) {
             init(acc_full0 + 8 * a, 2);             // the step's MMAs, and its scales
-            init(acc_empty0 + 8 * a, 2 * DRAIN);    // used in the even CTA: both CTAs' drain warps
-            init(sc_empty0 + 8 * a, DRAIN);         // the slot of the accumulator's scales has been read
+            init(acc_empty0 + 8 * a, 2 * DRAIN / HALVES);   // used in the even CTA: both CTAs' drain warps
         }
-        init(done, 2);
+        for (int s = 0; s < TURNS; ++s) init(sc_empty0 + 8 * s, DRAIN);   // a step's scales have been read
+        init(done, P::ISSUERS);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         abort_sh = 0;
     }
@@ -350,58 +334,57 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const int pair = blockIdx.x >> 1;
 
     if (warp >= DRAIN) {
-        if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
-        // columns of a tile's accumulator: tokens, or weight rows, rounded up to 16
-        auto mma_n = [&](const F8Seg &sg) {
-            const int n = P::WIDE ? min(kTileN, p.N - sg.ntile * kTileN) : sg.cols;
-            return (n + 15) / 16 * 16;
+        if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // columns of accumulator h of a tile: tokens, or weight rows, rounded up to 16 (one
+        // without any still takes part, and nothing of it is stored)
+        auto mma_n = [&](const F8Seg &sg, int h) {
+            const int n = P::WIDE ? min(P::ACC_COLS, p.N - sg.ntile * kTileN - h * P::ACC_COLS) : sg.cols;
+            return (max(n, 1) + 15) / 16 * 16;
         };
-        if (warp == DRAIN || warp == DRAIN + 3) {
-            // -------------------------------------------- MMA issue (even CTA, a thread of two warps)
-            // The two take the steps in turn: one's waits, commits and issues take 800 cycles a
-            // step, a step's MMAs 512.
+        if (warp < DRAIN + P::ISSUERS) {
+            // -------------------------------------------- MMA issue (even CTA, one thread a warp)
+            // A step's waits, commits and issues take one thread 800 cycles, its MMAs 512.
             if (rank == 0 && lane == 0) {
-                const uint32_t turn = warp == DRAIN ? 0 : 1;
+                const int h = (warp - DRAIN) % HALVES;
+                const uint32_t turn = (warp - DRAIN) / HALVES;
                 uint32_t it = 0;
                 F8Iter iter(cut, pair);
                 F8Seg sg;
                 while (!abort_sh && iter.next(cut, list, p, sg)) {
                     // D fp32, A and B e4m3, K-major, M = 256
-                    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(mma_n(sg) >> 3) << 17) | (16u << 24);
+                    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(mma_n(sg, h) >> 3) << 17) | (16u << 24);
                     for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
                         if ((it & 1) != turn) continue;
-                        const int s = it % STAGES, a = it % ACCS;
-                        if (!f8_wait(acc_empty0 + 8 * a, ((it / ACCS) & 1) ^ 1, &abort_sh, p.status)) break;
+                        const int s = it % STAGES, a = (it % TURNS) * HALVES + h;
                         if (!f8_wait(full0 + 8 * s, (it / STAGES) & 1, &abort_sh, p.status)) break;
+                        if (!f8_wait(acc_empty0 + 8 * a, ((it / TURNS) & 1) ^ 1, &abort_sh, p.status)) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const uint32_t at = smem_u32(smem + s * P::STAGE);
-                        const uint64_t ad = f8_desc(at), bd = f8_desc(at + kABytes);
+                        const uint64_t ad = f8_desc(at), bd = f8_desc(at + kABytes + h * P::B_BOX * kStepK);
 #pragma unroll
                         for (int kk = 0; kk < kStepK / 32; ++kk)
                             asm volatile(
                                 "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
                                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-                                ::"r"(tmem + static_cast<uint32_t>(P::NCOLS * a)), "l"(ad + 2 * kk), "l"(bd + 2 * kk),
+                                ::"r"(tmem + static_cast<uint32_t>(P::ACC_COLS * a)), "l"(ad + 2 * kk), "l"(bd + 2 * kk),
                                   "r"(idesc), "r"(kk > 0 ? 1u : 0u));
                         auto commit = [](uint32_t bar) {
                             asm volatile(
                                 "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
                                 ".b64 [%0], %1;" ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
                         };
-                        commit(empty0 + 8 * s);
                         commit(acc_full0 + 8 * a);
+                        commit(empty0 + 8 * s);
                     }
                 }
                 // let every issued MMA finish before the pair's TMEM is released
-                {
-                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                                 ::"r"(done) : "memory");
-                    const long long t0 = clock64();
-                    while (!mbar_try(done, 0) && clock64() - t0 < kF8WaitLimit) {
-                    }
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                             ::"r"(done) : "memory");
+                const long long t0 = clock64();
+                while (!f8_try(done, 0) && clock64() - t0 < kF8WaitLimit) {
                 }
             }
-        } else if (warp == DRAIN + 1) {
+        } else if (warp == DRAIN + P::ISSUERS) {
             // -------------------------------------------- tensor copies
             if (lane == 0) {
                 uint32_t it = 0;
@@ -409,16 +392,16 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 F8Seg sg;
                 while (!abort_sh && iter.next(cut, list, p, sg)) {
                     // rows of the M side that are past the tile's are not loaded (what comes of
-                    // them is not stored); the N side is copied in whole boxes
-                    const int n0 = sg.ntile * kTileN, half = mma_n(sg) / 2;
+                    // them is not stored); the N side is copied in whole boxes, which hold half
+                    // of an accumulator's columns in each CTA
+                    const int n0 = sg.ntile * kTileN;
                     const int wrow = sg.e * p.N + n0;
                     const int rows_a = P::WIDE ? sg.cols : p.N - n0;
-                    const int boxes = (half + P::B_BOX - 1) / P::B_BOX;
+                    const int halves = HALVES == 2 && p.N - n0 > P::ACC_COLS ? 2 : 1;
                     const bool mine = static_cast<int>(rank) * kHalf < rows_a;
                     const uint32_t bytes =
-                        2 * boxes * P::B_BOX * kStepK + (kHalf < rows_a ? 2 * kABytes : kABytes);
+                        2 * halves * P::B_BOX * kStepK + (kHalf < rows_a ? 2 * kABytes : kABytes);
                     const int arow = (P::WIDE ? sg.m0 : wrow) + static_cast<int>(rank) * kHalf;
-                    const int brow = (P::WIDE ? wrow : sg.m0) + static_cast<int>(rank) * half;
                     for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
                         const int s = it % STAGES;
                         if (!f8_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, &abort_sh, p.status)) break;
@@ -435,22 +418,25 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                                 : "memory");
                         };
                         if (mine) copy(at, &tmA, arow);
-                        for (int b = 0; b < boxes; ++b)
-                            copy(at + kABytes + b * P::B_BOX * kStepK, &tmB, brow + b * P::B_BOX);
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+                            if (h < halves)
+                                copy(at + kABytes + h * P::B_BOX * kStepK, &tmB,
+                                     (P::WIDE ? wrow + h * P::ACC_COLS : sg.m0) + static_cast<int>(rank) * (mma_n(sg, h) / 2));
                     }
                 }
                 // after a wait ran out: the copies in flight land before the pair leaves
                 if (abort_sh && rank == 0)
                     for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j) {
                         const long long t0 = clock64();
-                        while (!mbar_try(full0 + 8 * (j % STAGES), (j / STAGES) & 1) &&
+                        while (!f8_try(full0 + 8 * (j % STAGES), (j / STAGES) & 1) &&
                                clock64() - t0 < kF8WaitLimit / 16) {
                         }
                     }
             }
-        } else if (warp == DRAIN + 2) {
+        } else if (warp == DRAIN + P::ISSUERS + 1) {
             // -------------------------------------------- scales
-            // Each step's sx * sw into the accumulator's slot, loaded AHEAD steps before.  Many
+            // Each step's sx * sw into its turn's slot, loaded AHEAD steps before.  Many
             // tokens: 128 of this CTA's tokens with the first scale block of columns, then with
             // the second.  Few: each token with this CTA's block.  (Places past the tile's rows or
             // N take their last one's; what comes of them is not stored.)
@@ -486,17 +472,17 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
                     for (int d = 0; d < AHEAD; ++d) {
                         if (!ok || ks + d >= sg.k1) break;
-                        const int a = it % ACCS;
-                        ok = __all_sync(0xffffffffu, f8_wait(sc_empty0 + 8 * a, ((it / ACCS) & 1) ^ 1, &abort_sh,
+                        const int s = it % TURNS;
+                        ok = __all_sync(0xffffffffu, f8_wait(sc_empty0 + 8 * s, ((it / TURNS) & 1) ^ 1, &abort_sh,
                                                              p.status));
                         if (!ok) break;
-                        float *to = reinterpret_cast<float *>(smem + P::OFF_SCALES) + a * P::SCALES + lane;
+                        float *to = reinterpret_cast<float *>(smem + P::OFF_SCALES) + s * P::SCALES + lane;
 #pragma unroll
                         for (int j = 0; j < BLOCKS; ++j)
 #pragma unroll
                             for (int i = 0; i < EACH; ++i) to[32 * (j * EACH + i)] = x[d][i] * w[d][j];
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_local(acc_full0 + 8 * a);
+                        if (lane < HALVES) mbar_arrive_local(acc_full0 + 8 * (s * HALVES + lane));
                         load(ks + d + AHEAD, x[d], w[d]);
                         ++it;
                     }
@@ -507,7 +493,8 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if constexpr (P::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ------------------------------------------------ drain
         constexpr int GROUPS = P::COLS / 32;             // 32 columns at a time
-        const int q = warp & 3, c0 = (warp >> 2) * P::COLS;
+        const int q = warp & 3, c0 = (warp >> 2) * P::COLS;     // c0: first column of the tile
+        const int h = HALVES == 2 ? warp >> 2 : 0;       // the accumulator it drains
         const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
         const uint32_t acc_empty_even = in_even_cta(acc_empty0);
         const float *scales = reinterpret_cast<const float *>(smem + P::OFF_SCALES) +
@@ -529,24 +516,23 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const int cols_left = (P::WIDE ? p.N - n0 : sg.cols) - c0;
             const bool some = rows_left > 0 && cols_left > 0;            // this warp has some of the tile
             const int groups = some ? min(GROUPS, (cols_left + 31) / 32) : 0;
-            uint64_t acc[GROUPS][16];
+            float acc[GROUPS][32];
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[g][i] = 0ull;
+                for (int i = 0; i < 32; ++i) acc[g][i] = 0.0f;
             bool ok = true;
             int left = sg.k1 - sg.k0;
 #pragma unroll 1
             for (; left > 0; --left, ++it) {
-                const int a = it % ACCS;
-                ok = __all_sync(0xffffffffu, f8_wait(acc_full0 + 8 * a, (it / ACCS) & 1, &abort_sh, p.status));
+                const int s = it % TURNS, a = s * HALVES + h;
+                ok = __all_sync(0xffffffffu, f8_wait(acc_full0 + 8 * a, (it / TURNS) & 1, &abort_sh, p.status));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t at = tmem + lanes + static_cast<uint32_t>(P::NCOLS * a + c0);
+                const uint32_t at = tmem + lanes + static_cast<uint32_t>(P::ACC_COLS * a + (HALVES == 2 ? 0 : c0));
                 if constexpr (P::WIDE) {
                     // (columns past N too: what comes of them is not stored)
-                    const float f1 = scales[a * P::SCALES];
-                    const uint64_t f = pair64(f1, f1);
+                    const float f1 = scales[s * P::SCALES];
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g) {
                         uint32_t v[32];
@@ -554,7 +540,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         tmem_wait32(v);
                         if (g == GROUPS - 1) hand_back(a);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) fma2(acc[g][i], pair64(v[2 * i], v[2 * i + 1]), f);
+                        for (int i = 0; i < 32; ++i) acc[g][i] = fmaf(__uint_as_float(v[i]), f1, acc[g][i]);
                     }
                 } else {
 #pragma unroll
@@ -565,35 +551,37 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             float4 f[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                f[i] = *reinterpret_cast<const float4 *>(scales + a * P::SCALES + 32 * g + 4 * i);
+                                f[i] = *reinterpret_cast<const float4 *>(scales + s * P::SCALES + 32 * g + 4 * i);
                             tmem_wait32(v);
                             if (g == groups - 1) hand_back(a);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                fma2(acc[g][2 * i], pair64(v[4 * i], v[4 * i + 1]), pair64(f[i].x, f[i].y));
-                                fma2(acc[g][2 * i + 1], pair64(v[4 * i + 2], v[4 * i + 3]), pair64(f[i].z, f[i].w));
+                                acc[g][4 * i] = fmaf(__uint_as_float(v[4 * i]), f[i].x, acc[g][4 * i]);
+                                acc[g][4 * i + 1] = fmaf(__uint_as_float(v[4 * i + 1]), f[i].y, acc[g][4 * i + 1]);
+                                acc[g][4 * i + 2] = fmaf(__uint_as_float(v[4 * i + 2]), f[i].z, acc[g][4 * i + 2]);
+                                acc[g][4 * i + 3] = fmaf(__uint_as_float(v[4 * i + 3]), f[i].w, acc[g][4 * i + 3]);
                             }
                         }
                     if (groups == 0) hand_back(a);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive_local(sc_empty0 + 8 * a);
+                if (lane == 0) mbar_arrive_local(sc_empty0 + 8 * s);
             }
             if (!ok) break;                              // a wait ran out
             if (!some) continue;
             if (!sg.whole) {
                 // store the part; the warp that comes last adds all parts in order
                 auto slot = [&](int pr) {
-                    return reinterpret_cast<unsigned long long *>(
+                    return reinterpret_cast<float2 *>(
                                p.slots + (static_cast<int64_t>(pr) * 4 + (pr == sg.first ? 2 : 0) + rank) * P::SLOT) +
                            static_cast<int64_t>(warp) * GROUPS * 16 * 32 + lane;
                 };
-                unsigned long long *to = slot(pair);
+                float2 *to = slot(pair);
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g)
                     if (g < groups)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) __stcg(to + (g * 16 + i) * 32, acc[g][i]);
+                        for (int i = 0; i < 16; ++i) __stcg(to + (g * 16 + i) * 32, make_float2(acc[g][2 * i], acc[g][2 * i + 1]));
                 __threadfence();
                 __syncwarp();
                 unsigned int *counter = p.counters + (sg.first * 2 + static_cast<int>(rank)) * kF8MaxDrain + warp;
@@ -606,14 +594,18 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[g][i] = 0ull;
+                    for (int i = 0; i < 32; ++i) acc[g][i] = 0.0f;
                 for (int pr = sg.first; pr <= sg.last; ++pr) {
-                    const unsigned long long *from = slot(pr);
+                    const float2 *from = slot(pr);
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g)
                         if (g < groups)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[g][i] = add2(acc[g][i], __ldcg(from + (g * 16 + i) * 32));
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 v = __ldcg(from + (g * 16 + i) * 32);
+                                acc[g][2 * i] += v.x;
+                                acc[g][2 * i + 1] += v.y;
+                            }
                 }
             }
             if constexpr (P::WIDE) {
@@ -662,9 +654,9 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const float2 a = floats(acc[g][hh * 8 + 2 * j]), b = floats(acc[g][hh * 8 + 2 * j + 1]);
-                                u[j] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
-                                                  __float_as_uint(b.y));
+                                const float *a = acc[g] + 16 * hh + 4 * j;
+                                u[j] = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                                                  __float_as_uint(a[3]));
                             }
                             turn_out(u, 32 * g + 16 * hh);
                         }
@@ -674,8 +666,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             uint32_t h[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const float2 a = floats(acc[g][4 * j + i]);
-                                h[i] = bf16_pair(a.x, a.y);
+                                h[i] = bf16_pair(acc[g][8 * j + 2 * i], acc[g][8 * j + 2 * i + 1]);
                             }
                             u[j] = make_uint4(h[0], h[1], h[2], h[3]);
                         }
@@ -697,7 +688,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const int c = 32 * g + 2 * i;
-                                const float2 v = floats(acc[g][i]);
+                                const float2 v = make_float2(acc[g][2 * i], acc[g][2 * i + 1]);
                                 const float got = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.y, 1);
                                 const uint32_t both = bf16_pair(odd ? got : v.x, odd ? v.y : got);
                                 if (c + odd < cols_left) {
@@ -714,7 +705,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         if (g < groups)
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const float2 v = floats(acc[g][i]);
+                                const float2 v = make_float2(acc[g][2 * i], acc[g][2 * i + 1]);
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
                                     const int c = 32 * g + 2 * i + j;
@@ -757,7 +748,7 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
         cudaError_t e = cudaFuncGetAttributes(&at, kern);
         if (e != cudaSuccess) return cuda_fail(e);
         // the warps' own register counts have to be covered by the launch's
-        if (P::WIDE && at.numRegs * P::THREADS < 184 * 256 + 136 * 128) return TQ_ERR_DEVICE;
+        if (P::WIDE && at.numRegs * P::THREADS < 184 * 256 + 72 * 256) return TQ_ERR_DEVICE;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::smem(TQ_MAX_EXPERTS));
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dev.id] = true;
