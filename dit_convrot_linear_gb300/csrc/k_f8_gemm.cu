@@ -81,12 +81,13 @@ struct F8Plan {
     // the list of experts: first row, rows, tiles before
     static constexpr int smem(int64_t experts) { return OFF_LIST + static_cast<int>(experts + 1) * 12 + 16; }
     static constexpr int PART = DRAIN * 32 * COLS * 4;         // bytes of a CTA's partial tile
+    static constexpr int MIN_STEPS = 4, JOIN_STEPS = WIDE ? 8 : 12;   // of split tiles: steps a worker, steps saved
     static constexpr int DRAIN_REGS = 184, OTHER_REGS = 72;     // many tokens: registers a thread
 };
 static_assert(F8Plan<true>::smem(TQ_MAX_EXPERTS) <= 226 * 1024 && F8Plan<false>::smem(TQ_MAX_EXPERTS) <= 226 * 1024,
               "shared memory");
 
-constexpr int kF8MaxDrain = 8;
+constexpr int kF8MaxDrain = 8, kF8MaxParts = 4;
 
 struct F8Params {
     const float *sx;
@@ -101,7 +102,6 @@ struct F8Params {
     unsigned int *status;
     unsigned int *counters;              // [workers][CTAs][kF8MaxDrain]
     unsigned char *parts;                // [workers][2][CTAs][PART]
-    int min_steps;                       // K steps a worker takes of split tiles, at least
 };
 
 // A piece of work: the tile's place, K steps k0 .. k1 - 1, and for a piece of a
@@ -345,8 +345,12 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
     }
     const int *list = reinterpret_cast<const int *>(smem + P::OFF_LIST);
+    int *row0 = reinterpret_cast<int *>(smem + P::OFF_LIST), *rows = row0 + p.experts + 1, *tiles = rows + p.experts + 1;
+    if (p.offsets) {
+        for (int e = threadIdx.x; e <= p.experts; e += P::THREADS) row0[e] = p.offsets[e];
+        __syncthreads();
+    }
     if (warp == 0) {
-        int *row0 = reinterpret_cast<int *>(smem + P::OFF_LIST), *rows = row0 + p.experts + 1, *tiles = rows + p.experts + 1;
         int total = static_cast<int>((p.M + P::TOKENS - 1) / P::TOKENS);       // token tiles
         if (p.offsets == nullptr) {
             if (lane == 0) {
@@ -362,7 +366,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             for (int e0 = 0; e0 < p.experts; e0 += 32) {
                 const int e = e0 + lane;
                 const bool in = e < p.experts;
-                const int a = in ? p.offsets[e] : INT32_MIN, b = in ? p.offsets[e + 1] : INT32_MIN;
+                const int a = in ? row0[e] : INT32_MIN, b = in ? row0[e + 1] : INT32_MIN;
                 int top = a;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -381,7 +385,6 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (lane >= o) s += v;
                 }
                 if (in) {
-                    row0[e] = a;
                     rows[e] = n;
                     tiles[e] = sum + s - t;
                 }
@@ -393,12 +396,15 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             total = sum;
         }
         if (lane == 0) {
-            // the last round of tiles is split where it would leave a good part of the workers idle
+            // The tiles of a last round that leaves workers idle are split where that saves more
+            // steps than the joining costs, in at most kF8MaxParts parts each.
             const int n = total * p.ntiles, workers = gridDim.x / CTAS, rest = n % workers;
-            const bool split = rest > 0 && rest * 100 < workers * 85;
+            const int units = rest * p.ksteps;
+            const int use = max(1, min(min(workers, rest * kF8MaxParts), units / P::MIN_STEPS));
+            const bool split = rest > 0 && p.ksteps - (units + use - 1) / use >= P::JOIN_STEPS;
             cut.whole = split ? n - rest : n;
-            cut.units = split ? rest * p.ksteps : 0;
-            cut.use = max(1, min(workers, cut.units / p.min_steps));
+            cut.units = split ? units : 0;
+            cut.use = use;
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -674,13 +680,16 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     const float2 *from = part(pr);
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g)
-                        if (g < groups)
+                        if (g < groups) {
+                            float2 v[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] = __ldcg(from + (g * 8 + i) * 32);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float2 v = __ldcg(from + (g * 8 + i) * 32);
-                                acc[g][2 * i] += v.x;
-                                acc[g][2 * i + 1] += v.y;
+                                acc[g][2 * i] += v[i].x;
+                                acc[g][2 * i + 1] += v[i].y;
                             }
+                        }
                 }
             }
             if constexpr (P::WIDE) {
@@ -850,7 +859,6 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     if (!p.status) return TQ_ERR_DEVICE;
     p.counters = static_cast<unsigned int *>(f.ws);
     p.parts = static_cast<unsigned char *>(f.ws) + f8_counter_bytes(dev.sms);
-    p.min_steps = 2;
     CUtensorMap tmW, tmX;
     if (!make_map_u8(&tmW, f.Wq, p.experts * f.N, f.K, kStepK, WIDE ? P::B_BOX : kRowsA, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_u8(&tmX, f.Xq, f.M, f.K, kStepK, WIDE ? kRowsA : P::B_BOX, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -858,7 +866,8 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     // token tiles there may be: one more an expert than whole ones
     const int64_t token_tiles = f.M / P::TOKENS + (f.M < p.experts ? f.M : p.experts);
     if (token_tiles * p.ntiles > (1ll << 30)) return TQ_ERR_OVERFLOW;
-    const int64_t pieces = token_tiles * p.ntiles * p.ksteps / p.min_steps;
+    const int64_t tiles = token_tiles * p.ntiles, parts = p.ksteps / P::MIN_STEPS;
+    const int64_t pieces = tiles * (parts < 1 ? 1 : (parts < kF8MaxParts ? parts : kF8MaxParts));
     const int64_t most = dev.sms / P::CTAS, workers = pieces < 1 ? 1 : (pieces < most ? pieces : most);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
