@@ -83,6 +83,8 @@ struct QuantF8 {
 template <bool SWIGLU>
 __global__ void __launch_bounds__(32 * kF8Warps) k_quant_act_f8(const QuantF8 p) {
     const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
     const int64_t items = p.M * p.chunks, step = static_cast<int64_t>(gridDim.x) * kF8Warps;
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * kF8Warps + (threadIdx.x >> 5); it < items; it += step) {
         const int64_t m = it / p.chunks;
@@ -178,13 +180,8 @@ tq_status launch_quant_act_f8(const uint16_t *X, int64_t rows_x, int64_t K, int6
     QuantF8 p{X, U, ldx, ldu, M, K, rows_x, rows, Xq, sx, static_cast<int>((K + 511) / 512), status_word()};
     if (!p.status) return TQ_ERR_DEVICE;
     const int64_t ctas = (M * p.chunks + kF8Warps - 1) / kF8Warps, most = static_cast<int64_t>(dev.sms) * 8;
-    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
-    if (U)
-        k_quant_act_f8<true><<<grid, 32 * kF8Warps, 0, s>>>(p);
-    else
-        k_quant_act_f8<false><<<grid, 32 * kF8Warps, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+    return launch_pdl(U ? k_quant_act_f8<true> : k_quant_act_f8<false>, static_cast<unsigned>(ctas < most ? ctas : most),
+                      32 * kF8Warps, s, p);
 }
 
 }  // namespace tq

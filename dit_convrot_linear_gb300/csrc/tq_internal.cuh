@@ -31,6 +31,24 @@ tq_status cuda_fail(cudaError_t e);
 // Device address of the library's status word on the current device.
 unsigned int *status_word();
 
+// A launch that may start while the kernel before it ends: the kernel calls pdl_wait
+// before it touches what an earlier one reads or writes, and pdl_launch_dependents only
+// after that.
+template <typename... A>
+tq_status launch_pdl(void (*kernel)(A...), unsigned grid, unsigned block, cudaStream_t s, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
+}
+
 // Launchers (one per kernel family).  Arguments are validated by the caller.
 tq_status launch_quantize_weights(const uint16_t *W, int64_t N, int64_t K,
                                   int64_t ldw, int bits, void *codes,
