@@ -55,23 +55,25 @@ struct F8Plan {
     static constexpr bool WIDE = WIDE_;                        // many tokens: they are the M side, of a pair
     static constexpr int CTAS = WIDE ? 2 : 1;                  // of a tile
     static constexpr int TOKENS = WIDE ? 256 : 64;             // of a tile, at most
-    static constexpr int YCOLS = WIDE ? 256 : 128;             // weight rows of a tile
+    static constexpr int YCOLS = WIDE ? 256 : 128;             // weight rows of a tile, at most
     static constexpr int NCOLS = WIDE ? YCOLS : TOKENS;        // the N side
     static constexpr int COLS = WIDE ? 128 : 64;               // of them a drain warp
     static constexpr int SETS = WIDE ? 1 : 2;                  // of drain warps, that take the steps in turn
     static constexpr int DRAIN = 4 * NCOLS / COLS * SETS;      // drain warps
     static constexpr int HALVES = WIDE ? 2 : 1;                // accumulators a step
-    static constexpr int ISSUERS = 2 * HALVES;
+    static constexpr int ISSUERS = 2 * HALVES, IN_TURN = ISSUERS / HALVES;  // MMA warps; of them a half's, that take the steps in turn
     static constexpr int SCALERS = 2;                           // scale warps: the steps in turn
     static constexpr int OTHERS = 8;                           // warps that do not drain
     static constexpr int THREADS = (DRAIN + OTHERS) * 32;
     static constexpr int B_BOX = WIDE ? 64 : 32;               // rows of one tensor copy of the N side
     static constexpr int STAGE = kABytes + NCOLS / CTAS * kStepK;
-    static constexpr int STAGES = WIDE ? 6 : 7;
+    static constexpr int STAGES = 6;
     static constexpr int TURNS = WIDE ? 2 : 4;                 // steps with accumulators in TMEM
     static constexpr int ACCS = TURNS * HALVES, ACC_COLS = NCOLS / HALVES;
     static constexpr int TMEM = ACC_COLS * ACCS;
-    static constexpr int SCALES = WIDE ? 256 : TOKENS;         // of a step (many tokens: 128 for each half)
+    // of a step.  Many tokens: 128 products for each half; few: the tokens', and of the weights
+    // the tile's two blocks'
+    static constexpr int SCALES = WIDE ? 256 : TOKENS + 4;
     static constexpr int SLOTS = 2 * TURNS;                    // steps with scales in shared memory
     static constexpr int OFF_SCALES = STAGES * STAGE;
     // many tokens: 64 bytes of 32 rows a warp; few: the second set's sums
@@ -86,10 +88,18 @@ struct F8Plan {
     static constexpr int MIN_STEPS = 4, JOIN_STEPS = WIDE ? 16 : 12;   // of split tiles: steps a worker, steps saved
     static constexpr int DRAIN_REGS = 176, OTHER_REGS = 80;     // many tokens: registers a thread
 };
+// A wait for a parity tells two neighbouring rounds of a barrier apart, no more: who
+// waits for a stage's or an accumulator's round has to have seen the round before it.  So
+// those that take the steps in turn meet the same stages and accumulators every time.
+template <class P>
+constexpr bool f8_turns() {
+    return P::STAGES % P::IN_TURN == 0 && P::TURNS % P::IN_TURN == 0 && P::TURNS % P::SETS == 0 && P::TURNS % P::SCALERS == 0;
+}
+static_assert(f8_turns<F8Plan<true>>() && f8_turns<F8Plan<false>>(), "rounds");
 static_assert(F8Plan<true>::smem(TQ_MAX_EXPERTS) <= 226 * 1024 && F8Plan<false>::smem(TQ_MAX_EXPERTS) <= 226 * 1024,
               "shared memory");
 
-constexpr int kF8MaxDrain = 8, kF8MaxParts = 4;
+constexpr int kF8MaxDrain = 8, kF8MaxParts = 4, kF8MinRows = 32;
 
 struct F8Params {
     const float *sx;
@@ -98,6 +108,7 @@ struct F8Params {
     int experts;
     const float *sw;
     int N, ksteps, nblocks, ntiles;      // nblocks: scale blocks of N; ntiles: tiles of N
+    int ycols;                           // weight rows of a tile (few tokens: at most 128, even)
     void *Y;
     int64_t ldy;
     int ytype, vec;                      // vec: rows of Y allow 16-byte stores (few tokens: 4-byte ones)
@@ -256,6 +267,20 @@ __device__ __forceinline__ bool f8_wait_warp(uint32_t bar, uint32_t parity, vola
     return __all_sync(0xffffffffu, ok);
 }
 
+// A place in a ring of N stages and the parity of the round that fills it.
+template <int N>
+struct F8Ring {
+    int s = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void on(int n) {
+        s += n;
+        if (s >= N) {
+            s -= N;
+            round ^= 1u;
+        }
+    }
+};
+
 // K-major operand of 128-byte rows in the 128-byte swizzle: groups of eight rows
 // 1024 bytes apart; 32 values on along K are 32 bytes on.
 __device__ __forceinline__ uint64_t f8_desc(uint32_t addr) {
@@ -394,40 +419,49 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     // columns of accumulator h of a tile: tokens, or weight rows, rounded up to 16 (one
     // without any still takes part, and nothing of it is stored)
     auto mma_n = [&](const F8Seg &sg, int h) {
-        const int n = P::WIDE ? min(P::ACC_COLS, p.N - sg.ntile * P::YCOLS - h * P::ACC_COLS) : sg.cols;
+        const int n = P::WIDE ? min(P::ACC_COLS, p.N - sg.ntile * p.ycols - h * P::ACC_COLS) : sg.cols;
         return (max(n, 1) + 15) / 16 * 16;
     };
-    // The copy warp's part of a step's copies, for the stage s: the bytes that are expected
-    // there (a pair's, in the even CTA), the weights, the tokens.  Rows of a pair's tokens that
-    // are past the tile's are not loaded (what comes of them is not stored).  The N side comes
-    // in boxes: many tokens, one for each half that has columns, this CTA's share of them; few,
-    // as many as hold the tile's tokens.
-    auto boxes = [&](const F8Seg &sg) {
-        return P::WIDE ? (p.N - sg.ntile * P::YCOLS > P::ACC_COLS ? 2 : 1) : (sg.cols + P::B_BOX - 1) / P::B_BOX;
+    // The copy warp's work on a tile: where its operands lie, and a step's copies into the
+    // stage s, the weights (with the bytes that are expected there; a pair's, in the even CTA)
+    // and the tokens.  Rows of a pair's tokens that are past the tile's are not loaded (what
+    // comes of them is not stored).  The N side comes in boxes: many tokens, one for each half
+    // that has columns, this CTA's share of them; few, as many as hold the tile's tokens.
+    struct Source {
+        int wrow[2], xrow, boxes;
+        uint32_t bytes;
+        bool mine;
     };
-    auto full_of = [&](int s) { return CTAS == 2 ? in_even_cta(full0 + 8 * s) : full0 + 8 * s; };
-    auto copy_weights = [&](const F8Seg &sg, int s, int ks) {
-        const uint32_t at = smem_u32(smem + s * P::STAGE);
+    auto source = [&](const F8Seg &sg) {
+        Source c;
+        c.boxes = P::WIDE ? (p.N - sg.ntile * p.ycols > P::ACC_COLS ? 2 : 1) : (sg.cols + P::B_BOX - 1) / P::B_BOX;
+        c.bytes = CTAS * c.boxes * P::B_BOX * kStepK + (P::WIDE ? (sg.cols > kRowsA ? 2 : 1) * kABytes : p.ycols * kStepK);
+        c.wrow[0] = c.wrow[1] = sg.e * p.N + sg.ntile * p.ycols;
+        if (P::WIDE)
+            for (int h = 0; h < 2; ++h) c.wrow[h] += h * P::ACC_COLS + rank * (mma_n(sg, h) / 2);
+        c.xrow = sg.m0 + (P::WIDE ? rank * kRowsA : 0);
+        c.mine = !P::WIDE || rank * kRowsA < sg.cols;
+        return c;
+    };
+    const uint32_t full_even = CTAS == 2 ? in_even_cta(full0) : full0, stage0 = smem_u32(smem);
+    auto copy_weights = [&](const Source &c, int s, int k) {
+        const uint32_t at = stage0 + s * P::STAGE, bar = full_even + 8 * s;
         if (rank == 0)
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full0 + 8 * s),
-                         "r"(CTAS * boxes(sg) * P::B_BOX * kStepK + (P::WIDE && sg.cols > kRowsA ? 2 : 1) * kABytes)
-                         : "memory");
-        const int wrow = sg.e * p.N + sg.ntile * P::YCOLS;
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full0 + 8 * s), "r"(c.bytes) : "memory");
         if constexpr (P::WIDE) {
-            for (int b = 0; b < boxes(sg); ++b)
-                f8_copy<CTAS>(at + kABytes + b * P::B_BOX * kStepK, &tmB, ks * kStepK,
-                              wrow + b * P::ACC_COLS + rank * (mma_n(sg, b) / 2), full_of(s));
+            f8_copy<CTAS>(at + kABytes, &tmB, k, c.wrow[0], bar);
+            if (c.boxes > 1) f8_copy<CTAS>(at + kABytes + P::B_BOX * kStepK, &tmB, k, c.wrow[1], bar);
         } else {
-            f8_copy<CTAS>(at, &tmA, ks * kStepK, wrow, full_of(s));
+            f8_copy<CTAS>(at, &tmA, k, c.wrow[0], bar);
         }
     };
-    auto copy_tokens = [&](const F8Seg &sg, int s, int ks) {
-        const uint32_t at = smem_u32(smem + s * P::STAGE);
+    auto copy_tokens = [&](const Source &c, int s, int k) {
+        const uint32_t at = stage0 + s * P::STAGE, bar = full_even + 8 * s;
         if constexpr (P::WIDE) {
-            if (rank * kRowsA < sg.cols) f8_copy<CTAS>(at, &tmA, ks * kStepK, sg.m0 + rank * kRowsA, full_of(s));
+            if (c.mine) f8_copy<CTAS>(at, &tmA, k, c.xrow, bar);
         } else {
-            for (int b = 0; b < boxes(sg); ++b)
-                f8_copy<CTAS>(at + kABytes + b * P::B_BOX * kStepK, &tmB, ks * kStepK, sg.m0 + b * P::B_BOX, full_of(s));
+            f8_copy<CTAS>(at + kABytes, &tmB, k, c.xrow, bar);
+            if (c.boxes > 1) f8_copy<CTAS>(at + kABytes + P::B_BOX * kStepK, &tmB, k, c.xrow + P::B_BOX, bar);
         }
     };
     uint32_t early = 0;                  // steps whose weights were asked for before the wait
@@ -435,9 +469,11 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (warp == DRAIN + P::ISSUERS && lane == 0) {
             F8Iter<CTAS> iter(cut);
             F8Seg sg;
-            if (iter.next(cut, list, p, sg))
-                for (early = 0; early < STAGES && sg.k0 + static_cast<int>(early) < sg.k1; ++early)
-                    copy_weights(sg, early, sg.k0 + early);
+            if (iter.next(cut, list, p, sg)) {
+                const Source c = source(sg);
+                for (; early < STAGES && sg.k0 + static_cast<int>(early) < sg.k1; ++early)
+                    copy_weights(c, early, (sg.k0 + early) * kStepK);
+            }
         }
         __syncwarp();
         pdl_wait();
@@ -467,25 +503,29 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (rank == 0 && lane == 0) {
                 const int h = (warp - DRAIN) % HALVES;
                 const uint32_t turn = (warp - DRAIN) / HALVES;
-                uint32_t it = 0;
+                uint32_t it = 0, mine = turn;            // mine: the next step of this thread's
+                F8Ring<STAGES> at;
+                at.on(turn);
                 F8Iter<CTAS> iter(cut);
                 F8Seg sg;
                 while (!abort_sh && iter.next(cut, list, p, sg)) {
                     // D fp32, A and B e4m3, K-major, M = 128 a CTA
                     const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(mma_n(sg, h) >> 3) << 17) | (CTAS * 8u << 24);
-                    for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
-                        if ((it & 1) != turn) continue;
-                        const int s = it % STAGES, a = (it % TURNS) * HALVES + h;
-                        if (!f8_wait(full0 + 8 * s, (it / STAGES) & 1, &abort_sh, p.status)) break;
-                        if (!f8_wait(acc_empty0 + 8 * a, ((it / TURNS) & 1) ^ 1, &abort_sh, p.status)) break;
+                    const uint32_t end = it + sg.k1 - sg.k0;
+                    for (; mine < end; mine += P::IN_TURN, at.on(P::IN_TURN)) {
+                        const int a = (mine % TURNS) * HALVES + h;
+                        if (!f8_wait(full0 + 8 * at.s, at.round, &abort_sh, p.status)) break;
+                        if (!f8_wait(acc_empty0 + 8 * a, ((mine / TURNS) & 1) ^ 1, &abort_sh, p.status)) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        const uint32_t at = smem_u32(smem + s * P::STAGE), d = tmem + static_cast<uint32_t>(P::ACC_COLS * a);
-                        const uint64_t ad = f8_desc(at), bd = f8_desc(at + kABytes + h * (P::ACC_COLS / CTAS) * kStepK);
+                        const uint32_t d = tmem + static_cast<uint32_t>(P::ACC_COLS * a);
+                        const uint64_t ad = f8_desc(stage0 + at.s * P::STAGE);
+                        const uint64_t bd = f8_desc(stage0 + at.s * P::STAGE + kABytes + h * (P::ACC_COLS / CTAS) * kStepK);
 #pragma unroll
                         for (int kk = 0; kk < kStepK / 32; ++kk) f8_mma<CTAS>(d, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
                         f8_commit<CTAS>(acc_full0 + 8 * a);
-                        f8_commit<CTAS>(empty0 + 8 * s);
+                        f8_commit<CTAS>(empty0 + 8 * at.s);
                     }
+                    it = end;
                 }
                 // let every issued MMA finish before the TMEM is released
                 if constexpr (CTAS == 2)
@@ -501,15 +541,17 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             // -------------------------------------------- tensor copies
             if (lane == 0) {
                 uint32_t it = 0;
+                F8Ring<STAGES> at;
                 F8Iter<CTAS> iter(cut);
                 F8Seg sg;
-                while (!abort_sh && iter.next(cut, list, p, sg))
-                    for (int ks = sg.k0; ks < sg.k1; ++ks, ++it) {
-                        const int s = it % STAGES;
-                        if (!f8_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, &abort_sh, p.status)) break;
-                        if (it >= early) copy_weights(sg, s, ks);
-                        copy_tokens(sg, s, ks);
+                while (!abort_sh && iter.next(cut, list, p, sg)) {
+                    const Source c = source(sg);
+                    for (int k = sg.k0 * kStepK; k < sg.k1 * kStepK; k += kStepK, ++it, at.on(1)) {
+                        if (!f8_wait(empty0 + 8 * at.s, at.round ^ 1u, &abort_sh, p.status)) break;
+                        if (it >= early) copy_weights(c, at.s, k);
+                        copy_tokens(c, at.s, k);
                     }
+                }
                 // after a wait ran out: the copies in flight land before the CTA leaves
                 if (abort_sh && rank == 0)
                     for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j) {
@@ -522,8 +564,8 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         } else if (warp < DRAIN + P::ISSUERS + 1 + P::SCALERS) {
             // -------------------------------------------- scales
             // Each step's sx * sw into its slot, loaded AHEAD steps before.  Many tokens: this CTA's
-            // tokens with the first scale block of columns, then with the second.  Few: each token
-            // with the tile's block.  (Places past the tile's rows or N take their last one's; what
+            // tokens with the first scale block of columns, then with the second.  Few: sx of each
+            // token, and sw of the tile's first block of weight rows and the next.  (Places past the tile's rows or N take their last one's; what
             // comes of them is not stored.)  A slot is free again 2 * TURNS steps later: step
             // it - TURNS has its sums only after step it - 2 * TURNS was drained.
             constexpr int SC = P::SCALERS, AHEAD = 2, EACH = P::WIDE ? 4 : P::TOKENS / 32;
@@ -536,18 +578,18 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 int off[EACH];
 #pragma unroll
                 for (int i = 0; i < EACH; ++i) off[i] = min(rank * kRowsA + lane + 32 * i, sg.cols - 1);
-                const int nb = sg.ntile * (P::YCOLS / 128);
+                const int nb = sg.ntile * p.ycols / 128;
                 const float *sx = p.sx + (sg.k0 + skip) * p.M + sg.m0;
                 const float *sw = p.sw + (static_cast<int64_t>(sg.e) * p.nblocks + nb) * p.ksteps + sg.k0 + skip;
                 const int second = nb + 1 < p.nblocks ? p.ksteps : 0;    // the second block's scales, from the first's
-                float x[AHEAD][EACH], w[AHEAD][HALVES];
+                float x[AHEAD][EACH], w[AHEAD][2];
                 int left = sg.k1 - sg.k0 - skip;                         // steps to the piece's end, from the next load
-                auto load = [&](float (&xs)[EACH], float (&ws)[HALVES]) {
+                auto load = [&](float (&xs)[EACH], float (&ws)[2]) {
                     if (left > 0) {
 #pragma unroll
                         for (int i = 0; i < EACH; ++i) xs[i] = __ldg(sx + off[i]);
 #pragma unroll
-                        for (int j = 0; j < HALVES; ++j) ws[j] = __ldg(sw + j * second);
+                        for (int j = 0; j < 2; ++j) ws[j] = __ldg(sw + j * second);
                     }
                     sx += SC * p.M;
                     sw += SC;
@@ -569,10 +611,16 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                                 ok = ok && f8_wait_warp(acc_full0 + 8 * (s * HALVES + h), (j / TURNS - 1) & 1, &abort_sh, p.status);
                         if (!ok) break;
                         float *to = reinterpret_cast<float *>(smem + P::OFF_SCALES) + j % P::SLOTS * P::SCALES + lane;
+                        if constexpr (P::WIDE) {
 #pragma unroll
-                        for (int h = 0; h < HALVES; ++h)
+                            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                            for (int i = 0; i < EACH; ++i) to[32 * (h * EACH + i)] = x[d][i] * w[d][h];
+                                for (int i = 0; i < EACH; ++i) to[32 * (h * EACH + i)] = x[d][i] * w[d][h];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < EACH; ++i) to[32 * i] = x[d][i];
+                            if (lane < 2) to[P::TOKENS] = lane == 0 ? w[d][0] : w[d][1];
+                        }
                         __syncwarp();
                         if (lane < HALVES) mbar_arrive_local(acc_full0 + 8 * (s * HALVES + lane));
                         load(x[d], w[d]);
@@ -609,9 +657,10 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         F8Seg sg;
         // the warp acts as one: a lane that saw an abort takes the others along
         while (__all_sync(0xffffffffu, !abort_sh) && iter.next(cut, list, p, sg)) {
-            const int n0 = sg.ntile * P::YCOLS, row = rank * kRowsA + q * 32;    // row: of this warp, on the M side
+            const int n0 = sg.ntile * p.ycols, row = rank * kRowsA + q * 32;    // row: of this warp, on the M side
             static_assert(!P::WIDE || P::SCALES == P::NCOLS, "a scale a token and half");
-            const int rows_left = (P::WIDE ? sg.cols : p.N - n0) - row;
+            const int rows_left = (P::WIDE ? sg.cols : min(p.ycols, p.N - n0)) - row;
+            const int block = P::TOKENS + (n0 + row + lane) / 128 - n0 / 128;   // few tokens: where this lane's sw is
             const int cols_left = (P::WIDE ? p.N - n0 : sg.cols) - c0;
             const bool some = rows_left > 0 && cols_left > 0;            // this warp has some of the tile
             const int groups = some ? min(GROUPS, (cols_left + 15) / 16) : 0;
@@ -646,6 +695,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             acc[g + i / 16][i % 16] = fmaf(__uint_as_float(v[i]), f1, acc[g + i / 16][i % 16]);
                     }
                 } else {
+                    const float w = f[block];
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g)
                         if (g < groups) {
@@ -655,6 +705,13 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             uint32_t v[16];
                             tmem_read16(at + 16 * g, v);
                             if (g == groups - 1) hand_back(a);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                x[i].x *= w;
+                                x[i].y *= w;
+                                x[i].z *= w;
+                                x[i].w *= w;
+                            }
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 acc[g][4 * i] = fmaf(__uint_as_float(v[4 * i]), x[i].x, acc[g][4 * i]);
@@ -805,7 +862,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
             } else {
                 // ---- Y: this lane's column n of tokens c0, c0 + 1, ...
-                const int n = n0 + row + lane;
+                const int n = n0 + row + lane, n_end = min(p.N, n0 + p.ycols);
                 const int64_t first = (static_cast<int64_t>(sg.m0) + c0) * p.ldy;
                 if (p.ytype == 1 && p.vec) {
                     // two lanes exchange a value: the even one takes both columns of one token, the
@@ -823,9 +880,9 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                                 const uint32_t both = bf16_pair(odd ? got : v.x, odd ? v.y : got);
                                 if (c + odd < cols_left) {
                                     uint16_t *to = y + c * p.ldy;
-                                    if (ne + 1 < p.N)
+                                    if (ne + 1 < n_end)
                                         *reinterpret_cast<uint32_t *>(to) = both;
-                                    else if (ne < p.N)
+                                    else if (ne < n_end)
                                         *to = static_cast<uint16_t>(both);
                                 }
                             }
@@ -840,7 +897,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                                 for (int j = 0; j < 2; ++j) {
                                     const int c = 16 * g + 2 * i + j;
                                     const float u = j ? v.y : v.x;
-                                    if (n >= p.N || c >= cols_left) continue;
+                                    if (n >= n_end || c >= cols_left) continue;
                                     if (p.ytype == 0)
                                         static_cast<float *>(p.Y)[first + c * p.ldy + n] = u;
                                     else
@@ -898,7 +955,17 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     p.N = static_cast<int>(f.N);
     p.ksteps = static_cast<int>((f.K + kStepK - 1) / kStepK);
     p.nblocks = static_cast<int>((f.N + 127) / 128);
-    p.ntiles = static_cast<int>((f.N + P::YCOLS - 1) / P::YCOLS);
+    // Few tokens of one matrix: as many tiles as CTAs, where tiles of 128 rows would leave some
+    // idle in the last round (an SM draws at most some 42 GB/s from the DRAM: 48 tokens of 12288
+    // x 4096 18 us with 96 tiles, 14 with 150)
+    p.ycols = P::YCOLS;
+    if (!WIDE && !f.offsets) {
+        const int64_t by_tokens = (f.M + P::TOKENS - 1) / P::TOKENS, tiles = by_tokens * ((f.N + 127) / 128);
+        const int64_t most = (tiles + dev.sms - 1) / dev.sms * dev.sms / by_tokens;
+        const int64_t rows = (f.N + most - 1) / most;
+        p.ycols = static_cast<int>(rows < kF8MinRows ? kF8MinRows : (rows + 1) / 2 * 2);
+    }
+    p.ntiles = static_cast<int>((f.N + p.ycols - 1) / p.ycols);
     p.Y = f.Y;
     p.ldy = f.ldy;
     p.ytype = f.ytype;
@@ -909,7 +976,7 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     p.counters = static_cast<unsigned int *>(f.ws);
     p.parts = static_cast<unsigned char *>(f.ws) + f8_counter_bytes(dev.sms);
     CUtensorMap tmW, tmX;
-    if (!make_map_u8(&tmW, f.Wq, p.experts * f.N, f.K, kStepK, WIDE ? P::B_BOX : kRowsA, CU_TENSOR_MAP_SWIZZLE_128B) ||
+    if (!make_map_u8(&tmW, f.Wq, p.experts * f.N, f.K, kStepK, WIDE ? P::B_BOX : p.ycols, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_u8(&tmX, f.Xq, f.M, f.K, kStepK, WIDE ? kRowsA : P::B_BOX, CU_TENSOR_MAP_SWIZZLE_128B))
         return TQ_ERR_DEVICE;
     // token tiles there may be: one more an expert than whole ones

@@ -350,3 +350,27 @@ def test_product_in_a_graph_and_on_two_streams(tq, M):
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 4])
     assert tq.device_status() == 0
+
+
+@pytest.mark.parametrize("counts,N,K", [([16] * 64, 2048, 2048), ([33, 2, 40, 1] * 16, 2048, 1024),
+                                        ([31, 33] * 4, 4096, 2048), ([300, 500, 7] * 8, 1024, 2048)])
+def test_experts_many_tiles_again_and_again(tq, counts, N, K):
+    """Several tiles a CTA, twenty times: the rounds of the stages and accumulators stay
+    in step, and nothing depends on timing."""
+    import torch
+    g = gen(len(counts) + K)
+    M = sum(counts)
+    off = offsets_of(counts)
+    q, sx = tq.quant_act_f8(rows(g, M, K))
+    Wq, sw = matrix(g, len(counts), N, K)
+    ws = tq.f8_workspace()
+    first = tq.linear_f8_experts(q, sx, off, Wq, sw, ws, out="f32")
+    a = 0
+    for e, n in enumerate(counts):
+        if e % 5 == 0:
+            want, S = ref.product(q[a:a + n], sx[:, a:a + n], Wq[e], sw[e])
+            check(first[a:a + n], want, S, K)
+        a += n
+    got = [tq.linear_f8_experts(q, sx, off, Wq, sw, ws, out="f32") for _ in range(20)]
+    assert all(torch.equal(y, first) for y in got)
+    assert tq.device_status() == 0
