@@ -955,15 +955,26 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     p.N = static_cast<int>(f.N);
     p.ksteps = static_cast<int>((f.K + kStepK - 1) / kStepK);
     p.nblocks = static_cast<int>((f.N + 127) / 128);
-    // Few tokens of one matrix: as many tiles as CTAs, where tiles of 128 rows would leave some
-    // idle in the last round (an SM draws at most some 42 GB/s from the DRAM: 48 tokens of 12288
-    // x 4096 18 us with 96 tiles, 14 with 150)
     p.ycols = P::YCOLS;
     if (!WIDE && !f.offsets) {
-        const int64_t by_tokens = (f.M + P::TOKENS - 1) / P::TOKENS, tiles = by_tokens * ((f.N + 127) / 128);
-        const int64_t most = (tiles + dev.sms - 1) / dev.sms * dev.sms / by_tokens;
-        const int64_t rows = (f.N + most - 1) / most;
-        p.ycols = static_cast<int>(rows < kF8MinRows ? kF8MinRows : (rows + 1) / 2 * 2);
+        // Few tokens of one matrix: tiles of 128 rows, the steps of the last round split, or tiles
+        // of fewer rows, as many as CTAs.  A step of r rows takes about 3 r ns (what an SM draws
+        // from the DRAM) and 250 at least; joining takes 5 us, a round of smaller tiles 1.5 more
+        // to begin.  48 tokens of 12288 x 4096: 96 tiles 18 us, 150 of 82 rows 17; 64 of 4096 x
+        // 12288: 128 tiles of 32 rows 42, 32 in four parts 22.
+        const int64_t by_tokens = (f.M + P::TOKENS - 1) / P::TOKENS, sms = dev.sms;
+        auto whole = [&](int64_t rows) {
+            const int64_t tiles = by_tokens * ((f.N + rows - 1) / rows);
+            return (tiles + sms - 1) / sms * p.ksteps * (3 * rows > 250 ? 3 * rows : 250);
+        };
+        const int64_t tiles = by_tokens * ((f.N + 127) / 128);
+        const int64_t parts = tiles < sms ? (sms / tiles < kF8MaxParts ? sms / tiles : kF8MaxParts) : 1;
+        int64_t large = whole(128);
+        if (parts > 1 && p.ksteps - p.ksteps / parts >= P::JOIN_STEPS && large / parts + 5000 < large)
+            large = large / parts + 5000;
+        const int64_t most = (tiles + sms - 1) / sms * sms / by_tokens, even = ((f.N + most - 1) / most + 1) / 2 * 2;
+        const int64_t rows = even < kF8MinRows ? kF8MinRows : even;
+        if (rows < 128 && whole(rows) + 1500 < large) p.ycols = static_cast<int>(rows);
     }
     p.ntiles = static_cast<int>((f.N + p.ycols - 1) / p.ycols);
     p.Y = f.Y;
