@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(256) k_expert_topk(const L *__restrict__ X, in
                                                      float *__restrict__ weights) {
     const int lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+    pdl_wait();
+    pdl_launch_dependents();
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += step) {
         uint32_t key[NI];
         int ex[NI];
@@ -149,6 +151,8 @@ __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ 
                                                           L *__restrict__ dX, int64_t ldd, unsigned int *status) {
     const int lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+    pdl_wait();
+    pdl_launch_dependents();
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += step) {
         int id = -1;
         float d = 0.0f, v = 0.0f;
@@ -244,6 +248,8 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
     __shared__ int part[kSortWarps + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ctas = gridDim.x, cta = blockIdx.x;
     for (int i = threadIdx.x; i < kSortWarps * E; i += blockDim.x) cnt[i] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
     const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
     const int64_t per = ((n + warps - 1) / warps + 31) / 32 * 32;
     const int64_t f0 = (static_cast<int64_t>(cta) * kSortWarps + warp) * per, f1 = f0 + per < n ? f0 + per : n;
@@ -391,6 +397,8 @@ __global__ void __launch_bounds__(256) k_expert_gather(const uint4 *__restrict__
                                                        int64_t ldx, const int32_t *__restrict__ rows, int64_t M,
                                                        uint4 *__restrict__ Y, int64_t ldy, unsigned int *status) {
     const int64_t n = M * pieces, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    pdl_wait();
+    pdl_launch_dependents();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
         const int64_t m = i / pieces;
         const int c = static_cast<int>(i - m * pieces);
@@ -414,6 +422,8 @@ __global__ void __launch_bounds__(256) k_expert_combine(const uint4 *__restrict_
                                                         uint4 *__restrict__ O, int64_t ldo, unsigned int *status) {
     using P = Piece<V>;
     const int64_t n = T * pieces, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    pdl_wait();
+    pdl_launch_dependents();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
         const int64_t t = i / pieces;
         const int c = static_cast<int>(i - t * pieces);
@@ -453,6 +463,8 @@ __global__ void __launch_bounds__(kGradThreads) k_expert_combine_grad(
     int64_t lddy, float *__restrict__ dw, unsigned int *status) {
     using P = Piece<V>;
     __shared__ float part[kGradRows][kGradThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
     for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
         for (int j0 = 0; j0 < k; j0 += kGradRows) {
             int32_t at[kGradRows];
@@ -513,20 +525,15 @@ unsigned grid_of(int64_t ctas, const DeviceInfo &dev, int each) {
     return static_cast<unsigned>(ctas < most ? ctas : most);
 }
 
-tq_status launched() {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TQ_OK : cuda_fail(e);
-}
-
 // F<NI> for the 32-expert pieces of E
 template <template <int> class F, typename... A>
-void by_experts(int64_t E, A... a) {
-    if (E <= 32) F<1>::run(a...);
-    else if (E <= 64) F<2>::run(a...);
-    else if (E <= 128) F<4>::run(a...);
-    else if (E <= 256) F<8>::run(a...);
-    else if (E <= 512) F<16>::run(a...);
-    else F<32>::run(a...);
+tq_status by_experts(int64_t E, A... a) {
+    if (E <= 32) return F<1>::run(a...);
+    if (E <= 64) return F<2>::run(a...);
+    if (E <= 128) return F<4>::run(a...);
+    if (E <= 256) return F<8>::run(a...);
+    if (E <= 512) return F<16>::run(a...);
+    return F<32>::run(a...);
 }
 
 }  // namespace
@@ -534,34 +541,32 @@ void by_experts(int64_t E, A... a) {
 namespace {
 template <int NI>
 struct Topk {
-    static void run(const void *x, int type, int64_t T, int E, int64_t ld, int k, int renorm, int32_t *ids, float *w,
-                    unsigned grid, cudaStream_t s) {
+    static tq_status run(const void *x, int type, int64_t T, int E, int64_t ld, int k, int renorm, int32_t *ids, float *w,
+                         unsigned grid, cudaStream_t s) {
         if (type == 0)
-            k_expert_topk<float, NI><<<grid, 256, 0, s>>>(static_cast<const float *>(x), T, E, ld, k, renorm, ids, w);
-        else
-            k_expert_topk<uint16_t, NI><<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(x), T, E, ld, k, renorm,
-                                                             ids, w);
+            return launch_pdl(k_expert_topk<float, NI>, grid, 256, s, static_cast<const float *>(x), T, E, ld, k, renorm,
+                              ids, w);
+        return launch_pdl(k_expert_topk<uint16_t, NI>, grid, 256, s, static_cast<const uint16_t *>(x), T, E, ld, k,
+                          renorm, ids, w);
     }
 };
 template <int NI>
 struct TopkGrad {
-    static void run(const void *x, int type, int64_t T, int E, int64_t ld, const int32_t *ids, const float *dw, int k,
-                    int renorm, void *dx, int64_t ldd, unsigned int *status, unsigned grid, cudaStream_t s) {
+    static tq_status run(const void *x, int type, int64_t T, int E, int64_t ld, const int32_t *ids, const float *dw,
+                         int k, int renorm, void *dx, int64_t ldd, unsigned int *status, unsigned grid, cudaStream_t s) {
         if (type == 0)
-            k_expert_topk_grad<float, NI><<<grid, 256, 0, s>>>(static_cast<const float *>(x), T, E, ld, ids, dw, k,
-                                                               renorm, static_cast<float *>(dx), ldd, status);
-        else
-            k_expert_topk_grad<uint16_t, NI><<<grid, 256, 0, s>>>(static_cast<const uint16_t *>(x), T, E, ld, ids, dw,
-                                                                  k, renorm, static_cast<uint16_t *>(dx), ldd, status);
+            return launch_pdl(k_expert_topk_grad<float, NI>, grid, 256, s, static_cast<const float *>(x), T, E, ld, ids,
+                              dw, k, renorm, static_cast<float *>(dx), ldd, status);
+        return launch_pdl(k_expert_topk_grad<uint16_t, NI>, grid, 256, s, static_cast<const uint16_t *>(x), T, E, ld,
+                          ids, dw, k, renorm, static_cast<uint16_t *>(dx), ldd, status);
     }
 };
 }  // namespace
 
 tq_status launch_expert_topk(const void *logits, int type, int64_t T, int64_t E, int64_t ld, int k, int renorm,
                              int32_t *ids, float *weights, const DeviceInfo &dev, cudaStream_t s) {
-    by_experts<Topk>(E, logits, type, T, static_cast<int>(E), ld, k, renorm, ids, weights,
-                     grid_of((T + 7) / 8, dev, 64), s);
-    return launched();
+    return by_experts<Topk>(E, logits, type, T, static_cast<int>(E), ld, k, renorm, ids, weights,
+                            grid_of((T + 7) / 8, dev, 64), s);
 }
 
 tq_status launch_expert_topk_grad(const void *logits, int type, int64_t T, int64_t E, int64_t ld, const int32_t *ids,
@@ -569,9 +574,8 @@ tq_status launch_expert_topk_grad(const void *logits, int type, int64_t T, int64
                                   const DeviceInfo &dev, cudaStream_t s) {
     unsigned int *status = status_word();
     if (!status) return TQ_ERR_DEVICE;
-    by_experts<TopkGrad>(E, logits, type, T, static_cast<int>(E), ld, ids, dw, k, renorm, dlogits, ldd, status,
-                         grid_of((T + 7) / 8, dev, 64), s);
-    return launched();
+    return by_experts<TopkGrad>(E, logits, type, T, static_cast<int>(E), ld, ids, dw, k, renorm, dlogits, ldd, status,
+                                grid_of((T + 7) / 8, dev, 64), s);
 }
 
 tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, int32_t *offsets, int32_t *token,
@@ -588,7 +592,9 @@ tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, in
         if (e != cudaSuccess) return cuda_fail(e);
         configured[dev.id] = true;
     }
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     const unsigned ctas = T * k <= kSortOneCta ? 1u : static_cast<unsigned>(kSortCtas);
     attr[0].val.clusterDim = {ctas, 1u, 1u};
@@ -598,7 +604,7 @@ tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, in
     cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, k_expert_sort, ids, T * k, k, static_cast<int>(E), offsets, token,
                                              place, status);
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
@@ -610,10 +616,8 @@ tq_status launch_expert_gather(const void *X, int type, int64_t rows_x, int64_t 
     if (!status) return TQ_ERR_DEVICE;
     const int each = type == 0 ? 4 : 8;          // values of 16 bytes
     const int64_t n = M * (W / each);
-    k_expert_gather<<<grid_of((n + 255) / 256, dev, 8), 256, 0, s>>>(
-        static_cast<const uint4 *>(X), rows_x, static_cast<int>(W / each), ldx / each, rows, M,
-        static_cast<uint4 *>(Y), ldy / each, status);
-    return launched();
+    return launch_pdl(k_expert_gather, grid_of((n + 255) / 256, dev, 8), 256, s, static_cast<const uint4 *>(X), rows_x,
+                      static_cast<int>(W / each), ldx / each, rows, M, static_cast<uint4 *>(Y), ldy / each, status);
 }
 
 tq_status launch_expert_combine(const void *Y, int type, int64_t rows, int64_t W, int64_t ldy, const int32_t *place,
@@ -625,13 +629,8 @@ tq_status launch_expert_combine(const void *Y, int type, int64_t rows, int64_t W
     const unsigned grid = grid_of((T * pieces + 255) / 256, dev, 8);
     auto y = static_cast<const uint4 *>(Y);
     auto o = static_cast<uint4 *>(O);
-    if (type == 0)
-        k_expert_combine<float><<<grid, 256, 0, s>>>(y, rows, pieces, ldy / each, place, weights, T, k, o, ldo / each,
-                                                     status);
-    else
-        k_expert_combine<uint16_t><<<grid, 256, 0, s>>>(y, rows, pieces, ldy / each, place, weights, T, k, o,
-                                                        ldo / each, status);
-    return launched();
+    return launch_pdl(type == 0 ? k_expert_combine<float> : k_expert_combine<uint16_t>, grid, 256, s, y, rows, pieces,
+                      ldy / each, place, weights, T, k, o, ldo / each, status);
 }
 
 tq_status launch_expert_combine_grad(const void *dO, int64_t ldo, const void *Y, int type, int64_t rows, int64_t W,
@@ -644,14 +643,8 @@ tq_status launch_expert_combine_grad(const void *dO, int64_t ldo, const void *Y,
     auto d = static_cast<const uint4 *>(dO);
     auto y = static_cast<const uint4 *>(Y);
     auto o = static_cast<uint4 *>(dY);
-    if (type == 0)
-        k_expert_combine_grad<float><<<grid, kGradThreads, 0, s>>>(d, ldo / each, y, rows, pieces, ldy / each, place,
-                                                                   weights, T, k, o, lddy / each, dw, status);
-    else
-        k_expert_combine_grad<uint16_t><<<grid, kGradThreads, 0, s>>>(d, ldo / each, y, rows, pieces, ldy / each,
-                                                                      place, weights, T, k, o, lddy / each, dw,
-                                                                      status);
-    return launched();
+    return launch_pdl(type == 0 ? k_expert_combine_grad<float> : k_expert_combine_grad<uint16_t>, grid, kGradThreads, s,
+                      d, ldo / each, y, rows, pieces, ldy / each, place, weights, T, k, o, lddy / each, dw, status);
 }
 
 }  // namespace tq

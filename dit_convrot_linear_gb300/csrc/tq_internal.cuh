@@ -34,8 +34,8 @@ unsigned int *status_word();
 // A launch that may start while the kernel before it ends: the kernel calls pdl_wait
 // before it touches what an earlier one reads or writes, and pdl_launch_dependents only
 // after that.
-template <typename... A>
-tq_status launch_pdl(void (*kernel)(A...), unsigned grid, unsigned block, cudaStream_t s, A... args) {
+template <typename... P, typename... A>
+tq_status launch_pdl(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t s, A... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -45,7 +45,7 @@ tq_status launch_pdl(void (*kernel)(A...), unsigned grid, unsigned block, cudaSt
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
 
