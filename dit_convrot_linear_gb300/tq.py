@@ -929,117 +929,139 @@ def kv4_attention(batch: KV4Batch, Q, scale: float, workspace, causal: bool = Tr
 
 
 # ------------------------------------- products in 8-bit floating point, experts
-# Codes are e4m3 bytes: uint8 tensors, or torch.float8_e4m3fn ones.
+# Codes are e4m3 bytes: uint8 tensors, or torch.float8_e4m3fn ones.  All tensors of a
+# call are on the current device, the one that the library launches on.  A call of a few
+# tokens takes a few microseconds, so its checks are few and plain: a tensor that passes
+# none of them is described afterwards.
 
-def _codes(t, what, *shape):
-    """Dense e4m3 codes of this shape."""
-    if not (t.is_cuda and t.element_size() == 1 and tuple(t.shape) == shape and t.is_contiguous()):
-        raise ValueError(f"{what} must be a dense CUDA tensor of e4m3 bytes {shape}, got {t.dtype} {tuple(t.shape)}")
-
-
-def _list(t, what, n):
-    """A contiguous int32 CUDA tensor of n numbers."""
-    import torch
-    if not (t.is_cuda and t.dtype is torch.int32 and t.numel() == n and t.is_contiguous()):
-        raise ValueError(f"{what} must be {n} contiguous int32 numbers on the GPU, got {t.dtype} {tuple(t.shape)}")
+_torch = None
 
 
-def _here(*tensors):
-    """All on the current device, the one that the library launches on."""
-    import torch
-    d = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.device.index != d:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{d}")
+def _module():
+    """torch, once it is loaded (an import statement costs as much as a check)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        load()
+    return _torch
+
+
+def _bad(t, what, wanted):
+    if t is None:
+        raise ValueError(f"{what} is required")
+    raise ValueError(f"{what} must be {wanted} on the current device (cuda:{_module()._C._cuda_getDevice()}), got "
+                     f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+
+
+def _dense(t, what, dtype, shape, d):
+    """The address of a contiguous tensor of this type and shape."""
+    if t.get_device() != d or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _bad(t, what, f"contiguous {dtype} {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _codes(t, what, shape, d):
+    """The address of contiguous e4m3 codes of this shape."""
+    if t.get_device() != d or t.element_size() != 1 or t.shape != shape or not t.is_contiguous():
+        _bad(t, what, f"contiguous e4m3 bytes {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _list(t, what, n, d):
+    """The address of n contiguous int32 numbers."""
+    if t.get_device() != d or t.dtype is not _torch.int32 or t.numel() != n or not t.is_contiguous():
+        _bad(t, what, f"{n} contiguous int32 numbers")
+    return t.data_ptr()
+
+
+def _matrix(t, what, dtype, M, K, d) -> int:
+    """The row stride of rows of K values (a matrix of at least M x K).  One row has no
+    step to the next: its length stands for it."""
+    s = t.shape
+    if t.get_device() != d or t.dtype is not dtype or len(s) != 2 or s[0] < M or s[1] < K:
+        _bad(t, what, f"{dtype} of at least {M} x {K}")
+    ld, one = t.stride()
+    if one != 1 and t.numel():
+        _bad(t, what, "row-major")
+    return ld if s[0] > 1 else max(s[1], 1)
 
 
 def _floats(t, what) -> int:
     """0 for fp32, 1 for bf16."""
-    import torch
-    if t.dtype is torch.bfloat16:
+    if t.dtype is _torch.bfloat16:
         return 1
-    if t.dtype is torch.float32:
+    if t.dtype is _torch.float32:
         return 0
     raise ValueError(f"{what} is {t.dtype}, expected float32 or bfloat16")
 
 
+def _stream_of(stream, d) -> int:
+    return _torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+
+
 def quantize_weights_f8(W, codes=None, scales=None, stream=None):
-    """bf16 W [N, K], or [experts, N, K] (an expert's rows dense) -> (e4m3 codes of
-    the same shape, fp32 scales [..., ceil(N / 128), ceil(K / 128)])."""
-    import torch
+    """bf16 W [N, K], or [experts, N, K] -> (e4m3 codes of the same shape, fp32 scales
+    [..., ceil(N / 128), ceil(K / 128)])."""
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     if W.dim() not in (2, 3):
         raise ValueError("W must be [N, K] or [experts, N, K]")
     N, K = W.shape[-2:]
+    blocks = (*W.shape[:-2], -(-N // 128), -(-K // 128))
     if codes is None:
         codes = torch.empty(W.shape, dtype=torch.uint8, device=W.device)
-    blocks = (*W.shape[:-2], -(-N // 128), -(-K // 128))
     if scales is None:
         scales = torch.empty(blocks, dtype=torch.float32, device=W.device)
-    _codes(codes, "codes", *W.shape)
-    _flat(scales, "scales", torch.float32, scales.numel())
-    if tuple(scales.shape) != blocks:
-        raise ValueError(f"scales are {tuple(scales.shape)}, expected {blocks}")
-    _here(W, codes, scales)
-    one = W.dim() == 2
-    for w, c, s in ((W, codes, scales),) if one else zip(W, codes, scales):
-        ldw = _rows(w, "W", torch.bfloat16, N, K)
-        _check((_lib or load()).tq_quantize_weights_f8(w.data_ptr(), N, K, ldw if N > 1 else K, c.data_ptr(),
-                                                       s.data_ptr(), _raw_stream(W, stream)),
+    _codes(codes, "codes", W.shape, d)
+    _dense(scales, "scales", torch.float32, blocks, d)
+    for w, c, s in ((W, codes, scales),) if W.dim() == 2 else zip(W, codes, scales):
+        ldw = _matrix(w, "W", torch.bfloat16, N, K, d)
+        _check(_lib.tq_quantize_weights_f8(w.data_ptr(), N, K, ldw, c.data_ptr(), s.data_ptr(), _stream_of(stream, d)),
                "tq_quantize_weights_f8")
     return codes, scales
 
 
-def _operand(M, K, Xq, sx, device):
-    import torch
+def _operand(torch, M, K, Xq, sx, device):
     if Xq is None:
         Xq = torch.empty((M, K), dtype=torch.uint8, device=device)
     if sx is None:
         sx = torch.empty((-(-K // 128), M), dtype=torch.float32, device=device)
-    _codes(Xq, "Xq", M, K)
-    _scales(sx, "sx", -(-K // 128), M)
     return Xq, sx
-
-
-def _scales(t, what, *shape):
-    import torch
-    if not (t.is_cuda and t.dtype is torch.float32 and tuple(t.shape) == shape and t.is_contiguous()):
-        raise ValueError(f"{what} must be a dense fp32 CUDA tensor {shape}, got {t.dtype} {tuple(t.shape)}")
-
-
-def _ld(t, ld: int) -> int:
-    """A row stride; one row has no step to the next: its length stands for it."""
-    return ld if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
 def quant_act_f8(X, rows=None, Xq=None, sx=None, stream=None):
     """bf16 X [M, K] (any row stride), or its rows named by ``rows`` (int32 [M];
     -1: left as it was) -> (e4m3 codes [M, K], fp32 scales [ceil(K / 128), M])."""
-    import torch
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     R, K = X.shape
     M = R if rows is None else rows.numel()
-    ldx = _ld(X, _rows(X, "X", torch.bfloat16, R, K))
-    if rows is not None:
-        _list(rows, "rows", M)
-    Xq, sx = _operand(M, K, Xq, sx, X.device)
-    _here(X, rows, Xq, sx)
-    _check((_lib or load()).tq_quant_act_f8(X.data_ptr(), R, K, ldx, 0 if rows is None else rows.data_ptr(), M,
-                                            Xq.data_ptr(), sx.data_ptr(), _raw_stream(X, stream)), "tq_quant_act_f8")
+    if Xq is None or sx is None:
+        Xq, sx = _operand(torch, M, K, Xq, sx, X.device)
+    rc = _lib.tq_quant_act_f8(X.data_ptr(), R, K, _matrix(X, "X", torch.bfloat16, R, K, d),
+                              None if rows is None else _list(rows, "rows", M, d), M, _codes(Xq, "Xq", (M, K), d),
+                              _dense(sx, "sx", torch.float32, (-(-K // 128), M), d), _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_quant_act_f8")
     return Xq, sx
 
 
 def swiglu_quant_act_f8(G, U, Xq=None, sx=None, stream=None):
     """``quant_act_f8`` of silu(G) * U (bf16 [M, K], any row strides, for example the
     halves of a gate+up product's output)."""
-    import torch
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     M, K = G.shape
-    ldg = _ld(G, _rows(G, "G", torch.bfloat16, M, K))
-    if tuple(U.shape) != (M, K):
+    if U.shape != G.shape:
         raise ValueError(f"U is {tuple(U.shape)}, expected {(M, K)}")
-    ldu = _ld(U, _rows(U, "U", torch.bfloat16, M, K))
-    Xq, sx = _operand(M, K, Xq, sx, G.device)
-    _here(G, U, Xq, sx)
-    _check((_lib or load()).tq_swiglu_quant_act_f8(G.data_ptr(), ldg, U.data_ptr(), ldu, M, K, Xq.data_ptr(),
-                                                   sx.data_ptr(), _raw_stream(G, stream)), "tq_swiglu_quant_act_f8")
+    if Xq is None or sx is None:
+        Xq, sx = _operand(torch, M, K, Xq, sx, G.device)
+    rc = _lib.tq_swiglu_quant_act_f8(G.data_ptr(), _matrix(G, "G", torch.bfloat16, M, K, d), U.data_ptr(),
+                                     _matrix(U, "U", torch.bfloat16, M, K, d), M, K, _codes(Xq, "Xq", (M, K), d),
+                                     _dense(sx, "sx", torch.float32, (-(-K // 128), M), d), _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_swiglu_quant_act_f8")
     return Xq, sx
 
 
@@ -1049,149 +1071,151 @@ def f8_workspace(device="cuda"):
     return torch.zeros(int(lib().tq_f8_workspace_bytes()), dtype=torch.uint8, device=device)
 
 
-def _linear_f8(Xq, sx, offsets, Wq, sw, workspace, out, Y, stream):
-    import torch
-    if Wq.dim() != (2 if offsets is None else 3):
-        raise ValueError(f"Wq is {tuple(Wq.shape)}, expected {'[N, K]' if offsets is None else '[experts, N, K]'}")
-    M, K = Xq.shape
-    N = Wq.shape[-2]
-    lead = () if offsets is None else (Wq.shape[0],)
-    _codes(Xq, "Xq", M, K)
-    _codes(Wq, "Wq", *lead, N, K)
-    _scales(sx, "sx", -(-K // 128), M)
-    _scales(sw, "sw", *lead, -(-N // 128), -(-K // 128))
-    if out not in ("f32", "bf16"):
-        raise ValueError("the 8-bit floating-point products write f32 or bf16")
-    dtype = torch.float32 if out == "f32" else torch.bfloat16
-    if Y is None:       # rows that no expert has are not written
-        Y = (torch.empty if offsets is None else torch.zeros)((M, N), dtype=dtype, device=Xq.device)
-    ldy = _ld(Y, _rows(Y, "Y", dtype, M, N))
-    _flat(workspace, "workspace", torch.uint8, 1)
-    _here(Xq, sx, offsets, Wq, sw, Y, workspace)
-    lib_ = _lib or load()
-    tail = (Wq.data_ptr(), sw.data_ptr(), N, Y.data_ptr(), OUT[out], ldy, workspace.data_ptr(), workspace.numel(),
-            _raw_stream(Xq, stream))
-    if offsets is None:
-        _check(lib_.tq_linear_f8(Xq.data_ptr(), sx.data_ptr(), M, K, *tail), "tq_linear_f8")
-    else:
-        _list(offsets, "offsets", lead[0] + 1)
-        _check(lib_.tq_linear_f8_experts(Xq.data_ptr(), sx.data_ptr(), M, K, offsets.data_ptr(), lead[0], *tail),
-               "tq_linear_f8_experts")
-    return Y
-
-
 def linear_f8(Xq, sx, Wq, sw, workspace, out: str = "bf16", Y=None, stream=None):
     """Y [M, N] = the product of e4m3 operands with a scale for each block of 128:
     (Xq, sx) from ``quant_act_f8``, Wq [N, K] and sw [ceil(N / 128), ceil(K / 128)]
     from ``quantize_weights_f8`` or as published; workspace from ``f8_workspace()``."""
-    return _linear_f8(Xq, sx, None, Wq, sw, workspace, out, Y, stream)
+    torch = _module()
+    d = torch._C._cuda_getDevice()
+    f32 = torch.float32
+    if out != "bf16" and out != "f32":
+        raise ValueError("the 8-bit floating-point products write f32 or bf16")
+    dtype = torch.bfloat16 if out == "bf16" else f32
+    M, K = Xq.shape
+    N = Wq.shape[0]
+    if Y is None:
+        Y = torch.empty((M, N), dtype=dtype, device=Xq.device)
+    kb = -(-K // 128)
+    rc = _lib.tq_linear_f8(_codes(Xq, "Xq", (M, K), d), _dense(sx, "sx", f32, (kb, M), d), M, K,
+                           _codes(Wq, "Wq", (N, K), d), _dense(sw, "sw", f32, (-(-N // 128), kb), d), N, Y.data_ptr(),
+                           OUT[out], _matrix(Y, "Y", dtype, M, N, d),
+                           _dense(workspace, "workspace", torch.uint8, workspace.shape, d), workspace.numel(),
+                           _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_linear_f8")
+    return Y
 
 
 def linear_f8_experts(Xq, sx, offsets, Wq, sw, workspace, out: str = "bf16", Y=None, stream=None):
     """``linear_f8`` with a weight matrix an expert: rows offsets[e] .. offsets[e + 1] - 1
-    (int32 [experts + 1]) by Wq[e].  Rows that no expert has are left as they were
-    (zeros in a Y made here)."""
-    return _linear_f8(Xq, sx, offsets, Wq, sw, workspace, out, Y, stream)
+    (int32 [experts + 1]) by Wq[e] ([experts, N, K], sw [experts, ceil(N / 128),
+    ceil(K / 128)]).  Rows that no expert has are left as they were (zeros in a Y made
+    here)."""
+    torch = _module()
+    d = torch._C._cuda_getDevice()
+    f32 = torch.float32
+    if out != "bf16" and out != "f32":
+        raise ValueError("the 8-bit floating-point products write f32 or bf16")
+    dtype = torch.bfloat16 if out == "bf16" else f32
+    if Wq.dim() != 3:
+        raise ValueError(f"Wq is {tuple(Wq.shape)}, expected [experts, N, K]")
+    M, K = Xq.shape
+    E, N = Wq.shape[:2]
+    if Y is None:
+        Y = torch.zeros((M, N), dtype=dtype, device=Xq.device)
+    kb = -(-K // 128)
+    rc = _lib.tq_linear_f8_experts(_codes(Xq, "Xq", (M, K), d), _dense(sx, "sx", f32, (kb, M), d), M, K,
+                                   _list(offsets, "offsets", E + 1, d), E, _codes(Wq, "Wq", (E, N, K), d),
+                                   _dense(sw, "sw", f32, (E, -(-N // 128), kb), d), N, Y.data_ptr(), OUT[out],
+                                   _matrix(Y, "Y", dtype, M, N, d),
+                                   _dense(workspace, "workspace", torch.uint8, workspace.shape, d), workspace.numel(),
+                                   _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_linear_f8_experts")
+    return Y
 
 
 def expert_topk(logits, top: int, renorm: bool = True, ids=None, weights=None, stream=None):
     """The router's choice: logits (fp32 or bf16 [tokens, experts], any row stride) ->
     (ids int32 [tokens, top], weights fp32 [tokens, top])."""
-    import torch
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     T, E = logits.shape
-    kind = _floats(logits, "logits")
-    ld = _ld(logits, _rows(logits, "logits", logits.dtype, T, E))
     if ids is None:
         ids = torch.empty((T, top), dtype=torch.int32, device=logits.device)
     if weights is None:
         weights = torch.empty((T, top), dtype=torch.float32, device=logits.device)
-    _list(ids, "ids", T * top)
-    _scales(weights, "weights", T, top)
-    _here(logits, ids, weights)
-    _check((_lib or load()).tq_expert_topk(logits.data_ptr(), kind, T, E, ld, top, int(renorm), ids.data_ptr(),
-                                           weights.data_ptr(), _raw_stream(logits, stream)), "tq_expert_topk")
+    rc = _lib.tq_expert_topk(logits.data_ptr(), _floats(logits, "logits"), T, E,
+                             _matrix(logits, "logits", logits.dtype, T, E, d), top, int(renorm),
+                             _list(ids, "ids", T * top, d), _dense(weights, "weights", torch.float32, (T, top), d),
+                             _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_expert_topk")
     return ids, weights
 
 
 def expert_topk_grad(logits, ids, dweights, renorm: bool = True, dlogits=None, stream=None):
     """dlogits (of the logits' type) from the gradients of ``expert_topk``'s weights."""
-    import torch
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     T, E = logits.shape
-    kind = _floats(logits, "logits")
-    ld = _ld(logits, _rows(logits, "logits", logits.dtype, T, E))
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, top]")
     top = ids.shape[1]
-    _list(ids, "ids", T * top)
-    _scales(dweights, "dweights", T, top)
     if dlogits is None:
         dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    ldd = _ld(dlogits, _rows(dlogits, "dlogits", logits.dtype, T, E))
-    _here(logits, ids, dweights, dlogits)
-    _check((_lib or load()).tq_expert_topk_grad(logits.data_ptr(), kind, T, E, ld, ids.data_ptr(),
-                                                dweights.data_ptr(), top, int(renorm), dlogits.data_ptr(), ldd,
-                                                _raw_stream(logits, stream)), "tq_expert_topk_grad")
+    rc = _lib.tq_expert_topk_grad(logits.data_ptr(), _floats(logits, "logits"), T, E,
+                                  _matrix(logits, "logits", logits.dtype, T, E, d), _list(ids, "ids", T * top, d),
+                                  _dense(dweights, "dweights", torch.float32, (T, top), d), top, int(renorm),
+                                  dlogits.data_ptr(), _matrix(dlogits, "dlogits", logits.dtype, T, E, d),
+                                  _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_expert_topk_grad")
     return dlogits
 
 
 def expert_sort(ids, experts: int, offsets=None, token=None, place=None, stream=None):
     """Choices (int32 [tokens, top], -1: none) sorted by expert: (offsets int32
     [experts + 1], token int32 [tokens * top], place int32 [tokens, top])."""
-    import torch
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     T, top = ids.shape
-    _list(ids, "ids", T * top)
-
-    def made(n):
-        return torch.empty(n, dtype=torch.int32, device=ids.device)
-
-    offsets = made(experts + 1) if offsets is None else offsets
-    token = made(T * top) if token is None else token
-    place = made((T, top)) if place is None else place
-    _list(offsets, "offsets", experts + 1)
-    _list(token, "token", T * top)
-    _list(place, "place", T * top)
-    _here(ids, offsets, token, place)
-    _check((_lib or load()).tq_expert_sort(ids.data_ptr(), T, top, experts, offsets.data_ptr(), token.data_ptr(),
-                                           place.data_ptr(), _raw_stream(ids, stream)), "tq_expert_sort")
+    n = T * top
+    if offsets is None:
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+    if token is None:
+        token = torch.empty(n, dtype=torch.int32, device=ids.device)
+    if place is None:
+        place = torch.empty((T, top), dtype=torch.int32, device=ids.device)
+    rc = _lib.tq_expert_sort(_list(ids, "ids", n, d), T, top, experts, _list(offsets, "offsets", experts + 1, d),
+                             _list(token, "token", n, d), _list(place, "place", n, d), _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_expert_sort")
     return offsets, token, place
 
 
 def expert_gather(X, rows, Y=None, stream=None):
     """X's rows (fp32 or bf16 [., width]) named by ``rows`` (int32 [M]; -1: left as it
     was, zeros in a Y made here).  Returns Y [M, width]."""
-    import torch
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     R, W = X.shape
     M = rows.numel()
-    kind = _floats(X, "X")
-    ldx = _ld(X, _rows(X, "X", X.dtype, R, W))
-    _list(rows, "rows", M)
     if Y is None:
         Y = torch.zeros((M, W), dtype=X.dtype, device=X.device)
-    ldy = _ld(Y, _rows(Y, "Y", X.dtype, M, W))
-    _here(X, rows, Y)
-    _check((_lib or load()).tq_expert_gather(X.data_ptr(), kind, R, W, ldx, rows.data_ptr(), M, Y.data_ptr(), ldy,
-                                             _raw_stream(X, stream)), "tq_expert_gather")
+    rc = _lib.tq_expert_gather(X.data_ptr(), _floats(X, "X"), R, W, _matrix(X, "X", X.dtype, R, W, d),
+                               _list(rows, "rows", M, d), M, Y.data_ptr(), _matrix(Y, "Y", X.dtype, M, W, d),
+                               _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_expert_gather")
     return Y
 
 
 def expert_combine(Y, place, weights=None, O=None, stream=None):
     """O[t] = sum over j of weights[t, j] * Y[place[t, j]] (Y fp32 or bf16 [rows,
     width]; place int32, weights fp32 [tokens, top], none: 1).  Returns O."""
-    import torch
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     R, W = Y.shape
     T, top = place.shape
-    kind = _floats(Y, "Y")
-    ldy = _ld(Y, _rows(Y, "Y", Y.dtype, R, W))
-    _list(place, "place", T * top)
-    if weights is not None:
-        _scales(weights, "weights", T, top)
     if O is None:
         O = torch.empty((T, W), dtype=Y.dtype, device=Y.device)
-    ldo = _ld(O, _rows(O, "O", Y.dtype, T, W))
-    _here(Y, place, weights, O)
-    _check((_lib or load()).tq_expert_combine(Y.data_ptr(), kind, R, W, ldy, place.data_ptr(),
-                                              0 if weights is None else weights.data_ptr(), T, top, O.data_ptr(), ldo,
-                                              _raw_stream(Y, stream)), "tq_expert_combine")
+    rc = _lib.tq_expert_combine(Y.data_ptr(), _floats(Y, "Y"), R, W, _matrix(Y, "Y", Y.dtype, R, W, d),
+                                _list(place, "place", T * top, d),
+                                None if weights is None else _dense(weights, "weights", torch.float32, (T, top), d), T,
+                                top, O.data_ptr(), _matrix(O, "O", Y.dtype, T, W, d), _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_expert_combine")
     return O
 
 
@@ -1199,26 +1223,22 @@ def expert_combine_grad(dO, Y, place, weights=None, dY=None, dweights=None, stre
     """The gradients of ``expert_combine``: (dY [rows, width], dweights fp32 [tokens,
     top]).  Rows of dY that no choice leads to are left as they were (zeros in a dY
     made here)."""
-    import torch
+    torch = _module()
+    d = torch._C._cuda_getDevice()
     R, W = Y.shape
     T, top = place.shape
-    kind = _floats(Y, "Y")
-    ldy = _ld(Y, _rows(Y, "Y", Y.dtype, R, W))
-    if tuple(dO.shape) != (T, W):
+    if dO.shape != (T, W):
         raise ValueError(f"dO is {tuple(dO.shape)}, expected {(T, W)}")
-    ldo = _ld(dO, _rows(dO, "dO", Y.dtype, T, W))
-    _list(place, "place", T * top)
-    if weights is not None:
-        _scales(weights, "weights", T, top)
     if dY is None:
         dY = torch.zeros((R, W), dtype=Y.dtype, device=Y.device)
-    lddy = _ld(dY, _rows(dY, "dY", Y.dtype, R, W))
     if dweights is None:
         dweights = torch.empty((T, top), dtype=torch.float32, device=Y.device)
-    _scales(dweights, "dweights", T, top)
-    _here(dO, Y, place, weights, dY, dweights)
-    _check((_lib or load()).tq_expert_combine_grad(
-        dO.data_ptr(), ldo, Y.data_ptr(), kind, R, W, ldy, place.data_ptr(),
-        0 if weights is None else weights.data_ptr(), T, top, dY.data_ptr(), lddy, dweights.data_ptr(),
-        _raw_stream(Y, stream)), "tq_expert_combine_grad")
+    rc = _lib.tq_expert_combine_grad(dO.data_ptr(), _matrix(dO, "dO", Y.dtype, T, W, d), Y.data_ptr(),
+                                     _floats(Y, "Y"), R, W, _matrix(Y, "Y", Y.dtype, R, W, d),
+                                     _list(place, "place", T * top, d),
+                                     None if weights is None else _dense(weights, "weights", torch.float32, (T, top), d),
+                                     T, top, dY.data_ptr(), _matrix(dY, "dY", Y.dtype, R, W, d),
+                                     _dense(dweights, "dweights", torch.float32, (T, top), d), _stream_of(stream, d))
+    if rc:
+        _check(rc, "tq_expert_combine_grad")
     return dY, dweights
