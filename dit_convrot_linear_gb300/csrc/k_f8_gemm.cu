@@ -6,30 +6,33 @@
 // A step of K is one scale block, four MMAs of 32.  The accumulator of each step lies
 // in TMEM of its own, and the drain warps add it, times its scales, to the sums in
 // their registers.  Two forms of a tile:
-//   many tokens  256 tokens by 256 columns of Y, by a pair of CTAs (cta_group::2).  The
-//                tokens are the MMA's M side, 128 a CTA, so that a TMEM lane is a token
-//                and a step's scales are one number a thread,
-//                acc += (sx[b][token] * sw[block][b]) * part.
-//   few tokens   128 columns of Y by up to 64 tokens, by one CTA.  The weights are the
-//                M side and the tokens the N side, in steps of 16: an expert's few rows
-//                cost no empty rows of a 128-row tile.  The scales differ from column
-//                to column and come from shared memory, 4 bytes a lane and value; at 64
-//                tokens that hides behind the weights' stream.
+//   many tokens  128 tokens by 256 columns of Y (128 where that saves a round).  The tokens
+//                are the MMA's M side, so that a TMEM lane is a token and a step's scales are
+//                one number a thread, acc += (sx[b][token] * sw[block][b]) * part.
+//   few tokens   128 columns of Y by up to 64 tokens.  The weights are the M side and the
+//                tokens the N side, in steps of 16: an expert's few rows cost no empty rows
+//                of a 128-row tile.  The scales differ from column to column and come from
+//                shared memory, 4 bytes a lane and value; at 64 tokens that hides behind the
+//                weights' stream.
 // Warps of a CTA (one an SM):
-//   drain warps   (a TMEM lane quarter and 64 columns each) multiply and add, write Y;
-//   MMA warps     one thread of each issues (of a pair: in the even CTA);
-//   copy warp     tensor copies of both operands into the ring (128-byte swizzle);
-//   scale warp    each step's scales, sx * sw, into shared memory.
+//   8 drain warps  multiply and add, write Y: a TMEM lane quarter and 128 columns each, or
+//                  64 columns, four warps a step in turn, whose sums are put together;
+//   MMA warps      one thread of each issues: two a half, that take the steps in turn;
+//   copy warp      tensor copies of both operands into the ring (128-byte swizzle);
+//   2 scale warps  each step's scales into shared memory, in turn.
 //
-// What bounds it.  With many tokens a step's MMAs take 512 cycles, and shared memory is
-// written and read 64 KB a step, 512 cycles too (two single CTAs of 128 x 256: 96 KB).
-// Between an accumulator's last MMA and the first that fills it again lie a commit
-// (300 cycles), the drain, its arrival in the other SM (240) and an issue; TMEM holds
-// two steps.  So a step's columns are two accumulators of 128 with MMAs of their own
-// (80 KB a step), one filled while the other is drained; four threads issue, each
-// every other step of a half; and sixteen warps drain, so that the accumulator is read
-// after two TMEM loads of each.  Few tokens: the weights' stream, eight stages of 16 KB
-// of it in flight.
+// What bounds it.  With many tokens a step's MMAs take 512 cycles, and it takes about 950
+// (4032 tokens, 4096 to 12288: 185 us, 2200 TFLOP/s).  Between an accumulator's last MMA
+// and the first that fills it again lie a commit (300 cycles), the drain, its arrival (200)
+// and an issue, and TMEM holds two steps; shared memory is written and read 96 KB a step,
+// 750 cycles.  So a step's columns are two accumulators of 128 with MMAs of their own, one
+// filled while the other is drained, and four threads issue.  Pairs of CTAs (256 x 256, 80
+// KB a step and CTA) take as long for such a matrix, as the arrivals cross to the other SM,
+// and waste more of an expert's last tile: 512 tokens of 64 experts, eight each, 2048 x
+// 2048: 87 us against 57; 4096 tokens 178 against 164.  Sixteen drain warps: 10% slower.
+// Few tokens: the weights' stream, of which an SM draws 42 bytes a ns; six stages of 16 KB
+// of it in flight.  In both forms the copies are one thread's, and its instructions a step
+// count: a loop over the boxes of the N side in place of two calls costs 10%.
 //
 // The work is a list of tiles (expert, columns, tokens).  Whole rounds of tiles go to
 // the CTAs one by one; the K steps of a last round that would leave CTAs idle are
@@ -52,22 +55,21 @@ constexpr unsigned int kStatusF8Timeout = 64u;
 
 template <bool WIDE_>
 struct F8Plan {
-    static constexpr bool WIDE = WIDE_;                        // many tokens: they are the M side, of a pair
-    static constexpr int CTAS = WIDE ? 2 : 1;                  // of a tile
-    static constexpr int TOKENS = WIDE ? 256 : 64;             // of a tile, at most
+    static constexpr bool WIDE = WIDE_;                        // many tokens: they are the M side
+    static constexpr int TOKENS = WIDE ? 128 : 64;             // of a tile, at most
     static constexpr int YCOLS = WIDE ? 256 : 128;             // weight rows of a tile, at most
     static constexpr int NCOLS = WIDE ? YCOLS : TOKENS;        // the N side
     static constexpr int COLS = WIDE ? 128 : 64;               // of them a drain warp
     static constexpr int SETS = WIDE ? 1 : 2;                  // of drain warps, that take the steps in turn
     static constexpr int DRAIN = 4 * NCOLS / COLS * SETS;      // drain warps
     static constexpr int HALVES = WIDE ? 2 : 1;                // accumulators a step
-    static constexpr int ISSUERS = 2 * HALVES, IN_TURN = ISSUERS / HALVES;  // MMA warps; of them a half's, that take the steps in turn
+    static constexpr int ISSUERS = 2 * HALVES, IN_TURN = ISSUERS / HALVES;  // MMA warps; a half's, the steps in turn
     static constexpr int SCALERS = 2;                           // scale warps: the steps in turn
     static constexpr int OTHERS = 8;                           // warps that do not drain
     static constexpr int THREADS = (DRAIN + OTHERS) * 32;
-    static constexpr int B_BOX = WIDE ? 64 : 32;               // rows of one tensor copy of the N side
-    static constexpr int STAGE = kABytes + NCOLS / CTAS * kStepK;
-    static constexpr int STAGES = 6;
+    static constexpr int B_BOX = WIDE ? 128 : 32;               // rows of one tensor copy of the N side
+    static constexpr int STAGE = kABytes + NCOLS * kStepK;
+    static constexpr int STAGES = WIDE ? 4 : 6;
     static constexpr int TURNS = WIDE ? 2 : 4;                 // steps with accumulators in TMEM
     static constexpr int ACCS = TURNS * HALVES, ACC_COLS = NCOLS / HALVES;
     static constexpr int TMEM = ACC_COLS * ACCS;
@@ -85,7 +87,7 @@ struct F8Plan {
     // the list of experts: first row, rows, tiles before
     static constexpr int smem(int64_t experts) { return OFF_LIST + static_cast<int>(experts + 1) * 12 + 16; }
     static constexpr int PART = DRAIN * 32 * COLS * 4;         // bytes of a CTA's partial tile
-    static constexpr int MIN_STEPS = 4, JOIN_STEPS = WIDE ? 16 : 12;   // of split tiles: steps a worker, steps saved
+    static constexpr int MIN_STEPS = 4, JOIN_STEPS = WIDE ? 44 : 12;   // of split tiles: steps a CTA, steps saved
     static constexpr int DRAIN_REGS = 176, OTHER_REGS = 80;     // many tokens: registers a thread
 };
 // A wait for a parity tells two neighbouring rounds of a barrier apart, no more: who
@@ -113,12 +115,12 @@ struct F8Params {
     int64_t ldy;
     int ytype, vec;                      // vec: rows of Y allow 16-byte stores (few tokens: 4-byte ones)
     unsigned int *status;
-    unsigned int *counters;              // [workers][CTAs][kF8MaxDrain]
-    unsigned char *parts;                // [workers][2][CTAs][PART]
+    unsigned int *counters;              // [CTAs][kF8MaxDrain]
+    unsigned char *parts;                // [CTAs][2][PART]
 };
 
 // A piece of work: the tile's place, K steps k0 .. k1 - 1, and for a piece of a
-// split tile the workers (pairs or CTAs) that have its first and last step.
+// split tile the CTAs that have its first and last step.
 struct F8Seg {
     int e, ntile, m0, cols, k0, k1;      // cols: tokens of the tile
     bool whole;
@@ -130,20 +132,19 @@ struct F8Seg {
 struct F8Cut {
     int whole;       // tiles computed whole
     int units;       // K steps of the others,
-    int use;         // shared by this many workers
+    int use;         // shared by this many CTAs
 };
 
-// The pieces of work of a worker, in order.  (What does not change lies in shared
+// The pieces of work of a CTA, in order.  (What does not change lies in shared
 // memory: the drain warps have few registers to spare.)
-template <int CTAS>
 struct F8Iter {
     int i, u0;
-    static __device__ int me() { return blockIdx.x / CTAS; }
-    __device__ explicit F8Iter(const F8Cut &c) : i(0), u0(me() < c.use ? bound(c, me()) : 0) {}
+    __device__ explicit F8Iter(const F8Cut &c)
+        : i(0), u0(static_cast<int>(blockIdx.x) < c.use ? bound(c, blockIdx.x) : 0) {}
     static __device__ int bound(const F8Cut &c, int q) {
         return static_cast<int>(static_cast<long long>(c.units) * q / c.use);
     }
-    // the worker whose steps include x
+    // the CTA whose steps include x
     static __device__ int owner(const F8Cut &c, int x) {
         int q = static_cast<int>(static_cast<long long>(x) * c.use / c.units);
         while (q + 1 < c.use && bound(c, q + 1) <= x) ++q;
@@ -166,8 +167,8 @@ struct F8Iter {
         s.cols = min(each, n - part * each);
     }
     __device__ bool next(const F8Cut &c, const int *list, const F8Params &p, F8Seg &s) {
-        const int worker = me(), ksteps = p.ksteps;
-        const int t = worker + i * static_cast<int>(gridDim.x / CTAS);
+        const int cta = blockIdx.x, ksteps = p.ksteps;
+        const int t = cta + i * static_cast<int>(gridDim.x);
         if (t < c.whole) {
             ++i;
             place(list, p, t, s);
@@ -176,14 +177,14 @@ struct F8Iter {
             s.whole = true;
             return true;
         }
-        const int u1 = worker < c.use ? bound(c, worker + 1) : 0;
+        const int u1 = cta < c.use ? bound(c, cta + 1) : 0;
         if (u0 >= u1) return false;
         const int tl = u0 / ksteps, ts = tl * ksteps;
         place(list, p, c.whole + tl, s);
         s.k0 = u0 - ts;
         s.k1 = min(u1, ts + ksteps) - ts;
         s.whole = s.k0 == 0 && s.k1 == ksteps;
-        s.first = s.last = worker;
+        s.first = s.last = cta;
         if (!s.whole) {
             s.first = owner(c, ts);
             s.last = owner(c, ts + ksteps - 1);
@@ -217,54 +218,19 @@ __device__ __forceinline__ bool f8_wait(uint32_t bar, uint32_t parity, volatile 
     return true;
 }
 
-// The address of the same place in the pair's even CTA, and an arrival there.  What it
-// hands over is TMEM that has been read (tcgen05.wait::ld came before), no memory: a
-// release at cluster scope would wait for all that this thread has in flight (2000
-// cycles a step).
-__device__ __forceinline__ uint32_t in_even_cta(uint32_t addr) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(addr));
-    return remote;
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t remote) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
-}
-
-// a step's four MMAs into the accumulator at d, and the commit to a barrier
-template <int CTAS>
-__device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    if constexpr (CTAS == 2)
-        asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u));
-    else
-        asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
-                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u));
-}
-template <int CTAS>
-__device__ __forceinline__ void f8_commit(uint32_t bar) {
-    if constexpr (CTAS == 2)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                     ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-// a tensor copy that completes on a barrier of this CTA, or of the pair's even one
-template <int CTAS>
-__device__ __forceinline__ void f8_copy(uint32_t dst, const CUtensorMap *map, int k, int row, uint32_t bar) {
-    if constexpr (CTAS == 2)
-        asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-                     "[%0], [%1, {%2, %3}], [%4];"
-                     ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(k), "r"(row), "r"(bar) : "memory");
-    else
-        tma_load_2d(dst, map, k, row, bar);
-}
-
 // A warp's wait: all or none of its lanes go on.
 __device__ __forceinline__ bool f8_wait_warp(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *status) {
     const bool ok = f8_wait(bar, parity, abort, status);
     return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u));
+}
+__device__ __forceinline__ void f8_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // A place in a ring of N stages and the parity of the round that fills it.
@@ -314,7 +280,6 @@ template <class P>
 __global__ void __launch_bounds__(P::THREADS, 1)
 k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Params p) {
     constexpr int DRAIN = P::DRAIN, STAGES = P::STAGES, ACCS = P::ACCS, TURNS = P::TURNS, HALVES = P::HALVES;
-    constexpr int CTAS = P::CTAS;
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + P::OFF_BARS);
     __shared__ uint32_t tmem_base_sh;
@@ -325,19 +290,18 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
     const uint32_t acc_full0 = empty0 + 8 * STAGES, acc_empty0 = acc_full0 + 8 * ACCS;
     const uint32_t done = acc_empty0 + 8 * ACCS, sum_full0 = done + 8, sum_empty0 = sum_full0 + 32;
-    const int rank = static_cast<int>(blockIdx.x) % CTAS;      // in the pair
 
     if (threadIdx.x == 32) {
         auto init = [](uint32_t bar, uint32_t n) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n));
         };
         for (int s = 0; s < STAGES; ++s) {
-            init(full0 + 8 * s, 1);                 // (a pair's: used in the even CTA, its bytes cover both)
+            init(full0 + 8 * s, 1);
             init(empty0 + 8 * s, HALVES);
         }
         for (int a = 0; a < ACCS; ++a) {
             init(acc_full0 + 8 * a, 2);             // the step's MMAs, and its scales
-            init(acc_empty0 + 8 * a, CTAS * DRAIN / HALVES / P::SETS);   // (a pair's: used in the even CTA)
+            init(acc_empty0 + 8 * a, DRAIN / HALVES / P::SETS);
         }
         for (int i = 0; i < 8; ++i) init(sum_full0 + 8 * i, 1);         // a quarter's sums: put there, taken
         init(done, P::ISSUERS);
@@ -403,11 +367,14 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             total = sum;
         }
         if (lane == 0) {
-            // The tiles of a last round that leaves workers idle are split where that saves more
-            // steps than the joining costs, in at most kF8MaxParts parts each.
-            const int n = total * p.ntiles, workers = gridDim.x / CTAS, rest = n % workers;
+            // The tiles of a last round that leaves CTAs idle are split where that saves more
+            // steps than the joining costs, in at most kF8MaxParts parts each.  (Many tokens, 4096
+            // to 12288: 512 of them, whose last 40 tiles of 32 steps could be of 9, 38 us whole and
+            // 50 split.  12288 to 4096: 4032, the last 56 tiles of 96 steps in parts of 35, 199
+            // us whole and 188 split.)
+            const int n = total * p.ntiles, ctas = gridDim.x, rest = n % ctas;
             const int units = rest * p.ksteps;
-            const int use = max(1, min(min(workers, rest * kF8MaxParts), units / P::MIN_STEPS));
+            const int use = max(1, min(min(ctas, rest * kF8MaxParts), units / P::MIN_STEPS));
             const bool split = rest > 0 && p.ksteps - (units + use - 1) / use >= P::JOIN_STEPS;
             cut.whole = split ? n - rest : n;
             cut.units = split ? units : 0;
@@ -415,59 +382,48 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
     }
     __syncthreads();
-    if constexpr (CTAS == 2) cluster_sync_all();     // barriers of both CTAs initialised
-    // columns of accumulator h of a tile: tokens, or weight rows, rounded up to 16 (one
-    // without any still takes part, and nothing of it is stored)
+    // weight rows of a tile, and columns of its accumulator h: tokens, or weight rows, rounded
+    // up to 16 (one without any still takes part, and nothing of it is stored)
+    auto tile_rows = [&](const F8Seg &sg) { return min(p.ycols, p.N - sg.ntile * p.ycols); };
     auto mma_n = [&](const F8Seg &sg, int h) {
-        const int n = P::WIDE ? min(P::ACC_COLS, p.N - sg.ntile * p.ycols - h * P::ACC_COLS) : sg.cols;
+        const int n = P::WIDE ? min(P::ACC_COLS, tile_rows(sg) - h * P::ACC_COLS) : sg.cols;
         return (max(n, 1) + 15) / 16 * 16;
     };
     // The copy warp's work on a tile: where its operands lie, and a step's copies into the
-    // stage s, the weights (with the bytes that are expected there; a pair's, in the even CTA)
-    // and the tokens.  Rows of a pair's tokens that are past the tile's are not loaded (what
-    // comes of them is not stored).  The N side comes in boxes: many tokens, one for each half
-    // that has columns, this CTA's share of them; few, as many as hold the tile's tokens.
+    // stage s, the weights (with the bytes that are expected there) and the tokens.  The N side
+    // comes in one box or two, as many as hold the tile's columns.
     struct Source {
-        int wrow[2], xrow, boxes;
+        int wrow, xrow, boxes;
         uint32_t bytes;
-        bool mine;
     };
     auto source = [&](const F8Seg &sg) {
         Source c;
-        c.boxes = P::WIDE ? (p.N - sg.ntile * p.ycols > P::ACC_COLS ? 2 : 1) : (sg.cols + P::B_BOX - 1) / P::B_BOX;
-        c.bytes = CTAS * c.boxes * P::B_BOX * kStepK + (P::WIDE ? (sg.cols > kRowsA ? 2 : 1) * kABytes : p.ycols * kStepK);
-        c.wrow[0] = c.wrow[1] = sg.e * p.N + sg.ntile * p.ycols;
-        if (P::WIDE)
-            for (int h = 0; h < 2; ++h) c.wrow[h] += h * P::ACC_COLS + rank * (mma_n(sg, h) / 2);
-        c.xrow = sg.m0 + (P::WIDE ? rank * kRowsA : 0);
-        c.mine = !P::WIDE || rank * kRowsA < sg.cols;
+        c.boxes = ((P::WIDE ? tile_rows(sg) : sg.cols) + P::B_BOX - 1) / P::B_BOX;
+        c.bytes = (c.boxes * P::B_BOX + (P::WIDE ? kRowsA : p.ycols)) * kStepK;
+        c.wrow = sg.e * p.N + sg.ntile * p.ycols;
+        c.xrow = sg.m0;
         return c;
     };
-    const uint32_t full_even = CTAS == 2 ? in_even_cta(full0) : full0, stage0 = smem_u32(smem);
+    const uint32_t stage0 = smem_u32(smem);
+    auto copy_a = [&](int s, int k, int row) { tma_load_2d(stage0 + s * P::STAGE, &tmA, k, row, full0 + 8 * s); };
+    auto copy_b = [&](int boxes, int s, int k, int row) {
+        const uint32_t at = stage0 + s * P::STAGE + kABytes;
+        tma_load_2d(at, &tmB, k, row, full0 + 8 * s);
+        if (boxes > 1) tma_load_2d(at + P::B_BOX * kStepK, &tmB, k, row + P::B_BOX, full0 + 8 * s);
+    };
     auto copy_weights = [&](const Source &c, int s, int k) {
-        const uint32_t at = stage0 + s * P::STAGE, bar = full_even + 8 * s;
-        if (rank == 0)
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full0 + 8 * s), "r"(c.bytes) : "memory");
-        if constexpr (P::WIDE) {
-            f8_copy<CTAS>(at + kABytes, &tmB, k, c.wrow[0], bar);
-            if (c.boxes > 1) f8_copy<CTAS>(at + kABytes + P::B_BOX * kStepK, &tmB, k, c.wrow[1], bar);
-        } else {
-            f8_copy<CTAS>(at, &tmA, k, c.wrow[0], bar);
-        }
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full0 + 8 * s), "r"(c.bytes) : "memory");
+        if constexpr (P::WIDE) copy_b(c.boxes, s, k, c.wrow);
+        else copy_a(s, k, c.wrow);
     };
     auto copy_tokens = [&](const Source &c, int s, int k) {
-        const uint32_t at = stage0 + s * P::STAGE, bar = full_even + 8 * s;
-        if constexpr (P::WIDE) {
-            if (c.mine) f8_copy<CTAS>(at, &tmA, k, c.xrow, bar);
-        } else {
-            f8_copy<CTAS>(at + kABytes, &tmB, k, c.xrow, bar);
-            if (c.boxes > 1) f8_copy<CTAS>(at + kABytes + P::B_BOX * kStepK, &tmB, k, c.xrow + P::B_BOX, bar);
-        }
+        if constexpr (P::WIDE) copy_a(s, k, c.xrow);
+        else copy_b(c.boxes, s, k, c.xrow);
     };
     uint32_t early = 0;                  // steps whose weights were asked for before the wait
     if (!p.offsets) {
         if (warp == DRAIN + P::ISSUERS && lane == 0) {
-            F8Iter<CTAS> iter(cut);
+            F8Iter iter(cut);
             F8Seg sg;
             if (iter.next(cut, list, p, sg)) {
                 const Source c = source(sg);
@@ -479,19 +435,12 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         pdl_wait();
     }
     if (warp == DRAIN) {
-        if constexpr (CTAS == 2) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                         ::"r"(smem_u32(&tmem_base_sh)), "r"(static_cast<uint32_t>(P::TMEM)));
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                         ::"r"(smem_u32(&tmem_base_sh)), "r"(static_cast<uint32_t>(P::TMEM)));
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        }
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&tmem_base_sh)), "r"(static_cast<uint32_t>(P::TMEM)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if constexpr (CTAS == 2) cluster_sync_all();     // TMEM of both CTAs allocated
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = tmem_base_sh;
     pdl_launch_dependents();
@@ -500,17 +449,17 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::OTHER_REGS));
         if (warp < DRAIN + P::ISSUERS) {
             // -------------------------------------------- MMA issue (one thread a warp)
-            if (rank == 0 && lane == 0) {
+            if (lane == 0) {
                 const int h = (warp - DRAIN) % HALVES;
                 const uint32_t turn = (warp - DRAIN) / HALVES;
                 uint32_t it = 0, mine = turn;            // mine: the next step of this thread's
                 F8Ring<STAGES> at;
                 at.on(turn);
-                F8Iter<CTAS> iter(cut);
+                F8Iter iter(cut);
                 F8Seg sg;
                 while (!abort_sh && iter.next(cut, list, p, sg)) {
-                    // D fp32, A and B e4m3, K-major, M = 128 a CTA
-                    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(mma_n(sg, h) >> 3) << 17) | (CTAS * 8u << 24);
+                    // D fp32, A and B e4m3, K-major, M = 128
+                    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(mma_n(sg, h) >> 3) << 17) | (8u << 24);
                     const uint32_t end = it + sg.k1 - sg.k0;
                     for (; mine < end; mine += P::IN_TURN, at.on(P::IN_TURN)) {
                         const int a = (mine % TURNS) * HALVES + h;
@@ -519,20 +468,16 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const uint32_t d = tmem + static_cast<uint32_t>(P::ACC_COLS * a);
                         const uint64_t ad = f8_desc(stage0 + at.s * P::STAGE);
-                        const uint64_t bd = f8_desc(stage0 + at.s * P::STAGE + kABytes + h * (P::ACC_COLS / CTAS) * kStepK);
+                        const uint64_t bd = f8_desc(stage0 + at.s * P::STAGE + kABytes + h * P::ACC_COLS * kStepK);
 #pragma unroll
-                        for (int kk = 0; kk < kStepK / 32; ++kk) f8_mma<CTAS>(d, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
-                        f8_commit<CTAS>(acc_full0 + 8 * a);
-                        f8_commit<CTAS>(empty0 + 8 * at.s);
+                        for (int kk = 0; kk < kStepK / 32; ++kk) f8_mma(d, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0);
+                        f8_commit(acc_full0 + 8 * a);
+                        f8_commit(empty0 + 8 * at.s);
                     }
                     it = end;
                 }
                 // let every issued MMA finish before the TMEM is released
-                if constexpr (CTAS == 2)
-                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                                 ::"r"(done) : "memory");
-                else
-                    f8_commit<CTAS>(done);
+                f8_commit(done);
                 const long long t0 = clock64();
                 while (!f8_try(done, 0) && clock64() - t0 < kF8WaitLimit) {
                 }
@@ -542,9 +487,9 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (lane == 0) {
                 uint32_t it = 0;
                 F8Ring<STAGES> at;
-                F8Iter<CTAS> iter(cut);
+                F8Iter iter(cut);
                 F8Seg sg;
-                while (!abort_sh && iter.next(cut, list, p, sg)) {
+                while ((it < early || !abort_sh) && iter.next(cut, list, p, sg)) {
                     const Source c = source(sg);
                     for (int k = sg.k0 * kStepK; k < sg.k1 * kStepK; k += kStepK, ++it, at.on(1)) {
                         if (!f8_wait(empty0 + 8 * at.s, at.round ^ 1u, &abort_sh, p.status)) break;
@@ -553,7 +498,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     }
                 }
                 // after a wait ran out: the copies in flight land before the CTA leaves
-                if (abort_sh && rank == 0)
+                if (abort_sh)
                     for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j) {
                         const long long t0 = clock64();
                         while (!f8_try(full0 + 8 * (j % STAGES), (j / STAGES) & 1) &&
@@ -565,19 +510,20 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             // -------------------------------------------- scales
             // Each step's sx * sw into its slot, loaded AHEAD steps before.  Many tokens: this CTA's
             // tokens with the first scale block of columns, then with the second.  Few: sx of each
-            // token, and sw of the tile's first block of weight rows and the next.  (Places past the tile's rows or N take their last one's; what
-            // comes of them is not stored.)  A slot is free again 2 * TURNS steps later: step
-            // it - TURNS has its sums only after step it - 2 * TURNS was drained.
+            // token, and sw of the tile's first block of weight rows and the next.  (Places past the
+            // tile's rows or N take their last one's; what comes of them is not stored.)  A slot is
+            // free again 2 * TURNS steps later: step it - TURNS has its sums only after step
+            // it - 2 * TURNS was drained.
             constexpr int SC = P::SCALERS, AHEAD = 2, EACH = P::WIDE ? 4 : P::TOKENS / 32;
             const int turn = warp - (DRAIN + P::ISSUERS + 1);
             uint32_t it = 0;
-            F8Iter<CTAS> iter(cut);
+            F8Iter iter(cut);
             F8Seg sg;
             while (__all_sync(0xffffffffu, !abort_sh) && iter.next(cut, list, p, sg)) {
                 const int skip = (turn + SC - static_cast<int>(it % SC)) % SC;      // steps until this warp's first
                 int off[EACH];
 #pragma unroll
-                for (int i = 0; i < EACH; ++i) off[i] = min(rank * kRowsA + lane + 32 * i, sg.cols - 1);
+                for (int i = 0; i < EACH; ++i) off[i] = min(lane + 32 * i, sg.cols - 1);
                 const int nb = sg.ntile * p.ycols / 128;
                 const float *sx = p.sx + (sg.k0 + skip) * p.M + sg.m0;
                 const float *sw = p.sw + (static_cast<int64_t>(sg.e) * p.nblocks + nb) * p.ksteps + sg.k0 + skip;
@@ -638,30 +584,24 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         uint32_t sums = 0;                               // tiles whose sums the sets have put together
         const int h = c0 / P::ACC_COLS;                  // the accumulator it drains
         const uint32_t lanes = (static_cast<uint32_t>(q * 32) << 16) + c0 % P::ACC_COLS;
-        const uint32_t acc_empty_even = CTAS == 2 ? in_even_cta(acc_empty0) : acc_empty0;
         const float *scales = reinterpret_cast<const float *>(smem + P::OFF_SCALES) +
                               (P::WIDE ? c0 / 128 * 128 + q * 32 + lane : c0);
         // an accumulator has been read
         auto hand_back = [&](int a) {
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
-            if (lane == 0) {
-                if constexpr (CTAS == 2)
-                    arrive_cluster(acc_empty_even + 8 * a);
-                else
-                    mbar_arrive_local(acc_empty0 + 8 * a);
-            }
+            if (lane == 0) mbar_arrive_local(acc_empty0 + 8 * a);
         };
         uint32_t it = 0;
-        F8Iter<CTAS> iter(cut);
+        F8Iter iter(cut);
         F8Seg sg;
         // the warp acts as one: a lane that saw an abort takes the others along
         while (__all_sync(0xffffffffu, !abort_sh) && iter.next(cut, list, p, sg)) {
-            const int n0 = sg.ntile * p.ycols, row = rank * kRowsA + q * 32;    // row: of this warp, on the M side
+            const int n0 = sg.ntile * p.ycols, row = q * 32;      // row: of this warp, on the M side
             static_assert(!P::WIDE || P::SCALES == P::NCOLS, "a scale a token and half");
-            const int rows_left = (P::WIDE ? sg.cols : min(p.ycols, p.N - n0)) - row;
+            const int rows_left = (P::WIDE ? sg.cols : tile_rows(sg)) - row;
             const int block = P::TOKENS + (n0 + row + lane) / 128 - n0 / 128;   // few tokens: where this lane's sw is
-            const int cols_left = (P::WIDE ? p.N - n0 : sg.cols) - c0;
+            const int cols_left = (P::WIDE ? tile_rows(sg) : sg.cols) - c0;
             const bool some = rows_left > 0 && cols_left > 0;            // this warp has some of the tile
             const int groups = some ? min(GROUPS, (cols_left + 15) / 16) : 0;
             float acc[GROUPS][16];
@@ -749,14 +689,72 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 __syncwarp();
                 if (lane == 0) mbar_arrive_local(sum_empty0 + 8 * q);
             }
+            // ---- Y of many tokens: a lane has 32 columns of a token.  64 bytes of each of the
+            // warp's 32 rows at a time go through shared memory, so that four lanes store a row's 64
+            // bytes.  A row's chunk c lies at c ^ (row / 2 % 4): no two of eight rows in one bank.
+            unsigned char *turn = smem + P::OFF_OUT + warp * 32 * 64;
+            const int esize = p.ytype == 0 ? 4 : 2, piece = 16 / esize;
+            unsigned char *y = static_cast<unsigned char *>(p.Y) +
+                               ((static_cast<int64_t>(sg.m0) + row + (lane >> 2)) * p.ldy + n0 + c0 + (lane & 3) * piece) * esize;
+            auto turn_out = [&](const uint4 (&u)[4], int col) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4 *>(turn + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = u[j];
+                __syncwarp();
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = r * 8 + (lane >> 2), left = cols_left - col - (lane & 3) * piece;
+                    if (at >= rows_left || left <= 0) continue;
+                    const uint4 o = *reinterpret_cast<const uint4 *>(turn + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4));
+                    unsigned char *to = y + (static_cast<int64_t>(r) * 8 * p.ldy + col) * esize;
+                    if (p.vec && left >= piece) {
+                        *reinterpret_cast<uint4 *>(to) = o;
+                    } else {
+                        const uint32_t h[4] = {o.x, o.y, o.z, o.w};
+                        if (esize == 4) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (j < left) reinterpret_cast<uint32_t *>(to)[j] = h[j];
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (j < left)
+                                    reinterpret_cast<uint16_t *>(to)[j] = static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1)));
+                        }
+                    }
+                }
+            };
+            auto store = [&](const float (&x0)[16], const float (&x1)[16], int col) {
+                uint4 u[4];
+                if (p.ytype == 0) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float *x = half ? x1 : x0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            u[j] = make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                                              __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
+                        turn_out(u, col + 16 * half);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float *x = (j < 2 ? x0 : x1) + 8 * (j & 1);
+                        u[j] = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]),
+                                          bf16_pair(x[6], x[7]));
+                    }
+                    turn_out(u, col);
+                }
+            };
             if (!sg.whole) {
                 // store the part; the warp that comes last adds all parts in order
-                auto part = [&](int worker) {
+                auto part = [&](int cta) {
                     return reinterpret_cast<float2 *>(
-                               p.parts + ((static_cast<int64_t>(worker) * 2 + (worker == sg.first ? 1 : 0)) * CTAS + rank) * P::PART) +
+                               p.parts + (static_cast<int64_t>(cta) * 2 + (cta == sg.first ? 1 : 0)) * P::PART) +
                            static_cast<int64_t>(warp) * GROUPS * 8 * 32 + lane;
                 };
-                float2 *to = part(F8Iter<CTAS>::me());
+                float2 *to = part(blockIdx.x);
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g)
                     if (g < groups)
@@ -764,102 +762,52 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         for (int i = 0; i < 8; ++i) __stcg(to + (g * 8 + i) * 32, make_float2(acc[g][2 * i], acc[g][2 * i + 1]));
                 __threadfence();
                 __syncwarp();
-                unsigned int *counter = p.counters + (sg.first * CTAS + rank) * kF8MaxDrain + warp;
+                unsigned int *counter = p.counters + sg.first * kF8MaxDrain + warp;
                 unsigned int before = 0;
                 if (lane == 0) before = atomicAdd(counter, 1u);
                 before = __shfl_sync(0xffffffffu, before, 0);
                 if (before != static_cast<unsigned int>(sg.last - sg.first)) continue;
                 __threadfence();
                 if (lane == 0) *counter = 0u;
-                // (a few columns of two parts at a time: half the trips to memory)
+                // (what bounds the join is its trips to memory: as many columns and parts at a
+                // time as there are registers for)
+                constexpr int PARTS = P::WIDE ? 3 : 2, CHUNK = P::WIDE ? 2 : 1;
 #pragma unroll
-                for (int g = 0; g < GROUPS; ++g) {
+                for (int g = 0; g < GROUPS; g += CHUNK) {
                     if (g >= groups) break;
+                    float sum[CHUNK][16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[g][i] = 0.0f;
-                    for (int p0 = sg.first; p0 <= sg.last; p0 += 2) {
-                        const float2 *one = part(p0) + g * 8 * 32, *two = part(min(p0 + 1, sg.last)) + g * 8 * 32;
-                        float2 v[8], u[8];
+                    for (int i = 0; i < CHUNK * 16; ++i) sum[i / 16][i % 16] = 0.0f;
+                    for (int p0 = sg.first; p0 <= sg.last; p0 += PARTS) {
+                        float2 v[PARTS][CHUNK * 8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            v[i] = __ldcg(one + i * 32);
-                            u[i] = __ldcg(two + i * 32);
+                        for (int j = 0; j < PARTS; ++j) {
+                            const float2 *from = part(min(p0 + j, sg.last)) + g * 8 * 32;
+#pragma unroll
+                            for (int i = 0; i < CHUNK * 8; ++i) v[j][i] = __ldcg(from + i * 32);
                         }
-                        const bool both = p0 < sg.last;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            acc[g][2 * i] += v[i].x;
-                            acc[g][2 * i + 1] += v[i].y;
-                            if (both) {
-                                acc[g][2 * i] += u[i].x;
-                                acc[g][2 * i + 1] += u[i].y;
-                            }
-                        }
+                        for (int j = 0; j < PARTS; ++j)
+                            if (p0 + j <= sg.last)
+#pragma unroll
+                                for (int i = 0; i < CHUNK * 8; ++i) {
+                                    sum[i / 8][i % 8 * 2] += v[j][i].x;
+                                    sum[i / 8][i % 8 * 2 + 1] += v[j][i].y;
+                                }
+                    }
+                    if constexpr (P::WIDE) {
+                        store(sum[0], sum[CHUNK - 1], 16 * g);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[g][i] = sum[0][i];
                     }
                 }
+                if (P::WIDE) continue;
             }
             if constexpr (P::WIDE) {
-                // ---- Y: a lane has a token's columns; 64 bytes of each of the warp's 32 rows at a
-                // time go through shared memory, so that four lanes store a row's 64 bytes.  A
-                // row's chunk c lies at c ^ (row / 2 % 4): no two of eight rows in one bank.
-                unsigned char *turn = smem + P::OFF_OUT + warp * 32 * 64;
-                const int esize = p.ytype == 0 ? 4 : 2, piece = 16 / esize;
-                unsigned char *y = static_cast<unsigned char *>(p.Y) +
-                                   ((static_cast<int64_t>(sg.m0) + row + (lane >> 2)) * p.ldy + n0 + c0 + (lane & 3) * piece) * esize;
-                auto turn_out = [&](const uint4 (&u)[4], int col) {
-                    __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4 *>(turn + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = u[j];
-                    __syncwarp();
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int at = r * 8 + (lane >> 2), left = cols_left - col - (lane & 3) * piece;
-                        if (at >= rows_left || left <= 0) continue;
-                        const uint4 o = *reinterpret_cast<const uint4 *>(turn + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4));
-                        unsigned char *to = y + (static_cast<int64_t>(r) * 8 * p.ldy + col) * esize;
-                        if (p.vec && left >= piece) {
-                            *reinterpret_cast<uint4 *>(to) = o;
-                        } else {
-                            const uint32_t h[4] = {o.x, o.y, o.z, o.w};
-                            if (esize == 4) {
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    if (j < left) reinterpret_cast<uint32_t *>(to)[j] = h[j];
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    if (j < left)
-                                        reinterpret_cast<uint16_t *>(to)[j] = static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1)));
-                            }
-                        }
-                    }
-                };
-                if (p.ytype == 0) {
-#pragma unroll
-                    for (int g = 0; g < GROUPS; ++g) {
-                        if (g >= groups) break;
-                        uint4 u[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            u[j] = make_uint4(__float_as_uint(acc[g][4 * j]), __float_as_uint(acc[g][4 * j + 1]),
-                                              __float_as_uint(acc[g][4 * j + 2]), __float_as_uint(acc[g][4 * j + 3]));
-                        turn_out(u, 16 * g);
-                    }
-                } else {
-#pragma unroll
-                    for (int g = 0; g < GROUPS; g += 2) {
-                        if (g >= groups) break;
-                        uint4 u[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float *x = acc[g + (j >> 1)] + 8 * (j & 1);
-                            u[j] = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]),
-                                              bf16_pair(x[6], x[7]));
-                        }
-                        turn_out(u, 16 * g);
-                    }
-                }
+                for (int g = 0; g < GROUPS; g += 2)
+                    if (g < groups) store(acc[g], acc[g + 1], 16 * g);
             } else {
                 // ---- Y: this lane's column n of tokens c0, c0 + 1, ...
                 const int n = n0 + row + lane, n_end = min(p.N, n0 + p.ycols);
@@ -908,32 +856,24 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
         }
     }
-    // Nobody leaves while the peer may still arrive on this CTA's barriers; the MMAs in
-    // flight have ended (their issuers waited for them above).
+    // (The MMAs in flight have ended: their issuers waited for them above.)
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
-    if constexpr (CTAS == 2) cluster_sync_all();
     if (warp == DRAIN) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if constexpr (CTAS == 2)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                         "r"(static_cast<uint32_t>(P::TMEM)));
-        else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                         "r"(static_cast<uint32_t>(P::TMEM)));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(P::TMEM)));
     }
 }
 
-// (a worker is a pair or a CTA: as many CTAs as SMs in both forms)
 constexpr size_t f8_counter_bytes(int ctas) {
     return (static_cast<size_t>(ctas) * kF8MaxDrain * 4 + 255) / 256 * 256;
 }
 
 template <bool WIDE>
-tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
+tq_status launch_f8(const F8Product &f, int ycols, const DeviceInfo &dev, cudaStream_t s) {
     using P = F8Plan<WIDE>;
     auto kern = k_linear_f8<P>;
-    if (dev.id < 0 || dev.id >= 64 || dev.sms < P::CTAS) return TQ_ERR_DEVICE;
+    if (dev.id < 0 || dev.id >= 64 || dev.sms < 1) return TQ_ERR_DEVICE;
     static bool configured[64] = {false};
     if (!configured[dev.id]) {
         cudaFuncAttributes at;
@@ -955,7 +895,7 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     p.N = static_cast<int>(f.N);
     p.ksteps = static_cast<int>((f.K + kStepK - 1) / kStepK);
     p.nblocks = static_cast<int>((f.N + 127) / 128);
-    p.ycols = P::YCOLS;
+    p.ycols = ycols;
     if (!WIDE && !f.offsets) {
         // Few tokens of one matrix: tiles of 128 rows, the steps of the last round split, or tiles
         // of fewer rows, as many as CTAs.  A step of r rows takes about 3 r ns (what an SM draws
@@ -995,19 +935,17 @@ tq_status launch_f8(const F8Product &f, const DeviceInfo &dev, cudaStream_t s) {
     if (token_tiles * p.ntiles > (1ll << 30)) return TQ_ERR_OVERFLOW;
     const int64_t tiles = token_tiles * p.ntiles, parts = p.ksteps / P::MIN_STEPS;
     const int64_t pieces = tiles * (parts < 1 ? 1 : (parts < kF8MaxParts ? parts : kF8MaxParts));
-    const int64_t most = dev.sms / P::CTAS, workers = pieces < 1 ? 1 : (pieces < most ? pieces : most);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {static_cast<unsigned>(P::CTAS), 1u, 1u};
+    const int64_t ctas = pieces < 1 ? 1 : (pieces < dev.sms ? pieces : dev.sms);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(workers * P::CTAS));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(P::THREADS);
     cfg.dynamicSmemBytes = static_cast<size_t>(P::smem(p.experts));
     cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = P::CTAS == 2 ? 2 : 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, WIDE ? tmX : tmW, WIDE ? tmW : tmX, p);
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
@@ -1019,16 +957,20 @@ size_t f8_workspace_bytes(const DeviceInfo &dev) {
     return f8_counter_bytes(dev.sms) + static_cast<size_t>(dev.sms) * 2 * F8Plan<true>::PART;
 }
 
-// The form with the fewer steps, a step of 256 x 256 taken as 11 and one of 64 x 128 as 8
-// (measured: 0.55 and 0.38 us), with rows spread evenly over the experts.
+// The form that takes the least time by rounds of tiles and the time of a step in 10 ns, with
+// rows spread evenly over the experts; the weights of a lone tile come from the DRAM.  Measured with 4096 to 12288: 48 tokens 16.6 us (few)
+// and 19.9 (many, 128 columns); 65: 33.7, 19.6 and with 256 columns 21.5; 256: 49, 34.5 and
+// 21.5; 512: 92, 49 and 37.5.  64 experts of about two rows each, 2048 x 2048: 41 (few) and
+// 51 (256 columns); 16 rows: 50, 71 and 53; 64 rows: 91, 73 and 57.
 tq_status launch_linear_f8(const F8Product &p, const DeviceInfo &dev, cudaStream_t s) {
     const int64_t experts = p.offsets ? (p.experts < p.M ? p.experts : p.M) : 1, rows = (p.M + experts - 1) / experts;
-    auto cost = [&](int64_t tokens, int64_t cols, int64_t workers, int64_t step) {
-        const int64_t tiles = experts * ((rows + tokens - 1) / tokens) * ((p.N + cols - 1) / cols);
-        return (tiles + workers - 1) / workers * step;
+    auto cost = [&](int64_t tokens, int64_t cols, int64_t lone, int64_t other) {
+        const int64_t token_tiles = (rows + tokens - 1) / tokens, tiles = experts * token_tiles * ((p.N + cols - 1) / cols);
+        return (tiles + dev.sms - 1) / dev.sms * (token_tiles == 1 ? lone : other);
     };
-    return cost(64, 128, dev.sms, 8) <= cost(256, 256, dev.sms / 2, 11) ? launch_f8<false>(p, dev, s)
-                                                                      : launch_f8<true>(p, dev, s);
+    const int64_t few = cost(64, 128, 36 + rows / 4, 52), half = cost(128, 128, 62, 52), many = cost(128, 256, 80, 60);
+    if (few <= half && few <= many) return launch_f8<false>(p, 128, dev, s);
+    return launch_f8<true>(p, half < many ? 128 : 256, dev, s);
 }
 
 }  // namespace tq
