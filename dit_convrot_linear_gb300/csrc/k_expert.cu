@@ -14,19 +14,19 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 // ------------------------------------------------------------ the router
 
-// Order of logits as unsigned numbers: 0 for -inf (never chosen), all bits set for
-// NaN (chosen first: the row's weights come out as NaN, not as a quiet choice).  The
-// two zeros are equal.
+// Order of logits as unsigned numbers: 0 for -inf (never chosen), NaN above +inf (chosen
+// first: the row's weights come out as NaN, not as a quiet choice).  The addition makes
+// the two zeros one, and all NaN (a sum's is 0x7FFFFFFF).
+constexpr uint32_t kLowest = 0x007FFFFFu;        // -inf, as the others before it is subtracted
+
 __device__ __forceinline__ uint32_t logit_key(float x) {
-    const uint32_t b = __float_as_uint(x + 0.0f);
-    if (x != x) return 0xFFFFFFFFu;
-    if (b == 0xFF800000u) return 0u;
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    const int b = __float_as_int(x + 0.0f);
+    return (static_cast<uint32_t>(b) ^ (static_cast<uint32_t>(b >> 31) | 0x80000000u)) - kLowest;
 }
 
 __device__ __forceinline__ float key_logit(uint32_t key) {
-    if (key == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
-    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+    const uint32_t b = key + kLowest;
+    return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -43,41 +43,32 @@ __device__ __forceinline__ float load_logit(const L *p) {
         return bf16_bits_to_f32(__ldg(p));
 }
 
-// Puts the larger of two (key, expert) first; among equals the lower expert.
-__device__ __forceinline__ void order(uint32_t &ka, int &ea, uint32_t &kb, int &eb) {
-    const bool swap = kb > ka || (kb == ka && eb < ea);
-    const uint32_t k = swap ? kb : ka;
-    const int e = swap ? eb : ea;
-    kb = swap ? ka : kb;
-    eb = swap ? ea : eb;
-    ka = k;
-    ea = e;
-}
-
-// A warp a token; lane l holds experts l, l + 32, ..., sorted (a bitonic network).
-// Each choice is two warp reductions over the lanes' first ones: the largest key,
-// then the lowest expert that has it.
+// A warp a token; lane l holds experts l, l + 32, ...  The k-th largest of the lanes'
+// largest keys is no larger than the k-th key: what reaches it is brought together in
+// shared memory, a key a lane in the order of the experts (usually k to 2 k are), and
+// each choice is the largest of them, of the lowest lane that has it.  Where more than
+// 32 reach it each choice looks through all keys.  Bound by the instructions: 16384
+// tokens, 8 of 256 experts 10.4 us (13.9 with each lane's keys sorted instead); the
+// logits' 17 MB take 2.5 at the copy rate.
 template <typename L, int NI>
 __global__ void __launch_bounds__(256) k_expert_topk(const L *__restrict__ X, int64_t T, int E, int64_t ld, int k,
                                                      int renorm, int32_t *__restrict__ ids,
                                                      float *__restrict__ weights) {
+    __shared__ uint2 found_sh[8][32];
     const int lane = threadIdx.x & 31;
+    uint2 *found = found_sh[threadIdx.x >> 5];
     const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
     pdl_wait();
     pdl_launch_dependents();
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += step) {
-        uint32_t key[NI];
-        int ex[NI];
+        const L *x = X + t * ld + lane;
+        uint32_t key[NI], most = 0u;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            ex[i] = lane + 32 * i;
-            key[i] = ex[i] < E ? logit_key(load_logit(X + t * ld + ex[i])) : 0u;
-        }
+        for (int i = 0; i < NI; ++i) key[i] = lane + 32 * i < E ? logit_key(load_logit(x + 32 * i)) : 0u;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) most = max(most, key[i]);
         // the softmax over all experts is relative to the largest logit
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) top = max(top, key[i]);
-        top = __reduce_max_sync(kAll, top);
+        const uint32_t top = __reduce_max_sync(kAll, most);
         float all = 0.0f;
         if (!renorm) {
 #pragma unroll
@@ -85,58 +76,74 @@ __global__ void __launch_bounds__(256) k_expert_topk(const L *__restrict__ X, in
                 if (key[i] != 0u) all += expf(key_logit(key[i]) - key_logit(top));
             all = warp_sum(all);
         }
-        if constexpr (NI <= 8) {
+        uint32_t mine = key[0];                  // one of those that may be chosen, of expert at
+        int at = lane, many = 0;
+        if constexpr (NI > 1) {
+            uint32_t bound = top;
+            for (int n = 0; bound != 0u;) {
+                n += __popc(__ballot_sync(kAll, most == bound));
+                if (n >= k) break;
+                if (most == bound) most = 0u;
+                bound = __reduce_max_sync(kAll, most);
+            }
+            bound = max(bound, 1u);
 #pragma unroll
-            for (int size = 2; size <= NI; size <<= 1)
-#pragma unroll
-                for (int gap = size >> 1; gap > 0; gap >>= 1)
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if ((i & gap) == 0) {
-                            if ((i & size) == 0 || size == NI)
-                                order(key[i], ex[i], key[i | gap], ex[i | gap]);
-                            else
-                                order(key[i | gap], ex[i | gap], key[i], ex[i]);
-                        }
+            for (int i = 0; i < NI; ++i) {
+                const uint32_t b = __ballot_sync(kAll, key[i] >= bound);
+                const int to = many + __popc(b & ((1u << lane) - 1u));
+                if (key[i] >= bound && to < 32) found[to] = make_uint2(key[i], lane + 32 * i);
+                many += __popc(b);
+            }
+            __syncwarp();
+            const uint2 f = found[lane];
+            mine = lane < many ? f.x : 0u;
+            at = static_cast<int>(f.y);
+            __syncwarp();                        // the next token's
         }
-        uint32_t chosen = 0u;                    // key of this lane's choice
-        int id = -1;
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = key[0];
-            int at = ex[0];
-            if constexpr (NI > 8) {
+        int id = -1, rank = lane;                // this lane's choice, and which one it is
+        uint32_t chosen = 0u;
+        if (many <= 32) {
+            int j = 0;
+            for (rank = k; j < k; ++j) {
+                const uint32_t win = __reduce_max_sync(kAll, mine);
+                if (win == 0u) break;            // nothing left that may be chosen
+                if (lane == __ffs(__ballot_sync(kAll, mine == win)) - 1) {
+                    chosen = win;
+                    id = at;
+                    rank = j;
+                    mine = 0u;
+                }
+            }
+            // places without a choice, one a lane
+            const uint32_t none = __ballot_sync(kAll, rank == k);
+            if (rank == k) rank = j + __popc(none & ((1u << lane) - 1u));
+        } else {
+            for (int j = 0; j < k; ++j) {
+                uint32_t best = key[0];
+                int e = lane;
 #pragma unroll
                 for (int i = 1; i < NI; ++i)
                     if (key[i] > best) {
                         best = key[i];
-                        at = ex[i];
+                        e = lane + 32 * i;
                     }
-            }
-            const uint32_t win = __reduce_max_sync(kAll, best);
-            if (win == 0u) break;                // nothing left that may be chosen
-            const int e = static_cast<int>(__reduce_min_sync(kAll, best == win ? static_cast<uint32_t>(at) : 0xFFFFu));
-            if constexpr (NI > 8) {
+                const uint32_t win = __reduce_max_sync(kAll, best);
+                if (win == 0u) break;
+                e = static_cast<int>(__reduce_min_sync(kAll, best == win ? static_cast<uint32_t>(e) : 0xFFFFu));
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
-                    if (ex[i] == e) key[i] = 0u;
-            } else if (at == e) {
-#pragma unroll
-                for (int i = 0; i + 1 < NI; ++i) {
-                    key[i] = key[i + 1];
-                    ex[i] = ex[i + 1];
+                    if (lane + 32 * i == e) key[i] = 0u;
+                if (lane == j) {
+                    id = e;
+                    chosen = win;
                 }
-                key[NI - 1] = 0u;
-            }
-            if (lane == j) {
-                id = e;
-                chosen = win;
             }
         }
         const float w = id >= 0 ? expf(key_logit(chosen) - key_logit(top)) : 0.0f;
         if (renorm) all = warp_sum(w);
-        if (lane < k) {
-            ids[t * k + lane] = id;
-            weights[t * k + lane] = id >= 0 ? w / all : 0.0f;
+        if (rank < k) {
+            ids[t * k + rank] = id;
+            weights[t * k + rank] = id >= 0 ? w / all : 0.0f;
         }
     }
 }
@@ -144,12 +151,18 @@ __global__ void __launch_bounds__(256) k_expert_topk(const L *__restrict__ X, in
 // dlogits of the weights' gradients dw.  With the chosen ones' own softmax w:
 //   w_i (dw_i - sum_j w_j dw_j) at the chosen, 0 elsewhere;
 // with the softmax p over all experts: p_e (dw at e - sum_j p_j dw_j).
+// 16384 tokens, 8 of 256 experts, fp32: 8.3 us (10.2 with a look at each choice for each
+// logit in place of the trip through shared memory), 5.0 at the copy rate.
 template <typename L, int NI>
 __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ X, int64_t T, int E, int64_t ld,
                                                           const int32_t *__restrict__ ids,
                                                           const float *__restrict__ dw, int k, int renorm,
                                                           L *__restrict__ dX, int64_t ldd, unsigned int *status) {
+    __shared__ float at_sh[8][32 * NI];           // the chosen experts' part of dlogits, 0 at the others
     const int lane = threadIdx.x & 31;
+    float *at = at_sh[threadIdx.x >> 5];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) at[lane + 32 * i] = 0.0f;
     const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
     pdl_wait();
     pdl_launch_dependents();
@@ -167,13 +180,12 @@ __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ 
                 v = load_logit(X + t * ld + id);
             }
         }
-        float x[NI], g[NI];
+        float x[NI];
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int e = lane + 32 * i;
             x[i] = !renorm && e < E ? load_logit(X + t * ld + e) : -INFINITY;
-            g[i] = 0.0f;
             top = x[i] > top || x[i] != x[i] ? x[i] : top;
         }
         if (renorm && id >= 0) top = v;
@@ -194,22 +206,32 @@ __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ 
         w *= inv;
         const float mean = warp_sum(w * d);
         const float part = renorm ? w * (d - mean) : d;
-        for (int j = 0; j < k; ++j) {
-            const int e = __shfl_sync(kAll, id, j);
-            const float c = __shfl_sync(kAll, part, j);
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (lane + 32 * i == e) g[i] += c;
+        // (one that ids has twice gets both parts, in their order)
+        const bool once = __match_any_sync(kAll, id) == 1u << lane;
+        __syncwarp();
+        if (__all_sync(kAll, once || id < 0)) {
+            if (id >= 0) at[id] = part;
+        } else {
+            for (int j = 0; j < k; ++j) {
+                if (lane == j && id >= 0) at[id] += part;
+                __syncwarp();
+            }
         }
+        __syncwarp();
+        float r[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) r[i] = at[lane + 32 * i];
+        __syncwarp();
+        if (id >= 0) at[id] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int e = lane + 32 * i;
             if (e >= E) continue;
-            const float r = renorm ? g[i] : x[i] * inv * (g[i] - mean);
+            if (!renorm) r[i] = x[i] * inv * (r[i] - mean);
             if constexpr (sizeof(L) == 4)
-                dX[t * ldd + e] = r;
+                dX[t * ldd + e] = r[i];
             else
-                dX[t * ldd + e] = f32_to_bf16_bits(r);
+                dX[t * ldd + e] = f32_to_bf16_bits(r[i]);
         }
     }
 }
@@ -219,10 +241,11 @@ __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ 
 // A counting sort by one cluster.  Each warp counts the experts of its own piece of the
 // choices; the counts are summed over warps, CTAs (through distributed shared memory)
 // and experts; then each warp places its piece.  Pieces are in order, and so are the
-// choices within one, so equal experts stay in order.  Bound by the chain of the steps
-// (a vote among lanes, an update of a shared counter) of a warp: 131072 choices of 256
-// experts 9.5 us with eight CTAs, 311 with one; at 128 choices one CTA takes 3.0 us,
-// eight take 5.7.
+// choices within one, so equal experts stay in order.  131072 choices of 256 experts take
+// 10.8 us, more than half of it in the placing: a step of a warp's 32 choices stores to as
+// many sectors, one a cycle and SM.  Eight CTAs take twice as long, one 300 us; a second
+// kernel that scatters the tokens from all SMs 12.2; a match among the lanes in place of a
+// vote for each bit 15.8.  128 choices take 2.9 us by one CTA.
 constexpr int kSortWarps = 32, kSortCtas = 16, kSortAhead = 8;
 constexpr int64_t kSortOneCta = 2048;            // choices that one CTA sorts alone
 
@@ -234,11 +257,10 @@ __device__ __forceinline__ int remote_int(uint32_t addr, int cta) {
     return v;
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+template <int BITS>
 __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *__restrict__ ids, int64_t n, int k,
                                                                  int E, int32_t *__restrict__ offsets,
                                                                  int32_t *__restrict__ token,
@@ -287,7 +309,12 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
         }
         sum_cta[e] = sum;
     }
-    if (ctas > 1) cluster_barrier(); else __syncthreads();
+    if (ctas > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
     // a thread an expert (E <= 1024): choices of it in all CTAs, and in those before this one
     const int e = threadIdx.x;
     int all = 0, before = 0;
@@ -304,6 +331,8 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
             all = sum_cta[e];
         }
     }
+    __syncwarp();
+    if (ctas > 1) cluster_arrive();              // the other CTAs' counts have been read
     int s = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -329,11 +358,14 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
     }
     if (cta == 0 && threadIdx.x == 0) offsets[E] = total;
     __syncthreads();
-    const int bits = 32 - __clz(E);
+    // the choice's token: its number by k, a step of 32 at a time
+    const int by = 32 / k, over = 32 % k;
+    int tok = static_cast<int>((f0 + lane) / k), rest = static_cast<int>((f0 + lane) % k);
     walk([&](int64_t f, int e, int) {
         // the lanes with the same expert: a vote for each bit of its number
         uint32_t same = __ballot_sync(kAll, e >= 0);
-        for (int b = 0; b < bits; ++b) {
+#pragma unroll
+        for (int b = 0; b < BITS; ++b) {
             const bool one = (e >> b) & 1;
             const uint32_t v = __ballot_sync(kAll, one);
             same &= one ? v : ~v;
@@ -341,9 +373,15 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
         int at = -1;
         if (e >= 0) {
             at = base[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
-            token[at] = static_cast<int32_t>(f / k);
+            token[at] = tok;
         }
         if (f < f1) place[f] = at;
+        tok += by;
+        rest += over;
+        if (rest >= k) {
+            rest -= k;
+            ++tok;
+        }
         __syncwarp();
         if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
         __syncwarp();
@@ -351,7 +389,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
     for (int64_t i = total + static_cast<int64_t>(cta) * blockDim.x + threadIdx.x; i < n;
          i += static_cast<int64_t>(ctas) * blockDim.x)
         token[i] = -1;
-    if (ctas > 1) cluster_barrier();             // nobody leaves while its counts may still be read
+    if (ctas > 1) cluster_wait();                // nobody leaves while its counts may still be read
 }
 
 // ------------------------------------------------------------ rows there and back
@@ -583,13 +621,15 @@ tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, in
     unsigned int *status = status_word();
     if (!status || dev.id < 0 || dev.id >= 64) return TQ_ERR_DEVICE;
     const int bytes = static_cast<int>((kSortWarps * E + 2 * E) * 4);
+    auto kern = E <= 64 ? k_expert_sort<6> : (E <= 256 ? k_expert_sort<8> : k_expert_sort<10>);
     static bool configured[64] = {false};
     if (!configured[dev.id]) {
-        cudaError_t e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (kSortWarps + 2) * TQ_MAX_EXPERTS * 4);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k_expert_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return cuda_fail(e);
+        for (auto f : {k_expert_sort<6>, k_expert_sort<8>, k_expert_sort<10>}) {
+            cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (kSortWarps + 2) * TQ_MAX_EXPERTS * 4);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
         configured[dev.id] = true;
     }
     cudaLaunchAttribute attr[2];
@@ -605,7 +645,7 @@ tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, in
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_expert_sort, ids, T * k, k, static_cast<int>(E), offsets, token,
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ids, T * k, k, static_cast<int>(E), offsets, token,
                                              place, status);
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
