@@ -50,8 +50,23 @@ namespace {
 constexpr int kStepK = 128;               // K of a step: one scale block
 constexpr int kRowsA = 128;               // rows of the M side a CTA
 constexpr int kABytes = kRowsA * kStepK;  // a stage's M side
-constexpr long long kF8WaitLimit = 4000000000ll;   // clock cycles, about 2 s
-constexpr unsigned int kStatusF8Timeout = 64u;
+// Waits for operands are bounded by kF8WaitLimit clock cycles (about 2 s; a build for the
+// library's own tests sets TQ_TEST_WAIT_CYCLES), those for what is in flight once one ran
+// out by kF8LandLimit each.
+#ifdef TQ_TEST_WAIT_CYCLES
+constexpr long long kF8WaitLimit = TQ_TEST_WAIT_CYCLES;
+#else
+constexpr long long kF8WaitLimit = 4000000000ll;
+#endif
+constexpr long long kF8LandLimit = 250000000ll;
+// A build for the library's own tests expects bytes that no copy brings, so that no
+// stage completes and the waits run out, with every issued copy landed.
+#ifdef TQ_TEST_UNSET_BYTES
+constexpr uint32_t kF8Unset = TQ_TEST_UNSET_BYTES;
+#else
+constexpr uint32_t kF8Unset = 0;
+#endif
+constexpr unsigned int kStatusF8Timeout = 512u;
 
 template <bool WIDE_>
 struct F8Plan {
@@ -233,6 +248,11 @@ __device__ __forceinline__ void f8_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void f8_prefetch(const CUtensorMap *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
+}
+
 // A place in a ring of N stages and the parity of the round that fills it.
 template <int N>
 struct F8Ring {
@@ -313,7 +333,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     // What an earlier kernel wrote is read, and the workspace used, after pdl_wait; the TMEM
     // is taken then too (that kernel's CTAs may still need theirs), and the next kernel may
     // start once this one has its own.  One matrix's list of work needs nothing of that, and
-    // its weights may come before: they are no earlier kernel's output, or that one has ended.
+    // its first weights may come into L2 before (coherent: whoever writes them still may).
     if (p.offsets) pdl_wait();
     const int *list = reinterpret_cast<const int *>(smem + P::OFF_LIST);
     int *row0 = reinterpret_cast<int *>(smem + P::OFF_LIST), *rows = row0 + p.experts + 1, *tiles = rows + p.experts + 1;
@@ -399,7 +419,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     auto source = [&](const F8Seg &sg) {
         Source c;
         c.boxes = ((P::WIDE ? tile_rows(sg) : sg.cols) + P::B_BOX - 1) / P::B_BOX;
-        c.bytes = (c.boxes * P::B_BOX + (P::WIDE ? kRowsA : p.ycols)) * kStepK;
+        c.bytes = (c.boxes * P::B_BOX + (P::WIDE ? kRowsA : p.ycols)) * kStepK + kF8Unset;
         c.wrow = sg.e * p.N + sg.ntile * p.ycols;
         c.xrow = sg.m0;
         return c;
@@ -420,15 +440,16 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if constexpr (P::WIDE) copy_a(s, k, c.xrow);
         else copy_b(c.boxes, s, k, c.xrow);
     };
-    uint32_t early = 0;                  // steps whose weights were asked for before the wait
     if (!p.offsets) {
         if (warp == DRAIN + P::ISSUERS && lane == 0) {
             F8Iter iter(cut);
             F8Seg sg;
             if (iter.next(cut, list, p, sg)) {
                 const Source c = source(sg);
-                for (; early < STAGES && sg.k0 + static_cast<int>(early) < sg.k1; ++early)
-                    copy_weights(c, early, (sg.k0 + early) * kStepK);
+                for (int k = sg.k0; k < min(sg.k1, sg.k0 + STAGES); ++k) {
+                    f8_prefetch(P::WIDE ? &tmB : &tmA, k * kStepK, c.wrow);
+                    if (P::WIDE && c.boxes > 1) f8_prefetch(&tmB, k * kStepK, c.wrow + P::B_BOX);
+                }
             }
         }
         __syncwarp();
@@ -479,7 +500,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 // let every issued MMA finish before the TMEM is released
                 f8_commit(done);
                 const long long t0 = clock64();
-                while (!f8_try(done, 0) && clock64() - t0 < kF8WaitLimit) {
+                while (!f8_try(done, 0) && clock64() - t0 < kF8LandLimit) {
                 }
             }
         } else if (warp == DRAIN + P::ISSUERS) {
@@ -489,11 +510,11 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 F8Ring<STAGES> at;
                 F8Iter iter(cut);
                 F8Seg sg;
-                while ((it < early || !abort_sh) && iter.next(cut, list, p, sg)) {
+                while (!abort_sh && iter.next(cut, list, p, sg)) {
                     const Source c = source(sg);
                     for (int k = sg.k0 * kStepK; k < sg.k1 * kStepK; k += kStepK, ++it, at.on(1)) {
                         if (!f8_wait(empty0 + 8 * at.s, at.round ^ 1u, &abort_sh, p.status)) break;
-                        if (it >= early) copy_weights(c, at.s, k);
+                        copy_weights(c, at.s, k);
                         copy_tokens(c, at.s, k);
                     }
                 }
@@ -502,7 +523,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j) {
                         const long long t0 = clock64();
                         while (!f8_try(full0 + 8 * (j % STAGES), (j / STAGES) & 1) &&
-                               clock64() - t0 < kF8WaitLimit / 16) {
+                               clock64() - t0 < kF8LandLimit) {
                         }
                     }
             }

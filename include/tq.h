@@ -920,8 +920,9 @@ size_t tq_f8_workspace_bytes(void);
  * The product
  *   Y[m][n] = sum_b sx[b][m] * sw[n / 128][b] * sum_{k in block b} xq[m][k] * wq[n][k].
  * A block's sum is formed by the tensor cores in fp32, the sum over blocks by fp32
- * fused multiply-adds in the order of b (in parts where K is split, the parts
- * added in order; the split depends on the sizes alone).  sx * sw is formed in fp32
+ * fused multiply-adds in the order of b (in parts where K is split, or the even and
+ * the odd blocks apart, the parts added in order; how depends on the sizes and the
+ * offsets alone, so repeated calls give identical bytes).  sx * sw is formed in fp32
  * first and has to be finite.
  *
  *   Xq, sx   as written by tq_quant_act_f8.
