@@ -935,14 +935,15 @@ def kv4_attention(batch: KV4Batch, Q, scale: float, workspace, causal: bool = Tr
 # none of them is described afterwards.
 
 _torch = None
+_e4m3 = ()
 
 
 def _module():
     """torch, once it is loaded (an import statement costs as much as a check)."""
-    global _torch
+    global _torch, _e4m3
     if _torch is None:
         import torch
-        _torch = torch
+        _torch, _e4m3 = torch, (torch.uint8, torch.float8_e4m3fn)
         load()
     return _torch
 
@@ -963,8 +964,8 @@ def _dense(t, what, dtype, shape, d):
 
 def _codes(t, what, shape, d):
     """The address of contiguous e4m3 codes of this shape."""
-    if t.get_device() != d or t.element_size() != 1 or t.shape != shape or not t.is_contiguous():
-        _bad(t, what, f"contiguous e4m3 bytes {tuple(shape)}")
+    if t.get_device() != d or t.dtype not in _e4m3 or t.shape != shape or not t.is_contiguous():
+        _bad(t, what, f"contiguous e4m3 codes (uint8 or float8_e4m3fn) {tuple(shape)}")
     return t.data_ptr()
 
 

@@ -149,3 +149,18 @@ def test_experts(on0):
     reaches(on0, on0.expert_combine_grad, O, Y, ids, w, dY=Fake((24, 64), bf), dweights=w)
     refused(on0.expert_combine_grad, Fake((6, 32), bf), Y, ids, w, dY=Y, dweights=w)
     refused(on0.expert_combine_grad, O, Y, ids, w, dY=Y, dweights=Fake((6, 4), bf))
+
+
+@pytest.mark.parametrize("name", ["int8", "bool", "float8_e5m2"])
+def test_other_bytes_are_not_codes(on0, name):
+    """A byte of another type would be read as e4m3 and give wrong products quietly."""
+    import torch
+    bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    other = getattr(torch, name)
+    good = dict(Xq=Fake((4, 896), u8), sx=Fake((7, 4), f32), Wq=Fake((300, 896), u8), sw=Fake((3, 7), f32),
+                workspace=Fake((1 << 28,), u8), Y=Fake((4, 300), bf))
+    refused(on0.linear_f8, **{**good, "Xq": Fake((4, 896), other)})
+    refused(on0.linear_f8, **{**good, "Wq": Fake((300, 896), other)})
+    refused(on0.quant_act_f8, Fake((4, 896), bf), Xq=Fake((4, 896), other), sx=Fake((7, 4), f32))
+    good.update(offsets=Fake((6,), i32), Wq=Fake((5, 300, 896), other), sw=Fake((5, 3, 7), f32))
+    refused(on0.linear_f8_experts, **good)

@@ -67,6 +67,33 @@ def test_topk(tq, T, E, top, masked, dtype, renorm):
     assert torch.equal(a, ids) and torch.equal(b, w)
 
 
+@pytest.mark.parametrize("top", [1, 2, 8, 9, 32])
+def test_topk_many_near_the_last(tq, top):
+    """Rows in which more or fewer reach the last choice than a warp has lanes: equal
+    ones among them, the large ones in one lane's column or one after the other, NaN."""
+    import torch
+    E = 256
+    g = gen(top)
+    x = torch.randn(12, E, generator=g, device="cuda")
+    for i, n in enumerate((1, 31, 32, 33, 64)):
+        at = torch.randperm(E, generator=g, device="cuda")[:n]
+        x[i, at] = 5.0
+    x[5, ::32] = torch.arange(8.0, device="cuda") + 4      # one lane's
+    x[6] = torch.arange(E, device="cuda") / 8.0
+    x[7] = -x[6]
+    x[8, ::2] = math.nan
+    x[9] = -math.inf
+    x[9, 255] = -1.0
+    x[10, 40:] = -math.inf
+    x[11, 77] = math.inf
+    ids, w = tq.expert_topk(x, top)
+    assert torch.equal(ids.cpu(), ref.topk(x, top))
+    fine = [i for i in range(12) if i not in (8, 11)]
+    want = ref.weights(x[fine], ids[fine], True)
+    assert ((w[fine].double() - want).abs() <= bar_weights(x[fine], ids[fine], want)).all()
+    assert torch.isnan(w[[8, 11]]).any(1).all()
+
+
 @pytest.mark.parametrize("renorm", [True, False])
 def test_topk_not_finite(tq, renorm):
     import torch

@@ -208,6 +208,33 @@ def test_product(tq, M, N, K, out):
     assert tq.device_status() == 0
 
 
+# many tokens: tiles of 128 columns; one round, two, and a last one that is cut along K;
+# columns that end inside a tile's half
+@pytest.mark.parametrize("M,N,K", [(70, 12288, 256), (128, 12200, 400), (300, 4096, 640), (640, 4096, 12288),
+                                   (777, 12288, 512), (700, 12298, 256)])
+def test_product_forms(tq, M, N, K):
+    test_product(tq, M, N, K, "bf16")
+
+
+def test_product_of_weights_written_just_before(tq):
+    """The weights' kernel and the product with nothing in between."""
+    import torch
+    g = gen(5)
+    N, K = 4096, 2048
+    a, b = (torch.randn(N, K, generator=g, device="cuda").bfloat16() for _ in range(2))
+    for M in (4, 300):
+        q, sx = tq.quant_act_f8(rows(g, M, K))
+        ws = tq.f8_workspace()
+        want = [tq.linear_f8(q, sx, *tq.quantize_weights_f8(w), ws, out="f32") for w in (a, b)]
+        Wq, sw = tq.quantize_weights_f8(a)
+        got = []
+        for i in range(12):
+            tq.quantize_weights_f8((a, b)[i % 2], Wq, sw)
+            got.append(tq.linear_f8(q, sx, Wq, sw, ws, out="f32"))
+        for i, y in enumerate(got):
+            assert torch.equal(y, want[i % 2])
+
+
 def test_product_empty(tq):
     import torch
     ws = tq.f8_workspace()
