@@ -24,12 +24,15 @@
 // What bounds it.  With many tokens a step's MMAs take 512 cycles, and it takes about 950
 // (4032 tokens, 4096 to 12288: 185 us, 2200 TFLOP/s).  Between an accumulator's last MMA
 // and the first that fills it again lie a commit (300 cycles), the drain, its arrival (200)
-// and an issue, and TMEM holds two steps; shared memory is written and read 96 KB a step,
-// 750 cycles.  So a step's columns are two accumulators of 128 with MMAs of their own, one
-// filled while the other is drained, and four threads issue.  Pairs of CTAs (256 x 256, 80
-// KB a step and CTA) take as long for such a matrix, as the arrivals cross to the other SM,
-// and waste more of an expert's last tile: 512 tokens of 64 experts, eight each, 2048 x
-// 2048: 87 us against 57; 4096 tokens 178 against 164.  Sixteen drain warps: 10% slower.
+// and an issue, and TMEM holds two steps; shared memory is written and read 112 KB a step,
+// 870 cycles; each step's sums are read out of TMEM, 128 KB.  A step's columns are two
+// accumulators of 128 with MMAs of their own, one filled while the other is drained, and
+// four threads issue.  One accumulator of 256 columns (96 KB a step), the next columns
+// loaded ahead of the sums, 192 registers a drain thread: all within 3%.  Pairs of CTAs
+// (256 x 256, 80 KB a step and CTA) take as long for such a matrix, as the arrivals cross
+// to the other SM, and waste more of an expert's last tile: 512 tokens of 64 experts, eight
+// each, 2048 x 2048: 87 us against 57; 4096 tokens 178 against 164.  Sixteen drain warps:
+// 10% slower.
 // Few tokens: the weights' stream, of which an SM draws 42 bytes a ns; six stages of 16 KB
 // of it in flight.  In both forms the copies are one thread's, and its instructions a step
 // count: a loop over the boxes of the N side in place of two calls costs 10%.
