@@ -48,7 +48,7 @@ __device__ __forceinline__ float load_logit(const L *p) {
 // shared memory, a key a lane in the order of the experts (usually k to 2 k are), and
 // each looks at the others for its place.  Where more than 32 reach it each choice looks
 // through all keys.  Bound by the instructions: 16384
-// tokens, 8 of 256 experts 10.4 us (13.9 with each lane's keys sorted instead); the
+// tokens, 8 of 256 experts 10.1 us (13.9 with each lane's keys sorted instead); the
 // logits' 17 MB take 2.5 at the copy rate.
 template <typename L, int NI>
 __global__ void __launch_bounds__(256) k_expert_topk(const L *__restrict__ X, int64_t T, int E, int64_t ld, int k,
@@ -240,10 +240,10 @@ __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ 
 // choices; the counts are summed over warps, CTAs (through distributed shared memory)
 // and experts; then each warp places its piece.  Pieces are in order, and so are the
 // choices within one, so equal experts stay in order.  131072 choices of 256 experts take
-// 10.7 us, more than half of it in the placing: a step of a warp's 32 choices stores to as
-// many sectors, one a cycle and SM.  Eight CTAs take 16.4, one 102; a second kernel that
-// scatters the tokens from all SMs 12.2; a match among the lanes in place of a vote for
-// each bit 15.8.  Few choices go to one CTA: 2048 take 5.0 by it and 5.5 by the cluster,
+// 10.7 us, more than half of it in the placing: the votes, counters and stores of a warp's
+// eight steps, 32 warps an SM.  Eight CTAs take 16.4, one 102; a second kernel that scatters
+// the tokens from all SMs 12.2; the tokens put in order in shared memory first 10.9; a
+// match among the lanes in place of a vote for each bit 15.8.  Few choices go to one CTA: 2048 take 5.0 by it and 5.5 by the cluster,
 // 4096 6.3 and 5.7.
 constexpr int kSortWarps = 32, kSortCtas = 16, kSortAhead = 8;
 constexpr int64_t kSortOneCta = 2048;            // choices that one CTA sorts alone
