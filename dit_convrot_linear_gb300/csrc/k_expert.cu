@@ -240,11 +240,12 @@ __global__ void __launch_bounds__(256) k_expert_topk_grad(const L *__restrict__ 
 // choices; the counts are summed over warps, CTAs (through distributed shared memory)
 // and experts; then each warp places its piece.  Pieces are in order, and so are the
 // choices within one, so equal experts stay in order.  131072 choices of 256 experts take
-// 10.7 us, more than half of it in the placing: the votes, counters and stores of a warp's
-// eight steps, 32 warps an SM.  Eight CTAs take 16.4, one 102; a second kernel that scatters
-// the tokens from all SMs 12.2; the tokens put in order in shared memory first 10.9; a
-// match among the lanes in place of a vote for each bit 15.8.  Few choices go to one CTA: 2048 take 5.0 by it and 5.5 by the cluster,
-// 4096 6.3 and 5.7.
+// 10.4 us, more than half of it in the placing: the instructions of a warp's eight steps,
+// 32 warps an SM (10.7 with indexes of 64 bits).  Before that: eight CTAs 16.4, one 102; a
+// second kernel that scatters the tokens from all SMs 12.2; the tokens put in order in
+// shared memory first 10.9; a match among the lanes in place of a vote for each bit 15.8,
+// masks in shared memory 11.0.  Few choices go to one CTA: 2048 take 5.0 by it and 5.5 by
+// the cluster, 4096 6.3 and 5.7.
 constexpr int kSortWarps = 32, kSortCtas = 16, kSortAhead = 8;
 constexpr int64_t kSortOneCta = 2048;            // choices that one CTA sorts alone
 
@@ -260,7 +261,7 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <int BITS>
-__global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *__restrict__ ids, int64_t n, int k,
+__global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *__restrict__ ids, uint32_t n, uint32_t k,
                                                                  int E, int32_t *__restrict__ offsets,
                                                                  int32_t *__restrict__ token,
                                                                  int32_t *__restrict__ place, unsigned int *status) {
@@ -271,17 +272,17 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
     for (int i = threadIdx.x; i < kSortWarps * E; i += blockDim.x) cnt[i] = 0;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
-    const int64_t per = ((n + warps - 1) / warps + 31) / 32 * 32;
-    const int64_t f0 = (static_cast<int64_t>(cta) * kSortWarps + warp) * per, f1 = f0 + per < n ? f0 + per : n;
+    // (n < 2^31, and all of it in 32 bits: the instructions count)
+    const uint32_t warps = ctas * kSortWarps, per = ((n + warps - 1) / warps + 31) / 32 * 32;
+    const uint32_t f0 = min((cta * kSortWarps + warp) * per, n), f1 = min(f0 + per, n);
     int *mine = cnt + warp * E;
     // f(position, expert or -1, the number given) for the piece's choices in order
     auto walk = [&](auto &&f) {
-        for (int64_t at = f0; at < f1; at += 32 * kSortAhead) {
+        for (uint32_t at = f0; at < f1; at += 32 * kSortAhead) {
             int e[kSortAhead];
 #pragma unroll
             for (int i = 0; i < kSortAhead; ++i) {
-                const int64_t g = at + 32 * i + lane;
+                const uint32_t g = at + 32 * i + lane;
                 e[i] = g < f1 ? __ldg(ids + g) : -1;
             }
 #pragma unroll
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
         }
     };
     __syncthreads();
-    walk([&](int64_t, int e, int given) {
+    walk([&](uint32_t, int e, int given) {
         if (given != e) atomicOr(status, kStatusIndex);
         if (e >= 0) atomicAdd(mine + e, 1);
     });
@@ -358,9 +359,9 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
     if (cta == 0 && threadIdx.x == 0) offsets[E] = total;
     __syncthreads();
     // the choice's token: its number by k, a step of 32 at a time
-    const int by = 32 / k, over = 32 % k;
-    int tok = static_cast<int>((f0 + lane) / k), rest = static_cast<int>((f0 + lane) % k);
-    walk([&](int64_t f, int e, int) {
+    const uint32_t by = 32 / k, over = 32 % k;
+    uint32_t tok = (f0 + lane) / k, rest = f0 + lane - tok * k;
+    walk([&](uint32_t f, int e, int) {
         // the lanes with the same expert: a vote for each bit of its number
         uint32_t same = __ballot_sync(kAll, e >= 0);
 #pragma unroll
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
         int at = -1;
         if (e >= 0) {
             at = base[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
-            token[at] = tok;
+            token[at] = static_cast<int32_t>(tok);
         }
         if (f < f1) place[f] = at;
         tok += by;
@@ -385,9 +386,7 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
         if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
         __syncwarp();
     });
-    for (int64_t i = total + static_cast<int64_t>(cta) * blockDim.x + threadIdx.x; i < n;
-         i += static_cast<int64_t>(ctas) * blockDim.x)
-        token[i] = -1;
+    for (uint32_t i = total + cta * blockDim.x + threadIdx.x; i < n; i += ctas * blockDim.x) token[i] = -1;
     if (ctas > 1) cluster_wait();                // nobody leaves while its counts may still be read
 }
 
@@ -667,7 +666,8 @@ tq_status launch_expert_sort(const int32_t *ids, int64_t T, int k, int64_t E, in
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ids, T * k, k, static_cast<int>(E), offsets, token,
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ids, static_cast<uint32_t>(T * k),
+                                             static_cast<uint32_t>(k), static_cast<int>(E), offsets, token,
                                              place, status);
     return e == cudaSuccess ? TQ_OK : cuda_fail(e);
 }
