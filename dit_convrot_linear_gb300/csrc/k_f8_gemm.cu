@@ -131,7 +131,7 @@ struct F8Params {
     int ycols;                           // weight rows of a tile (few tokens: at most 128, even)
     void *Y;
     int64_t ldy;
-    int ytype, vec;                      // vec: rows of Y allow 16-byte stores (few tokens: 4-byte ones)
+    int ytype, vec;                      // vec: rows of Y allow stores of 16 bytes, 4 or 2
     unsigned int *status;
     unsigned int *counters;              // [CTAs][kF8MaxDrain]
     unsigned char *parts;                // [CTAs][2][PART]
@@ -715,37 +715,66 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
             // ---- Y of many tokens: a lane has 32 columns of a token.  64 bytes of each of the
             // warp's 32 rows at a time go through shared memory, so that four lanes store a row's 64
-            // bytes.  A row's chunk c lies at c ^ (row / 2 % 4): no two of eight rows in one bank.
+            // bytes (16 or 32 lanes where Y's rows are not aligned to 16: 3974 tokens of 272 to 1730,
+            // bf16, 16.5 us, and 42 with 16 bytes a lane in pieces; to 1728 12.3).  A row's chunk c lies at
+            // c ^ (row / 2 % 4): no two of eight rows in one bank.
             unsigned char *turn = smem + P::OFF_OUT + warp * 32 * 64;
             const int esize = p.ytype == 0 ? 4 : 2, piece = 16 / esize;
             unsigned char *y = static_cast<unsigned char *>(p.Y) +
-                               ((static_cast<int64_t>(sg.m0) + row + (lane >> 2)) * p.ldy + n0 + c0 + (lane & 3) * piece) * esize;
+                               ((static_cast<int64_t>(sg.m0) + row) * p.ldy + n0 + c0) * esize;
+            unsigned char *y16 = y + (static_cast<int64_t>(lane >> 2) * p.ldy + (lane & 3) * piece) * esize;
             auto turn_out = [&](const uint4 (&u)[4], int col) {
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     *reinterpret_cast<uint4 *>(turn + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = u[j];
                 __syncwarp();
+                if (p.vec == 16) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int at = r * 8 + (lane >> 2), left = cols_left - col - (lane & 3) * piece;
-                    if (at >= rows_left || left <= 0) continue;
-                    const uint4 o = *reinterpret_cast<const uint4 *>(turn + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4));
-                    unsigned char *to = y + (static_cast<int64_t>(r) * 8 * p.ldy + col) * esize;
-                    if (p.vec && left >= piece) {
-                        *reinterpret_cast<uint4 *>(to) = o;
-                    } else {
-                        const uint32_t h[4] = {o.x, o.y, o.z, o.w};
-                        if (esize == 4) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (j < left) reinterpret_cast<uint32_t *>(to)[j] = h[j];
+                    for (int r = 0; r < 4; ++r) {
+                        const int at = r * 8 + (lane >> 2), left = cols_left - col - (lane & 3) * piece;
+                        if (at >= rows_left || left <= 0) continue;
+                        const uint4 o = *reinterpret_cast<const uint4 *>(turn + at * 64 + (((lane & 3) ^ ((at >> 1) & 3)) << 4));
+                        unsigned char *to = y16 + (static_cast<int64_t>(r) * 8 * p.ldy + col) * esize;
+                        if (left >= piece) {
+                            *reinterpret_cast<uint4 *>(to) = o;
                         } else {
+                            const uint32_t h[4] = {o.x, o.y, o.z, o.w};
+                            if (esize == 4) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (j < left)
-                                    reinterpret_cast<uint16_t *>(to)[j] = static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1)));
+                                for (int j = 0; j < 4; ++j)
+                                    if (j < left) reinterpret_cast<uint32_t *>(to)[j] = h[j];
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (j < left)
+                                        reinterpret_cast<uint16_t *>(to)[j] = static_cast<uint16_t>(h[j >> 1] >> (16 * (j & 1)));
+                            }
                         }
+                    }
+                } else if (p.vec == 4) {
+                    // 4 bytes a lane, 16 lanes a row
+                    const int w = lane & 15, c = col + w * 4 / esize;
+#pragma unroll 4
+                    for (int r = 0; r < 16; ++r) {
+                        const int at = r * 2 + (lane >> 4);
+                        if (at >= rows_left || c >= cols_left) continue;
+                        const uint32_t o = *reinterpret_cast<const uint32_t *>(
+                            turn + at * 64 + (((w >> 2) ^ ((at >> 1) & 3)) << 4) + (w & 3) * 4);
+                        unsigned char *to = y + (static_cast<int64_t>(at) * p.ldy + c) * esize;
+                        if (esize == 4 || c + 1 < cols_left)
+                            *reinterpret_cast<uint32_t *>(to) = o;
+                        else
+                            *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(o);
+                    }
+                } else {
+                    // (rows of bf16 that begin between words) a value a lane
+#pragma unroll 4
+                    for (int at = 0; at < 32; ++at) {
+                        if (at >= rows_left || col + lane >= cols_left) continue;
+                        reinterpret_cast<uint16_t *>(y)[static_cast<int64_t>(at) * p.ldy + col + lane] =
+                            *reinterpret_cast<const uint16_t *>(
+                                turn + at * 64 + (((lane >> 3) ^ ((at >> 1) & 3)) << 4) + (lane & 7) * 2);
                     }
                 }
             };
@@ -836,7 +865,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 // ---- Y: this lane's column n of tokens c0, c0 + 1, ...
                 const int n = n0 + row + lane, n_end = min(p.N, n0 + p.ycols);
                 const int64_t first = (static_cast<int64_t>(sg.m0) + c0) * p.ldy;
-                if (p.ytype == 1 && p.vec) {
+                if (p.ytype == 1 && p.vec >= 4) {
                     // two lanes exchange a value: the even one takes both columns of one token, the
                     // odd one of the next, and a store is 4 bytes
                     const int odd = lane & 1, ne = n - odd;
@@ -944,8 +973,8 @@ tq_status launch_f8(const F8Product &f, int ycols, const DeviceInfo &dev, cudaSt
     p.Y = f.Y;
     p.ldy = f.ldy;
     p.ytype = f.ytype;
-    const int piece = WIDE ? 16 : 4;
-    p.vec = reinterpret_cast<uintptr_t>(f.Y) % piece == 0 && f.ldy * (f.ytype == 0 ? 4 : 2) % piece == 0 ? 1 : 0;
+    const uint64_t step = reinterpret_cast<uintptr_t>(f.Y) | static_cast<uint64_t>(f.ldy * (f.ytype == 0 ? 4 : 2));
+    p.vec = step % 16 == 0 ? 16 : (step % 4 == 0 ? 4 : 2);
     p.status = status_word();
     if (!p.status) return TQ_ERR_DEVICE;
     p.counters = static_cast<unsigned int *>(f.ws);

@@ -216,6 +216,13 @@ def test_product_forms(tq, M, N, K):
     test_product(tq, M, N, K, "bf16")
 
 
+# rows of Y that begin anywhere: many tokens, columns that end inside a word
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(777, 6001), (778, 6002), (779, 6003), (902, 6004)])
+def test_product_unaligned_rows(tq, M, N, out):
+    test_product(tq, M, N, 272, out)
+
+
 def test_product_of_weights_written_just_before(tq):
     """The weights' kernel and the product with nothing in between."""
     import torch
