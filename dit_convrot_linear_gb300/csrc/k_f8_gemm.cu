@@ -1010,11 +1010,12 @@ size_t f8_workspace_bytes(const DeviceInfo &dev) {
     return f8_counter_bytes(dev.sms) + static_cast<size_t>(dev.sms) * 2 * F8Plan<true>::PART;
 }
 
-// The form that takes the least time by rounds of tiles and the time of a step in 10 ns, with
-// rows spread evenly over the experts; the weights of a lone tile come from the DRAM.  Measured with 4096 to 12288: 48 tokens 16.6 us (few)
-// and 19.9 (many, 128 columns); 65: 33.7, 19.6 and with 256 columns 21.5; 256: 49, 34.5 and
-// 21.5; 512: 92, 49 and 37.5.  64 experts of about two rows each, 2048 x 2048: 41 (few) and
-// 51 (256 columns); 16 rows: 50, 71 and 53; 64 rows: 91, 73 and 57.
+// The form that takes the least time by rounds of tiles and the time of a step in 10 ns,
+// with rows spread evenly over the experts; the weights of a lone tile come from the DRAM.
+// Measured with 4096 to 12288: 48 tokens 16.6 us (few) and 19.9 (many, 128 columns); 65:
+// 33.7, 19.6 and with 256 columns 21.5; 256: 49, 34.5 and 21.5; 512: 92, 49 and 37.5.  64
+// experts of about two rows each, 2048 x 2048: 41 (few) and 51 (256 columns); 16 rows: 50,
+// 71 and 53; 64 rows: 91, 73 and 57.
 tq_status launch_linear_f8(const F8Product &p, const DeviceInfo &dev, cudaStream_t s) {
     const int64_t experts = p.offsets ? (p.experts < p.M ? p.experts : p.M) : 1, rows = (p.M + experts - 1) / experts;
     auto cost = [&](int64_t tokens, int64_t cols, int64_t lone, int64_t other) {
