@@ -106,7 +106,12 @@ struct F8Plan {
     static constexpr int smem(int64_t experts) { return OFF_LIST + static_cast<int>(experts + 1) * 12 + 16; }
     static constexpr int PART = DRAIN * 32 * COLS * 4;         // bytes of a CTA's partial tile
     static constexpr int MIN_STEPS = 4, JOIN_STEPS = WIDE ? 44 : 12;   // of split tiles: steps a CTA, steps saved
-    static constexpr int DRAIN_REGS = 176, OTHER_REGS = 80;     // many tokens: registers a thread
+    // registers a thread at the launch, then of the drain warps and the others.  Few tokens leave
+    // room for a CTA of the next kernel, an operand's quantiser, which then waits where it runs:
+    // 16 tokens' layer of 64 experts, eight each, 2048 x 1024, 80 us, and 85 with all registers
+    // taken and the list of work made after the wait.
+    static constexpr int REGS = WIDE ? 128 : 112, DRAIN_REGS = WIDE ? 176 : 136, OTHER_REGS = WIDE ? 80 : 88;
+    static_assert(REGS * THREADS >= 32 * (DRAIN * DRAIN_REGS + OTHERS * OTHER_REGS), "registers");
 };
 // A wait for a parity tells two neighbouring rounds of a barrier apart, no more: who
 // waits for a stage's or an accumulator's round has to have seen the round before it.  So
@@ -300,7 +305,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 }
 
 template <class P>
-__global__ void __launch_bounds__(P::THREADS, 1)
+__global__ void __maxnreg__(P::REGS)
 k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Params p) {
     constexpr int DRAIN = P::DRAIN, STAGES = P::STAGES, ACCS = P::ACCS, TURNS = P::TURNS, HALVES = P::HALVES;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -335,16 +340,14 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     }
     // What an earlier kernel wrote is read, and the workspace used, after pdl_wait; the TMEM
     // is taken then too (that kernel's CTAs may still need theirs), and the next kernel may
-    // start once this one has its own.  One matrix's list of work needs nothing of that, and
-    // its first weights may come into L2 before (coherent: whoever writes them still may).
-    if (p.offsets) pdl_wait();
+    // start once this one has its own.  The list of work is made before, from offsets that may
+    // still change (it is made again if they did), and the first weights come into L2 (coherent:
+    // whoever writes them still may).
     const int *list = reinterpret_cast<const int *>(smem + P::OFF_LIST);
     int *row0 = reinterpret_cast<int *>(smem + P::OFF_LIST), *rows = row0 + p.experts + 1, *tiles = rows + p.experts + 1;
-    if (p.offsets) {
-        for (int e = threadIdx.x; e <= p.experts; e += P::THREADS) row0[e] = p.offsets[e];
-        __syncthreads();
-    }
-    if (warp == 0) {
+    const volatile int32_t *offsets = p.offsets;
+    bool bad = false;
+    auto make_list = [&]() {
         int total = static_cast<int>((p.M + P::TOKENS - 1) / P::TOKENS);       // token tiles
         if (p.offsets == nullptr) {
             if (lane == 0) {
@@ -356,7 +359,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         } else {
             // an expert whose range is out of order has no rows
             int sum = 0, most = INT32_MIN;
-            bool bad = false;
+            bad = false;
             for (int e0 = 0; e0 < p.experts; e0 += 32) {
                 const int e = e0 + lane;
                 const bool in = e < p.experts;
@@ -385,7 +388,6 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 sum += __shfl_sync(0xffffffffu, s, 31);
                 most = __shfl_sync(0xffffffffu, top, 31);
             }
-            if (bad) atomicOr(p.status, kStatusIndex);
             if (lane == 0) tiles[p.experts] = sum;
             total = sum;
         }
@@ -403,7 +405,12 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             cut.units = split ? units : 0;
             cut.use = use;
         }
+    };
+    if (p.offsets) {
+        for (int e = threadIdx.x; e <= p.experts; e += P::THREADS) row0[e] = offsets[e];
+        __syncthreads();
     }
+    if (warp == 0) make_list();
     __syncthreads();
     // weight rows of a tile, and columns of its accumulator h: tokens, or weight rows, rounded
     // up to 16 (one without any still takes part, and nothing of it is stored)
@@ -443,20 +450,33 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if constexpr (P::WIDE) copy_a(s, k, c.xrow);
         else copy_b(c.boxes, s, k, c.xrow);
     };
-    if (!p.offsets) {
-        if (warp == DRAIN + P::ISSUERS && lane == 0) {
-            F8Iter iter(cut);
-            F8Seg sg;
-            if (iter.next(cut, list, p, sg)) {
-                const Source c = source(sg);
-                for (int k = sg.k0; k < min(sg.k1, sg.k0 + STAGES); ++k) {
-                    f8_prefetch(P::WIDE ? &tmB : &tmA, k * kStepK, c.wrow);
-                    if (P::WIDE && c.boxes > 1) f8_prefetch(&tmB, k * kStepK, c.wrow + P::B_BOX);
-                }
+    if (warp == DRAIN + P::ISSUERS && lane == 0) {
+        F8Iter iter(cut);
+        F8Seg sg;
+        if (iter.next(cut, list, p, sg)) {
+            const Source c = source(sg);
+            for (int k = sg.k0; k < min(sg.k1, sg.k0 + STAGES); ++k) {
+                f8_prefetch(P::WIDE ? &tmB : &tmA, k * kStepK, c.wrow);
+                if (P::WIDE && c.boxes > 1) f8_prefetch(&tmB, k * kStepK, c.wrow + P::B_BOX);
             }
         }
-        __syncwarp();
-        pdl_wait();
+    }
+    __syncwarp();
+    pdl_wait();
+    if (p.offsets) {
+        int changed = 0;
+        for (int e = threadIdx.x; e <= p.experts; e += P::THREADS) {
+            const int32_t now = offsets[e];
+            if (now != row0[e]) {            // (the prefetch above does not read it)
+                row0[e] = now;
+                changed = 1;
+            }
+        }
+        if (__syncthreads_or(changed)) {
+            if (warp == 0) make_list();
+            __syncthreads();
+        }
+        if (bad) atomicOr(p.status, kStatusIndex);
     }
     if (warp == DRAIN) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -470,7 +490,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     pdl_launch_dependents();
 
     if (warp >= DRAIN) {
-        if constexpr (P::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::OTHER_REGS));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::OTHER_REGS));
         if (warp < DRAIN + P::ISSUERS) {
             // -------------------------------------------- MMA issue (one thread a warp)
             if (lane == 0) {
@@ -600,7 +620,7 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
         __syncwarp();
     } else {
-        if constexpr (P::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::DRAIN_REGS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::DRAIN_REGS));
         // ------------------------------------------------ drain
         constexpr int GROUPS = P::COLS / 16;             // 16 columns at a time
         const int q = warp & 3, c0 = P::WIDE ? (warp >> 2) * P::COLS : 0;     // c0: first column of the tile
@@ -933,7 +953,7 @@ tq_status launch_f8(const F8Product &f, int ycols, const DeviceInfo &dev, cudaSt
         cudaError_t e = cudaFuncGetAttributes(&at, kern);
         if (e != cudaSuccess) return cuda_fail(e);
         // the warps' own register counts have to be covered by the launch's
-        if (WIDE && at.numRegs * P::THREADS < 32 * (P::DRAIN * P::DRAIN_REGS + P::OTHERS * P::OTHER_REGS))
+        if (at.numRegs * P::THREADS < 32 * (P::DRAIN * P::DRAIN_REGS + P::OTHERS * P::OTHER_REGS))
             return TQ_ERR_DEVICE;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::smem(TQ_MAX_EXPERTS));
         if (e != cudaSuccess) return cuda_fail(e);

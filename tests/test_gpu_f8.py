@@ -347,6 +347,32 @@ def test_experts_bad_ranges_are_empty_and_reported(tq, bad, M):
     assert tq.device_status() == 0
 
 
+@pytest.mark.parametrize("M,E", [(40, 16), (1200, 16), (300, 200)])
+def test_experts_offsets_written_just_before(tq, M, E):
+    """The kernel that writes the offsets, over other ones, and the product with nothing in
+    between; every other time the offsets stay as they are."""
+    import torch
+    g = gen(M)
+    N, K = 384, 512
+    q, sx = tq.quant_act_f8(rows(g, M, K))
+    Wq, sw = matrix(g, E, N, K)
+    ws = tq.f8_workspace()
+    ids = [torch.randint(0, E, (M, 1), generator=g, device="cuda", dtype=torch.int32) ** p % E for p in (1, 2, 3)]
+    want = []
+    for i in ids:
+        off = tq.expert_sort(i, E)[0]
+        torch.cuda.synchronize()
+        want.append(tq.linear_f8_experts(q, sx, off, Wq, sw, ws, out="f32"))
+    lists = tq.expert_sort(ids[0], E)
+    got = []
+    for i in range(24):
+        off = tq.expert_sort(ids[i // 2 % 3], E, *lists)[0]
+        got.append(tq.linear_f8_experts(q, sx, off, Wq, sw, ws, out="f32", Y=torch.empty(M, N, device="cuda")))
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i // 2 % 3])
+    assert tq.device_status() == 0
+
+
 @pytest.mark.parametrize("M", [24, 700])
 def test_product_in_a_graph_and_on_two_streams(tq, M):
     """A captured call replayed on new inputs, and two streams with a workspace each."""
