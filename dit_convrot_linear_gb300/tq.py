@@ -932,7 +932,8 @@ def kv4_attention(batch: KV4Batch, Q, scale: float, workspace, causal: bool = Tr
 # Codes are e4m3 bytes: uint8 tensors, or torch.float8_e4m3fn ones.  All tensors of a
 # call are on the current device, the one that the library launches on.  A call of a few
 # tokens takes a few microseconds, so its checks are few and plain: a tensor that passes
-# none of them is described afterwards.
+# none of them is described afterwards.  What a call with ``stream`` makes itself is made
+# on that stream: other streams wait for it as for any other work there.
 
 _torch = None
 _e4m3 = ()
@@ -1001,6 +1002,22 @@ def _stream_of(stream, d) -> int:
     return _torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
 
 
+def _made(make, shape, dtype, device, stream):
+    """A tensor that a call makes itself.  It is made on the call's stream, where no
+    earlier kernel still uses its memory and zeros are filled in before the call's kernel
+    runs; and the current stream, whose caller has it from here, is recorded: the memory
+    is not given out again before that stream has done what it has when the tensor goes."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def quantize_weights_f8(W, codes=None, scales=None, stream=None):
     """bf16 W [N, K], or [experts, N, K] -> (e4m3 codes of the same shape, fp32 scales
     [..., ceil(N / 128), ceil(K / 128)])."""
@@ -1011,9 +1028,9 @@ def quantize_weights_f8(W, codes=None, scales=None, stream=None):
     N, K = W.shape[-2:]
     blocks = (*W.shape[:-2], -(-N // 128), -(-K // 128))
     if codes is None:
-        codes = torch.empty(W.shape, dtype=torch.uint8, device=W.device)
+        codes = _made(torch.empty, W.shape, torch.uint8, W.device, stream)
     if scales is None:
-        scales = torch.empty(blocks, dtype=torch.float32, device=W.device)
+        scales = _made(torch.empty, blocks, torch.float32, W.device, stream)
     _codes(codes, "codes", W.shape, d)
     _dense(scales, "scales", torch.float32, blocks, d)
     for w, c, s in ((W, codes, scales),) if W.dim() == 2 else zip(W, codes, scales):
@@ -1023,11 +1040,11 @@ def quantize_weights_f8(W, codes=None, scales=None, stream=None):
     return codes, scales
 
 
-def _operand(torch, M, K, Xq, sx, device):
+def _operand(torch, M, K, Xq, sx, device, stream):
     if Xq is None:
-        Xq = torch.empty((M, K), dtype=torch.uint8, device=device)
+        Xq = _made(torch.empty, (M, K), torch.uint8, device, stream)
     if sx is None:
-        sx = torch.empty((-(-K // 128), M), dtype=torch.float32, device=device)
+        sx = _made(torch.empty, (-(-K // 128), M), torch.float32, device, stream)
     return Xq, sx
 
 
@@ -1039,7 +1056,7 @@ def quant_act_f8(X, rows=None, Xq=None, sx=None, stream=None):
     R, K = X.shape
     M = R if rows is None else rows.numel()
     if Xq is None or sx is None:
-        Xq, sx = _operand(torch, M, K, Xq, sx, X.device)
+        Xq, sx = _operand(torch, M, K, Xq, sx, X.device, stream)
     rc = _lib.tq_quant_act_f8(X.data_ptr(), R, K, _matrix(X, "X", torch.bfloat16, R, K, d),
                               None if rows is None else _list(rows, "rows", M, d), M, _codes(Xq, "Xq", (M, K), d),
                               _dense(sx, "sx", torch.float32, (-(-K // 128), M), d), _stream_of(stream, d))
@@ -1057,7 +1074,7 @@ def swiglu_quant_act_f8(G, U, Xq=None, sx=None, stream=None):
     if U.shape != G.shape:
         raise ValueError(f"U is {tuple(U.shape)}, expected {(M, K)}")
     if Xq is None or sx is None:
-        Xq, sx = _operand(torch, M, K, Xq, sx, G.device)
+        Xq, sx = _operand(torch, M, K, Xq, sx, G.device, stream)
     rc = _lib.tq_swiglu_quant_act_f8(G.data_ptr(), _matrix(G, "G", torch.bfloat16, M, K, d), U.data_ptr(),
                                      _matrix(U, "U", torch.bfloat16, M, K, d), M, K, _codes(Xq, "Xq", (M, K), d),
                                      _dense(sx, "sx", torch.float32, (-(-K // 128), M), d), _stream_of(stream, d))
@@ -1085,7 +1102,7 @@ def linear_f8(Xq, sx, Wq, sw, workspace, out: str = "bf16", Y=None, stream=None)
     M, K = Xq.shape
     N = Wq.shape[0]
     if Y is None:
-        Y = torch.empty((M, N), dtype=dtype, device=Xq.device)
+        Y = _made(torch.empty, (M, N), dtype, Xq.device, stream)
     kb = -(-K // 128)
     rc = _lib.tq_linear_f8(_codes(Xq, "Xq", (M, K), d), _dense(sx, "sx", f32, (kb, M), d), M, K,
                            _codes(Wq, "Wq", (N, K), d), _dense(sw, "sw", f32, (-(-N // 128), kb), d), N, Y.data_ptr(),
@@ -1113,7 +1130,7 @@ def linear_f8_experts(Xq, sx, offsets, Wq, sw, workspace, out: str = "bf16", Y=N
     M, K = Xq.shape
     E, N = Wq.shape[:2]
     if Y is None:
-        Y = torch.zeros((M, N), dtype=dtype, device=Xq.device)
+        Y = _made(torch.zeros, (M, N), dtype, Xq.device, stream)
     kb = -(-K // 128)
     rc = _lib.tq_linear_f8_experts(_codes(Xq, "Xq", (M, K), d), _dense(sx, "sx", f32, (kb, M), d), M, K,
                                    _list(offsets, "offsets", E + 1, d), E, _codes(Wq, "Wq", (E, N, K), d),
@@ -1133,9 +1150,9 @@ def expert_topk(logits, top: int, renorm: bool = True, ids=None, weights=None, s
     d = torch._C._cuda_getDevice()
     T, E = logits.shape
     if ids is None:
-        ids = torch.empty((T, top), dtype=torch.int32, device=logits.device)
+        ids = _made(torch.empty, (T, top), torch.int32, logits.device, stream)
     if weights is None:
-        weights = torch.empty((T, top), dtype=torch.float32, device=logits.device)
+        weights = _made(torch.empty, (T, top), torch.float32, logits.device, stream)
     rc = _lib.tq_expert_topk(logits.data_ptr(), _floats(logits, "logits"), T, E,
                              _matrix(logits, "logits", logits.dtype, T, E, d), top, int(renorm),
                              _list(ids, "ids", T * top, d), _dense(weights, "weights", torch.float32, (T, top), d),
@@ -1154,7 +1171,7 @@ def expert_topk_grad(logits, ids, dweights, renorm: bool = True, dlogits=None, s
         raise ValueError("ids must be [tokens, top]")
     top = ids.shape[1]
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        dlogits = _made(torch.empty, (T, E), logits.dtype, logits.device, stream)
     rc = _lib.tq_expert_topk_grad(logits.data_ptr(), _floats(logits, "logits"), T, E,
                                   _matrix(logits, "logits", logits.dtype, T, E, d), _list(ids, "ids", T * top, d),
                                   _dense(dweights, "dweights", torch.float32, (T, top), d), top, int(renorm),
@@ -1173,11 +1190,11 @@ def expert_sort(ids, experts: int, offsets=None, token=None, place=None, stream=
     T, top = ids.shape
     n = T * top
     if offsets is None:
-        offsets = torch.empty(experts + 1, dtype=torch.int32, device=ids.device)
+        offsets = _made(torch.empty, experts + 1, torch.int32, ids.device, stream)
     if token is None:
-        token = torch.empty(n, dtype=torch.int32, device=ids.device)
+        token = _made(torch.empty, n, torch.int32, ids.device, stream)
     if place is None:
-        place = torch.empty((T, top), dtype=torch.int32, device=ids.device)
+        place = _made(torch.empty, (T, top), torch.int32, ids.device, stream)
     rc = _lib.tq_expert_sort(_list(ids, "ids", n, d), T, top, experts, _list(offsets, "offsets", experts + 1, d),
                              _list(token, "token", n, d), _list(place, "place", n, d), _stream_of(stream, d))
     if rc:
@@ -1193,7 +1210,7 @@ def expert_gather(X, rows, Y=None, stream=None):
     R, W = X.shape
     M = rows.numel()
     if Y is None:
-        Y = torch.zeros((M, W), dtype=X.dtype, device=X.device)
+        Y = _made(torch.zeros, (M, W), X.dtype, X.device, stream)
     rc = _lib.tq_expert_gather(X.data_ptr(), _floats(X, "X"), R, W, _matrix(X, "X", X.dtype, R, W, d),
                                _list(rows, "rows", M, d), M, Y.data_ptr(), _matrix(Y, "Y", X.dtype, M, W, d),
                                _stream_of(stream, d))
@@ -1210,7 +1227,7 @@ def expert_combine(Y, place, weights=None, O=None, stream=None):
     R, W = Y.shape
     T, top = place.shape
     if O is None:
-        O = torch.empty((T, W), dtype=Y.dtype, device=Y.device)
+        O = _made(torch.empty, (T, W), Y.dtype, Y.device, stream)
     rc = _lib.tq_expert_combine(Y.data_ptr(), _floats(Y, "Y"), R, W, _matrix(Y, "Y", Y.dtype, R, W, d),
                                 _list(place, "place", T * top, d),
                                 None if weights is None else _dense(weights, "weights", torch.float32, (T, top), d), T,
@@ -1231,9 +1248,9 @@ def expert_combine_grad(dO, Y, place, weights=None, dY=None, dweights=None, stre
     if dO.shape != (T, W):
         raise ValueError(f"dO is {tuple(dO.shape)}, expected {(T, W)}")
     if dY is None:
-        dY = torch.zeros((R, W), dtype=Y.dtype, device=Y.device)
+        dY = _made(torch.zeros, (R, W), Y.dtype, Y.device, stream)
     if dweights is None:
-        dweights = torch.empty((T, top), dtype=torch.float32, device=Y.device)
+        dweights = _made(torch.empty, (T, top), torch.float32, Y.device, stream)
     rc = _lib.tq_expert_combine_grad(dO.data_ptr(), _matrix(dO, "dO", Y.dtype, T, W, d), Y.data_ptr(),
                                      _floats(Y, "Y"), R, W, _matrix(Y, "Y", Y.dtype, R, W, d),
                                      _list(place, "place", T * top, d),

@@ -1,0 +1,66 @@
+"""Calls on a stream of their own (``stream=``) while the current stream is busy, with
+outputs that the call makes: complete on that stream, and not touched by the other one
+later.  Bit for bit what the same call gives without ``stream``."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+BUSY = 200_000_000            # cycles: 0.1 s
+
+
+def calls(tq):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    M, K, N, E, top = 200, 896, 300, 6, 2
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, both = n(M, K).bfloat16(), n(M, 2 * K).bfloat16()
+    W = n(E, N, K).bfloat16()
+    q, sx = tq.quant_act_f8(x)
+    Wq, sw = tq.quantize_weights_f8(W)
+    logits, dw = n(M // top, E), n(M // top, top)
+    ids, w = tq.expert_topk(logits, top)
+    ids[::5, 1] = -1                                   # rows of no expert: left as the call's zeros
+    offsets, token, place = tq.expert_sort(ids, E)
+    y, do, ws = n(M, 64).bfloat16(), n(M // top, 64).bfloat16(), tq.f8_workspace()
+    return {
+        "quantize_weights_f8": lambda **s: tq.quantize_weights_f8(W, **s),
+        "quant_act_f8": lambda **s: tq.quant_act_f8(x, **s),
+        "swiglu_quant_act_f8": lambda **s: tq.swiglu_quant_act_f8(both[:, :K], both[:, K:], **s),
+        "linear_f8": lambda **s: tq.linear_f8(q, sx, Wq[0], sw[0], ws, **s),
+        "linear_f8_experts": lambda **s: tq.linear_f8_experts(q, sx, offsets, Wq, sw, ws, **s),
+        "expert_topk": lambda **s: tq.expert_topk(logits, top, **s),
+        "expert_topk_grad": lambda **s: tq.expert_topk_grad(logits, ids, dw, **s),
+        "expert_sort": lambda **s: tq.expert_sort(ids, E, **s),
+        "expert_gather": lambda **s: tq.expert_gather(do, token, **s),
+        "expert_combine": lambda **s: tq.expert_combine(y, place, w, **s),
+        "expert_combine_grad": lambda **s: tq.expert_combine_grad(do, y, place, w, **s),
+    }
+
+
+NAMES = ["quantize_weights_f8", "quant_act_f8", "swiglu_quant_act_f8", "linear_f8", "linear_f8_experts", "expert_topk",
+         "expert_topk_grad", "expert_sort", "expert_gather", "expert_combine", "expert_combine_grad"]
+
+
+def several(v):
+    return v if isinstance(v, tuple) else (v,)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_made_while_the_current_stream_is_busy(tq, name):
+    import torch
+    f = calls(tq)[name]
+    want = several(f())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    f(stream=side)                                     # (the stream's memory is there from now on)
+    with torch.cuda.stream(side):
+        assert all(torch.equal(a, a) for a in want)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    got = several(f(stream=side))
+    with torch.cuda.stream(side):                      # (waits for the side stream alone)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert tq.device_status() == 0
