@@ -52,15 +52,15 @@ def test_outputs_made_while_the_current_stream_is_busy(tq, name):
     want = several(f())
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    f(stream=side)                                     # (the stream's memory is there from now on)
-    with torch.cuda.stream(side):
-        assert all(torch.equal(a, a) for a in want)
-    torch.cuda.synchronize()
-    torch.cuda._sleep(BUSY)
-    got = several(f(stream=side))
-    with torch.cuda.stream(side):                      # (waits for the side stream alone)
-        assert all(torch.equal(a, b) for a, b in zip(got, want))
-    assert not torch.cuda.current_stream().query()
-    torch.cuda.synchronize()
-    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # once with nothing in the way (kernels are loaded, each stream has its memory), once busy
+    for cycles in (0, BUSY):
+        if cycles:
+            torch.cuda._sleep(cycles)
+        got = several(f(stream=side))
+        with torch.cuda.stream(side):                  # (waits for the side stream alone)
+            same = [torch.equal(a, b) for a, b in zip(got, want)]
+        busy = not torch.cuda.current_stream().query()
+        torch.cuda.synchronize()
+        assert all(same) and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert busy                                        # the other stream was not waited for
     assert tq.device_status() == 0
