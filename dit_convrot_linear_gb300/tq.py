@@ -4,8 +4,9 @@ Argument marshalling only: every step of the projection runs in the CUDA
 library.  Tensors are PyTorch device tensors (PyTorch provides memory and
 streams); the functions pass their pointers, sizes and the current stream to
 the C entry points of the same names and raise ``TQError`` on any status other
-than ``TQ_OK``.  There is no fallback: if the library is missing, ``load()``
-raises.
+than ``TQ_OK``.  A call with ``stream`` runs there, and what it makes itself is
+made there: other streams wait for it as for any other work.  There is no
+fallback: if the library is missing, ``load()`` raises.
 """
 from __future__ import annotations
 
@@ -151,6 +152,22 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _made(make, shape, dtype, device, stream):
+    """A tensor that a call makes itself.  It is made on the call's stream, where no
+    earlier kernel still uses its memory and zeros are filled in before the call's kernel
+    runs; and the current stream, whose caller has it from here, is recorded: the memory
+    is not given out again before that stream has done what it has when the tensor goes."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -210,10 +227,10 @@ def quantize_weights(W, bits: int, codes=None, scales=None, stream=None):
     import torch
     N, K = W.shape
     if codes is None:
-        codes = torch.empty((N, K if bits == 8 else K // 2),
-                            dtype=torch.int8 if bits == 8 else torch.uint8, device=W.device)
+        codes = _made(torch.empty, (N, K if bits == 8 else K // 2), torch.int8 if bits == 8 else torch.uint8, W.device,
+                      stream)
     if scales is None:
-        scales = torch.empty(N, dtype=torch.float32, device=W.device)
+        scales = _made(torch.empty, N, torch.float32, W.device, stream)
     _req(W, "W", dtype=torch.bfloat16, rows=N, cols=K)
     _req(codes, "codes", nbytes=N * K * bits // 8)
     _req(scales, "scales", dtype=torch.float32, nbytes=4 * N)
@@ -229,10 +246,10 @@ def quantize_weights_blocked(W, bits: int, G: int, rotate: bool = True, codes=No
     import torch
     N, K = W.shape
     if codes is None:
-        codes = torch.empty((N, K if bits == 8 else K // 2),
-                            dtype=torch.int8 if bits == 8 else torch.uint8, device=W.device)
+        codes = _made(torch.empty, (N, K if bits == 8 else K // 2), torch.int8 if bits == 8 else torch.uint8, W.device,
+                      stream)
     if scales is None:
-        scales = torch.empty((N, K // G if G > 0 else 0), dtype=torch.float32, device=W.device)
+        scales = _made(torch.empty, (N, K // G if G > 0 else 0), torch.float32, W.device, stream)
     _req(W, "W", dtype=torch.bfloat16, rows=N, cols=K)
     _req(codes, "codes", nbytes=N * K * bits // 8)
     if G > 0:
@@ -251,7 +268,7 @@ def linear_blocked(X, Wq, sw, N: int, bits: int, G: int, rotate: bool = True, Y=
     if out not in ("f32", "bf16"):
         raise ValueError("tq_linear_blocked writes f32 or bf16")
     if Y is None:
-        Y = torch.empty((M, N), dtype=_dt(out), device=X.device)
+        Y = _made(torch.empty, (M, N), _dt(out), X.device, stream)
     _req(X, "X", dtype=torch.bfloat16, rows=M, cols=K)
     _req(Wq, "Wq", nbytes=N * K * bits // 8)
     if G > 0:
@@ -266,9 +283,9 @@ def rotate_quant_act(X, Xq=None, sx=None, stream=None):
     import torch
     M, K = X.shape
     if Xq is None:
-        Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
+        Xq = _made(torch.empty, (M, K), torch.int8, X.device, stream)
     if sx is None:
-        sx = torch.empty(M, dtype=torch.float32, device=X.device)
+        sx = _made(torch.empty, M, torch.float32, X.device, stream)
     _req(X, "X", dtype=torch.bfloat16, rows=M, cols=K)
     _req(Xq, "Xq", dtype=torch.int8, rows=M, cols=K, dense=True)
     _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
@@ -281,7 +298,7 @@ def rotate_act_bf16(X, Xr=None, stream=None):
     import torch
     M, K = X.shape
     if Xr is None:
-        Xr = torch.empty((M, K), dtype=torch.bfloat16, device=X.device)
+        Xr = _made(torch.empty, (M, K), torch.bfloat16, X.device, stream)
     _req(X, "X", dtype=torch.bfloat16, rows=M, cols=K)
     _req(Xr, "Xr", dtype=torch.bfloat16, rows=M, cols=K, dense=True)
     _check(lib().tq_rotate_act_bf16(_ptr(X), M, K, X.stride(0), _ptr(Xr), _stream(stream)),
@@ -301,13 +318,13 @@ def linear(X, Wq, sw, N: int, bits: int, mode: str, Y=None, out: str = "f32",
     if out not in ("f32", "bf16"):
         raise ValueError("tq_linear writes f32 or bf16")
     if Y is None:
-        Y = torch.empty((M, N), dtype=_dt(out), device=X.device)
+        Y = _made(torch.empty, (M, N), _dt(out), X.device, stream)
     _req(X, "X", dtype=torch.bfloat16, rows=M, cols=K)
     _weights(Wq, sw, N, K, bits)
     _req(Y, "Y", dtype=_dt(out), rows=M, cols=N)
     need = linear_workspace_bytes(M, K, N, bits, mode)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = _made(torch.empty, need, torch.uint8, X.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().tq_linear(_ptr(X), M, K, X.stride(0), _ptr(Wq), _ptr(sw), N, bits,
                            MODES[mode], _ptr(Y), OUT[out], Y.stride(0), _ptr(workspace),
@@ -326,7 +343,7 @@ def linear_swiglu(G, U, Wq, sw, N: int, bits: int, mode: str, Y=None, out: str =
     if out not in ("f32", "bf16"):
         raise ValueError("tq_linear_swiglu writes f32 or bf16")
     if Y is None:
-        Y = torch.empty((M, N), dtype=_dt(out), device=G.device)
+        Y = _made(torch.empty, (M, N), _dt(out), G.device, stream)
     _req(G, "G", dtype=torch.bfloat16, rows=M, cols=K)
     _req(U, "U", dtype=torch.bfloat16, rows=M, cols=K)
     _weights(Wq, sw, N, K, bits)
@@ -341,7 +358,7 @@ def linear_q8(Xq, sx, Wq, sw, N: int, bits: int, Y=None, out: str = "f32", strea
     import torch
     M, K = Xq.shape
     if Y is None:
-        Y = torch.empty((M, N), dtype=_dt(out), device=Xq.device)
+        Y = _made(torch.empty, (M, N), _dt(out), Xq.device, stream)
     _req(Xq, "Xq", dtype=torch.int8, rows=M, cols=K, dense=True)
     if out != "i32":
         _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
@@ -363,9 +380,9 @@ def rotate_quant_act_tiled(X, At=None, sx=None, stream=None):
     M, K = X.shape
     need = act_tiled_bytes(M, K)
     if At is None:
-        At = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+        At = _made(torch.empty, max(need, 1), torch.uint8, X.device, stream)
     if sx is None:
-        sx = torch.empty(M, dtype=torch.float32, device=X.device)
+        sx = _made(torch.empty, M, torch.float32, X.device, stream)
     _req(X, "X", dtype=torch.bfloat16, rows=M, cols=K)
     _req(At, "At", nbytes=need)
     _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
@@ -384,9 +401,9 @@ def modnorm_quant_act_tiled(X, shift, scale, eps=1e-6, At=None, sx=None, stream=
     M, K = X.shape
     need = act_tiled_bytes(M, K)
     if At is None:
-        At = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+        At = _made(torch.empty, max(need, 1), torch.uint8, X.device, stream)
     if sx is None:
-        sx = torch.empty(M, dtype=torch.float32, device=X.device)
+        sx = _made(torch.empty, M, torch.float32, X.device, stream)
     _req(X, "X", dtype=torch.bfloat16, rows=M, cols=K)
     _req(shift, "shift", dtype=torch.float32, nbytes=4 * K)
     _req(scale, "scale", dtype=torch.float32, nbytes=4 * K)
@@ -408,9 +425,9 @@ def swiglu_quant_act_tiled(G, U, At=None, sx=None, stream=None):
         raise ValueError(f"U is {tuple(U.shape)}, expected {(M, K)}")
     need = act_tiled_bytes(M, K)
     if At is None:
-        At = torch.empty(max(need, 1), dtype=torch.uint8, device=G.device)
+        At = _made(torch.empty, max(need, 1), torch.uint8, G.device, stream)
     if sx is None:
-        sx = torch.empty(M, dtype=torch.float32, device=G.device)
+        sx = _made(torch.empty, M, torch.float32, G.device, stream)
     _req(G, "G", dtype=torch.bfloat16, rows=M, cols=K)
     _req(U, "U", dtype=torch.bfloat16, rows=M, cols=K)
     _req(At, "At", nbytes=need)
@@ -425,7 +442,7 @@ def linear_tiled(At, sx, M: int, K: int, Wq, sw, N: int, bits: int, Y=None, out:
                  stream=None):
     import torch
     if Y is None:
-        Y = torch.empty((M, N), dtype=_dt(out), device=At.device)
+        Y = _made(torch.empty, (M, N), _dt(out), At.device, stream)
     _req(At, "At", nbytes=act_tiled_bytes(M, K))
     if out != "i32":
         _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
@@ -446,7 +463,7 @@ def tile_weights(Wq, N: int, K: int, bits: int, Wt=None, stream=None):
     import torch
     need = weights_tiled_bytes(N, K)
     if Wt is None:
-        Wt = torch.empty(max(need, 1), dtype=torch.uint8, device=Wq.device)
+        Wt = _made(torch.empty, max(need, 1), torch.uint8, Wq.device, stream)
     _req(Wq, "Wq", nbytes=N * K * bits // 8)
     _req(Wt, "Wt", nbytes=need)
     _check(lib().tq_tile_weights(_ptr(Wq), N, K, bits, _ptr(Wt), _nbytes(Wt), _stream(stream)),
@@ -473,7 +490,7 @@ def linear_tt(At, sx, M: int, K: int, Wt, sw, N: int, bits: int, Y=None, out: st
     pair (tq_linear_tt_split)."""
     import torch
     if Y is None:
-        Y = torch.empty((M, N), dtype=_dt(out), device=At.device)
+        Y = _made(torch.empty, (M, N), _dt(out), At.device, stream)
     _req(At, "At", nbytes=act_tiled_bytes(M, K))
     if out != "i32":
         _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
@@ -499,7 +516,7 @@ def linear_tt_ex(At, sx, M: int, K: int, Wt, sw, N: int, bits: int, Y=None, out:
     if out not in ("f32", "bf16"):
         raise ValueError("the epilogue writes f32 or bf16")
     if Y is None:
-        Y = torch.empty((M, N), dtype=_dt(out), device=At.device)
+        Y = _made(torch.empty, (M, N), _dt(out), At.device, stream)
     _req(At, "At", nbytes=act_tiled_bytes(M, K))
     _req(sx, "sx", dtype=torch.float32, nbytes=4 * M)
     _req(Wt, "Wt", nbytes=weights_tiled_bytes(N, K))
@@ -732,9 +749,9 @@ def rmsnorm_quant_act(X, gamma, eps=1e-6, R=None, H=None, Y=None, Xq=None, sx=No
     for linear_q8."""
     import torch
     if Xq is None:
-        Xq = torch.empty(X.shape, dtype=torch.int8, device=X.device)
+        Xq = _made(torch.empty, X.shape, torch.int8, X.device, stream)
     if sx is None:
-        sx = torch.empty(X.shape[0], dtype=torch.float32, device=X.device)
+        sx = _made(torch.empty, X.shape[0], torch.float32, X.device, stream)
     _norm(X, gamma, eps, R, H, Y, Xq, sx, stream)
     return Xq, sx
 
@@ -744,7 +761,7 @@ def rmsnorm(X, gamma, eps=1e-6, R=None, H=None, Y=None, stream=None):
     ``rmsnorm_quant_act`` without its codes.  Returns Y."""
     import torch
     if Y is None:
-        Y = torch.empty(X.shape, dtype=torch.bfloat16, device=X.device)
+        Y = _made(torch.empty, X.shape, torch.bfloat16, X.device, stream)
     _norm(X, gamma, eps, R, H, Y, None, None, stream)
     return Y
 
@@ -761,9 +778,9 @@ def rmsnorm_quant_act_tiled(X, gamma, eps=1e-6, R=None, H=None, At=None, sx=None
     ldh = 0 if H is None else _rows(H, "H", bf16, M, K)
     need = act_tiled_bytes(M, K)
     if At is None:
-        At = torch.empty(max(need, 1), dtype=torch.uint8, device=X.device)
+        At = _made(torch.empty, max(need, 1), torch.uint8, X.device, stream)
     if sx is None:
-        sx = torch.empty(M, dtype=torch.float32, device=X.device)
+        sx = _made(torch.empty, M, torch.float32, X.device, stream)
     _req(At, "At", nbytes=need)
     _flat(sx, "sx", torch.float32, M)
     _check((_lib or load()).tq_rmsnorm_quant_act_tiled(
@@ -816,7 +833,7 @@ def rope(X, pos, spec: RopeSpec, Y=None, stream=None):
     import torch
     T, H, D = X.shape
     if Y is None:
-        Y = torch.empty((T, H, D), dtype=torch.bfloat16, device=X.device)
+        Y = _made(torch.empty, (T, H, D), torch.bfloat16, X.device, stream)
     ldx = _heads(X, "X")
     ldy = ldx if Y is X else _heads(Y, "Y", T, H, D)
     ldpos = _rows(pos, "pos", torch.int32, 1, T)
@@ -899,8 +916,8 @@ def kv4_read(batch: KV4Batch, K=None, V=None, stream=None):
     import torch
     c = batch.cache
     shape = (batch.tokens, c.heads, c.dim)
-    K = torch.zeros(shape, dtype=torch.bfloat16, device=c.pool.device) if K is None else K
-    V = torch.zeros(shape, dtype=torch.bfloat16, device=c.pool.device) if V is None else V
+    K = _made(torch.zeros, shape, torch.bfloat16, c.pool.device, stream) if K is None else K
+    V = _made(torch.zeros, shape, torch.bfloat16, c.pool.device, stream) if V is None else V
     ldk, ldv = _heads(K, "K", *shape), _heads(V, "V", *shape)
     _check((_lib or load()).tq_kv4_read(batch._p, K.data_ptr(), ldk, V.data_ptr(), ldv, _raw_stream(K, stream)),
            "tq_kv4_read")
@@ -916,7 +933,7 @@ def kv4_attention(batch: KV4Batch, Q, scale: float, workspace, causal: bool = Tr
     import torch
     T, H, D = Q.shape
     if O is None:
-        O = torch.zeros((T, H, D), dtype=torch.bfloat16, device=Q.device)
+        O = _made(torch.zeros, (T, H, D), torch.bfloat16, Q.device, stream)
     ldq, ldo = _heads(Q, "Q", batch.tokens, None, batch.cache.dim), _heads(O, "O", T, H, D)
     if lse is not None:
         _flat(lse, "lse", torch.float32, T * H)
@@ -932,8 +949,7 @@ def kv4_attention(batch: KV4Batch, Q, scale: float, workspace, causal: bool = Tr
 # Codes are e4m3 bytes: uint8 tensors, or torch.float8_e4m3fn ones.  All tensors of a
 # call are on the current device, the one that the library launches on.  A call of a few
 # tokens takes a few microseconds, so its checks are few and plain: a tensor that passes
-# none of them is described afterwards.  What a call with ``stream`` makes itself is made
-# on that stream: other streams wait for it as for any other work there.
+# none of them is described afterwards.
 
 _torch = None
 _e4m3 = ()
@@ -1000,22 +1016,6 @@ def _floats(t, what) -> int:
 
 def _stream_of(stream, d) -> int:
     return _torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
-
-
-def _made(make, shape, dtype, device, stream):
-    """A tensor that a call makes itself.  It is made on the call's stream, where no
-    earlier kernel still uses its memory and zeros are filled in before the call's kernel
-    runs; and the current stream, whose caller has it from here, is recorded: the memory
-    is not given out again before that stream has done what it has when the tensor goes."""
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    import torch
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    with torch.cuda.stream(stream):
-        t = make(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(t.device))
-    return t
 
 
 def quantize_weights_f8(W, codes=None, scales=None, stream=None):

@@ -5,10 +5,20 @@ earlier kernel there still uses, and zeros filled in there could wipe what the c
 kernel wrote: nothing orders the two streams, and the caller cannot, as both happen
 inside the call."""
 import contextlib
+import types
 
 import pytest
 
 from test_binding_expert import Fake, on0, tq  # noqa: F401
+
+
+class Dense(Fake):
+    """With what the other calls ask of a tensor besides."""
+    is_cuda = True
+
+    def __init__(self, *a, **kw):
+        super().__init__(*a, **kw)
+        self.device = types.SimpleNamespace(index=0)
 
 
 class Stream:
@@ -43,7 +53,7 @@ def made(monkeypatch):
     import torch
     at, log, recorded = ["current"], [], []
 
-    class Made(Fake):
+    class Made(Dense):
         def record_stream(self, s):
             recorded.append(s)
 
@@ -81,3 +91,41 @@ def test_made_on_the_call_s_stream(on0, made, name):  # noqa: F811
     with pytest.raises(on0.TQError):
         getattr(on0, name)(*args)
     assert [at for at, _ in log] == ["current"] * n and not recorded
+
+
+def other_calls(tq):  # noqa: F811
+    import torch
+    bf, f32, u8, i8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int8, torch.int32
+    big, X, sx, w = Dense((1 << 24,), u8), Dense((4, 896), bf), Dense((4,), f32), Dense((896,), f32)
+    sw, heads = Dense((1024,), f32), Dense((4, 2, 128), bf)
+    cache = types.SimpleNamespace(pool=big, npages=4, page_size=16, heads=2, dim=128)
+    batch = tq.KV4Batch(cache, Dense((4, 1), i32), Dense((4,), i32), Dense((5,), i32), 4)
+    return {
+        "quantize_weights": (X, 8), "quantize_weights_blocked": (X, 4, 32), "rotate_quant_act": (X,),
+        "linear_blocked": (X, big, sw, 128, 8, 128), "rotate_act_bf16": (X,), "linear": (X, big, sw, 128, 8, "W8A8"),
+        "linear_swiglu": (X, X, big, sw, 128, 8, "W8A16"), "linear_q8": (Dense((4, 896), i8), sx, big, sw, 128, 8),
+        "rotate_quant_act_tiled": (X,), "modnorm_quant_act_tiled": (X, w, w), "swiglu_quant_act_tiled": (X, X),
+        "linear_tiled": (big, sx, 4, 896, big, sw, 128, 8), "tile_weights": (big, 128, 896, 8),
+        "linear_tt": (big, sx, 4, 896, big, sw, 128, 8), "linear_tt_ex": (big, sx, 4, 896, big, sw, 128, 8),
+        "rmsnorm_quant_act": (X, w), "rmsnorm": (X, w), "rmsnorm_quant_act_tiled": (X, w),
+        "rope": (heads, Dense((1, 4), i32), tq.RopeSpec(Dense((64,), f32))), "kv4_read": (batch,),
+        "kv4_attention": (batch, heads, 0.1, big),
+    }
+
+
+OTHERS = {"quantize_weights": 2, "quantize_weights_blocked": 2, "rotate_quant_act": 2, "linear_blocked": 1,
+          "rotate_act_bf16": 1, "linear": 2, "linear_swiglu": 1, "linear_q8": 1, "rotate_quant_act_tiled": 2,
+          "modnorm_quant_act_tiled": 2, "swiglu_quant_act_tiled": 2, "linear_tiled": 1, "tile_weights": 1,
+          "linear_tt": 1, "linear_tt_ex": 1, "rmsnorm_quant_act": 2, "rmsnorm": 1, "rmsnorm_quant_act_tiled": 2,
+          "rope": 1, "kv4_read": 2, "kv4_attention": 1}
+
+
+@pytest.mark.parametrize("name", sorted(OTHERS))
+def test_other_calls_tensors_are_made_there_too(on0, made, name, monkeypatch):  # noqa: F811
+    log, recorded = made
+    monkeypatch.setattr(on0, "linear_workspace_bytes", lambda *a: 4096)      # as a device's would be
+    args = other_calls(on0)[name]
+    with pytest.raises(on0.TQError):
+        getattr(on0, name)(*args, stream=Stream())
+    assert [at for at, _ in log] == ["stream 5"] * OTHERS[name]
+    assert recorded == ["current"] * OTHERS[name]

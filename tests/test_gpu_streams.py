@@ -22,7 +22,19 @@ def calls(tq):
     ids[::5, 1] = -1                                   # rows of no expert: left as the call's zeros
     offsets, token, place = tq.expert_sort(ids, E)
     y, do, ws = n(M, 64).bfloat16(), n(M // top, 64).bfloat16(), tq.f8_workspace()
+    codes, s8 = tq.quantize_weights(W[0], 8)
+    gamma, qkv = n(K).abs(), n(40, 2, 128).bfloat16()
+    cache = tq.KV4Cache(8, 16, 2, 128)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = tq.KV4Batch(cache, torch.arange(8, **i32).view(2, 4), torch.tensor([30, 10], **i32),
+                        torch.tensor([0, 30, 40], **i32), 40, 30)
+    tq.kv4_append(batch, qkv, qkv.flip(0).contiguous())
+    kws = tq.kv4_workspace()
     return {
+        "linear": lambda **s: tq.linear(x, codes, s8, N, 8, "W8A8", **s),
+        "rmsnorm_quant_act": lambda **s: tq.rmsnorm_quant_act(x, gamma, **s),
+        "kv4_read": lambda **s: tq.kv4_read(batch, **s),
+        "kv4_attention": lambda **s: tq.kv4_attention(batch, qkv, 128 ** -0.5, kws, **s),
         "quantize_weights_f8": lambda **s: tq.quantize_weights_f8(W, **s),
         "quant_act_f8": lambda **s: tq.quant_act_f8(x, **s),
         "swiglu_quant_act_f8": lambda **s: tq.swiglu_quant_act_f8(both[:, :K], both[:, K:], **s),
@@ -38,7 +50,8 @@ def calls(tq):
 
 
 NAMES = ["quantize_weights_f8", "quant_act_f8", "swiglu_quant_act_f8", "linear_f8", "linear_f8_experts", "expert_topk",
-         "expert_topk_grad", "expert_sort", "expert_gather", "expert_combine", "expert_combine_grad"]
+         "expert_topk_grad", "expert_sort", "expert_gather", "expert_combine", "expert_combine_grad",
+         "linear", "rmsnorm_quant_act", "kv4_read", "kv4_attention"]
 
 
 def several(v):
