@@ -956,12 +956,15 @@ _e4m3 = ()
 
 
 def _module():
-    """torch, once it is loaded (an import statement costs as much as a check)."""
+    """torch, once it and the library are loaded (an import statement costs as much as a
+    check).  ``_torch`` is set last: who finds it, another thread or a call after a load
+    that failed, finds the library too."""
     global _torch, _e4m3
     if _torch is None:
         import torch
-        _torch, _e4m3 = torch, (torch.uint8, torch.float8_e4m3fn)
         load()
+        _e4m3 = (torch.uint8, torch.float8_e4m3fn)
+        _torch = torch
     return _torch
 
 

@@ -164,3 +164,54 @@ def test_other_bytes_are_not_codes(on0, name):
     refused(on0.quant_act_f8, Fake((4, 896), bf), Xq=Fake((4, 896), other), sx=Fake((7, 4), f32))
     good.update(offsets=Fake((6,), i32), Wq=Fake((5, 300, 896), other), sw=Fake((5, 3, 7), f32))
     refused(on0.linear_f8_experts, **good)
+
+
+def test_every_call_says_that_the_library_is_missing(on0, monkeypatch):
+    """A load that failed is not taken for one that succeeded."""
+    import torch
+
+    def missing(*a):
+        raise RuntimeError("libtq.so is missing: build it")
+
+    monkeypatch.setattr(on0, "_torch", None)
+    monkeypatch.setattr(on0, "_lib", None)
+    monkeypatch.setattr(on0, "load", missing)
+    for _ in range(3):
+        with pytest.raises(RuntimeError, match="is missing"):
+            on0.quant_act_f8(Fake((4, 896), torch.bfloat16), Xq=Fake((4, 896), torch.uint8),
+                             sx=Fake((7, 4), torch.float32))
+
+
+def test_a_call_of_another_thread_waits_for_the_library(on0, monkeypatch):
+    """While one thread loads, another one does not go past the load."""
+    import threading
+
+    import torch
+    lib, inside, go = on0._lib, threading.Event(), threading.Event()
+
+    def slow(*a):
+        inside.set()
+        assert go.wait(20)
+        on0._lib = lib
+        return lib
+
+    monkeypatch.setattr(on0, "_torch", None)
+    monkeypatch.setattr(on0, "_lib", None)
+    monkeypatch.setattr(on0, "load", slow)
+    out = []
+
+    def call():
+        try:
+            on0.quant_act_f8(Fake((4, 896), torch.bfloat16), Xq=Fake((4, 896), torch.uint8), sx=Fake((7, 4), torch.float32))
+        except Exception as e:
+            out.append(e)
+
+    threads = [threading.Thread(target=call) for _ in range(2)]
+    threads[0].start()
+    assert inside.wait(20)
+    threads[1].start()
+    threads[1].join(1.0)
+    go.set()
+    for t in threads:
+        t.join(20)
+    assert [getattr(e, "status", e) for e in out] == [10, 10]     # both reach the library (which finds no device)
