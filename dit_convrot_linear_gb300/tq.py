@@ -968,30 +968,35 @@ def _module():
     return _torch
 
 
+def _missing(**tensors):
+    for what, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{what} is required")
+
+
 def _bad(t, what, wanted):
-    if t is None:
-        raise ValueError(f"{what} is required")
+    _missing(**{what: t})
     raise ValueError(f"{what} must be {wanted} on the current device (cuda:{_module()._C._cuda_getDevice()}), got "
                      f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
 def _dense(t, what, dtype, shape, d):
     """The address of a contiguous tensor of this type and shape."""
-    if t.get_device() != d or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+    if t is None or t.get_device() != d or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         _bad(t, what, f"contiguous {dtype} {tuple(shape)}")
     return t.data_ptr()
 
 
 def _codes(t, what, shape, d):
     """The address of contiguous e4m3 codes of this shape."""
-    if t.get_device() != d or t.dtype not in _e4m3 or t.shape != shape or not t.is_contiguous():
+    if t is None or t.get_device() != d or t.dtype not in _e4m3 or t.shape != shape or not t.is_contiguous():
         _bad(t, what, f"contiguous e4m3 codes (uint8 or float8_e4m3fn) {tuple(shape)}")
     return t.data_ptr()
 
 
 def _list(t, what, n, d):
     """The address of n contiguous int32 numbers."""
-    if t.get_device() != d or t.dtype is not _torch.int32 or t.numel() != n or not t.is_contiguous():
+    if t is None or t.get_device() != d or t.dtype is not _torch.int32 or t.numel() != n or not t.is_contiguous():
         _bad(t, what, f"{n} contiguous int32 numbers")
     return t.data_ptr()
 
@@ -999,6 +1004,8 @@ def _list(t, what, n, d):
 def _matrix(t, what, dtype, M, K, d) -> int:
     """The row stride of rows of K values (a matrix of at least M x K).  One row has no
     step to the next: its length stands for it."""
+    if t is None:
+        _bad(t, what, "a matrix")
     s = t.shape
     if t.get_device() != d or t.dtype is not dtype or len(s) != 2 or s[0] < M or s[1] < K:
         _bad(t, what, f"{dtype} of at least {M} x {K}")
@@ -1006,6 +1013,13 @@ def _matrix(t, what, dtype, M, K, d) -> int:
     if one != 1 and t.numel():
         _bad(t, what, "row-major")
     return ld if s[0] > 1 else max(s[1], 1)
+
+
+def _bytes(t, what, d):
+    """The address of a contiguous tensor of bytes."""
+    if t is None or t.get_device() != d or t.dtype is not _torch.uint8 or not t.is_contiguous():
+        _bad(t, what, "contiguous uint8")
+    return t.data_ptr()
 
 
 def _floats(t, what) -> int:
@@ -1026,6 +1040,8 @@ def quantize_weights_f8(W, codes=None, scales=None, stream=None):
     [..., ceil(N / 128), ceil(K / 128)])."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if W is None:
+        _missing(W=W)
     if W.dim() not in (2, 3):
         raise ValueError("W must be [N, K] or [experts, N, K]")
     N, K = W.shape[-2:]
@@ -1056,6 +1072,8 @@ def quant_act_f8(X, rows=None, Xq=None, sx=None, stream=None):
     -1: left as it was) -> (e4m3 codes [M, K], fp32 scales [ceil(K / 128), M])."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if X is None:
+        _missing(X=X)
     R, K = X.shape
     M = R if rows is None else rows.numel()
     if Xq is None or sx is None:
@@ -1073,6 +1091,8 @@ def swiglu_quant_act_f8(G, U, Xq=None, sx=None, stream=None):
     halves of a gate+up product's output)."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if G is None or U is None:
+        _missing(G=G, U=U)
     M, K = G.shape
     if U.shape != G.shape:
         raise ValueError(f"U is {tuple(U.shape)}, expected {(M, K)}")
@@ -1102,6 +1122,8 @@ def linear_f8(Xq, sx, Wq, sw, workspace, out: str = "bf16", Y=None, stream=None)
     if out != "bf16" and out != "f32":
         raise ValueError("the 8-bit floating-point products write f32 or bf16")
     dtype = torch.bfloat16 if out == "bf16" else f32
+    if Xq is None or Wq is None:
+        _missing(Xq=Xq, Wq=Wq)
     M, K = Xq.shape
     N = Wq.shape[0]
     if Y is None:
@@ -1110,7 +1132,7 @@ def linear_f8(Xq, sx, Wq, sw, workspace, out: str = "bf16", Y=None, stream=None)
     rc = _lib.tq_linear_f8(_codes(Xq, "Xq", (M, K), d), _dense(sx, "sx", f32, (kb, M), d), M, K,
                            _codes(Wq, "Wq", (N, K), d), _dense(sw, "sw", f32, (-(-N // 128), kb), d), N, Y.data_ptr(),
                            OUT[out], _matrix(Y, "Y", dtype, M, N, d),
-                           _dense(workspace, "workspace", torch.uint8, workspace.shape, d), workspace.numel(),
+                           _bytes(workspace, "workspace", d), workspace.numel(),
                            _stream_of(stream, d))
     if rc:
         _check(rc, "tq_linear_f8")
@@ -1128,6 +1150,8 @@ def linear_f8_experts(Xq, sx, offsets, Wq, sw, workspace, out: str = "bf16", Y=N
     if out != "bf16" and out != "f32":
         raise ValueError("the 8-bit floating-point products write f32 or bf16")
     dtype = torch.bfloat16 if out == "bf16" else f32
+    if Xq is None or Wq is None:
+        _missing(Xq=Xq, Wq=Wq)
     if Wq.dim() != 3:
         raise ValueError(f"Wq is {tuple(Wq.shape)}, expected [experts, N, K]")
     M, K = Xq.shape
@@ -1139,7 +1163,7 @@ def linear_f8_experts(Xq, sx, offsets, Wq, sw, workspace, out: str = "bf16", Y=N
                                    _list(offsets, "offsets", E + 1, d), E, _codes(Wq, "Wq", (E, N, K), d),
                                    _dense(sw, "sw", f32, (E, -(-N // 128), kb), d), N, Y.data_ptr(), OUT[out],
                                    _matrix(Y, "Y", dtype, M, N, d),
-                                   _dense(workspace, "workspace", torch.uint8, workspace.shape, d), workspace.numel(),
+                                   _bytes(workspace, "workspace", d), workspace.numel(),
                                    _stream_of(stream, d))
     if rc:
         _check(rc, "tq_linear_f8_experts")
@@ -1151,6 +1175,8 @@ def expert_topk(logits, top: int, renorm: bool = True, ids=None, weights=None, s
     (ids int32 [tokens, top], weights fp32 [tokens, top])."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if logits is None:
+        _missing(logits=logits)
     T, E = logits.shape
     if ids is None:
         ids = _made(torch.empty, (T, top), torch.int32, logits.device, stream)
@@ -1169,6 +1195,8 @@ def expert_topk_grad(logits, ids, dweights, renorm: bool = True, dlogits=None, s
     """dlogits (of the logits' type) from the gradients of ``expert_topk``'s weights."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if logits is None or ids is None:
+        _missing(logits=logits, ids=ids)
     T, E = logits.shape
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, top]")
@@ -1190,6 +1218,8 @@ def expert_sort(ids, experts: int, offsets=None, token=None, place=None, stream=
     [experts + 1], token int32 [tokens * top], place int32 [tokens, top])."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if ids is None:
+        _missing(ids=ids)
     T, top = ids.shape
     n = T * top
     if offsets is None:
@@ -1210,6 +1240,8 @@ def expert_gather(X, rows, Y=None, stream=None):
     was, zeros in a Y made here).  Returns Y [M, width]."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if X is None or rows is None:
+        _missing(X=X, rows=rows)
     R, W = X.shape
     M = rows.numel()
     if Y is None:
@@ -1227,6 +1259,8 @@ def expert_combine(Y, place, weights=None, O=None, stream=None):
     width]; place int32, weights fp32 [tokens, top], none: 1).  Returns O."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if Y is None or place is None:
+        _missing(Y=Y, place=place)
     R, W = Y.shape
     T, top = place.shape
     if O is None:
@@ -1246,6 +1280,8 @@ def expert_combine_grad(dO, Y, place, weights=None, dY=None, dweights=None, stre
     made here)."""
     torch = _module()
     d = torch._C._cuda_getDevice()
+    if dO is None or Y is None or place is None:
+        _missing(dO=dO, Y=Y, place=place)
     R, W = Y.shape
     T, top = place.shape
     if dO.shape != (T, W):

@@ -215,3 +215,35 @@ def test_a_call_of_another_thread_waits_for_the_library(on0, monkeypatch):
     for t in threads:
         t.join(20)
     assert [getattr(e, "status", e) for e in out] == [10, 10]     # both reach the library (which finds no device)
+
+
+def required():
+    """Each call's tensors, all of which it needs."""
+    import torch
+    bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    X, Xq, sx, ids = Fake((4, 896), bf), Fake((4, 896), u8), Fake((7, 4), f32), Fake((6, 4), i32)
+    Y, O, w, L, ws = Fake((24, 64), bf), Fake((6, 64), bf), Fake((6, 4), f32), Fake((6, 40), f32), Fake((1 << 28,), u8)
+    made = dict(Xq=Xq, sx=sx)
+    product = dict(Xq=Xq, sx=sx, sw=Fake((3, 7), f32), Wq=Fake((300, 896), u8), workspace=ws)
+    experts = {**product, "offsets": Fake((6,), i32), "Wq": Fake((5, 300, 896), u8), "sw": Fake((5, 3, 7), f32)}
+    # name: tensors that are required, and what the call gets besides
+    return {
+        "quantize_weights_f8": (dict(W=X), dict(codes=Xq, scales=Fake((1, 7), f32))),
+        "quant_act_f8": (dict(X=X), made), "swiglu_quant_act_f8": (dict(G=X, U=X), made),
+        "linear_f8": (product, dict(Y=Fake((4, 300), bf))), "linear_f8_experts": (experts, dict(Y=Fake((4, 300), bf))),
+        "expert_topk": (dict(logits=L), dict(top=4, ids=ids, weights=w)),
+        "expert_topk_grad": (dict(logits=L, ids=ids, dweights=w), dict(dlogits=L)),
+        "expert_sort": (dict(ids=ids), dict(experts=40, offsets=Fake((41,), i32), token=Fake((24,), i32), place=ids)),
+        "expert_gather": (dict(X=O, rows=Fake((24,), i32)), dict(Y=Y)),
+        "expert_combine": (dict(Y=Y, place=ids), dict(O=O)),
+        "expert_combine_grad": (dict(dO=O, Y=Y, place=ids), dict(dY=Y, dweights=w)),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(required()))
+def test_a_missing_tensor_is_named(on0, name):
+    tensors, others = required()[name]
+    reaches(on0, getattr(on0, name), **tensors, **others)
+    for missing in tensors:
+        with pytest.raises(ValueError, match=f"^{missing} is required"):
+            getattr(on0, name)(**{**tensors, **others, missing: None})
