@@ -168,6 +168,17 @@ def _made(make, shape, dtype, device, stream):
     return t
 
 
+def _zeroed(nbytes: int, device):
+    """A workspace of zeros.  They are there on return, whatever stream uses it first: a
+    fill that came after a product's first counts would leave wrong ones behind for good.
+    (In a capture the fill is the graph's, and so has to be the use.)"""
+    import torch
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    if ws.is_cuda and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(ws.device).synchronize()
+    return ws
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -478,8 +489,7 @@ def split_workspace_bytes() -> int:
 def split_workspace(device="cuda"):
     """A zeroed split workspace for ``linear_tt(..., split=ws)`` (one per
     stream; every completed call leaves it zeroed)."""
-    import torch
-    return torch.zeros(split_workspace_bytes(), dtype=torch.uint8, device=device)
+    return _zeroed(split_workspace_bytes(), device)
 
 
 def linear_tt(At, sx, M: int, K: int, Wt, sw, N: int, bits: int, Y=None, out: str = "f32",
@@ -853,8 +863,7 @@ def kv4_page_bytes(heads: int, dim: int, page_size: int) -> int:
 
 def kv4_workspace(device="cuda"):
     """A zeroed workspace for ``kv4_attention`` (one per stream)."""
-    import torch
-    return torch.zeros(int(lib().tq_kv4_workspace_bytes()), dtype=torch.uint8, device=device)
+    return _zeroed(int(lib().tq_kv4_workspace_bytes()), device)
 
 
 class KV4Cache:
@@ -1108,8 +1117,7 @@ def swiglu_quant_act_f8(G, U, Xq=None, sx=None, stream=None):
 
 def f8_workspace(device="cuda"):
     """A zeroed workspace for ``linear_f8`` and ``linear_f8_experts`` (one per stream)."""
-    import torch
-    return torch.zeros(int(lib().tq_f8_workspace_bytes()), dtype=torch.uint8, device=device)
+    return _zeroed(int(lib().tq_f8_workspace_bytes()), device)
 
 
 def linear_f8(Xq, sx, Wq, sw, workspace, out: str = "bf16", Y=None, stream=None):

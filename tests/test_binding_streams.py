@@ -129,3 +129,23 @@ def test_other_calls_tensors_are_made_there_too(on0, made, name, monkeypatch):  
         getattr(on0, name)(*args, stream=Stream())
     assert [at for at, _ in log] == ["stream 5"] * OTHERS[name]
     assert recorded == ["current"] * OTHERS[name]
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+@pytest.mark.parametrize("name", ["f8_workspace", "kv4_workspace", "split_workspace"])
+def test_a_workspace_is_zeroed_on_return(on0, monkeypatch, name, capturing):  # noqa: F811
+    """Its first use may be on any stream: the fill is over when the call returns (a
+    capture's is a node of the graph and cannot be waited for)."""
+    import torch
+    log = []
+
+    def zeros(shape, dtype=None, device=None):
+        log.append(("zeros", device))
+        return Dense((shape,), dtype)
+
+    stream = types.SimpleNamespace(synchronize=lambda: log.append("synchronize"))
+    monkeypatch.setattr(torch, "zeros", zeros)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    assert getattr(on0, name)().dtype is torch.uint8
+    assert log == [("zeros", "cuda")] + ([] if capturing else ["synchronize"])

@@ -77,3 +77,41 @@ def test_outputs_made_while_the_current_stream_is_busy(tq, name):
         assert all(same) and all(torch.equal(a, b) for a, b in zip(got, want))
     assert busy                                        # the other stream was not waited for
     assert tq.device_status() == 0
+
+
+@pytest.mark.parametrize("name", ["f8_workspace", "kv4_workspace", "split_workspace"])
+def test_a_workspace_may_be_used_on_any_stream_at_once(tq, name):
+    """Zeros on another stream that waits for nothing, in memory that held something else,
+    while the stream that fills it is busy."""
+    import torch
+    side = torch.cuda.Stream()
+    old = getattr(tq, name)().fill_(255)
+    size = old.numel()
+    with torch.cuda.stream(side):                      # (the side stream has its memory)
+        assert int(old.count_nonzero()) == size
+    torch.cuda.synchronize()
+    del old
+    torch.cuda._sleep(BUSY)
+    ws = getattr(tq, name)()
+    with torch.cuda.stream(side):
+        assert int(ws.count_nonzero()) == 0
+    torch.cuda.synchronize()
+    assert ws.numel() == size and int(ws.count_nonzero()) == 0
+
+
+def test_a_workspace_made_in_a_capture(tq):
+    """A workspace that a graph makes itself is filled by the graph at every replay."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(24, 2048, generator=g, device="cuda").bfloat16()
+    W = tq.quantize_weights_f8(torch.randn(896, 2048, generator=g, device="cuda").bfloat16())
+    want = tq.linear_f8(*tq.quant_act_f8(x), *W, tq.f8_workspace())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y = tq.linear_f8(*tq.quant_act_f8(x), *W, tq.f8_workspace())
+    for _ in range(3):
+        Y.zero_()
+        graph.replay()
+        assert torch.equal(Y, want)
+    assert tq.device_status() == 0
