@@ -78,8 +78,10 @@ def run(width=512, hidden=256, experts=16, top=4, tokens=16, steps=4, seed=0):
     rs = torch.randn(steps, tokens, width, generator=g, device="cuda").bfloat16()
     x, r = xs[0].clone(), rs[0].clone()
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())       # the weights and rows are made there
     with torch.cuda.stream(side):
         layer(x, r)
+    torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
