@@ -257,8 +257,16 @@ __device__ __forceinline__ int remote_int(uint32_t addr, int cta) {
     return v;
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// (.aligned: a warp's lanes have to come together, also after a loop that they leave at
+// different times)
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 template <int BITS>
 __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *__restrict__ ids, uint32_t n, uint32_t k,
@@ -331,7 +339,6 @@ __global__ void __launch_bounds__(32 * kSortWarps) k_expert_sort(const int32_t *
             all = sum_cta[e];
         }
     }
-    __syncwarp();
     if (ctas > 1) cluster_arrive();              // the other CTAs' counts have been read
     int s = all;
 #pragma unroll

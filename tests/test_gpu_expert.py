@@ -215,6 +215,24 @@ def test_sort(tq, T, top, E, drop, skew):
         assert all(torch.equal(a.cpu(), b) for a, b in zip((off, token, place), want))
 
 
+@pytest.mark.parametrize("T,top,E,drop", [(400, 8, 1000, 0.3), (700, 4, 33, 1.0), (1025, 2, 1, 0.97), (2081, 1, 1023, 0.0)])
+def test_sort_whose_lanes_part(tq, T, top, E, drop):
+    """Clusters whose warps' lanes leave the loops over experts, choices and the rows behind
+    the last one at different times, twenty times each."""
+    import torch
+    ids = choices(gen(E), T, top, E, drop)
+    flat = ids.reshape(-1).long().cpu()
+    n = int((flat >= 0).sum())
+    order = torch.argsort(torch.where(flat >= 0, flat, E), stable=True)
+    want = torch.cat([order[:n] // top, torch.full((flat.numel() - n,), -1)]).int()
+    got = [tq.expert_sort(ids, E) for _ in range(20)]
+    for off, token, place in got:
+        assert torch.equal(token.cpu(), want)
+        assert all(torch.equal(a, b) for a, b in zip((off, place), (got[0][0], got[0][2])))
+    assert int(got[0][0][E]) == n
+    assert tq.device_status() == 0
+
+
 def test_sort_many(tq):
     """Half a million choices and more, one expert's share past 65536."""
     import torch
