@@ -436,8 +436,10 @@ struct Piece<uint16_t> {
 };
 
 // A warp a row, or a quarter of one: four 16-byte pieces a lane on their way at once.
-// Bound by the stores: 65536 rows of 4096 bf16 out of 8192, an eighth left out, 125 us
-// (470 MB written at 3.8 TB/s; 124 with a thread a piece); 8192 out of 4096 13.3 (15.9).
+// Bound by the stores: 65536 rows of 4096 bf16 out of 8192, an eighth left out, 126 us
+// (470 MB written at 3.7 TB/s; 124 with a thread a piece); with none left out 137 (3.9 TB/s),
+// and zeros filled in over the same 537 MB, with nothing read, take 134 (4.0 TB/s); 8192
+// out of 4096 13.3 to 17 (15.9).
 __global__ void __launch_bounds__(256) k_expert_gather(const uint4 *__restrict__ X, int64_t rows_x, int pieces,
                                                        int parts, int64_t ldx, const int32_t *__restrict__ rows,
                                                        int64_t M, uint4 *__restrict__ Y, int64_t ldy,

@@ -8,7 +8,8 @@
 // a code of four exponent bits keeps the same relative precision wherever its
 // block's largest value lies, so a finer scale would gain nothing.  No rotation
 // for the same reason: a channel forty times its neighbours costs them no bits
-// until they fall 2^15 below it.
+// until they fall 2^13.8 below it (a block's largest |x| / s lies above 224, and e4m3's
+// smallest normal number is 2^-6).
 //
 // Bound by memory: 2 B read (4 for the SwiGLU) and 1 B written a value.  A lane
 // takes 16 columns (two 16-byte loads, one 16-byte store), eight lanes a block; eight
@@ -152,7 +153,8 @@ __global__ void __launch_bounds__(32 * kF8Warps, 8) k_quant_act_f8(const QuantF8
     }
 }
 
-// A CTA a 128 x 128 block of W, a thread 16 columns of every 32nd row.
+// A CTA a 128 x 128 block of W, a thread 16 columns of every 32nd row.  Once a matrix, so
+// left as it is: 12288 x 4096 37.7 us, 4000 GB/s; 2048 x 2048 5.8, 2160 GB/s (the launch).
 __global__ void __launch_bounds__(256) k_quantize_weights_f8(const uint16_t *__restrict__ W, int64_t N, int64_t K,
                                                              int64_t ldw, uint8_t *__restrict__ codes,
                                                              float *__restrict__ scales, int kb) {

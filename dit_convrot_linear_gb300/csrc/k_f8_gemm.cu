@@ -22,13 +22,15 @@
 //   2 scale warps  each step's scales into shared memory, in turn.
 //
 // What bounds it.  With many tokens a step's MMAs take 512 cycles, and it takes about 950
-// (4032 tokens, 4096 to 12288: 185 us, 2200 TFLOP/s).  Between an accumulator's last MMA
-// and the first that fills it again lie a commit (300 cycles), the drain, its arrival (200)
-// and an issue, and TMEM holds two steps; shared memory is written and read 112 KB a step,
-// 870 cycles; each step's sums are read out of TMEM, 128 KB.  A step's columns are two
-// accumulators of 128 with MMAs of their own, one filled while the other is drained, and
-// four threads issue.  One accumulator of 256 columns (96 KB a step), the next columns
-// loaded ahead of the sums, 192 registers a drain thread: all within 3%.  Pairs of CTAs
+// (4032 tokens, 4096 to 12288: 185 us, 2200 TFLOP/s).  TMEM holds two steps, so that an
+// accumulator comes round every 1900: its MMAs 512, their commit 300, the drain from there
+// to the hand-back 390, its arrival 200, and the issue, whose four MMAs and two commits
+// hold a thread for 600 (drain and issue by the clock in a build for it; a drain warp waits
+// 240 a step, and its sums past the hand-back take 40).  Shared memory is not what binds: a
+// step writes and reads 112 KB of it, and one accumulator of 256 columns, with 96 KB, is
+// within 3%.  So are the next columns loaded ahead of the sums and 192 registers a drain
+// thread.  A step's columns are two accumulators of 128 with MMAs of their own, one filled
+// while the other is drained, and four threads issue.  Pairs of CTAs
 // (256 x 256, 80 KB a step and CTA) take as long for such a matrix, as the arrivals cross
 // to the other SM, and waste more of an expert's last tile: 512 tokens of 64 experts, eight
 // each, 2048 x 2048: 87 us against 57; 4096 tokens 178 against 164.  Sixteen drain warps:
@@ -393,7 +395,8 @@ k_linear_f8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
         if (lane == 0) {
             // The tiles of a last round that leaves CTAs idle are split where that saves more
-            // steps than the joining costs, in at most kF8MaxParts parts each.  (Many tokens, 4096
+            // steps than the joining costs, among at most kF8MaxParts CTAs a tile (a tile whose ends
+            // lie within two CTAs' shares has a part more).  (Many tokens, 4096
             // to 12288: 512 of them, whose last 40 tiles of 32 steps could be of 9, 38 us whole and
             // 50 split.  12288 to 4096: 4032, the last 56 tiles of 96 steps in parts of 35, 199
             // us whole and 188 split.)
@@ -974,7 +977,10 @@ tq_status launch_f8(const F8Product &f, int ycols, const DeviceInfo &dev, cudaSt
         // of fewer rows, as many as CTAs.  A step of r rows takes about 3 r ns (what an SM draws
         // from the DRAM) and 250 at least; joining takes 5 us, a round of smaller tiles 1.5 more
         // to begin.  48 tokens of 12288 x 4096: 96 tiles 18 us, 150 of 82 rows 17; 64 of 4096 x
-        // 12288: 128 tiles of 32 rows 42, 32 in four parts 22.
+        // 12288: 128 tiles of 32 rows 42, 32 in four parts 22.  (The device splits tiles of fewer
+        // rows too, by JOIN_STEPS, which this estimate leaves out: it does at 16 to 22 steps.
+        // 64 to 512 rows of 2048: one and 16 tokens 7.0 to 7.5 us split, 7.5 to 8.1 whole; 64
+        // tokens 11.0 to 12.7 and 10.8 to 11.1.)
         const int64_t by_tokens = (f.M + P::TOKENS - 1) / P::TOKENS, sms = dev.sms;
         auto whole = [&](int64_t rows) {
             const int64_t tiles = by_tokens * ((f.N + rows - 1) / rows);

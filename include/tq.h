@@ -906,7 +906,9 @@ tq_status tq_quant_act_f8(const void *X, int64_t rows_x, int64_t K, int64_t ldx,
 /*
  * The same of h = silu(G) * U, silu(g) = g / (1 + e^-g), formed in fp32 and
  * quantised without a rounding in between (the operand of a gated feed-forward's
- * down projection).
+ * down projection).  The exponential and the division are the hardware's approximate
+ * ones: h is within (5 + 1.2 |g|) 2^-23 of itself, and for g < -87 it may be 0.  All
+ * M rows are formed, those that no expert has among them.
  *   G, U   bf16 [M, K] rows at G + m * ldg and U + m * ldu (X's rules).
  */
 tq_status tq_swiglu_quant_act_f8(const void *G, int64_t ldg, const void *U, int64_t ldu, int64_t M, int64_t K,
@@ -923,7 +925,8 @@ size_t tq_f8_workspace_bytes(void);
  * fused multiply-adds in the order of b (in parts where K is split, or the even and
  * the odd blocks apart, the parts added in order; how depends on the sizes and the
  * offsets alone, so repeated calls give identical bytes).  sx * sw is formed in fp32
- * first and has to be finite.
+ * first and has to be finite; below 2^-126 it keeps fewer bits: it is off by up to
+ * 2^-150, and a block's part of Y by that times the block's sum of |xq * wq|.
  *
  *   Xq, sx   as written by tq_quant_act_f8.
  *   Wq, sw   e4m3 [N, K] dense and its scales; Wq 16-byte aligned.
@@ -949,7 +952,9 @@ tq_status tq_linear_f8(const uint8_t *Xq, const float *sx, int64_t M, int64_t K,
  *            without rows costs nothing).  A range that runs backwards, leaves 0 ..
  *            M or starts before an earlier offset is taken as empty and sets
  *            TQ_ERR_INDEX.
- *   experts  1 .. TQ_MAX_EXPERTS.
+ *   experts  1 .. TQ_MAX_EXPERTS.  The offsets are the device's, so the host takes a
+ *            tile's form by M / experts rows an expert: an M far above the last offset,
+ *            or rows with a few experts alone, cost time and no more.
  *   M        rows of Xq and Y, and of sx ([ceil(K / 128), M]).  Rows of Y that no
  *            expert has are left as they were.
  *   Wq, sw   e4m3 [experts, N, K] dense, scales [experts, ceil(N / 128),

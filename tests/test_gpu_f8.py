@@ -373,6 +373,26 @@ def test_experts_offsets_written_just_before(tq, M, E):
     assert tq.device_status() == 0
 
 
+@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("power", [-122, -136, -146])
+def test_scales_whose_product_is_subnormal(tq, M, power):
+    """sx * sw rounds to a multiple of 2^-149: off by 2^-150, on top of the usual bar, times
+    a block's sum of magnitudes; Y itself is as coarse, and so is each block's addition."""
+    import torch
+    g = gen(-power)
+    N, K = 140, 400
+    q = torch.randint(0, 126, (M, K), generator=g, device="cuda", dtype=torch.uint8)
+    w = torch.randint(0, 126, (N, K), generator=g, device="cuda", dtype=torch.uint8)
+    sx = (1.0 + torch.rand(4, M, generator=g, device="cuda")) * 2.0 ** (power // 2)
+    sw = (1.0 + torch.rand(2, 4, generator=g, device="cuda")) * 2.0 ** (power - power // 2)
+    got = tq.linear_f8(q, sx, w, sw, tq.f8_workspace(), out="f32")
+    want, S = ref.product(q, sx, w, sw)
+    size = ref.decode(q) @ ref.decode(w).t()               # (no code is negative)
+    bar = ref.product_bar(K, S, want, False) + 2.0 ** -150 * (size + 2 * 4 + 2)
+    assert ((got.double() - want).abs() <= bar).all()
+    assert tq.device_status() == 0
+
+
 @pytest.mark.parametrize("M", [24, 700])
 def test_product_in_a_graph_and_on_two_streams(tq, M):
     """A captured call replayed on new inputs, and two streams with a workspace each."""
