@@ -115,3 +115,38 @@ def test_a_workspace_made_in_a_capture(tq):
         graph.replay()
         assert torch.equal(Y, want)
     assert tq.device_status() == 0
+
+
+def test_no_tokens_on_a_stream(tq):
+    """Outputs without memory have nothing to record."""
+    import torch
+    side = torch.cuda.Stream()
+    x = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    q, sx = tq.quant_act_f8(x, stream=side)
+    off, token, place = tq.expert_sort(torch.empty(0, 2, dtype=torch.int32, device="cuda"), 3, stream=side)
+    assert q.shape == (0, 128) and sx.shape == (1, 0) and token.shape == (0,) and place.shape == (0, 2)
+    assert tq.expert_gather(x, token, stream=side).shape == (0, 128)
+    side.synchronize()
+    assert off.tolist() == [0, 0, 0, 0]
+    assert tq.device_status() == 0
+
+
+def test_a_stream_within_a_capture(tq):
+    """A graph with a branch on a stream of its own, whose outputs the calls make."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(70, 512, generator=g, device="cuda").bfloat16()
+    W = tq.quantize_weights_f8(torch.randn(256, 512, generator=g, device="cuda").bfloat16())
+    ws, side = tq.f8_workspace(), torch.cuda.Stream()
+    want = tq.linear_f8(*tq.quant_act_f8(x), *W, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        Y = tq.linear_f8(*tq.quant_act_f8(x, stream=side), *W, ws, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        Y.zero_()
+        graph.replay()
+        assert torch.equal(Y, want)
+    assert tq.device_status() == 0
